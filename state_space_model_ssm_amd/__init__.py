@@ -25,6 +25,24 @@ __all__ = [
     "scan_resolved_chunks", "ssd_workspace_size", "status_string", "last_error", "version",
 ]
 
+# The second library's binding (block.py), imported at the first use of a name.
+_BLOCK = (
+    "GLR_STATE_STEP", "GlrDims", "RmsDims", "SwaDims", "block_lib", "block_library_path", "block_last_error",
+    "glr_fwd", "glr_bwd", "glr_step", "glr_workspace_size", "glr_bwd_workspace_size",
+    "rms_add_fwd", "rms_add_q8_fwd", "rms_add_bwd", "rms_add_bwd_workspace_size",
+    "swa_fwd", "swa_bwd", "swa_bwd_workspace_size", "swa_step", "swa_step_workspace_size", "swa_fill",
+)
+__all__ += _BLOCK
+
+
+def __getattr__(name):
+    if name not in _BLOCK:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    from . import block
+    globals().update({n: getattr(block, n) for n in _BLOCK})
+    return globals()[name]
+
+
 SSM_F32, SSM_BF16 = 0, 1
 SSM_DT_SOFTPLUS, SSM_LAM_SIGMOID = 1, 2   # dims.flags bits (Phase-0 maps of dt and lam)
 STATUS = {0: "SSM_OK", -1: "SSM_ERR_NULL", -2: "SSM_ERR_SHAPE", -3: "SSM_ERR_DTYPE",

@@ -1,10 +1,12 @@
-"""Build libssm.so (the HIP kernels and the C ABI) in-tree for gfx950.
+"""Build libssm.so and libssm_block.so (the HIP kernels and the C ABIs) in-tree
+for gfx950.
 
     python -m state_space_model_ssm_amd.build
 
 Each ``csrc/*.hip`` file is compiled with hipcc into ``_build/`` and linked
-into ``state_space_model_ssm_amd/libssm.so``.  Packed-FP32 instructions are
-disabled for all device code.
+into ``state_space_model_ssm_amd/libssm.so``; ``csrc/block/*.hip`` go into
+``libssm_block.so`` alike.  Packed-FP32 instructions are disabled for all
+device code.
 """
 from __future__ import annotations
 
@@ -19,6 +21,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libssm.so")
+BLOCK_CSRC = os.path.join(CSRC, "block")
+BLOCK_LIB = os.path.join(PKG, "libssm_block.so")
 ARCH = "gfx950"
 
 HIPCC = os.environ.get("HIPCC", shutil.which("hipcc") or "/opt/rocm/bin/hipcc")
@@ -30,18 +34,21 @@ CFLAGS = [
 ]
 
 
-def sources() -> list[str]:
-    return sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".hip"))
+def _object(src: str) -> str:
+    return os.path.join(BUILD, os.path.basename(src)[:-4] + ".o")
+
+
+def sources(folder: str = CSRC) -> list[str]:
+    return sorted(os.path.join(folder, f) for f in os.listdir(folder) if f.endswith(".hip"))
 
 
 def build(verbose: bool = False) -> str:
-    """Compile every source and link libssm.so. Returns the library path."""
+    """Compile every source and link both libraries. Returns libssm's path."""
     os.makedirs(BUILD, exist_ok=True)
+    objects = {LIB: sources(), BLOCK_LIB: sources(BLOCK_CSRC)}
     procs = []
-    objs = []
-    for src in sources():
-        obj = os.path.join(BUILD, os.path.basename(src)[:-4] + ".o")
-        objs.append(obj)
+    for src in objects[LIB] + objects[BLOCK_LIB]:
+        obj = _object(src)
         cmd = [HIPCC, *CFLAGS, "-c", src, "-o", obj]
         if verbose:
             print(" ".join(cmd), flush=True)
@@ -59,12 +66,13 @@ def build(verbose: bool = False) -> str:
         for src, text in failed:
             print(f"--- {src}\n{text}", file=sys.stderr)
         raise RuntimeError("hipcc failed for: " + ", ".join(os.path.basename(s) for s, _ in failed))
-    tmp = LIB + ".tmp"
-    link = [HIPCC, "-shared", "-fPIC", f"--offload-arch={ARCH}", *objs, "-o", tmp]
-    if verbose:
-        print(" ".join(link), flush=True)
-    subprocess.check_call(link)
-    os.replace(tmp, LIB)
+    for lib, srcs in objects.items():
+        tmp = lib + ".tmp"
+        link = [HIPCC, "-shared", "-fPIC", f"--offload-arch={ARCH}", *map(_object, srcs), "-o", tmp]
+        if verbose:
+            print(" ".join(link), flush=True)
+        subprocess.check_call(link)
+        os.replace(tmp, lib)
     return LIB
 
 

@@ -1,0 +1,207 @@
+"""Residual addition with RMS norm (plain, 8-bit, backward) against float64."""
+import numpy as np
+import pytest
+import torch
+
+import block_reference as ref
+import state_space_model_ssm_amd as ssm
+
+pytestmark = pytest.mark.gpu
+BF16, F32 = torch.bfloat16, torch.float32
+E4M3 = torch.float8_e4m3fn
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+
+
+def make(rows, dim, dtype, seed):
+    g = torch.Generator().manual_seed(seed)
+    x, res, dy, dres = ((torch.randn(rows, dim, generator=g) * s).to(dtype) for s in (1.0, 2.0, 1.0, 1.0))
+    return x, res, 1 + 0.2 * torch.randn(dim, generator=g), dy, dres
+
+
+def nan(shape, dtype):
+    return torch.full(shape, float("nan"), dtype=dtype, device="cuda")
+
+
+SIZES = [(1, 1), (3, 2), (5, 7), (2, 64), (33, 65), (4, 128), (7, 255), (3, 256), (1, 512), (130, 520), (9, 1000),
+         (2, 1024), (70, 1537), (3, 2048), (5, 4104), (2, 5120), (3, 8192), (2, 8200), (1, 16384), (2, 20001),
+         (1030, 96)]
+
+
+@pytest.mark.parametrize("rows,dim", SIZES)
+@pytest.mark.parametrize("dtype,out", [(F32, F32), (BF16, BF16), (BF16, F32), (F32, BF16)])
+def test_forward(rows, dim, dtype, out):
+    x, res, w, _, _ = make(rows, dim, dtype, rows + dim)
+    y, s = nan((rows, dim), out), nan((rows, dim), dtype)
+    got = ssm.rms_add_fwd(x.cuda(), w.cuda(), res.cuda(), out_dtype=out, y=y, residual_out=s)
+    assert got[0] is y and got[1] is s
+    want, total = ref.rms(x, w, res)
+    ref.assert_close(y, want, ref.storage_tol(want, out), "y")
+    ref.assert_close(s, total, ref.storage_tol(total, dtype), "s")
+    y, s = ssm.rms_add_fwd(x.cuda(), w.cuda(), out_dtype=out, eps=0.1)
+    want, _ = ref.rms(x, w, eps=0.1)
+    ref.assert_close(y, want, ref.storage_tol(want, out), "y without residual")
+    assert torch.equal(s.cpu(), x)
+
+
+@pytest.mark.parametrize("rows,dim", SIZES)
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_backward(rows, dim, dtype):
+    _, s, w, dy, dres = make(rows, dim, dtype, rows * 3 + dim)
+    dx, dw = nan((rows, dim), dtype), nan((dim,), F32)
+    ssm.rms_add_bwd(dy.cuda(), s.cuda(), w.cuda(), dres=dres.cuda(), dx=dx, dw=dw)
+    want, want_w, size = ref.rms_bwd(dy, s, w, dres)
+    ref.assert_close(dx, want, ref.storage_tol(want, dtype), "dx")
+    ref.assert_close(dw, want_w, ref.storage_tol(want_w, F32, size), "dw")
+    dx, none = ssm.rms_add_bwd(dy.cuda(), s.cuda(), w.cuda(), return_dw=False, eps=0.1)
+    want, _, _ = ref.rms_bwd(dy, s, w, eps=0.1)
+    assert none is None
+    ref.assert_close(dx, want, ref.storage_tol(want, dtype), "dx without dres and dw")
+
+
+def test_backward_against_differences():
+    _, s, w, dy, dres = make(3, 70, F32, 1)
+    dx, dw = ssm.rms_add_bwd(dy.cuda(), s.cuda(), w.cuda(), dres=dres.cuda(), eps=1e-3)
+
+    def loss(s, w):
+        return float((ref.rms(s, w, eps=1e-3)[0] * ref.f64(dy)).sum() + (ref.f64(s) * ref.f64(dres)).sum())
+
+    for k, t in enumerate((dx, dw)):
+        for j in np.random.default_rng(k).integers(0, t.numel(), 8):
+            at = [[v.double().clone() for v in (s, w)] for _ in range(2)]
+            at[0][k].view(-1)[j] += 1e-5
+            at[1][k].view(-1)[j] -= 1e-5
+            want = (loss(*at[0]) - loss(*at[1])) / 2e-5
+            assert abs(float(t.view(-1)[j]) - want) <= 1e-5 * max(1.0, float(t.abs().max())), (k, j)
+
+
+@pytest.mark.parametrize("rows,dim,group", [(1, 1, 0), (5, 7, 0), (3, 64, 32), (33, 65, 32), (4, 128, 128), (7, 255, 64),
+                                            (130, 520, 128), (2, 1024, 0), (70, 1537, 128), (3, 2048, 96),
+                                            (2, 5120, 0), (2, 5120, 128), (3, 8200, 128), (1, 20001, 0), (2, 20001, 1024),
+                                            (4, 100, 512)])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_8_bit_output(rows, dim, group, dtype):
+    x, res, w, _, _ = make(rows, dim, dtype, rows + dim)
+    width = group if 0 < group < dim else dim
+    groups = -(-dim // width)
+    q, scale, s = nan((rows, dim), E4M3), nan((rows, groups), F32), nan((rows, dim), dtype)
+    ssm.rms_add_q8_fwd(x.cuda(), w.cuda(), res.cuda(), group=group, q=q, scale=scale, residual_out=s)
+    want, total = ref.rms(x, w, res)
+    ref.assert_close(s, total, ref.storage_tol(total, dtype), "s")
+    tops = np.stack([np.abs(want[:, k * width:(k + 1) * width]).max(1) / 448 for k in range(groups)], 1)
+    ref.assert_close(scale, tops, 1e-6 * tops, "scale")
+    # q is the nearest e4m3 value of y / scale; 1e-6 of its size lets float32 fall on either side of a tie.
+    v = want / np.repeat(ref.f64(scale), width, 1)[:, :dim]
+    table = ref.e4m3_values()
+    got = q.float().cpu().double().numpy()
+    near = table[np.abs(table[None] - v.reshape(-1, 1)).argmin(1)].reshape(v.shape) if v.size < 50000 else None
+    if near is not None:
+        assert np.all(np.abs(got - v) <= np.abs(near - v) + 2e-6 * np.abs(v) + 1e-9)
+    assert np.all(np.abs(got - v) <= np.maximum(np.abs(v) / 16, 2.0 ** -10) * (1 + 1e-5))
+
+
+def test_8_bit_output_of_zeros_and_nan():
+    x = torch.randn(4, 256)
+    x[1] = 0
+    x[2, 130] = float("nan")
+    q, scale, _ = ssm.rms_add_q8_fwd(x.cuda(), torch.ones(256).cuda(), group=128)
+    assert not q[1].float().any() and not scale[1].any()
+    assert torch.isnan(scale[2]).all() and torch.isnan(q[2].float()).all()   # the row's norm is NaN
+    assert not torch.isnan(scale[[0, 1, 3]]).any() and not torch.isnan(q[[0, 1, 3]].float()).any()
+    w = torch.ones(256)
+    w[5] = float("nan")
+    q, scale, _ = ssm.rms_add_q8_fwd(x[:1].cuda(), w.cuda(), group=128)
+    assert torch.isnan(scale[0, 0]) and not torch.isnan(scale[0, 1])
+
+
+def test_rows_do_not_meet():
+    x, res, w, _, _ = make(6, 300, F32, 3)
+    clean, _ = ssm.rms_add_fwd(x.cuda(), w.cuda(), res.cuda())
+    x[2, 7], x[4, 100] = float("inf"), float("nan")
+    y, _ = ssm.rms_add_fwd(x.cuda(), w.cuda(), res.cuda())
+    keep = [0, 1, 3, 5]
+    assert torch.equal(y[keep], clean[keep]) and torch.isnan(y[4]).all() and torch.isnan(y[2, 7])
+
+
+@pytest.mark.parametrize("dtype,dim", [(BF16, 1024), (F32, 1537)])
+def test_in_place(dtype, dim):
+    x, res, w, dy, dres = (t.cuda() for t in make(40, dim, dtype, 4))
+    y, s = ssm.rms_add_fwd(x, w, res)
+    a, b = x.clone(), res.clone()
+    ssm.rms_add_fwd(a, w, b, y=a, residual_out=b)
+    assert torch.equal(a, y) and torch.equal(b, s)
+    a = x.clone()
+    q, scale, s2 = ssm.rms_add_q8_fwd(a, w, res, residual_out=a)
+    assert s2 is a and torch.equal(a, s)
+    dx, _ = ssm.rms_add_bwd(dy, s, w, dres=dres)
+    a = dres.clone()
+    ssm.rms_add_bwd(dy, s, w, dres=a, dx=a)
+    assert torch.equal(a, dx)
+
+
+def test_unaligned_rows():
+    """A tensor that starts at an element, not at a vector: the same values as its aligned copy."""
+    for dtype, dim in ((BF16, 1024), (F32, 512)):
+        flat = torch.randn(9 * dim + 1, device="cuda").to(dtype)
+        x, w = flat[1:].view(9, dim), torch.rand(dim + 1, device="cuda")[1:]
+        y, _ = ssm.rms_add_fwd(x, w)
+        ref_y = ref.rms(x, w)[0]
+        ref.assert_close(y, ref_y, ref.storage_tol(ref_y, dtype), "y")
+        dx, dw = ssm.rms_add_bwd(x, x, w)
+        want, want_w, size = ref.rms_bwd(x, x, w)
+        ref.assert_close(dx, want, ref.storage_tol(want, dtype), "dx")
+        ref.assert_close(dw, want_w, ref.storage_tol(want_w, F32, size), "dw")
+
+
+def test_leading_axes_and_no_rows():
+    w = torch.ones(48, device="cuda")
+    x = torch.randn(2, 3, 5, 48, device="cuda")
+    assert torch.equal(ssm.rms_add_fwd(x, w)[0], ssm.rms_add_fwd(x.view(30, 48), w)[0].view(x.shape))
+    assert ssm.rms_add_q8_fwd(x, w, group=32)[1].shape == (2, 3, 5, 2)
+    e = torch.empty(0, 48, device="cuda")
+    dw = nan((48,), F32)
+    assert ssm.rms_add_fwd(e, w, e)[0].shape == (0, 48) and ssm.rms_add_q8_fwd(e, w)[1].shape == (0, 1)
+    ssm.rms_add_bwd(e, e, w, dw=dw)
+    assert not dw.any()
+
+
+def test_repeats_bit_for_bit_on_another_stream_and_in_a_graph():
+    x, res, w, dy, dres = (t.cuda() for t in make(3000, 640, BF16, 8))
+
+    def all_of(stream=None):
+        y, s = ssm.rms_add_fwd(x, w, res, stream=stream)
+        q, scale, _ = ssm.rms_add_q8_fwd(x, w, res, group=128, stream=stream)
+        return (y, s, q.view(torch.uint8), scale) + ssm.rms_add_bwd(dy, s, w, dres=dres, stream=stream)
+
+    first = [t.clone() for t in all_of()]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    other = all_of(stream=side)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(first, other))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = all_of()
+    for _ in range(3):
+        for t in held:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(first, held))
+        assert all(torch.equal(a, b) for a, b in zip(first, all_of()))
+
+
+def test_offsets_past_32_bits():
+    rows, dim = 262150, 8200
+    x = torch.randn(rows, dim, device="cuda", dtype=BF16)
+    w = torch.rand(dim, device="cuda") + 0.5
+    y, s = ssm.rms_add_fwd(x, w, x)
+    tail = x[-8:].contiguous()
+    y2, s2 = ssm.rms_add_fwd(tail, w, tail)
+    assert torch.equal(y[-8:], y2) and torch.equal(s[-8:], s2)
+    dx, _ = ssm.rms_add_bwd(x, x, w, dres=x, return_dw=False)
+    assert torch.equal(dx[-8:], ssm.rms_add_bwd(tail, tail, w, dres=tail, return_dw=False)[0])
