@@ -94,6 +94,7 @@ int check_workspace(const void *ws, size_t have, size_t need) {
 }
 
 constexpr int64_t kMaxGrid = 2147483647;
+constexpr int64_t kMaxToken = int64_t{1} << 24;  // elements between two tokens
 
 // ---------------------------------------------------------------------------
 // Gated linear recurrence
@@ -201,6 +202,8 @@ int check_swa(const ssm_swa_dims_t *d, bool step) {
   for (const int64_t s : strides)
     if (s < 0 || s % 8 != 0 || s > (int64_t{1} << 40))
       return fail(SSM_ERR_SHAPE, "strides must be multiples of 8 elements, not negative (got %lld)", (long long)s);
+  if (d->q_token > kMaxToken || d->k_token > kMaxToken || d->v_token > kMaxToken)
+    return fail(SSM_ERR_UNSUPPORTED, "token strides must be at most 2^24 elements");
   if (d->seqlen > 1 && (d->q_token < d->nheads * d->headdim || d->k_token < d->nkv * d->headdim ||
                         d->v_token < d->nkv * d->headdim))
     return fail(SSM_ERR_SHAPE, "a token stride is smaller than the token");

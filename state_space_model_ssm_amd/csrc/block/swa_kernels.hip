@@ -1,151 +1,245 @@
-// Sliding-window attention with sinks for gfx950.
+// Sliding-window attention with sinks for gfx950, forward.
 //
-// Query t sees key j when j <= t < length and (t - j < window or j < sinks).
-// Simplest form: one wavefront per query (forward, dq) or per key (dk, dv),
-// lanes over the head's elements, one pass with the running maximum and sum.
-#include "block_internal.h"
+// Query t sees key j when j <= t < length and (t - j < window or j < sinks):
+//   y_t = sum_j exp(scale q_t.k_j) v_j / sum_j exp(scale q_t.k_j)
+// in one pass over the keys with a running maximum and sum.
+//
+// A wavefront takes 32 queries of one head; the four of a workgroup share
+// tiles of 64 keys and values in LDS and take up to four heads of a group
+// over the same 32 queries (few tiles that only part of the workgroup sees)
+// or up to 128 queries of one head.  S^T = K Q^T leaves a query's scores in
+// one lane (and its other half), so the softmax needs one exchange per tile,
+// and p goes into O^T = V^T P^T as it lies (see swa_tile.h).
+#include "swa_tile.h"
 
 namespace ssmb {
 namespace {
 
-__device__ __forceinline__ float wave_sum(float v) {
+constexpr float kLn2 = 0.6931471805599453f;
+// The running maximum is raised (and what is summed so far scaled down) only
+// when a score passes it by this factor's log2: p stays below 2^8, which
+// costs no precision in float32 or bfloat16.
+constexpr float kSlack = 8.0f;
+
+// Bits 15 and 31 are set where that half, a bfloat16, is an infinity or NaN.
+__device__ __forceinline__ unsigned not_finite(unsigned x) { return (x & 0x7fff7fffu) + 0x00800080u; }
+
+// What the infinities and NaN of a tile of values add to the queries that see
+// them, out[db] += vis * v over those elements alone.  vis: 1 or 0 per key.
+template <int D>
+__device__ __forceinline__ void add_not_finite(const u4 *tile, const bf8 (&vis)[4], f16v (&out)[D / 32], int lane) {
 #pragma unroll
-  for (int m = 1; m < 64; m <<= 1) v += __shfl_xor(v, m);
-  return v;
-}
-
-__device__ __forceinline__ int64_t row_length(const SwaParams &p, int64_t b) {
-  if (p.lengths == nullptr) return p.seqlen;
-  const int64_t n = p.lengths[b];
-  return n < 0 ? 0 : n > p.seqlen ? p.seqlen : n;
-}
-
-template <int D>
-__global__ void __launch_bounds__(64) swa_fwd_kernel(const SwaParams p) {
-  constexpr int E = D / 64;
-  const int lane = threadIdx.x;
-  const int64_t t = blockIdx.x, b = blockIdx.y / p.nheads, h = blockIdx.y % p.nheads;
-  const int64_t c = h / (p.nheads / p.nkv);
-  const int64_t out = ((b * p.seqlen + t) * p.nheads + h) * D;
-  float acc[E] = {}, top = -INFINITY, sum = 0.0f;
-  if (t < row_length(p, b)) {
-    float q[E];
-    for (int e = 0; e < E; ++e) q[e] = ld(p.q, b * p.q_batch + t * p.q_token + h * D + lane + 64 * e) * p.scale;
-    const int64_t lo = t - p.window + 1 > 0 ? t - p.window + 1 : 0;
-    for (int64_t j = p.sinks > 0 ? 0 : lo; j <= t; ++j) {
-      if (j >= p.sinks && j < lo) j = lo;
-      float s = 0.0f;
-      for (int e = 0; e < E; ++e) s = fmaf(q[e], ld(p.k, b * p.k_batch + j * p.k_token + c * D + lane + 64 * e), s);
-      s = wave_sum(s);
-      const float m = s > top ? s : top;
-      const float keep = __builtin_amdgcn_exp2f((top - m) * kLog2e), w = __builtin_amdgcn_exp2f((s - m) * kLog2e);
-      sum = fmaf(sum, keep, w);
-      for (int e = 0; e < E; ++e)
-        acc[e] = fmaf(acc[e], keep, w * ld(p.v, b * p.v_batch + j * p.v_token + c * D + lane + 64 * e));
-      top = m;
-    }
-  }
-  for (int e = 0; e < E; ++e) st(p.y, out + lane + 64 * e, sum != 0.0f ? acc[e] / sum : 0.0f);
-  if (p.lse != nullptr && lane == 0)
-    p.lse[(b * p.nheads + h) * p.seqlen + t] = sum != 0.0f ? top + logf(sum) : -INFINITY;
-}
-
-// dq and delta = dy.y of one query.
-template <int D>
-__global__ void __launch_bounds__(64) swa_dq_kernel(const SwaParams p) {
-  constexpr int E = D / 64;
-  const int lane = threadIdx.x;
-  const int64_t t = blockIdx.x, b = blockIdx.y / p.nheads, h = blockIdx.y % p.nheads;
-  const int64_t c = h / (p.nheads / p.nkv);
-  const int64_t out = ((b * p.seqlen + t) * p.nheads + h) * D;
-  float acc[E] = {}, delta = 0.0f;
-  if (t < row_length(p, b)) {
-    const float lse = p.lse[(b * p.nheads + h) * p.seqlen + t];
-    float q[E], dy[E];
-    for (int e = 0; e < E; ++e) {
-      q[e] = ld(p.q, b * p.q_batch + t * p.q_token + h * D + lane + 64 * e) * p.scale;
-      dy[e] = ld(p.dy, out + lane + 64 * e);
-      delta = fmaf(dy[e], ld(p.y, out + lane + 64 * e), delta);
-    }
-    delta = wave_sum(delta);
-    const int64_t lo = t - p.window + 1 > 0 ? t - p.window + 1 : 0;
-    for (int64_t j = p.sinks > 0 ? 0 : lo; j <= t; ++j) {
-      if (j >= p.sinks && j < lo) j = lo;
-      float s = 0.0f, dp = 0.0f, k[E];
-      for (int e = 0; e < E; ++e) {
-        k[e] = ld(p.k, b * p.k_batch + j * p.k_token + c * D + lane + 64 * e);
-        s = fmaf(q[e], k[e], s);
-        dp = fmaf(dy[e], ld(p.v, b * p.v_batch + j * p.v_token + c * D + lane + 64 * e), dp);
-      }
-      const float w = __builtin_amdgcn_exp2f((wave_sum(s) - lse) * kLog2e);
-      const float ds = w * (wave_sum(dp) - delta) * p.scale;
-      for (int e = 0; e < E; ++e) acc[e] = fmaf(ds, k[e], acc[e]);
-    }
-  }
-  for (int e = 0; e < E; ++e) st(p.dq, out + lane + 64 * e, acc[e]);
-  if (lane == 0) p.ws_delta[(b * p.nheads + h) * p.seqlen + t] = delta;
-}
-
-// dk and dv of one key, over the queries and the group's heads that see it.
-template <int D>
-__global__ void __launch_bounds__(64) swa_dkv_kernel(const SwaParams p) {
-  constexpr int E = D / 64;
-  const int lane = threadIdx.x;
-  const int64_t j = blockIdx.x, b = blockIdx.y / p.nkv, c = blockIdx.y % p.nkv, group = p.nheads / p.nkv;
-  const int64_t n = row_length(p, b);
-  float dk[E] = {}, dv[E] = {};
-  if (j < n) {
-    float k[E], v[E];
-    for (int e = 0; e < E; ++e) {
-      k[e] = ld(p.k, b * p.k_batch + j * p.k_token + c * D + lane + 64 * e);
-      v[e] = ld(p.v, b * p.v_batch + j * p.v_token + c * D + lane + 64 * e);
-    }
-    const int64_t hi = j < p.sinks || n - j < p.window ? n : j + p.window;
-    for (int64_t h = c * group; h < (c + 1) * group; ++h) {
-      for (int64_t t = j; t < hi; ++t) {
-        const int64_t row = ((b * p.seqlen + t) * p.nheads + h) * D, at = (b * p.nheads + h) * p.seqlen + t;
-        float q[E], dy[E], s = 0.0f, dp = 0.0f;
-        for (int e = 0; e < E; ++e) {
-          q[e] = ld(p.q, b * p.q_batch + t * p.q_token + h * D + lane + 64 * e) * p.scale;
-          dy[e] = ld(p.dy, row + lane + 64 * e);
-          s = fmaf(q[e], k[e], s);
-          dp = fmaf(dy[e], v[e], dp);
+  for (int db = 0; db < D / 32; ++db) {
+#pragma unroll
+    for (int kind = 0; kind < 3; ++kind) {  // +inf, -inf, NaN
+      f16v count = {};
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        u4 v = __builtin_bit_cast(u4, col_operand<D>(tile, 16 * s, db, lane));
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          auto is = [&](unsigned b) {
+            return kind == 0 ? b == 0x7f80u : kind == 1 ? b == 0xff80u : (b & 0x7fffu) > 0x7f80u;
+          };
+          v[k] = (is(v[k] & 0xffffu) ? 0x3f80u : 0u) | (is(v[k] >> 16) ? 0x3f800000u : 0u);  // 1 or 0
         }
-        const float w = __builtin_amdgcn_exp2f((wave_sum(s) - p.lse[at]) * kLog2e);
-        const float ds = w * (wave_sum(dp) - p.ws_delta[at]);
-        for (int e = 0; e < E; ++e) {
-          dk[e] = fmaf(ds, q[e], dk[e]);
-          dv[e] = fmaf(w, dy[e], dv[e]);
+        count = mfma(__builtin_bit_cast(bf8, v), vis[s], count);
+      }
+      const float add = kind == 0 ? INFINITY : kind == 1 ? -INFINITY : NAN;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) out[db][i] += count[i] > 0.0f ? add : 0.0f;
+    }
+  }
+}
+
+// What a workgroup knows of its work.
+struct FwdWork {
+  const uint16_t *k, *v;  // of the key head
+  int wq0;                // first query of this wavefront
+  int len, lo, ns, tiles; // length; first window tile; sink tiles before it; tiles in all
+  float c2;               // |scale| log2(e)
+};
+
+// One pass over the keys: o and sum (of this lane's half of the keys) of the
+// lane's query t, with weights 2^(c2 s - top).  Returns whether a tile that
+// some query sees in part held an infinity or NaN among its values: their
+// products with weights of 0 would reach queries that do not see them.  SAFE
+// keeps them out of the product and adds what they are worth by themselves.
+template <int D, bool SAFE>
+__device__ __forceinline__ bool attend(const SwaParams &p, const FwdWork &w, u4 (&lds)[2][2][kTile * D / 8],
+                                       const bf8 (&q)[D / 16], f16v (&o)[D / 32], float &top, float &sum, int tid) {
+  constexpr int CH = D / 8, NB = D / 32, NS = D / 16;
+  const int lane = tid & 63, half = lane >> 5, t = w.wq0 + (lane & 31);
+  const int window = static_cast<int>(p.window), sinks = static_cast<int>(p.sinks);
+  const int own = sinks < t + 1 ? sinks : t + 1;  // sinks this query sees
+  unsigned bad = 0;
+  top = -INFINITY;
+  sum = 0.0f;
+#pragma unroll
+  for (int db = 0; db < NB; ++db) o[db] = f16v{};
+  auto start = [&](int i) {
+    const int k0 = (i < w.ns ? i : w.lo + i - w.ns) * kTile;
+    load_tile<D, 256>(lds[i & 1][0], w.k, p.k_token, k0, w.len - 1, tid);
+    load_tile<D, 256>(lds[i & 1][1], w.v, p.v_token, k0, w.len - 1, tid);
+  };
+  start(0);
+  for (int i = 0; i < w.tiles; ++i) {
+    wait_tiles();
+    __syncthreads();  // tile i has landed, and nobody reads the other buffer any more
+    if (i + 1 < w.tiles) start(i + 1);
+    const int k0 = (i < w.ns ? i : w.lo + i - w.ns) * kTile;
+    const u4 *kt = lds[i & 1][0], *vt = lds[i & 1][1];
+    // Does this wavefront see any of the tile, or all of it?
+    if (k0 > w.wq0 + 31 || (k0 + kTile - 1 <= w.wq0 - window && k0 >= sinks) || w.wq0 >= w.len) continue;
+    const bool whole = k0 + kTile - 1 <= w.wq0 && w.wq0 + 31 - k0 < window;
+    f16v s[2] = {};
+#pragma unroll
+    for (int blk = 0; blk < 2; ++blk)
+#pragma unroll
+      for (int ks = 0; ks < NS; ++ks) s[blk] = mfma(row_operand<D>(kt, 32 * blk, ks, lane), q[ks], s[blk]);
+    auto sees = [&](int blk, int r) {
+      const int j = k0 + 32 * blk + d_row(r, half);
+      return static_cast<unsigned>(t - j) < static_cast<unsigned>(window) || j < own;
+    };
+    if (!whole) {
+#pragma unroll
+      for (int blk = 0; blk < 2; ++blk)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) s[blk][r] = sees(blk, r) ? s[blk][r] : -INFINITY;
+      if constexpr (SAFE) {
+        bf8 vis[4];
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) vis[ks][e] = static_cast<__bf16>(sees(ks / 2, (ks % 2) * 8 + e) ? 1.0f : 0.0f);
+        add_not_finite<D>(vt, vis, o, lane);
+      } else {
+#pragma unroll
+        for (int k = 0; k < kTile * CH / 64; ++k) {
+          const u4 v = vt[k * 64 + lane];
+          bad |= not_finite(v[0]) | not_finite(v[1]) | not_finite(v[2]) | not_finite(v[3]);
         }
       }
     }
+    float m = s[0][0];
+#pragma unroll
+    for (int r = 1; r < 32; ++r) m = fmaxf(m, s[r / 16][r % 16]);
+    m = fmaxf(m, other_half(m)) * w.c2;
+    if (__any(m > top + kSlack)) {
+      const float now = m > top + kSlack ? m : top;  // by each query for itself: no row's bits depend on another's
+      const float keep = now == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(top - now);
+      sum *= keep;
+#pragma unroll
+      for (int db = 0; db < NB; ++db)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) o[db][r] *= keep;
+      top = now;
+    }
+    const float off = top == -INFINITY ? 0.0f : top;
+    float part[2] = {};
+#pragma unroll
+    for (int blk = 0; blk < 2; ++blk)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        s[blk][r] = __builtin_amdgcn_exp2f(fmaf(s[blk][r], w.c2, -off));
+        part[r & 1] += s[blk][r];
+      }
+    sum += part[0] + part[1];
+#pragma unroll
+    for (int ks = 0; ks < 4; ++ks) {
+      const bf8 pk = as_operand(s[ks / 2], ks % 2);
+#pragma unroll
+      for (int db = 0; db < NB; ++db) {
+        u4 v = __builtin_bit_cast(u4, col_operand<D>(vt, 16 * ks, db, lane));
+        if constexpr (SAFE) {
+          if (!whole) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[k] &= ~(((not_finite(v[k]) >> 15) & 0x00010001u) * 0xffffu);
+          }
+        }
+        o[db] = mfma(__builtin_bit_cast(bf8, v), pk, o[db]);
+      }
+    }
   }
-  const int64_t out = ((b * p.seqlen + j) * p.nkv + c) * D;
-  for (int e = 0; e < E; ++e) {
-    st(p.dk, out + lane + 64 * e, dk[e]);
-    st(p.dv, out + lane + 64 * e, dv[e]);
+  return (bad & 0x80008000u) != 0;
+}
+
+template <int D>
+__global__ void __launch_bounds__(256, 2) swa_fwd_kernel(const SwaParams p, int hw, unsigned qtiles, unsigned n) {
+  constexpr int CH = D / 8, NB = D / 32, NS = D / 16;
+  __shared__ __align__(16) u4 lds[2][2][kTile * CH];  // buffer, K or V
+  __shared__ int found;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, half = lane >> 5;
+  const unsigned nheads = static_cast<unsigned>(p.nheads), nkv = static_cast<unsigned>(p.nkv);
+  const unsigned group = nheads / nkv, hb = group / hw;
+  // Work order: query tile fastest, then head block of a key head, key head, batch row.
+  const unsigned id = xcd_order(blockIdx.x, n);
+  const unsigned qt = id % qtiles, rest = id / qtiles;
+  const int64_t b = rest / (hb * nkv), c = rest / hb % nkv;
+  const int64_t head = c * group + (rest % hb) * hw + wave % hw;
+  const int qspan = 32 * (4 / hw), q0 = static_cast<int>(qt) * qspan;
+  FwdWork w;
+  w.len = row_length(p, b);
+  w.wq0 = q0 + 32 * (wave / hw);
+  w.c2 = fmaxf(fabsf(p.scale) * kLog2e, 0x1p-100f);
+  const int t = w.wq0 + (lane & 31), L = static_cast<int>(p.seqlen);  // t: this lane's query
+
+  f16v o[NB] = {};
+  float top = -INFINITY, sum = 0.0f;
+  if (q0 < w.len) {
+    const int last = w.len - 1, qlast = q0 + qspan - 1 < last ? q0 + qspan - 1 : last;
+    const int window = static_cast<int>(p.window), sinks = static_cast<int>(p.sinks);
+    w.k = p.k + b * p.k_batch + c * D;
+    w.v = p.v + b * p.v_batch + c * D;
+    w.lo = q0 - window + 1 > 0 ? (q0 - window + 1) / kTile : 0;
+    const int seen = ((sinks < qlast + 1 ? sinks : qlast + 1) + kTile - 1) / kTile;
+    w.ns = seen < w.lo ? seen : w.lo;
+    w.tiles = w.ns + qlast / kTile - w.lo + 1;
+    bf8 q[NS];
+    const int row = t < last ? t : last;
+    const u4 *src = reinterpret_cast<const u4 *>(p.q + b * p.q_batch + row * p.q_token + head * D);
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+      u4 v = src[2 * s + half];
+      if (p.scale < 0.0f) v ^= 0x80008000u;  // a negative scale is taken as -q
+      q[s] = __builtin_bit_cast(bf8, v);
+    }
+    if (tid == 0) found = 0;  // before the first barrier in attend()
+    const bool bad = attend<D, false>(p, w, lds, q, o, top, sum, tid);
+    if (__any(bad)) found = 1;
+    __syncthreads();
+    if (found) attend<D, true>(p, w, lds, q, o, top, sum, tid);
   }
+  sum += other_half(sum);
+  if (t >= L) return;
+  const bool none = t >= w.len || sum == 0.0f;
+  const float inv = none ? 0.0f : 1.0f / sum;
+  uint16_t *out = p.y + ((b * p.seqlen + t) * p.nheads + head) * D;
+#pragma unroll
+  for (int db = 0; db < NB; ++db)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      bf4 v;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) v[r] = static_cast<__bf16>(none ? 0.0f : o[db][4 * j + r] * inv);
+      *reinterpret_cast<bf4 *>(out + 32 * db + 8 * j + 4 * half) = v;
+    }
+  if (p.lse != nullptr && half == 0)
+    p.lse[(b * p.nheads + head) * p.seqlen + t] = none ? -INFINITY : top * kLn2 + logf(sum);
 }
 
 }  // namespace
 
 hipError_t launch_swa_fwd(const SwaParams &p, hipStream_t s) {
-  const dim3 g(static_cast<uint32_t>(p.seqlen), static_cast<uint32_t>(p.batch * p.nheads)), t(64);
-  if (p.headdim == 64) hipLaunchKernelGGL((swa_fwd_kernel<64>), g, t, 0, s, p);
-  else hipLaunchKernelGGL((swa_fwd_kernel<128>), g, t, 0, s, p);
-  return hipGetLastError();
-}
-
-hipError_t launch_swa_bwd(const SwaParams &p, hipStream_t s) {
-  const dim3 g(static_cast<uint32_t>(p.seqlen), static_cast<uint32_t>(p.batch * p.nheads)), t(64);
-  const dim3 gk(static_cast<uint32_t>(p.seqlen), static_cast<uint32_t>(p.batch * p.nkv));
-  if (p.headdim == 64) {
-    hipLaunchKernelGGL((swa_dq_kernel<64>), g, t, 0, s, p);
-    hipLaunchKernelGGL((swa_dkv_kernel<64>), gk, t, 0, s, p);
-  } else {
-    hipLaunchKernelGGL((swa_dq_kernel<128>), g, t, 0, s, p);
-    hipLaunchKernelGGL((swa_dkv_kernel<128>), gk, t, 0, s, p);
-  }
+  const int64_t group = p.nheads / p.nkv;
+  const int hw = group % 4 == 0 ? 4 : group % 2 == 0 ? 2 : 1;
+  const int64_t qspan = 32 * (4 / hw), qtiles = (p.seqlen + qspan - 1) / qspan;
+  const int64_t n = qtiles * (group / hw) * p.nkv * p.batch;
+  if (n > 0x7fffffff) return hipErrorInvalidValue;
+  const dim3 g(static_cast<uint32_t>(n)), t(256);
+  const unsigned qt = static_cast<unsigned>(qtiles), un = static_cast<unsigned>(n);
+  if (p.headdim == 64) hipLaunchKernelGGL((swa_fwd_kernel<64>), g, t, 0, s, p, hw, qt, un);
+  else hipLaunchKernelGGL((swa_fwd_kernel<128>), g, t, 0, s, p, hw, qt, un);
   return hipGetLastError();
 }
 

@@ -1,0 +1,122 @@
+// Tiles of the sliding-window attention kernels: 64 rows of one head in LDS,
+// read as matrix-core operands along the head's elements (rows) or along the
+// rows (transposed).
+//
+// v_mfma_f32_32x32x16_bf16, lane l with m = l % 32, h = l / 32: A holds row m,
+// k = 8h .. 8h + 7; B column m, the same k; D column m, rows 8j + 4h + r in
+// register 4j + r.  A sum over k does not care for its order as long as A and
+// B agree, so where D becomes the next product's B (p and ds), k is counted
+// as D's rows lie: element 4j + r of lane half h stands for row 8j + 4h + r of
+// 16, and the A operand is read from LDS in that order.  No value crosses
+// lanes between the two products.
+#pragma once
+
+#include "block_internal.h"
+
+namespace ssmb {
+
+typedef __attribute__((ext_vector_type(8))) __bf16 bf8;
+typedef __attribute__((ext_vector_type(4))) __bf16 bf4;
+typedef __attribute__((ext_vector_type(4))) short sh4;
+typedef __attribute__((ext_vector_type(16))) float f16v;
+typedef __attribute__((ext_vector_type(4))) unsigned int u4;
+
+constexpr int kTile = 64;  // rows of a tile
+
+__device__ __forceinline__ f16v mfma(bf8 a, bf8 b, f16v c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+
+// LDS slot of 16-byte chunk c of row r.  Rows are a whole (D = 128) or half
+// (D = 64) a turn of the 64 banks, so chunk c of all rows would share its
+// banks; c is exchanged with a rotated row number instead.  16 rows in turn
+// then fill the 16 slots of the banks (row reads), and so do the four rows by
+// two chunks that 16 lanes of a transposed read take.
+template <int D>
+__device__ __forceinline__ int slot(int r, int c) {
+  if constexpr (D == 128) return r * 16 + (c ^ (((r & 7) << 1) | ((r >> 3) & 1)));
+  else return r * 8 + (c ^ ((((r >> 1) & 3) << 1) | ((r >> 3) & 1)));
+}
+
+// Operand of rows base .. base + 31, elements 16 s + 8 h .. + 7.
+template <int D>
+__device__ __forceinline__ bf8 row_operand(const u4 *tile, int base, int s, int lane) {
+  return __builtin_bit_cast(bf8, tile[slot<D>(base + (lane & 31), 2 * s + (lane >> 5))]);
+}
+
+// Operand of elements (columns) 32 db + lane % 32 over rows base .. base + 15
+// in the order above: two transposing reads of 4 rows each.
+template <int D>
+__device__ __forceinline__ bf8 col_operand(const u4 *tile, int base, int db, int lane) {
+  const int i = lane & 15, g = (lane >> 4) & 1, h = lane >> 5;
+  const int c = db * 4 + g * 2 + ((i >> 1) & 1), r = base + 4 * h + (i >> 2);
+  typedef __attribute__((address_space(3))) sh4 lds4;
+  typedef __attribute__((address_space(3))) char ldsc;
+  ldsc *at = (ldsc *)tile;
+  const sh4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)(at + slot<D>(r, c) * 16 + (i & 1) * 8));
+  const sh4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)(at + slot<D>(r + 8, c) * 16 + (i & 1) * 8));
+  return __builtin_bit_cast(bf8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+
+// Registers 8 s .. 8 s + 7 of a D result as the B operand over its rows 16 s .. 16 s + 15.
+__device__ __forceinline__ bf8 as_operand(const f16v &d, int s) {
+  bf8 v;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = static_cast<__bf16>(d[8 * s + e]);
+  return v;
+}
+
+// The row that register i of a D result stands for in lane half h.
+__device__ __forceinline__ constexpr int d_row(int i, int h) { return 8 * (i / 4) + 4 * h + i % 4; }
+
+// Start the copy of tile rows t0 .. t0 + 63 of a strided tensor (p: row 0 of
+// the head) into LDS, `NT` threads of the workgroup taking part; rows past
+// `last` are read as row `last`, so nothing past a length is touched.  The
+// copy goes from memory to LDS without registers: a wavefront's 64 pieces of
+// 16 bytes land in order from the address in M0, so the slots are permuted by
+// the source address.  In asm, because the compiler would wait for the copy
+// before any LDS read, of the other buffer too: wait_tiles() waits for it.
+// (M0 has no other use in these kernels.)
+template <int D, int NT>
+__device__ __forceinline__ void load_tile(u4 *tile, const uint16_t *p, int64_t token, int t0, int last, int tid) {
+  constexpr int CH = D / 8;
+  const uint16_t *base = p + t0 * token;
+  const unsigned stride = static_cast<unsigned>(token) * 2;  // at most 2^25 bytes, so 63 rows fit 32 bits
+  const unsigned lds = __builtin_amdgcn_readfirstlane(
+      static_cast<unsigned>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) void *)(tile))) +
+      (tid & ~63) * 16);
+#pragma unroll
+  for (int k = 0; k < kTile * CH / NT; ++k) {
+    const int id = k * NT + tid, r = id / CH;
+    const int c = slot<D>(r, id % CH) - r * CH;  // slot() is its own inverse within a row
+    const unsigned off = static_cast<unsigned>(r < last - t0 ? r : last - t0) * stride + c * 16;
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+                 :
+                 : "s"(lds + k * NT * 16), "v"(off), "s"(base)
+                 : "memory");
+  }
+}
+
+// Every copy this wavefront has started has landed.
+__device__ __forceinline__ void wait_tiles() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
+__device__ __forceinline__ float other_half(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float((threadIdx.x & 32) ? r[0] : r[1]);
+}
+
+__device__ __forceinline__ int row_length(const SwaParams &p, int64_t b) {
+  if (p.lengths == nullptr) return static_cast<int>(p.seqlen);
+  const int n = p.lengths[b], L = static_cast<int>(p.seqlen);
+  return n < 0 ? 0 : n > L ? L : n;
+}
+
+// Workgroup number -> work number: the hardware deals workgroups out to the 8
+// XCDs in turn, and each XCD has its own L2, so each XCD gets a contiguous
+// range of the work (neighbouring tiles of a head read the same keys).
+__device__ __forceinline__ unsigned xcd_order(unsigned id, unsigned n) {
+  const unsigned x = id & 7, k = id >> 3, base = n >> 3, extra = n & 7;
+  return x * base + (x < extra ? x : extra) + k;
+}
+
+}  // namespace ssmb
