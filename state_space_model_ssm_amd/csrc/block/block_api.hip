@@ -244,8 +244,16 @@ ssmb::SwaParams swa_params(const ssm_swa_dims_t &d, const void *q, const void *k
   return p;
 }
 
+ssmb::SwaBwdPlan swa_plan(const ssm_swa_dims_t &d) {
+  return ssmb::swa_bwd_plan(d.batch, d.seqlen, d.nheads, d.nkv, d.window, d.sinks);
+}
+
+// log2(e) lse and dy.y of every query, then the terms of dk and dv.
+size_t swa_bwd_stats(const ssm_swa_dims_t &d) { return up256(static_cast<size_t>(d.batch) * d.nheads * d.seqlen * 4); }
 size_t swa_bwd_workspace(const ssm_swa_dims_t &d) {
-  return up256(static_cast<size_t>(d.batch) * d.nheads * d.seqlen * 4);
+  const ssmb::SwaBwdPlan plan = swa_plan(d);
+  const size_t part = plan.has_parts ? static_cast<size_t>(plan.items) * d.batch * d.nkv * 2 * 128 * d.headdim * 4 : 0;
+  return 2 * swa_bwd_stats(d) + part;
 }
 
 size_t swa_step_workspace(const ssm_swa_dims_t &) { return 0; }
@@ -500,8 +508,11 @@ int ssm_swa_bwd(const void *q, const void *k, const void *v, const int32_t *leng
   p.dq = static_cast<uint16_t *>(dq);
   p.dk = static_cast<uint16_t *>(dk);
   p.dv = static_cast<uint16_t *>(dv);
-  p.ws_delta = static_cast<float *>(d.workspace);
-  return launched(ssmb::launch_swa_bwd(p, static_cast<hipStream_t>(stream)), "swa_bwd");
+  char *ws = static_cast<char *>(d.workspace);
+  p.ws_lse2 = reinterpret_cast<float *>(ws);
+  p.ws_delta = reinterpret_cast<float *>(ws + swa_bwd_stats(d));
+  p.ws_part = reinterpret_cast<float *>(ws + 2 * swa_bwd_stats(d));
+  return launched(ssmb::launch_swa_bwd(p, swa_plan(d), static_cast<hipStream_t>(stream)), "swa_bwd");
 }
 
 int ssm_swa_step_workspace_size(const ssm_swa_dims_t *dims, size_t *bytes) {

@@ -169,7 +169,8 @@ __global__ void __launch_bounds__(256, 2) swa_fwd_kernel(const SwaParams p, int 
   constexpr int CH = D / 8, NB = D / 32, NS = D / 16;
   __shared__ __align__(16) u4 lds[2][2][kTile * CH];  // buffer, K or V
   __shared__ int found;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, half = lane >> 5;
+  const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const unsigned nheads = static_cast<unsigned>(p.nheads), nkv = static_cast<unsigned>(p.nkv);
   const unsigned group = nheads / nkv, hb = group / hw;
   // Work order: query tile fastest, then head block of a key head, key head, batch row.

@@ -97,6 +97,18 @@ __device__ __forceinline__ void load_tile(u4 *tile, const uint16_t *p, int64_t t
   }
 }
 
+// The same for one float of each of the rows t0 .. t0 + 63, by one wavefront.
+__device__ __forceinline__ void load_stats(float *to, const float *p, int t0, int last, int lane) {
+  const unsigned off = static_cast<unsigned>(lane < last - t0 ? lane : last - t0) * 4;
+  const unsigned lds = __builtin_amdgcn_readfirstlane(
+      static_cast<unsigned>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) void *)(to))));
+  const float *base = p + t0;
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2"
+               :
+               : "s"(lds), "v"(off), "s"(base)
+               : "memory");
+}
+
 // Every copy this wavefront has started has landed.
 __device__ __forceinline__ void wait_tiles() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 

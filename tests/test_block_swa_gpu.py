@@ -50,6 +50,7 @@ CASES = [  # B, L, H, KV, d, window, sinks
     (1, 64, 8, 2, 128, 16, 4), (2, 65, 4, 2, 64, 64, 1), (1, 127, 2, 2, 128, 500, 0), (1, 128, 5, 5, 64, 1, 3),
     (1, 130, 6, 2, 128, 1, 0), (1, 200, 4, 1, 64, 63, 64), (1, 257, 8, 1, 128, 65, 70), (1, 300, 2, 1, 64, 100, 150),
     (1, 500, 16, 2, 64, 129, 4), (3, 190, 7, 7, 128, 96, 16), (1, 700, 4, 2, 128, 256, 4), (1, 1500, 2, 1, 64, 200, 1),
+    (1, 1300, 4, 2, 128, 90, 140), (2, 1100, 3, 1, 64, 40, 4),
 ]
 
 
