@@ -256,7 +256,16 @@ size_t swa_bwd_workspace(const ssm_swa_dims_t &d) {
   return 2 * swa_bwd_stats(d) + part;
 }
 
-size_t swa_step_workspace(const ssm_swa_dims_t &) { return 0; }
+int swa_splits(const ssm_swa_dims_t &d) { return ssmb::swa_step_splits(d.batch, d.nheads, d.nkv, d.sinks + d.window); }
+
+// Per (row, head, split): the sum of values, then the maximum and sum of weights.
+size_t swa_step_sums(const ssm_swa_dims_t &d) {
+  return up256(static_cast<size_t>(d.batch) * d.nheads * swa_splits(d) * d.headdim * 4);
+}
+size_t swa_step_workspace(const ssm_swa_dims_t &d) {
+  const size_t rows = static_cast<size_t>(d.batch) * d.nheads * swa_splits(d);
+  return swa_splits(d) > 1 ? swa_step_sums(d) + up256(rows * 8) : 0;
+}
 
 }  // namespace
 
@@ -562,7 +571,9 @@ int ssm_swa_step(const void *q, const void *k, const void *v, void *k_cache, voi
   p.v_batch = d.v_batch;
   p.scale = d.scale;
   p.headdim = static_cast<int32_t>(d.headdim);
-  return launched(ssmb::launch_swa_step(p, static_cast<hipStream_t>(stream)), "swa_step");
+  p.ws_o = static_cast<float *>(d.workspace);
+  if (d.workspace) p.ws_stat = reinterpret_cast<float *>(static_cast<char *>(d.workspace) + swa_step_sums(d));
+  return launched(ssmb::launch_swa_step(p, swa_splits(d), static_cast<hipStream_t>(stream)), "swa_step");
 }
 
 int ssm_swa_fill(const void *k, const void *v, const int32_t *lengths, void *k_cache, void *v_cache,

@@ -103,12 +103,15 @@ struct SwaStepParams {
   uint16_t *k_cache, *v_cache;
   const int32_t *pos;
   uint16_t *y;
+  float *ws_o, *ws_stat;       // per (row, head, split): [headdim], and maximum and sum
   int64_t batch, nheads, nkv, window, sinks;
   int64_t q_batch, k_batch, v_batch;
   float scale;
   int32_t headdim;
 };
-hipError_t launch_swa_step(const SwaStepParams &p, hipStream_t stream);
+// Workgroups that share the slots of a (row, key head).
+int swa_step_splits(int64_t batch, int64_t nheads, int64_t nkv, int64_t slots);
+hipError_t launch_swa_step(const SwaStepParams &p, int splits, hipStream_t stream);
 
 // Cache fill: k, v (batch, seqlen, nkv, headdim) into the ring.
 hipError_t launch_swa_fill(const SwaParams &p, uint16_t *k_cache, uint16_t *v_cache, hipStream_t stream);

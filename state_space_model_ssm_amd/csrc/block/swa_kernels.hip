@@ -16,10 +16,6 @@ namespace ssmb {
 namespace {
 
 constexpr float kLn2 = 0.6931471805599453f;
-// The running maximum is raised (and what is summed so far scaled down) only
-// when a score passes it by this factor's log2: p stays below 2^8, which
-// costs no precision in float32 or bfloat16.
-constexpr float kSlack = 8.0f;
 
 // Bits 15 and 31 are set where that half, a bfloat16, is an infinity or NaN.
 __device__ __forceinline__ unsigned not_finite(unsigned x) { return (x & 0x7fff7fffu) + 0x00800080u; }
@@ -121,30 +117,7 @@ __device__ __forceinline__ bool attend(const SwaParams &p, const FwdWork &w, u4 
         }
       }
     }
-    float m = s[0][0];
-#pragma unroll
-    for (int r = 1; r < 32; ++r) m = fmaxf(m, s[r / 16][r % 16]);
-    m = fmaxf(m, other_half(m)) * w.c2;
-    if (__any(m > top + kSlack)) {
-      const float now = m > top + kSlack ? m : top;  // by each query for itself: no row's bits depend on another's
-      const float keep = now == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(top - now);
-      sum *= keep;
-#pragma unroll
-      for (int db = 0; db < NB; ++db)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) o[db][r] *= keep;
-      top = now;
-    }
-    const float off = top == -INFINITY ? 0.0f : top;
-    float part[2] = {};
-#pragma unroll
-    for (int blk = 0; blk < 2; ++blk)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        s[blk][r] = __builtin_amdgcn_exp2f(fmaf(s[blk][r], w.c2, -off));
-        part[r & 1] += s[blk][r];
-      }
-    sum += part[0] + part[1];
+    to_weights(s, w.c2, o, top, sum);
 #pragma unroll
     for (int ks = 0; ks < 4; ++ks) {
       const bf8 pk = as_operand(s[ks / 2], ks % 2);

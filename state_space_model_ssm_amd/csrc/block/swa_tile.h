@@ -109,12 +109,55 @@ __device__ __forceinline__ void load_stats(float *to, const float *p, int t0, in
                : "memory");
 }
 
-// Every copy this wavefront has started has landed.
-__device__ __forceinline__ void wait_tiles() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+// All but the last N copies this wavefront has started have landed.
+template <int N = 0>
+__device__ __forceinline__ void wait_tiles() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+
+// Every LDS read this wavefront has started has its value: the copies that
+// follow may overwrite what it read.
+__device__ __forceinline__ void wait_reads() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
 
 __device__ __forceinline__ float other_half(float v) {
   const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
   return __uint_as_float((threadIdx.x & 32) ? r[0] : r[1]);
+}
+
+// The running maximum is raised (and what is summed so far scaled down) only
+// when a score passes it by this factor's log2: weights stay below 2^8, which
+// costs no precision in float32 or bfloat16.
+constexpr float kSlack = 8.0f;
+
+// Scores of 64 keys (rows) for the lane's query -> weights 2^(c2 s - top),
+// with the running maximum `top` (in units of log2) raised where it must be,
+// `sum` (of this lane's half of the keys) and o taken along.
+template <int NB>
+__device__ __forceinline__ void to_weights(f16v (&s)[2], float c2, f16v (&o)[NB], float &top, float &sum) {
+  float m = s[0][0];
+#pragma unroll
+  for (int r = 1; r < 32; ++r) m = fmaxf(m, s[r / 16][r % 16]);
+  m = fmaxf(m, other_half(m)) * c2;
+  if (__any(m > top + kSlack)) {
+    const float now = m > top + kSlack ? m : top;  // by each query for itself: no row's bits depend on another's
+    const float keep = now == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(top - now);
+    sum *= keep;
+#pragma unroll
+    for (int db = 0; db < NB; ++db)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) o[db][r] *= keep;
+    top = now;
+  }
+  const float off = top == -INFINITY ? 0.0f : top;
+  float part[2] = {};
+#pragma unroll
+  for (int blk = 0; blk < 2; ++blk)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      s[blk][r] = __builtin_amdgcn_exp2f(fmaf(s[blk][r], c2, -off));
+      part[r & 1] += s[blk][r];
+    }
+  sum += part[0] + part[1];
 }
 
 __device__ __forceinline__ int row_length(const SwaParams &p, int64_t b) {

@@ -255,3 +255,16 @@ def test_offsets_past_32_bits():
     y2 = ssm.swa_step(*tail)
     ref.assert_close(y[-1:], ref.f64(y2), 2.0 ** -7 * (y2.float().abs().cpu().double().numpy() + 0.05), "y")
     assert torch.equal(kc[-1:], tail[3]) and torch.equal(vc[-1:], tail[4])
+
+
+def test_nan_queries_give_nan_alone():
+    q, k, v, _ = make(1, 100, 2, 1, 64, 12)
+    clean, _ = ssm.swa_fwd(q.cuda(), k.cuda(), v.cuda(), window=30, sinks=1)
+    q[0, 40, 1, 5] = float("nan")
+    y, _ = ssm.swa_fwd(q.cuda(), k.cuda(), v.cuda(), window=30, sinks=1)
+    bad = torch.isnan(y.float()).cpu()
+    assert bad[0, 40, 1].all() and int(bad.sum()) == 64 and torch.equal(y.cpu()[~bad], clean.cpu()[~bad])
+    kc, vc = (torch.randn(1, 1, 400, 64, device="cuda").to(BF16) for _ in range(2))
+    pos = torch.tensor([900], dtype=torch.int32, device="cuda")
+    y = ssm.swa_step(q[:, 40].cuda(), k[:, 40].cuda(), v[:, 40].cuda(), kc, vc, pos)
+    assert torch.isnan(y[0, 1].float()).all() and not torch.isnan(y[0, 0].float()).any()
