@@ -111,10 +111,18 @@ int check_glr(const ssm_glr_dims_t *d) {
   const int64_t tiles = mul(d->batch, ceil_div(d->dim, 32)), n = mul(mul(d->batch, d->dim), d->seqlen);
   if (tiles < 0 || tiles > kMaxGrid / 64 || n < 0 || mul(n, 4) < 0)
     return fail(SSM_ERR_UNSUPPORTED, "batch * ceil(dim / 32) must be below 2^31 / 64");
+  if (d->dim > (int64_t{1} << 22)) return fail(SSM_ERR_UNSUPPORTED, "dim must be at most 2^22");
   return SSM_OK;
 }
 
-size_t glr_bwd_workspace(const ssm_glr_dims_t &d) { return up256(static_cast<size_t>(d.batch) * d.dim * 4); }
+ssmb::GlrPlan glr_plan(const ssm_glr_dims_t &d) { return ssmb::glr_plan(d.batch, d.seqlen, d.dim); }
+// Summaries of the segments, and in the backward the terms of dA.
+size_t glr_workspace(const ssm_glr_dims_t &d) {
+  return up256(static_cast<size_t>(d.batch) * d.dim * (glr_plan(d).segs - 1) * 8);
+}
+size_t glr_bwd_workspace(const ssm_glr_dims_t &d) {
+  return glr_workspace(d) + up256(static_cast<size_t>(d.batch) * d.dim * glr_plan(d).segs * 4);
+}
 
 // ---------------------------------------------------------------------------
 // Residual addition with RMS norm
@@ -277,7 +285,7 @@ int ssm_glr_workspace_size(const ssm_glr_dims_t *dims, size_t *bytes) {
   if (!bytes) return fail(SSM_ERR_NULL, "bytes is NULL");
   const int rc = check_glr(dims);
   if (rc != SSM_OK) return rc;
-  *bytes = 0;
+  *bytes = glr_workspace(*dims);
   return ok();
 }
 
@@ -301,6 +309,7 @@ int ssm_glr_fwd(const void *x, const void *rec, const void *inp, const float *A,
                       {"states", states, bd * ceil_div(d.seqlen, SSM_GLR_STATE_STEP) * 4, 4, false}};
   const void *const same[3][2] = {{nullptr, nullptr}, {h0, nullptr}, {nullptr, nullptr}};
   rc = check_args(ins, outs, same);
+  if (rc == SSM_OK) rc = check_workspace(d.workspace, d.workspace_bytes, glr_workspace(d));
   if (rc != SSM_OK) return rc;
   if (bd == 0 || (d.seqlen == 0 && h_last == nullptr)) return ok();
   ssmb::GlrParams p{};
@@ -316,7 +325,8 @@ int ssm_glr_fwd(const void *x, const void *rec, const void *inp, const float *A,
   p.batch = d.batch;
   p.seqlen = d.seqlen;
   p.dim = d.dim;
-  return launched(ssmb::launch_glr(p, d.in_dtype == SSM_BF16, d.out_dtype == SSM_BF16, static_cast<hipStream_t>(stream)),
+  p.ws = static_cast<float *>(d.workspace);
+  return launched(ssmb::launch_glr(p, glr_plan(d), d.in_dtype == SSM_BF16, d.out_dtype == SSM_BF16, static_cast<hipStream_t>(stream)),
                   "glr_fwd");
 }
 
@@ -403,11 +413,12 @@ int ssm_glr_bwd(const void *x, const void *rec, const void *inp, const float *A,
   p.dinp = dinp;
   p.dA = dA;
   p.dh0 = dh0;
-  p.ws_dA = static_cast<float *>(d.workspace);
+  p.ws_seg = static_cast<float *>(d.workspace);
+  p.ws_dA = reinterpret_cast<float *>(static_cast<char *>(d.workspace) + glr_workspace(d));
   p.batch = d.batch;
   p.seqlen = d.seqlen;
   p.dim = d.dim;
-  return launched(ssmb::launch_glr_bwd(p, d.in_dtype == SSM_BF16, static_cast<hipStream_t>(stream)), "glr_bwd");
+  return launched(ssmb::launch_glr_bwd(p, glr_plan(d), d.in_dtype == SSM_BF16, static_cast<hipStream_t>(stream)), "glr_bwd");
 }
 
 int ssm_rms_add_fwd(const void *x, const void *residual, const float *w, void *y, void *residual_out,

@@ -26,9 +26,16 @@ struct GlrParams {
   const uint8_t *reset;        // nullable
   void *y;                     // out dtype
   float *h_last, *states;      // nullable
+  float *ws;                   // (batch, segs - 1, dim, 2): summaries of segments
   int64_t batch, seqlen, dim;
 };
-hipError_t launch_glr(const GlrParams &p, int in_bf16, int out_bf16, hipStream_t stream);
+// The sequence in `segs` segments of seg_tiles tiles (128 steps each).
+struct GlrPlan {
+  unsigned segs;
+  int64_t seg_tiles;
+};
+GlrPlan glr_plan(int64_t batch, int64_t seqlen, int64_t dim);
+hipError_t launch_glr(const GlrParams &p, const GlrPlan &plan, int in_bf16, int out_bf16, hipStream_t stream);
 hipError_t launch_glr_step(const GlrParams &p, int in_bf16, int out_bf16, hipStream_t stream);
 
 struct GlrBwdParams {
@@ -37,10 +44,10 @@ struct GlrBwdParams {
   const uint8_t *reset;
   void *dx, *drec, *dinp;
   float *dA, *dh0;             // dh0 nullable
-  float *ws_dA;                // (batch, dim)
+  float *ws_dA, *ws_seg;       // (batch, segs, dim); (batch, segs - 1, dim, 2)
   int64_t batch, seqlen, dim;
 };
-hipError_t launch_glr_bwd(const GlrBwdParams &p, int in_bf16, hipStream_t stream);
+hipError_t launch_glr_bwd(const GlrBwdParams &p, const GlrPlan &plan, int in_bf16, hipStream_t stream);
 
 // Residual addition with RMS norm (see ssm_rms_add_fwd and its neighbours).
 struct RmsParams {
