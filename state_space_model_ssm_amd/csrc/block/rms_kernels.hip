@@ -2,15 +2,29 @@
 // with s = x + residual, in storage types or in e4m3 bytes with scales, and
 // its backward.
 //
-// Simplest form: one wavefront per row, which it reads again for each pass.
+// All of it is bound by memory: a row is read once into registers (16 bytes
+// per lane and load, by 16 or 64 lanes or the whole workgroup, whichever
+// leaves a lane the fewest idle loads), summed across its lanes, and written.
+// Workgroups walk rows with w in registers, and with the backward's sums over
+// rows for dw, which they write once each; a second launch adds those in
+// order.  Rows that do not start on 16 bytes go value by value, the forward's
+// through LDS; rows too long for registers and LDS are read again per pass.
 #include "block_internal.h"
 
 namespace ssmb {
 namespace {
 
-__device__ __forceinline__ float wave_sum(float v) {
+// Sum over the TPR lanes of a row (in one wavefront, or the workgroup's four
+// through `lds`, which nobody else uses until the next barrier but one).
+template <int TPR>
+__device__ __forceinline__ float row_sum(float v, float *lds) {
 #pragma unroll
-  for (int m = 1; m < 64; m <<= 1) v += __shfl_xor(v, m);
+  for (int m = 1; m < (TPR < 64 ? TPR : 64); m <<= 1) v += __shfl_xor(v, m);
+  if constexpr (TPR == 256) {
+    if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = (lds[0] + lds[1]) + (lds[2] + lds[3]);
+  }
   return v;
 }
 
@@ -20,70 +34,330 @@ __device__ __forceinline__ float amax(float a, float b) {
   return (a != a || a > c) ? a : c;
 }
 
-__device__ __forceinline__ float wave_amax(float v) {
-#pragma unroll
-  for (int m = 1; m < 64; m <<= 1) v = amax(v, __shfl_xor(v, m));
+// amax over `lanes` neighbours, a power of two up to 64.
+__device__ __forceinline__ float lanes_amax(float v, int lanes) {
+  for (int m = 1; m < lanes; m <<= 1) v = amax(v, __shfl_xor(v, m));
   return v;
 }
 
-// v (within +-448 or NaN) as an e4m3 byte, rounded to nearest even.
-__device__ __forceinline__ uint8_t to_e4m3(float v) {
-  return static_cast<uint8_t>(__builtin_amdgcn_cvt_pk_fp8_f32(v, v, 0, false) & 0xff);
+// Values of a group are divided by its scale as (v * lift) * inverse: lift
+// keeps the inverse of a tiny scale finite.  A scale of 0 (whose values are
+// all 0) counts as 1.
+__device__ __forceinline__ float lift(float scale) { return scale < 0x1p-90f ? 0x1p90f : 1.0f; }
+__device__ __forceinline__ float inverse(float scale) { return 1.0f / (scale != 0.0f ? scale * lift(scale) : 1.0f); }
+
+// Two values within +-448 (or NaN) as e4m3 bytes, rounded to nearest even.
+// (A value can pass 448 by the rounding of the scale; it is held there.)
+__device__ __forceinline__ float hold(float v) { return v > 448.0f ? 448.0f : v < -448.0f ? -448.0f : v; }
+__device__ __forceinline__ int to_e4m3(float a, float b, int old, bool high) {
+  return high ? __builtin_amdgcn_cvt_pk_fp8_f32(hold(a), hold(b), old, true)
+              : __builtin_amdgcn_cvt_pk_fp8_f32(hold(a), hold(b), old, false);
 }
 
+// V values of a row in a lane: 16 bytes, or one value.
+template <typename E, int V>
+struct Piece {
+  __device__ static __forceinline__ void get(const void *p, int64_t at, float (&f)[V]) { f[0] = ld(static_cast<const E *>(p), at); }
+  __device__ static __forceinline__ void put(void *p, int64_t at, const float (&f)[V]) { st(static_cast<E *>(p), at, f[0]); }
+};
+template <>
+struct Piece<float, 4> {
+  __device__ static __forceinline__ void get(const void *p, int64_t at, float (&f)[4]) {
+    const float4 v = *reinterpret_cast<const float4 *>(static_cast<const float *>(p) + at);
+    f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
+  }
+  __device__ static __forceinline__ void put(void *p, int64_t at, const float (&f)[4]) {
+    *reinterpret_cast<float4 *>(static_cast<float *>(p) + at) = make_float4(f[0], f[1], f[2], f[3]);
+  }
+};
+template <>
+struct Piece<float, 8> {
+  __device__ static __forceinline__ void get(const void *p, int64_t at, float (&f)[8]) {
+    const float4 *q = reinterpret_cast<const float4 *>(static_cast<const float *>(p) + at);
+    const float4 v = q[0], u = q[1];
+    f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w; f[4] = u.x; f[5] = u.y; f[6] = u.z; f[7] = u.w;
+  }
+  __device__ static __forceinline__ void put(void *p, int64_t at, const float (&f)[8]) {
+    float4 *q = reinterpret_cast<float4 *>(static_cast<float *>(p) + at);
+    q[0] = make_float4(f[0], f[1], f[2], f[3]);
+    q[1] = make_float4(f[4], f[5], f[6], f[7]);
+  }
+};
+__device__ __forceinline__ uint32_t pack(float a, float b) {
+  typedef __attribute__((ext_vector_type(2))) __bf16 bf2;
+  const bf2 v = {static_cast<__bf16>(a), static_cast<__bf16>(b)};
+  return __builtin_bit_cast(uint32_t, v);
+}
+template <>
+struct Piece<uint16_t, 8> {
+  __device__ static __forceinline__ void get(const void *p, int64_t at, float (&f)[8]) {
+    const uint4 v = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p) + at);
+    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      f[2 * k] = __uint_as_float(u[k] << 16);
+      f[2 * k + 1] = __uint_as_float(u[k] & 0xffff0000u);
+    }
+  }
+  __device__ static __forceinline__ void put(void *p, int64_t at, const float (&f)[8]) {
+    *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p) + at) =
+        make_uint4(pack(f[0], f[1]), pack(f[2], f[3]), pack(f[4], f[5]), pack(f[6], f[7]));
+  }
+};
+template <>
+struct Piece<uint16_t, 4> {
+  __device__ static __forceinline__ void put(void *p, int64_t at, const float (&f)[4]) {
+    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p) + at) = make_uint2(pack(f[0], f[1]), pack(f[2], f[3]));
+  }
+};
+
+// Rows in registers: piece n of lane l is piece l + TPR n of the row.
+// Q8: groups are the row or 2^k neighbouring lanes of a wavefront (group_lanes).
+template <typename Tin, typename Tout, int TPR, int NV, bool Q8>
+__global__ void __launch_bounds__(256) rms_rows_kernel(const RmsParams p, int group_lanes) {
+  constexpr int V = 16 / sizeof(Tin), kRows = 256 / TPR;
+  __shared__ float lds[2][2][4];
+  const int l = threadIdx.x % TPR, pieces = static_cast<int>(p.dim / V);
+  const float inv = 1.0f / static_cast<float>(p.dim);
+  float w[NV][V];
+#pragma unroll
+  for (int n = 0; n < NV; ++n) {
+    const int at = l + TPR * n < pieces ? l + TPR * n : 0;
+    Piece<float, V>::get(p.w, static_cast<int64_t>(at) * V, w[n]);
+  }
+  int odd = 0;  // turns of the workgroup-wide sums' scratch
+  for (int64_t first = static_cast<int64_t>(blockIdx.x) * kRows; first < p.rows; first += static_cast<int64_t>(gridDim.x) * kRows) {
+    const int64_t row = first + threadIdx.x / TPR;
+    const bool live = row < p.rows;
+    const int64_t base = (live ? row : first) * p.dim;
+    float s[NV][V], ss = 0.0f;
+#pragma unroll
+    for (int n = 0; n < NV; ++n) {
+      const bool in = l + TPR * n < pieces;
+#pragma unroll
+      for (int e = 0; e < V; ++e) s[n][e] = 0.0f;
+      if (in) {
+        const int64_t at = base + static_cast<int64_t>(l + TPR * n) * V;
+        Piece<Tin, V>::get(p.x, at, s[n]);
+        if (p.residual != nullptr) {
+          float r[V];
+          Piece<Tin, V>::get(p.residual, at, r);
+#pragma unroll
+          for (int e = 0; e < V; ++e) s[n][e] += r[e];
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < V; ++e) ss = fmaf(s[n][e], s[n][e], ss);
+    }
+    const float rstd = 1.0f / sqrtf(fmaf(row_sum<TPR>(ss, lds[odd][0]), inv, p.eps));
+    if (p.residual_out != nullptr && live) {
+#pragma unroll
+      for (int n = 0; n < NV; ++n)
+        if (l + TPR * n < pieces) Piece<Tin, V>::put(p.residual_out, base + static_cast<int64_t>(l + TPR * n) * V, s[n]);
+    }
+#pragma unroll
+    for (int n = 0; n < NV; ++n)
+#pragma unroll
+      for (int e = 0; e < V; ++e) s[n][e] = s[n][e] * rstd * w[n][e];
+    if constexpr (!Q8) {
+#pragma unroll
+      for (int n = 0; n < NV; ++n)
+        if (l + TPR * n < pieces && live) Piece<Tout, V>::put(p.y, base + static_cast<int64_t>(l + TPR * n) * V, s[n]);
+    } else {
+      float top[NV];
+#pragma unroll
+      for (int n = 0; n < NV; ++n) {
+        top[n] = 0.0f;
+        if (l + TPR * n < pieces) {
+#pragma unroll
+          for (int e = 0; e < V; ++e) top[n] = amax(top[n], s[n][e]);
+        }
+      }
+      if (group_lanes == 0) {  // the row
+        float all = top[0];
+#pragma unroll
+        for (int n = 1; n < NV; ++n) all = amax(all, top[n]);
+        all = lanes_amax(all, TPR < 64 ? TPR : 64);
+        if constexpr (TPR == 256) {
+          float *scratch = lds[odd][1];
+          if ((threadIdx.x & 63) == 0) scratch[threadIdx.x >> 6] = all;
+          __syncthreads();
+          all = amax(amax(scratch[0], scratch[1]), amax(scratch[2], scratch[3]));
+        }
+#pragma unroll
+        for (int n = 0; n < NV; ++n) top[n] = all;
+        if (l == 0 && live) p.scale[row] = all * (1.0f / 448.0f);
+      } else {
+        const int64_t ngroup = (p.dim + p.group - 1) / p.group;
+#pragma unroll
+        for (int n = 0; n < NV; ++n) {
+          top[n] = lanes_amax(top[n], group_lanes);
+          const int piece = l + TPR * n;
+          if (piece < pieces && live && piece % group_lanes == 0)
+            p.scale[row * ngroup + piece / group_lanes] = top[n] * (1.0f / 448.0f);
+        }
+      }
+#pragma unroll
+      for (int n = 0; n < NV; ++n) {
+        const float scale = top[n] * (1.0f / 448.0f), k = inverse(scale);
+        if (scale < 0x1p-90f) {
+#pragma unroll
+          for (int e = 0; e < V; ++e) s[n][e] *= lift(scale);
+        }
+        if (l + TPR * n < pieces && live) {
+          uint8_t *q = static_cast<uint8_t *>(p.y) + base + static_cast<int64_t>(l + TPR * n) * V;
+          int b[V / 4];
+#pragma unroll
+          for (int e = 0; e < V; e += 4) {
+            b[e / 4] = to_e4m3(s[n][e] * k, s[n][e + 1] * k, 0, false);
+            b[e / 4] = to_e4m3(s[n][e + 2] * k, s[n][e + 3] * k, b[e / 4], true);
+          }
+          if constexpr (V == 8) *reinterpret_cast<int2 *>(q) = make_int2(b[0], b[1]);
+          else *reinterpret_cast<int *>(q) = b[0];
+        }
+      }
+    }
+    odd ^= 1;
+  }
+}
+
+// Rows of any alignment, a workgroup per row, through LDS (`keep`: the row's
+// sums stay there between the passes) or, too long for that, read again.
 template <typename Tin, typename Tout, bool Q8>
-__global__ void __launch_bounds__(64) rms_fwd_kernel(const RmsParams p) {
+__global__ void __launch_bounds__(256) rms_any_kernel(const RmsParams p, int keep) {
+  extern __shared__ float held[];
+  __shared__ float lds[4];
   const int64_t row = blockIdx.x, base = row * p.dim;
-  const int lane = threadIdx.x;
   const Tin *x = static_cast<const Tin *>(p.x), *res = static_cast<const Tin *>(p.residual);
   auto sum_at = [&](int64_t c) { return ld(x, base + c) + (res != nullptr ? ld(res, base + c) : 0.0f); };
   float ss = 0.0f;
-  for (int64_t c = lane; c < p.dim; c += 64) {
+  for (int64_t c = threadIdx.x; c < p.dim; c += 256) {
     const float s = sum_at(c);
+    if (keep) held[c] = s;
     ss = fmaf(s, s, ss);
   }
-  const float rstd = 1.0f / sqrtf(wave_sum(ss) / static_cast<float>(p.dim) + p.eps);
+  const float rstd = 1.0f / sqrtf(fmaf(row_sum<256>(ss, lds), 1.0f / static_cast<float>(p.dim), p.eps));
+  auto value = [&](int64_t c) { return keep ? held[c] : sum_at(c); };  // (row_sum() has a barrier)
   if constexpr (Q8) {
+    // A wavefront per group in turn.
+    const int lane = threadIdx.x & 63;
     const int64_t ngroup = (p.dim + p.group - 1) / p.group;
-    for (int64_t g = 0; g < ngroup; ++g) {
+    for (int64_t g = threadIdx.x >> 6; g < ngroup; g += 4) {
       const int64_t lo = g * p.group, hi = lo + p.group < p.dim ? lo + p.group : p.dim;
       float top = 0.0f;
-      for (int64_t c = lo + lane; c < hi; c += 64) top = amax(top, sum_at(c) * rstd * p.w[c]);
-      const float scale = wave_amax(top) / 448.0f;
+      for (int64_t c = lo + lane; c < hi; c += 64) top = amax(top, value(c) * rstd * p.w[c]);
+      const float scale = lanes_amax(top, 64) * (1.0f / 448.0f), k = inverse(scale);
       if (lane == 0) p.scale[row * ngroup + g] = scale;
-      for (int64_t c = lo + lane; c < hi; c += 64) {
-        const float v = sum_at(c) * rstd * p.w[c] / (scale > 0.0f ? scale : 1.0f);
-        static_cast<uint8_t *>(p.y)[base + c] = to_e4m3(v > 448.0f ? 448.0f : v < -448.0f ? -448.0f : v);
-      }
+      for (int64_t c = lo + lane; c < hi; c += 64)
+        static_cast<uint8_t *>(p.y)[base + c] =
+            static_cast<uint8_t>(to_e4m3(value(c) * rstd * p.w[c] * lift(scale) * k, 0.0f, 0, false) & 0xff);
     }
+    if (!keep) __syncthreads();  // residual_out may be x: every group has been read
   }
-  for (int64_t c = lane; c < p.dim; c += 64) {
-    const float s = sum_at(c);
+  for (int64_t c = threadIdx.x; c < p.dim; c += 256) {
+    const float s = value(c);
     if (p.residual_out != nullptr) st(static_cast<Tin *>(p.residual_out), base + c, s);
     if constexpr (!Q8) st(static_cast<Tout *>(p.y), base + c, s * rstd * p.w[c]);
   }
 }
 
+// Backward with rows in registers, V values per piece.
+template <typename Tin, int V, int TPR, int NV>
+__global__ void __launch_bounds__(256) rms_bwd_rows_kernel(const RmsBwdParams p) {
+  constexpr int kRows = 256 / TPR;
+  __shared__ float lds[2][2][4];
+  __shared__ __align__(16) float sums[kRows > 1 ? kRows * TPR * V : 1];
+  const int l = threadIdx.x % TPR, pieces = static_cast<int>(p.dim / V);
+  const float inv = 1.0f / static_cast<float>(p.dim);
+  float w[NV][V], dw[NV][V];
+#pragma unroll
+  for (int n = 0; n < NV; ++n) {
+    const int at = l + TPR * n < pieces ? l + TPR * n : 0;
+    Piece<float, V>::get(p.w, static_cast<int64_t>(at) * V, w[n]);
+#pragma unroll
+    for (int e = 0; e < V; ++e) dw[n][e] = 0.0f;
+  }
+  int odd = 0;
+  for (int64_t first = static_cast<int64_t>(blockIdx.x) * kRows; first < p.rows; first += p.parts * kRows) {
+    const int64_t row = first + threadIdx.x / TPR;
+    const bool live = row < p.rows;
+    const int64_t base = (live ? row : first) * p.dim;
+    float s[NV][V], d[NV][V], r[NV][V], ss = 0.0f, dot = 0.0f;
+#pragma unroll
+    for (int n = 0; n < NV; ++n) {
+#pragma unroll
+      for (int e = 0; e < V; ++e) s[n][e] = d[n][e] = r[n][e] = 0.0f;
+      if (l + TPR * n < pieces) {
+        const int64_t at = base + static_cast<int64_t>(l + TPR * n) * V;
+        Piece<Tin, V>::get(p.s, at, s[n]);
+        Piece<Tin, V>::get(p.dy, at, d[n]);
+        if (p.dres != nullptr) Piece<Tin, V>::get(p.dres, at, r[n]);
+      }
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        ss = fmaf(s[n][e], s[n][e], ss);
+        dot = fmaf(d[n][e] * w[n][e], s[n][e], dot);
+      }
+    }
+    const float rstd = 1.0f / sqrtf(fmaf(row_sum<TPR>(ss, lds[odd][0]), inv, p.eps));
+    const float mean = row_sum<TPR>(dot, lds[odd][1]) * rstd * inv;
+    odd ^= 1;
+#pragma unroll
+    for (int n = 0; n < NV; ++n) {
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const float norm = s[n][e] * rstd;
+        if (live) dw[n][e] = fmaf(d[n][e], norm, dw[n][e]);
+        r[n][e] = fmaf(rstd, d[n][e] * w[n][e] - norm * mean, r[n][e]);
+      }
+      if (l + TPR * n < pieces && live) Piece<Tin, V>::put(p.dx, base + static_cast<int64_t>(l + TPR * n) * V, r[n]);
+    }
+  }
+  if (p.dw == nullptr) return;
+  float *part = p.ws + static_cast<int64_t>(blockIdx.x) * p.dim;
+#pragma unroll
+  for (int n = 0; n < NV; ++n) {
+    if constexpr (kRows > 1) {  // over the rows in turn of the workgroup
+      __syncthreads();
+#pragma unroll
+      for (int e = 0; e < V; ++e) sums[threadIdx.x * V + e] = dw[n][e];
+      __syncthreads();
+      for (int c = threadIdx.x; c < TPR * V; c += 256) {
+        float t = 0.0f;
+#pragma unroll
+        for (int k = 0; k < kRows; ++k) t += sums[k * TPR * V + c];
+        const int64_t at = static_cast<int64_t>(TPR) * n * V + c;
+        if (at < p.dim) part[at] = t;
+      }
+    } else if (l + TPR * n < pieces) {
+      Piece<float, V>::put(part, static_cast<int64_t>(l + TPR * n) * V, dw[n]);
+    }
+  }
+}
+
+// Backward of rows too long for registers: a workgroup per row in turn, which
+// it reads twice.
 template <typename Tin>
-__global__ void __launch_bounds__(64) rms_bwd_kernel(const RmsBwdParams p) {
-  const int lane = threadIdx.x;
+__global__ void __launch_bounds__(256) rms_bwd_any_kernel(const RmsBwdParams p) {
+  __shared__ float lds[2][4];
   const Tin *dy = static_cast<const Tin *>(p.dy), *s = static_cast<const Tin *>(p.s);
   const Tin *dres = static_cast<const Tin *>(p.dres);
   float *part = p.ws + static_cast<int64_t>(blockIdx.x) * p.dim;
   if (p.dw != nullptr)
-    for (int64_t c = lane; c < p.dim; c += 64) part[c] = 0.0f;
-  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
+    for (int64_t c = threadIdx.x; c < p.dim; c += 256) part[c] = 0.0f;
+  for (int64_t row = blockIdx.x; row < p.rows; row += p.parts) {
     const int64_t base = row * p.dim;
     float ss = 0.0f, dot = 0.0f;
-    for (int64_t c = lane; c < p.dim; c += 64) {
+    for (int64_t c = threadIdx.x; c < p.dim; c += 256) {
       const float v = ld(s, base + c);
       ss = fmaf(v, v, ss);
       dot = fmaf(ld(dy, base + c) * p.w[c], v, dot);
     }
     const float inv = 1.0f / static_cast<float>(p.dim);
-    const float rstd = 1.0f / sqrtf(wave_sum(ss) * inv + p.eps);
-    const float mean = wave_sum(dot) * rstd * inv;
-    for (int64_t c = lane; c < p.dim; c += 64) {
+    __syncthreads();  // the last row's sums have been read
+    const float rstd = 1.0f / sqrtf(fmaf(row_sum<256>(ss, lds[0]), inv, p.eps));
+    const float mean = row_sum<256>(dot, lds[1]) * rstd * inv;
+    for (int64_t c = threadIdx.x; c < p.dim; c += 256) {
       const float n = ld(s, base + c) * rstd, d = ld(dy, base + c);
       const float r = dres != nullptr ? ld(dres, base + c) : 0.0f;
       st(static_cast<Tin *>(p.dx), base + c, fmaf(rstd, d * p.w[c] - n * mean, r));
@@ -92,38 +366,119 @@ __global__ void __launch_bounds__(64) rms_bwd_kernel(const RmsBwdParams p) {
   }
 }
 
-__global__ void __launch_bounds__(256) rms_sum_kernel(const float *part, float *dw, int64_t parts, int64_t dim) {
-  const int64_t c = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  if (c >= dim) return;
+// dw: 16 threads share the terms of a column, a workgroup has 64 columns.
+__global__ void __launch_bounds__(1024) rms_sum_kernel(const float *part, float *dw, int64_t parts, int64_t dim) {
+  __shared__ float lds[16][64];
+  const int64_t c = static_cast<int64_t>(blockIdx.x) * 64 + threadIdx.x % 64;
+  const int k0 = threadIdx.x / 64;
   float s = 0.0f;
-  for (int64_t k = 0; k < parts; ++k) s += part[k * dim + c];
+  if (c < dim) {
+#pragma unroll 8
+    for (int64_t k = k0; k < parts; k += 16) s += part[k * dim + c];
+  }
+  lds[k0][threadIdx.x % 64] = s;
+  __syncthreads();
+  if (k0 != 0 || c >= dim) return;
+#pragma unroll
+  for (int k = 1; k < 16; ++k) s += lds[k][threadIdx.x];
   dw[c] = s;
+}
+
+bool aligned16(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+
+// Lanes per row and pieces per lane for `pieces` of a row, and the kernel's
+// instance for them; false where they are too many.
+template <bool LONG = false, typename F>
+bool with_shape(int64_t pieces, F f) {
+  if (pieces <= 16) f.template operator()<16, 1>();
+  else if (pieces <= 32) f.template operator()<16, 2>();
+  else if (pieces <= 64) f.template operator()<64, 1>();
+  else if (pieces <= 128) f.template operator()<64, 2>();
+  else if (pieces <= 256) f.template operator()<64, 4>();
+  else if (pieces <= 512) f.template operator()<256, 2>();
+  else if (pieces <= 768) f.template operator()<256, 3>();
+  else if (pieces <= 1024) f.template operator()<256, 4>();
+  else if (pieces <= 2048) f.template operator()<256, 8>();
+  else if constexpr (LONG) {
+    if (pieces <= 4096) f.template operator()<256, 16>();
+    else if (pieces <= 8192) f.template operator()<256, 32>();
+    else return false;
+  } else return false;
+  return true;
+}
+
+// Workgroups of 256 / lanes rows each; more than fit at once walk the rows.
+constexpr int64_t kMostGroups = 2048;
+
+template <typename Tin, typename Tout, bool Q8>
+struct RowsLaunch {
+  const RmsParams &p;
+  int group_lanes;
+  hipStream_t st;
+  template <int TPR, int NV>
+  void operator()() {
+    const int64_t n = (p.rows + 256 / TPR - 1) / (256 / TPR);
+    hipLaunchKernelGGL((rms_rows_kernel<Tin, Tout, TPR, NV, Q8>), dim3(static_cast<uint32_t>(n < kMostGroups ? n : kMostGroups)),
+                       dim3(256), 0, st, p, group_lanes);
+  }
+};
+
+template <typename Tin, typename Tout, bool Q8>
+hipError_t run_fwd(const RmsParams &p, hipStream_t st) {
+  constexpr int V = 16 / sizeof(Tin);
+  // Stores of y are 4 to 32 bytes wide, by its type; its rows start on as many
+  // where they start on 16 bytes of x.
+  bool rows = p.dim % V == 0 && aligned16(p.x) && aligned16(p.residual) && aligned16(p.residual_out) && aligned16(p.y) &&
+              aligned16(p.w);
+  int lanes = 0;
+  if (Q8 && p.group < p.dim) {
+    lanes = p.group % V == 0 && p.group / V <= 64 ? static_cast<int>(p.group / V) : -1;
+    if (lanes < 1 || (lanes & (lanes - 1)) != 0 || (lanes > 16 && p.dim / V <= 32)) rows = false;
+  }
+  if (rows && with_shape(p.dim / V, RowsLaunch<Tin, Tout, Q8>{p, lanes, st})) return hipGetLastError();
+  const int keep = p.dim <= 8192;  // 32 KiB of LDS: four workgroups per CU and more
+  hipLaunchKernelGGL((rms_any_kernel<Tin, Tout, Q8>), dim3(static_cast<uint32_t>(p.rows)), dim3(256),
+                     keep ? static_cast<size_t>(p.dim) * 4 : 0, st, p, keep);
+  return hipGetLastError();
+}
+
+template <typename Tin, int V>
+struct BwdLaunch {
+  const RmsBwdParams &p;
+  hipStream_t st;
+  template <int TPR, int NV>
+  void operator()() {
+    hipLaunchKernelGGL((rms_bwd_rows_kernel<Tin, V, TPR, NV>), dim3(static_cast<uint32_t>(p.parts)), dim3(256), 0, st, p);
+  }
+};
+
+template <typename Tin>
+void run_bwd(const RmsBwdParams &p, hipStream_t st) {
+  constexpr int V = 16 / sizeof(Tin);
+  const bool vec = p.dim % V == 0 && aligned16(p.dy) && aligned16(p.s) && aligned16(p.dres) && aligned16(p.dx) &&
+                   aligned16(p.w) && aligned16(p.ws);
+  if (vec && with_shape(p.dim / V, BwdLaunch<Tin, V>{p, st})) return;
+  if (!vec && with_shape<true>(p.dim, BwdLaunch<Tin, 1>{p, st})) return;
+  hipLaunchKernelGGL((rms_bwd_any_kernel<Tin>), dim3(static_cast<uint32_t>(p.parts)), dim3(256), 0, st, p);
 }
 
 }  // namespace
 
 hipError_t launch_rms(const RmsParams &p, int in_bf16, int out_bf16, hipStream_t st) {
-  const dim3 g(static_cast<uint32_t>(p.rows)), t(64);
-  if (p.scale != nullptr) {
-    if (in_bf16) hipLaunchKernelGGL((rms_fwd_kernel<uint16_t, uint16_t, true>), g, t, 0, st, p);
-    else hipLaunchKernelGGL((rms_fwd_kernel<float, float, true>), g, t, 0, st, p);
-  } else if (in_bf16 && out_bf16) hipLaunchKernelGGL((rms_fwd_kernel<uint16_t, uint16_t, false>), g, t, 0, st, p);
-  else if (in_bf16) hipLaunchKernelGGL((rms_fwd_kernel<uint16_t, float, false>), g, t, 0, st, p);
-  else if (out_bf16) hipLaunchKernelGGL((rms_fwd_kernel<float, uint16_t, false>), g, t, 0, st, p);
-  else hipLaunchKernelGGL((rms_fwd_kernel<float, float, false>), g, t, 0, st, p);
-  return hipGetLastError();
+  if (p.scale != nullptr) return in_bf16 ? run_fwd<uint16_t, uint16_t, true>(p, st) : run_fwd<float, float, true>(p, st);
+  if (in_bf16) return out_bf16 ? run_fwd<uint16_t, uint16_t, false>(p, st) : run_fwd<uint16_t, float, false>(p, st);
+  return out_bf16 ? run_fwd<float, uint16_t, false>(p, st) : run_fwd<float, float, false>(p, st);
 }
 
-int64_t rms_bwd_parts(int64_t rows, int64_t) { return rows < 1024 ? rows : 1024; }
+int64_t rms_bwd_parts(int64_t rows, int64_t) { return rows < 512 ? rows : 512; }
 
 hipError_t launch_rms_bwd(const RmsBwdParams &p, int in_bf16, hipStream_t st) {
-  const dim3 g(static_cast<uint32_t>(p.parts)), t(64);
   if (p.rows > 0) {
-    if (in_bf16) hipLaunchKernelGGL((rms_bwd_kernel<uint16_t>), g, t, 0, st, p);
-    else hipLaunchKernelGGL((rms_bwd_kernel<float>), g, t, 0, st, p);
+    if (in_bf16) run_bwd<uint16_t>(p, st);
+    else run_bwd<float>(p, st);
   }
   if (p.dw != nullptr)
-    hipLaunchKernelGGL(rms_sum_kernel, dim3(static_cast<uint32_t>((p.dim + 255) / 256)), dim3(256), 0, st, p.ws, p.dw,
+    hipLaunchKernelGGL(rms_sum_kernel, dim3(static_cast<uint32_t>((p.dim + 63) / 64)), dim3(1024), 0, st, p.ws, p.dw,
                        p.parts, p.dim);
   return hipGetLastError();
 }

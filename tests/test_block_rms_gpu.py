@@ -205,3 +205,16 @@ def test_offsets_past_32_bits():
     assert torch.equal(y[-8:], y2) and torch.equal(s[-8:], s2)
     dx, _ = ssm.rms_add_bwd(x, x, w, dres=x, return_dw=False)
     assert torch.equal(dx[-8:], ssm.rms_add_bwd(tail, tail, w, dres=tail, return_dw=False)[0])
+
+
+def test_8_bit_output_of_tiny_values():
+    """Scales far below float32's normal range keep their values' ratios."""
+    for dim, group in ((256, 0), (256, 128), (101, 0), (256, 96)):
+        w = torch.full((dim,), 1e-36)
+        x = torch.randn(3, dim, generator=torch.Generator().manual_seed(dim))
+        x[0, 3] = 0
+        q, scale, _ = ssm.rms_add_q8_fwd(x.cuda(), w.cuda(), group=group)
+        want, _ = ref.rms(x, w)
+        got = q.float().cpu().double().numpy() * np.repeat(ref.f64(scale), group or dim, 1)[:, :dim]
+        # half a step of e4m3 (2^-4 of a value), and the scale's own step of 2^-149 against about 2^-128
+        assert np.all(np.abs(got - want) <= np.abs(want) * (2.0 ** -4 + 2.0 ** -18) + 2.0 ** -10 * np.abs(want).max())
