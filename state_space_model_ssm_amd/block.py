@@ -19,7 +19,7 @@ import os
 
 import torch
 
-from . import _BLOCK, SsmError, _alloc_on, _dtype_code, _out, _ptr, _stream
+from . import _BLOCK, SSM_BF16, SSM_F32, SsmError
 
 __all__ = list(_BLOCK)
 
@@ -28,6 +28,11 @@ GLR_STATE_STEP = 16   # steps between two saved states of the recurrence
 _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libssm_block.so")
 _lib = None
 _F32, _BF16 = torch.float32, torch.bfloat16
+_CODES = {_F32: SSM_F32, _BF16: SSM_BF16}
+
+# The calls below are single kernels of a few microseconds at decoding sizes,
+# so their marshalling is kept to what costs little: no context managers, no
+# stream objects, no conversions.
 
 
 class GlrDims(ctypes.Structure):
@@ -90,8 +95,49 @@ def block_last_error() -> str:
 
 
 def _check(rc: int):
-    if rc != 0:
+    if rc:
         raise SsmError(rc, block_last_error())
+
+
+def _code(dtype) -> int:
+    code = _CODES.get(dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {dtype} (float32 or bfloat16)")
+    return code
+
+
+def _ptr(t):
+    if t is None:
+        return None
+    if not t.is_cuda:
+        raise ValueError("tensors must be on the GPU")
+    if not t.is_contiguous():
+        raise ValueError("tensors must be contiguous")
+    return t.data_ptr() or None
+
+
+def _stream(stream):
+    """The stream's handle: the current one's of the current device, or the given one's."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()) or None
+    return stream.cuda_stream or None
+
+
+def _out(t, shape, dtype, like, name, stream):
+    """A caller-given output, checked against what the call writes, or a new
+    one, allocated on the stream the kernels will run on (the caching
+    allocator reuses a freed block only for later work of that stream)."""
+    if t is None:
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return torch.empty(shape, dtype=dtype, device=like.device)
+        if dtype == like.dtype and shape == like.shape and like.is_contiguous():
+            return torch.empty_like(like)
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    if t.shape != shape or t.dtype != dtype or t.device != like.device:
+        raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)} on {like.device}, "
+                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+    return t
 
 
 def _size(call, dims) -> int:
@@ -120,12 +166,12 @@ def swa_step_workspace_size(dims: SwaDims) -> int:
     return _size(block_lib().ssm_swa_step_workspace_size, dims)
 
 
-def _scratch(dims, need: int, workspace, like):
+def _scratch(dims, need: int, workspace, like, stream):
     """Give ``dims`` a workspace of ``need`` bytes: the caller's if it is large
     enough, else a new one, which the caller of this keeps until the launch."""
     if need > 0:
         if workspace is None or workspace.numel() * workspace.element_size() < need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=like.device)
+            workspace = _out(None, (need,), torch.uint8, like, "workspace", stream)
         dims.workspace = _ptr(workspace)
         dims.workspace_bytes = workspace.numel() * workspace.element_size()
     return workspace
@@ -170,14 +216,13 @@ def glr_fwd(x, rec, inp, A, *, h0=None, reset=None, out_dtype=None, return_h_las
     batch, L, dim = x.shape
     _same("h0", h0, _F32, (batch, dim))
     out_dt = x.dtype if out_dtype is None else out_dtype
-    dims = GlrDims(batch, L, dim, _dtype_code(x.dtype), _dtype_code(out_dt))
-    with _alloc_on(stream):
-        y = _out(y, (batch, L, dim), out_dt, x, "y")
-        if h_last is not None or return_h_last:
-            h_last = _out(h_last, (batch, dim), _F32, x, "h_last")
-        if states is not None or return_states:
-            states = _out(states, (batch, -(-L // GLR_STATE_STEP), dim), _F32, x, "states")
-        workspace = _scratch(dims, glr_workspace_size(dims), workspace, x)
+    dims = GlrDims(batch, L, dim, _code(x.dtype), _code(out_dt))
+    y = _out(y, (batch, L, dim), out_dt, x, "y", stream)
+    if h_last is not None or return_h_last:
+        h_last = _out(h_last, (batch, dim), _F32, x, "h_last", stream)
+    if states is not None or return_states:
+        states = _out(states, (batch, -(-L // GLR_STATE_STEP), dim), _F32, x, "states", stream)
+    workspace = _scratch(dims, glr_workspace_size(dims), workspace, x, stream)
     _check(block_lib().ssm_glr_fwd(_ptr(x), _ptr(rec), _ptr(inp), _ptr(A), _ptr(h0), _ptr(reset), _ptr(y),
                                    _ptr(h_last), _ptr(states), ctypes.byref(dims), _stream(stream)))
     return (y, h_last, states) if return_states else (y, h_last)
@@ -196,14 +241,13 @@ def glr_bwd(x, rec, inp, A, states, dy, *, dh_last=None, reset=None, return_dh0:
     _same("states", states, _F32, (batch, -(-L // GLR_STATE_STEP), dim))
     _same("dy", dy, x.dtype, x.shape)
     _same("dh_last", dh_last, _F32, (batch, dim))
-    code = _dtype_code(x.dtype)
+    code = _code(x.dtype)
     dims = GlrDims(batch, L, dim, code, code)
     o = out or {}
-    with _alloc_on(stream):
-        dx, drec, dinp = (_out(o.get(k), x.shape, x.dtype, x, k) for k in ("dx", "drec", "dinp"))
-        dA = _out(o.get("dA"), (dim,), _F32, x, "dA")
-        dh0 = _out(o.get("dh0"), (batch, dim), _F32, x, "dh0") if return_dh0 else None
-        workspace = _scratch(dims, glr_bwd_workspace_size(dims), workspace, x)
+    dx, drec, dinp = (_out(o.get(k), x.shape, x.dtype, x, k, stream) for k in ("dx", "drec", "dinp"))
+    dA = _out(o.get("dA"), (dim,), _F32, x, "dA", stream)
+    dh0 = _out(o.get("dh0"), (batch, dim), _F32, x, "dh0", stream) if return_dh0 else None
+    workspace = _scratch(dims, glr_bwd_workspace_size(dims), workspace, x, stream)
     _check(block_lib().ssm_glr_bwd(_ptr(x), _ptr(rec), _ptr(inp), _ptr(A), _ptr(reset), _ptr(states), _ptr(dy),
                                    _ptr(dh_last), _ptr(dx), _ptr(drec), _ptr(dinp), _ptr(dA), _ptr(dh0),
                                    ctypes.byref(dims), _stream(stream)))
@@ -218,10 +262,9 @@ def glr_step(x, rec, inp, A, h, *, h_out=None, out_dtype=None, y=None, stream=No
     batch, dim = x.shape
     _same("h", h, _F32, x.shape)
     out_dt = x.dtype if out_dtype is None else out_dtype
-    dims = GlrDims(batch, 1, dim, _dtype_code(x.dtype), _dtype_code(out_dt))
-    with _alloc_on(stream):
-        y = _out(y, x.shape, out_dt, x, "y")
-    h_out = h if h_out is None else _out(h_out, x.shape, _F32, x, "h_out")
+    dims = GlrDims(batch, 1, dim, _code(x.dtype), _code(out_dt))
+    y = _out(y, x.shape, out_dt, x, "y", stream)
+    h_out = h if h_out is None else _out(h_out, x.shape, _F32, x, "h_out", stream)
     _check(block_lib().ssm_glr_step(_ptr(x), _ptr(rec), _ptr(inp), _ptr(A), _ptr(h), _ptr(y), _ptr(h_out),
                                     ctypes.byref(dims), _stream(stream)))
     return y, h_out
@@ -237,7 +280,7 @@ def _rms_dims(x, w, residual, eps, out_dt, group=0) -> RmsDims:
     dim = x.shape[-1]
     _same("w", w, _F32, (dim,))
     _same("residual", residual, x.dtype, x.shape)
-    return RmsDims(x.numel() // dim if dim else 0, dim, group, _dtype_code(x.dtype), _dtype_code(out_dt), eps)
+    return RmsDims(x.numel() // dim if dim else 0, dim, group, _code(x.dtype), _code(out_dt), eps)
 
 
 def rms_add_fwd(x, w, residual=None, *, eps: float = 1e-5, out_dtype=None, y=None, residual_out=None, stream=None):
@@ -248,10 +291,9 @@ def rms_add_fwd(x, w, residual=None, *, eps: float = 1e-5, out_dtype=None, y=Non
     residual, y may be x."""
     out_dt = x.dtype if out_dtype is None else out_dtype
     dims = _rms_dims(x, w, residual, eps, out_dt)
-    with _alloc_on(stream):
-        y = _out(y, x.shape, out_dt, x, "y")
-        if residual is not None or residual_out is not None:
-            residual_out = _out(residual_out, x.shape, x.dtype, x, "residual_out")
+    y = _out(y, x.shape, out_dt, x, "y", stream)
+    if residual is not None or residual_out is not None:
+        residual_out = _out(residual_out, x.shape, x.dtype, x, "residual_out", stream)
     _check(block_lib().ssm_rms_add_fwd(_ptr(x), _ptr(residual), _ptr(w), _ptr(y), _ptr(residual_out),
                                        ctypes.byref(dims), _stream(stream)))
     return y, x if residual_out is None else residual_out
@@ -266,11 +308,10 @@ def rms_add_q8_fwd(x, w, residual=None, *, eps: float = 1e-5, group: int = 0, q=
     dims = _rms_dims(x, w, residual, eps, x.dtype, group)
     dim = x.shape[-1]
     groups = -(-dim // group) if 0 < group < dim else 1
-    with _alloc_on(stream):
-        q = _out(q, x.shape, torch.float8_e4m3fn, x, "q")
-        scale = _out(scale, (*x.shape[:-1], groups), _F32, x, "scale")
-        if residual is not None or residual_out is not None:
-            residual_out = _out(residual_out, x.shape, x.dtype, x, "residual_out")
+    q = _out(q, x.shape, torch.float8_e4m3fn, x, "q", stream)
+    scale = _out(scale, (*x.shape[:-1], groups), _F32, x, "scale", stream)
+    if residual is not None or residual_out is not None:
+        residual_out = _out(residual_out, x.shape, x.dtype, x, "residual_out", stream)
     _check(block_lib().ssm_rms_add_q8_fwd(_ptr(x), _ptr(residual), _ptr(w), _ptr(q), _ptr(scale), _ptr(residual_out),
                                           ctypes.byref(dims), _stream(stream)))
     return q, scale, x if residual_out is None else residual_out
@@ -284,11 +325,10 @@ def rms_add_bwd(dy, s, w, *, dres=None, eps: float = 1e-5, return_dw: bool = Tru
     x and of residual alike, dw (dim,) float32 (None without return_dw)."""
     _same("dy", dy, s.dtype, s.shape)
     dims = _rms_dims(s, w, dres, eps, s.dtype)
-    with _alloc_on(stream):
-        dx = _out(dx, s.shape, s.dtype, s, "dx")
-        if dw is not None or return_dw:
-            dw = _out(dw, w.shape, _F32, s, "dw")
-            workspace = _scratch(dims, rms_add_bwd_workspace_size(dims), workspace, s)
+    dx = _out(dx, s.shape, s.dtype, s, "dx", stream)
+    if dw is not None or return_dw:
+        dw = _out(dw, w.shape, _F32, s, "dw", stream)
+        workspace = _scratch(dims, rms_add_bwd_workspace_size(dims), workspace, s, stream)
     _check(block_lib().ssm_rms_add_bwd(_ptr(dy), _ptr(s), _ptr(w), _ptr(dres), _ptr(dx), _ptr(dw),
                                        ctypes.byref(dims), _stream(stream)))
     return dx, dw
@@ -341,10 +381,9 @@ def swa_fwd(q, k, v, *, window: int, sinks: int = 0, scale=None, lengths=None, r
     dims = _swa_dims(q, k, v, window, sinks, scale, 2)
     batch, L, H, _ = q.shape
     _same("lengths", lengths, torch.int32, (batch,))
-    with _alloc_on(stream):
-        y = _out(y, q.shape, _BF16, q, "y")
-        if lse is not None or return_lse:
-            lse = _out(lse, (batch, H, L), _F32, q, "lse")
+    y = _out(y, q.shape, _BF16, q, "y", stream)
+    if lse is not None or return_lse:
+        lse = _out(lse, (batch, H, L), _F32, q, "lse", stream)
     _check(block_lib().ssm_swa_fwd(_at(q), _at(k), _at(v), _ptr(lengths), _ptr(y), _ptr(lse), ctypes.byref(dims),
                                    _stream(stream)))
     return y, lse
@@ -362,9 +401,8 @@ def swa_bwd(q, k, v, y, lse, dy, *, window: int, sinks: int = 0, scale=None, len
     _same("dy", dy, _BF16, q.shape)
     _same("lse", lse, _F32, (batch, H, L))
     o = out or {}
-    with _alloc_on(stream):
-        dq, dk, dv = (_out(o.get(n), t.shape, _BF16, q, n) for n, t in (("dq", q), ("dk", k), ("dv", v)))
-        workspace = _scratch(dims, swa_bwd_workspace_size(dims), workspace, q)
+    dq, dk, dv = (_out(o.get(n), t.shape, _BF16, q, n, stream) for n, t in (("dq", q), ("dk", k), ("dv", v)))
+    workspace = _scratch(dims, swa_bwd_workspace_size(dims), workspace, q, stream)
     _check(block_lib().ssm_swa_bwd(_at(q), _at(k), _at(v), _ptr(lengths), _ptr(y), _ptr(lse), _ptr(dy), _ptr(dq),
                                    _ptr(dk), _ptr(dv), ctypes.byref(dims), _stream(stream)))
     return dq, dk, dv
@@ -388,9 +426,8 @@ def swa_step(q, k, v, k_cache, v_cache, pos, *, sinks: int = 0, scale=None, y=No
     dims = _swa_dims(q, k, v, 1, sinks, scale, 1)
     dims.window = _swa_caches(k_cache, v_cache, k.shape[0], k.shape[1], k.shape[2], sinks)
     _same("pos", pos, torch.int32, (q.shape[0],))
-    with _alloc_on(stream):
-        y = _out(y, q.shape, _BF16, q, "y")
-        workspace = _scratch(dims, swa_step_workspace_size(dims), workspace, q)
+    y = _out(y, q.shape, _BF16, q, "y", stream)
+    workspace = _scratch(dims, swa_step_workspace_size(dims), workspace, q, stream)
     _check(block_lib().ssm_swa_step(_at(q), _at(k), _at(v), _ptr(k_cache), _ptr(v_cache), _ptr(pos), _ptr(y),
                                     ctypes.byref(dims), _stream(stream)))
     return y
