@@ -46,7 +46,7 @@ SSM_API const char *ssm_block_last_error(void);
 /*
  * Sizes of one call.  in_dtype: x, rec, inp (and dy, dx, drec, dinp);
  * out_dtype: y.  reserved must be 0.  Supported: any batch, seqlen, dim >= 0
- * with dim <= 2^22 and batch * ceil(dim / 32) < 2^31 / 64.
+ * with dim <= 2^22 and batch * ceil(dim / 32) * ceil(seqlen / 128) < 2^31.
  */
 typedef struct {
   int64_t batch, seqlen, dim;

@@ -109,19 +109,19 @@ int check_glr(const ssm_glr_dims_t *d) {
     return fail(SSM_ERR_DTYPE, "in_dtype %d or out_dtype %d is not an ssm_dtype_t", d->in_dtype, d->out_dtype);
   if (d->reserved != 0 || d->reserved2 != 0) return fail(SSM_ERR_SHAPE, "reserved fields must be 0");
   const int64_t tiles = mul(d->batch, ceil_div(d->dim, 32)), n = mul(mul(d->batch, d->dim), d->seqlen);
-  if (tiles < 0 || tiles > kMaxGrid / 64 || n < 0 || mul(n, 4) < 0)
-    return fail(SSM_ERR_UNSUPPORTED, "batch * ceil(dim / 32) must be below 2^31 / 64");
+  const int64_t all = mul(tiles, ceil_div(d->seqlen, 128));
+  if (tiles < 0 || n < 0 || mul(n, 4) < 0 || all < 0 || all > kMaxGrid || tiles > kMaxGrid)
+    return fail(SSM_ERR_UNSUPPORTED, "batch * ceil(dim / 32) * ceil(seqlen / 128) must be below 2^31");
   if (d->dim > (int64_t{1} << 22)) return fail(SSM_ERR_UNSUPPORTED, "dim must be at most 2^22");
   return SSM_OK;
 }
 
-ssmb::GlrPlan glr_plan(const ssm_glr_dims_t &d) { return ssmb::glr_plan(d.batch, d.seqlen, d.dim); }
-// Summaries of the segments, and in the backward the terms of dA.
 size_t glr_workspace(const ssm_glr_dims_t &d) {
-  return up256(static_cast<size_t>(d.batch) * d.dim * (glr_plan(d).segs - 1) * 8);
+  const size_t chain = ssmb::glr_chain_bytes(d.batch, d.seqlen, d.dim);
+  return chain > 0 ? up256(256 + chain) : 0;
 }
-size_t glr_bwd_workspace(const ssm_glr_dims_t &d) {
-  return glr_workspace(d) + up256(static_cast<size_t>(d.batch) * d.dim * glr_plan(d).segs * 4);
+size_t glr_bwd_workspace(const ssm_glr_dims_t &d) {  // and the terms of dA
+  return glr_workspace(d) + up256(static_cast<size_t>(ssmb::glr_bwd_parts(d.batch, d.seqlen)) * d.dim * 4);
 }
 
 // ---------------------------------------------------------------------------
@@ -325,8 +325,8 @@ int ssm_glr_fwd(const void *x, const void *rec, const void *inp, const float *A,
   p.batch = d.batch;
   p.seqlen = d.seqlen;
   p.dim = d.dim;
-  p.ws = static_cast<float *>(d.workspace);
-  return launched(ssmb::launch_glr(p, glr_plan(d), d.in_dtype == SSM_BF16, d.out_dtype == SSM_BF16, static_cast<hipStream_t>(stream)),
+  p.chain = ssmb::glr_chain(d.workspace, d.batch, d.seqlen, d.dim);
+  return launched(ssmb::launch_glr(p, d.in_dtype == SSM_BF16, d.out_dtype == SSM_BF16, static_cast<hipStream_t>(stream)),
                   "glr_fwd");
 }
 
@@ -413,12 +413,12 @@ int ssm_glr_bwd(const void *x, const void *rec, const void *inp, const float *A,
   p.dinp = dinp;
   p.dA = dA;
   p.dh0 = dh0;
-  p.ws_seg = static_cast<float *>(d.workspace);
+  p.chain = ssmb::glr_chain(d.workspace, d.batch, d.seqlen, d.dim);
   p.ws_dA = reinterpret_cast<float *>(static_cast<char *>(d.workspace) + glr_workspace(d));
   p.batch = d.batch;
   p.seqlen = d.seqlen;
   p.dim = d.dim;
-  return launched(ssmb::launch_glr_bwd(p, glr_plan(d), d.in_dtype == SSM_BF16, static_cast<hipStream_t>(stream)), "glr_bwd");
+  return launched(ssmb::launch_glr_bwd(p, d.in_dtype == SSM_BF16, static_cast<hipStream_t>(stream)), "glr_bwd");
 }
 
 int ssm_rms_add_fwd(const void *x, const void *residual, const float *w, void *y, void *residual_out,

@@ -19,6 +19,18 @@ __device__ __forceinline__ void st(uint16_t *p, int64_t i, float v) {
   p[i] = __builtin_bit_cast(uint16_t, static_cast<__bf16>(v));  // round to nearest even
 }
 
+// What tiles of a recurrence tell each other, in the workspace: a counter (256
+// bytes kept for it), a summary (product, end) per (row, tile, channel), and
+// the state at the start of each group of tiles.  Nothing for one tile.
+struct GlrChain {
+  unsigned *counter;
+  uint64_t *sums;
+  unsigned *starts;
+  int64_t bytes;               // of sums and starts
+};
+size_t glr_chain_bytes(int64_t batch, int64_t seqlen, int64_t dim);
+GlrChain glr_chain(void *workspace, int64_t batch, int64_t seqlen, int64_t dim);
+
 // Gated linear recurrence (see ssm_glr_fwd and ssm_glr_bwd in ssm_block.h).
 struct GlrParams {
   const void *x, *rec, *inp;   // in dtype
@@ -26,16 +38,10 @@ struct GlrParams {
   const uint8_t *reset;        // nullable
   void *y;                     // out dtype
   float *h_last, *states;      // nullable
-  float *ws;                   // (batch, segs - 1, dim, 2): summaries of segments
+  GlrChain chain;
   int64_t batch, seqlen, dim;
 };
-// The sequence in `segs` segments of seg_tiles tiles (128 steps each).
-struct GlrPlan {
-  unsigned segs;
-  int64_t seg_tiles;
-};
-GlrPlan glr_plan(int64_t batch, int64_t seqlen, int64_t dim);
-hipError_t launch_glr(const GlrParams &p, const GlrPlan &plan, int in_bf16, int out_bf16, hipStream_t stream);
+hipError_t launch_glr(const GlrParams &p, int in_bf16, int out_bf16, hipStream_t stream);
 hipError_t launch_glr_step(const GlrParams &p, int in_bf16, int out_bf16, hipStream_t stream);
 
 struct GlrBwdParams {
@@ -44,10 +50,12 @@ struct GlrBwdParams {
   const uint8_t *reset;
   void *dx, *drec, *dinp;
   float *dA, *dh0;             // dh0 nullable
-  float *ws_dA, *ws_seg;       // (batch, segs, dim); (batch, segs - 1, dim, 2)
+  float *ws_dA;                // (glr_bwd_parts, dim)
+  GlrChain chain;
   int64_t batch, seqlen, dim;
 };
-hipError_t launch_glr_bwd(const GlrBwdParams &p, const GlrPlan &plan, int in_bf16, hipStream_t stream);
+int64_t glr_bwd_parts(int64_t batch, int64_t seqlen);
+hipError_t launch_glr_bwd(const GlrBwdParams &p, int in_bf16, hipStream_t stream);
 
 // Residual addition with RMS norm (see ssm_rms_add_fwd and its neighbours).
 struct RmsParams {

@@ -6,12 +6,24 @@
 // A lane takes 16 steps of one channel, or of two that share a dword, in
 // registers; a workgroup's tile is 128 steps by 32 lanes of channels (rows of
 // 128 bytes).  A lane's steps are summed up as (product of a, end state from
-// zero), the 8 summaries of a channel meet in LDS, and each lane then runs its
-// steps from the state it starts with, so the tile is read once.  A workgroup
-// walks its tiles in time with the state in registers; where there are too few
-// channels to fill the GPU, the sequence is cut into segments, a first launch
-// sums up the segments, and each workgroup starts from its predecessors'
-// summaries, taken in order (so the result does not depend on timing).
+// zero), the 8 summaries of a channel meet in LDS, the tile publishes its own
+// summary, takes the state it starts with from its predecessors', and runs its
+// steps: every tensor is read once, whatever the shape.  (Cutting the sequence
+// into segments that a first launch sums up reads the inputs twice: 195 us
+// against 101 for 1 x 32749 x 1536, and walking whole sequences with one
+// workgroup per 64 channels leaves 320 workgroups for 4 x 5120 channels, at
+// 2.3 of the 4.7 TB/s that enough tiles in flight reach.)
+//
+// Tiles of a channel block are grouped by 16 in time.  A tile waits for the
+// state at its group's start and the summaries of the tiles before it in the
+// group, and combines them in order; the group's last tile publishes the next
+// group's start.  So a long sequence costs one wait per group, and the result
+// does not depend on timing.  Tiles are numbered by a counter in the order in
+// which workgroups start, first by time: a workgroup only waits for lower
+// numbers, which have started, so the lowest unfinished one never waits.
+// A published word carries its own sign of being there (it is not all ones,
+// which the words are set to before), so no word has to be ordered against
+// another and the caches need not be written back.
 //
 // 1 - a^2 is computed as -expm1(2 A r) (see one_minus_exp), since a is close
 // to 1 in slow channels.
@@ -94,16 +106,35 @@ struct Raw<float, 2> {
 // Where a workgroup and its lanes stand.
 struct Place {
   int64_t b, dim, seqlen;
-  int sub, c, seg;      // place in time within a tile; first channel; segment
-  int64_t tile0, tile1; // tiles of the segment
+  int sub, c;           // place in time within the tile; first channel
+  int tiles, pos, k;    // tiles of a sequence; place in their order; the tile
   unsigned off;         // of the first of the lane's steps in a tile, in elements
   bool live;            // c is a channel (a pair never ends past dim: dim is even there)
 };
-template <int C>
-__device__ __forceinline__ Place place(int64_t dim, int64_t seqlen, unsigned segs, int64_t seg_tiles) {
+
+constexpr int kGroup = 16;                // tiles between two published states
+constexpr unsigned kMissing = 0xffffffffu;  // a word not yet published
+constexpr int kMostPolls = 1 << 22;       // some seconds: a wait that long would be a fault, and ends in NaN
+
+// The workgroup's tile, from the counter (which needs no order if there is
+// one tile per sequence).
+template <int C, bool REVERSE>
+__device__ __forceinline__ Place place(int64_t dim, int64_t seqlen, int64_t batch, const GlrChain &chain) {
+  __shared__ unsigned number;
+  unsigned id = blockIdx.x;
+  const int tiles = static_cast<int>((seqlen + T * kSubs - 1) / (T * kSubs));
+  if (tiles > 1) {
+    if (threadIdx.x == 0) number = atomicAdd(chain.counter, 1u);
+    __syncthreads();
+    id = number;
+  }
   Place w;
-  const unsigned ct = static_cast<unsigned>((dim + kLanes * C - 1) / (kLanes * C));
-  const unsigned id = blockIdx.x, seg = id % segs, rest = id / segs;
+  const unsigned ct = static_cast<unsigned>((dim + kLanes * C - 1) / (kLanes * C)), rows = static_cast<unsigned>(batch) * ct;
+  id = __builtin_amdgcn_readfirstlane(id);
+  const unsigned rest = id % rows;
+  w.pos = static_cast<int>(id / rows);
+  w.tiles = tiles;
+  w.k = REVERSE ? tiles - 1 - w.pos : w.pos;
   w.b = rest / ct;
   w.dim = dim;
   w.seqlen = seqlen;
@@ -112,10 +143,6 @@ __device__ __forceinline__ Place place(int64_t dim, int64_t seqlen, unsigned seg
   w.live = w.c < dim;
   if (!w.live) w.c = static_cast<int>(dim) - C;
   w.off = static_cast<unsigned>(w.sub * T) * static_cast<unsigned>(dim) + w.c;
-  w.seg = seg;
-  const int64_t tiles = (seqlen + T * kSubs - 1) / (T * kSubs);
-  w.tile0 = seg * seg_tiles;
-  w.tile1 = w.tile0 + seg_tiles < tiles ? w.tile0 + seg_tiles : tiles;
   return w;
 }
 
@@ -205,18 +232,6 @@ __device__ __forceinline__ unsigned reset_bits(unsigned byte) {
   return static_cast<unsigned>(all >> (threadIdx.x & 32)) & 0xffffu;
 }
 
-template <typename Tin, int C>
-struct Tile {
-  typename Raw<Tin, C>::type x[T], rec[T], inp[T];
-  unsigned reset;
-  __device__ __forceinline__ void get(const GlrParams &p, const Place &w, int64_t k) {
-    load<Tin, C>(p.rec, w, k, rec);
-    load<Tin, C>(p.inp, w, k, inp);
-    load<Tin, C>(p.x, w, k, x);
-    reset = load_reset(p.reset, w, k);
-  }
-};
-
 // A product of a that has a reset among its steps is negative: what comes
 // before does not pass, be it NaN or infinite.
 constexpr float kReset = -1.0f;
@@ -228,145 +243,179 @@ __device__ __forceinline__ float both(float p, float q) {
   return __uint_as_float((__float_as_uint(p * q) & 0x7fffffffu) | ((__float_as_uint(p) | __float_as_uint(q)) & 0x80000000u));
 }
 
-// The state a lane starts tile `it` with, and (next) the tile's end state:
-// from `carry` through the lanes' summaries prod, end.  REVERSE: time runs
-// from the last lane to the first.
-template <int C, bool REVERSE>
-__device__ __forceinline__ void join(float (&lds)[2][kSubs][kLanes][2 * C], int it, const Place &w,
-                                     const float (&prod)[C], const float (&end)[C], const float (&carry)[C],
-                                     float (&start)[C], float (&next)[C]) {
-  const int l = threadIdx.x % kLanes;
-  float *mine = lds[it & 1][w.sub][l];
-#pragma unroll
-  for (int c = 0; c < C; ++c) {
-    mine[2 * c] = prod[c];
-    mine[2 * c + 1] = end[c];
+// Words that are read by other workgroups, at the scope of the whole GPU.
+template <typename W>
+__device__ __forceinline__ void publish(W *p, W v) {
+  __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+template <typename W>
+__device__ __forceinline__ W await(const W *p) {
+  W v = __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  for (int n = 0; v == static_cast<W>(~W{0}) && n < kMostPolls; ++n) {
+    __builtin_amdgcn_s_sleep(2);
+    v = __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   }
-  __syncthreads();  // (the other buffer is written two tiles later, past the next barrier)
-  float s[C];
-#pragma unroll
-  for (int c = 0; c < C; ++c) s[c] = start[c] = carry[c];
-#pragma unroll
-  for (int k = 0; k < kSubs; ++k) {
-    const int sub = REVERSE ? kSubs - 1 - k : k;
-    const float *v = lds[it & 1][sub][l];
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-      if (sub == w.sub) start[c] = s[c];
-      s[c] = after(v[2 * c], s[c], v[2 * c + 1]);
-    }
-  }
-#pragma unroll
-  for (int c = 0; c < C; ++c) next[c] = s[c];
+  return v;  // (all ones is a NaN)
+}
+__device__ __forceinline__ unsigned word(float v) {  // a NaN keeps its sign, and is not all ones
+  const unsigned b = __float_as_uint(v);
+  return v != v ? (b & 0x80000000u) | 0x7fc00000u : b;
 }
 
-// SUM: only the segment's summary, (product of a, end state from zero), into ws.
-template <typename Tin, typename Tout, int C, bool SUM>
-__global__ void __launch_bounds__(256, 3) glr_fwd_kernel(const GlrParams p, unsigned segs, int64_t seg_tiles) {
-  __shared__ __align__(16) float lds[2][kSubs][kLanes][2 * C];
-  const Place w = place<C>(p.dim, p.seqlen, SUM ? segs - 1 : segs, seg_tiles);
-  float A[C], carry[C], whole[C];
+struct Scratch {
+  float subs[kSubs][kLanes][4];    // (product, end) of the lanes in time
+  float tiles[kGroup][kLanes][4];  // and of the tiles before this one in its group
+  float start[kLanes][2];          // state at the group's start
+};
+
+// The state this lane starts with, from all lanes' summaries prod, end, the
+// tiles before, and `first`, the state the sequence starts with; `last` is the
+// state after the tile, where the sequence or a group ends.
+template <int C, bool REVERSE>
+__device__ __forceinline__ void join(Scratch &lds, const GlrChain &chain, const Place &w, const float (&prod)[C],
+                                     const float (&end)[C], const float (&first)[C], float (&start)[C], float (&last)[C]) {
+  const int l = threadIdx.x % kLanes, before = w.pos % kGroup, group = w.pos / kGroup;
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    lds.subs[w.sub][l][2 * c] = prod[c];
+    lds.subs[w.sub][l][2 * c + 1] = end[c];
+  }
+  __syncthreads();
+  if (w.tiles > 1) {
+    uint64_t *sums = chain.sums + (w.b * w.tiles + w.pos - before) * w.dim + w.c;  // of the group's first tile
+    if (w.sub == 0 && w.live && before < kGroup - 1 && w.pos + 1 < w.tiles) {
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        float p = 1.0f, e = 0.0f;
+#pragma unroll
+        for (int k = 0; k < kSubs; ++k) {
+          const float *v = lds.subs[REVERSE ? kSubs - 1 - k : k][l];
+          e = after(v[2 * c], e, v[2 * c + 1]);
+          p = both(p, v[2 * c]);
+        }
+        publish(sums + before * w.dim + c, static_cast<uint64_t>(word(p)) | static_cast<uint64_t>(word(e)) << 32);
+      }
+    }
+    for (int m = w.sub; m < before; m += kSubs) {
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        const uint64_t v = await(sums + m * w.dim + c);
+        lds.tiles[m][l][2 * c] = __uint_as_float(static_cast<unsigned>(v));
+        lds.tiles[m][l][2 * c + 1] = __uint_as_float(static_cast<unsigned>(v >> 32));
+      }
+    }
+    if (group > 0 && w.sub == kSubs - 1) {
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+        lds.start[l][c] = __uint_as_float(
+            await(chain.starts + (w.b * ((w.tiles + kGroup - 1) / kGroup) + group) * w.dim + w.c + c));
+    }
+    __syncthreads();
+  }
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    float s = group > 0 ? lds.start[l][c] : first[c];
+    for (int m = 0; m < before; ++m) s = after(lds.tiles[m][l][2 * c], s, lds.tiles[m][l][2 * c + 1]);
+#pragma unroll
+    for (int k = 0; k < kSubs; ++k) {
+      const int sub = REVERSE ? kSubs - 1 - k : k;
+      if (sub == w.sub) start[c] = s;
+      s = after(lds.subs[sub][l][2 * c], s, lds.subs[sub][l][2 * c + 1]);
+    }
+    last[c] = s;
+  }
+  if (w.sub == 0 && w.live && before == kGroup - 1 && w.pos + 1 < w.tiles) {
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+      publish(chain.starts + (w.b * ((w.tiles + kGroup - 1) / kGroup) + group + 1) * w.dim + w.c + c, word(last[c]));
+  }
+}
+
+// All words missing, and the counter at 0.
+__global__ void __launch_bounds__(256) glr_clear_kernel(uint4 *words, int64_t n, unsigned *counter) {
+  const int64_t id = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (id < n) words[id] = make_uint4(kMissing, kMissing, kMissing, kMissing);
+  if (id == 0) *counter = 0;
+}
+
+template <typename Tin, typename Tout, int C>
+__global__ void __launch_bounds__(256, 3) glr_fwd_kernel(const GlrParams p) {
+  __shared__ __align__(16) Scratch lds;
+  const Place w = place<C, false>(p.dim, p.seqlen, p.batch, p.chain);
+  typename Raw<Tin, C>::type rx[T], rrec[T], rinp[T];
+  load<Tin, C>(p.rec, w, w.k, rrec);
+  load<Tin, C>(p.inp, w, w.k, rinp);
+  load<Tin, C>(p.x, w, w.k, rx);
+  const unsigned reset = reset_bits(load_reset(p.reset, w, w.k));
+  float A[C], first[C];
 #pragma unroll
   for (int c = 0; c < C; ++c) {
     A[c] = p.A[w.c + c];
-    carry[c] = SUM || p.h0 == nullptr ? 0.0f : p.h0[w.b * p.dim + w.c + c];
-    whole[c] = 1.0f;
+    first[c] = p.h0 == nullptr ? 0.0f : p.h0[w.b * p.dim + w.c + c];
   }
-  if constexpr (!SUM) {
-    for (int k = 0; k < w.seg; ++k) {
-      const float *s = p.ws + ((w.b * (segs - 1) + k) * p.dim + w.c) * 2;
+  const int64_t t0 = static_cast<int64_t>(w.k) * T * kSubs + w.sub * T;
+  const int steps = p.seqlen - t0 < T ? static_cast<int>(p.seqlen - t0) : T;  // of this lane
+  float a[T][C], u[T][C], prod[C], end[C], start[C], last[C];
 #pragma unroll
-      for (int c = 0; c < C; ++c) carry[c] = after(s[2 * c], carry[c], s[2 * c + 1]);
-    }
+  for (int j = 0; j < T; ++j) {
+    float x[C], rec[C], inp[C];
+    Raw<Tin, C>::get(rx[j], x);
+    Raw<Tin, C>::get(rrec[j], rec);
+    Raw<Tin, C>::get(rinp[j], inp);
+#pragma unroll
+    for (int c = 0; c < C; ++c) gates(x[c], rec[c], inp[c], A[c], a[j][c], u[j][c]);
+    if (j % 4 == 3) __builtin_amdgcn_sched_barrier(0);  // bounds the registers of interleaved steps
   }
-  const int64_t nstate = (p.seqlen + T - 1) / T;
-  Tile<Tin, C> now;
-  if (w.tile0 < w.tile1) now.get(p, w, w.tile0);
-  for (int64_t k = w.tile0; k < w.tile1; ++k) {
-    const int64_t t0 = k * T * kSubs + w.sub * T;
-    const int steps = p.seqlen - t0 < T ? static_cast<int>(p.seqlen - t0) : T;  // of this lane
-    float a[T][C], u[T][C], prod[C], end[C], start[C], next[C];
+  if (w.k + 1 == w.tiles) {  // steps past the end change nothing
 #pragma unroll
-    for (int j = 0; j < T; ++j) {
-      float x[C], rec[C], inp[C];
-      Raw<Tin, C>::get(now.x[j], x);
-      Raw<Tin, C>::get(now.rec[j], rec);
-      Raw<Tin, C>::get(now.inp[j], inp);
+    for (int j = 0; j < T; ++j)
 #pragma unroll
-      for (int c = 0; c < C; ++c) gates(x[c], rec[c], inp[c], A[c], a[j][c], u[j][c]);
-      if (j % 4 == 3) __builtin_amdgcn_sched_barrier(0);  // bounds the registers of interleaved steps
-    }
-    const unsigned reset = reset_bits(now.reset);
-    if (k + 1 < w.tile1) now.get(p, w, k + 1);  // on its way during the rest of this tile
-    if ((k + 1) * T * kSubs > p.seqlen) {       // steps past the end change nothing
-#pragma unroll
-      for (int j = 0; j < T; ++j)
-#pragma unroll
-        for (int c = 0; c < C; ++c) {
-          a[j][c] = j < steps ? a[j][c] : 1.0f;
-          u[j][c] = j < steps ? u[j][c] : 0.0f;
-        }
-    }
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-      prod[c] = 1.0f;
-      end[c] = 0.0f;
-    }
-    const bool resets = __any(reset != 0);  // few tiles have one
-    if (!resets) {
-#pragma unroll
-      for (int j = 0; j < T; ++j)
-#pragma unroll
-        for (int c = 0; c < C; ++c) {
-          prod[c] *= a[j][c];
-          end[c] = fmaf(a[j][c], end[c], u[j][c]);
-        }
-    } else {
-#pragma unroll
-      for (int j = 0; j < T; ++j)
-#pragma unroll
-        for (int c = 0; c < C; ++c) {
-          const bool cut = reset >> j & 1;
-          prod[c] = (cut ? kReset : prod[c]) * a[j][c];
-          end[c] = fmaf(a[j][c], cut ? 0.0f : end[c], u[j][c]);
-        }
-    }
-    join<C, false>(lds, static_cast<int>(k - w.tile0), w, prod, end, carry, start, next);
-    if constexpr (SUM) {
-#pragma unroll
-      for (int sub = 0; sub < kSubs; ++sub)
-#pragma unroll
-        for (int c = 0; c < C; ++c)
-          whole[c] = both(whole[c], lds[(k - w.tile0) & 1][sub][threadIdx.x % kLanes][2 * c]);
-    } else {
-      if (p.states != nullptr) {
-        const __amdgpu_buffer_rsrc_t r = rows_of(p.states, w.b * nstate + k * kSubs, nstate - k * kSubs, kSubs, p.dim * 4);
-        const unsigned at = (static_cast<unsigned>(w.sub) * static_cast<unsigned>(p.dim) + w.c) * 4;
-        write(Raw<float, C>::put(start), r, w.live ? at : 0xfffffff0u);
+      for (int c = 0; c < C; ++c) {
+        a[j][c] = j < steps ? a[j][c] : 1.0f;
+        u[j][c] = j < steps ? u[j][c] : 0.0f;
       }
-      const __amdgpu_buffer_rsrc_t r = tile_of<Tout>(p.y, w, k);
-#pragma unroll
-      for (int j = 0; j < T; ++j) {
-#pragma unroll
-        for (int c = 0; c < C; ++c)
-          start[c] = fmaf(a[j][c], resets && (reset >> j & 1) ? 0.0f : start[c], u[j][c]);
-        write(Raw<Tout, C>::put(start), r, store_at<Tout>(w, j));
-      }
-    }
-#pragma unroll
-    for (int c = 0; c < C; ++c) carry[c] = next[c];
   }
-  if (!w.live || w.sub != 0) return;
-  if constexpr (SUM) {
-    float *s = p.ws + ((w.b * (segs - 1) + w.seg) * p.dim + w.c) * 2;
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      s[2 * c] = whole[c];
-      s[2 * c + 1] = carry[c];
-    }
-  } else if (p.h_last != nullptr && w.seg + 1 == static_cast<int>(segs)) {
+  for (int c = 0; c < C; ++c) {
+    prod[c] = 1.0f;
+    end[c] = 0.0f;
+  }
+  const bool resets = __any(reset != 0);  // few tiles have one
+  if (!resets) {
 #pragma unroll
-    for (int c = 0; c < C; ++c) p.h_last[w.b * p.dim + w.c + c] = carry[c];
+    for (int j = 0; j < T; ++j)
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        prod[c] *= a[j][c];
+        end[c] = fmaf(a[j][c], end[c], u[j][c]);
+      }
+  } else {
+#pragma unroll
+    for (int j = 0; j < T; ++j)
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        const bool cut = reset >> j & 1;
+        prod[c] = (cut ? kReset : prod[c]) * a[j][c];
+        end[c] = fmaf(a[j][c], cut ? 0.0f : end[c], u[j][c]);
+      }
+  }
+  join<C, false>(lds, p.chain, w, prod, end, first, start, last);
+  if (p.states != nullptr) {
+    const int64_t nstate = (p.seqlen + T - 1) / T, row = static_cast<int64_t>(w.k) * kSubs;
+    const __amdgpu_buffer_rsrc_t r = rows_of(p.states, w.b * nstate + row, nstate - row, kSubs, p.dim * 4);
+    const unsigned at = (static_cast<unsigned>(w.sub) * static_cast<unsigned>(p.dim) + w.c) * 4;
+    write(Raw<float, C>::put(start), r, w.live ? at : 0xfffffff0u);
+  }
+  const __amdgpu_buffer_rsrc_t r = tile_of<Tout>(p.y, w, w.k);
+#pragma unroll
+  for (int j = 0; j < T; ++j) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) start[c] = fmaf(a[j][c], resets && (reset >> j & 1) ? 0.0f : start[c], u[j][c]);
+    write(Raw<Tout, C>::put(start), r, store_at<Tout>(w, j));
+  }
+  if (p.h_last != nullptr && w.k + 1 == w.tiles && w.live && w.sub == 0) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) p.h_last[w.b * p.dim + w.c + c] = last[c];
   }
 }
 
@@ -375,165 +424,144 @@ __global__ void __launch_bounds__(256, 3) glr_fwd_kernel(const GlrParams p, unsi
 // steps takes a alone and sums up (product of a, what arrives before the
 // lane); once joined, one pass back in time gives g, and one forward the state
 // and every output, so each gate is computed once (r twice).
-// SUM: only the segment's summary, from rec and dy.
-template <typename Tin, int C, bool SUM>
-__global__ void __launch_bounds__(256, C == 2 ? 2 : 3) glr_bwd_kernel(const GlrBwdParams p, unsigned segs, int64_t seg_tiles) {
-  __shared__ __align__(16) float lds[2][kSubs][kLanes][2 * C];
+template <typename Tin, int C>
+__global__ void __launch_bounds__(256, C == 2 ? 2 : 3) glr_bwd_kernel(const GlrBwdParams p) {
+  __shared__ __align__(16) Scratch lds;
   typedef typename Raw<Tin, C>::type raw;
-  Place w = place<C>(p.dim, p.seqlen, SUM ? segs - 1 : segs, seg_tiles);
-  if constexpr (SUM) {  // segments 1 ..: nothing is carried out of the first
-    w.seg += 1;
-    w.tile0 += seg_tiles;
-    const int64_t tiles = (p.seqlen + T * kSubs - 1) / (T * kSubs);
-    w.tile1 = w.tile0 + seg_tiles < tiles ? w.tile0 + seg_tiles : tiles;
+  const Place w = place<C, true>(p.dim, p.seqlen, p.batch, p.chain);
+  raw rec[T], dy[T], x[T], inp[T];
+  load<Tin, C>(p.rec, w, w.k, rec);
+  load<Tin, C>(p.dy, w, w.k, dy);
+  load<Tin, C>(p.x, w, w.k, x);
+  load<Tin, C>(p.inp, w, w.k, inp);
+  const unsigned reset = reset_bits(load_reset(p.reset, w, w.k));
+  float A[C], first[C], dA[C], h[C];
+  {
+    const int64_t nstate = (p.seqlen + T - 1) / T, row = static_cast<int64_t>(w.k) * kSubs;
+    const __amdgpu_buffer_rsrc_t r = rows_of(p.states, w.b * nstate + row, nstate - row, kSubs, p.dim * 4);
+    const unsigned at = (static_cast<unsigned>(w.sub) * static_cast<unsigned>(p.dim) + w.c) * 4;
+    Raw<float, C>::get(fetch<typename Raw<float, C>::type>(r, at), h);
   }
-  float A[C], carry[C], whole[C], dA[C];
 #pragma unroll
   for (int c = 0; c < C; ++c) {
     A[c] = p.A[w.c + c];
-    carry[c] = SUM || p.dh_last == nullptr ? 0.0f : p.dh_last[w.b * p.dim + w.c + c];
-    whole[c] = 1.0f;
+    first[c] = p.dh_last == nullptr ? 0.0f : p.dh_last[w.b * p.dim + w.c + c];
     dA[c] = 0.0f;
   }
-  if constexpr (!SUM) {
-    for (int k = static_cast<int>(segs) - 1; k > w.seg; --k) {
-      const float *s = p.ws_seg + ((w.b * (segs - 1) + k - 1) * p.dim + w.c) * 2;
+  const int64_t t0 = static_cast<int64_t>(w.k) * T * kSubs + w.sub * T;
+  const int steps = p.seqlen - t0 < T ? static_cast<int>(p.seqlen - t0) : T;  // of this lane
+  float a[T][C], g[T][C], prod[C], end[C], start[C], last[C];
 #pragma unroll
-      for (int c = 0; c < C; ++c) carry[c] = after(s[2 * c], carry[c], s[2 * c + 1]);
-    }
+  for (int c = 0; c < C; ++c) {
+    prod[c] = 1.0f;
+    end[c] = 0.0f;
   }
-  const int64_t nstate = (p.seqlen + T - 1) / T;
-  for (int64_t k = w.tile1 - 1; k >= w.tile0; --k) {
-    raw rec[T], dy[T], x[T], inp[T];
-    const int64_t t0 = k * T * kSubs + w.sub * T;
-    load<Tin, C>(p.rec, w, k, rec);
-    load<Tin, C>(p.dy, w, k, dy);
-    float h[C];
-    if constexpr (!SUM) {
-      load<Tin, C>(p.x, w, k, x);
-      load<Tin, C>(p.inp, w, k, inp);
-      const __amdgpu_buffer_rsrc_t r = rows_of(p.states, w.b * nstate + k * kSubs, nstate - k * kSubs, kSubs, p.dim * 4);
-      const unsigned at = (static_cast<unsigned>(w.sub) * static_cast<unsigned>(p.dim) + w.c) * 4;
-      Raw<float, C>::get(fetch<typename Raw<float, C>::type>(r, at), h);
-    }
-    const unsigned reset = reset_bits(load_reset(p.reset, w, k));
-    const int steps = p.seqlen - t0 < T ? static_cast<int>(p.seqlen - t0) : T;  // of this lane
-    float a[T][C], g[T][C], prod[C], end[C], start[C], next[C];
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      prod[c] = 1.0f;
-      end[c] = 0.0f;
-    }
+  for (int j = T - 1; j >= 0; --j) {
+    float r[C];
+    Raw<Tin, C>::get(rec[j], r);
+    Raw<Tin, C>::get(dy[j], g[j]);
 #pragma unroll
-    for (int j = T - 1; j >= 0; --j) {
-      float r[C];
-      Raw<Tin, C>::get(rec[j], r);
-      Raw<Tin, C>::get(dy[j], g[j]);
+    for (int c = 0; c < C; ++c) a[j][c] = __builtin_amdgcn_exp2f(A[c] * sigmoid(r[c]) * kLog2e);
+  }
+  if (w.k + 1 == w.tiles) {  // steps past the end change nothing
 #pragma unroll
-      for (int c = 0; c < C; ++c) a[j][c] = __builtin_amdgcn_exp2f(A[c] * sigmoid(r[c]) * kLog2e);
-    }
-    if ((k + 1) * T * kSubs > p.seqlen) {  // steps past the end change nothing
-#pragma unroll
-      for (int j = 0; j < T; ++j)
-#pragma unroll
-        for (int c = 0; c < C; ++c) {
-          a[j][c] = j < steps ? a[j][c] : 1.0f;
-          g[j][c] = j < steps ? g[j][c] : 0.0f;
-        }
-    }
-#pragma unroll
-    for (int j = T - 1; j >= 0; --j)
+    for (int j = 0; j < T; ++j)
 #pragma unroll
       for (int c = 0; c < C; ++c) {
-        const bool cut = reset >> j & 1;
-        end[c] = cut ? 0.0f : a[j][c] * (end[c] + g[j][c]);
-        prod[c] = cut ? kReset : a[j][c] * prod[c];
+        a[j][c] = j < steps ? a[j][c] : 1.0f;
+        g[j][c] = j < steps ? g[j][c] : 0.0f;
       }
-    join<C, true>(lds, static_cast<int>(w.tile1 - 1 - k), w, prod, end, carry, start, next);
-    if constexpr (SUM) {
-#pragma unroll
-      for (int sub = 0; sub < kSubs; ++sub)
-#pragma unroll
-        for (int c = 0; c < C; ++c)
-          whole[c] = both(whole[c], lds[(w.tile1 - 1 - k) & 1][sub][threadIdx.x % kLanes][2 * c]);
-    } else {
-#pragma unroll
-      for (int j = T - 1; j >= 0; --j)
-#pragma unroll
-        for (int c = 0; c < C; ++c) {
-          g[j][c] += start[c];
-          start[c] = (reset >> j & 1) ? 0.0f : a[j][c] * g[j][c];
-        }
-      if ((k + 1) * T * kSubs > p.seqlen) {  // dh_last has passed the steps past the end: they add nothing to dA
-#pragma unroll
-        for (int j = 0; j < T; ++j)
-#pragma unroll
-          for (int c = 0; c < C; ++c) g[j][c] = j < steps ? g[j][c] : 0.0f;
-      }
-      const __amdgpu_buffer_rsrc_t rdx = tile_of<Tin>(p.dx, w, k), rdr = tile_of<Tin>(p.drec, w, k);
-      const __amdgpu_buffer_rsrc_t rdi = tile_of<Tin>(p.dinp, w, k);
-#pragma unroll
-      for (int j = 0; j < T; ++j) {
-        float fx[C], fr[C], fi[C], dx[C], dr[C], di[C];
-        Raw<Tin, C>::get(x[j], fx);
-        Raw<Tin, C>::get(rec[j], fr);
-        Raw<Tin, C>::get(inp[j], fi);
-#pragma unroll
-        for (int c = 0; c < C; ++c) {
-          // s(v) with 1 - s(v) = e s(v), e = exp(-v): no cancellation at either end.
-          const float vr = fr[c] < -87.0f ? -87.0f : fr[c], vi = fi[c] < -87.0f ? -87.0f : fi[c];
-          const float er = __builtin_amdgcn_exp2f(-vr * kLog2e), r = __builtin_amdgcn_rcpf(1.0f + er);
-          const float ei = __builtin_amdgcn_exp2f(-vi * kLog2e), i = __builtin_amdgcn_rcpf(1.0f + ei);
-          const float la = A[c] * r, q = one_minus_exp(2.0f * la, a[j][c]);
-          const float rb = q >= kSmallest ? __builtin_amdgcn_rsqf(q) : 0.0f;  // 1 / b
-          const float ix = i * fx[c], gb = g[j][c] * (q * rb), hp = (reset >> j & 1) ? 0.0f : h[c];
-          const float wt = g[j][c] * a[j][c] * fmaf(-a[j][c] * rb, ix, hp);
-          dx[c] = gb * i;
-          dr[c] = wt * la * (er * r);
-          di[c] = gb * ix * (ei * i);
-          dA[c] = fmaf(wt, r, dA[c]);
-          h[c] = fmaf(a[j][c], hp, q * rb * ix);
-        }
-        const unsigned at = store_at<Tin>(w, j);
-        write(Raw<Tin, C>::put(dx), rdx, at);
-        write(Raw<Tin, C>::put(dr), rdr, at);
-        write(Raw<Tin, C>::put(di), rdi, at);
-      }
-    }
-#pragma unroll
-    for (int c = 0; c < C; ++c) carry[c] = next[c];
   }
-  if constexpr (SUM) {
-    if (!w.live || w.sub != 0) return;
-    float *s = p.ws_seg + ((w.b * (segs - 1) + w.seg - 1) * p.dim + w.c) * 2;
+#pragma unroll
+  for (int j = T - 1; j >= 0; --j)
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      s[2 * c] = whole[c];
-      s[2 * c + 1] = carry[c];
+      const bool cut = reset >> j & 1;
+      end[c] = cut ? 0.0f : a[j][c] * (end[c] + g[j][c]);
+      prod[c] = cut ? kReset : a[j][c] * prod[c];
     }
-  } else {
-    // dA over the lanes of a channel, in their order.
-    __syncthreads();
+  join<C, true>(lds, p.chain, w, prod, end, first, start, last);
 #pragma unroll
-    for (int c = 0; c < C; ++c) lds[0][w.sub][threadIdx.x % kLanes][c] = dA[c];
-    __syncthreads();
-    if (!w.live || w.sub != 0) return;
+  for (int j = T - 1; j >= 0; --j)
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      float s = 0.0f;
-      for (int sub = 0; sub < kSubs; ++sub) s += lds[0][sub][threadIdx.x % kLanes][c];
-      p.ws_dA[(w.b * segs + w.seg) * p.dim + w.c + c] = s;
-      if (p.dh0 != nullptr && w.seg == 0) p.dh0[w.b * p.dim + w.c + c] = carry[c];
+      g[j][c] += start[c];
+      start[c] = (reset >> j & 1) ? 0.0f : a[j][c] * g[j][c];
     }
+  if (w.k + 1 == w.tiles) {  // dh_last has passed the steps past the end: they add nothing to dA
+#pragma unroll
+    for (int j = 0; j < T; ++j)
+#pragma unroll
+      for (int c = 0; c < C; ++c) g[j][c] = j < steps ? g[j][c] : 0.0f;
+  }
+  const __amdgpu_buffer_rsrc_t rdx = tile_of<Tin>(p.dx, w, w.k), rdr = tile_of<Tin>(p.drec, w, w.k);
+  const __amdgpu_buffer_rsrc_t rdi = tile_of<Tin>(p.dinp, w, w.k);
+#pragma unroll
+  for (int j = 0; j < T; ++j) {
+    float fx[C], fr[C], fi[C], dx[C], dr[C], di[C];
+    Raw<Tin, C>::get(x[j], fx);
+    Raw<Tin, C>::get(rec[j], fr);
+    Raw<Tin, C>::get(inp[j], fi);
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      // s(v) with 1 - s(v) = e s(v), e = exp(-v): no cancellation at either end.
+      const float vr = fr[c] < -87.0f ? -87.0f : fr[c], vi = fi[c] < -87.0f ? -87.0f : fi[c];
+      const float er = __builtin_amdgcn_exp2f(-vr * kLog2e), r = __builtin_amdgcn_rcpf(1.0f + er);
+      const float ei = __builtin_amdgcn_exp2f(-vi * kLog2e), i = __builtin_amdgcn_rcpf(1.0f + ei);
+      const float la = A[c] * r, q = one_minus_exp(2.0f * la, a[j][c]);
+      const float rb = q >= kSmallest ? __builtin_amdgcn_rsqf(q) : 0.0f;  // 1 / b
+      const float ix = i * fx[c], gb = g[j][c] * (q * rb), hp = (reset >> j & 1) ? 0.0f : h[c];
+      const float wt = g[j][c] * a[j][c] * fmaf(-a[j][c] * rb, ix, hp);
+      dx[c] = gb * i;
+      dr[c] = wt * la * (er * r);
+      di[c] = gb * ix * (ei * i);
+      dA[c] = fmaf(wt, r, dA[c]);
+      h[c] = fmaf(a[j][c], hp, q * rb * ix);
+    }
+    const unsigned at = store_at<Tin>(w, j);
+    write(Raw<Tin, C>::put(dx), rdx, at);
+    write(Raw<Tin, C>::put(dr), rdr, at);
+    write(Raw<Tin, C>::put(di), rdi, at);
+  }
+  // dA over the lanes of a channel, in their order.
+  __syncthreads();
+  const int l = threadIdx.x % kLanes;
+#pragma unroll
+  for (int c = 0; c < C; ++c) lds.subs[w.sub][l][c] = dA[c];
+  __syncthreads();
+  if (!w.live || w.sub != 0) return;
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    float s = 0.0f;
+    for (int sub = 0; sub < kSubs; ++sub) s += lds.subs[sub][l][c];
+    p.ws_dA[(w.b * w.tiles + w.k) * p.dim + w.c + c] = s;
+    if (p.dh0 != nullptr && w.k == 0) p.dh0[w.b * p.dim + w.c + c] = last[c];
   }
 }
 
-__global__ void __launch_bounds__(256) glr_sum_kernel(const float *part, float *dA, int64_t parts, int64_t dim) {
-  const int64_t d = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  if (d >= dim) return;
+// dA: 16 threads share the terms of a channel, a workgroup has 64 channels.
+__global__ void __launch_bounds__(1024) glr_sum_kernel(const float *part, float *dA, int64_t parts, int64_t dim) {
+  __shared__ float lds[16][64];
+  const int64_t c = static_cast<int64_t>(blockIdx.x) * 64 + threadIdx.x % 64;
+  const int k0 = threadIdx.x / 64;
   float s = 0.0f;
-  for (int64_t k = 0; k < parts; ++k) s += part[k * dim + d];
-  dA[d] = s;
+  if (c < dim) {
+#pragma unroll 8
+    for (int64_t k = k0; k < parts; k += 16) s += part[k * dim + c];
+  }
+  lds[k0][threadIdx.x % 64] = s;
+  __syncthreads();
+  if (k0 != 0 || c >= dim) return;
+#pragma unroll
+  for (int k = 1; k < 16; ++k) s += lds[k][threadIdx.x];
+  dA[c] = s;
+}
+
+// An empty sequence: the state passes through.
+__global__ void __launch_bounds__(256) glr_pass_kernel(const float *from, float *to, int64_t n) {
+  const int64_t id = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (id < n) to[id] = from != nullptr ? from[id] : 0.0f;
 }
 
 template <typename Tin, typename Tout>
@@ -550,28 +578,33 @@ __global__ void __launch_bounds__(256) glr_step_kernel(const GlrParams p) {
 
 dim3 blocks(int64_t n, int64_t per) { return dim3(static_cast<uint32_t>((n + per - 1) / per)); }
 
+// Tiles of all sequences, in workgroups.
+template <int C>
+int64_t all_tiles(int64_t batch, int64_t seqlen, int64_t dim) {
+  return batch * ((dim + kLanes * C - 1) / (kLanes * C)) * ((seqlen + T * kSubs - 1) / (T * kSubs));
+}
+
+void clear(const GlrChain &chain, int64_t seqlen, hipStream_t s) {
+  if (seqlen <= T * kSubs) return;  // one tile per sequence: nothing is published
+  hipLaunchKernelGGL(glr_clear_kernel, blocks(chain.bytes / 16, 256), dim3(256), 0, s, reinterpret_cast<uint4 *>(chain.sums),
+                     chain.bytes / 16, chain.counter);
+}
+
 template <typename Tin, typename Tout, int C>
-hipError_t run_fwd(const GlrParams &p, const GlrPlan &g, hipStream_t s) {
-  const int64_t ct = (p.dim + kLanes * C - 1) / (kLanes * C);
-  if (g.segs > 1)
-    hipLaunchKernelGGL((glr_fwd_kernel<Tin, Tout, C, true>), dim3(static_cast<uint32_t>(p.batch * ct * (g.segs - 1))),
-                       dim3(256), 0, s, p, g.segs, g.seg_tiles);
-  hipLaunchKernelGGL((glr_fwd_kernel<Tin, Tout, C, false>), dim3(static_cast<uint32_t>(p.batch * ct * g.segs)), dim3(256), 0,
-                     s, p, g.segs, g.seg_tiles);
+hipError_t run_fwd(const GlrParams &p, hipStream_t s) {
+  const int64_t n = all_tiles<C>(p.batch, p.seqlen, p.dim);
+  if (n > 0x7fffffff) return hipErrorInvalidValue;
+  clear(p.chain, p.seqlen, s);
+  hipLaunchKernelGGL((glr_fwd_kernel<Tin, Tout, C>), dim3(static_cast<uint32_t>(n)), dim3(256), 0, s, p);
   return hipGetLastError();
 }
 
 template <typename Tin, int C>
-hipError_t run_bwd(const GlrBwdParams &p, const GlrPlan &g, hipStream_t s) {
-  const int64_t ct = (p.dim + kLanes * C - 1) / (kLanes * C);
-  if (p.batch > 0) {
-    if (g.segs > 1)
-      hipLaunchKernelGGL((glr_bwd_kernel<Tin, C, true>), dim3(static_cast<uint32_t>(p.batch * ct * (g.segs - 1))), dim3(256),
-                         0, s, p, g.segs, g.seg_tiles);
-    hipLaunchKernelGGL((glr_bwd_kernel<Tin, C, false>), dim3(static_cast<uint32_t>(p.batch * ct * g.segs)), dim3(256), 0, s,
-                       p, g.segs, g.seg_tiles);
-  }
-  hipLaunchKernelGGL(glr_sum_kernel, blocks(p.dim, 256), dim3(256), 0, s, p.ws_dA, p.dA, p.batch * g.segs, p.dim);
+hipError_t run_bwd(const GlrBwdParams &p, hipStream_t s) {
+  const int64_t n = all_tiles<C>(p.batch, p.seqlen, p.dim);
+  if (n > 0x7fffffff) return hipErrorInvalidValue;
+  clear(p.chain, p.seqlen, s);
+  hipLaunchKernelGGL((glr_bwd_kernel<Tin, C>), dim3(static_cast<uint32_t>(n)), dim3(256), 0, s, p);
   return hipGetLastError();
 }
 
@@ -580,28 +613,35 @@ bool even8(const void *p) { return reinterpret_cast<uintptr_t>(p) % 8 == 0; }
 
 }  // namespace
 
-GlrPlan glr_plan(int64_t batch, int64_t seqlen, int64_t dim) {
-  // Workgroups of a whole sequence are enough from one per CU on; below that,
-  // segments up to about three workgroups per CU (what fits at once).
-  const int64_t tiles = (seqlen + T * kSubs - 1) / (T * kSubs), ct = (dim + kLanes - 1) / kLanes;
-  const int64_t wide = batch * ((ct + 1) / 2);
-  int64_t segs = 1;
-  if (wide > 0 && wide < 256) segs = 768 / wide;
-  if (segs > tiles) segs = tiles;
-  if (segs > 64) segs = 64;
-  GlrPlan g;
-  g.seg_tiles = segs > 1 ? (tiles + segs - 1) / segs : (tiles > 0 ? tiles : 1);
-  g.segs = static_cast<unsigned>(tiles > 0 ? (tiles + g.seg_tiles - 1) / g.seg_tiles : 1);
-  return g;
+size_t glr_chain_bytes(int64_t batch, int64_t seqlen, int64_t dim) {
+  const int64_t tiles = (seqlen + T * kSubs - 1) / (T * kSubs);
+  if (tiles <= 1) return 0;
+  const int64_t sums = batch * tiles * dim * 8, starts = batch * ((tiles + kGroup - 1) / kGroup) * dim * 4;
+  return static_cast<size_t>((sums + starts + 15) / 16 * 16);
 }
 
-hipError_t launch_glr(const GlrParams &p, const GlrPlan &g, int in_bf16, int out_bf16, hipStream_t s) {
+GlrChain glr_chain(void *at, int64_t batch, int64_t seqlen, int64_t dim) {
+  GlrChain c{};
+  c.bytes = static_cast<int64_t>(glr_chain_bytes(batch, seqlen, dim));
+  if (c.bytes == 0) return c;
+  char *base = static_cast<char *>(at);
+  c.counter = reinterpret_cast<unsigned *>(base);
+  c.sums = reinterpret_cast<uint64_t *>(base + 256);
+  c.starts = reinterpret_cast<unsigned *>(c.sums + batch * ((seqlen + T * kSubs - 1) / (T * kSubs)) * dim);
+  return c;
+}
+
+hipError_t launch_glr(const GlrParams &p, int in_bf16, int out_bf16, hipStream_t s) {
+  if (p.seqlen == 0) {
+    hipLaunchKernelGGL(glr_pass_kernel, blocks(p.batch * p.dim, 256), dim3(256), 0, s, p.h0, p.h_last, p.batch * p.dim);
+    return hipGetLastError();
+  }
   // Two channels per lane where every row of two starts on a dword.
   const bool pairs = p.dim % 2 == 0 && even(p.x) && even(p.rec) && even(p.inp) && even8(p.states) &&
                      (out_bf16 ? even(p.y) : even8(p.y));
-  if (in_bf16 && out_bf16) return pairs ? run_fwd<uint16_t, uint16_t, 2>(p, g, s) : run_fwd<uint16_t, uint16_t, 1>(p, g, s);
-  if (in_bf16) return pairs ? run_fwd<uint16_t, float, 2>(p, g, s) : run_fwd<uint16_t, float, 1>(p, g, s);
-  return out_bf16 ? run_fwd<float, uint16_t, 1>(p, g, s) : run_fwd<float, float, 1>(p, g, s);
+  if (in_bf16 && out_bf16) return pairs ? run_fwd<uint16_t, uint16_t, 2>(p, s) : run_fwd<uint16_t, uint16_t, 1>(p, s);
+  if (in_bf16) return pairs ? run_fwd<uint16_t, float, 2>(p, s) : run_fwd<uint16_t, float, 1>(p, s);
+  return out_bf16 ? run_fwd<float, uint16_t, 1>(p, s) : run_fwd<float, float, 1>(p, s);
 }
 
 hipError_t launch_glr_step(const GlrParams &p, int in_bf16, int out_bf16, hipStream_t s) {
@@ -613,11 +653,20 @@ hipError_t launch_glr_step(const GlrParams &p, int in_bf16, int out_bf16, hipStr
   return hipGetLastError();
 }
 
-hipError_t launch_glr_bwd(const GlrBwdParams &p, const GlrPlan &g, int in_bf16, hipStream_t s) {
-  const bool pairs = p.dim % 2 == 0 && even(p.x) && even(p.rec) && even(p.inp) && even(p.dy) && even8(p.states) &&
-                     even(p.dx) && even(p.drec) && even(p.dinp);
-  if (!in_bf16) return run_bwd<float, 1>(p, g, s);
-  return pairs ? run_bwd<uint16_t, 2>(p, g, s) : run_bwd<uint16_t, 1>(p, g, s);
+int64_t glr_bwd_parts(int64_t batch, int64_t seqlen) { return batch * ((seqlen + T * kSubs - 1) / (T * kSubs)); }
+
+hipError_t launch_glr_bwd(const GlrBwdParams &p, int in_bf16, hipStream_t s) {
+  if (p.batch > 0 && p.seqlen > 0) {
+    const bool pairs = p.dim % 2 == 0 && even(p.x) && even(p.rec) && even(p.inp) && even(p.dy) && even8(p.states) &&
+                       even(p.dx) && even(p.drec) && even(p.dinp);
+    const hipError_t e = !in_bf16 ? run_bwd<float, 1>(p, s) : pairs ? run_bwd<uint16_t, 2>(p, s) : run_bwd<uint16_t, 1>(p, s);
+    if (e != hipSuccess) return e;
+  } else if (p.batch > 0 && p.dh0 != nullptr) {
+    hipLaunchKernelGGL(glr_pass_kernel, blocks(p.batch * p.dim, 256), dim3(256), 0, s, p.dh_last, p.dh0, p.batch * p.dim);
+  }
+  hipLaunchKernelGGL(glr_sum_kernel, blocks(p.dim, 64), dim3(1024), 0, s, p.ws_dA, p.dA, glr_bwd_parts(p.batch, p.seqlen),
+                     p.dim);
+  return hipGetLastError();
 }
 
 }  // namespace ssmb
