@@ -36,19 +36,16 @@ namespace {
 // The smallest normal float: below it the reciprocal square root has no use.
 constexpr float kSmallest = 0x1p-126f;
 
-// 1 - exp(u) for u <= 0.  Above -0.5, where the subtraction would cancel, the
-// series -u (1 + u/2 (1 + u/3 (...))) to the 9th power (error below 1.1e-8 of
-// the result); below, 1 - a^2 with a = exp(u / 2) at hand.
+// 1 - exp(u) for u <= 0, where a = exp(u / 2) is at hand.  Above -0.4, where
+// 1 - a^2 would cancel, -u times a polynomial fitted to expm1(u) / u there
+// (relative error 2.6e-8, 1.4e-7 with its float32 roundings); below, 1 - a^2
+// (1.3e-7 in its root).
 __device__ __forceinline__ float one_minus_exp(float u, float a) {
-  float p = fmaf(u, 1.0f / 9.0f, 1.0f);
-  p = fmaf(u * (1.0f / 8.0f), p, 1.0f);
-  p = fmaf(u * (1.0f / 7.0f), p, 1.0f);
-  p = fmaf(u * (1.0f / 6.0f), p, 1.0f);
-  p = fmaf(u * (1.0f / 5.0f), p, 1.0f);
-  p = fmaf(u * (1.0f / 4.0f), p, 1.0f);
-  p = fmaf(u * (1.0f / 3.0f), p, 1.0f);
-  p = fmaf(u * (1.0f / 2.0f), p, 1.0f);
-  return u > -0.5f ? -u * p : fmaf(-a, a, 1.0f);
+  float p = fmaf(u, 0x1.ce7feep-8f, 0x1.51c052p-5f);
+  p = fmaf(u, p, 0x1.5534a4p-3f);
+  p = fmaf(u, p, 0x1.ffff2cp-2f);
+  p = fmaf(u, p, 1.0f);
+  return u > -0.4f ? -u * p : fmaf(-a, a, 1.0f);
 }
 
 __device__ __forceinline__ float sigmoid(float v) {
@@ -57,9 +54,9 @@ __device__ __forceinline__ float sigmoid(float v) {
 
 // The decay a and the weighted input u = b i x of one step.
 __device__ __forceinline__ void gates(float x, float rec, float inp, float A, float &a, float &u) {
-  const float la = A * sigmoid(rec);
-  a = __builtin_amdgcn_exp2f(la * kLog2e);
-  u = __builtin_amdgcn_sqrtf(one_minus_exp(2.0f * la, a)) * sigmoid(inp) * x;
+  const float r = sigmoid(rec);
+  a = __builtin_amdgcn_exp2f(A * kLog2e * r);
+  u = __builtin_amdgcn_sqrtf(one_minus_exp(2.0f * A * r, a)) * sigmoid(inp) * x;
 }
 
 constexpr int T = SSM_GLR_STATE_STEP;  // steps of a lane
@@ -425,7 +422,7 @@ __global__ void __launch_bounds__(256, 3) glr_fwd_kernel(const GlrParams p) {
 // lane); once joined, one pass back in time gives g, and one forward the state
 // and every output, so each gate is computed once (r twice).
 template <typename Tin, int C>
-__global__ void __launch_bounds__(256, C == 2 ? 2 : 3) glr_bwd_kernel(const GlrBwdParams p) {
+__global__ void __launch_bounds__(256, 3) glr_bwd_kernel(const GlrBwdParams p) {
   __shared__ __align__(16) Scratch lds;
   typedef typename Raw<Tin, C>::type raw;
   const Place w = place<C, true>(p.dim, p.seqlen, p.batch, p.chain);
@@ -462,7 +459,8 @@ __global__ void __launch_bounds__(256, C == 2 ? 2 : 3) glr_bwd_kernel(const GlrB
     Raw<Tin, C>::get(rec[j], r);
     Raw<Tin, C>::get(dy[j], g[j]);
 #pragma unroll
-    for (int c = 0; c < C; ++c) a[j][c] = __builtin_amdgcn_exp2f(A[c] * sigmoid(r[c]) * kLog2e);
+    for (int c = 0; c < C; ++c) a[j][c] = __builtin_amdgcn_exp2f(A[c] * kLog2e * sigmoid(r[c]));
+    if (j % 4 == 0) __builtin_amdgcn_sched_barrier(0);  // bounds the registers of interleaved steps
   }
   if (w.k + 1 == w.tiles) {  // steps past the end change nothing
 #pragma unroll
@@ -482,6 +480,14 @@ __global__ void __launch_bounds__(256, C == 2 ? 2 : 3) glr_bwd_kernel(const GlrB
       prod[c] = cut ? kReset : a[j][c] * prod[c];
     }
   join<C, true>(lds, p.chain, w, prod, end, first, start, last);
+  // The compiler is not to keep what it computed from rec and the offsets
+  // above: computing it again is cheaper than the registers.
+  Place to = w;
+  asm volatile("" : "+v"(to.off));
+  if constexpr (C == 2) {
+#pragma unroll
+    for (int j = 0; j < T; ++j) asm volatile("" : "+v"(rec[j]));
+  }
 #pragma unroll
   for (int j = T - 1; j >= 0; --j)
 #pragma unroll
@@ -519,10 +525,11 @@ __global__ void __launch_bounds__(256, C == 2 ? 2 : 3) glr_bwd_kernel(const GlrB
       dA[c] = fmaf(wt, r, dA[c]);
       h[c] = fmaf(a[j][c], hp, q * rb * ix);
     }
-    const unsigned at = store_at<Tin>(w, j);
+    const unsigned at = store_at<Tin>(to, j);
     write(Raw<Tin, C>::put(dx), rdx, at);
     write(Raw<Tin, C>::put(dr), rdr, at);
     write(Raw<Tin, C>::put(di), rdi, at);
+    if (j % 2 == 1) __builtin_amdgcn_sched_barrier(0);
   }
   // dA over the lanes of a channel, in their order.
   __syncthreads();
