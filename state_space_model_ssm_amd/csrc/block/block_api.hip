@@ -118,7 +118,7 @@ int check_glr(const ssm_glr_dims_t *d) {
 
 size_t glr_workspace(const ssm_glr_dims_t &d) {
   const size_t chain = ssmb::glr_chain_bytes(d.batch, d.seqlen, d.dim);
-  return chain > 0 ? up256(256 + chain) : 0;
+  return chain > 0 ? up256(ssmb::kGlrSets * ssmb::kGlrCounterBytes + chain) : 0;
 }
 size_t glr_bwd_workspace(const ssm_glr_dims_t &d) {  // and the terms of dA
   return glr_workspace(d) + up256(static_cast<size_t>(ssmb::glr_bwd_parts(d.batch, d.seqlen)) * d.dim * 4);

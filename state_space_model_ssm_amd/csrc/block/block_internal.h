@@ -19,8 +19,8 @@ __device__ __forceinline__ void st(uint16_t *p, int64_t i, float v) {
   p[i] = __builtin_bit_cast(uint16_t, static_cast<__bf16>(v));  // round to nearest even
 }
 
-// What tiles of a recurrence tell each other, in the workspace: a counter (256
-// bytes kept for it), a summary (product, end) per (row, tile, channel), and
+// What tiles of a recurrence tell each other, in the workspace: counters (one
+// per set of channel blocks, 128 bytes apart), a summary (product, end) per (row, tile, channel), and
 // the state at the start of each group of tiles.  Nothing for one tile.
 struct GlrChain {
   unsigned *counter;
@@ -28,6 +28,13 @@ struct GlrChain {
   unsigned *starts;
   int64_t bytes;               // of sums and starts
 };
+constexpr unsigned kGlrSets = 32, kGlrCounterBytes = 128;
+// Sets of `rows` channel blocks: the most that share them evenly.
+__host__ __device__ inline unsigned glr_sets(unsigned rows) {
+  unsigned n = rows < kGlrSets ? rows : kGlrSets;
+  while (rows % n != 0) --n;
+  return n;
+}
 size_t glr_chain_bytes(int64_t batch, int64_t seqlen, int64_t dim);
 GlrChain glr_chain(void *workspace, int64_t batch, int64_t seqlen, int64_t dim);
 

@@ -113,23 +113,23 @@ constexpr int kGroup = 16;                // tiles between two published states
 constexpr unsigned kMissing = 0xffffffffu;  // a word not yet published
 constexpr int kMostPolls = 1 << 22;       // some seconds: a wait that long would be a fault, and ends in NaN
 
-// The workgroup's tile, from the counter (which needs no order if there is
-// one tile per sequence).
+// The workgroup's tile, from its set's counter (needed only if a sequence has
+// more than one tile).
 template <int C, bool REVERSE>
 __device__ __forceinline__ Place place(int64_t dim, int64_t seqlen, int64_t batch, const GlrChain &chain) {
   __shared__ unsigned number;
   unsigned id = blockIdx.x;
   const int tiles = static_cast<int>((seqlen + T * kSubs - 1) / (T * kSubs));
+  const unsigned ct = static_cast<unsigned>((dim + kLanes * C - 1) / (kLanes * C)), rows = static_cast<unsigned>(batch) * ct;
+  const unsigned sets = tiles > 1 ? glr_sets(rows) : 1, set = id % sets;
   if (tiles > 1) {
-    if (threadIdx.x == 0) number = atomicAdd(chain.counter, 1u);
+    if (threadIdx.x == 0) number = atomicAdd(chain.counter + set * (kGlrCounterBytes / 4), 1u);
     __syncthreads();
-    id = number;
+    id = __builtin_amdgcn_readfirstlane(number);
   }
   Place w;
-  const unsigned ct = static_cast<unsigned>((dim + kLanes * C - 1) / (kLanes * C)), rows = static_cast<unsigned>(batch) * ct;
-  id = __builtin_amdgcn_readfirstlane(id);
-  const unsigned rest = id % rows;
-  w.pos = static_cast<int>(id / rows);
+  const unsigned own = rows / sets, rest = set * own + id % own;  // rows of the set are adjacent
+  w.pos = static_cast<int>(id / own);
   w.tiles = tiles;
   w.k = REVERSE ? tiles - 1 - w.pos : w.pos;
   w.b = rest / ct;
@@ -328,11 +328,11 @@ __device__ __forceinline__ void join(Scratch &lds, const GlrChain &chain, const 
   }
 }
 
-// All words missing, and the counter at 0.
+// All words missing, and the counters at 0.
 __global__ void __launch_bounds__(256) glr_clear_kernel(uint4 *words, int64_t n, unsigned *counter) {
   const int64_t id = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   if (id < n) words[id] = make_uint4(kMissing, kMissing, kMissing, kMissing);
-  if (id == 0) *counter = 0;
+  if (id < kGlrSets) counter[id * (kGlrCounterBytes / 4)] = 0;
 }
 
 template <typename Tin, typename Tout, int C>
@@ -633,7 +633,7 @@ GlrChain glr_chain(void *at, int64_t batch, int64_t seqlen, int64_t dim) {
   if (c.bytes == 0) return c;
   char *base = static_cast<char *>(at);
   c.counter = reinterpret_cast<unsigned *>(base);
-  c.sums = reinterpret_cast<uint64_t *>(base + 256);
+  c.sums = reinterpret_cast<uint64_t *>(base + kGlrSets * kGlrCounterBytes);
   c.starts = reinterpret_cast<unsigned *>(c.sums + batch * ((seqlen + T * kSubs - 1) / (T * kSubs)) * dim);
   return c;
 }
