@@ -88,6 +88,7 @@ __global__ void __launch_bounds__(256, 2) swa_dq_kernel(const SwaParams p, int h
           s = mfma(row_operand<D>(kt, 32 * blk, ks, lane), q[ks], s);
           dp = mfma(row_operand<D>(vt, 32 * blk, ks, lane), dy[ks], dp);
         }
+        reads_ahead<2 * NS>();
 #pragma unroll
         for (int r = 0; r < 16; ++r)
           dp[r] = __builtin_amdgcn_exp2f(fmaf(s[r], c2, -lse2)) * (dp[r] - delta);
@@ -203,6 +204,7 @@ __global__ void __launch_bounds__(256, 2) swa_dkv_kernel(const SwaParams p, cons
           s = mfma(row_operand<D>(qt, 32 * blk, ks, lane), kf[ks], s);
           dp = mfma(row_operand<D>(dt, 32 * blk, ks, lane), vf[ks], dp);
         }
+        reads_ahead<2 * NS>();
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
           const float4 l4 = *reinterpret_cast<const float4 *>(lse2 + 32 * blk + 8 * g + 4 * half);

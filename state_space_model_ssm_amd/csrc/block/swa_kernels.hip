@@ -90,9 +90,10 @@ __device__ __forceinline__ bool attend(const SwaParams &p, const FwdWork &w, u4 
     const bool whole = k0 + kTile - 1 <= w.wq0 && w.wq0 + 31 - k0 < window;
     f16v s[2] = {};
 #pragma unroll
-    for (int blk = 0; blk < 2; ++blk)
+    for (int ks = 0; ks < NS; ++ks)
 #pragma unroll
-      for (int ks = 0; ks < NS; ++ks) s[blk] = mfma(row_operand<D>(kt, 32 * blk, ks, lane), q[ks], s[blk]);
+      for (int blk = 0; blk < 2; ++blk) s[blk] = mfma(row_operand<D>(kt, 32 * blk, ks, lane), q[ks], s[blk]);
+    reads_ahead<2 * NS>();
     auto sees = [&](int blk, int r) {
       const int j = k0 + 32 * blk + d_row(r, half);
       return static_cast<unsigned>(t - j) < static_cast<unsigned>(window) || j < own;

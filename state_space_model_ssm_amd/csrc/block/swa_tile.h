@@ -115,6 +115,21 @@ __device__ __forceinline__ void wait_tiles() {
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
 
+// Order of N matrix products and the N LDS reads of their A operands in this
+// block of code: six reads ahead of the products (left to itself the compiler
+// keeps one ahead, and each product waits for LDS).
+template <int N>
+__device__ __forceinline__ void reads_ahead() {
+  constexpr int kAhead = N < 12 ? N / 2 : 6;
+  __builtin_amdgcn_sched_group_barrier(0x100, kAhead, 0);
+#pragma unroll
+  for (int i = 0; i < (N - kAhead) / 2; ++i) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);
+    __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+  }
+  __builtin_amdgcn_sched_group_barrier(0x008, kAhead, 0);
+}
+
 // Every LDS read this wavefront has started has its value: the copies that
 // follow may overwrite what it read.
 __device__ __forceinline__ void wait_reads() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
