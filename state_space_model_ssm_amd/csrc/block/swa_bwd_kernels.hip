@@ -37,14 +37,12 @@ __global__ void __launch_bounds__(256, 2) swa_dq_kernel(const SwaParams p, int h
   f16v dq[NB] = {};
   if (q0 < len) {
     const int qlast = q0 + qspan - 1 < last ? q0 + qspan - 1 : last;
-    const int lo = q0 - window + 1 > 0 ? (q0 - window + 1) / kTile : 0;
-    const int seen = ((sinks < qlast + 1 ? sinks : qlast + 1) + kTile - 1) / kTile;
-    const int ns = seen < lo ? seen : lo, tiles = ns + qlast / kTile - lo + 1;
+    const KeyRow keys = key_row(q0, window, sinks);
+    const int tiles = (keys.first + qlast - keys.low) / kTile + 1;
     const uint16_t *kp = p.k + b * p.k_batch + c * D, *vp = p.v + b * p.v_batch + c * D;
     auto start = [&](int i) {
-      const int k0 = (i < ns ? i : lo + i - ns) * kTile;
-      load_tile<D, 256>(lds[i & 1][0], kp, p.k_token, k0, last, tid);
-      load_tile<D, 256>(lds[i & 1][1], vp, p.v_token, k0, last, tid);
+      load_keys<D, 256>(lds[i & 1][0], kp, p.k_token, keys, i * kTile, last, tid);
+      load_keys<D, 256>(lds[i & 1][1], vp, p.v_token, keys, i * kTile, last, tid);
     };
     bf8 q[NS], dy[NS];
     const int row = t < last ? t : last;
@@ -76,10 +74,10 @@ __global__ void __launch_bounds__(256, 2) swa_dq_kernel(const SwaParams p, int h
       wait_tiles();
       __syncthreads();  // tile i has landed, and nobody reads the other buffer any more
       if (i + 1 < tiles) start(i + 1);
-      const int k0 = (i < ns ? i : lo + i - ns) * kTile;
+      const int v0 = i * kTile, j0 = keys.key(v0), j1 = keys.key(v0 + kTile - 1);
       const u4 *kt = lds[i & 1][0], *vt = lds[i & 1][1];
-      if (k0 > wq0 + 31 || (k0 + kTile - 1 <= wq0 - window && k0 >= sinks) || wq0 >= len) continue;
-      const bool whole = k0 + kTile - 1 <= wq0 && wq0 + 31 - k0 < window;
+      if (j0 > wq0 + 31 || (j1 <= wq0 - window && j0 >= sinks) || wq0 >= len) continue;
+      const bool whole = j1 <= wq0 && wq0 + 31 - j0 < window;
 #pragma unroll
       for (int blk = 0; blk < 2; ++blk) {
         f16v s = {}, dp = {};
@@ -95,7 +93,7 @@ __global__ void __launch_bounds__(256, 2) swa_dq_kernel(const SwaParams p, int h
         if (!whole) {
 #pragma unroll
           for (int r = 0; r < 16; ++r) {
-            const int j = k0 + 32 * blk + d_row(r, half);
+            const int j = keys.key(v0 + 32 * blk + d_row(r, half));
             dp[r] = static_cast<unsigned>(t - j) < static_cast<unsigned>(window) || j < own ? dp[r] : 0.0f;
           }
         }

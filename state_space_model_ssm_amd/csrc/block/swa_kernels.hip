@@ -52,7 +52,8 @@ __device__ __forceinline__ void add_not_finite(const u4 *tile, const bf8 (&vis)[
 struct FwdWork {
   const uint16_t *k, *v;  // of the key head
   int wq0;                // first query of this wavefront
-  int len, lo, ns, tiles; // length; first window tile; sink tiles before it; tiles in all
+  KeyRow row;             // the keys its queries see
+  int len, tiles;
   float c2;               // |scale| log2(e)
 };
 
@@ -74,20 +75,19 @@ __device__ __forceinline__ bool attend(const SwaParams &p, const FwdWork &w, u4 
 #pragma unroll
   for (int db = 0; db < NB; ++db) o[db] = f16v{};
   auto start = [&](int i) {
-    const int k0 = (i < w.ns ? i : w.lo + i - w.ns) * kTile;
-    load_tile<D, 256>(lds[i & 1][0], w.k, p.k_token, k0, w.len - 1, tid);
-    load_tile<D, 256>(lds[i & 1][1], w.v, p.v_token, k0, w.len - 1, tid);
+    load_keys<D, 256>(lds[i & 1][0], w.k, p.k_token, w.row, i * kTile, w.len - 1, tid);
+    load_keys<D, 256>(lds[i & 1][1], w.v, p.v_token, w.row, i * kTile, w.len - 1, tid);
   };
   start(0);
   for (int i = 0; i < w.tiles; ++i) {
     wait_tiles();
     __syncthreads();  // tile i has landed, and nobody reads the other buffer any more
     if (i + 1 < w.tiles) start(i + 1);
-    const int k0 = (i < w.ns ? i : w.lo + i - w.ns) * kTile;
+    const int v0 = i * kTile, j0 = w.row.key(v0), j1 = w.row.key(v0 + kTile - 1);
     const u4 *kt = lds[i & 1][0], *vt = lds[i & 1][1];
     // Does this wavefront see any of the tile, or all of it?
-    if (k0 > w.wq0 + 31 || (k0 + kTile - 1 <= w.wq0 - window && k0 >= sinks) || w.wq0 >= w.len) continue;
-    const bool whole = k0 + kTile - 1 <= w.wq0 && w.wq0 + 31 - k0 < window;
+    if (j0 > w.wq0 + 31 || (j1 <= w.wq0 - window && j0 >= sinks) || w.wq0 >= w.len) continue;
+    const bool whole = j1 <= w.wq0 && w.wq0 + 31 - j0 < window;
     f16v s[2] = {};
 #pragma unroll
     for (int ks = 0; ks < NS; ++ks)
@@ -95,7 +95,7 @@ __device__ __forceinline__ bool attend(const SwaParams &p, const FwdWork &w, u4 
       for (int blk = 0; blk < 2; ++blk) s[blk] = mfma(row_operand<D>(kt, 32 * blk, ks, lane), q[ks], s[blk]);
     reads_ahead<2 * NS>();
     auto sees = [&](int blk, int r) {
-      const int j = k0 + 32 * blk + d_row(r, half);
+      const int j = w.row.key(v0 + 32 * blk + d_row(r, half));
       return static_cast<unsigned>(t - j) < static_cast<unsigned>(window) || j < own;
     };
     if (!whole) {
@@ -103,14 +103,7 @@ __device__ __forceinline__ bool attend(const SwaParams &p, const FwdWork &w, u4 
       for (int blk = 0; blk < 2; ++blk)
 #pragma unroll
         for (int r = 0; r < 16; ++r) s[blk][r] = sees(blk, r) ? s[blk][r] : -INFINITY;
-      if constexpr (SAFE) {
-        bf8 vis[4];
-#pragma unroll
-        for (int ks = 0; ks < 4; ++ks)
-#pragma unroll
-          for (int e = 0; e < 8; ++e) vis[ks][e] = static_cast<__bf16>(sees(ks / 2, (ks % 2) * 8 + e) ? 1.0f : 0.0f);
-        add_not_finite<D>(vt, vis, o, lane);
-      } else {
+      if constexpr (!SAFE) {
 #pragma unroll
         for (int k = 0; k < kTile * CH / 64; ++k) {
           const u4 v = vt[k * 64 + lane];
@@ -119,6 +112,16 @@ __device__ __forceinline__ bool attend(const SwaParams &p, const FwdWork &w, u4 
       }
     }
     to_weights(s, w.c2, o, top, sum);
+    if constexpr (SAFE) {
+      if (!whole) {
+          bf8 vis[4];
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) vis[ks][e] = static_cast<__bf16>(sees(ks / 2, (ks % 2) * 8 + e) ? 1.0f : 0.0f);
+          add_not_finite<D>(vt, vis, o, lane);
+      }
+    }
 #pragma unroll
     for (int ks = 0; ks < 4; ++ks) {
       const bf8 pk = as_operand(s[ks / 2], ks % 2);
@@ -163,13 +166,10 @@ __global__ void __launch_bounds__(256, 2) swa_fwd_kernel(const SwaParams p, int 
   float top = -INFINITY, sum = 0.0f;
   if (q0 < w.len) {
     const int last = w.len - 1, qlast = q0 + qspan - 1 < last ? q0 + qspan - 1 : last;
-    const int window = static_cast<int>(p.window), sinks = static_cast<int>(p.sinks);
     w.k = p.k + b * p.k_batch + c * D;
     w.v = p.v + b * p.v_batch + c * D;
-    w.lo = q0 - window + 1 > 0 ? (q0 - window + 1) / kTile : 0;
-    const int seen = ((sinks < qlast + 1 ? sinks : qlast + 1) + kTile - 1) / kTile;
-    w.ns = seen < w.lo ? seen : w.lo;
-    w.tiles = w.ns + qlast / kTile - w.lo + 1;
+    w.row = key_row(q0, static_cast<int>(p.window), static_cast<int>(p.sinks));
+    w.tiles = (w.row.first + qlast - w.row.low) / kTile + 1;
     bf8 q[NS];
     const int row = t < last ? t : last;
     const u4 *src = reinterpret_cast<const u4 *>(p.q + b * p.q_batch + row * p.q_token + head * D);

@@ -69,39 +69,76 @@ __device__ __forceinline__ bf8 as_operand(const f16v &d, int s) {
 // The row that register i of a D result stands for in lane half h.
 __device__ __forceinline__ constexpr int d_row(int i, int h) { return 8 * (i / 4) + 4 * h + i % 4; }
 
-// Start the copy of tile rows t0 .. t0 + 63 of a strided tensor (p: row 0 of
-// the head) into LDS, `NT` threads of the workgroup taking part; rows past
-// `last` are read as row `last`, so nothing past a length is touched.  The
-// copy goes from memory to LDS without registers: a wavefront's 64 pieces of
-// 16 bytes land in order from the address in M0, so the slots are permuted by
-// the source address.  In asm, because the compiler would wait for the copy
-// before any LDS read, of the other buffer too: wait_tiles() waits for it.
-// (M0 has no other use in these kernels.)
-template <int D, int NT>
+// Copy 16 bytes per lane from base + off to LDS, from `lds` on in lane order.
+// The copy goes from memory to LDS without registers.  In asm, because the
+// compiler would wait for it before any LDS read, of another buffer too:
+// wait_tiles() waits for it.  (M0 has no other use in these kernels.)
+__device__ __forceinline__ void copy16(unsigned lds, const void *base, unsigned off) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+               :
+               : "s"(lds), "v"(off), "s"(base)
+               : "memory");
+}
+__device__ __forceinline__ void copy16(unsigned lds, const void *at) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" : : "s"(lds), "v"(at) : "memory");
+}
+__device__ __forceinline__ unsigned lds_at(const void *p) {
+  return static_cast<unsigned>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const void *)(p)));
+}
+
+// Start the copy of tile rows t0 .. t0 + ROWS - 1 of a strided tensor (p: row
+// 0 of the head) into LDS, `NT` threads taking part; rows past `last` are read
+// as row `last`, so nothing past a length is touched.  A wavefront's 64 pieces
+// land in order, so the slots are permuted by the source address.
+template <int D, int NT, int ROWS = kTile>
 __device__ __forceinline__ void load_tile(u4 *tile, const uint16_t *p, int64_t token, int t0, int last, int tid) {
   constexpr int CH = D / 8;
   const uint16_t *base = p + t0 * token;
   const unsigned stride = static_cast<unsigned>(token) * 2;  // at most 2^25 bytes, so 63 rows fit 32 bits
-  const unsigned lds = __builtin_amdgcn_readfirstlane(
-      static_cast<unsigned>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) void *)(tile))) +
-      (tid & ~63) * 16);
+  const unsigned lds = __builtin_amdgcn_readfirstlane(lds_at(tile) + (tid & ~63) * 16);
 #pragma unroll
-  for (int k = 0; k < kTile * CH / NT; ++k) {
+  for (int k = 0; k < ROWS * CH / NT; ++k) {
     const int id = k * NT + tid, r = id / CH;
     const int c = slot<D>(r, id % CH) - r * CH;  // slot() is its own inverse within a row
-    const unsigned off = static_cast<unsigned>(r < last - t0 ? r : last - t0) * stride + c * 16;
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
-                 :
-                 : "s"(lds + k * NT * 16), "v"(off), "s"(base)
-                 : "memory");
+    copy16(lds + k * NT * 16, base, static_cast<unsigned>(r < last - t0 ? r : last - t0) * stride + c * 16);
+  }
+}
+
+// The keys that some queries see, in one row: the sinks before the window,
+// 0 .. first - 1, then the keys from `low` on.
+struct KeyRow {
+  int first, low;
+  __device__ __forceinline__ int key(int v) const { return v < first ? v : v - first + low; }
+};
+__device__ __forceinline__ KeyRow key_row(int q0, int window, int sinks) {
+  KeyRow k;
+  k.low = q0 - window + 1 > 0 ? q0 - window + 1 : 0;
+  k.first = sinks < k.low ? sinks : k.low;
+  return k;
+}
+
+// The same for the places v0 .. v0 + 63 of such a row.
+template <int D, int NT>
+__device__ __forceinline__ void load_keys(u4 *tile, const uint16_t *p, int64_t token, const KeyRow &row, int v0, int last,
+                                          int tid) {
+  if (v0 >= row.first) {
+    load_tile<D, NT>(tile, p, token, row.key(v0), last, tid);
+    return;
+  }
+  constexpr int CH = D / 8;
+  const unsigned lds = __builtin_amdgcn_readfirstlane(lds_at(tile) + (tid & ~63) * 16);
+#pragma unroll
+  for (int k = 0; k < kTile * CH / NT; ++k) {
+    const int id = k * NT + tid, r = id / CH, j = row.key(v0 + r);
+    const int c = slot<D>(r, id % CH) - r * CH;
+    copy16(lds + k * NT * 16, p + (j < last ? j : last) * token + c * 8);
   }
 }
 
 // The same for one float of each of the rows t0 .. t0 + 63, by one wavefront.
 __device__ __forceinline__ void load_stats(float *to, const float *p, int t0, int last, int lane) {
   const unsigned off = static_cast<unsigned>(lane < last - t0 ? lane : last - t0) * 4;
-  const unsigned lds = __builtin_amdgcn_readfirstlane(
-      static_cast<unsigned>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) void *)(to))));
+  const unsigned lds = __builtin_amdgcn_readfirstlane(lds_at(to));
   const float *base = p + t0;
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2"
                :
