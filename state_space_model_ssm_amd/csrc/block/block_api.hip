@@ -253,15 +253,19 @@ ssmb::SwaParams swa_params(const ssm_swa_dims_t &d, const void *q, const void *k
 }
 
 ssmb::SwaBwdPlan swa_plan(const ssm_swa_dims_t &d) {
-  return ssmb::swa_bwd_plan(d.batch, d.seqlen, d.nheads, d.nkv, d.window, d.sinks);
+  return ssmb::swa_bwd_plan(d.batch, d.seqlen, d.nheads, d.nkv, d.headdim, d.window, d.sinks);
 }
 
 // log2(e) lse and dy.y of every query, then the terms of dk and dv.
 size_t swa_bwd_stats(const ssm_swa_dims_t &d) { return up256(static_cast<size_t>(d.batch) * d.nheads * d.seqlen * 4); }
+size_t swa_bwd_terms(const ssm_swa_dims_t &d) {
+  const ssmb::SwaBwdPlan plan = swa_plan(d);
+  return up256(static_cast<size_t>(d.batch) * d.nkv * plan.sum_blocks * plan.slices * 2 * 128 * d.headdim * 4);
+}
 size_t swa_bwd_workspace(const ssm_swa_dims_t &d) {
   const ssmb::SwaBwdPlan plan = swa_plan(d);
-  const size_t part = plan.has_parts ? static_cast<size_t>(plan.items) * d.batch * d.nkv * 2 * 128 * d.headdim * 4 : 0;
-  return 2 * swa_bwd_stats(d) + part;
+  const size_t far = static_cast<size_t>(d.batch) * d.nkv * plan.far_blocks * plan.far_chunks * 2 * 32 * d.headdim * 4;
+  return 2 * swa_bwd_stats(d) + swa_bwd_terms(d) + up256(far);
 }
 
 int swa_splits(const ssm_swa_dims_t &d) { return ssmb::swa_step_splits(d.batch, d.nheads, d.nkv, d.sinks + d.window); }
@@ -532,6 +536,7 @@ int ssm_swa_bwd(const void *q, const void *k, const void *v, const int32_t *leng
   p.ws_lse2 = reinterpret_cast<float *>(ws);
   p.ws_delta = reinterpret_cast<float *>(ws + swa_bwd_stats(d));
   p.ws_part = reinterpret_cast<float *>(ws + 2 * swa_bwd_stats(d));
+  p.ws_far = reinterpret_cast<float *>(ws + 2 * swa_bwd_stats(d) + swa_bwd_terms(d));
   return launched(ssmb::launch_swa_bwd(p, swa_plan(d), static_cast<hipStream_t>(stream)), "swa_bwd");
 }
 

@@ -98,7 +98,7 @@ struct SwaParams {
   const uint16_t *dy;          // backward
   uint16_t *dq, *dk, *dv;
   float *ws_lse2, *ws_delta;   // (batch, nheads, seqlen): log2(e) lse and dy.y
-  float *ws_part;              // terms of dk and dv (see SwaBwdPlan)
+  float *ws_part, *ws_far;     // terms of dk and dv (see SwaBwdPlan)
   int64_t batch, seqlen, nheads, nkv, window, sinks;
   int64_t q_batch, q_token, k_batch, k_token, v_batch, v_token;
   float scale;
@@ -106,18 +106,20 @@ struct SwaParams {
 };
 hipError_t launch_swa_fwd(const SwaParams &p, hipStream_t stream);
 
-// How the work of dk and dv is shared out: per (batch row, key head), blocks
-// of 128 keys.  The first sink_blocks of them are seen by queries to the end
-// and have `chunks` workgroups, of chunk_tiles 64-query tiles each; the group's
-// heads are shared by `slices` workgroups.  Where a block has more than one
-// workgroup, each writes its terms, 2 x 128 x headdim floats per item, and
-// another launch adds them in their order.
+// How the work of dk and dv is shared out, per (batch row, key head).  A
+// workgroup has a block of 128 keys, over the queries that see them through
+// the window; the group's heads are shared by `slices` workgroups.  Sinks are
+// also seen by all queries after those: where there are any, each of the first
+// far_blocks blocks of 32 keys has far_chunks more workgroups, whose wavefronts
+// take queries in turn.  The first sum_blocks blocks of 128 have more than one
+// workgroup: each writes its terms, (2, 128, headdim) or (2, 32, headdim)
+// floats, and another launch adds them in their order.
 struct SwaBwdPlan {
-  unsigned blocks, sink_blocks, chunks, chunk_tiles, slices;
+  unsigned blocks, slices, far_blocks, far_chunks, sum_blocks;
   int64_t items;               // workgroups per (batch row, key head)
-  bool has_parts;
 };
-SwaBwdPlan swa_bwd_plan(int64_t batch, int64_t seqlen, int64_t nheads, int64_t nkv, int64_t window, int64_t sinks);
+SwaBwdPlan swa_bwd_plan(int64_t batch, int64_t seqlen, int64_t nheads, int64_t nkv, int64_t headdim, int64_t window,
+                        int64_t sinks);
 hipError_t launch_swa_bwd(const SwaParams &p, const SwaBwdPlan &plan, hipStream_t stream);
 
 struct SwaStepParams {

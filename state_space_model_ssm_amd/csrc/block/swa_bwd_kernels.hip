@@ -46,9 +46,9 @@ __global__ void __launch_bounds__(256, 2) swa_dq_kernel(const SwaParams p, int h
     };
     bf8 q[NS], dy[NS];
     const int row = t < last ? t : last;
-    const int64_t at = ((b * p.seqlen + row) * p.nheads + head) * D;
+    const int64_t from = ((b * p.seqlen + row) * p.nheads + head) * D;
     const u4 *qs = reinterpret_cast<const u4 *>(p.q + b * p.q_batch + row * p.q_token + head * D);
-    const u4 *ds = reinterpret_cast<const u4 *>(p.dy + at), *ys = reinterpret_cast<const u4 *>(p.y + at);
+    const u4 *ds = reinterpret_cast<const u4 *>(p.dy + from), *ys = reinterpret_cast<const u4 *>(p.y + from);
     float delta = 0.0f;
 #pragma unroll
     for (int s = 0; s < NS; ++s) {
@@ -69,6 +69,7 @@ __global__ void __launch_bounds__(256, 2) swa_dq_kernel(const SwaParams p, int h
       p.ws_delta[stat] = delta;
     }
     const int own = sinks < t + 1 ? sinks : t + 1;
+    const Lanes at = lanes_of<D>(lane);
     start(0);
     for (int i = 0; i < tiles; ++i) {
       wait_tiles();
@@ -83,8 +84,8 @@ __global__ void __launch_bounds__(256, 2) swa_dq_kernel(const SwaParams p, int h
         f16v s = {}, dp = {};
 #pragma unroll
         for (int ks = 0; ks < NS; ++ks) {
-          s = mfma(row_operand<D>(kt, 32 * blk, ks, lane), q[ks], s);
-          dp = mfma(row_operand<D>(vt, 32 * blk, ks, lane), dy[ks], dp);
+          s = mfma(row_operand<D>(kt, 32 * blk, ks, at), q[ks], s);
+          dp = mfma(row_operand<D>(vt, 32 * blk, ks, at), dy[ks], dp);
         }
         reads_ahead<2 * NS>();
 #pragma unroll
@@ -101,7 +102,7 @@ __global__ void __launch_bounds__(256, 2) swa_dq_kernel(const SwaParams p, int h
         for (int ks = 0; ks < 2; ++ks) {
           const bf8 dsk = as_operand(dp, ks);
 #pragma unroll
-          for (int db = 0; db < NB; ++db) dq[db] = mfma(col_operand<D>(kt, 32 * blk + 16 * ks, db, lane), dsk, dq[db]);
+          for (int db = 0; db < NB; ++db) dq[db] = mfma(col_operand<D>(kt, 32 * blk + 16 * ks, db, at), dsk, dq[db]);
         }
       }
     }
@@ -118,56 +119,165 @@ __global__ void __launch_bounds__(256, 2) swa_dq_kernel(const SwaParams p, int h
     }
 }
 
-// dk and dv of 128 keys, 32 per wavefront, over a range of query tiles and
-// heads (see SwaBwdPlan).
+// The gradients that 32 queries (rows base .. base + 31 of the tiles qt and dt,
+// with their stats) give the 32 keys of a wavefront, lane % 32 its key.  WHOLE:
+// every query sees every key; else sees(row) tells.
+template <int D, typename F>
+__device__ __forceinline__ void add_queries(const u4 *qt, const u4 *dt, const float *lse2, const float *delta, int base,
+                                            const bf8 (&kf)[D / 16], const bf8 (&vf)[D / 16], float c2, bool whole, F sees,
+                                            f16v (&dk)[D / 32], f16v (&dv)[D / 32], const Lanes &at, int half) {
+  constexpr int NB = D / 32, NS = D / 16;
+  f16v s = {}, dp = {};
+#pragma unroll
+  for (int ks = 0; ks < NS; ++ks) {
+    s = mfma(row_operand<D>(qt, base, ks, at), kf[ks], s);
+    dp = mfma(row_operand<D>(dt, base, ks, at), vf[ks], dp);
+  }
+  reads_ahead<2 * NS>();
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    const float4 l4 = *reinterpret_cast<const float4 *>(lse2 + base + 8 * g + 4 * half);
+    const float4 d4 = *reinterpret_cast<const float4 *>(delta + base + 8 * g + 4 * half);
+    const float l[4] = {l4.x, l4.y, l4.z, l4.w}, d[4] = {d4.x, d4.y, d4.z, d4.w};
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      s[4 * g + r] = __builtin_amdgcn_exp2f(fmaf(s[4 * g + r], c2, -l[r]));
+      dp[4 * g + r] = s[4 * g + r] * (dp[4 * g + r] - d[r]);
+    }
+  }
+  if (!whole) {
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      const bool yes = sees(d_row(r, half));
+      s[r] = yes ? s[r] : 0.0f;
+      dp[r] = yes ? dp[r] : 0.0f;
+    }
+  }
+#pragma unroll
+  for (int ks = 0; ks < 2; ++ks) {
+    const bf8 pk = as_operand(s, ks), dsk = as_operand(dp, ks);
+#pragma unroll
+    for (int db = 0; db < NB; ++db) {
+      dv[db] = mfma(col_operand<D>(dt, base + 16 * ks, db, at), pk, dv[db]);
+      dk[db] = mfma(col_operand<D>(qt, base + 16 * ks, db, at), dsk, dk[db]);
+    }
+  }
+}
+
+// The keys and values of a wavefront as B operands.
 template <int D>
-__global__ void __launch_bounds__(256, 2) swa_dkv_kernel(const SwaParams p, const SwaBwdPlan plan, unsigned n) {
+__device__ __forceinline__ void load_keys_and_values(const SwaParams &p, int64_t b, int64_t c, int row, int half,
+                                                     bf8 (&kf)[D / 16], bf8 (&vf)[D / 16]) {
+  const u4 *ks = reinterpret_cast<const u4 *>(p.k + b * p.k_batch + row * p.k_token + c * D);
+  const u4 *vs = reinterpret_cast<const u4 *>(p.v + b * p.v_batch + row * p.v_token + c * D);
+#pragma unroll
+  for (int s = 0; s < D / 16; ++s) {
+    kf[s] = __builtin_bit_cast(bf8, ks[2 * s + half]);
+    vf[s] = __builtin_bit_cast(bf8, vs[2 * s + half]);
+  }
+}
+
+// A D result, elements of 32 keys, as rows of D floats.
+template <int D>
+__device__ __forceinline__ void put_rows(float *to, int row, int half, const f16v (&v)[D / 32]) {
+#pragma unroll
+  for (int db = 0; db < D / 32; ++db)
+#pragma unroll
+    for (int g = 0; g < 4; ++g)
+      *reinterpret_cast<float4 *>(to + row * D + 32 * db + 8 * g + 4 * half) =
+          make_float4(v[db][4 * g], v[db][4 * g + 1], v[db][4 * g + 2], v[db][4 * g + 3]);
+}
+
+__device__ __forceinline__ void add(float4 &a, const float4 &x) {
+  a.x += x.x;
+  a.y += x.y;
+  a.z += x.z;
+  a.w += x.w;
+}
+
+// The first query tile past those that see a block of 128 keys through the window.
+__device__ __forceinline__ int far_tile(int b0, int window, int len) {
+  const int reach = len - b0 <= window + 127 ? len : b0 + 127 + window;
+  return (reach + kTile - 1) / kTile;
+}
+
+// dk and dv of 128 keys, 32 per wavefront, over the queries that see them
+// through the window, or of the sinks among 32 keys over the queries past it
+// (see SwaBwdPlan).  Two workgroups per CU with headdim 64; with 128 the sums
+// and operands need more than half the registers, and one per CU that has them
+// all took 567 us against 673 for two that spill (2 x 4096 tokens, 32 heads on
+// 8, window 1024).
+template <int D>
+__global__ void __launch_bounds__(256, D == 64 ? 2 : 1) swa_dkv_kernel(const SwaParams p, const SwaBwdPlan plan, unsigned n) {
   constexpr int CH = D / 8, NB = D / 32, NS = D / 16;
   __shared__ __align__(16) u4 lds[2][2][kTile * CH];  // buffer, Q or dy
-  __shared__ __align__(16) float stats[2][2][kTile];  // buffer, log2(e) lse or dy.y
+  __shared__ __align__(16) float stats[4][2][kTile];  // buffer or wavefront, log2(e) lse or dy.y
   const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const unsigned nkv = static_cast<unsigned>(p.nkv), group = static_cast<unsigned>(p.nheads) / nkv;
-  const unsigned item = xcd_order(blockIdx.x, n);
-  // Items of a (batch row, key head): sink blocks x chunks x slices, then the other blocks x slices.
-  const unsigned per = plan.sink_blocks * plan.chunks * plan.slices + (plan.blocks - plan.sink_blocks) * plan.slices;
-  const unsigned bc = item / per, k = item % per, slice = k % plan.slices, kb = k / plan.slices;
-  const bool sink = kb < plan.sink_blocks * plan.chunks;
-  const unsigned block = sink ? kb / plan.chunks : kb - plan.sink_blocks * plan.chunks + plan.sink_blocks;
-  const unsigned chunk = sink ? kb % plan.chunks : 0;
+  // The far items come last, where they fill what the others leave.
+  const unsigned far_items = plan.far_blocks * plan.far_chunks, near_items = plan.blocks * plan.slices;
+  const unsigned nnear = n / (far_items + near_items) * near_items;
+  const bool far = blockIdx.x >= nnear;
+  const unsigned item = far ? xcd_order(blockIdx.x - nnear, n - nnear) : xcd_order(blockIdx.x, nnear);
+  const unsigned per = far ? far_items : near_items, bc = item / per, k = item % per;
   const int64_t b = bc / nkv, c = bc % nkv;
-  const int heads = group / plan.slices, head0 = static_cast<int>(c * group + slice * heads);
   const int len = row_length(p, b), last = len - 1, L = static_cast<int>(p.seqlen);
   const int window = static_cast<int>(p.window), sinks = static_cast<int>(p.sinks);
-  const int b0 = static_cast<int>(block) * 128, wk0 = b0 + 32 * wave, j = wk0 + (lane & 31);  // j: this lane's key
   const float c2 = p.scale * kLog2e;
-
-  // Query tiles: from the block's own to the last that sees one of its keys.
-  int t_lo = b0 / kTile, t_hi = 0;
-  if (b0 < len) {
-    const int reach = b0 < sinks || len - b0 <= window + 127 ? len : b0 + 127 + window;  // past the last query
-    t_hi = (reach + kTile - 1) / kTile;
-    if (sink) {
-      t_lo += static_cast<int>(chunk * plan.chunk_tiles);
-      const int end = t_lo + static_cast<int>(plan.chunk_tiles);
-      t_hi = t_hi < end ? t_hi : end;
-    }
-  }
-  const int nq = t_hi > t_lo ? t_hi - t_lo : 0, steps = nq * heads;
-
+  const Lanes at = lanes_of<D>(lane);
   f16v dk[NB] = {}, dv[NB] = {};
-  if (steps > 0) {
-    bf8 kf[NS], vf[NS];
-    {
-      const int row = j < last ? j : last;
-      const u4 *ks = reinterpret_cast<const u4 *>(p.k + b * p.k_batch + row * p.k_token + c * D);
-      const u4 *vs = reinterpret_cast<const u4 *>(p.v + b * p.v_batch + row * p.v_token + c * D);
+  bf8 kf[NS], vf[NS];
+
+  if (far) {
+    // Each wavefront walks (query tile of 32, head) pairs of its own, in LDS of its own.
+    const unsigned fb = k / plan.far_chunks, chunk = k % plan.far_chunks;
+    const int j0 = static_cast<int>(fb) * 32, j = j0 + (lane & 31);
+    const int first = 2 * far_tile(j0 / 128 * 128, window, len), tiles = (len + 31) / 32 - first;
+    const int units = tiles > 0 ? tiles * static_cast<int>(group) : 0, step = 4 * static_cast<int>(plan.far_chunks);
+    u4 *qt = &lds[0][0][0] + wave * (2 * 32 * CH), *dt = qt + 32 * CH;
+    if (units > 0) load_keys_and_values<D>(p, b, c, j < last ? j : last, half, kf, vf);
+    auto start = [&](int u) {
+      const int t0 = (first + u % tiles) * 32, head = static_cast<int>(c * group) + u / tiles;
+      load_tile<D, 64, 32>(qt, p.q + b * p.q_batch + head * D, p.q_token, t0, last, lane);
+      load_tile<D, 64, 32>(dt, p.dy + (b * p.seqlen * p.nheads + head) * D, p.nheads * D, t0, last, lane);
+      load_stats(stats[wave][0], p.ws_lse2 + (b * p.nheads + head) * p.seqlen, t0, last, lane);
+      load_stats(stats[wave][1], p.ws_delta + (b * p.nheads + head) * p.seqlen, t0, last, lane);
+    };
+    for (int u = static_cast<int>(chunk) * 4 + wave; u < units; u += step) {
+      start(u);
+      wait_tiles();
+      const int t0 = (first + u % tiles) * 32;
+      add_queries<D>(qt, dt, stats[wave][0], stats[wave][1], 0, kf, vf, c2, t0 + 31 < len && j0 + 31 < sinks,
+                     [&](int r) { return t0 + r < len && j < sinks; }, dk, dv, at, half);
+      wait_reads();
+    }
+    // Add the wavefronts' terms, dk then dv, in LDS.
+    float *sums = reinterpret_cast<float *>(lds), *out = p.ws_far + (static_cast<int64_t>(bc) * far_items + k) * 2 * 32 * D;
+    for (int which = 0; which < 2; ++which) {
+      __syncthreads();
+      put_rows<D>(sums + wave * 32 * D, lane & 31, half, which == 0 ? dk : dv);
+      __syncthreads();
+      for (int i = tid * 4; i < 32 * D; i += 1024) {
+        float4 a = *reinterpret_cast<const float4 *>(sums + i);
 #pragma unroll
-      for (int s = 0; s < NS; ++s) {
-        kf[s] = __builtin_bit_cast(bf8, ks[2 * s + half]);
-        vf[s] = __builtin_bit_cast(bf8, vs[2 * s + half]);
+        for (int w = 1; w < 4; ++w) add(a, *reinterpret_cast<const float4 *>(sums + w * 32 * D + i));
+        *reinterpret_cast<float4 *>(out + which * 32 * D + i) = a;
       }
     }
+    return;
+  }
+
+  const unsigned slice = k % plan.slices, block = k / plan.slices;
+  const int heads = group / plan.slices, head0 = static_cast<int>(c * group + slice * heads);
+  const int b0 = static_cast<int>(block) * 128, wk0 = b0 + 32 * wave, j = wk0 + (lane & 31);  // j: this lane's key
+  // Query tiles: from the block's own to the last that sees one of its keys
+  // (of the sinks, without far items: to the end).
+  const int t_lo = b0 / kTile;
+  const int t_hi = b0 >= len ? 0 : b0 < sinks && far_items == 0 ? (len + kTile - 1) / kTile : far_tile(b0, window, len);
+  const int nq = t_hi > t_lo ? t_hi - t_lo : 0, steps = nq * heads;
+  if (steps > 0) {
+    load_keys_and_values<D>(p, b, c, j < last ? j : last, half, kf, vf);
     int at_head = head0, at_tile = t_lo;  // of the next tile to start
     auto start = [&](int i) {
       const int t0 = at_tile * kTile, buf = i & 1;
@@ -188,66 +298,25 @@ __global__ void __launch_bounds__(256, 2) swa_dkv_kernel(const SwaParams p, cons
       if (i + 1 < steps) start(i + 1);
       const int t0 = tile * kTile;
       if (++tile == t_hi) tile = t_lo;
-      const u4 *qt = lds[i & 1][0], *dt = lds[i & 1][1];
-      const float *lse2 = stats[i & 1][0], *delta = stats[i & 1][1];
 #pragma unroll
       for (int blk = 0; blk < 2; ++blk) {
         const int q0 = t0 + 32 * blk;
         // Does any of these 32 queries see any of the wavefront's keys, or all of them all?
         if (q0 + 31 < wk0 || (q0 >= wk0 + 31 + window && wk0 >= sinks) || q0 >= len || wk0 >= len) continue;
         const bool whole = q0 >= wk0 + 31 && q0 + 31 < len && (q0 + 31 - wk0 < window || wk0 + 31 < sinks);
-        f16v s = {}, dp = {};
-#pragma unroll
-        for (int ks = 0; ks < NS; ++ks) {
-          s = mfma(row_operand<D>(qt, 32 * blk, ks, lane), kf[ks], s);
-          dp = mfma(row_operand<D>(dt, 32 * blk, ks, lane), vf[ks], dp);
-        }
-        reads_ahead<2 * NS>();
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const float4 l4 = *reinterpret_cast<const float4 *>(lse2 + 32 * blk + 8 * g + 4 * half);
-          const float4 d4 = *reinterpret_cast<const float4 *>(delta + 32 * blk + 8 * g + 4 * half);
-          const float l[4] = {l4.x, l4.y, l4.z, l4.w}, d[4] = {d4.x, d4.y, d4.z, d4.w};
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            s[4 * g + r] = __builtin_amdgcn_exp2f(fmaf(s[4 * g + r], c2, -l[r]));
-            dp[4 * g + r] = s[4 * g + r] * (dp[4 * g + r] - d[r]);
-          }
-        }
-        if (!whole) {
-#pragma unroll
-          for (int r = 0; r < 16; ++r) {
-            const int t = q0 + d_row(r, half);
-            const bool sees = t < len && (static_cast<unsigned>(t - j) < static_cast<unsigned>(window) || (j < sinks && j <= t));
-            s[r] = sees ? s[r] : 0.0f;
-            dp[r] = sees ? dp[r] : 0.0f;
-          }
-        }
-#pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
-          const bf8 pk = as_operand(s, ks), dsk = as_operand(dp, ks);
-#pragma unroll
-          for (int db = 0; db < NB; ++db) {
-            dv[db] = mfma(col_operand<D>(dt, 32 * blk + 16 * ks, db, lane), pk, dv[db]);
-            dk[db] = mfma(col_operand<D>(qt, 32 * blk + 16 * ks, db, lane), dsk, dk[db]);
-          }
-        }
+        add_queries<D>(lds[i & 1][0], lds[i & 1][1], stats[i & 1][0], stats[i & 1][1], 32 * blk, kf, vf, c2, whole,
+                       [&](int r) {
+                         const int t = q0 + r;
+                         return t < len && (static_cast<unsigned>(t - j) < static_cast<unsigned>(window) || (j < sinks && j <= t));
+                       },
+                       dk, dv, at, half);
       }
     }
   }
-  if (sink || plan.slices > 1) {
-    // Terms of a sum over parts: [item][dk or dv][key][D] float32.
-    float *part = p.ws_part + static_cast<int64_t>(item) * 2 * 128 * D + (32 * wave + (lane & 31)) * D;
-#pragma unroll
-    for (int db = 0; db < NB; ++db)
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const int e = 32 * db + 8 * g + 4 * half;
-        *reinterpret_cast<float4 *>(part + e) =
-            make_float4(dk[db][4 * g], dk[db][4 * g + 1], dk[db][4 * g + 2], dk[db][4 * g + 3]);
-        *reinterpret_cast<float4 *>(part + 128 * D + e) =
-            make_float4(dv[db][4 * g], dv[db][4 * g + 1], dv[db][4 * g + 2], dv[db][4 * g + 3]);
-      }
+  if (block < plan.sum_blocks) {
+    const int64_t part = (static_cast<int64_t>(bc) * plan.sum_blocks + block) * plan.slices + slice;
+    put_rows<D>(p.ws_part + part * 2 * 128 * D, 32 * wave + (lane & 31), half, dk);
+    put_rows<D>(p.ws_part + (part * 2 + 1) * 128 * D, 32 * wave + (lane & 31), half, dv);
     return;
   }
   if (j >= L) return;
@@ -267,38 +336,40 @@ __global__ void __launch_bounds__(256, 2) swa_dkv_kernel(const SwaParams p, cons
     }
 }
 
-// Sum the parts of the blocks that have them, in their order; one workgroup
-// per (batch row, key head, block), a thread for 4 elements of a key.
+// Sum the terms of the blocks that have them, in their order: a thread for 4
+// elements of a key, a workgroup for 1024 of the elements of a (batch row, key
+// head) block of 32 keys.
 template <int D>
-__global__ void __launch_bounds__(256) swa_parts_kernel(const SwaParams p, const SwaBwdPlan plan, unsigned nsum) {
-  const unsigned bc = blockIdx.x / nsum, block = blockIdx.x % nsum, nkv = static_cast<unsigned>(p.nkv);
-  const unsigned per = plan.sink_blocks * plan.chunks * plan.slices + (plan.blocks - plan.sink_blocks) * plan.slices;
-  const bool sink = block < plan.sink_blocks;
-  const unsigned parts = plan.slices * (sink ? plan.chunks : 1);
-  const int64_t first = static_cast<int64_t>(bc) * per +
-                        (sink ? block * parts
-                              : plan.sink_blocks * plan.chunks * plan.slices + (block - plan.sink_blocks) * plan.slices);
+__global__ void __launch_bounds__(256) swa_parts_kernel(const SwaParams p, const SwaBwdPlan plan) {
+  const unsigned nkv = static_cast<unsigned>(p.nkv), per = plan.sum_blocks * 4;
+  const int i = static_cast<int>(blockIdx.x % (D / 32)) * 256 + threadIdx.x;
+  const unsigned id = blockIdx.x / (D / 32), bc = id / per, b32 = id % per, block = b32 / 4;
   const int64_t b = bc / nkv, c = bc % nkv;
-  const int len = row_length(p, b), L = static_cast<int>(p.seqlen);
-  for (int i = threadIdx.x; i < 128 * D / 4; i += 256) {
-    const int j = static_cast<int>(block) * 128 + i / (D / 4);
-    if (j >= L) break;
-    float4 a = make_float4(0, 0, 0, 0), v = a;
-    const float4 *part = reinterpret_cast<const float4 *>(p.ws_part + first * 2 * 128 * D) + i;
-    for (unsigned k = 0; k < parts; ++k) {
-      const float4 x = part[k * (128 * D / 2)], y = part[k * (128 * D / 2) + 128 * D / 4];
-      a.x += x.x; a.y += x.y; a.z += x.z; a.w += x.w;
-      v.x += y.x; v.y += y.y; v.z += y.z; v.w += y.w;
-    }
-    const float keep = j < len ? 1.0f : 0.0f, ka = keep * p.scale;
-    const int64_t out = ((b * p.seqlen + j) * p.nkv + c) * D + i % (D / 4) * 4;
-    const bf4 oa = {static_cast<__bf16>(a.x * ka), static_cast<__bf16>(a.y * ka), static_cast<__bf16>(a.z * ka),
-                    static_cast<__bf16>(a.w * ka)};
-    const bf4 ov = {static_cast<__bf16>(v.x * keep), static_cast<__bf16>(v.y * keep), static_cast<__bf16>(v.z * keep),
-                    static_cast<__bf16>(v.w * keep)};
-    *reinterpret_cast<bf4 *>(p.dk + out) = oa;
-    *reinterpret_cast<bf4 *>(p.dv + out) = ov;
+  const int len = row_length(p, b), L = static_cast<int>(p.seqlen), j = static_cast<int>(b32) * 32 + i / (D / 4);
+  if (j >= L) return;
+  const float4 *main = reinterpret_cast<const float4 *>(
+      p.ws_part + (static_cast<int64_t>(bc) * plan.sum_blocks + block) * plan.slices * 2 * 128 * D + (b32 % 4) * 32 * D) + i;
+  const unsigned nfar = b32 < plan.far_blocks ? plan.far_chunks : 0;
+  const float4 *far = reinterpret_cast<const float4 *>(
+      p.ws_far + (static_cast<int64_t>(bc) * plan.far_blocks + b32) * plan.far_chunks * 2 * 32 * D) + i;
+  float4 a = make_float4(0, 0, 0, 0), v = a;
+  for (unsigned k = 0; k < plan.slices; ++k) {
+    add(a, main[k * (2 * 128 * D / 4)]);
+    add(v, main[k * (2 * 128 * D / 4) + 128 * D / 4]);
   }
+#pragma unroll 4
+  for (unsigned k = 0; k < nfar; ++k) {
+    add(a, far[k * (2 * 32 * D / 4)]);
+    add(v, far[k * (2 * 32 * D / 4) + 32 * D / 4]);
+  }
+  const float keep = j < len ? 1.0f : 0.0f, ka = keep * p.scale;
+  const int64_t out = ((b * p.seqlen + j) * p.nkv + c) * D + i % (D / 4) * 4;
+  const bf4 oa = {static_cast<__bf16>(a.x * ka), static_cast<__bf16>(a.y * ka), static_cast<__bf16>(a.z * ka),
+                  static_cast<__bf16>(a.w * ka)};
+  const bf4 ov = {static_cast<__bf16>(v.x * keep), static_cast<__bf16>(v.y * keep), static_cast<__bf16>(v.z * keep),
+                  static_cast<__bf16>(v.w * keep)};
+  *reinterpret_cast<bf4 *>(p.dk + out) = oa;
+  *reinterpret_cast<bf4 *>(p.dv + out) = ov;
 }
 
 template <int D>
@@ -312,43 +383,39 @@ hipError_t launch_d(const SwaParams &p, const SwaBwdPlan &plan, hipStream_t s) {
                      static_cast<unsigned>(qtiles), static_cast<unsigned>(n));
   hipLaunchKernelGGL((swa_dkv_kernel<D>), dim3(static_cast<uint32_t>(items)), dim3(256), 0, s, p, plan,
                      static_cast<unsigned>(items));
-  const unsigned nsum = plan.slices > 1 ? plan.blocks : plan.sink_blocks;
-  if (nsum > 0)
-    hipLaunchKernelGGL((swa_parts_kernel<D>), dim3(static_cast<uint32_t>(nsum * p.batch * p.nkv)), dim3(256), 0, s, p, plan,
-                       nsum);
+  if (plan.sum_blocks > 0)
+    hipLaunchKernelGGL((swa_parts_kernel<D>), dim3(static_cast<uint32_t>(plan.sum_blocks * 4 * (D / 32) * p.batch * p.nkv)), dim3(256), 0, s,
+                       p, plan);
   return hipGetLastError();
 }
 
 }  // namespace
 
-SwaBwdPlan swa_bwd_plan(int64_t batch, int64_t seqlen, int64_t nheads, int64_t nkv, int64_t window, int64_t sinks) {
+SwaBwdPlan swa_bwd_plan(int64_t batch, int64_t seqlen, int64_t nheads, int64_t nkv, int64_t headdim, int64_t window,
+                        int64_t sinks) {
   SwaBwdPlan plan{};
-  const int64_t blocks = (seqlen + 127) / 128;
+  const int64_t blocks = (seqlen + 127) / 128, group = nheads / nkv;
   window = window < seqlen ? window : seqlen;
   sinks = sinks < seqlen ? sinks : seqlen;
   plan.blocks = static_cast<unsigned>(blocks);
-  plan.chunks = 1;
-  plan.slices = 1;
-  const int64_t regular = (window + 127) / kTile + 1;  // query tiles that see a block through the window
-  int64_t chunk = regular < 16 ? 16 : regular;
-  const int64_t all = (seqlen + kTile - 1) / kTile;
-  // Blocks that hold sinks are seen to the sequence's end: their queries are
-  // cut into chunks of about an ordinary block's work.
-  if (sinks > 0 && all > chunk) {
-    plan.sink_blocks = static_cast<unsigned>((sinks + 127) / 128);
-    plan.chunks = static_cast<unsigned>((all + chunk - 1) / chunk);
-  }
-  plan.chunk_tiles = static_cast<unsigned>(chunk);
   // Too few workgroups for the 256 CUs: the heads of a group are shared out.
-  const int64_t group = nheads / nkv;
+  const int64_t want = headdim == 64 ? 512 : 256;
   int64_t slices = 1;
-  while (slices < group && batch * nkv * blocks * slices < 512) {
+  while (slices < group && batch * nkv * blocks * slices < want) {
     do ++slices;
     while (group % slices != 0);
   }
   plan.slices = static_cast<unsigned>(slices);
-  plan.items = (static_cast<int64_t>(plan.sink_blocks) * plan.chunks + blocks - plan.sink_blocks) * slices;
-  plan.has_parts = plan.sink_blocks > 0 || slices > 1;
+  // Far items, where queries lie past the first block's window: about six
+  // (32 queries, head) pairs per wavefront.
+  const int64_t pairs = ((seqlen + 31) / 32 - 2 * ((window + 127 + kTile - 1) / kTile)) * group;
+  if (sinks > 0 && pairs > 0) {
+    plan.far_blocks = static_cast<unsigned>((sinks + 31) / 32);
+    plan.far_chunks = static_cast<unsigned>((pairs + 23) / 24);
+  }
+  const int64_t sink_blocks = plan.far_blocks > 0 ? (sinks + 127) / 128 : 0;
+  plan.sum_blocks = static_cast<unsigned>(slices > 1 ? blocks : sink_blocks);
+  plan.items = static_cast<int64_t>(plan.far_blocks) * plan.far_chunks + blocks * slices;
   return plan;
 }
 

@@ -23,7 +23,7 @@ __device__ __forceinline__ unsigned not_finite(unsigned x) { return (x & 0x7fff7
 // What the infinities and NaN of a tile of values add to the queries that see
 // them, out[db] += vis * v over those elements alone.  vis: 1 or 0 per key.
 template <int D>
-__device__ __forceinline__ void add_not_finite(const u4 *tile, const bf8 (&vis)[4], f16v (&out)[D / 32], int lane) {
+__device__ __forceinline__ void add_not_finite(const u4 *tile, const bf8 (&vis)[4], f16v (&out)[D / 32], const Lanes &at) {
 #pragma unroll
   for (int db = 0; db < D / 32; ++db) {
 #pragma unroll
@@ -31,7 +31,7 @@ __device__ __forceinline__ void add_not_finite(const u4 *tile, const bf8 (&vis)[
       f16v count = {};
 #pragma unroll
       for (int s = 0; s < 4; ++s) {
-        u4 v = __builtin_bit_cast(u4, col_operand<D>(tile, 16 * s, db, lane));
+        u4 v = __builtin_bit_cast(u4, col_operand<D>(tile, 16 * s, db, at));
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           auto is = [&](unsigned b) {
@@ -69,6 +69,7 @@ __device__ __forceinline__ bool attend(const SwaParams &p, const FwdWork &w, u4 
   const int lane = tid & 63, half = lane >> 5, t = w.wq0 + (lane & 31);
   const int window = static_cast<int>(p.window), sinks = static_cast<int>(p.sinks);
   const int own = sinks < t + 1 ? sinks : t + 1;  // sinks this query sees
+  const Lanes at = lanes_of<D>(lane);
   unsigned bad = 0;
   top = -INFINITY;
   sum = 0.0f;
@@ -92,7 +93,7 @@ __device__ __forceinline__ bool attend(const SwaParams &p, const FwdWork &w, u4 
 #pragma unroll
     for (int ks = 0; ks < NS; ++ks)
 #pragma unroll
-      for (int blk = 0; blk < 2; ++blk) s[blk] = mfma(row_operand<D>(kt, 32 * blk, ks, lane), q[ks], s[blk]);
+      for (int blk = 0; blk < 2; ++blk) s[blk] = mfma(row_operand<D>(kt, 32 * blk, ks, at), q[ks], s[blk]);
     reads_ahead<2 * NS>();
     auto sees = [&](int blk, int r) {
       const int j = w.row.key(v0 + 32 * blk + d_row(r, half));
@@ -119,7 +120,7 @@ __device__ __forceinline__ bool attend(const SwaParams &p, const FwdWork &w, u4 
           for (int ks = 0; ks < 4; ++ks)
 #pragma unroll
             for (int e = 0; e < 8; ++e) vis[ks][e] = static_cast<__bf16>(sees(ks / 2, (ks % 2) * 8 + e) ? 1.0f : 0.0f);
-          add_not_finite<D>(vt, vis, o, lane);
+          add_not_finite<D>(vt, vis, o, at);
       }
     }
 #pragma unroll
@@ -127,7 +128,7 @@ __device__ __forceinline__ bool attend(const SwaParams &p, const FwdWork &w, u4 
       const bf8 pk = as_operand(s[ks / 2], ks % 2);
 #pragma unroll
       for (int db = 0; db < NB; ++db) {
-        u4 v = __builtin_bit_cast(u4, col_operand<D>(vt, 16 * ks, db, lane));
+        u4 v = __builtin_bit_cast(u4, col_operand<D>(vt, 16 * ks, db, at));
         if constexpr (SAFE) {
           if (!whole) {
 #pragma unroll

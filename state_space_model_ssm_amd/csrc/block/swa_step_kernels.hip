@@ -49,6 +49,7 @@ __global__ void __launch_bounds__(256) swa_step_kernel(const SwaStepParams p, un
     const int64_t base = static_cast<int64_t>(bc) * slots * D;
     const uint16_t *kn = p.k + b * p.k_batch + c * D, *vn = p.v + b * p.v_batch + c * D;
     u4 *kt = lds[wave][0], *vt = lds[wave][1];
+    const Lanes at = lanes_of<D>(lane);
     if (lo < hi) {
       bf8 q[NS];
       const int row = (lane & 31) < heads ? lane & 31 : 0;  // lanes past the group repeat its first head
@@ -73,7 +74,7 @@ __global__ void __launch_bounds__(256) swa_step_kernel(const SwaStepParams p, un
 #pragma unroll
         for (int blk = 0; blk < 2; ++blk)
 #pragma unroll
-          for (int ks = 0; ks < NS; ++ks) s[blk] = mfma(row_operand<D>(kt, 32 * blk, ks, lane), q[ks], s[blk]);
+          for (int ks = 0; ks < NS; ++ks) s[blk] = mfma(row_operand<D>(kt, 32 * blk, ks, at), q[ks], s[blk]);
         wait_reads();
         if (i + 1 < hi) load_tile<D, 64>(kt, p.k_cache + base, D, k0 + kTile, last, lane);
         if (k0 + kTile > count) {
@@ -91,7 +92,7 @@ __global__ void __launch_bounds__(256) swa_step_kernel(const SwaStepParams p, un
         for (int ks = 0; ks < 4; ++ks) {
           const bf8 pk = as_operand(s[ks / 2], ks % 2);
 #pragma unroll
-          for (int db = 0; db < NB; ++db) o[db] = mfma(col_operand<D>(vt, 16 * ks, db, lane), pk, o[db]);
+          for (int db = 0; db < NB; ++db) o[db] = mfma(col_operand<D>(vt, 16 * ks, db, at), pk, o[db]);
         }
         wait_reads();
         if (i + 1 < hi) load_tile<D, 64>(vt, p.v_cache + base, D, k0 + kTile, last, lane);

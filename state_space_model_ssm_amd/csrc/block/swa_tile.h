@@ -38,23 +38,40 @@ __device__ __forceinline__ int slot(int r, int c) {
   else return r * 8 + (c ^ ((((r >> 1) & 3) << 1) | ((r >> 3) & 1)));
 }
 
+__device__ __forceinline__ unsigned lds_at(const void *p) {
+  return static_cast<unsigned>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const void *)(p)));
+}
+
+// Where a lane reads in a tile, in bytes.  The chunk's exchange is an
+// exclusive or, so the other operands of a tile lie at one of these two
+// addresses with constant bits flipped, plus whole rows: no register per
+// operand.
+struct Lanes {
+  unsigned row, col;
+};
+template <int D>
+__device__ __forceinline__ Lanes lanes_of(int lane) {
+  const int i = lane & 15, g = (lane >> 4) & 1, h = lane >> 5;
+  return {static_cast<unsigned>(slot<D>(lane & 31, h)) * 16,
+          static_cast<unsigned>(slot<D>(4 * h + (i >> 2), g * 2 + ((i >> 1) & 1))) * 16 + (i & 1) * 8};
+}
+
 // Operand of rows base .. base + 31, elements 16 s + 8 h .. + 7.
 template <int D>
-__device__ __forceinline__ bf8 row_operand(const u4 *tile, int base, int s, int lane) {
-  return __builtin_bit_cast(bf8, tile[slot<D>(base + (lane & 31), 2 * s + (lane >> 5))]);
+__device__ __forceinline__ bf8 row_operand(const u4 *tile, int base, int s, const Lanes &l) {
+  typedef __attribute__((address_space(3))) const u4 lds16;
+  return __builtin_bit_cast(bf8, *(lds16 *)(((lds_at(tile) + l.row) ^ (32 * s)) + base * 2 * D));
 }
 
 // Operand of elements (columns) 32 db + lane % 32 over rows base .. base + 15
-// in the order above: two transposing reads of 4 rows each.
+// (base a multiple of 16) in the order above: two transposing reads of 4 rows
+// each, 8 rows apart (which flips the lowest bit of the chunk's exchange).
 template <int D>
-__device__ __forceinline__ bf8 col_operand(const u4 *tile, int base, int db, int lane) {
-  const int i = lane & 15, g = (lane >> 4) & 1, h = lane >> 5;
-  const int c = db * 4 + g * 2 + ((i >> 1) & 1), r = base + 4 * h + (i >> 2);
+__device__ __forceinline__ bf8 col_operand(const u4 *tile, int base, int db, const Lanes &l) {
   typedef __attribute__((address_space(3))) sh4 lds4;
-  typedef __attribute__((address_space(3))) char ldsc;
-  ldsc *at = (ldsc *)tile;
-  const sh4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)(at + slot<D>(r, c) * 16 + (i & 1) * 8));
-  const sh4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)(at + slot<D>(r + 8, c) * 16 + (i & 1) * 8));
+  const unsigned at = (lds_at(tile) + l.col) ^ (64 * db);
+  const sh4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)(at + base * 2 * D));
+  const sh4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)((at ^ 16) + (base + 8) * 2 * D));
   return __builtin_bit_cast(bf8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
@@ -82,10 +99,6 @@ __device__ __forceinline__ void copy16(unsigned lds, const void *base, unsigned 
 __device__ __forceinline__ void copy16(unsigned lds, const void *at) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" : : "s"(lds), "v"(at) : "memory");
 }
-__device__ __forceinline__ unsigned lds_at(const void *p) {
-  return static_cast<unsigned>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const void *)(p)));
-}
-
 // Start the copy of tile rows t0 .. t0 + ROWS - 1 of a strided tensor (p: row
 // 0 of the head) into LDS, `NT` threads taking part; rows past `last` are read
 // as row `last`, so nothing past a length is touched.  A wavefront's 64 pieces
