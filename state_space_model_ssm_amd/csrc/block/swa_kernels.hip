@@ -20,25 +20,30 @@ constexpr float kLn2 = 0.6931471805599453f;
 // Bits 15 and 31 are set where that half, a bfloat16, is an infinity or NaN.
 __device__ __forceinline__ unsigned not_finite(unsigned x) { return (x & 0x7fff7fffu) + 0x00800080u; }
 
+// 1.0 in the halves that equal those of `what`, or that are NaN, 0 in the others.
+__device__ __forceinline__ unsigned is_half(unsigned x, unsigned what) {
+  const unsigned t = x ^ what, other = ((t & 0x7fff7fffu) + 0x7fff7fffu) | t;  // bits 15 and 31: not equal
+  return ((~other >> 15) & 0x00010001u) * 0x3f80u;
+}
+__device__ __forceinline__ unsigned is_nan(unsigned x) {
+  return ((((x & 0x7fff7fffu) + 0x007f007fu) >> 15) & 0x00010001u) * 0x3f80u;
+}
+
 // What the infinities and NaN of a tile of values add to the queries that see
 // them, out[db] += vis * v over those elements alone.  vis: 1 or 0 per key.
 template <int D>
 __device__ __forceinline__ void add_not_finite(const u4 *tile, const bf8 (&vis)[4], f16v (&out)[D / 32], const Lanes &at) {
 #pragma unroll
   for (int db = 0; db < D / 32; ++db) {
-#pragma unroll
+    // (Not unrolled: this is rare, and must not cost the others registers.)
+#pragma unroll 1
     for (int kind = 0; kind < 3; ++kind) {  // +inf, -inf, NaN
       f16v count = {};
 #pragma unroll
       for (int s = 0; s < 4; ++s) {
         u4 v = __builtin_bit_cast(u4, col_operand<D>(tile, 16 * s, db, at));
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          auto is = [&](unsigned b) {
-            return kind == 0 ? b == 0x7f80u : kind == 1 ? b == 0xff80u : (b & 0x7fffu) > 0x7f80u;
-          };
-          v[k] = (is(v[k] & 0xffffu) ? 0x3f80u : 0u) | (is(v[k] >> 16) ? 0x3f800000u : 0u);  // 1 or 0
-        }
+        for (int k = 0; k < 4; ++k) v[k] = kind == 2 ? is_nan(v[k]) : is_half(v[k], kind == 0 ? 0x7f807f80u : 0xff80ff80u);
         count = mfma(__builtin_bit_cast(bf8, v), vis[s], count);
       }
       const float add = kind == 0 ? INFINITY : kind == 1 ? -INFINITY : NAN;
@@ -115,12 +120,12 @@ __device__ __forceinline__ bool attend(const SwaParams &p, const FwdWork &w, u4 
     to_weights(s, w.c2, o, top, sum);
     if constexpr (SAFE) {
       if (!whole) {
-          bf8 vis[4];
+        bf8 vis[4];
 #pragma unroll
-          for (int ks = 0; ks < 4; ++ks)
+        for (int ks = 0; ks < 4; ++ks)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) vis[ks][e] = static_cast<__bf16>(sees(ks / 2, (ks % 2) * 8 + e) ? 1.0f : 0.0f);
-          add_not_finite<D>(vt, vis, o, at);
+          for (int e = 0; e < 8; ++e) vis[ks][e] = static_cast<__bf16>(sees(ks / 2, (ks % 2) * 8 + e) ? 1.0f : 0.0f);
+        add_not_finite<D>(vt, vis, o, at);
       }
     }
 #pragma unroll
@@ -136,6 +141,7 @@ __device__ __forceinline__ bool attend(const SwaParams &p, const FwdWork &w, u4 
           }
         }
         o[db] = mfma(__builtin_bit_cast(bf8, v), pk, o[db]);
+        if constexpr (SAFE) __builtin_amdgcn_sched_barrier(0);
       }
     }
   }
@@ -143,7 +149,7 @@ __device__ __forceinline__ bool attend(const SwaParams &p, const FwdWork &w, u4 
 }
 
 template <int D>
-__global__ void __launch_bounds__(256, 2) swa_fwd_kernel(const SwaParams p, int hw, unsigned qtiles, unsigned n) {
+__global__ void __launch_bounds__(256, D == 64 ? 3 : 2) swa_fwd_kernel(const SwaParams p, int hw, unsigned qtiles, unsigned n) {
   constexpr int CH = D / 8, NB = D / 32, NS = D / 16;
   __shared__ __align__(16) u4 lds[2][2][kTile * CH];  // buffer, K or V
   __shared__ int found;
