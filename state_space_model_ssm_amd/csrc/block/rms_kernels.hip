@@ -7,8 +7,11 @@
 // leaves a lane the fewest idle loads), summed across its lanes, and written.
 // Workgroups walk rows with w in registers, and with the backward's sums over
 // rows for dw, which they write once each; a second launch adds those in
-// order.  Rows that do not start on 16 bytes go value by value, the forward's
-// through LDS; rows too long for registers and LDS are read again per pass.
+// order.  Where rows do not start on 16 bytes the same loads start at any value
+// (16384 x 2047 bfloat16: forward 44 us, backward 52, against 43 and 48 for
+// 2048; value by value they were 61 and 142).  Rows too short or too long for
+// that, and groups that fit no lanes, go value by value, the forward's through
+// LDS, or are read again per pass if they are too long for LDS.
 #include "block_internal.h"
 
 namespace ssmb {
@@ -54,77 +57,77 @@ __device__ __forceinline__ int to_e4m3(float a, float b, int old, bool high) {
               : __builtin_amdgcn_cvt_pk_fp8_f32(hold(a), hold(b), old, false);
 }
 
-// V values of a row in a lane: 16 bytes, or one value.
-template <typename E, int V>
-struct Piece {
-  __device__ static __forceinline__ void get(const void *p, int64_t at, float (&f)[V]) { f[0] = ld(static_cast<const E *>(p), at); }
-  __device__ static __forceinline__ void put(void *p, int64_t at, const float (&f)[V]) { st(static_cast<E *>(p), at, f[0]); }
-};
-template <>
-struct Piece<float, 4> {
-  __device__ static __forceinline__ void get(const void *p, int64_t at, float (&f)[4]) {
-    const float4 v = *reinterpret_cast<const float4 *>(static_cast<const float *>(p) + at);
-    f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
-  }
-  __device__ static __forceinline__ void put(void *p, int64_t at, const float (&f)[4]) {
-    *reinterpret_cast<float4 *>(static_cast<float *>(p) + at) = make_float4(f[0], f[1], f[2], f[3]);
-  }
-};
-template <>
-struct Piece<float, 8> {
-  __device__ static __forceinline__ void get(const void *p, int64_t at, float (&f)[8]) {
-    const float4 *q = reinterpret_cast<const float4 *>(static_cast<const float *>(p) + at);
-    const float4 v = q[0], u = q[1];
-    f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w; f[4] = u.x; f[5] = u.y; f[6] = u.z; f[7] = u.w;
-  }
-  __device__ static __forceinline__ void put(void *p, int64_t at, const float (&f)[8]) {
-    float4 *q = reinterpret_cast<float4 *>(static_cast<float *>(p) + at);
-    q[0] = make_float4(f[0], f[1], f[2], f[3]);
-    q[1] = make_float4(f[4], f[5], f[6], f[7]);
-  }
-};
 __device__ __forceinline__ uint32_t pack(float a, float b) {
   typedef __attribute__((ext_vector_type(2))) __bf16 bf2;
   const bf2 v = {static_cast<__bf16>(a), static_cast<__bf16>(b)};
   return __builtin_bit_cast(uint32_t, v);
 }
-template <>
-struct Piece<uint16_t, 8> {
-  __device__ static __forceinline__ void get(const void *p, int64_t at, float (&f)[8]) {
-    const uint4 v = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p) + at);
-    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+
+// V values of a row in a lane, as words in loads of up to 16 bytes that start
+// at any value if LOOSE.
+template <int N, int ALIGN>
+struct Words {
+  typedef unsigned type __attribute__((ext_vector_type(N), aligned(ALIGN)));
+};
+template <typename E, int V, bool LOOSE>
+struct Piece {
+  static constexpr int kWords = V * sizeof(E) / 4, kAtOnce = kWords < 4 ? kWords : 4;
+  typedef typename Words<kAtOnce, LOOSE ? sizeof(E) : 4 * kAtOnce>::type type;
+  __device__ static __forceinline__ void get(const void *from, int64_t at, float (&f)[V]) {
+    const type *p = reinterpret_cast<const type *>(static_cast<const E *>(from) + at);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      f[2 * k] = __uint_as_float(u[k] << 16);
-      f[2 * k + 1] = __uint_as_float(u[k] & 0xffff0000u);
+    for (int k = 0; k < kWords; ++k) {
+      const unsigned v = p[k / kAtOnce][k % kAtOnce];
+      if constexpr (sizeof(E) == 4) {
+        f[k] = __uint_as_float(v);
+      } else {
+        f[2 * k] = __uint_as_float(v << 16);
+        f[2 * k + 1] = __uint_as_float(v & 0xffff0000u);
+      }
     }
   }
-  __device__ static __forceinline__ void put(void *p, int64_t at, const float (&f)[8]) {
-    *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p) + at) =
-        make_uint4(pack(f[0], f[1]), pack(f[2], f[3]), pack(f[4], f[5]), pack(f[6], f[7]));
-  }
-};
-template <>
-struct Piece<uint16_t, 4> {
-  __device__ static __forceinline__ void put(void *p, int64_t at, const float (&f)[4]) {
-    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p) + at) = make_uint2(pack(f[0], f[1]), pack(f[2], f[3]));
+  __device__ static __forceinline__ void put(void *to, int64_t at, const float (&f)[V]) {
+    type *p = reinterpret_cast<type *>(static_cast<E *>(to) + at);
+#pragma unroll
+    for (int k = 0; k < kWords; k += kAtOnce) {
+      type v;
+#pragma unroll
+      for (int n = 0; n < kAtOnce; ++n) {
+        if constexpr (sizeof(E) == 4) v[n] = __float_as_uint(f[k + n]);
+        else v[n] = pack(f[2 * (k + n)], f[2 * (k + n) + 1]);
+      }
+      p[k / kAtOnce] = v;
+    }
   }
 };
 
+// Where piece k of a row starts.  LOOSE: the last piece ends with the row, and
+// takes over values of the piece before it where the row is no multiple of V:
+// both lanes then write the same, and sums leave the first seen() out.
+template <int V, bool LOOSE>
+__device__ __forceinline__ int piece_at(int k, int dim) {
+  return LOOSE && k * V > dim - V ? dim - V : k * V;
+}
+template <int V, bool LOOSE>
+__device__ __forceinline__ int seen(int k, int at) {
+  int n = k * V - at;
+  if constexpr (!LOOSE) return 0;
+  asm volatile("" : "+v"(n));  // comparisons with it are not to be kept across rows: they would take 128 scalar registers
+  return n;
+}
+
 // Rows in registers: piece n of lane l is piece l + TPR n of the row.
 // Q8: groups are the row or 2^k neighbouring lanes of a wavefront (group_lanes).
-template <typename Tin, typename Tout, int TPR, int NV, bool Q8>
+template <typename Tin, typename Tout, int TPR, int NV, bool Q8, bool LOOSE>
 __global__ void __launch_bounds__(256) rms_rows_kernel(const RmsParams p, int group_lanes) {
   constexpr int V = 16 / sizeof(Tin), kRows = 256 / TPR;
   __shared__ float lds[2][2][4];
-  const int l = threadIdx.x % TPR, pieces = static_cast<int>(p.dim / V);
+  const int l = threadIdx.x % TPR, dim = static_cast<int>(p.dim), pieces = (dim + V - 1) / V;
   const float inv = 1.0f / static_cast<float>(p.dim);
   float w[NV][V];
 #pragma unroll
-  for (int n = 0; n < NV; ++n) {
-    const int at = l + TPR * n < pieces ? l + TPR * n : 0;
-    Piece<float, V>::get(p.w, static_cast<int64_t>(at) * V, w[n]);
-  }
+  for (int n = 0; n < NV; ++n)
+    Piece<float, V, LOOSE>::get(p.w, piece_at<V, LOOSE>(l + TPR * n < pieces ? l + TPR * n : 0, dim), w[n]);
   int odd = 0;  // turns of the workgroup-wide sums' scratch
   for (int64_t first = static_cast<int64_t>(blockIdx.x) * kRows; first < p.rows; first += static_cast<int64_t>(gridDim.x) * kRows) {
     const int64_t row = first + threadIdx.x / TPR;
@@ -133,27 +136,30 @@ __global__ void __launch_bounds__(256) rms_rows_kernel(const RmsParams p, int gr
     float s[NV][V], ss = 0.0f;
 #pragma unroll
     for (int n = 0; n < NV; ++n) {
-      const bool in = l + TPR * n < pieces;
+      const int k = l + TPR * n, at = piece_at<V, LOOSE>(k, dim);
 #pragma unroll
       for (int e = 0; e < V; ++e) s[n][e] = 0.0f;
-      if (in) {
-        const int64_t at = base + static_cast<int64_t>(l + TPR * n) * V;
-        Piece<Tin, V>::get(p.x, at, s[n]);
+      if (k < pieces) {
+        Piece<Tin, V, LOOSE>::get(p.x, base + at, s[n]);
         if (p.residual != nullptr) {
           float r[V];
-          Piece<Tin, V>::get(p.residual, at, r);
+          Piece<Tin, V, LOOSE>::get(p.residual, base + at, r);
 #pragma unroll
           for (int e = 0; e < V; ++e) s[n][e] += r[e];
         }
       }
+      const int skip = seen<V, LOOSE>(k, at);
 #pragma unroll
-      for (int e = 0; e < V; ++e) ss = fmaf(s[n][e], s[n][e], ss);
+      for (int e = 0; e < V; ++e) {
+        const float v = e < skip ? 0.0f : s[n][e];
+        ss = fmaf(v, v, ss);
+      }
     }
     const float rstd = 1.0f / sqrtf(fmaf(row_sum<TPR>(ss, lds[odd][0]), inv, p.eps));
     if (p.residual_out != nullptr && live) {
 #pragma unroll
       for (int n = 0; n < NV; ++n)
-        if (l + TPR * n < pieces) Piece<Tin, V>::put(p.residual_out, base + static_cast<int64_t>(l + TPR * n) * V, s[n]);
+        if (l + TPR * n < pieces) Piece<Tin, V, LOOSE>::put(p.residual_out, base + piece_at<V, LOOSE>(l + TPR * n, dim), s[n]);
     }
 #pragma unroll
     for (int n = 0; n < NV; ++n)
@@ -162,7 +168,7 @@ __global__ void __launch_bounds__(256) rms_rows_kernel(const RmsParams p, int gr
     if constexpr (!Q8) {
 #pragma unroll
       for (int n = 0; n < NV; ++n)
-        if (l + TPR * n < pieces && live) Piece<Tout, V>::put(p.y, base + static_cast<int64_t>(l + TPR * n) * V, s[n]);
+        if (l + TPR * n < pieces && live) Piece<Tout, V, LOOSE>::put(p.y, base + piece_at<V, LOOSE>(l + TPR * n, dim), s[n]);
     } else {
       float top[NV];
 #pragma unroll
@@ -205,15 +211,18 @@ __global__ void __launch_bounds__(256) rms_rows_kernel(const RmsParams p, int gr
           for (int e = 0; e < V; ++e) s[n][e] *= lift(scale);
         }
         if (l + TPR * n < pieces && live) {
-          uint8_t *q = static_cast<uint8_t *>(p.y) + base + static_cast<int64_t>(l + TPR * n) * V;
+          uint8_t *q = static_cast<uint8_t *>(p.y) + base + piece_at<V, LOOSE>(l + TPR * n, dim);
           int b[V / 4];
 #pragma unroll
           for (int e = 0; e < V; e += 4) {
             b[e / 4] = to_e4m3(s[n][e] * k, s[n][e + 1] * k, 0, false);
             b[e / 4] = to_e4m3(s[n][e + 2] * k, s[n][e + 3] * k, b[e / 4], true);
           }
-          if constexpr (V == 8) *reinterpret_cast<int2 *>(q) = make_int2(b[0], b[1]);
-          else *reinterpret_cast<int *>(q) = b[0];
+          typedef typename Words<V / 4, LOOSE ? 1 : V>::type bytes;
+          bytes v;
+#pragma unroll
+          for (int n4 = 0; n4 < V / 4; ++n4) v[n4] = static_cast<unsigned>(b[n4]);
+          *reinterpret_cast<bytes *>(q) = v;
         }
       }
     }
@@ -261,19 +270,18 @@ __global__ void __launch_bounds__(256) rms_any_kernel(const RmsParams p, int kee
   }
 }
 
-// Backward with rows in registers, V values per piece.
-template <typename Tin, int V, int TPR, int NV>
+// Backward with rows in registers.
+template <typename Tin, int TPR, int NV, bool LOOSE>
 __global__ void __launch_bounds__(256) rms_bwd_rows_kernel(const RmsBwdParams p) {
-  constexpr int kRows = 256 / TPR;
+  constexpr int V = 16 / sizeof(Tin), kRows = 256 / TPR;
   __shared__ float lds[2][2][4];
   __shared__ __align__(16) float sums[kRows > 1 ? kRows * TPR * V : 1];
-  const int l = threadIdx.x % TPR, pieces = static_cast<int>(p.dim / V);
+  const int l = threadIdx.x % TPR, dim = static_cast<int>(p.dim), pieces = (dim + V - 1) / V;
   const float inv = 1.0f / static_cast<float>(p.dim);
   float w[NV][V], dw[NV][V];
 #pragma unroll
   for (int n = 0; n < NV; ++n) {
-    const int at = l + TPR * n < pieces ? l + TPR * n : 0;
-    Piece<float, V>::get(p.w, static_cast<int64_t>(at) * V, w[n]);
+    Piece<float, V, LOOSE>::get(p.w, piece_at<V, LOOSE>(l + TPR * n < pieces ? l + TPR * n : 0, dim), w[n]);
 #pragma unroll
     for (int e = 0; e < V; ++e) dw[n][e] = 0.0f;
   }
@@ -285,18 +293,20 @@ __global__ void __launch_bounds__(256) rms_bwd_rows_kernel(const RmsBwdParams p)
     float s[NV][V], d[NV][V], r[NV][V], ss = 0.0f, dot = 0.0f;
 #pragma unroll
     for (int n = 0; n < NV; ++n) {
+      const int k = l + TPR * n, at = piece_at<V, LOOSE>(k, dim);
 #pragma unroll
       for (int e = 0; e < V; ++e) s[n][e] = d[n][e] = r[n][e] = 0.0f;
-      if (l + TPR * n < pieces) {
-        const int64_t at = base + static_cast<int64_t>(l + TPR * n) * V;
-        Piece<Tin, V>::get(p.s, at, s[n]);
-        Piece<Tin, V>::get(p.dy, at, d[n]);
-        if (p.dres != nullptr) Piece<Tin, V>::get(p.dres, at, r[n]);
+      if (k < pieces) {
+        Piece<Tin, V, LOOSE>::get(p.s, base + at, s[n]);
+        Piece<Tin, V, LOOSE>::get(p.dy, base + at, d[n]);
+        if (p.dres != nullptr) Piece<Tin, V, LOOSE>::get(p.dres, base + at, r[n]);
       }
+      const int skip = seen<V, LOOSE>(k, at);
 #pragma unroll
       for (int e = 0; e < V; ++e) {
-        ss = fmaf(s[n][e], s[n][e], ss);
-        dot = fmaf(d[n][e] * w[n][e], s[n][e], dot);
+        const float v = e < skip ? 0.0f : s[n][e], dv = e < skip ? 0.0f : d[n][e] * w[n][e];
+        ss = fmaf(v, v, ss);
+        dot = fmaf(dv, v, dot);
       }
     }
     const float rstd = 1.0f / sqrtf(fmaf(row_sum<TPR>(ss, lds[odd][0]), inv, p.eps));
@@ -310,7 +320,7 @@ __global__ void __launch_bounds__(256) rms_bwd_rows_kernel(const RmsBwdParams p)
         if (live) dw[n][e] = fmaf(d[n][e], norm, dw[n][e]);
         r[n][e] = fmaf(rstd, d[n][e] * w[n][e] - norm * mean, r[n][e]);
       }
-      if (l + TPR * n < pieces && live) Piece<Tin, V>::put(p.dx, base + static_cast<int64_t>(l + TPR * n) * V, r[n]);
+      if (l + TPR * n < pieces && live) Piece<Tin, V, LOOSE>::put(p.dx, base + piece_at<V, LOOSE>(l + TPR * n, dim), r[n]);
     }
   }
   if (p.dw == nullptr) return;
@@ -318,9 +328,11 @@ __global__ void __launch_bounds__(256) rms_bwd_rows_kernel(const RmsBwdParams p)
 #pragma unroll
   for (int n = 0; n < NV; ++n) {
     if constexpr (kRows > 1) {  // over the rows in turn of the workgroup
+      const int k = l + TPR * n, skip = seen<V, LOOSE>(k, piece_at<V, LOOSE>(k, dim));
       __syncthreads();
 #pragma unroll
-      for (int e = 0; e < V; ++e) sums[threadIdx.x * V + e] = dw[n][e];
+      for (int e = 0; e < V; ++e)
+        if (e >= skip && k < pieces) sums[threadIdx.x * V + e - skip] = dw[n][e];
       __syncthreads();
       for (int c = threadIdx.x; c < TPR * V; c += 256) {
         float t = 0.0f;
@@ -330,7 +342,7 @@ __global__ void __launch_bounds__(256) rms_bwd_rows_kernel(const RmsBwdParams p)
         if (at < p.dim) part[at] = t;
       }
     } else if (l + TPR * n < pieces) {
-      Piece<float, V>::put(part, static_cast<int64_t>(l + TPR * n) * V, dw[n]);
+      Piece<float, V, LOOSE>::put(part, piece_at<V, LOOSE>(l + TPR * n, dim), dw[n]);
     }
   }
 }
@@ -388,7 +400,7 @@ bool aligned16(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0;
 
 // Lanes per row and pieces per lane for `pieces` of a row, and the kernel's
 // instance for them; false where they are too many.
-template <bool LONG = false, typename F>
+template <typename F>
 bool with_shape(int64_t pieces, F f) {
   if (pieces <= 16) f.template operator()<16, 1>();
   else if (pieces <= 32) f.template operator()<16, 2>();
@@ -399,18 +411,14 @@ bool with_shape(int64_t pieces, F f) {
   else if (pieces <= 768) f.template operator()<256, 3>();
   else if (pieces <= 1024) f.template operator()<256, 4>();
   else if (pieces <= 2048) f.template operator()<256, 8>();
-  else if constexpr (LONG) {
-    if (pieces <= 4096) f.template operator()<256, 16>();
-    else if (pieces <= 8192) f.template operator()<256, 32>();
-    else return false;
-  } else return false;
+  else return false;
   return true;
 }
 
 // Workgroups of 256 / lanes rows each; more than fit at once walk the rows.
 constexpr int64_t kMostGroups = 2048;
 
-template <typename Tin, typename Tout, bool Q8>
+template <typename Tin, typename Tout, bool Q8, bool LOOSE>
 struct RowsLaunch {
   const RmsParams &p;
   int group_lanes;
@@ -418,7 +426,7 @@ struct RowsLaunch {
   template <int TPR, int NV>
   void operator()() {
     const int64_t n = (p.rows + 256 / TPR - 1) / (256 / TPR);
-    hipLaunchKernelGGL((rms_rows_kernel<Tin, Tout, TPR, NV, Q8>), dim3(static_cast<uint32_t>(n < kMostGroups ? n : kMostGroups)),
+    hipLaunchKernelGGL((rms_rows_kernel<Tin, Tout, TPR, NV, Q8, LOOSE>), dim3(static_cast<uint32_t>(n < kMostGroups ? n : kMostGroups)),
                        dim3(256), 0, st, p, group_lanes);
   }
 };
@@ -428,37 +436,44 @@ hipError_t run_fwd(const RmsParams &p, hipStream_t st) {
   constexpr int V = 16 / sizeof(Tin);
   // Stores of y are 4 to 32 bytes wide, by its type; its rows start on as many
   // where they start on 16 bytes of x.
-  bool rows = p.dim % V == 0 && aligned16(p.x) && aligned16(p.residual) && aligned16(p.residual_out) && aligned16(p.y) &&
-              aligned16(p.w);
+  const bool loose = p.dim % V != 0 || !aligned16(p.x) || !aligned16(p.residual) || !aligned16(p.residual_out) ||
+                     !aligned16(p.y) || !aligned16(p.w);
+  const int64_t pieces = (p.dim + V - 1) / V;
+  bool rows = p.dim >= V;
   int lanes = 0;
   if (Q8 && p.group < p.dim) {
+    if (p.dim % V != 0) rows = false;  // the last piece would span two groups
     lanes = p.group % V == 0 && p.group / V <= 64 ? static_cast<int>(p.group / V) : -1;
-    if (lanes < 1 || (lanes & (lanes - 1)) != 0 || (lanes > 16 && p.dim / V <= 32)) rows = false;
+    if (lanes < 1 || (lanes & (lanes - 1)) != 0 || (lanes > 16 && pieces <= 32)) rows = false;
   }
-  if (rows && with_shape(p.dim / V, RowsLaunch<Tin, Tout, Q8>{p, lanes, st})) return hipGetLastError();
+  if (rows && (loose ? with_shape(pieces, RowsLaunch<Tin, Tout, Q8, true>{p, lanes, st})
+                     : with_shape(pieces, RowsLaunch<Tin, Tout, Q8, false>{p, lanes, st})))
+    return hipGetLastError();
   const int keep = p.dim <= 8192;  // 32 KiB of LDS: four workgroups per CU and more
   hipLaunchKernelGGL((rms_any_kernel<Tin, Tout, Q8>), dim3(static_cast<uint32_t>(p.rows)), dim3(256),
                      keep ? static_cast<size_t>(p.dim) * 4 : 0, st, p, keep);
   return hipGetLastError();
 }
 
-template <typename Tin, int V>
+template <typename Tin, bool LOOSE>
 struct BwdLaunch {
   const RmsBwdParams &p;
   hipStream_t st;
   template <int TPR, int NV>
   void operator()() {
-    hipLaunchKernelGGL((rms_bwd_rows_kernel<Tin, V, TPR, NV>), dim3(static_cast<uint32_t>(p.parts)), dim3(256), 0, st, p);
+    hipLaunchKernelGGL((rms_bwd_rows_kernel<Tin, TPR, NV, LOOSE>), dim3(static_cast<uint32_t>(p.parts)), dim3(256), 0, st, p);
   }
 };
 
 template <typename Tin>
 void run_bwd(const RmsBwdParams &p, hipStream_t st) {
   constexpr int V = 16 / sizeof(Tin);
-  const bool vec = p.dim % V == 0 && aligned16(p.dy) && aligned16(p.s) && aligned16(p.dres) && aligned16(p.dx) &&
-                   aligned16(p.w) && aligned16(p.ws);
-  if (vec && with_shape(p.dim / V, BwdLaunch<Tin, V>{p, st})) return;
-  if (!vec && with_shape<true>(p.dim, BwdLaunch<Tin, 1>{p, st})) return;
+  const bool loose = p.dim % V != 0 || !aligned16(p.dy) || !aligned16(p.s) || !aligned16(p.dres) || !aligned16(p.dx) ||
+                     !aligned16(p.w) || !aligned16(p.ws);
+  const int64_t pieces = (p.dim + V - 1) / V;
+  if (p.dim >= V &&
+      (loose ? with_shape(pieces, BwdLaunch<Tin, true>{p, st}) : with_shape(pieces, BwdLaunch<Tin, false>{p, st})))
+    return;
   hipLaunchKernelGGL((rms_bwd_any_kernel<Tin>), dim3(static_cast<uint32_t>(p.parts)), dim3(256), 0, st, p);
 }
 

@@ -104,6 +104,36 @@ def test_8_bit_output(rows, dim, group, dtype):
     assert np.all(np.abs(got - v) <= np.maximum(np.abs(v) / 16, 2.0 ** -10) * (1 + 1e-5))
 
 
+# Widths about the 16 bytes of a load, and rows that start at any value.
+@pytest.mark.parametrize("dim", [3, 4, 5, 8, 9, 15, 17, 63, 66, 257, 1023, 4097, 8191])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_rows_that_start_at_any_value(dim, dtype):
+    rows = 5
+    x, res, w, dy, dres = make(rows, dim, dtype, dim)
+
+    def shifted(t):
+        flat = torch.empty(t.numel() + 1, dtype=t.dtype, device="cuda")
+        flat[1:] = t.flatten()
+        return flat[1:].view(t.shape)
+
+    a, b = shifted(x), shifted(res)
+    y, s = ssm.rms_add_fwd(a, shifted(w), b, y=shifted(nan((rows, dim), dtype)), residual_out=shifted(nan((rows, dim), dtype)))
+    want, total = ref.rms(x, w, res)
+    ref.assert_close(s, total, ref.storage_tol(total, dtype), "s")
+    ref.assert_close(y, want, ref.storage_tol(want, dtype), "y")
+    ssm.rms_add_fwd(a, shifted(w), b, y=a, residual_out=b)  # in place
+    assert torch.equal(a, y) and torch.equal(b, s)
+    q, scale, _ = ssm.rms_add_q8_fwd(x.cuda(), w.cuda(), res.cuda())
+    q2, scale2, s2 = ssm.rms_add_q8_fwd(shifted(x), shifted(w), shifted(res))
+    assert torch.equal(q.view(torch.uint8), q2.view(torch.uint8)) and torch.equal(scale, scale2) and torch.equal(s2, s)
+    dx, dw = ssm.rms_add_bwd(shifted(dy), s, shifted(w), dres=shifted(dres), dw=shifted(nan((dim,), F32)))
+    aligned = ssm.rms_add_bwd(dy.cuda(), s.clone(), w.cuda(), dres=dres.cuda())
+    want, want_w, size = ref.rms_bwd(dy, s.cpu(), w, dres)
+    for got in ((dx, dw), aligned):
+        ref.assert_close(got[0], want, ref.storage_tol(want, dtype), "dx")
+        ref.assert_close(got[1], want_w, ref.storage_tol(want_w, F32, size), "dw")
+
+
 def test_8_bit_output_of_zeros_and_nan():
     x = torch.randn(4, 256)
     x[1] = 0
