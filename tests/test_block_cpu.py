@@ -135,6 +135,7 @@ def test_glr_sizes():
         assert call(name, in_dtype=2) == DTYPE and call(name, out_dtype=-1) == DTYPE
         assert call(name, reserved=1) == SHAPE and call(name, reserved2=1) == SHAPE
         assert call(name, batch=1 << 40, dim=1 << 40) == UNSUPPORTED
+        assert call(name, dim=(1 << 22) + 1) == UNSUPPORTED
     assert call("ssm_glr_step", seqlen=2) == SHAPE and call("ssm_glr_fwd", seqlen=-3) == SHAPE
     assert call("ssm_glr_fwd", seqlen=1 << 60) == UNSUPPORTED
     n = ctypes.c_size_t()
@@ -176,6 +177,9 @@ def test_swa_sizes():
         assert call(name, v_batch=8) == SHAPE
     for name in ("ssm_swa_fwd", "ssm_swa_bwd", "ssm_swa_fill"):
         assert call(name, seqlen=-1) == SHAPE and call(name, k_token=64) == SHAPE and call(name, seqlen=1 << 31) == UNSUPPORTED
+        for axis in ("q_token", "k_token", "v_token"):
+            far = (1 << 24) + 8
+            assert call(name, batch=1, **{axis: far, axis[0] + "_batch": 40 * far}) == UNSUPPORTED
     assert call("ssm_swa_step", seqlen=2) == SHAPE
     for name in ("ssm_swa_step", "ssm_swa_fill"):
         assert call(name, window=1 << 30, sinks=1 << 30) == UNSUPPORTED
