@@ -25,9 +25,9 @@ __global__ void __launch_bounds__(256, 2) swa_dq_kernel(const SwaParams p, int h
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const unsigned nheads = static_cast<unsigned>(p.nheads), nkv = static_cast<unsigned>(p.nkv);
   const unsigned group = nheads / nkv, hb = group / hw;
-  const unsigned id = xcd_order(blockIdx.x, n);
-  const unsigned qt = id % qtiles, rest = id / qtiles;
-  const int64_t b = rest / (hb * nkv), c = rest / hb % nkv;
+  const unsigned batch = static_cast<unsigned>(p.batch), id = xcd_order(blockIdx.x, n, nkv * batch);
+  const unsigned rest = id / qtiles, qt = uneven(p.window, p.seqlen) ? qtiles - 1 - id % qtiles : id % qtiles;
+  const int64_t c = rest / (hb * batch), b = rest / hb % batch;
   const int64_t head = c * group + (rest % hb) * hw + wave % hw;
   const int qspan = 32 * (4 / hw), q0 = static_cast<int>(qt) * qspan, wq0 = q0 + 32 * (wave / hw);
   const int len = row_length(p, b), last = len - 1, t = wq0 + (lane & 31), L = static_cast<int>(p.seqlen);
@@ -219,9 +219,10 @@ __global__ void __launch_bounds__(256, D == 64 ? 2 : 1) swa_dkv_kernel(const Swa
   const unsigned far_items = plan.far_blocks * plan.far_chunks, near_items = plan.blocks * plan.slices;
   const unsigned nnear = n / (far_items + near_items) * near_items;
   const bool far = blockIdx.x >= nnear;
-  const unsigned item = far ? xcd_order(blockIdx.x - nnear, n - nnear) : xcd_order(blockIdx.x, nnear);
-  const unsigned per = far ? far_items : near_items, bc = item / per, k = item % per;
-  const int64_t b = bc / nkv, c = bc % nkv;
+  const unsigned batch = static_cast<unsigned>(p.batch);
+  const unsigned item = far ? xcd_order(blockIdx.x - nnear, n - nnear, nkv * batch) : xcd_order(blockIdx.x, nnear, nkv * batch);
+  const unsigned per = far ? far_items : near_items, k = item % per;
+  const int64_t c = item / per / batch, b = item / per % batch, bc = b * nkv + c;
   const int len = row_length(p, b), last = len - 1, L = static_cast<int>(p.seqlen);
   const int window = static_cast<int>(p.window), sinks = static_cast<int>(p.sinks);
   const float c2 = p.scale * kLog2e;
@@ -253,7 +254,7 @@ __global__ void __launch_bounds__(256, D == 64 ? 2 : 1) swa_dkv_kernel(const Swa
       wait_reads();
     }
     // Add the wavefronts' terms, dk then dv, in LDS.
-    float *sums = reinterpret_cast<float *>(lds), *out = p.ws_far + (static_cast<int64_t>(bc) * far_items + k) * 2 * 32 * D;
+    float *sums = reinterpret_cast<float *>(lds), *out = p.ws_far + (bc * far_items + k) * 2 * 32 * D;
     for (int which = 0; which < 2; ++which) {
       __syncthreads();
       put_rows<D>(sums + wave * 32 * D, lane & 31, half, which == 0 ? dk : dv);
@@ -314,7 +315,7 @@ __global__ void __launch_bounds__(256, D == 64 ? 2 : 1) swa_dkv_kernel(const Swa
     }
   }
   if (block < plan.sum_blocks) {
-    const int64_t part = (static_cast<int64_t>(bc) * plan.sum_blocks + block) * plan.slices + slice;
+    const int64_t part = (bc * plan.sum_blocks + block) * plan.slices + slice;
     put_rows<D>(p.ws_part + part * 2 * 128 * D, 32 * wave + (lane & 31), half, dk);
     put_rows<D>(p.ws_part + (part * 2 + 1) * 128 * D, 32 * wave + (lane & 31), half, dv);
     return;
@@ -398,8 +399,10 @@ SwaBwdPlan swa_bwd_plan(int64_t batch, int64_t seqlen, int64_t nheads, int64_t n
   window = window < seqlen ? window : seqlen;
   sinks = sinks < seqlen ? sinks : seqlen;
   plan.blocks = static_cast<unsigned>(blocks);
-  // Too few workgroups for the 256 CUs: the heads of a group are shared out.
-  const int64_t want = headdim == 64 ? 512 : 256;
+  // Too few workgroups for the 256 CUs, or for uneven ones to even out: the heads
+  // of a group are shared out (8192 tokens, 16 heads of 128 on 4: window 1024
+  // 311 us, with four times as many workgroups 351; window 8192 1547 and 1146).
+  const int64_t want = (headdim == 64 ? 512 : 256) * (uneven(window, seqlen) ? 4 : 1);
   int64_t slices = 1;
   while (slices < group && batch * nkv * blocks * slices < want) {
     do ++slices;

@@ -157,10 +157,10 @@ __global__ void __launch_bounds__(256, D == 64 ? 3 : 2) swa_fwd_kernel(const Swa
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const unsigned nheads = static_cast<unsigned>(p.nheads), nkv = static_cast<unsigned>(p.nkv);
   const unsigned group = nheads / nkv, hb = group / hw;
-  // Work order: query tile fastest, then head block of a key head, key head, batch row.
-  const unsigned id = xcd_order(blockIdx.x, n);
-  const unsigned qt = id % qtiles, rest = id / qtiles;
-  const int64_t b = rest / (hb * nkv), c = rest / hb % nkv;
+  // Work order: query tile fastest, then head block of a key head, batch row, key head.
+  const unsigned batch = static_cast<unsigned>(p.batch), id = xcd_order(blockIdx.x, n, nkv * batch);
+  const unsigned rest = id / qtiles, qt = uneven(p.window, p.seqlen) ? qtiles - 1 - id % qtiles : id % qtiles;
+  const int64_t c = rest / (hb * batch), b = rest / hb % batch;
   const int64_t head = c * group + (rest % hb) * hw + wave % hw;
   const int qspan = 32 * (4 / hw), q0 = static_cast<int>(qt) * qspan;
   FwdWork w;
