@@ -29,13 +29,14 @@ __device__ __forceinline__ f16v mfma(bf8 a, bf8 b, f16v c) {
 
 // LDS slot of 16-byte chunk c of row r.  Rows are a whole (D = 128) or half
 // (D = 64) a turn of the 64 banks, so chunk c of all rows would share its
-// banks; c is exchanged with a rotated row number instead.  16 rows in turn
-// then fill the 16 slots of the banks (row reads), and so do the four rows by
-// two chunks that 16 lanes of a transposed read take.
+// banks; c is exchanged with a number made of the row instead.  16 rows in
+// turn then fill the 16 slots of the banks (row reads), and so do the four rows
+// by four chunks that 32 lanes of a transposed read take: that is why the
+// row's lowest bits flip the chunk's highest.
 template <int D>
 __device__ __forceinline__ int slot(int r, int c) {
-  if constexpr (D == 128) return r * 16 + (c ^ (((r & 7) << 1) | ((r >> 3) & 1)));
-  else return r * 8 + (c ^ ((((r >> 1) & 3) << 1) | ((r >> 3) & 1)));
+  if constexpr (D == 128) return r * 16 + (c ^ (((r & 3) << 2) | ((r >> 2) & 3)));
+  else return r * 8 + (c ^ ((((r >> 1) & 1) << 2) | ((r >> 2) & 3)));
 }
 
 __device__ __forceinline__ unsigned lds_at(const void *p) {
@@ -65,13 +66,13 @@ __device__ __forceinline__ bf8 row_operand(const u4 *tile, int base, int s, cons
 
 // Operand of elements (columns) 32 db + lane % 32 over rows base .. base + 15
 // (base a multiple of 16) in the order above: two transposing reads of 4 rows
-// each, 8 rows apart (which flips the lowest bit of the chunk's exchange).
+// each, 8 rows apart (which flips bit 1 of the chunk's exchange).
 template <int D>
 __device__ __forceinline__ bf8 col_operand(const u4 *tile, int base, int db, const Lanes &l) {
   typedef __attribute__((address_space(3))) sh4 lds4;
   const unsigned at = (lds_at(tile) + l.col) ^ (64 * db);
   const sh4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)(at + base * 2 * D));
-  const sh4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)((at ^ 16) + (base + 8) * 2 * D));
+  const sh4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)((at ^ 32) + (base + 8) * 2 * D));
   return __builtin_bit_cast(bf8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
