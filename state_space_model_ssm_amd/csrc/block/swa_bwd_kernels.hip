@@ -68,7 +68,6 @@ __global__ void __launch_bounds__(256, 2) swa_dq_kernel(const SwaParams p, int h
       p.ws_lse2[stat] = lse2;
       p.ws_delta[stat] = delta;
     }
-    const int own = sinks < t + 1 ? sinks : t + 1;
     const Lanes at = lanes_of<D>(lane);
     start(0);
     for (int i = 0; i < tiles; ++i) {
@@ -79,6 +78,7 @@ __global__ void __launch_bounds__(256, 2) swa_dq_kernel(const SwaParams p, int h
       const u4 *kt = lds[i & 1][0], *vt = lds[i & 1][1];
       if (j0 > wq0 + 31 || (j1 <= wq0 - window && j0 >= sinks) || wq0 >= len) continue;
       const bool whole = j1 <= wq0 && wq0 + 31 - j0 < window;
+      const Seen seen = seen_by(keys, t, v0, half, window, sinks);
 #pragma unroll
       for (int blk = 0; blk < 2; ++blk) {
         f16v s = {}, dp = {};
@@ -93,10 +93,7 @@ __global__ void __launch_bounds__(256, 2) swa_dq_kernel(const SwaParams p, int h
           dp[r] = __builtin_amdgcn_exp2f(fmaf(s[r], c2, -lse2)) * (dp[r] - delta);
         if (!whole) {
 #pragma unroll
-          for (int r = 0; r < 16; ++r) {
-            const int j = keys.key(v0 + 32 * blk + d_row(r, half));
-            dp[r] = static_cast<unsigned>(t - j) < static_cast<unsigned>(window) || j < own ? dp[r] : 0.0f;
-          }
+          for (int r = 0; r < 16; ++r) dp[r] = seen(32 * blk + d_row(r, 0)) ? dp[r] : 0.0f;
         }
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks) {
@@ -121,7 +118,7 @@ __global__ void __launch_bounds__(256, 2) swa_dq_kernel(const SwaParams p, int h
 
 // The gradients that 32 queries (rows base .. base + 31 of the tiles qt and dt,
 // with their stats) give the 32 keys of a wavefront, lane % 32 its key.  WHOLE:
-// every query sees every key; else sees(row) tells.
+// every query sees every key; else sees(row) tells, rows less 4 in the second lane half.
 template <int D, typename F>
 __device__ __forceinline__ void add_queries(const u4 *qt, const u4 *dt, const float *lse2, const float *delta, int base,
                                             const bf8 (&kf)[D / 16], const bf8 (&vf)[D / 16], float c2, bool whole, F sees,
@@ -148,7 +145,7 @@ __device__ __forceinline__ void add_queries(const u4 *qt, const u4 *dt, const fl
   if (!whole) {
 #pragma unroll
     for (int r = 0; r < 16; ++r) {
-      const bool yes = sees(d_row(r, half));
+      const bool yes = sees(d_row(r, 0));
       s[r] = yes ? s[r] : 0.0f;
       dp[r] = yes ? dp[r] : 0.0f;
     }
@@ -250,7 +247,7 @@ __global__ void __launch_bounds__(256, D == 64 ? 2 : 1) swa_dkv_kernel(const Swa
       wait_tiles();
       const int t0 = (first + u % tiles) * 32;
       add_queries<D>(qt, dt, stats[wave][0], stats[wave][1], 0, kf, vf, c2, t0 + 31 < len && j0 + 31 < sinks,
-                     [&](int r) { return t0 + r < len && j < sinks; }, dk, dv, at, half);
+                     [&](int r) { return t0 + 4 * half + r < len && j < sinks; }, dk, dv, at, half);
       wait_reads();
     }
     // Add the wavefronts' terms, dk then dv, in LDS.
@@ -279,6 +276,8 @@ __global__ void __launch_bounds__(256, D == 64 ? 2 : 1) swa_dkv_kernel(const Swa
   const int nq = t_hi > t_lo ? t_hi - t_lo : 0, steps = nq * heads;
   if (steps > 0) {
     load_keys_and_values<D>(p, b, c, j < last ? j : last, half, kf, vf);
+    // How many queries from its own on see this lane's key: the window's, or all of a sink's, up to the length.
+    const unsigned reach = j >= len ? 0 : j < sinks || window > len - j ? len - j : window;
     int at_head = head0, at_tile = t_lo;  // of the next tile to start
     auto start = [&](int i) {
       const int t0 = at_tile * kTile, buf = i & 1;
@@ -305,12 +304,9 @@ __global__ void __launch_bounds__(256, D == 64 ? 2 : 1) swa_dkv_kernel(const Swa
         // Does any of these 32 queries see any of the wavefront's keys, or all of them all?
         if (q0 + 31 < wk0 || (q0 >= wk0 + 31 + window && wk0 >= sinks) || q0 >= len || wk0 >= len) continue;
         const bool whole = q0 >= wk0 + 31 && q0 + 31 < len && (q0 + 31 - wk0 < window || wk0 + 31 < sinks);
+        const int behind = q0 + 4 * half - j;  // of the lane's first query after its key
         add_queries<D>(lds[i & 1][0], lds[i & 1][1], stats[i & 1][0], stats[i & 1][1], 32 * blk, kf, vf, c2, whole,
-                       [&](int r) {
-                         const int t = q0 + r;
-                         return t < len && (static_cast<unsigned>(t - j) < static_cast<unsigned>(window) || (j < sinks && j <= t));
-                       },
-                       dk, dv, at, half);
+                       [&](int r) { return static_cast<unsigned>(behind + r) < reach; }, dk, dv, at, half);
       }
     }
   }

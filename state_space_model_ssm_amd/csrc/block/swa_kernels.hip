@@ -56,7 +56,7 @@ __device__ __forceinline__ void add_not_finite(const u4 *tile, const bf8 (&vis)[
 // What a workgroup knows of its work.
 struct FwdWork {
   const uint16_t *k, *v;  // of the key head
-  int wq0;                // first query of this wavefront
+  int q0, q1, wq0;        // first and last query of the workgroup, first of this wavefront
   KeyRow row;             // the keys its queries see
   int len, tiles;
   float c2;               // |scale| log2(e)
@@ -73,7 +73,6 @@ __device__ __forceinline__ bool attend(const SwaParams &p, const FwdWork &w, u4 
   constexpr int CH = D / 8, NB = D / 32, NS = D / 16;
   const int lane = tid & 63, half = lane >> 5, t = w.wq0 + (lane & 31);
   const int window = static_cast<int>(p.window), sinks = static_cast<int>(p.sinks);
-  const int own = sinks < t + 1 ? sinks : t + 1;  // sinks this query sees
   const Lanes at = lanes_of<D>(lane);
   unsigned bad = 0;
   top = -INFINITY;
@@ -91,6 +90,15 @@ __device__ __forceinline__ bool attend(const SwaParams &p, const FwdWork &w, u4 
     if (i + 1 < w.tiles) start(i + 1);
     const int v0 = i * kTile, j0 = w.row.key(v0), j1 = w.row.key(v0 + kTile - 1);
     const u4 *kt = lds[i & 1][0], *vt = lds[i & 1][1];
+    if constexpr (!SAFE) {
+      if (j1 > w.q0 || w.q1 - j0 >= window) {  // some of the workgroup's queries see part of it: each wavefront looks at a quarter
+#pragma unroll
+        for (int k = 0; k < kTile * CH / 256; ++k) {
+          const u4 v = vt[k * 256 + tid];
+          bad |= not_finite(v[0]) | not_finite(v[1]) | not_finite(v[2]) | not_finite(v[3]);
+        }
+      }
+    }
     // Does this wavefront see any of the tile, or all of it?
     if (j0 > w.wq0 + 31 || (j1 <= w.wq0 - window && j0 >= sinks) || w.wq0 >= w.len) continue;
     const bool whole = j1 <= w.wq0 && w.wq0 + 31 - j0 < window;
@@ -100,31 +108,22 @@ __device__ __forceinline__ bool attend(const SwaParams &p, const FwdWork &w, u4 
 #pragma unroll
       for (int blk = 0; blk < 2; ++blk) s[blk] = mfma(row_operand<D>(kt, 32 * blk, ks, at), q[ks], s[blk]);
     reads_ahead<2 * NS>();
-    auto sees = [&](int blk, int r) {
-      const int j = w.row.key(v0 + 32 * blk + d_row(r, half));
-      return static_cast<unsigned>(t - j) < static_cast<unsigned>(window) || j < own;
-    };
+    Seen seen = seen_by(w.row, t, v0, half, window, sinks);
     if (!whole) {
 #pragma unroll
       for (int blk = 0; blk < 2; ++blk)
 #pragma unroll
-        for (int r = 0; r < 16; ++r) s[blk][r] = sees(blk, r) ? s[blk][r] : -INFINITY;
-      if constexpr (!SAFE) {
-#pragma unroll
-        for (int k = 0; k < kTile * CH / 64; ++k) {
-          const u4 v = vt[k * 64 + lane];
-          bad |= not_finite(v[0]) | not_finite(v[1]) | not_finite(v[2]) | not_finite(v[3]);
-        }
-      }
+        for (int r = 0; r < 16; ++r) s[blk][r] = seen(32 * blk + d_row(r, 0)) ? s[blk][r] : -INFINITY;
     }
     to_weights(s, w.c2, o, top, sum);
     if constexpr (SAFE) {
       if (!whole) {
+        asm volatile("" : "+v"(seen.ahead), "+v"(seen.own));  // 32 masks are not to be kept for this
         bf8 vis[4];
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks)
 #pragma unroll
-          for (int e = 0; e < 8; ++e) vis[ks][e] = static_cast<__bf16>(sees(ks / 2, (ks % 2) * 8 + e) ? 1.0f : 0.0f);
+          for (int e = 0; e < 8; ++e) vis[ks][e] = static_cast<__bf16>(seen(32 * (ks / 2) + d_row(ks % 2 * 8 + e, 0)) ? 1.0f : 0.0f);
         add_not_finite<D>(vt, vis, o, at);
       }
     }
@@ -165,6 +164,8 @@ __global__ void __launch_bounds__(256, D == 64 ? 3 : 2) swa_fwd_kernel(const Swa
   const int qspan = 32 * (4 / hw), q0 = static_cast<int>(qt) * qspan;
   FwdWork w;
   w.len = row_length(p, b);
+  w.q0 = q0;
+  w.q1 = q0 + qspan - 1;
   w.wq0 = q0 + 32 * (wave / hw);
   w.c2 = fmaxf(fabsf(p.scale) * kLog2e, 0x1p-100f);
   const int t = w.wq0 + (lane & 31), L = static_cast<int>(p.seqlen);  // t: this lane's query

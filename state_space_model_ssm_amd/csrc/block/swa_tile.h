@@ -131,7 +131,23 @@ __device__ __forceinline__ KeyRow key_row(int q0, int window, int sinks) {
   return k;
 }
 
-// The same for the places v0 .. v0 + 63 of such a row.
+// Which places of such a row, c past v0 for this lane half, query t sees: those
+// through the window count down from `ahead`, and sinks are the first ones (the
+// keys before the window, or, where the window starts among the sinks, the
+// first `own`).  Two comparisons with constants and a subtraction per place.
+struct Seen {
+  int ahead, own;
+  unsigned window;
+  __device__ __forceinline__ bool operator()(int c) const {
+    return static_cast<unsigned>(ahead - c) < window || c < own;
+  }
+};
+__device__ __forceinline__ Seen seen_by(const KeyRow &k, int t, int v0, int half, int window, int sinks) {
+  const int own = k.first < k.low ? k.first : sinks < t + 1 ? sinks : t + 1;
+  return {t - (v0 - k.first + k.low) - 4 * half, own - v0 - 4 * half, static_cast<unsigned>(window)};
+}
+
+// load_tile() for the places v0 .. v0 + 63 of such a row.
 template <int D, int NT>
 __device__ __forceinline__ void load_keys(u4 *tile, const uint16_t *p, int64_t token, const KeyRow &row, int v0, int last,
                                           int tid) {
