@@ -10,9 +10,11 @@
 // summary, takes the state it starts with from its predecessors', and runs its
 // steps: every tensor is read once, whatever the shape.  (Cutting the sequence
 // into segments that a first launch sums up reads the inputs twice: 195 us
-// against 101 for 1 x 32749 x 1536, and walking whole sequences with one
+// against 106 for 1 x 32749 x 1536, and walking whole sequences with one
 // workgroup per 64 channels leaves 320 workgroups for 4 x 5120 channels, at
-// 2.3 of the 4.7 TB/s that enough tiles in flight reach.)
+// 2.3 TB/s against the 3.9 of enough tiles in flight.)  Bound by memory, inputs
+// out of the caches: bfloat16, 4 x 4096 x 5120, forward 175 us, backward 290,
+// both 3.9 TB/s; float32, 8 x 2048 x 1536, 92 and 134 us, 4.4 and 5.3 TB/s.
 //
 // Tiles of a channel block are grouped by 16 in time.  A tile waits for the
 // state at its group's start and the summaries of the tiles before it in the
@@ -124,7 +126,7 @@ __device__ __forceinline__ Place place(int64_t dim, int64_t seqlen, int64_t batc
   const unsigned ct = static_cast<unsigned>((dim + kLanes * C - 1) / (kLanes * C)), rows = static_cast<unsigned>(batch) * ct;
   // Each round of ids begins a set later: workgroups go to the XCDs in turn, and
   // an XCD that kept the same few columns of 128 bytes would find them in as few
-  // of its L2's channels (1 x 32749 x 1536: 125 -> 105 us).
+  // of its L2's channels (1 x 32749 x 1536: 125 us against 105).
   const unsigned sets = tiles > 1 ? glr_sets(rows) : 1, set = (id + id / sets) % sets;
   if (tiles > 1) {
     if (threadIdx.x == 0) lds = atomicAdd(chain.counter + set * (kGlrCounterBytes / 4), 1u);
