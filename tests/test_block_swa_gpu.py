@@ -75,6 +75,15 @@ def test_lengths(d, sinks):
     assert not y[:2].any() and torch.isinf(lse[:2]).all()
 
 
+@pytest.mark.parametrize("B,L,H,KV,d,window,sinks", [
+    (8, 260, 4, 1, 64, 64, 3), (4, 200, 4, 2, 128, 150, 5), (2, 330, 12, 4, 64, 330, 0), (3, 520, 6, 2, 64, 100, 40),
+    (1, 900, 4, 1, 64, 500, 5), (1, 900, 8, 1, 128, 500, 130), (5, 300, 2, 1, 128, 40, 2), (16, 70, 1, 1, 64, 70, 1)])
+def test_rows_of_unequal_length_in_every_work_order(B, L, H, KV, d, window, sinks):
+    """Key heads by rows that share out over 8 or do not, windows of less and of more than half the sequence."""
+    g = torch.Generator().manual_seed(B * L)
+    check(*make(B, L, H, KV, d, L + H), window, sinks, torch.randint(0, L + 1, (B,), generator=g, dtype=torch.int32))
+
+
 def test_garbage_gradients_past_a_length_are_not_read():
     q, k, v, dy = make(2, 100, 2, 1, 64, 6)
     lengths = torch.tensor([40, 100], dtype=torch.int32)
