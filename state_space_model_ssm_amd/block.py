@@ -133,7 +133,7 @@ def _out(t, shape, dtype, like, name, stream):
                 return torch.empty(shape, dtype=dtype, device=like.device)
         if dtype == like.dtype and shape == like.shape and like.is_contiguous():
             return torch.empty_like(like)
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return like.new_empty(shape, dtype=dtype)
     if t.shape != shape or t.dtype != dtype or t.device != like.device:
         raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)} on {like.device}, "
                          f"got {t.dtype} {tuple(t.shape)} on {t.device}")
@@ -359,6 +359,11 @@ def _swa_dims(q, k, v, window, sinks, scale, lead) -> SwaDims:
         raise ValueError("k and v must have q's batch, seqlen and headdim")
     d = q.shape[-1]
     scale = 1.0 / math.sqrt(d) if scale is None else scale
+    if lead == 1 and q.is_contiguous() and k.is_contiguous() and v.is_contiguous():  # a step's usual call, in less time
+        if not (q.is_cuda and k.is_cuda and v.is_cuda):
+            raise ValueError("tensors must be on the GPU")
+        H, KV = q.shape[1], k.shape[1]
+        return SwaDims(q.shape[0], 1, H, KV, d, window, sinks, H * d, 0, KV * d, 0, KV * d, 0, scale)
     return SwaDims(q.shape[0], q.shape[1] if lead == 2 else 1, q.shape[-2], k.shape[-2], d, window, sinks,
                    *_heads("q", q, lead, d), *_heads("k", k, lead, d), *_heads("v", v, lead, d), scale)
 
