@@ -12,6 +12,11 @@
 // operand as they lie (see swa_tile.h); both are rounded to bfloat16 there, as
 // the matrix cores take them, and everything is summed in float32.
 //
+// dy.y comes from the rounded y.  Of rows with few keys its error is as large
+// as a rounding of dq itself, so dq takes ds in two parts, rounded and left
+// over (half as many products again; its error falls from 1.6 roundings to
+// 1.1), and finds the exact dy.y on its way, which dk gets for nothing.
+//
 // Bound as the forward is (matrix instructions busy a third of the time): 8192
 // tokens, 16 heads of 128 on 4, window 1024, 119 and 191 us (820 and 680
 // TFLOP/s); 4 x 2048 tokens, 32 heads of 64 on 8, window 512, 76 and 96 us (590
@@ -69,10 +74,7 @@ __global__ void __launch_bounds__(256, 2) swa_dq_kernel(const SwaParams p, int h
     delta += other_half(delta);
     const int64_t stat = (b * p.nheads + head) * p.seqlen + row;
     const float lse2 = p.lse[stat] * kLog2e, c2 = p.scale * kLog2e;
-    if (half == 0 && t < len) {
-      p.ws_lse2[stat] = lse2;
-      p.ws_delta[stat] = delta;
-    }
+    float off = 0.0f;  // what dy.y is too small by, since y is rounded: the weights' sum is 1, so sum_j ds_tj
     const Lanes at = lanes_of<D>(lane);
     start(0);
     for (int i = 0; i < tiles; ++i) {
@@ -101,12 +103,23 @@ __global__ void __launch_bounds__(256, 2) swa_dq_kernel(const SwaParams p, int h
           for (int r = 0; r < 16; ++r) dp[r] = seen(32 * blk + d_row(r, 0)) ? dp[r] : 0.0f;
         }
 #pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
-          const bf8 dsk = as_operand(dp, ks);
+        for (int r = 0; r < 16; ++r) off += dp[r];
 #pragma unroll
-          for (int db = 0; db < NB; ++db) dq[db] = mfma(col_operand<D>(kt, 32 * blk + 16 * ks, db, at), dsk, dq[db]);
+        for (int ks = 0; ks < 2; ++ks) {
+          const bf8 dsk = as_operand(dp, ks), rest = left_over(dp, ks, dsk);
+#pragma unroll
+          for (int db = 0; db < NB; ++db) {
+            const bf8 kc = col_operand<D>(kt, 32 * blk + 16 * ks, db, at);
+            dq[db] = mfma(kc, dsk, dq[db]);
+            dq[db] = mfma(kc, rest, dq[db]);
+          }
         }
       }
+    }
+    off += other_half(off);
+    if (half == 0 && t < len) {
+      p.ws_lse2[stat] = lse2;
+      p.ws_delta[stat] = delta + off;
     }
   }
   if (t >= L) return;

@@ -84,6 +84,16 @@ __device__ __forceinline__ bf8 as_operand(const f16v &d, int s) {
   return v;
 }
 
+// What as_operand() rounded off, as an operand.
+__device__ __forceinline__ bf8 left_over(const f16v &d, int s, bf8 rounded) {
+  const u4 bits = __builtin_bit_cast(u4, rounded);
+  bf8 v;
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    v[e] = static_cast<__bf16>(d[8 * s + e] - __uint_as_float(e % 2 != 0 ? bits[e / 2] & 0xffff0000u : bits[e / 2] << 16));
+  return v;
+}
+
 // The row that register i of a D result stands for in lane half h.
 __device__ __forceinline__ constexpr int d_row(int i, int h) { return 8 * (i / 4) + 4 * h + i % 4; }
 
