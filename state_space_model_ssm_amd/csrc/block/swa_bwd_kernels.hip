@@ -6,20 +6,22 @@
 //
 // Two kernels, so that every sum has one owner and no atomics: one walks the
 // keys of 32 queries per wavefront (dq), the other the queries and heads of 32
-// keys per wavefront (dk, dv).  That is 7 products of pairs x headdim against
-// the 5 that a single pass would need, which would have to add dq from many
-// workgroups.  p and ds go from one product's result into the next one's
-// operand as they lie (see swa_tile.h); both are rounded to bfloat16 there, as
-// the matrix cores take them, and everything is summed in float32.
+// keys per wavefront (dk, dv).  That is 7 products of pairs x headdim, 8 with
+// the second part of ds below, against the 5 that a single pass would need,
+// which would have to add dq from many workgroups.  p and ds go from one
+// product's result into the next one's operand as they lie (see swa_tile.h);
+// both are rounded to bfloat16 there, as the matrix cores take them, and
+// everything is summed in float32.
 //
 // dy.y comes from the rounded y.  Of rows with few keys its error is as large
 // as a rounding of dq itself, so dq takes ds in two parts, rounded and left
-// over (half as many products again; its error falls from 1.6 roundings to
-// 1.1), and finds the exact dy.y on its way, which dk gets for nothing.
+// over (a third more products in its kernel, 53 us -> 63 on 4 ragged rows of
+// 2048 tokens; its error falls from 1.6 roundings to 1.1), and finds the exact
+// dy.y on its way, which dk gets for nothing.
 //
 // Bound as the forward is (matrix instructions busy a third of the time): 8192
-// tokens, 16 heads of 128 on 4, window 1024, 119 and 191 us (820 and 680
-// TFLOP/s); 4 x 2048 tokens, 32 heads of 64 on 8, window 512, 76 and 96 us (590
+// tokens, 16 heads of 128 on 4, window 1024, 143 and 200 us (900 and 650
+// TFLOP/s); 4 x 2048 tokens, 32 heads of 64 on 8, window 512, 91 and 96 us (660
 // and 630).
 #include "swa_tile.h"
 
