@@ -98,8 +98,9 @@ __global__ void __launch_bounds__(256) swa_step_kernel(const SwaStepParams p, un
         wait_reads();
         if (i + 1 < hi) load_tile<D, 64>(vt, p.v_cache + base, D, k0 + kTile, last, lane);
         if (has && lane < CH) {  // the token takes its slot
-          reinterpret_cast<u4 *>(p.k_cache + base + own * D)[lane] = reinterpret_cast<const u4 *>(kn)[lane];
-          reinterpret_cast<u4 *>(p.v_cache + base + own * D)[lane] = reinterpret_cast<const u4 *>(vn)[lane];
+          const int64_t to = base + static_cast<int64_t>(own) * D;  // own * D passes 2^31 in a long cache
+          reinterpret_cast<u4 *>(p.k_cache + to)[lane] = reinterpret_cast<const u4 *>(kn)[lane];
+          reinterpret_cast<u4 *>(p.v_cache + to)[lane] = reinterpret_cast<const u4 *>(vn)[lane];
         }
       }
     }

@@ -277,3 +277,29 @@ def test_nan_queries_give_nan_alone():
     pos = torch.tensor([900], dtype=torch.int32, device="cuda")
     y = ssm.swa_step(q[:, 40].cuda(), k[:, 40].cuda(), v[:, 40].cuda(), kc, vc, pos)
     assert torch.isnan(y[0, 1].float()).all() and not torch.isnan(y[0, 0].float()).any()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_slots_past_2_31_elements_of_one_head(d):
+    """One head's cache of more than 2^31 elements, its keys far from the query but for the last 64: the token takes
+    its slot at the end of a part-filled and of a full ring, and no other slot changes."""
+    slots, sinks, tail = 2 ** 31 // d + 100, 4, 64
+    kc, vc = (torch.full((1, 1, slots, d), -16.0, dtype=BF16, device="cuda") for _ in range(2))
+    g = torch.Generator().manual_seed(d)
+    kc[0, 0, -tail:], vc[0, 0, -tail:] = (torch.randn(tail, d, generator=g).to(BF16).cuda() for _ in range(2))
+    q = torch.ones(1, 1, d, dtype=BF16)
+    for at in (slots - 3, 2 * slots - sinks - 2):
+        k, v = (torch.randn(1, 1, d, generator=g).to(BF16) for _ in range(2))
+        slot = at if at < slots else at - (slots - sinks)
+        count = min(at + 1, slots) - (slots - tail)   # of the last 64 slots
+        kt, vt = kc[0, 0, -tail:].cpu(), vc[0, 0, -tail:].cpu()
+        kt[slot - slots], vt[slot - slots] = k[0, 0], v[0, 0]
+        # The other keys' scores are -16 sqrt(d): 2^25 weights of e^-128 are nothing beside the tail's.
+        s = (ref.f64(kt[:count]) @ ref.f64(q[0, 0])) / d ** 0.5
+        w = np.exp(s) / np.exp(s).sum()
+        want, size = w @ ref.f64(vt[:count]), w @ np.abs(ref.f64(vt[:count]))
+        y = ssm.swa_step(q.cuda(), k.cuda(), v.cuda(), kc, vc, torch.tensor([at], dtype=torch.int32, device="cuda"), sinks=sinks)
+        ref.assert_close(y[0, 0], want, ref.U * np.abs(want) + (ref.U + 2.0 ** -14) * size, ("y", at))
+        assert torch.equal(kc[0, 0, -tail:].cpu(), kt) and torch.equal(vc[0, 0, -tail:].cpu(), vt), at
+        for cache in (kc, vc):
+            assert all(bool((part == -16).all()) for part in cache[0, 0, :-tail].split(1 << 20))
