@@ -232,6 +232,12 @@ __global__ void __launch_bounds__(256) rms_rows_kernel(const RmsParams p, int gr
   }
 }
 
+// Rows that are read in a loop are summed in runs of 256 terms per thread, and
+// the runs in float64: added up one by one in float32, equal values of a row of
+// 2^27 moved the sum by a thousandth.
+constexpr int64_t kRun = 256 * 256;
+__device__ __forceinline__ int64_t run_end(int64_t run, int64_t dim) { return run + kRun < dim ? run + kRun : dim; }
+
 // Rows of any alignment, a workgroup per row, through LDS (`keep`: the row's
 // sums stay there between the passes) or, too long for that, read again.
 template <typename Tin, typename Tout, bool Q8>
@@ -241,12 +247,17 @@ __global__ void __launch_bounds__(256) rms_any_kernel(const RmsParams p, int kee
   const int64_t row = blockIdx.x, base = row * p.dim;
   const Tin *x = static_cast<const Tin *>(p.x), *res = static_cast<const Tin *>(p.residual);
   auto sum_at = [&](int64_t c) { return ld(x, base + c) + (res != nullptr ? ld(res, base + c) : 0.0f); };
-  float ss = 0.0f;
-  for (int64_t c = threadIdx.x; c < p.dim; c += 256) {
-    const float s = sum_at(c);
-    if (keep) held[c] = s;
-    ss = fmaf(s, s, ss);
+  double total = 0.0;
+  for (int64_t run = 0; run < p.dim; run += kRun) {
+    float ss = 0.0f;
+    for (int64_t c = run + threadIdx.x, end = run_end(run, p.dim); c < end; c += 256) {
+      const float s = sum_at(c);
+      if (keep) held[c] = s;
+      ss = fmaf(s, s, ss);
+    }
+    total += ss;
   }
+  const float ss = static_cast<float>(total);
   const float rstd = 1.0f / sqrtf(fmaf(row_sum<256>(ss, lds), 1.0f / static_cast<float>(p.dim), p.eps));
   auto value = [&](int64_t c) { return keep ? held[c] : sum_at(c); };  // (row_sum() has a barrier)
   if constexpr (Q8) {
@@ -361,12 +372,18 @@ __global__ void __launch_bounds__(256) rms_bwd_any_kernel(const RmsBwdParams p) 
     for (int64_t c = threadIdx.x; c < p.dim; c += 256) part[c] = 0.0f;
   for (int64_t row = blockIdx.x; row < p.rows; row += p.parts) {
     const int64_t base = row * p.dim;
-    float ss = 0.0f, dot = 0.0f;
-    for (int64_t c = threadIdx.x; c < p.dim; c += 256) {
-      const float v = ld(s, base + c);
-      ss = fmaf(v, v, ss);
-      dot = fmaf(ld(dy, base + c) * p.w[c], v, dot);
+    double squares = 0.0, products = 0.0;
+    for (int64_t run = 0; run < p.dim; run += kRun) {
+      float ss = 0.0f, dot = 0.0f;
+      for (int64_t c = run + threadIdx.x, end = run_end(run, p.dim); c < end; c += 256) {
+        const float v = ld(s, base + c);
+        ss = fmaf(v, v, ss);
+        dot = fmaf(ld(dy, base + c) * p.w[c], v, dot);
+      }
+      squares += ss;
+      products += dot;
     }
+    const float ss = static_cast<float>(squares), dot = static_cast<float>(products);
     const float inv = 1.0f / static_cast<float>(p.dim);
     __syncthreads();  // the last row's sums have been read
     const float rstd = 1.0f / sqrtf(fmaf(row_sum<256>(ss, lds[0]), inv, p.eps));

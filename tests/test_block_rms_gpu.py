@@ -248,3 +248,18 @@ def test_8_bit_output_of_tiny_values():
         got = q.float().cpu().double().numpy() * np.repeat(ref.f64(scale), group or dim, 1)[:, :dim]
         # half a step of e4m3 (2^-4 of a value), and the scale's own step of 2^-149 against about 2^-128
         assert np.all(np.abs(got - want) <= np.abs(want) * (2.0 ** -4 + 2.0 ** -18) + 2.0 ** -10 * np.abs(want).max())
+
+
+def test_sums_of_long_rows():
+    """A row of 2^27 equal values, whose squares take more bits than a sum of them leaves: y is w, dx is 0."""
+    dim = 2 ** 27 + 9
+    x = torch.full((1, dim), 1.1, dtype=BF16, device="cuda")
+    w = torch.ones(dim, device="cuda")
+    y, _ = ssm.rms_add_fwd(x, w, out_dtype=F32)
+    rstd = 1 / (float(x[0, 0]) ** 2 + 1e-5) ** 0.5
+    assert bool(((y.double() - float(x[0, 0]) * rstd).abs() <= 1e-5).all())
+    dx, _ = ssm.rms_add_bwd(x, x, w, return_dw=False)
+    # dn - n mean(dn n) of equal values: 1 - n^2, times dn and rstd; 1e-5 of dn's part.
+    n = float(x[0, 0]) * rstd
+    want = rstd * float(x[0, 0]) * (1 - n * n)
+    assert bool(((dx.double() - want).abs() <= 1e-5).all())
