@@ -238,48 +238,51 @@ __global__ void __launch_bounds__(256) rms_rows_kernel(const RmsParams p, int gr
 constexpr int64_t kRun = 256 * 256;
 __device__ __forceinline__ int64_t run_end(int64_t run, int64_t dim) { return run + kRun < dim ? run + kRun : dim; }
 
-// Rows of any alignment, a workgroup per row, through LDS (`keep`: the row's
-// sums stay there between the passes) or, too long for that, read again.
+// Rows of any alignment, a workgroup per row in turn, through LDS (`keep`: the
+// row's sums stay there between the passes) or, too long for that, read again.
 template <typename Tin, typename Tout, bool Q8>
 __global__ void __launch_bounds__(256) rms_any_kernel(const RmsParams p, int keep) {
   extern __shared__ float held[];
   __shared__ float lds[4];
-  const int64_t row = blockIdx.x, base = row * p.dim;
   const Tin *x = static_cast<const Tin *>(p.x), *res = static_cast<const Tin *>(p.residual);
-  auto sum_at = [&](int64_t c) { return ld(x, base + c) + (res != nullptr ? ld(res, base + c) : 0.0f); };
-  double total = 0.0;
-  for (int64_t run = 0; run < p.dim; run += kRun) {
-    float ss = 0.0f;
-    for (int64_t c = run + threadIdx.x, end = run_end(run, p.dim); c < end; c += 256) {
-      const float s = sum_at(c);
-      if (keep) held[c] = s;
-      ss = fmaf(s, s, ss);
+  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
+    const int64_t base = row * p.dim;
+    auto sum_at = [&](int64_t c) { return ld(x, base + c) + (res != nullptr ? ld(res, base + c) : 0.0f); };
+    double total = 0.0;
+    for (int64_t run = 0; run < p.dim; run += kRun) {
+      float ss = 0.0f;
+      for (int64_t c = run + threadIdx.x, end = run_end(run, p.dim); c < end; c += 256) {
+        const float s = sum_at(c);
+        if (keep) held[c] = s;
+        ss = fmaf(s, s, ss);
+      }
+      total += ss;
     }
-    total += ss;
-  }
-  const float ss = static_cast<float>(total);
-  const float rstd = 1.0f / sqrtf(fmaf(row_sum<256>(ss, lds), 1.0f / static_cast<float>(p.dim), p.eps));
-  auto value = [&](int64_t c) { return keep ? held[c] : sum_at(c); };  // (row_sum() has a barrier)
-  if constexpr (Q8) {
-    // A wavefront per group in turn.
-    const int lane = threadIdx.x & 63;
-    const int64_t ngroup = (p.dim + p.group - 1) / p.group;
-    for (int64_t g = threadIdx.x >> 6; g < ngroup; g += 4) {
-      const int64_t lo = g * p.group, hi = lo + p.group < p.dim ? lo + p.group : p.dim;
-      float top = 0.0f;
-      for (int64_t c = lo + lane; c < hi; c += 64) top = amax(top, value(c) * rstd * p.w[c]);
-      const float scale = lanes_amax(top, 64) * (1.0f / 448.0f), k = inverse(scale);
-      if (lane == 0) p.scale[row * ngroup + g] = scale;
-      for (int64_t c = lo + lane; c < hi; c += 64)
-        static_cast<uint8_t *>(p.y)[base + c] =
-            static_cast<uint8_t>(to_e4m3(value(c) * rstd * p.w[c] * lift(scale) * k, 0.0f, 0, false) & 0xff);
+    const float ss = static_cast<float>(total);
+    const float rstd = 1.0f / sqrtf(fmaf(row_sum<256>(ss, lds), 1.0f / static_cast<float>(p.dim), p.eps));
+    auto value = [&](int64_t c) { return keep ? held[c] : sum_at(c); };  // (row_sum() has a barrier)
+    if constexpr (Q8) {
+      // A wavefront per group in turn.
+      const int lane = threadIdx.x & 63;
+      const int64_t ngroup = (p.dim + p.group - 1) / p.group;
+      for (int64_t g = threadIdx.x >> 6; g < ngroup; g += 4) {
+        const int64_t lo = g * p.group, hi = lo + p.group < p.dim ? lo + p.group : p.dim;
+        float top = 0.0f;
+        for (int64_t c = lo + lane; c < hi; c += 64) top = amax(top, value(c) * rstd * p.w[c]);
+        const float scale = lanes_amax(top, 64) * (1.0f / 448.0f), k = inverse(scale);
+        if (lane == 0) p.scale[row * ngroup + g] = scale;
+        for (int64_t c = lo + lane; c < hi; c += 64)
+          static_cast<uint8_t *>(p.y)[base + c] =
+              static_cast<uint8_t>(to_e4m3(value(c) * rstd * p.w[c] * lift(scale) * k, 0.0f, 0, false) & 0xff);
+      }
+      if (!keep) __syncthreads();  // residual_out may be x: every group has been read
     }
-    if (!keep) __syncthreads();  // residual_out may be x: every group has been read
-  }
-  for (int64_t c = threadIdx.x; c < p.dim; c += 256) {
-    const float s = value(c);
-    if (p.residual_out != nullptr) st(static_cast<Tin *>(p.residual_out), base + c, s);
-    if constexpr (!Q8) st(static_cast<Tout *>(p.y), base + c, s * rstd * p.w[c]);
+    for (int64_t c = threadIdx.x; c < p.dim; c += 256) {
+      const float s = value(c);
+      if (p.residual_out != nullptr) st(static_cast<Tin *>(p.residual_out), base + c, s);
+      if constexpr (!Q8) st(static_cast<Tout *>(p.y), base + c, s * rstd * p.w[c]);
+    }
+    __syncthreads();  // the next row takes `held` and `lds`
   }
 }
 
@@ -397,22 +400,26 @@ __global__ void __launch_bounds__(256) rms_bwd_any_kernel(const RmsBwdParams p) 
   }
 }
 
-// dw: 16 threads share the terms of a column, a workgroup has 64 columns.
+// dw: 16 threads share the terms of a column, a workgroup has 64 columns at a time.
 __global__ void __launch_bounds__(1024) rms_sum_kernel(const float *part, float *dw, int64_t parts, int64_t dim) {
   __shared__ float lds[16][64];
-  const int64_t c = static_cast<int64_t>(blockIdx.x) * 64 + threadIdx.x % 64;
-  const int k0 = threadIdx.x / 64;
-  float s = 0.0f;
-  if (c < dim) {
+  const int k0 = threadIdx.x / 64, col = threadIdx.x % 64;
+  for (int64_t first = static_cast<int64_t>(blockIdx.x) * 64; first < dim; first += static_cast<int64_t>(gridDim.x) * 64) {
+    const int64_t c = first + col;
+    float s = 0.0f;
+    if (c < dim) {
 #pragma unroll 8
-    for (int64_t k = k0; k < parts; k += 16) s += part[k * dim + c];
-  }
-  lds[k0][threadIdx.x % 64] = s;
-  __syncthreads();
-  if (k0 != 0 || c >= dim) return;
+      for (int64_t k = k0; k < parts; k += 16) s += part[k * dim + c];
+    }
+    lds[k0][col] = s;
+    __syncthreads();
+    if (k0 == 0 && c < dim) {
 #pragma unroll
-  for (int k = 1; k < 16; ++k) s += lds[k][threadIdx.x];
-  dw[c] = s;
+      for (int k = 1; k < 16; ++k) s += lds[k][col];
+      dw[c] = s;
+    }
+    __syncthreads();  // the next columns take `lds`
+  }
 }
 
 bool aligned16(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
@@ -436,6 +443,10 @@ bool with_shape(int64_t pieces, F f) {
 
 // Workgroups of 256 / lanes rows each; more than fit at once walk the rows.
 constexpr int64_t kMostGroups = 2048;
+// A launch has fewer than 2^32 threads along an axis.  Past this many
+// workgroups the other kernels walk too.
+constexpr int64_t kMostWalkers = 65536;
+uint32_t walkers(int64_t n) { return static_cast<uint32_t>(n < kMostWalkers ? n : kMostWalkers); }
 
 template <typename Tin, typename Tout, bool Q8, bool LOOSE>
 struct RowsLaunch {
@@ -469,7 +480,7 @@ hipError_t run_fwd(const RmsParams &p, hipStream_t st) {
                      : with_shape(pieces, RowsLaunch<Tin, Tout, Q8, false>{p, lanes, st})))
     return hipGetLastError();
   const int keep = p.dim <= 8192;  // 32 KiB of LDS: four workgroups per CU and more
-  hipLaunchKernelGGL((rms_any_kernel<Tin, Tout, Q8>), dim3(static_cast<uint32_t>(p.rows)), dim3(256),
+  hipLaunchKernelGGL((rms_any_kernel<Tin, Tout, Q8>), dim3(walkers(p.rows)), dim3(256),
                      keep ? static_cast<size_t>(p.dim) * 4 : 0, st, p, keep);
   return hipGetLastError();
 }
@@ -512,8 +523,7 @@ hipError_t launch_rms_bwd(const RmsBwdParams &p, int in_bf16, hipStream_t st) {
     else run_bwd<float>(p, st);
   }
   if (p.dw != nullptr)
-    hipLaunchKernelGGL(rms_sum_kernel, dim3(static_cast<uint32_t>((p.dim + 63) / 64)), dim3(1024), 0, st, p.ws, p.dw,
-                       p.parts, p.dim);
+    hipLaunchKernelGGL(rms_sum_kernel, dim3(walkers((p.dim + 63) / 64)), dim3(1024), 0, st, p.ws, p.dw, p.parts, p.dim);
   return hipGetLastError();
 }
 

@@ -263,3 +263,39 @@ def test_sums_of_long_rows():
     n = float(x[0, 0]) * rstd
     want = rstd * float(x[0, 0]) * (1 - n * n)
     assert bool(((dx.double() - want).abs() <= 1e-5).all())
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_rows_past_2_24(dtype):
+    """More narrow rows than a launch has workgroups."""
+    rows, dim = 2 ** 24 + 3, 3
+    g = torch.Generator(device="cuda").manual_seed(5)
+    x = torch.randn(rows, dim, generator=g, device="cuda").to(dtype)
+    w = torch.rand(dim, generator=g, device="cuda") + 0.5
+    s = x.double()
+    want = s / (s.pow(2).mean(-1, keepdim=True) + 1e-5).sqrt() * w.double()
+    top = float(want.abs().max())
+    y, _ = ssm.rms_add_fwd(x, w, y=nan((rows, dim), dtype))
+    tol = 1e-5 * top + (ref.U * want.abs() if dtype == BF16 else 0.0)
+    assert bool(((y.double() - want).abs() <= tol).all())
+    q, scale, _ = ssm.rms_add_q8_fwd(x, w, q=nan((rows, dim), E4M3), scale=nan((rows, 1), F32))
+    amax = want.abs().amax(-1, keepdim=True)
+    assert bool(((scale.double() * 448 - amax).abs() <= 1e-6 * amax).all())
+    # Half a step of e4m3: 2^-4 of a value, 2^-10 of the scale near zero.
+    err = (q.double() * scale.double() - want).abs()
+    assert bool((err <= (want.abs() / 16).maximum(scale.double() * 2.0 ** -10) * (1 + 1e-5) + 1e-6 * amax).all())
+
+
+def test_dw_of_columns_past_2_28():
+    """dw of more columns than a launch of its sum has threads for."""
+    dim = 2 ** 28 + 70
+    g = torch.Generator(device="cuda").manual_seed(6)
+    s, dy = (torch.randn(1, dim, generator=g, device="cuda", dtype=BF16) for _ in range(2))
+    w = torch.ones(dim, device="cuda")
+    dw = nan((dim,), F32)
+    ssm.rms_add_bwd(dy, s, w, dw=dw)
+    total = sum(float(part.double().pow(2).sum()) for part in s[0].split(1 << 24))
+    rstd = 1 / (total / dim + 1e-5) ** 0.5
+    for lo in range(0, dim, 1 << 24):
+        want = dy[0, lo:lo + (1 << 24)].double() * s[0, lo:lo + (1 << 24)].double() * rstd
+        assert bool(((dw[lo:lo + (1 << 24)].double() - want).abs() <= 1e-5 * want.abs().max()).all()), lo
