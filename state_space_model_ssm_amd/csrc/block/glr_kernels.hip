@@ -112,6 +112,10 @@ struct Place {
   bool many;            // channel blocks: at least 64, so that few tiles of each are in flight
 };
 
+// Workgroups along x of a larger launch: fewer than 2^32 threads fit an axis.
+// Past the last tile they have none (pos is not below tiles).
+constexpr unsigned kGridWidth = 1u << 20;
+
 constexpr int kGroup = 16;                // tiles between two published states
 constexpr unsigned kMissing = 0xffffffffu;  // a word not yet published
 constexpr int kMostPolls = 1 << 22;       // some seconds: a wait that long would be a fault, and ends in NaN
@@ -122,7 +126,7 @@ constexpr int kMostPolls = 1 << 22;       // some seconds: a wait that long woul
 // 206 us against 172 for the forward of 4 x 4096 x 5120.
 template <int C, bool REVERSE>
 __device__ __forceinline__ Place place(int64_t dim, int64_t seqlen, int64_t batch, const GlrChain &chain, unsigned &lds) {
-  unsigned id = blockIdx.x;
+  unsigned id = blockIdx.y * kGridWidth + blockIdx.x;
   const int tiles = static_cast<int>((seqlen + T * kSubs - 1) / (T * kSubs));
   const unsigned ct = static_cast<unsigned>((dim + kLanes * C - 1) / (kLanes * C)), rows = static_cast<unsigned>(batch) * ct;
   // Each round of ids begins a set later: workgroups go to the XCDs in turn, and
@@ -410,15 +414,17 @@ __device__ __forceinline__ void join(Scratch &lds, const GlrChain &chain, const 
 
 // All words missing, and the counters at 0.
 __global__ void __launch_bounds__(256) glr_clear_kernel(uint4 *words, int64_t n, unsigned *counter) {
-  const int64_t id = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  if (id < n) words[id] = make_uint4(kMissing, kMissing, kMissing, kMissing);
-  if (id < kGlrSets) counter[id * (kGlrCounterBytes / 4)] = 0;
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  for (int64_t id = first; id < n; id += static_cast<int64_t>(gridDim.x) * 256)
+    words[id] = make_uint4(kMissing, kMissing, kMissing, kMissing);
+  if (first < kGlrSets) counter[first * (kGlrCounterBytes / 4)] = 0;
 }
 
 template <typename Tin, typename Tout, int C>
 __global__ void __launch_bounds__(256, 4) glr_fwd_kernel(const GlrParams p) {
   __shared__ __align__(16) Scratch lds;
   const Place w = place<C, false>(p.dim, p.seqlen, p.batch, p.chain, lds.number);
+  if (w.pos >= w.tiles) return;
   typename Raw<Tin, C>::type rx[T], rrec[T], rinp[T];
   load<Tin, C>(p.rec, w, w.k, rrec);
   load<Tin, C>(p.inp, w, w.k, rinp);
@@ -510,6 +516,7 @@ __global__ void __launch_bounds__(256, 3) glr_bwd_kernel(const GlrBwdParams p) {
   __shared__ __align__(16) Scratch lds;
   typedef typename Raw<Tin, C>::type raw;
   const Place w = place<C, true>(p.dim, p.seqlen, p.batch, p.chain, lds.number);
+  if (w.pos >= w.tiles) return;
   raw rec[T], dy[T], x[T], inp[T];
   load<Tin, C>(p.rec, w, w.k, rec);
   load<Tin, C>(p.dy, w, w.k, dy);
@@ -651,28 +658,38 @@ __global__ void __launch_bounds__(1024) glr_sum_kernel(const float *part, float 
 
 // An empty sequence: the state passes through.
 __global__ void __launch_bounds__(256) glr_pass_kernel(const float *from, float *to, int64_t n) {
-  const int64_t id = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  if (id < n) to[id] = from != nullptr ? from[id] : 0.0f;
+  for (int64_t id = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; id < n; id += static_cast<int64_t>(gridDim.x) * 256)
+    to[id] = from != nullptr ? from[id] : 0.0f;
 }
 
 template <typename Tin, typename Tout>
 __global__ void __launch_bounds__(256) glr_step_kernel(const GlrParams p) {
-  const int64_t id = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  if (id >= p.batch * p.dim) return;
-  float a, u;
-  gates(ld(static_cast<const Tin *>(p.x), id), ld(static_cast<const Tin *>(p.rec), id),
-        ld(static_cast<const Tin *>(p.inp), id), p.A[id % p.dim], a, u);
-  const float h = fmaf(a, p.h0[id], u);
-  p.h_last[id] = h;
-  st(static_cast<Tout *>(p.y), id, h);
+  const int64_t n = p.batch * p.dim;
+  for (int64_t id = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; id < n; id += static_cast<int64_t>(gridDim.x) * 256) {
+    float a, u;
+    gates(ld(static_cast<const Tin *>(p.x), id), ld(static_cast<const Tin *>(p.rec), id),
+          ld(static_cast<const Tin *>(p.inp), id), p.A[id % p.dim], a, u);
+    const float h = fmaf(a, p.h0[id], u);
+    p.h_last[id] = h;
+    st(static_cast<Tout *>(p.y), id, h);
+  }
 }
 
-dim3 blocks(int64_t n, int64_t per) { return dim3(static_cast<uint32_t>((n + per - 1) / per)); }
+// Workgroups for n items, `per` each; past 65536 they walk (see kGridWidth).
+dim3 blocks(int64_t n, int64_t per) {
+  const int64_t all = (n + per - 1) / per;
+  return dim3(static_cast<uint32_t>(all < 65536 ? all : 65536));
+}
 
 // Tiles of all sequences, in workgroups.
 template <int C>
 int64_t all_tiles(int64_t batch, int64_t seqlen, int64_t dim) {
   return batch * ((dim + kLanes * C - 1) / (kLanes * C)) * ((seqlen + T * kSubs - 1) / (T * kSubs));
+}
+
+dim3 tile_grid(int64_t n) {
+  if (n <= kGridWidth) return dim3(static_cast<uint32_t>(n));
+  return dim3(kGridWidth, static_cast<uint32_t>((n + kGridWidth - 1) / kGridWidth));
 }
 
 void clear(const GlrChain &chain, int64_t seqlen, hipStream_t s) {
@@ -686,7 +703,7 @@ hipError_t run_fwd(const GlrParams &p, hipStream_t s) {
   const int64_t n = all_tiles<C>(p.batch, p.seqlen, p.dim);
   if (n > 0x7fffffff) return hipErrorInvalidValue;
   clear(p.chain, p.seqlen, s);
-  hipLaunchKernelGGL((glr_fwd_kernel<Tin, Tout, C>), dim3(static_cast<uint32_t>(n)), dim3(256), 0, s, p);
+  hipLaunchKernelGGL((glr_fwd_kernel<Tin, Tout, C>), tile_grid(n), dim3(256), 0, s, p);
   return hipGetLastError();
 }
 
@@ -695,7 +712,7 @@ hipError_t run_bwd(const GlrBwdParams &p, hipStream_t s) {
   const int64_t n = all_tiles<C>(p.batch, p.seqlen, p.dim);
   if (n > 0x7fffffff) return hipErrorInvalidValue;
   clear(p.chain, p.seqlen, s);
-  hipLaunchKernelGGL((glr_bwd_kernel<Tin, C>), dim3(static_cast<uint32_t>(n)), dim3(256), 0, s, p);
+  hipLaunchKernelGGL((glr_bwd_kernel<Tin, C>), tile_grid(n), dim3(256), 0, s, p);
   return hipGetLastError();
 }
 

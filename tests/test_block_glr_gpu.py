@@ -216,3 +216,57 @@ def test_offsets_past_32_bits():
     dx2, drec2, dinp2, _, _ = ssm.glr_bwd(tail, tail, tail, A, st[:, 262144 // 16:].contiguous(), tail)
     for a, b in ((dx, dx2), (drec, drec2), (dinp, dinp2)):
         ref.assert_close(a[:, 262144:], ref.f64(b), 2 * ref.storage_tol(ref.f64(b), BF16), "gradient")
+
+
+@pytest.mark.parametrize("batch,L", [(2 ** 24 + 5, 1), (2 ** 23 + 3, 129)])
+def test_tiles_past_2_24(batch, L):
+    """More tiles than a launch has workgroups along one axis, of one tile per row and of two."""
+    g = torch.Generator(device="cuda").manual_seed(L)
+    x, rec, dy = (torch.randn(batch, L, 1, generator=g, device="cuda") for _ in range(3))
+    A = torch.tensor([-0.3], device="cuda")
+    h0 = torch.randn(batch, 1, generator=g, device="cuda")
+    y, hl, st = ssm.glr_fwd(x, rec, x, A, h0=h0, return_states=True, y=nan(x.shape, F32), h_last=nan(h0.shape, F32))
+    out = {k: nan(x.shape, F32) for k in ("dx", "drec", "dinp")} | {"dh0": nan(h0.shape, F32)}
+    ssm.glr_bwd(x, rec, x, A, st, dy, out=out)
+
+    def gates(t):
+        r, i = torch.sigmoid(rec[:, t].double()), torch.sigmoid(x[:, t].double())
+        a = torch.exp(A.double() * r)
+        return a, torch.sqrt(-torch.expm1(2 * A.double() * r)), i
+
+    def close(got, want):
+        return bool(((got.double() - want).abs() <= 1e-5 * want.abs().max()).all())
+
+    h = h0.double()
+    for t in range(L):
+        a, b, i = gates(t)
+        h = a * h + b * i * x[:, t].double()
+        assert close(y[:, t], h), t
+    assert close(hl, h)
+    carry = torch.zeros_like(h)
+    for t in range(L - 1, -1, -1):
+        a, b, i = gates(t)
+        before = h0.double() if t == 0 else y[:, t - 1].double()
+        v, d = x[:, t].double(), dy[:, t].double() + carry
+        carry = a * d
+        w = d * (a * before - a * a / b * i * v)
+        r = torch.log(a) / A.double()
+        assert close(out["dx"][:, t], d * b * i) and close(out["dinp"][:, t], d * b * v * i * (1 - i)), t
+        assert close(out["drec"][:, t], w * A.double() * r * (1 - r)), t
+    assert close(out["dh0"], carry)
+
+
+def test_steps_and_empty_sequences_past_2_32_values():
+    batch, dim = 2 ** 22 + 1, 1024
+    x = torch.empty(batch, dim, device="cuda", dtype=BF16).normal_(generator=torch.Generator(device="cuda").manual_seed(3))
+    h = torch.ones(batch, dim, device="cuda")
+    A = -torch.rand(dim, device="cuda")
+    y, new = ssm.glr_step(x, x, x, A, h)
+    for rows in (slice(0, 64), slice(batch - 64, batch)):
+        part = x[rows].contiguous()
+        want, state = ssm.glr_step(part, part, part, A, torch.ones(64, dim, device="cuda"))
+        assert torch.equal(y[rows], want) and torch.equal(new[rows], state)
+    del x, y
+    empty = torch.empty(batch, 0, dim, device="cuda")
+    _, last = ssm.glr_fwd(empty, empty, empty, A, h0=h, h_last=nan((batch, dim), F32))
+    assert torch.equal(last[-64:], h[-64:]) and torch.equal(last[:64], h[:64])
