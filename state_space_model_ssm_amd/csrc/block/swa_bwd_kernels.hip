@@ -430,7 +430,10 @@ SwaBwdPlan swa_bwd_plan(int64_t batch, int64_t seqlen, int64_t nheads, int64_t n
   const int64_t pairs = ((seqlen + 31) / 32 - 2 * ((window + 127 + kTile - 1) / kTile)) * group;
   if (sinks > 0 && pairs > 0) {
     plan.far_blocks = static_cast<unsigned>((sinks + 31) / 32);
-    plan.far_chunks = static_cast<unsigned>((pairs + 23) / 24);
+    // No more than 2048 workgroups in all, or one per block: every chunk has
+    // terms of its own, which with thousands of sinks would grow as sinks x seqlen.
+    const int64_t rows = batch > 0 ? batch * nkv : 1, most = 2048 / (rows * plan.far_blocks), chunks = (pairs + 23) / 24;
+    plan.far_chunks = static_cast<unsigned>(chunks < most ? chunks : most > 1 ? most : 1);
   }
   const int64_t sink_blocks = plan.far_blocks > 0 ? (sinks + 127) / 128 : 0;
   plan.sum_blocks = static_cast<unsigned>(slices > 1 ? blocks : sink_blocks);

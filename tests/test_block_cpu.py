@@ -257,3 +257,17 @@ def test_the_float64_forms_catch_planted_mistakes():
     table = ref.e4m3_values()
     assert len(table) == 253 and table.max() == 448 and table[table > 0].min() == 2.0 ** -9
     assert set(torch.arange(256, dtype=torch.uint8).view(torch.float8_e4m3fn).float().nan_to_num(0).tolist()) == set(table.tolist())
+
+
+@pytest.mark.parametrize("batch,seqlen,nheads,nkv,headdim,sinks", [(1, 65536, 32, 8, 128, 8192), (1, 1 << 20, 1, 1, 64, 1 << 19),
+                                                                   (4, 8192, 16, 16, 64, 4096)])
+def test_workspace_of_many_sinks(batch, seqlen, nheads, nkv, headdim, sinks):
+    """Terms of the sinks' gradients: at most 2048 workgroups' (2 x 32 x headdim floats each) or one per 32 sinks, beside
+    two floats per query and head and the gradients of the first blocks of 128 keys."""
+    q, k = nheads * headdim, nkv * headdim
+    sizes = dict(seqlen=seqlen, nheads=nheads, nkv=nkv, headdim=headdim, window=1024, sinks=sinks, q_batch=seqlen * q,
+                 q_token=q, k_batch=seqlen * k, k_token=k, v_batch=seqlen * k, v_token=k)
+    assert ssm.swa_bwd_workspace_size(swa(batch=0, **sizes)) == 0
+    need = ssm.swa_bwd_workspace_size(swa(batch=batch, **sizes))
+    terms = max(2048, batch * nkv * sinks // 32) * 2 * 32 * headdim * 4
+    assert need <= 2 * batch * nheads * seqlen * 4 + batch * nkv * seqlen * headdim * 8 + terms + 4096

@@ -303,3 +303,16 @@ def test_slots_past_2_31_elements_of_one_head(d):
         assert torch.equal(kc[0, 0, -tail:].cpu(), kt) and torch.equal(vc[0, 0, -tail:].cpu(), vt), at
         for cache in (kc, vc):
             assert all(bool((part == -16).all()) for part in cache[0, 0, :-tail].split(1 << 20))
+
+
+def test_many_sinks():
+    """More (sink, later query) pairs than workgroups of their own: each takes a longer turn."""
+    B, L, H, window, sinks = 16, 2600, 8, 40, 640
+    q, k, v, dy = make(B, L, H, 1, 64, 14)
+    c, kw = [t.cuda() for t in (q, k, v)], dict(window=window, sinks=sinks)
+    y, lse = ssm.swa_fwd(*c, **kw)
+    got = dict(zip(("dq", "dk", "dv"), ssm.swa_bwd(*c, y, lse, dy.cuda(), **kw)))
+    row = slice(B - 1, B)
+    want, tol = ref.swa(q[row], k[row], v[row], window, sinks, dy=dy[row])
+    for n, t in got.items():
+        ref.assert_close(t[row], want[n], tol[n], n)
