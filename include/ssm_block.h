@@ -174,7 +174,9 @@ SSM_API int ssm_rms_add_bwd(const void *dy, const void *s, const float *w, const
  * k and v (heads of a token are adjacent: head stride headdim); the batch and
  * token strides must be multiples of 8 and q, k, v 16-byte aligned, and so
  * must y, dy, dq, dk and dv, which are dense; token strides are at most 2^24.
- * scale multiplies q.k.  seqlen <= 2^30; batch * nheads <= 65535.
+ * scale multiplies q.k.  seqlen <= 2^30, nheads and batch * nheads <= 65535,
+ * batch * nheads * seqlen < 2^31 (seqlen counted in whole blocks of 128), and
+ * in the backward batch * nkv * sinks < 2^27.
  */
 typedef struct {
   int64_t batch, seqlen, nheads, nkv, headdim;

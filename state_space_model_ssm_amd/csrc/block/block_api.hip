@@ -204,8 +204,11 @@ int check_swa(const ssm_swa_dims_t *d, bool step) {
   if (d->seqlen > kMax || d->window > kMax || d->sinks > kMax)
     return fail(SSM_ERR_UNSUPPORTED, "seqlen, window and sinks must be at most 2^30");
   const int64_t rows = mul(d->batch, d->nheads);
-  if (rows < 0 || rows > 65535 || mul(mul(rows, d->seqlen), 256) < 0)
-    return fail(SSM_ERR_UNSUPPORTED, "batch * nheads must be at most 65535");
+  if (rows < 0 || rows > 65535 || d->nheads > 65535)
+    return fail(SSM_ERR_UNSUPPORTED, "nheads and batch * nheads must be at most 65535");
+  // A workgroup has 128 (query, head) pairs, queries in blocks of 32, 64 or 128.
+  if (rows * ceil_div(d->seqlen, 128) > ssmb::kMaxGroups)
+    return fail(SSM_ERR_UNSUPPORTED, "batch * nheads * seqlen must be below 2^31");
   const int64_t strides[] = {d->q_batch, d->q_token, d->k_batch, d->k_token, d->v_batch, d->v_token};
   for (const int64_t s : strides)
     if (s < 0 || s % 8 != 0 || s > (int64_t{1} << 40))
@@ -254,6 +257,16 @@ ssmb::SwaParams swa_params(const ssm_swa_dims_t &d, const void *q, const void *k
 
 ssmb::SwaBwdPlan swa_plan(const ssm_swa_dims_t &d) {
   return ssmb::swa_bwd_plan(d.batch, d.seqlen, d.nheads, d.nkv, d.headdim, d.window, d.sinks);
+}
+
+int check_swa_bwd(const ssm_swa_dims_t *d) {
+  const int rc = check_swa(d, false);
+  if (rc != SSM_OK) return rc;
+  const ssmb::SwaBwdPlan plan = swa_plan(*d);
+  const int64_t heads = d->batch * d->nkv, sums = int64_t{plan.sum_blocks} * 4 * (d->headdim / 32);
+  if (plan.items * heads > ssmb::kMaxGroups || sums * heads > ssmb::kMaxGroups)
+    return fail(SSM_ERR_UNSUPPORTED, "batch * nkv * sinks is too large for the backward");
+  return SSM_OK;
 }
 
 // log2(e) lse and dy.y of every query, then the terms of dk and dv.
@@ -498,7 +511,7 @@ int ssm_swa_fwd(const void *q, const void *k, const void *v, const int32_t *leng
 
 int ssm_swa_bwd_workspace_size(const ssm_swa_dims_t *dims, size_t *bytes) {
   if (!bytes) return fail(SSM_ERR_NULL, "bytes is NULL");
-  const int rc = check_swa(dims, false);
+  const int rc = check_swa_bwd(dims);
   if (rc != SSM_OK) return rc;
   *bytes = swa_bwd_workspace(*dims);
   return ok();
@@ -506,7 +519,7 @@ int ssm_swa_bwd_workspace_size(const ssm_swa_dims_t *dims, size_t *bytes) {
 
 int ssm_swa_bwd(const void *q, const void *k, const void *v, const int32_t *lengths, const void *y, const float *lse,
                 const void *dy, void *dq, void *dk, void *dv, const ssm_swa_dims_t *dims, void *stream) {
-  int rc = check_swa(dims, false);
+  int rc = check_swa_bwd(dims);
   if (rc != SSM_OK) return rc;
   const ssm_swa_dims_t &d = *dims;
   const size_t rows = static_cast<size_t>(d.batch) * d.seqlen;
@@ -599,9 +612,7 @@ int ssm_swa_fill(const void *k, const void *v, const int32_t *lengths, void *k_c
   const ssm_swa_dims_t &d = *dims;
   if (d.sinks + d.window > (int64_t{1} << 30))
     return fail(SSM_ERR_UNSUPPORTED, "sinks + window must be at most 2^30");
-  const int64_t lanes = mul(mul(d.batch, d.nkv), (d.sinks + d.window) * (d.headdim / 8));
-  if (lanes < 0 || lanes / 256 >= kMaxGrid) return fail(SSM_ERR_UNSUPPORTED, "the cache exceeds the grid limit");
-  const size_t cache = static_cast<size_t>(lanes) * 16;
+  const size_t cache = static_cast<size_t>(d.batch) * d.nkv * (d.sinks + d.window) * d.headdim * 2;
   const Arg ins[] = {{"k", k, span(d, d.k_batch, d.k_token, d.nkv), 16, true},
                      {"v", v, span(d, d.v_batch, d.v_token, d.nkv), 16, true},
                      {"lengths", lengths, static_cast<size_t>(d.batch) * 4, 4, false}};

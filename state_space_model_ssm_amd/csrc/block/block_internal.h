@@ -8,6 +8,9 @@
 
 namespace ssmb {
 
+// Workgroups of 256 that a launch may have along an axis: fewer than 2^32 threads.
+constexpr int64_t kMaxGroups = (int64_t{1} << 24) - 1;
+
 constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ float ld(const float *p, int64_t i) { return p[i]; }

@@ -395,7 +395,6 @@ hipError_t launch_d(const SwaParams &p, const SwaBwdPlan &plan, hipStream_t s) {
   const int hw = group % 4 == 0 ? 4 : group % 2 == 0 ? 2 : 1;
   const int64_t qspan = 32 * (4 / hw), qtiles = (p.seqlen + qspan - 1) / qspan;
   const int64_t n = qtiles * (group / hw) * p.nkv * p.batch, items = plan.items * p.batch * p.nkv;
-  if (n > 0x7fffffff || items > 0x7fffffff) return hipErrorInvalidValue;
   hipLaunchKernelGGL((swa_dq_kernel<D>), dim3(static_cast<uint32_t>(n)), dim3(256), 0, s, p, hw,
                      static_cast<unsigned>(qtiles), static_cast<unsigned>(n));
   hipLaunchKernelGGL((swa_dkv_kernel<D>), dim3(static_cast<uint32_t>(items)), dim3(256), 0, s, p, plan,

@@ -226,7 +226,6 @@ hipError_t launch_swa_fwd(const SwaParams &p, hipStream_t s) {
   const int hw = group % 4 == 0 ? 4 : group % 2 == 0 ? 2 : 1;
   const int64_t qspan = 32 * (4 / hw), qtiles = (p.seqlen + qspan - 1) / qspan;
   const int64_t n = qtiles * (group / hw) * p.nkv * p.batch;
-  if (n > 0x7fffffff) return hipErrorInvalidValue;
   const dim3 g(static_cast<uint32_t>(n)), t(256);
   const unsigned qt = static_cast<unsigned>(qtiles), un = static_cast<unsigned>(n);
   if (p.headdim == 64) hipLaunchKernelGGL((swa_fwd_kernel<64>), g, t, 0, s, p, hw, qt, un);

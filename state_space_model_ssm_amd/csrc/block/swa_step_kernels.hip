@@ -160,24 +160,24 @@ __global__ void __launch_bounds__(D) swa_join_kernel(const SwaStepParams p, int 
   st(p.y, head * D + threadIdx.x, all == 0.0f ? 0.0f : acc / all);
 }
 
-// One thread per 16 bytes of a slot: slot s of a row of length n holds
-// position s below the sinks, else the largest position p < n with
+// A thread takes 16 bytes of a slot at a time: slot s of a row of length n
+// holds position s below the sinks, else the largest position p < n with
 // (p - sinks) mod window = s - sinks.
 __global__ void __launch_bounds__(256) swa_fill_kernel(const SwaParams p, uint16_t *kc, uint16_t *vc) {
-  const int64_t chunks = p.headdim / 8, slots = p.sinks + p.window;
-  const int64_t id = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  if (id >= p.batch * p.nkv * slots * chunks) return;
-  const int64_t e = id % chunks, s = id / chunks % slots, c = id / chunks / slots % p.nkv;
-  const int64_t b = id / chunks / slots / p.nkv;
-  int64_t n = p.lengths != nullptr ? p.lengths[b] : p.seqlen;
-  n = n < 0 ? 0 : n > p.seqlen ? p.seqlen : n;
-  int64_t pos = s;
-  if (s >= n) return;
-  if (s >= p.sinks) pos += (n - 1 - s) / p.window * p.window;
-  const uint4 k = *reinterpret_cast<const uint4 *>(p.k + b * p.k_batch + pos * p.k_token + c * p.headdim + e * 8);
-  const uint4 v = *reinterpret_cast<const uint4 *>(p.v + b * p.v_batch + pos * p.v_token + c * p.headdim + e * 8);
-  reinterpret_cast<uint4 *>(kc)[id] = k;
-  reinterpret_cast<uint4 *>(vc)[id] = v;
+  const int64_t chunks = p.headdim / 8, slots = p.sinks + p.window, all = p.batch * p.nkv * slots * chunks;
+  for (int64_t id = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; id < all; id += static_cast<int64_t>(gridDim.x) * 256) {
+    const int64_t e = id % chunks, s = id / chunks % slots, c = id / chunks / slots % p.nkv;
+    const int64_t b = id / chunks / slots / p.nkv;
+    int64_t n = p.lengths != nullptr ? p.lengths[b] : p.seqlen;
+    n = n < 0 ? 0 : n > p.seqlen ? p.seqlen : n;
+    int64_t pos = s;
+    if (s >= n) continue;
+    if (s >= p.sinks) pos += (n - 1 - s) / p.window * p.window;
+    const uint4 k = *reinterpret_cast<const uint4 *>(p.k + b * p.k_batch + pos * p.k_token + c * p.headdim + e * 8);
+    const uint4 v = *reinterpret_cast<const uint4 *>(p.v + b * p.v_batch + pos * p.v_token + c * p.headdim + e * 8);
+    reinterpret_cast<uint4 *>(kc)[id] = k;
+    reinterpret_cast<uint4 *>(vc)[id] = v;
+  }
 }
 
 }  // namespace
@@ -207,7 +207,8 @@ hipError_t launch_swa_step(const SwaStepParams &p, int splits, hipStream_t s) {
 hipError_t launch_swa_fill(const SwaParams &p, uint16_t *kc, uint16_t *vc, hipStream_t s) {
   const int64_t n = p.batch * p.nkv * (p.sinks + p.window) * (p.headdim / 8);
   if (n == 0) return hipSuccess;
-  hipLaunchKernelGGL(swa_fill_kernel, dim3(static_cast<uint32_t>((n + 255) / 256)), dim3(256), 0, s, p, kc, vc);
+  const int64_t groups = (n + 255) / 256 < kMaxGroups ? (n + 255) / 256 : kMaxGroups;
+  hipLaunchKernelGGL(swa_fill_kernel, dim3(static_cast<uint32_t>(groups)), dim3(256), 0, s, p, kc, vc);
   return hipGetLastError();
 }
 

@@ -271,3 +271,16 @@ def test_workspace_of_many_sinks(batch, seqlen, nheads, nkv, headdim, sinks):
     need = ssm.swa_bwd_workspace_size(swa(batch=batch, **sizes))
     terms = max(2048, batch * nkv * sinks // 32) * 2 * 32 * headdim * 4
     assert need <= 2 * batch * nheads * seqlen * 4 + batch * nkv * seqlen * headdim * 8 + terms + 4096
+
+
+@needs_no_gpu
+def test_swa_launch_limits():
+    """Requests of more workgroups than a launch can have are refused, and the plan of no rows is made at once."""
+    long = dict(batch=2, seqlen=1 << 28, q_batch=1 << 36, k_batch=1 << 35, v_batch=1 << 35)
+    for name in ("ssm_swa_fwd", "ssm_swa_bwd"):
+        assert call(name, **long) == UNSUPPORTED and "2^31" in ssm.block_last_error()
+        assert call(name, batch=0, nheads=1 << 40, nkv=1) == UNSUPPORTED
+    one = dict(batch=1, seqlen=1 << 29, nheads=1, nkv=1, q_batch=1 << 35, q_token=64, k_batch=1 << 35, k_token=64,
+               v_batch=1 << 35, v_token=64)
+    assert call("ssm_swa_bwd", **one, sinks=1 << 29) == UNSUPPORTED and "sinks" in ssm.block_last_error()
+    assert ssm.swa_bwd_workspace_size(swa(**one, sinks=1 << 20)) > 0

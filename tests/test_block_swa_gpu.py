@@ -316,3 +316,17 @@ def test_many_sinks():
     want, tol = ref.swa(q[row], k[row], v[row], window, sinks, dy=dy[row])
     for n, t in got.items():
         ref.assert_close(t[row], want[n], tol[n], n)
+
+
+def test_fill_past_2_32_pieces():
+    """Caches of more 16-byte pieces than a launch has threads: the prompts of the last rows arrive."""
+    B, KV, d, slots, L = 16, 8, 128, 2 ** 21 + 8, 9
+    k, v = (torch.randn(B, L, KV, d, device="cuda").to(BF16) for _ in range(2))
+    kc, vc = (torch.empty(B, KV, slots, d, dtype=BF16, device="cuda") for _ in range(2))
+    for cache in (kc, vc):
+        cache[:, :, :L + 1].zero_()
+    ssm.swa_fill(k, v, kc, vc, sinks=4)
+    for cache, new in ((kc, k), (vc, v)):
+        assert torch.equal(cache[:, :, :L], new.transpose(1, 2)) and not cache[:, :, L].any()
+    del kc, vc, cache
+    torch.cuda.empty_cache()   # 128 GiB
