@@ -21,7 +21,7 @@
  *   - Pointers must be aligned to their element size, and more where an entry
  *     point says so; otherwise SSM_ERR_ALIGN.
  *   - Outputs must not overlap inputs or each other, except where an entry
- *     point says so; otherwise SSM_ERR_SHAPE.
+ *     point says so, and the workspace none of them; otherwise SSM_ERR_SHAPE.
  *   - Unsupported sizes return SSM_ERR_UNSUPPORTED; there is no fallback path.
  *   - Indices and offsets are 64-bit throughout.
  *   - The same inputs give the same bits on every call: no result depends on

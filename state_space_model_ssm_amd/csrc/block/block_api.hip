@@ -85,11 +85,18 @@ int check_args(const Arg (&ins)[NI], const Arg (&outs)[NO], const void *const (&
   return SSM_OK;
 }
 
-int check_workspace(const void *ws, size_t have, size_t need) {
+// The workspace, last of `ins`: large enough, aligned, and none of the bytes
+// that are used lies in an input (check_args() has compared it with outputs).
+template <size_t NI>
+int check_workspace(const Arg (&ins)[NI], size_t need) {
+  Arg ws = ins[NI - 1];
   if (need == 0) return SSM_OK;
-  if (!ws || have < need)
-    return fail(SSM_ERR_WORKSPACE, "workspace of %zu bytes is smaller than the %zu required", ws ? have : size_t{0}, need);
-  if (!aligned(ws, 256)) return fail(SSM_ERR_ALIGN, "workspace must be aligned to 256 bytes");
+  if (!ws.p || ws.bytes < need)
+    return fail(SSM_ERR_WORKSPACE, "workspace of %zu bytes is smaller than the %zu required", ws.bytes, need);
+  if (!aligned(ws.p, 256)) return fail(SSM_ERR_ALIGN, "workspace must be aligned to 256 bytes");
+  ws.bytes = need;
+  for (size_t k = 0; k + 1 < NI; ++k)
+    if (overlap(ws, ins[k])) return fail(SSM_ERR_SHAPE, "workspace overlaps %s", ins[k].name);
   return SSM_OK;
 }
 
@@ -326,7 +333,7 @@ int ssm_glr_fwd(const void *x, const void *rec, const void *inp, const float *A,
                       {"states", states, bd * ceil_div(d.seqlen, SSM_GLR_STATE_STEP) * 4, 4, false}};
   const void *const same[3][2] = {{nullptr, nullptr}, {h0, nullptr}, {nullptr, nullptr}};
   rc = check_args(ins, outs, same);
-  if (rc == SSM_OK) rc = check_workspace(d.workspace, d.workspace_bytes, glr_workspace(d));
+  if (rc == SSM_OK) rc = check_workspace(ins, glr_workspace(d));
   if (rc != SSM_OK) return rc;
   if (bd == 0 || (d.seqlen == 0 && h_last == nullptr)) return ok();
   ssmb::GlrParams p{};
@@ -413,7 +420,7 @@ int ssm_glr_bwd(const void *x, const void *rec, const void *inp, const float *A,
                       {"dh0", dh0, bd * 4, 4, false}};
   const void *const same[5][2] = {};
   rc = check_args(ins, outs, same);
-  if (rc == SSM_OK) rc = check_workspace(d.workspace, d.workspace_bytes, need);
+  if (rc == SSM_OK) rc = check_workspace(ins, need);
   if (rc != SSM_OK) return rc;
   if (d.dim == 0) return ok();
   ssmb::GlrBwdParams p{};
@@ -470,7 +477,7 @@ int ssm_rms_add_bwd(const void *dy, const void *s, const float *w, const void *d
   const Arg outs[] = {{"dx", dx, n * ei, ei, true}, {"dw", dw, static_cast<size_t>(d.dim) * 4, 4, false}};
   const void *const same[2][2] = {{dy, dres}, {nullptr, nullptr}};
   rc = check_args(ins, outs, same);
-  if (rc == SSM_OK && dw != nullptr) rc = check_workspace(d.workspace, d.workspace_bytes, rms_bwd_workspace(d));
+  if (rc == SSM_OK && dw != nullptr) rc = check_workspace(ins, rms_bwd_workspace(d));
   if (rc != SSM_OK) return rc;
   if (d.rows == 0 && dw == nullptr) return ok();
   ssmb::RmsBwdParams p{};
@@ -535,7 +542,7 @@ int ssm_swa_bwd(const void *q, const void *k, const void *v, const int32_t *leng
   const Arg outs[] = {{"dq", dq, nq, 16, true}, {"dk", dk, nk, 16, true}, {"dv", dv, nk, 16, true}};
   const void *const same[3][2] = {};
   rc = check_args(ins, outs, same);
-  if (rc == SSM_OK) rc = check_workspace(d.workspace, d.workspace_bytes, swa_bwd_workspace(d));
+  if (rc == SSM_OK) rc = check_workspace(ins, swa_bwd_workspace(d));
   if (rc != SSM_OK) return rc;
   if (rows == 0) return ok();
   ssmb::SwaParams p = swa_params(d, q, k, v, lengths);
@@ -579,7 +586,7 @@ int ssm_swa_step(const void *q, const void *k, const void *v, void *k_cache, voi
                       {"y", y, static_cast<size_t>(d.batch) * d.nheads * d.headdim * 2, 16, true}};
   const void *const same[3][2] = {};
   rc = check_args(ins, outs, same);
-  if (rc == SSM_OK) rc = check_workspace(d.workspace, d.workspace_bytes, swa_step_workspace(d));
+  if (rc == SSM_OK) rc = check_workspace(ins, swa_step_workspace(d));
   if (rc != SSM_OK) return rc;
   if (d.batch == 0) return ok();
   ssmb::SwaStepParams p{};

@@ -284,3 +284,25 @@ def test_swa_launch_limits():
                v_batch=1 << 35, v_token=64)
     assert call("ssm_swa_bwd", **one, sinks=1 << 29) == UNSUPPORTED and "sinks" in ssm.block_last_error()
     assert ssm.swa_bwd_workspace_size(swa(**one, sinks=1 << 20)) > 0
+
+
+@needs_no_gpu
+@pytest.mark.parametrize("name,inputs,kw", [
+    ("ssm_glr_fwd", (0, 1, 2, 3, 4, 5), dict(seqlen=300)), ("ssm_glr_bwd", (0, 1, 2, 3, 4, 5, 6, 7), dict(seqlen=300)),
+    ("ssm_rms_add_bwd", (0, 1, 2, 3), {}), ("ssm_swa_bwd", (0, 1, 2, 3, 4, 5, 6), {}),
+    ("ssm_swa_step", (0, 1, 2, 5), dict(window=5000))])
+def test_workspace_over_an_input(name, inputs, kw):
+    for k in inputs:
+        assert call(name, pointers={k: at(50) + 512}, workspace_bytes=1 << 30, **kw) == SHAPE, k
+        assert "workspace overlaps" in ssm.block_last_error()
+
+
+@needs_no_gpu
+def test_workspaces_a_byte_short():
+    """Of a sequence of several tiles, and of a step that several workgroups share."""
+    need = ssm.glr_workspace_size(glr(batch=1, seqlen=30000))
+    assert need > 0 and call("ssm_glr_fwd", batch=1, seqlen=30000, workspace_bytes=need - 1) == WORKSPACE
+    need = ssm.swa_step_workspace_size(swa(seqlen=1, window=5000))
+    assert need > 0 and call("ssm_swa_step", window=5000, workspace_bytes=need - 1) == WORKSPACE
+    assert call("ssm_swa_step", window=5000, workspace=None) == WORKSPACE
+    assert call("ssm_swa_step", window=5000, workspace=at(50) + 4) == ALIGN
