@@ -484,6 +484,10 @@ __global__ void __launch_bounds__(256, 4) glr_fwd_kernel(const GlrParams p) {
         end[c] = fmaf(a[j][c], cut ? 0.0f : end[c], u[j][c]);
       }
   }
+  // h_last may be h0: each wavefront has its h0 before the barrier that comes
+  // before the tile's summary, so before the last tile can write.
+#pragma unroll
+  for (int c = 0; c < C; ++c) forget(first[c]);
   join<C, false>(lds, p.chain, w, words, prod, end, first, start, last);
   if (p.states != nullptr) {
     const int64_t nstate = (p.seqlen + T - 1) / T, row = static_cast<int64_t>(w.k) * kSubs;

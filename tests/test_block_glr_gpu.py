@@ -270,3 +270,16 @@ def test_steps_and_empty_sequences_past_2_32_values():
     empty = torch.empty(batch, 0, dim, device="cuda")
     _, last = ssm.glr_fwd(empty, empty, empty, A, h0=h, h_last=nan((batch, dim), F32))
     assert torch.equal(last[-64:], h[-64:]) and torch.equal(last[:64], h[:64])
+
+
+@pytest.mark.parametrize("batch,L,dim,dtype", [(2, 300, 70, F32), (3, 300, 64, BF16), (1, 4097, 200, BF16), (2, 4097, 33, F32),
+                                               (4, 2500, 2100, BF16)])
+def test_state_in_place_over_several_tiles(batch, L, dim, dtype):
+    """h_last given as h0 itself: every tile of the first group reads h0, the last tile overwrites it."""
+    x, rec, inp, A, _, h0, _, reset = make(batch, L, dim, dtype, L + dim, True)
+    c = cuda(x, rec, inp, A)
+    for cut in (None, reset.cuda()):
+        want, last, states = ssm.glr_fwd(*c, h0=h0.cuda(), reset=cut, return_states=True)
+        state = h0.cuda()
+        got, same, st = ssm.glr_fwd(*c, h0=state, h_last=state, reset=cut, return_states=True)
+        assert same is state and torch.equal(state, last) and torch.equal(got, want) and torch.equal(st, states)
