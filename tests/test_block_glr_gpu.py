@@ -283,3 +283,19 @@ def test_state_in_place_over_several_tiles(batch, L, dim, dtype):
         state = h0.cuda()
         got, same, st = ssm.glr_fwd(*c, h0=state, h_last=state, reset=cut, return_states=True)
         assert same is state and torch.equal(state, last) and torch.equal(got, want) and torch.equal(st, states)
+
+
+@pytest.mark.parametrize("batch,L,dim,dtype", [(1, 2300, 67 * 32, F32), (3, 2100, 25 * 64, BF16), (2, 4200, 33 * 32 - 5, BF16)])
+def test_many_channel_blocks_over_several_groups_of_tiles(batch, L, dim, dtype):
+    """64 channel blocks and more, numbers of them that no 32 counters share evenly, two groups of tiles and more, resets."""
+    x, rec, inp, A, dy, h0, dh, _ = make(batch, L, dim, dtype, dim)
+    reset = (torch.rand(batch, L, generator=torch.Generator().manual_seed(L)) < 1 / 200).to(torch.uint8)
+    c = cuda(x, rec, inp, A, dy, h0, dh, reset)
+    y, hl, st = ssm.glr_fwd(*c[:4], h0=c[5], reset=c[7], return_states=True, y=nan(x.shape, dtype))
+    h, last, _ = ref.glr(x, rec, inp, A, h0, reset)
+    ref.assert_close(y, h, ref.storage_tol(h, dtype), "y")
+    ref.assert_close(hl, last, ref.storage_tol(h, F32), "h_last")
+    got = ssm.glr_bwd(*c[:4], st, c[4], dh_last=c[6], reset=c[7], out={"dx": nan(x.shape, dtype)})
+    want, size = ref.glr_bwd(x, rec, inp, A, dy, h0, reset, dh)
+    for k, t in zip(("dx", "drec", "dinp", "dA", "dh0"), got):
+        ref.assert_close(t, want[k], ref.storage_tol(want[k], t.dtype, size.get(k)), k)
