@@ -287,12 +287,13 @@ def rms_add_fwd(x, w, residual=None, *, eps: float = 1e-5, out_dtype=None, y=Non
     """Residual addition with RMS norm (``ssm_rms_add_fwd``) over the last
     axis: s = x + residual, y = s / sqrt(mean(s^2) + eps) * w.  x, residual:
     (..., dim), one dtype; w: (dim,) float32.  Returns ``(y, s)``; s has x's
-    dtype (x itself when there is no residual) and residual_out may be x or
-    residual, y may be x."""
+    dtype (x itself when there is no residual, a copy of it where y takes its
+    place) and residual_out may be x or residual, y may be x."""
     out_dt = x.dtype if out_dtype is None else out_dtype
     dims = _rms_dims(x, w, residual, eps, out_dt)
+    over = y is not None and y.data_ptr() == x.data_ptr()
     y = _out(y, x.shape, out_dt, x, "y", stream)
-    if residual is not None or residual_out is not None:
+    if residual is not None or residual_out is not None or over:
         residual_out = _out(residual_out, x.shape, x.dtype, x, "residual_out", stream)
     _check(block_lib().ssm_rms_add_fwd(_ptr(x), _ptr(residual), _ptr(w), _ptr(y), _ptr(residual_out),
                                        ctypes.byref(dims), _stream(stream)))

@@ -299,3 +299,13 @@ def test_dw_of_columns_past_2_28():
     for lo in range(0, dim, 1 << 24):
         want = dy[0, lo:lo + (1 << 24)].double() * s[0, lo:lo + (1 << 24)].double() * rstd
         assert bool(((dw[lo:lo + (1 << 24)].double() - want).abs() <= 1e-5 * want.abs().max()).all()), lo
+
+
+@pytest.mark.parametrize("dtype,dim", [(BF16, 1024), (F32, 1537), (F32, 3), (F32, 8200)])
+def test_in_place_without_a_residual_keeps_the_sum(dtype, dim):
+    x, _, w, _, _ = (t.cuda() for t in make(6, dim, dtype, 9))
+    want, same = ssm.rms_add_fwd(x, w)
+    assert same is x
+    a = x.clone()
+    y, s = ssm.rms_add_fwd(a, w, y=a)
+    assert y is a and torch.equal(y, want) and torch.equal(s, x)
