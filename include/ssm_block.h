@@ -210,9 +210,10 @@ SSM_API int ssm_swa_fwd(const void *q, const void *k, const void *v, const int32
  *   dq_t = scale sum_j ds_tj k_j, dk_j = scale sum ds_tj q_t, dv_j = sum p_tj dy_t
  * the last two over the queries and query heads that see j.
  *   dy, y, dq: (batch, seqlen, nheads, headdim); dk, dv: (batch, seqlen, nkv, headdim)
- * Rows at or past the length are not used and get zero gradients.  Unlike in
- * the forward, an infinity or NaN in a row below the length may also reach
- * gradients of rows that do not see it (as 0 times that value).
+ * Rows at or past the length are not used and get zero gradients.  An infinity
+ * or NaN in a key or value reaches the queries that see it, and through their
+ * gradients the keys and values that those see; one in a query or its dy, the
+ * keys and values that it sees.
  */
 SSM_API int ssm_swa_bwd_workspace_size(const ssm_swa_dims_t *dims, size_t *bytes);
 SSM_API int ssm_swa_bwd(const void *q, const void *k, const void *v, const int32_t *lengths, const void *y,

@@ -23,16 +23,108 @@
 // tokens, 16 heads of 128 on 4, window 1024, 143 and 200 us (900 and 650
 // TFLOP/s); 4 x 2048 tokens, 32 heads of 64 on 8, window 512, 91 and 96 us (660
 // and 630).
+#include <type_traits>
+
 #include "swa_tile.h"
 
 namespace ssmb {
 namespace {
 
+// What a workgroup of the dq kernel knows of its work, and a lane of its query.
+struct DqWork {
+  const uint16_t *k, *v;  // of the key head
+  int q0, wq0, len, tiles;
+  KeyRow keys;
+  float c2, lse2, delta;
+};
+
+// One pass over the keys: dq of the lane's query, and off, what dy.y is too
+// small by, since y is rounded: the weights' sum is 1, so sum_j ds_tj (of this
+// lane's half of the keys).  Returns whether a tile that some query sees in
+// part had a score that is not finite.  An infinity or NaN in a key makes every
+// score with it one, and 0 times it would reach the queries that do not see it:
+// SAFE keeps such elements out of the product, and gives a NaN to the queries
+// that do (whose ds is NaN or 0 there).
+template <int D, bool SAFE>
+__device__ __forceinline__ bool dq_pass(const SwaParams &p, const DqWork &w, u4 (&lds)[2][2][kTile * D / 8],
+                                        const bf8 (&q)[D / 16], const bf8 (&dy)[D / 16], f16v (&dq)[D / 32], float &off,
+                                        int tid) {
+  constexpr int NB = D / 32, NS = D / 16;
+  const int lane = tid & 63, half = lane >> 5, t = w.wq0 + (lane & 31);
+  const int window = static_cast<int>(p.window), sinks = static_cast<int>(p.sinks);
+  const Lanes at = lanes_of<D>(lane);
+  float even = 0.0f;  // NaN once a score was not finite
+  off = 0.0f;
+#pragma unroll
+  for (int db = 0; db < NB; ++db) dq[db] = f16v{};
+  auto start = [&](int i) {
+    load_keys<D, 256>(lds[i & 1][0], w.k, p.k_token, w.keys, i * kTile, w.len - 1, tid);
+    load_keys<D, 256>(lds[i & 1][1], w.v, p.v_token, w.keys, i * kTile, w.len - 1, tid);
+  };
+  start(0);
+  for (int i = 0; i < w.tiles; ++i) {
+    wait_tiles();
+    __syncthreads();  // tile i has landed, and nobody reads the other buffer any more
+    if (i + 1 < w.tiles) start(i + 1);
+    const int v0 = i * kTile, j0 = w.keys.key(v0), j1 = w.keys.key(v0 + kTile - 1);
+    const u4 *kt = lds[i & 1][0], *vt = lds[i & 1][1];
+    if (j0 > w.wq0 + 31 || (j1 <= w.wq0 - window && j0 >= sinks) || w.wq0 >= w.len) continue;
+    const bool whole = j1 <= w.wq0 && w.wq0 + 31 - j0 < window;
+    const Seen seen = seen_by(w.keys, t, v0, half, window, sinks);
+#pragma unroll
+    for (int blk = 0; blk < 2; ++blk) {
+      f16v s = {}, dp = {};
+#pragma unroll
+      for (int ks = 0; ks < NS; ++ks) {
+        s = mfma(row_operand<D>(kt, 32 * blk, ks, at), q[ks], s);
+        dp = mfma(row_operand<D>(vt, 32 * blk, ks, at), dy[ks], dp);
+      }
+      reads_ahead<2 * NS>();
+#pragma unroll
+      for (int r = 0; r < 16; ++r)
+        dp[r] = __builtin_amdgcn_exp2f(fmaf(s[r], w.c2, -w.lse2)) * (dp[r] - w.delta);
+      if (!whole) {
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          if constexpr (!SAFE) even = fmaf(s[r], 0.0f, even);
+          dp[r] = seen(32 * blk + d_row(r, 0)) ? dp[r] : 0.0f;
+        }
+        if constexpr (SAFE) {
+          bf8 vis[2];
+#pragma unroll
+          for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) vis[ks][e] = static_cast<__bf16>(seen(32 * blk + d_row(8 * ks + e, 0)) ? 1.0f : 0.0f);
+          add_not_finite<D, 2, true>(kt, 32 * blk, vis, dq, at);
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < 16; ++r) off += dp[r];
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) {
+        const bf8 dsk = as_operand(dp, ks), rest = left_over(dp, ks, dsk);
+#pragma unroll
+        for (int db = 0; db < NB; ++db) {
+          bf8 kc = col_operand<D>(kt, 32 * blk + 16 * ks, db, at);
+          if constexpr (SAFE) {
+            if (!whole) kc = only_finite(kc);
+          }
+          dq[db] = mfma(kc, dsk, dq[db]);
+          dq[db] = mfma(kc, rest, dq[db]);
+          if constexpr (SAFE) __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+    }
+  }
+  return even != 0.0f;
+}
+
 // dq; also log2(e) lse and dy.y of every query for the kernel below.
 template <int D>
-__global__ void __launch_bounds__(256, 2) swa_dq_kernel(const SwaParams p, int hw, unsigned qtiles, unsigned n) {
+__global__ void __launch_bounds__(256, D == 64 ? 3 : 2) swa_dq_kernel(const SwaParams p, int hw, unsigned qtiles, unsigned n) {
   constexpr int CH = D / 8, NB = D / 32, NS = D / 16;
   __shared__ __align__(16) u4 lds[2][2][kTile * CH];  // buffer, K or V
+  __shared__ int found;
   const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const unsigned nheads = static_cast<unsigned>(p.nheads), nkv = static_cast<unsigned>(p.nkv);
@@ -41,27 +133,27 @@ __global__ void __launch_bounds__(256, 2) swa_dq_kernel(const SwaParams p, int h
   const unsigned rest = id / qtiles, qt = uneven(p.window, p.seqlen) ? qtiles - 1 - id % qtiles : id % qtiles;
   const int64_t c = rest / (hb * batch), b = rest / hb % batch;
   const int64_t head = c * group + (rest % hb) * hw + wave % hw;
-  const int qspan = 32 * (4 / hw), q0 = static_cast<int>(qt) * qspan, wq0 = q0 + 32 * (wave / hw);
-  const int len = row_length(p, b), last = len - 1, t = wq0 + (lane & 31), L = static_cast<int>(p.seqlen);
-  const int window = static_cast<int>(p.window), sinks = static_cast<int>(p.sinks);
+  const int qspan = 32 * (4 / hw), q0 = static_cast<int>(qt) * qspan;
+  DqWork w;
+  w.q0 = q0;
+  w.wq0 = q0 + 32 * (wave / hw);
+  w.len = row_length(p, b);
+  const int last = w.len - 1, t = w.wq0 + (lane & 31), L = static_cast<int>(p.seqlen);
   const int64_t out = ((b * p.seqlen + t) * p.nheads + head) * D;
 
   f16v dq[NB] = {};
-  if (q0 < len) {
+  if (q0 < w.len) {
     const int qlast = q0 + qspan - 1 < last ? q0 + qspan - 1 : last;
-    const KeyRow keys = key_row(q0, window, sinks);
-    const int tiles = (keys.first + qlast - keys.low) / kTile + 1;
-    const uint16_t *kp = p.k + b * p.k_batch + c * D, *vp = p.v + b * p.v_batch + c * D;
-    auto start = [&](int i) {
-      load_keys<D, 256>(lds[i & 1][0], kp, p.k_token, keys, i * kTile, last, tid);
-      load_keys<D, 256>(lds[i & 1][1], vp, p.v_token, keys, i * kTile, last, tid);
-    };
+    w.keys = key_row(q0, static_cast<int>(p.window), static_cast<int>(p.sinks));
+    w.tiles = (w.keys.first + qlast - w.keys.low) / kTile + 1;
+    w.k = p.k + b * p.k_batch + c * D;
+    w.v = p.v + b * p.v_batch + c * D;
     bf8 q[NS], dy[NS];
     const int row = t < last ? t : last;
     const int64_t from = ((b * p.seqlen + row) * p.nheads + head) * D;
     const u4 *qs = reinterpret_cast<const u4 *>(p.q + b * p.q_batch + row * p.q_token + head * D);
     const u4 *ds = reinterpret_cast<const u4 *>(p.dy + from), *ys = reinterpret_cast<const u4 *>(p.y + from);
-    float delta = 0.0f;
+    float delta = 0.0f, off;
 #pragma unroll
     for (int s = 0; s < NS; ++s) {
       q[s] = __builtin_bit_cast(bf8, qs[2 * s + half]);
@@ -73,55 +165,19 @@ __global__ void __launch_bounds__(256, 2) swa_dq_kernel(const SwaParams p, int h
         delta = fmaf(__uint_as_float(d4[e] & 0xffff0000u), __uint_as_float(y4[e] & 0xffff0000u), delta);
       }
     }
-    delta += other_half(delta);
+    w.delta = delta + other_half(delta);
     const int64_t stat = (b * p.nheads + head) * p.seqlen + row;
-    const float lse2 = p.lse[stat] * kLog2e, c2 = p.scale * kLog2e;
-    float off = 0.0f;  // what dy.y is too small by, since y is rounded: the weights' sum is 1, so sum_j ds_tj
-    const Lanes at = lanes_of<D>(lane);
-    start(0);
-    for (int i = 0; i < tiles; ++i) {
-      wait_tiles();
-      __syncthreads();  // tile i has landed, and nobody reads the other buffer any more
-      if (i + 1 < tiles) start(i + 1);
-      const int v0 = i * kTile, j0 = keys.key(v0), j1 = keys.key(v0 + kTile - 1);
-      const u4 *kt = lds[i & 1][0], *vt = lds[i & 1][1];
-      if (j0 > wq0 + 31 || (j1 <= wq0 - window && j0 >= sinks) || wq0 >= len) continue;
-      const bool whole = j1 <= wq0 && wq0 + 31 - j0 < window;
-      const Seen seen = seen_by(keys, t, v0, half, window, sinks);
-#pragma unroll
-      for (int blk = 0; blk < 2; ++blk) {
-        f16v s = {}, dp = {};
-#pragma unroll
-        for (int ks = 0; ks < NS; ++ks) {
-          s = mfma(row_operand<D>(kt, 32 * blk, ks, at), q[ks], s);
-          dp = mfma(row_operand<D>(vt, 32 * blk, ks, at), dy[ks], dp);
-        }
-        reads_ahead<2 * NS>();
-#pragma unroll
-        for (int r = 0; r < 16; ++r)
-          dp[r] = __builtin_amdgcn_exp2f(fmaf(s[r], c2, -lse2)) * (dp[r] - delta);
-        if (!whole) {
-#pragma unroll
-          for (int r = 0; r < 16; ++r) dp[r] = seen(32 * blk + d_row(r, 0)) ? dp[r] : 0.0f;
-        }
-#pragma unroll
-        for (int r = 0; r < 16; ++r) off += dp[r];
-#pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
-          const bf8 dsk = as_operand(dp, ks), rest = left_over(dp, ks, dsk);
-#pragma unroll
-          for (int db = 0; db < NB; ++db) {
-            const bf8 kc = col_operand<D>(kt, 32 * blk + 16 * ks, db, at);
-            dq[db] = mfma(kc, dsk, dq[db]);
-            dq[db] = mfma(kc, rest, dq[db]);
-          }
-        }
-      }
-    }
+    w.lse2 = p.lse[stat] * kLog2e;
+    w.c2 = p.scale * kLog2e;
+    if (tid == 0) found = 0;  // before the first barrier in dq_pass()
+    const bool bad = dq_pass<D, false>(p, w, lds, q, dy, dq, off, tid);
+    if (__any(bad)) found = 1;
+    __syncthreads();
+    if (found) dq_pass<D, true>(p, w, lds, q, dy, dq, off, tid);
     off += other_half(off);
-    if (half == 0 && t < len) {
-      p.ws_lse2[stat] = lse2;
-      p.ws_delta[stat] = delta + off;
+    if (half == 0 && t < w.len) {
+      p.ws_lse2[stat] = w.lse2;
+      p.ws_delta[stat] = w.delta + off;
     }
   }
   if (t >= L) return;
@@ -131,7 +187,7 @@ __global__ void __launch_bounds__(256, 2) swa_dq_kernel(const SwaParams p, int h
     for (int j = 0; j < 4; ++j) {
       bf4 v;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) v[r] = static_cast<__bf16>(t < len ? dq[db][4 * j + r] * p.scale : 0.0f);
+      for (int r = 0; r < 4; ++r) v[r] = static_cast<__bf16>(t < w.len ? dq[db][4 * j + r] * p.scale : 0.0f);
       *reinterpret_cast<bf4 *>(p.dq + out + 32 * db + 8 * j + 4 * half) = v;
     }
 }
@@ -139,7 +195,11 @@ __global__ void __launch_bounds__(256, 2) swa_dq_kernel(const SwaParams p, int h
 // The gradients that 32 queries (rows base .. base + 31 of the tiles qt and dt,
 // with their stats) give the 32 keys of a wavefront, lane % 32 its key.  WHOLE:
 // every query sees every key; else sees(row) tells, rows less 4 in the second lane half.
-template <int D, typename F>
+//
+// An infinity or NaN in a query or its dy, times 0, would reach the keys that it
+// does not see: SAFE keeps such elements out of the products and adds what they
+// are worth (dv: p is above 0; dk: ds is NaN or 0) to the keys that it sees.
+template <int D, bool SAFE, typename F>
 __device__ __forceinline__ void add_queries(const u4 *qt, const u4 *dt, const float *lse2, const float *delta, int base,
                                             const bf8 (&kf)[D / 16], const bf8 (&vf)[D / 16], float c2, bool whole, F sees,
                                             f16v (&dk)[D / 32], f16v (&dv)[D / 32], const Lanes &at, int half) {
@@ -169,14 +229,31 @@ __device__ __forceinline__ void add_queries(const u4 *qt, const u4 *dt, const fl
       s[r] = yes ? s[r] : 0.0f;
       dp[r] = yes ? dp[r] : 0.0f;
     }
+    if constexpr (SAFE) {
+      bf8 vis[2];
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) vis[ks][e] = static_cast<__bf16>(sees(d_row(8 * ks + e, 0)) ? 1.0f : 0.0f);
+      add_not_finite<D, 2, false>(dt, base, vis, dv, at);
+      add_not_finite<D, 2, true>(qt, base, vis, dk, at);
+    }
   }
 #pragma unroll
   for (int ks = 0; ks < 2; ++ks) {
     const bf8 pk = as_operand(s, ks), dsk = as_operand(dp, ks);
 #pragma unroll
     for (int db = 0; db < NB; ++db) {
-      dv[db] = mfma(col_operand<D>(dt, base + 16 * ks, db, at), pk, dv[db]);
-      dk[db] = mfma(col_operand<D>(qt, base + 16 * ks, db, at), dsk, dk[db]);
+      bf8 dc = col_operand<D>(dt, base + 16 * ks, db, at), qc = col_operand<D>(qt, base + 16 * ks, db, at);
+      if constexpr (SAFE) {
+        if (!whole) {
+          dc = only_finite(dc);
+          qc = only_finite(qc);
+        }
+      }
+      dv[db] = mfma(dc, pk, dv[db]);
+      dk[db] = mfma(qc, dsk, dk[db]);
+      if constexpr (SAFE) __builtin_amdgcn_sched_barrier(0);
     }
   }
 }
@@ -229,6 +306,7 @@ __global__ void __launch_bounds__(256, D == 64 ? 2 : 1) swa_dkv_kernel(const Swa
   constexpr int CH = D / 8, NB = D / 32, NS = D / 16;
   __shared__ __align__(16) u4 lds[2][2][kTile * CH];  // buffer, Q or dy
   __shared__ __align__(16) float stats[4][2][kTile];  // buffer or wavefront, log2(e) lse or dy.y
+  __shared__ int found;
   const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const unsigned nkv = static_cast<unsigned>(p.nkv), group = static_cast<unsigned>(p.nheads) / nkv;
@@ -246,6 +324,9 @@ __global__ void __launch_bounds__(256, D == 64 ? 2 : 1) swa_dkv_kernel(const Swa
   const Lanes at = lanes_of<D>(lane);
   f16v dk[NB] = {}, dv[NB] = {};
   bf8 kf[NS], vf[NS];
+  // An infinity or NaN in a query makes its lse one, or -infinity, and one in its
+  // dy makes dy.y one; NaN once such a query was met: then all over, safely.
+  float even = 0.0f;
 
   if (far) {
     // Each wavefront walks (query tile of 32, head) pairs of its own, in LDS of its own.
@@ -262,13 +343,24 @@ __global__ void __launch_bounds__(256, D == 64 ? 2 : 1) swa_dkv_kernel(const Swa
       load_stats(stats[wave][0], p.ws_lse2 + (b * p.nheads + head) * p.seqlen, t0, last, lane);
       load_stats(stats[wave][1], p.ws_delta + (b * p.nheads + head) * p.seqlen, t0, last, lane);
     };
-    for (int u = static_cast<int>(chunk) * 4 + wave; u < units; u += step) {
-      start(u);
-      wait_tiles();
-      const int t0 = (first + u % tiles) * 32;
-      add_queries<D>(qt, dt, stats[wave][0], stats[wave][1], 0, kf, vf, c2, t0 + 31 < len && j0 + 31 < sinks,
-                     [&](int r) { return t0 + 4 * half + r < len && j < sinks; }, dk, dv, at, half);
-      wait_reads();
+    auto pass = [&](auto safe) {
+      for (int u = static_cast<int>(chunk) * 4 + wave; u < units; u += step) {
+        start(u);
+        wait_tiles();
+        const float look = stats[wave][half][lane & 31];
+        const int t0 = (first + u % tiles) * 32;
+        add_queries<D, decltype(safe)::value>(
+            qt, dt, stats[wave][0], stats[wave][1], 0, kf, vf, c2, t0 + 31 < len && j0 + 31 < sinks,
+            [&](int r) { return t0 + 4 * half + r < len && j < sinks; }, dk, dv, at, half);
+        even = fmaf(look, 0.0f, even);
+        wait_reads();
+      }
+    };
+    pass(std::false_type());
+    if (__any(even != 0.0f)) {
+#pragma unroll
+      for (int db = 0; db < NB; ++db) dk[db] = dv[db] = f16v{};
+      pass(std::true_type());
     }
     // Add the wavefronts' terms, dk then dv, in LDS.
     float *sums = reinterpret_cast<float *>(lds), *out = p.ws_far + (bc * far_items + k) * 2 * 32 * D;
@@ -298,36 +390,50 @@ __global__ void __launch_bounds__(256, D == 64 ? 2 : 1) swa_dkv_kernel(const Swa
     load_keys_and_values<D>(p, b, c, j < last ? j : last, half, kf, vf);
     // How many queries from its own on see this lane's key: the window's, or all of a sink's, up to the length.
     const unsigned reach = j >= len ? 0 : j < sinks || window > len - j ? len - j : window;
-    int at_head = head0, at_tile = t_lo;  // of the next tile to start
-    auto start = [&](int i) {
-      const int t0 = at_tile * kTile, buf = i & 1;
-      load_tile<D, 256>(lds[buf][0], p.q + b * p.q_batch + at_head * D, p.q_token, t0, last, tid);
-      load_tile<D, 256>(lds[buf][1], p.dy + (b * p.seqlen * p.nheads + at_head) * D, p.nheads * D, t0, last, tid);
-      if (wave < 2) load_stats(stats[buf][wave], (wave == 0 ? p.ws_lse2 : p.ws_delta) + (b * p.nheads + at_head) * p.seqlen,
-                               t0, last, lane);
-      if (++at_tile == t_hi) {
-        at_tile = t_lo;
-        ++at_head;
+    auto pass = [&](auto safe) {
+      int at_head = head0, at_tile = t_lo;  // of the next tile to start
+      auto start = [&](int i) {
+        const int t0 = at_tile * kTile, buf = i & 1;
+        load_tile<D, 256>(lds[buf][0], p.q + b * p.q_batch + at_head * D, p.q_token, t0, last, tid);
+        load_tile<D, 256>(lds[buf][1], p.dy + (b * p.seqlen * p.nheads + at_head) * D, p.nheads * D, t0, last, tid);
+        if (wave < 2) load_stats(stats[buf][wave], (wave == 0 ? p.ws_lse2 : p.ws_delta) + (b * p.nheads + at_head) * p.seqlen,
+                                 t0, last, lane);
+        if (++at_tile == t_hi) {
+          at_tile = t_lo;
+          ++at_head;
+        }
+      };
+      start(0);
+      int tile = t_lo;
+      for (int i = 0; i < steps; ++i) {
+        wait_tiles();
+        __syncthreads();
+        if (i + 1 < steps) start(i + 1);
+        const float look = stats[i & 1][lane >> 4 & 1][16 * wave + (lane & 15)];  // a quarter of the queries
+        const int t0 = tile * kTile;
+        if (++tile == t_hi) tile = t_lo;
+#pragma unroll
+        for (int blk = 0; blk < 2; ++blk) {
+          const int q0 = t0 + 32 * blk;
+          // Does any of these 32 queries see any of the wavefront's keys, or all of them all?
+          if (q0 + 31 < wk0 || (q0 >= wk0 + 31 + window && wk0 >= sinks) || q0 >= len || wk0 >= len) continue;
+          const bool whole = q0 >= wk0 + 31 && q0 + 31 < len && (q0 + 31 - wk0 < window || wk0 + 31 < sinks);
+          const int behind = q0 + 4 * half - j;  // of the lane's first query after its key
+          add_queries<D, decltype(safe)::value>(
+              lds[i & 1][0], lds[i & 1][1], stats[i & 1][0], stats[i & 1][1], 32 * blk, kf, vf, c2, whole,
+              [&](int r) { return static_cast<unsigned>(behind + r) < reach; }, dk, dv, at, half);
+        }
+        even = fmaf(look, 0.0f, even);
       }
     };
-    start(0);
-    int tile = t_lo;
-    for (int i = 0; i < steps; ++i) {
-      wait_tiles();
-      __syncthreads();
-      if (i + 1 < steps) start(i + 1);
-      const int t0 = tile * kTile;
-      if (++tile == t_hi) tile = t_lo;
+    if (tid == 0) found = 0;  // before the first barrier in pass()
+    pass(std::false_type());
+    if (__any(even != 0.0f)) found = 1;
+    __syncthreads();
+    if (found) {
 #pragma unroll
-      for (int blk = 0; blk < 2; ++blk) {
-        const int q0 = t0 + 32 * blk;
-        // Does any of these 32 queries see any of the wavefront's keys, or all of them all?
-        if (q0 + 31 < wk0 || (q0 >= wk0 + 31 + window && wk0 >= sinks) || q0 >= len || wk0 >= len) continue;
-        const bool whole = q0 >= wk0 + 31 && q0 + 31 < len && (q0 + 31 - wk0 < window || wk0 + 31 < sinks);
-        const int behind = q0 + 4 * half - j;  // of the lane's first query after its key
-        add_queries<D>(lds[i & 1][0], lds[i & 1][1], stats[i & 1][0], stats[i & 1][1], 32 * blk, kf, vf, c2, whole,
-                       [&](int r) { return static_cast<unsigned>(behind + r) < reach; }, dk, dv, at, half);
-      }
+      for (int db = 0; db < NB; ++db) dk[db] = dv[db] = f16v{};
+      pass(std::true_type());
     }
   }
   if (block < plan.sum_blocks) {

@@ -25,42 +25,6 @@ namespace {
 
 constexpr float kLn2 = 0.6931471805599453f;
 
-// Bits 15 and 31 are set where that half, a bfloat16, is an infinity or NaN.
-__device__ __forceinline__ unsigned not_finite(unsigned x) { return (x & 0x7fff7fffu) + 0x00800080u; }
-
-// 1.0 in the halves that equal those of `what`, or that are NaN, 0 in the others.
-__device__ __forceinline__ unsigned is_half(unsigned x, unsigned what) {
-  const unsigned t = x ^ what, other = ((t & 0x7fff7fffu) + 0x7fff7fffu) | t;  // bits 15 and 31: not equal
-  return ((~other >> 15) & 0x00010001u) * 0x3f80u;
-}
-__device__ __forceinline__ unsigned is_nan(unsigned x) {
-  return ((((x & 0x7fff7fffu) + 0x007f007fu) >> 15) & 0x00010001u) * 0x3f80u;
-}
-
-// What the infinities and NaN of a tile of values add to the queries that see
-// them, out[db] += vis * v over those elements alone.  vis: 1 or 0 per key.
-template <int D>
-__device__ __forceinline__ void add_not_finite(const u4 *tile, const bf8 (&vis)[4], f16v (&out)[D / 32], const Lanes &at) {
-#pragma unroll
-  for (int db = 0; db < D / 32; ++db) {
-    // (Not unrolled: this is rare, and must not cost the others registers.)
-#pragma unroll 1
-    for (int kind = 0; kind < 3; ++kind) {  // +inf, -inf, NaN
-      f16v count = {};
-#pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        u4 v = __builtin_bit_cast(u4, col_operand<D>(tile, 16 * s, db, at));
-#pragma unroll
-        for (int k = 0; k < 4; ++k) v[k] = kind == 2 ? is_nan(v[k]) : is_half(v[k], kind == 0 ? 0x7f807f80u : 0xff80ff80u);
-        count = mfma(__builtin_bit_cast(bf8, v), vis[s], count);
-      }
-      const float add = kind == 0 ? INFINITY : kind == 1 ? -INFINITY : NAN;
-#pragma unroll
-      for (int i = 0; i < 16; ++i) out[db][i] += count[i] > 0.0f ? add : 0.0f;
-    }
-  }
-}
-
 // What a workgroup knows of its work.
 struct FwdWork {
   const uint16_t *k, *v;  // of the key head
@@ -132,7 +96,7 @@ __device__ __forceinline__ bool attend(const SwaParams &p, const FwdWork &w, u4 
         for (int ks = 0; ks < 4; ++ks)
 #pragma unroll
           for (int e = 0; e < 8; ++e) vis[ks][e] = static_cast<__bf16>(seen(32 * (ks / 2) + d_row(ks % 2 * 8 + e, 0)) ? 1.0f : 0.0f);
-        add_not_finite<D>(vt, vis, o, at);
+        add_not_finite<D, 4, false>(vt, 0, vis, o, at);
       }
     }
 #pragma unroll
@@ -140,14 +104,11 @@ __device__ __forceinline__ bool attend(const SwaParams &p, const FwdWork &w, u4 
       const bf8 pk = as_operand(s[ks / 2], ks % 2);
 #pragma unroll
       for (int db = 0; db < NB; ++db) {
-        u4 v = __builtin_bit_cast(u4, col_operand<D>(vt, 16 * ks, db, at));
+        bf8 v = col_operand<D>(vt, 16 * ks, db, at);
         if constexpr (SAFE) {
-          if (!whole) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) v[k] &= ~(((not_finite(v[k]) >> 15) & 0x00010001u) * 0xffffu);
-          }
+          if (!whole) v = only_finite(v);
         }
-        o[db] = mfma(__builtin_bit_cast(bf8, v), pk, o[db]);
+        o[db] = mfma(v, pk, o[db]);
         if constexpr (SAFE) __builtin_amdgcn_sched_barrier(0);
       }
     }

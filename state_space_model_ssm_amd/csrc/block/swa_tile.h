@@ -94,6 +94,58 @@ __device__ __forceinline__ bf8 left_over(const f16v &d, int s, bf8 rounded) {
   return v;
 }
 
+// Bits 15 and 31 are set where that half, a bfloat16, is an infinity or NaN.
+__device__ __forceinline__ unsigned not_finite(unsigned x) { return (x & 0x7fff7fffu) + 0x00800080u; }
+
+// 1.0 in the halves that equal those of `what`, that are NaN, or that are an
+// infinity or NaN, 0 in the others.
+__device__ __forceinline__ unsigned is_half(unsigned x, unsigned what) {
+  const unsigned t = x ^ what, other = ((t & 0x7fff7fffu) + 0x7fff7fffu) | t;  // bits 15 and 31: not equal
+  return ((~other >> 15) & 0x00010001u) * 0x3f80u;
+}
+__device__ __forceinline__ unsigned is_nan(unsigned x) {
+  return ((((x & 0x7fff7fffu) + 0x007f007fu) >> 15) & 0x00010001u) * 0x3f80u;
+}
+__device__ __forceinline__ unsigned is_not_finite(unsigned x) { return ((not_finite(x) >> 15) & 0x00010001u) * 0x3f80u; }
+
+// An operand with zeros for its infinities and NaN.
+__device__ __forceinline__ bf8 only_finite(bf8 operand) {
+  u4 v = __builtin_bit_cast(u4, operand);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) v[k] &= ~(((not_finite(v[k]) >> 15) & 0x00010001u) * 0xffffu);
+  return __builtin_bit_cast(bf8, v);
+}
+
+// What the infinities and NaN of 16 NS rows of a tile, from row `base` on, add
+// to the columns that see them: out[db] += vis * v over those elements alone.
+// vis: 1 or 0 per row, in the order of as_operand().  NANS: each counts as a
+// NaN, for factors that are NaN or 0 where the elements are not finite.
+template <int D, int NS, bool NANS>
+__device__ __forceinline__ void add_not_finite(const u4 *tile, int base, const bf8 (&vis)[NS], f16v (&out)[D / 32],
+                                               const Lanes &at) {
+#pragma unroll
+  for (int db = 0; db < D / 32; ++db) {
+    // (Not unrolled: this is rare, and must not cost the others registers.)
+#pragma unroll 1
+    for (int kind = NANS ? 2 : 0; kind < 3; ++kind) {  // +inf, -inf, NaN
+      f16v count = {};
+#pragma unroll
+      for (int s = 0; s < NS; ++s) {
+        u4 v = __builtin_bit_cast(u4, col_operand<D>(tile, base + 16 * s, db, at));
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if constexpr (NANS) v[k] = is_not_finite(v[k]);
+          else v[k] = kind == 2 ? is_nan(v[k]) : is_half(v[k], kind == 0 ? 0x7f807f80u : 0xff80ff80u);
+        }
+        count = mfma(__builtin_bit_cast(bf8, v), vis[s], count);
+      }
+      const float add = kind == 0 ? INFINITY : kind == 1 ? -INFINITY : NAN;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) out[db][i] += count[i] > 0.0f ? add : 0.0f;
+    }
+  }
+}
+
 // The row that register i of a D result stands for in lane half h.
 __device__ __forceinline__ constexpr int d_row(int i, int h) { return 8 * (i / 4) + 4 * h + i % 4; }
 

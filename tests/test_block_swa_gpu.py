@@ -330,3 +330,51 @@ def test_fill_past_2_32_pieces():
         assert torch.equal(cache[:, :, :L], new.transpose(1, 2)) and not cache[:, :, L].any()
     del kc, vc, cache
     torch.cuda.empty_cache()   # 128 GiB
+
+
+@pytest.mark.parametrize("d,window,sinks", [(64, 60, 2), (128, 60, 2), (64, 33, 0), (128, 500, 3), (64, 20, 70)])
+@pytest.mark.parametrize("lengths", [None, [400, 261]])
+def test_gradients_of_what_is_not_seen_stay_as_they_were(d, window, sinks, lengths):
+    """NaN and infinities in keys, values, queries and gradients reach the rows that see them, or are seen by them, alone."""
+    B, L, H, KV = 2, 400, 4, 2
+    q, k, v, dy = make(B, L, H, KV, d, 15)
+    n = torch.tensor(lengths or [L, L])
+    kw = dict(window=window, sinks=sinks, lengths=None if lengths is None else n.to(torch.int32).cuda())
+    see = torch.from_numpy(np.stack([np.pad(ref.visible(m, window, sinks, m), ((0, L - m), (0, L - m))) for m in n.tolist()]))
+
+    def run(q, k, v, dy):
+        c = [t.cuda() for t in (q, k, v)]
+        y, lse = ssm.swa_fwd(*c, **kw)
+        out = {name: nan(t.shape) for name, t in (("dq", q), ("dk", k), ("dv", v))}
+        ssm.swa_bwd(*c, y, lse, dy.cuda(), **kw, out=out)
+        return {name: t.cpu() for name, t in out.items()}
+
+    clean = run(q, k, v, dy)
+    head, group = torch.arange(H), H // KV
+    for what, at, bad in (("k", 100, "nan"), ("k", 100, "inf"), ("v", 250, "-inf"), ("q", 130, "nan"), ("q", 255, "inf"),
+                          ("dy", 130, "inf"), ("dy", 7, "nan")):
+        t = dict(q=q.clone(), k=k.clone(), v=v.clone(), dy=dy.clone())
+        h = 1 if what in ("k", "v") else 2              # a head of its own kind: key head 1, or its first query head
+        t[what][:, at, h, 5] = float(bad)
+        got = run(**t)
+        # Queries whose weights or gradients are not finite: those that see the key, or the one itself.
+        hit = torch.zeros(B, L, H, dtype=torch.bool)
+        if what in ("k", "v"):
+            hit[:] = see[:, :, at, None] & (head // group == h)
+        else:
+            hit[:, at, h] = at < n
+        seen_by_hit = torch.stack([(see[:, :, :, None] & hit[:, :, None, c * group:(c + 1) * group]).any(-1).any(1)
+                                   for c in range(KV)], -1)             # keys that such a query sees
+        assert torch.equal(got["dq"][~hit], clean["dq"][~hit]), (what, bad)
+        assert torch.equal(got["dk"][~seen_by_hit], clean["dk"][~seen_by_hit]), (what, bad)
+        touched = seen_by_hit if what != "v" else torch.zeros_like(seen_by_hit)   # values do not reach dv
+        assert torch.equal(got["dv"][~touched], clean["dv"][~touched]), (what, bad)
+        bad_dq, bad_dk, bad_dv = (~torch.isfinite(got[name].float()) for name in ("dq", "dk", "dv"))
+        if bad == "nan" and what != "v":
+            assert bad_dq[hit].all() and bad_dk[seen_by_hit].all()
+        if what == "dy":                                 # dv gets p times it in its element alone
+            assert bad_dv[seen_by_hit][:, 5].all() and not bad_dv[..., :5].any() and not bad_dv[..., 6:].any()
+            want = torch.isnan if bad == "nan" else lambda x: x == float("inf")
+            assert want(got["dv"][seen_by_hit][:, 5].float()).all()
+        elif bad == "nan":
+            assert bad_dv[seen_by_hit].all()
