@@ -1,0 +1,90 @@
+"""How exact sliding-window attention is, as a norm over all elements, in units
+of what rounding the exact result to bfloat16 loses.
+
+The kernels' roundings are made in float64 here, and two mistakes beside them:
+ds rounded to bfloat16 before dq (the kernel takes it in two parts), and ds for
+dk from dy.y of the rounded y (the kernel takes the exact dy.y, which the sum
+of ds tells).  A kernel passes when it is nearer to the first than to the
+mistakes."""
+import numpy as np
+import pytest
+import torch
+
+import block_reference as ref
+import state_space_model_ssm_amd as ssm
+
+BF16 = torch.bfloat16
+
+
+def rounded(x):
+    return torch.from_numpy(np.ascontiguousarray(x)).to(BF16).double().numpy()
+
+
+def loss(got, want):
+    return float(np.linalg.norm(got - want) / np.linalg.norm(rounded(want) - want))
+
+
+def make(B, L, H, KV, d, seed):
+    g = torch.Generator().manual_seed(seed)
+    return [torch.randn(B, L, n, d, generator=g).to(BF16) for n in (H, KV, KV, H)]
+
+
+def as_built(q, k, v, dy, window, sinks):
+    """y, dq, dk, dv with the kernels' roundings, and dq and dk with a mistake each."""
+    q, k, v, dy = (ref.f64(t) for t in (q, k, v, dy))
+    B, L, H, d = q.shape
+    see, scale = ref.visible(L, window, sinks, L), d ** -0.5
+    out = {n: np.zeros_like(q if n in ("y", "dq", "dq of rounded ds") else k)
+           for n in ("y", "dq", "dq of rounded ds", "dk", "dk of rounded y", "dv")}
+    for b in range(B):
+        for h in range(H):
+            c = h // (H // k.shape[2])
+            Q, K, V, G = q[b, :, h], k[b, :, c], v[b, :, c], dy[b, :, h]
+            s = np.where(see, Q @ K.T * scale, -np.inf)
+            e = np.exp(s - s.max(1, keepdims=True))
+            total = e.sum(1, keepdims=True)
+            p, y = e / total, rounded(rounded(e) @ V / total)
+            out["y"][b, :, h] = y
+            ds = p * (G @ V.T - (G * y).sum(1, keepdims=True))
+            exact = p * (G @ V.T - (G * y).sum(1, keepdims=True) - ds.sum(1, keepdims=True))
+            out["dq"][b, :, h] = ds @ K * scale
+            out["dq of rounded ds"][b, :, h] = rounded(ds) @ K * scale
+            out["dk"][b, :, c] += rounded(exact).T @ Q * scale
+            out["dk of rounded y"][b, :, c] += rounded(ds).T @ Q * scale
+            out["dv"][b, :, c] += rounded(p).T @ G
+    return {n: rounded(t) for n, t in out.items()}
+
+
+CASES = [  # B, L, H, KV, d, window, sinks: rows of few keys, where a rounding of dy.y weighs most
+    (2, 133, 8, 4, 64, 1024, 0), (4, 40, 4, 2, 64, 5, 0), (4, 24, 4, 1, 128, 100, 0), (2, 64, 4, 1, 128, 100, 1),
+    (1, 300, 8, 2, 64, 16, 2),
+]
+MISTAKES = {"dq": "dq of rounded ds", "dk": "dk of rounded y"}
+
+
+@pytest.mark.parametrize("case", CASES, ids=str)
+def test_the_planted_mistakes_show(case):
+    tensors = make(*case[:5], seed=case[1])
+    want, _ = ref.swa(*tensors[:3], *case[5:], dy=tensors[3])
+    built = as_built(*tensors, *case[5:])
+    for n, mistake in MISTAKES.items():
+        assert loss(built[mistake], want[n]) > 1.05 * loss(built[n], want[n]), n
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("case", CASES, ids=str)
+def test_gradients_lose_no_more_than_their_roundings(case):
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    tensors = make(*case[:5], seed=case[1])
+    kw = dict(window=case[5], sinks=case[6])
+    want, _ = ref.swa(*tensors[:3], *case[5:], dy=tensors[3])
+    built = as_built(*tensors, *case[5:])
+    q, k, v, dy = (t.cuda() for t in tensors)
+    y, lse = ssm.swa_fwd(q, k, v, **kw)
+    got = dict(zip(("y", "dq", "dk", "dv"), (y,) + ssm.swa_bwd(q, k, v, y, lse, dy, **kw)))
+    for n, t in got.items():
+        own = loss(built[n], want[n])
+        # Half the way to the mistake; 5% of its own where there is none.
+        most = (own + loss(built[MISTAKES[n]], want[n])) / 2 if n in MISTAKES else 1.05 * own
+        assert loss(ref.f64(t), want[n]) <= most, (n, own, most)
