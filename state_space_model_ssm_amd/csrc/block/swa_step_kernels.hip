@@ -5,10 +5,12 @@
 // tiles of 64 slots into LDS of its own (no barriers between wavefronts; the
 // next tile's keys start when this one's scores are done, its values when this
 // one's products are), and the matrix cores take up to 32 heads of a group at
-// once, padded, at a tenth of the time the bytes need.  The slots of a (row,
-// key head) are split over wavefronts and workgroups and joined by their
+// once, padded, at a tenth of the time the bytes need.  So the weights, which a
+// product takes in bfloat16, go through it in two parts, rounded and left over:
+// y is then off by its own rounding alone (1.67e-3 of its norm, 2.1e-3 with
+// rounded weights), for 1% of the time.  The slots of a (row, key head) are split over wavefronts and workgroups and joined by their
 // maxima: in LDS within a workgroup, by a second launch across workgroups.
-// 64 rows, 32 heads of 128 on 8, window 4096 (807 MB): 144 + 5 us, 5.6 TB/s.
+// 64 rows, 32 heads of 128 on 8, window 4096 (807 MB): 145 + 5 us, 5.6 TB/s.
 #include "swa_tile.h"
 
 namespace ssmb {
@@ -91,9 +93,13 @@ __global__ void __launch_bounds__(256) swa_step_kernel(const SwaStepParams p, un
         if (has) put_rows<D>(vt, vn, mine, end, lane);
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks) {
-          const bf8 pk = as_operand(s[ks / 2], ks % 2);
+          const bf8 pk = as_operand(s[ks / 2], ks % 2), rest = left_over(s[ks / 2], ks % 2, pk);
 #pragma unroll
-          for (int db = 0; db < NB; ++db) o[db] = mfma(col_operand<D>(vt, 16 * ks, db, at), pk, o[db]);
+          for (int db = 0; db < NB; ++db) {
+            const bf8 v = col_operand<D>(vt, 16 * ks, db, at);
+            o[db] = mfma(v, pk, o[db]);
+            o[db] = mfma(v, rest, o[db]);
+          }
         }
         wait_reads();
         if (i + 1 < hi) load_tile<D, 64>(vt, p.v_cache + base, D, k0 + kTile, last, lane);

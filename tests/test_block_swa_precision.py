@@ -88,3 +88,26 @@ def test_gradients_lose_no_more_than_their_roundings(case):
         # Half the way to the mistake; 5% of its own where there is none.
         most = (own + loss(built[MISTAKES[n]], want[n])) / 2 if n in MISTAKES else 1.05 * own
         assert loss(ref.f64(t), want[n]) <= most, (n, own, most)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B,H,KV,d,window,sinks", [(4, 16, 4, 128, 1024, 4), (8, 8, 1, 64, 100, 0), (2, 4, 4, 64, 3000, 16)])
+def test_a_step_loses_no_more_than_its_output_rounding(B, H, KV, d, window, sinks):
+    """Less than half of what weights rounded to bfloat16 would add."""
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    g = torch.Generator().manual_seed(window)
+    q, k, v = (torch.randn(B, n, d, generator=g).to(BF16) for n in (H, KV, KV))
+    kc, vc = (torch.randn(B, KV, window + sinks, d, generator=g).to(BF16) for _ in range(2))
+    pos = torch.randint(window // 2, 3 * window, (B,), generator=g).to(torch.int32)
+    want, _, keys, values = ref.swa_step(q, k, v, kc, vc, pos, sinks)
+    mistaken = np.zeros_like(want)
+    for b in range(B):
+        n = min(int(pos[b]) + 1, window + sinks)
+        for h in range(H):
+            s = ref.f64(keys[b, h // (H // KV), :n]) @ ref.f64(q[b, h]) * d ** -0.5
+            e = np.exp(s - s.max())
+            mistaken[b, h] = rounded(e) @ ref.f64(values[b, h // (H // KV), :n]) / e.sum()
+    y = ssm.swa_step(*(t.cuda() for t in (q, k, v, kc, vc, pos)), sinks=sinks)
+    most = (1 + loss(rounded(mistaken), want)) / 2
+    assert loss(ref.f64(y), want) <= most, (loss(ref.f64(y), want), most)
