@@ -73,7 +73,10 @@ enum { SSM_GLR_STATE_STEP = 16 };
  *   h_last      : (batch, dim) float32, nullable; may be exactly h0
  *   states      : (batch, ceil(seqlen / 16), dim) float32, nullable: the
  *                 state before step 16 k, which ssm_glr_bwd starts from
- * seqlen = 0 writes h_last = h0.  1 - a^2 is computed as -expm1(2 A r).
+ * seqlen = 0 writes h_last = h0.  1 - a^2 is computed without cancellation
+ * where a is near 1.  A sequence's tiles wait for their predecessors' states in
+ * the workspace; a wait of several seconds, which only a fault could cause,
+ * ends in NaN.
  */
 SSM_API int ssm_glr_workspace_size(const ssm_glr_dims_t *dims, size_t *bytes);
 SSM_API int ssm_glr_fwd(const void *x, const void *rec, const void *inp, const float *A, const float *h0,

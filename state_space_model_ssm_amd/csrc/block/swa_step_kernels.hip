@@ -8,8 +8,9 @@
 // once, padded, at a tenth of the time the bytes need.  So the weights, which a
 // product takes in bfloat16, go through it in two parts, rounded and left over:
 // y is then off by its own rounding alone (1.67e-3 of its norm, 2.1e-3 with
-// rounded weights), for 1% of the time.  The slots of a (row, key head) are split over wavefronts and workgroups and joined by their
-// maxima: in LDS within a workgroup, by a second launch across workgroups.
+// rounded weights), for 1% of the time.  The slots of a (row, key head) are
+// split over wavefronts and workgroups and joined by their maxima: in LDS
+// within a workgroup, by a second launch across workgroups.
 // 64 rows, 32 heads of 128 on 8, window 4096 (807 MB): 145 + 5 us, 5.6 TB/s.
 #include "swa_tile.h"
 

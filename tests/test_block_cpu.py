@@ -306,3 +306,20 @@ def test_workspaces_a_byte_short():
     assert need > 0 and call("ssm_swa_step", window=5000, workspace_bytes=need - 1) == WORKSPACE
     assert call("ssm_swa_step", window=5000, workspace=None) == WORKSPACE
     assert call("ssm_swa_step", window=5000, workspace=at(50) + 4) == ALIGN
+
+
+def test_the_series_for_one_minus_exp():
+    """The recurrence's polynomial for expm1(u) / u on (-0.4, 0): its error, and with the roundings of its float32 form."""
+    path = os.path.join(ROOT, "state_space_model_ssm_amd", "csrc", "block", "glr_kernels.hip")
+    body = re.search(r"float one_minus_exp\(.*?\n}", open(path).read(), re.S).group(0)
+    terms = [float.fromhex(t) for t in re.findall(r"0x1\.[0-9a-f]+p[+-]?\d+", body)] + [1.0]
+    assert len(terms) == 5 and "fmaf(u, p, 1.0f)" in body and "-0.4f" in body
+    u = -np.geomspace(1e-12, 0.4, 200001).astype(np.float32).astype(np.float64)
+    exact, wide, narrow = np.expm1(u) / u, np.zeros_like(u), np.full(u.shape, terms[0], np.float32)
+    for k, c in enumerate(terms):
+        wide = wide * u + c
+        if k:
+            narrow = (narrow.astype(np.float64) * u + c).astype(np.float32)   # a fused multiply-add
+    assert np.abs(wide / exact - 1).max() <= 6.2e-8
+    product = (-u * narrow).astype(np.float32)
+    assert np.abs(product / -np.expm1(u) - 1).max() <= 1.5e-7
