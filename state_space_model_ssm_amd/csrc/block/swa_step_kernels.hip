@@ -6,7 +6,7 @@
 // next tile's keys start when this one's scores are done, its values when this
 // one's products are), and the matrix cores take up to 32 heads of a group at
 // once, padded, at a tenth of the time the bytes need.  So the weights, which a
-// product takes in bfloat16, go through it in two parts, rounded and left over:
+// product takes in bfloat16, go through it in two parts, cut off and left over:
 // y is then off by its own rounding alone (1.67e-3 of its norm, 2.1e-3 with
 // rounded weights), for 1% of the time.  The slots of a (row, key head) are
 // split over wavefronts and workgroups and joined by their maxima: in LDS
@@ -17,12 +17,34 @@
 namespace ssmb {
 namespace {
 
-// The token's own key or value, from the arguments, into rows r .. end of a tile.
+// The token's own key or value, from the arguments, into row r of a tile.
 template <int D>
-__device__ __forceinline__ void put_rows(u4 *tile, const uint16_t *src, int r, int end, int lane) {
+__device__ __forceinline__ void put_row(u4 *tile, const uint16_t *src, int r, int lane) {
+  if (lane < D / 8) tile[slot<D>(r, lane)] = reinterpret_cast<const u4 *>(src)[lane];
+}
+
+// Zeros in the rows from r on: they repeat the last slot, whose infinity, if it
+// has one, would come out as 0 times itself.
+template <int D>
+__device__ __forceinline__ void clear_rows(u4 *tile, int r, int lane) {
   constexpr int CH = D / 8;
-  const u4 v = reinterpret_cast<const u4 *>(src)[lane % CH];
-  for (int k = r + lane / CH; k <= end; k += 64 / CH) tile[slot<D>(k, lane % CH)] = v;
+  for (int k = r + lane / CH; k < kTile; k += 64 / CH) tile[slot<D>(k, lane % CH)] = u4{};
+}
+
+// Weights (registers 8 s .. 8 s + 7 of a D result) as two operands whose sum
+// they are to 2^-16: cut off after 8 bits, and what that leaves, which is held
+// above 0, so that both times an infinity have its sign.
+__device__ __forceinline__ void two_parts(const f16v &d, int s, bf8 &cut, bf8 &rest) {
+  u4 c;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float a = d[8 * s + 2 * k], b = d[8 * s + 2 * k + 1];
+    const unsigned ca = __float_as_uint(a) & 0xffff0000u, cb = __float_as_uint(b) & 0xffff0000u;
+    c[k] = ca >> 16 | cb;
+    rest[2 * k] = static_cast<__bf16>(fmaxf(a - __uint_as_float(ca), 0x1p-100f));
+    rest[2 * k + 1] = static_cast<__bf16>(fmaxf(b - __uint_as_float(cb), 0x1p-100f));
+  }
+  cut = __builtin_bit_cast(bf8, c);
 }
 
 template <int D>
@@ -70,10 +92,8 @@ __global__ void __launch_bounds__(256) swa_step_kernel(const SwaStepParams p, un
       for (int i = lo; i < hi; ++i) {
         const int k0 = i * kTile, mine = own - k0;  // the token's row in this tile, if within it
         const bool has = mine >= 0 && mine < kTile;
-        // Rows past the last slot repeat it, and so its token if it is this one.
-        const int end = own == last ? kTile - 1 : mine;
         wait_tiles<kCopies>();  // the keys: all but the copies of the values
-        if (has) put_rows<D>(kt, kn, mine, end, lane);
+        if (has) put_row<D>(kt, kn, mine, lane);
         f16v s[2] = {};
 #pragma unroll
         for (int blk = 0; blk < 2; ++blk)
@@ -91,14 +111,16 @@ __global__ void __launch_bounds__(256) swa_step_kernel(const SwaStepParams p, un
         to_weights(s, c2, o, top, sum);
         if (i + 1 < hi) wait_tiles<kCopies>();  // the values: all but the copies of the next keys
         else wait_tiles<0>();
-        if (has) put_rows<D>(vt, vn, mine, end, lane);
+        if (has) put_row<D>(vt, vn, mine, lane);
+        if (k0 + kTile > count) clear_rows<D>(vt, count - k0, lane);
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks) {
-          const bf8 pk = as_operand(s[ks / 2], ks % 2), rest = left_over(s[ks / 2], ks % 2, pk);
+          bf8 cut, rest;
+          two_parts(s[ks / 2], ks % 2, cut, rest);
 #pragma unroll
           for (int db = 0; db < NB; ++db) {
             const bf8 v = col_operand<D>(vt, 16 * ks, db, at);
-            o[db] = mfma(v, pk, o[db]);
+            o[db] = mfma(v, cut, o[db]);
             o[db] = mfma(v, rest, o[db]);
           }
         }

@@ -378,3 +378,24 @@ def test_gradients_of_what_is_not_seen_stay_as_they_were(d, window, sinks, lengt
             assert want(got["dv"][seen_by_hit][:, 5].float()).all()
         elif bad == "nan":
             assert bad_dv[seen_by_hit].all()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("at,slot", [(9, 9), (9, 4), (200, 100), (300, 137), (273, 136)])
+def test_an_infinity_among_a_steps_values_stays_one(d, at, slot):
+    """In the token's own value or a stored one, last of a tile or not: its element alone, and not a NaN."""
+    window, sinks = 134, 3
+    g = torch.Generator().manual_seed(at)
+    q, k, v = (torch.randn(1, n, d, generator=g).to(BF16).cuda() for n in (4, 2, 2))
+    kc, vc = (torch.randn(1, 2, window + sinks, d, generator=g).to(BF16).cuda() for _ in range(2))
+    own = at if at < sinks else sinks + (at - sinks) % window
+    slot = min(slot, window + sinks - 1)
+    pos = torch.tensor([at], dtype=torch.int32, device="cuda")
+    clean = ssm.swa_step(q, k, v, kc.clone(), vc.clone(), pos, sinks=sinks)
+    vc[0, 1, slot, 5] = float("-inf")
+    if slot == own:
+        v[0, 1, 5] = float("-inf")
+    y = ssm.swa_step(q, k, v, kc, vc, pos, sinks=sinks)
+    assert bool((y[0, 2:, 5] == float("-inf")).all())
+    y[0, 2:, 5] = clean[0, 2:, 5]
+    assert torch.equal(y, clean)
