@@ -152,15 +152,15 @@ __device__ __forceinline__ constexpr int d_row(int i, int h) { return 8 * (i / 4
 // Copy 16 bytes per lane from base + off to LDS, from `lds` on in lane order.
 // The copy goes from memory to LDS without registers.  In asm, because the
 // compiler would wait for it before any LDS read, of another buffer too:
-// wait_tiles() waits for it.  (M0 has no other use in these kernels.)
+// wait_tiles() waits for it.
 __device__ __forceinline__ void copy16(unsigned lds, const void *base, unsigned off) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
                :
                : "s"(lds), "v"(off), "s"(base)
-               : "memory");
+               : "memory", "m0");
 }
 __device__ __forceinline__ void copy16(unsigned lds, const void *at) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" : : "s"(lds), "v"(at) : "memory");
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" : : "s"(lds), "v"(at) : "memory", "m0");
 }
 // Start the copy of tile rows t0 .. t0 + ROWS - 1 of a strided tensor (p: row
 // 0 of the head) into LDS, `NT` threads taking part; rows past `last` are read
@@ -235,7 +235,7 @@ __device__ __forceinline__ void load_stats(float *to, const float *p, int t0, in
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2"
                :
                : "s"(lds), "v"(off), "s"(base)
-               : "memory");
+               : "memory", "m0");
 }
 
 // All but the last N copies this wavefront has started have landed.
