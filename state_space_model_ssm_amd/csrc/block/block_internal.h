@@ -10,6 +10,8 @@ namespace ssmb {
 
 // Workgroups of 256 that a launch may have along an axis: fewer than 2^32 threads.
 constexpr int64_t kMaxGroups = (int64_t{1} << 24) - 1;
+// Workgroups along x of a launch that takes two axes, where there are more.
+constexpr unsigned kGridWidth = 1u << 20;
 
 constexpr float kLog2e = 1.4426950408889634f;
 

@@ -112,10 +112,6 @@ struct Place {
   bool many;            // channel blocks: at least 64, so that few tiles of each are in flight
 };
 
-// Workgroups along x of a larger launch: fewer than 2^32 threads fit an axis.
-// Past the last tile they have none (pos is not below tiles).
-constexpr unsigned kGridWidth = 1u << 20;
-
 constexpr int kGroup = 16;                // tiles between two published states
 constexpr unsigned kMissing = 0xffffffffu;  // a word not yet published
 constexpr int kMostPolls = 1 << 22;       // some seconds: a wait that long would be a fault, and ends in NaN
@@ -424,7 +420,7 @@ template <typename Tin, typename Tout, int C>
 __global__ void __launch_bounds__(256, 4) glr_fwd_kernel(const GlrParams p) {
   __shared__ __align__(16) Scratch lds;
   const Place w = place<C, false>(p.dim, p.seqlen, p.batch, p.chain, lds.number);
-  if (w.pos >= w.tiles) return;
+  if (w.pos >= w.tiles) return;  // past the last, in a grid of two axes
   typename Raw<Tin, C>::type rx[T], rrec[T], rinp[T];
   load<Tin, C>(p.rec, w, w.k, rrec);
   load<Tin, C>(p.inp, w, w.k, rinp);
@@ -520,7 +516,7 @@ __global__ void __launch_bounds__(256, 3) glr_bwd_kernel(const GlrBwdParams p) {
   __shared__ __align__(16) Scratch lds;
   typedef typename Raw<Tin, C>::type raw;
   const Place w = place<C, true>(p.dim, p.seqlen, p.batch, p.chain, lds.number);
-  if (w.pos >= w.tiles) return;
+  if (w.pos >= w.tiles) return;  // past the last, in a grid of two axes
   raw rec[T], dy[T], x[T], inp[T];
   load<Tin, C>(p.rec, w, w.k, rec);
   load<Tin, C>(p.dy, w, w.k, dy);
