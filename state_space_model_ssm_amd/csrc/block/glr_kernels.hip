@@ -13,7 +13,7 @@
 // against 106 for 1 x 32749 x 1536, and walking whole sequences with one
 // workgroup per 64 channels leaves 320 workgroups for 4 x 5120 channels, at
 // 2.3 TB/s against the 3.9 of enough tiles in flight.)  Bound by memory, inputs
-// out of the caches: bfloat16, 4 x 4096 x 5120, forward 175 us, backward 290,
+// out of the caches: bfloat16, 4 x 4096 x 5120, forward 175 us, backward 293,
 // both 3.9 TB/s; float32, 8 x 2048 x 1536, 92 and 134 us, 4.4 and 5.3 TB/s.
 //
 // Tiles of a channel block are grouped by 16 in time.  A tile waits for the

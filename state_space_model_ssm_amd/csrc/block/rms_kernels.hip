@@ -5,15 +5,15 @@
 // All of it is bound by memory: a row is read once into registers (16 bytes
 // per lane and load, by 16 or 64 lanes or the whole workgroup, whichever
 // leaves a lane the fewest idle loads), summed across its lanes, and written:
-// 16384 x 2048 bfloat16, out of the caches, forward 53 us (5.1 TB/s), backward
+// 16384 x 2048 bfloat16, out of the caches, forward 52 us (5.2 TB/s), backward
 // 48; in 8 bits 16384 x 5120 131 us (4.5 TB/s).
 // Workgroups walk rows with w in registers, and with the backward's sums over
 // rows for dw, which they write once each; a second launch adds those in
 // order.  Where rows do not start on 16 bytes the same loads start at any value
-// (16384 x 2047 bfloat16: forward 44 us, backward 52, against 43 and 48 for
-// 2048; value by value they were 61 and 142).  Rows too short or too long for
-// that, and groups that fit no lanes, go value by value, the forward's through
-// LDS, or are read again per pass if they are too long for LDS.
+// (16384 x 2047 bfloat16, a call forward and one backward: 110 us against 108
+// for 2048; value by value they were 203).  Rows too short or too long for that,
+// and groups that fit no lanes, go value by value, the forward's through LDS, or
+// are read again per pass if they are too long for LDS.
 #include "block_internal.h"
 
 namespace ssmb {

@@ -10,19 +10,24 @@
 // the second part of ds below, against the 5 that a single pass would need,
 // which would have to add dq from many workgroups.  p and ds go from one
 // product's result into the next one's operand as they lie (see swa_tile.h);
-// both are rounded to bfloat16 there, as the matrix cores take them, and
 // everything is summed in float32.
 //
-// dy.y comes from the rounded y.  Of rows with few keys its error is as large
-// as a rounding of dq itself, so dq takes ds in two parts, rounded and left
-// over (a third more products in its kernel, 53 us -> 63 on 4 ragged rows of
-// 2048 tokens; its error falls from 1.6 roundings to 1.1), and finds the exact
-// dy.y on its way, which dk gets for nothing.
+// Roundings.  The matrix cores take p and ds in bfloat16.  For dk and dv they
+// are rounded: the error is 2.3e-3 of their norm, where rounding the results
+// alone gives 1.65e-3; a second part of both would give that, and take a
+// quarter to two fifths more time (8192 tokens, 16 heads of 128, window 1024:
+// 223 -> 281 us; 4 x 4096 tokens over all their past, 32 heads of 64: 691 -> 918).
+// dq would also have the error of dy.y, which comes from the rounded y and in
+// rows of few keys weighs as much as a rounding of dq: 2.6e-3.  So ds goes into
+// dq in two parts, rounded and left over (1.8e-3 to 2.1e-3, for 15 to 24% of
+// the kernel: 130 -> 157 us and 501 -> 620 in those cases, 66 -> 76 on 4 ragged
+// rows of 2048, window 512).  dq keeps the inexact dy.y, but the sum of ds tells
+// what it lacks, and dk takes the exact one.
 //
-// Bound as the forward is (matrix instructions busy a third of the time): 8192
-// tokens, 16 heads of 128 on 4, window 1024, 143 and 200 us (900 and 650
-// TFLOP/s); 4 x 2048 tokens, 32 heads of 64 on 8, window 512, 91 and 96 us (660
-// and 630).
+// Bound as the forward is (matrix instructions busy a third of the time): dq and
+// dk with dv of 8192 tokens, 16 heads of 128 on 4, window 1024, 157 and 223 us
+// (820 and 580 TFLOP/s of what they compute); 4 x 2048 tokens, 32 heads of 64 on
+// 8, window 512, 100 and 110 us (600 and 550).
 #include <type_traits>
 
 #include "swa_tile.h"
@@ -119,7 +124,9 @@ __device__ __forceinline__ bool dq_pass(const SwaParams &p, const DqWork &w, u4 
   return even != 0.0f;
 }
 
-// dq; also log2(e) lse and dy.y of every query for the kernel below.
+// dq; also log2(e) lse and dy.y of every query for the kernel below.  Three
+// workgroups per CU with headdim 64 (what does not fit its registers is in the
+// rare pass).
 template <int D>
 __global__ void __launch_bounds__(256, D == 64 ? 3 : 2) swa_dq_kernel(const SwaParams p, int hw, unsigned qtiles, unsigned n) {
   constexpr int CH = D / 8, NB = D / 32, NS = D / 16;
