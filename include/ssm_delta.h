@@ -1,0 +1,131 @@
+/*
+ * libssm_delta: blocks of delta-rule layers and of attention with normalised
+ * keys, beside the operators of libssm_block, on AMD MI355X (gfx950): the
+ * gated delta rule, norms of queries and keys with the rotation by position,
+ * and sliding-window attention steps over a cache held in 8 bits.  Plain C
+ * ABI: device pointers, sizes, a HIP stream; no torch types.
+ *
+ * The conventions are those of ssm_block.h (status and dtype codes of ssm.h):
+ *   - Tensor pointers are DEVICE pointers owned by the caller, all on the
+ *     device of `stream`.  The library never allocates, frees or synchronises;
+ *     scratch memory ("workspace") is passed in by the caller, aligned to 256
+ *     bytes, and need not be initialised.  Calls that may run at the same time
+ *     (on two streams, or in two captured graphs that are replayed at once)
+ *     need a workspace each.
+ *   - Every tensor is dense, row-major, with the last listed index
+ *     contiguous, except where a stride is given.
+ *   - Calls are asynchronous on `stream` (a hipStream_t; NULL = null stream)
+ *     and may be captured into a HIP graph.
+ *   - All argument checks run on the host before any HIP call.  A call that
+ *     fails a check returns a negative ssm_status_t, launches nothing and
+ *     writes nothing; ssm_delta_last_error() then holds a one-line reason
+ *     (per host thread).  SSM_ERR_HIP is returned when a launch itself fails.
+ *   - Pointers must be aligned to their element size, and more where an entry
+ *     point says so; otherwise SSM_ERR_ALIGN.
+ *   - Outputs must not overlap inputs or each other, except where an entry
+ *     point says so, and the workspace none of them; otherwise SSM_ERR_SHAPE.
+ *   - Unsupported sizes return SSM_ERR_UNSUPPORTED; there is no fallback path.
+ *   - Indices and offsets are 64-bit throughout.
+ *   - The same inputs give the same bits on every call: no result depends on
+ *     the order in which workgroups finish.
+ */
+#ifndef SSM_DELTA_H
+#define SSM_DELTA_H
+
+#include "ssm.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* The reason of this thread's last failed call ("" after a call that passed). */
+SSM_API const char *ssm_delta_last_error(void);
+
+/* ------------------------------------------------------------------------ */
+/* Gated delta rule                                                          */
+/* ------------------------------------------------------------------------ */
+
+/*
+ * Sizes of one call.  nheads value heads share nqk query and key heads (nqk
+ * divides nheads; value head h has query and key head h / (nheads / nqk)).
+ * kdim and vdim: 64 or 128 each.  q, k, v, y and their gradients are bfloat16;
+ * gate_dtype: g, beta (and dg, dbeta).
+ * q_batch, q_token, ...: elements between two batch rows and two tokens of q,
+ * k and v (heads of a token are adjacent: head stride kdim or vdim); batch and
+ * token strides must be multiples of 8, token strides at most 2^24, and q, k,
+ * v, y, dy, dq, dk, dv and the states 16-byte aligned; all but q, k and v are
+ * dense.  scale multiplies y.  seqlen <= 2^30 and
+ * batch * nheads * ceil(seqlen / 64) < 2^24.
+ */
+typedef struct {
+  int64_t batch, seqlen, nqk, nheads, kdim, vdim;
+  int64_t q_batch, q_token, k_batch, k_token, v_batch, v_token;
+  float scale;
+  int32_t gate_dtype;
+  void *workspace;
+  size_t workspace_bytes;
+} ssm_gdr_dims_t;
+
+/* Steps between two saved states (see `states` below). */
+enum { SSM_GDR_STATE_STEP = 64 };
+
+/*
+ * Per batch row and value head, with the state S (vdim x kdim), a_t = exp(g_t):
+ *   u_t = beta_t (v_t - a_t S_{t-1} k_t)
+ *   S_t = a_t S_{t-1} + u_t k_t^T,   y_t = scale S_t q_t
+ * over the tokens below the row's length; y is 0 from there on.
+ *   q, k   : (batch, seqlen, nqk, kdim);  v, y: (batch, seqlen, nheads, vdim)
+ *   g, beta: (batch, seqlen, nheads) gate_dtype; g is the logarithm of the
+ *            decay (at or below 0 for a state that fades; -inf forgets, and
+ *            so does anything below -200)
+ *   h0     : (batch, nheads, vdim, kdim) float32, nullable (zero)
+ *   lengths: (batch) int32, nullable (seqlen); values outside 0 .. seqlen are
+ *            taken as the nearer end.  Rows at or past the length are not used.
+ *   h_last : as h0, nullable: the state after the row's last token (h0 where
+ *            there is none); may be exactly h0
+ *   states : (batch, nheads, ceil(seqlen / 64), vdim, kdim) float32, nullable:
+ *            the state before token 64 c, which ssm_gdr_bwd starts from;
+ *            those at or past the row's length are not written
+ * The rule is stable for beta |k|^2 below 2: keys are meant to have unit length.
+ * Tokens are taken 64 at a time: a value that is not finite reaches y from the
+ * start of its block of 64 tokens (of its channel, if it is one of v; of the
+ * value heads that share it, if it is one of q or k) and what comes after.
+ */
+SSM_API int ssm_gdr_workspace_size(const ssm_gdr_dims_t *dims, size_t *bytes);
+SSM_API int ssm_gdr_fwd(const void *q, const void *k, const void *v, const void *g, const void *beta, const float *h0,
+                        const int32_t *lengths, void *y, float *h_last, float *states, const ssm_gdr_dims_t *dims,
+                        void *stream);
+
+/*
+ * Backward: with dS_t the gradient of S_t (dS_t = a_{t+1} (dS_{t+1} -
+ * dv_{t+1} k_{t+1}^T) + scale dy_t q_t^T, from dh_last after the last token),
+ *   e_t = dS_t k_t,  dv_t = beta_t e_t,  dbeta_t = e_t.(v_t - a_t S_{t-1} k_t)
+ *   dq_t = scale S_t^T dy_t,  dk_t = dS_t^T u_t - a_t S_{t-1}^T dv_t
+ *   dg_t = a_t (<dS_t, S_{t-1}> - dv_t.S_{t-1} k_t)
+ * dq and dk are summed over the value heads that share a head.  Rows at or
+ * past the length get zero gradients.
+ *   states : what ssm_gdr_fwd saved for these inputs
+ *   dh_last, dh0: (batch, nheads, vdim, kdim) float32, both nullable
+ *   dq, dk : (batch, seqlen, nqk, kdim);  dv, dy: (batch, seqlen, nheads, vdim)
+ *   dg, dbeta: (batch, seqlen, nheads) gate_dtype
+ */
+SSM_API int ssm_gdr_bwd_workspace_size(const ssm_gdr_dims_t *dims, size_t *bytes);
+SSM_API int ssm_gdr_bwd(const void *q, const void *k, const void *v, const void *g, const void *beta,
+                        const int32_t *lengths, const float *states, const void *dy, const float *dh_last, void *dq,
+                        void *dk, void *dv, void *dg, void *dbeta, float *dh0, const ssm_gdr_dims_t *dims,
+                        void *stream);
+
+/*
+ * One token per batch row (dims.seqlen must be 1; no workspace): q, k are
+ * (batch, nqk, kdim), v, y (batch, nheads, vdim), g, beta (batch, nheads), h
+ * the state before the token and h_out (which may be exactly h) the state
+ * after it.  The token strides are not used.
+ */
+SSM_API int ssm_gdr_step(const void *q, const void *k, const void *v, const void *g, const void *beta, const float *h,
+                         void *y, float *h_out, const ssm_gdr_dims_t *dims, void *stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* SSM_DELTA_H */

@@ -32,14 +32,24 @@ _BLOCK = (
     "rms_add_fwd", "rms_add_q8_fwd", "rms_add_bwd", "rms_add_bwd_workspace_size",
     "swa_fwd", "swa_bwd", "swa_bwd_workspace_size", "swa_step", "swa_step_workspace_size", "swa_fill",
 )
-__all__ += _BLOCK
+# The third library's binding (delta.py), likewise.
+_DELTA = (
+    "GDR_STATE_STEP", "GdrDims", "delta_lib", "delta_library_path", "delta_last_error",
+    "gdr_fwd", "gdr_step", "gdr_workspace_size",
+)
+__all__ += _BLOCK + _DELTA
 
 
 def __getattr__(name):
-    if name not in _BLOCK:
+    if name in _BLOCK:
+        from . import block as binding
+        names = _BLOCK
+    elif name in _DELTA:
+        from . import delta as binding
+        names = _DELTA
+    else:
         raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
-    from . import block
-    globals().update({n: getattr(block, n) for n in _BLOCK})
+    globals().update({n: getattr(binding, n) for n in names})
     return globals()[name]
 
 

@@ -1,11 +1,11 @@
-"""Build libssm.so and libssm_block.so (the HIP kernels and the C ABIs) in-tree
-for gfx950.
+"""Build libssm.so, libssm_block.so and libssm_delta.so (the HIP kernels and the
+C ABIs) in-tree for gfx950.
 
     python -m state_space_model_ssm_amd.build
 
 Each ``csrc/*.hip`` file is compiled with hipcc into ``_build/`` and linked
 into ``state_space_model_ssm_amd/libssm.so``; ``csrc/block/*.hip`` go into
-``libssm_block.so`` alike.  Packed-FP32 instructions are disabled for all
+``libssm_block.so`` and ``csrc/delta/*.hip`` into ``libssm_delta.so`` alike.  Packed-FP32 instructions are disabled for all
 device code.
 """
 from __future__ import annotations
@@ -23,6 +23,8 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libssm.so")
 BLOCK_CSRC = os.path.join(CSRC, "block")
 BLOCK_LIB = os.path.join(PKG, "libssm_block.so")
+DELTA_CSRC = os.path.join(CSRC, "delta")
+DELTA_LIB = os.path.join(PKG, "libssm_delta.so")
 ARCH = "gfx950"
 
 HIPCC = os.environ.get("HIPCC", shutil.which("hipcc") or "/opt/rocm/bin/hipcc")
@@ -43,11 +45,11 @@ def sources(folder: str = CSRC) -> list[str]:
 
 
 def build(verbose: bool = False) -> str:
-    """Compile every source and link both libraries. Returns libssm's path."""
+    """Compile every source and link the libraries. Returns libssm's path."""
     os.makedirs(BUILD, exist_ok=True)
-    objects = {LIB: sources(), BLOCK_LIB: sources(BLOCK_CSRC)}
+    objects = {LIB: sources(), BLOCK_LIB: sources(BLOCK_CSRC), DELTA_LIB: sources(DELTA_CSRC)}
     procs = []
-    for src in objects[LIB] + objects[BLOCK_LIB]:
+    for src in [src for srcs in objects.values() for src in srcs]:
         obj = _object(src)
         cmd = [HIPCC, *CFLAGS, "-c", src, "-o", obj]
         if verbose:

@@ -1,0 +1,443 @@
+// Gated delta rule, forward and single tokens, for gfx950.
+#include <type_traits>
+
+#include "gdr_tile.h"
+
+namespace ssmb {
+namespace {
+
+// ---------------------------------------------------------------------------
+// Within a chunk
+// ---------------------------------------------------------------------------
+
+template <typename G>
+__device__ __forceinline__ float gate(const void *p, int64_t i) { return ld(static_cast<const G *>(p), i); }
+
+constexpr int kPitch = 68, kDiagPitch = 20;  // floats between rows in LDS: 16-byte aligned, rows on other banks
+
+// Call f with the wavefront's number as a constant.  Each wavefront's products
+// are straight code then: the compiler leaves out the wait between a matrix
+// product and a read of its result where a branch by a wavefront's number lies
+// between them.
+template <typename F>
+__device__ __forceinline__ void by_wave(int w, F &&f) {
+  switch (w) {
+    case 0: f(std::integral_constant<int, 0>{}); break;
+    case 1: f(std::integral_constant<int, 1>{}); break;
+    case 2: f(std::integral_constant<int, 2>{}); break;
+    default: f(std::integral_constant<int, 3>{}); break;
+  }
+}
+
+// Store row block W of a lower triangle, transposed D results, as fragments in two parts.
+template <int W>
+__device__ __forceinline__ void store_rows(const f4v (&t)[W + 1], u4 *to, int lane) {
+#pragma unroll
+  for (int s = 0; 2 * s <= W; ++s) {
+    const Parts x = parts(t[2 * s], 2 * s + 1 <= W ? t[2 * s + 1 <= W ? 2 * s + 1 : 0] : f4v{});
+    to[tri(W, s) * 64 + lane] = __builtin_bit_cast(u4, x.hi);
+    to[(kGdrFrags + tri(W, s)) * 64 + lane] = __builtin_bit_cast(u4, x.lo);
+  }
+}
+
+// One workgroup per chunk and value head, one wavefront per 16 of its tokens.
+template <int KD, typename G>
+__global__ void __launch_bounds__(256) gdr_chunk_kernel(const GdrParams p) {
+  __shared__ double sums[64];                       // log2 of the decay up to each token
+  __shared__ float betas[64];
+  __shared__ __align__(16) float low[64 * kPitch];  // L^T
+  __shared__ __align__(16) float diag[64 * kDiagPitch];  // (the blocks of T on the diagonal)^T
+  const int tid = threadIdx.x, lane = tid & 63, m = lane & 15, g = lane >> 4;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int64_t id = blockIdx.x, c = id % p.chunks, bh = id / p.chunks, b = bh / p.nheads, h = bh % p.nheads;
+  const int t0 = static_cast<int>(c) * 64, len = gdr_length(p.lengths, b, p.seqlen) - t0;
+  if (len <= 0) return;
+  char *ws = p.ws + id * static_cast<int64_t>(kGdrChunkBytes);
+  constexpr int NS = KD / 32;
+  const int64_t hk = h / (p.nheads / p.nqk);
+  const uint16_t *kp = p.k + b * p.k_batch + t0 * p.k_token + hk * KD + 8 * g;
+  const uint16_t *qp = p.q + b * p.q_batch + t0 * p.q_token + hk * KD + 8 * g;
+  const int i = 16 * w + m, ri = i < len ? i : len - 1;  // rows past the length repeat the last one
+  bf8 ki[NS], qi[NS];
+#pragma unroll
+  for (int a = 0; a < NS; ++a) {
+    ki[a] = *reinterpret_cast<const bf8 *>(kp + ri * p.k_token + 32 * a);
+    qi[a] = *reinterpret_cast<const bf8 *>(qp + ri * p.q_token + 32 * a);
+  }
+  if (w == 0) {
+    const int64_t at = (b * p.seqlen + t0 + lane) * p.nheads + h;
+    float gt = 0.0f, bt = 0.0f;
+    if (lane < len) {
+      gt = gate<G>(p.g, at);
+      gt = gt < -200.0f ? -200.0f : gt;  // exp(-200) is 0, and differences of the sums stay finite
+      bt = gate<G>(p.beta, at);
+    }
+    // In float64: after a strong decay the differences of later tokens' sums would lose what they have.
+    double s = static_cast<double>(gt) * 1.4426950408889634;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+      const double up = __shfl_up(s, d);
+      if (lane >= d) s += up;
+    }
+    sums[lane] = s;
+    betas[lane] = bt;
+    const double last = __shfl(s, 63);
+    const float into = __builtin_amdgcn_exp2f(static_cast<float>(s));
+    float *gates = reinterpret_cast<float *>(ws + 2 * kGdrTriBytes);
+    gates[lane] = p.scale * into;
+    gates[64 + lane] = into;
+    gates[128 + lane] = __builtin_amdgcn_exp2f(static_cast<float>(last - s));
+    gates[192 + lane] = bt;
+  }
+  __syncthreads();
+  u4 *out = reinterpret_cast<u4 *>(ws);
+  // Products of keys with this wavefront's keys and queries, transposed: rows j, columns i = 16 w + m.
+  by_wave(w, [&](auto wave) {
+    constexpr int W = wave;
+    f4v kk[W + 1] = {}, att[W + 1] = {};
+#pragma unroll
+    for (int jb = 0; jb <= W; ++jb) {
+      const int j = 16 * jb + m, rj = j < len ? j : len - 1;
+#pragma unroll
+      for (int a = 0; a < NS; ++a) {
+        const bf8 kj = *reinterpret_cast<const bf8 *>(kp + rj * p.k_token + 32 * a);
+        kk[jb] = mfma16(kj, ki[a], kk[jb]);
+        att[jb] = mfma16(kj, qi[a], att[jb]);
+      }
+    }
+    const double si = sums[i];
+    const float bi = betas[i];
+#pragma unroll
+    for (int jb = 0; jb <= W; ++jb)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int j = 16 * jb + 4 * g + r;
+        const float decay = j <= i ? __builtin_amdgcn_exp2f(static_cast<float>(si - sums[j])) : 0.0f;
+        att[jb][r] = j <= i ? att[jb][r] * decay * p.scale : 0.0f;
+        low[j * kPitch + i] = j < i ? kk[jb][r] * decay * bi : 0.0f;
+      }
+    store_rows<W>(att, out + kGdrTriBytes / 16, lane);
+  });
+  __syncthreads();
+  // Blocks on the diagonal, all in one wavefront: lane (block g, column m) by substitution.
+  if (w == 0) {
+    float x[16];
+#pragma unroll
+    for (int k = 0; k < 16; ++k) x[k] = k == m ? 1.0f : 0.0f;
+#pragma unroll
+    for (int j = 0; j < 15; ++j) {
+      const float *col = low + (16 * g + j) * kPitch + 16 * g;
+#pragma unroll
+      for (int k = (j + 1) / 4; k < 4; ++k) {
+        const f4v l = *reinterpret_cast<const f4v *>(col + 4 * k);
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (4 * k + r > j) x[4 * k + r] = fmaf(-l[r], x[j], x[4 * k + r]);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      *reinterpret_cast<f4v *>(diag + lane * kDiagPitch + 4 * k) = f4v{x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]};
+  }
+  __syncthreads();
+  // The other blocks, right to left: T_Wj = -(sum over k > j of T_Wk L_kj) T_jj, in float32 and transposed.
+  by_wave(w, [&](auto wave) {
+    constexpr int W = wave;
+    f4v t[W + 1] = {};
+#pragma unroll
+    for (int r = 0; r < 4; ++r) t[W][r] = diag[(16 * W + 4 * g + r) * kDiagPitch + m];
+#pragma unroll
+    for (int j = W - 1; j >= 0; --j) {
+      f4v acc = {};
+#pragma unroll
+      for (int k = j + 1; k <= W; ++k) {
+        const f4v l = *reinterpret_cast<const f4v *>(low + (16 * j + m) * kPitch + 16 * k + 4 * g);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) acc = mfma_f32(l[r], t[k][r], acc);
+      }
+      const f4v d = *reinterpret_cast<const f4v *>(diag + (16 * j + m) * kDiagPitch + 4 * g);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) t[j] = mfma_f32(-d[r], acc[r], t[j]);
+    }
+    store_rows<W>(t, out, lane);
+  });
+}
+
+// ---------------------------------------------------------------------------
+// From chunk to chunk
+// ---------------------------------------------------------------------------
+
+// All but the last N of this wavefront's copies and stores are done, then all wavefronts meet.
+template <int N>
+__device__ __forceinline__ void arrive() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+
+// LDS slot of a tile of 64 rows of NC values.
+template <int NC>
+__device__ __forceinline__ int vslot(int r, int c) {
+  if constexpr (NC == 32) return r * 4 + c;
+  else return slot<NC>(r, c);
+}
+
+// A workgroup takes 16 CT NW columns (value elements) of a head from chunk to
+// chunk, a wavefront 16 CT of them.
+template <int KD, int CT, int NW>
+__global__ void __launch_bounds__(64 * NW) gdr_fwd_kernel(const GdrParams p) {
+  constexpr int NT = 64 * NW, NC = 16 * CT * NW, NS = KD / 32, NB = KD / 16;
+  constexpr unsigned kRows = 64 * KD * 2, kValues = 64 * NC * 2;
+  constexpr unsigned kAtQ = kRows, kAtV = 2 * kRows, kAtW = kAtV + kValues, kBuffer = kAtW + kGdrChunkBytes;
+  __shared__ __align__(16) u4 lds[2 * kBuffer / 16];
+  const int tid = threadIdx.x, lane = tid & 63, m = lane & 15, g = lane >> 4;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const unsigned vtiles = static_cast<unsigned>(p.vdim) / NC;
+  const int64_t vt = blockIdx.x % vtiles, bh = blockIdx.x / vtiles, b = bh / p.nheads, h = bh % p.nheads;
+  const int len = gdr_length(p.lengths, b, p.seqlen), n = (len + 63) / 64;
+  const int64_t hk = h / (p.nheads / p.nqk);
+  const int col = static_cast<int>(vt) * NC + 16 * CT * w + m;
+  const uint16_t *kp = p.k + b * p.k_batch + hk * KD, *qp = p.q + b * p.q_batch + hk * KD;
+  const uint16_t *vp = p.v + b * p.v_batch + h * p.vdim + vt * NC;
+  const char *ws = p.ws + bh * p.chunks * static_cast<int64_t>(kGdrChunkBytes);
+  const unsigned base = lds_at(lds);
+  const Lanes16 at = lanes16_of<KD>(lane);
+
+  auto fetch = [&](int c) {
+    u4 *to = lds + (c & 1) * (kBuffer / 16);
+    load_tile<KD, NT>(to, kp, p.k_token, 64 * c, len - 1, tid);
+    load_tile<KD, NT>(to + kAtQ / 16, qp, p.q_token, 64 * c, len - 1, tid);
+    const uint16_t *v0 = vp + 64 * c * p.v_token;
+    const unsigned vl = __builtin_amdgcn_readfirstlane(base + (c & 1) * kBuffer + kAtV + (tid & ~63) * 16);
+    const int last = len - 1 - 64 * c;
+#pragma unroll
+    for (int k = 0; k < 64 * NC / 8 / NT; ++k) {
+      const int id = k * NT + tid, r = id / (NC / 8), e = vslot<NC>(r, id % (NC / 8)) - r * (NC / 8);
+      copy16(vl + k * NT * 16, v0, static_cast<unsigned>(r < last ? r : last) * static_cast<unsigned>(p.v_token) * 2 + e * 16);
+    }
+    const char *wc = ws + c * static_cast<int64_t>(kGdrChunkBytes);
+    for (int k = w; k < static_cast<int>(kGdrChunkBytes / 1024); k += NW)
+      copy16(__builtin_amdgcn_readfirstlane(base + (c & 1) * kBuffer + kAtW + k * 1024), wc, k * 1024 + lane * 16);
+  };
+
+  if (n > 0) fetch(0);
+  // The state: column `col` + 16 t, key elements 32 a + 8g + 4x + r.
+  f4v s[CT][NB];
+  const int64_t state = (bh * p.vdim + col) * KD + 8 * g;
+#pragma unroll
+  for (int t = 0; t < CT; ++t)
+#pragma unroll
+    for (int j = 0; j < NB; ++j)
+      s[t][j] = p.h0 != nullptr ? *reinterpret_cast<const f4v *>(p.h0 + state + t * 16 * KD + 32 * (j / 2) + 4 * (j % 2)) : f4v{};
+  uint16_t *yp = p.y + (b * p.seqlen * p.nheads + h) * p.vdim + col;
+  const int64_t yt = p.nheads * p.vdim;
+
+  for (int c = 0; c < n; ++c) {
+    if (p.states != nullptr) {
+      float *to = p.states + ((bh * p.chunks + c) * p.vdim + col) * KD + 8 * g;
+#pragma unroll
+      for (int t = 0; t < CT; ++t)
+#pragma unroll
+        for (int j = 0; j < NB; ++j) *reinterpret_cast<f4v *>(to + t * 16 * KD + 32 * (j / 2) + 4 * (j % 2)) = s[t][j];
+    }
+    arrive<0>();
+    if (c + 1 < n) fetch(c + 1);
+    const unsigned tile = base + (c & 1) * kBuffer, gates = tile + kAtW + 2 * kGdrTriBytes + 16 * g;
+    f4v x[CT][4] = {}, o[CT][4] = {};
+#pragma unroll
+    for (int a = 0; a < NS; ++a) {
+      Parts sp[CT];
+#pragma unroll
+      for (int t = 0; t < CT; ++t) sp[t] = parts(s[t][2 * a], s[t][2 * a + 1]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const bf8 ka = row16<KD>(tile, i, a, at), qa = row16<KD>(tile + kAtQ, i, a, at);
+#pragma unroll
+        for (int t = 0; t < CT; ++t) {
+          x[t][i] = mul_exact(ka, sp[t], x[t][i]);
+          o[t][i] = mul_exact(qa, sp[t], o[t][i]);
+        }
+      }
+    }
+    // beta (v - e^G x), and e^G scale o
+    typedef __attribute__((address_space(3))) sh4 lds4;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const f4v qs = lds_f4(gates + 64 * i), into = lds_f4(gates + 256 + 64 * i), beta = lds_f4(gates + 768 + 64 * i);
+#pragma unroll
+      for (int t = 0; t < CT; ++t) {
+        const int r0 = 16 * i + 4 * g + (m >> 2), piece = 4 * (CT * w + t) + (m & 3);
+        const sh4 v = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+            (lds4 *)(tile + kAtV + vslot<NC>(r0, piece >> 1) * 16 + (piece & 1) * 8));
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const float vf = __uint_as_float(static_cast<unsigned>(static_cast<uint16_t>(v[r])) << 16);
+          x[t][i][r] = beta[r] * fmaf(-into[r], x[t][i][r], vf);
+          o[t][i][r] *= qs[r];
+        }
+      }
+    }
+    // u = T x
+    f4v u[CT][4] = {};
+    const unsigned tri_t = tile + kAtW, tri_a = tri_t + kGdrTriBytes;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      Parts xp[CT];
+#pragma unroll
+      for (int t = 0; t < CT; ++t) xp[t] = parts(x[t][2 * k], x[t][2 * k + 1]);
+#pragma unroll
+      for (int i = 2 * k; i < 4; ++i) {
+        const Parts ta = {frag16(tri_t, tri(i, k), lane), frag16(tri_t, kGdrFrags + tri(i, k), lane)};
+#pragma unroll
+        for (int t = 0; t < CT; ++t) u[t][i] = mul_parts(ta, xp[t], u[t][i]);
+      }
+    }
+    // o += A u
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      Parts up[CT];
+#pragma unroll
+      for (int t = 0; t < CT; ++t) up[t] = parts(u[t][2 * k], u[t][2 * k + 1]);
+#pragma unroll
+      for (int i = 2 * k; i < 4; ++i) {
+        const Parts aa = {frag16(tri_a, tri(i, k), lane), frag16(tri_a, kGdrFrags + tri(i, k), lane)};
+#pragma unroll
+        for (int t = 0; t < CT; ++t) o[t][i] = mul_parts(aa, up[t], o[t][i]);
+      }
+    }
+    // s = e^GC s + sum over tokens of k (e^(GC - G) u)
+    const float whole = lds_f4(tile + kAtW + 2 * kGdrTriBytes + 256 + 240)[3];
+#pragma unroll
+    for (int t = 0; t < CT; ++t)
+#pragma unroll
+      for (int j = 0; j < NB; ++j) s[t][j] *= whole;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      Parts up[CT];
+      const f4v o0 = lds_f4(gates + 512 + 128 * k), o1 = lds_f4(gates + 512 + 128 * k + 64);
+#pragma unroll
+      for (int t = 0; t < CT; ++t) up[t] = parts(u[t][2 * k] * o0, u[t][2 * k + 1] * o1);
+#pragma unroll
+      for (int j = 0; j < NB; ++j) {
+        const bf8 kt = col16<KD>(tile, j, k, at);
+#pragma unroll
+        for (int t = 0; t < CT; ++t) s[t][j] = mul_exact(kt, up[t], s[t][j]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int64_t row = 64 * static_cast<int64_t>(c) + 16 * i + 4 * g + r;
+        if (row < p.seqlen)
+#pragma unroll
+          for (int t = 0; t < CT; ++t) st(yp, row * yt + 16 * t, row < len ? o[t][i][r] : 0.0f);
+      }
+  }
+  for (int64_t row = 64 * static_cast<int64_t>(n) + g; row < p.seqlen; row += 4)
+#pragma unroll
+    for (int t = 0; t < CT; ++t) st(yp, row * yt + 16 * t, 0.0f);
+  if (p.h_last != nullptr) {
+#pragma unroll
+    for (int t = 0; t < CT; ++t)
+#pragma unroll
+      for (int j = 0; j < NB; ++j)
+        *reinterpret_cast<f4v *>(p.h_last + state + t * 16 * KD + 32 * (j / 2) + 4 * (j % 2)) = s[t][j];
+  }
+}
+
+// ---------------------------------------------------------------------------
+// One token
+// ---------------------------------------------------------------------------
+
+// Sum over the 8 (KD = 128: 128 = 8 lanes of 16) lanes that share a row.
+__device__ __forceinline__ float sum8(float v) {
+  v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0xB1, 0xf, 0xf, true));   // lanes 1 apart
+  v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x4E, 0xf, 0xf, true));   // 2 apart
+  v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x141, 0xf, 0xf, true));  // the other half of 8
+  return v;
+}
+
+// 8 lanes share a row of the state (a value element), 32 R rows a workgroup.
+template <int KD, int R, typename G>
+__global__ void __launch_bounds__(256) gdr_step_kernel(const GdrParams p) {
+  constexpr int NP = KD / 32;  // pieces of 4 floats per lane
+  const int tid = threadIdx.x, e = tid & 7;
+  const unsigned vtiles = static_cast<unsigned>(p.vdim) / (32 * R);
+  const int64_t vt = blockIdx.x % vtiles, bh = blockIdx.x / vtiles, b = bh / p.nheads, h = bh % p.nheads;
+  const int64_t hk = h / (p.nheads / p.nqk);
+  const int row0 = static_cast<int>(vt) * 32 * R + (tid >> 3);
+  f4v s[R][NP], k[NP], q[NP];
+  const float *from = p.h0 + (bh * p.vdim + row0) * KD + 4 * e;
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int a = 0; a < NP; ++a) s[r][a] = *reinterpret_cast<const f4v *>(from + r * 32 * KD + 32 * a);
+  float kq = 0.0f;
+#pragma unroll
+  for (int a = 0; a < NP; ++a) {
+    const uint2 kb = *reinterpret_cast<const uint2 *>(p.k + b * p.k_batch + hk * KD + 32 * a + 4 * e);
+    const uint2 qb = *reinterpret_cast<const uint2 *>(p.q + b * p.q_batch + hk * KD + 32 * a + 4 * e);
+    k[a] = f4v{__uint_as_float(kb.x << 16), __uint_as_float(kb.x & 0xffff0000u), __uint_as_float(kb.y << 16),
+               __uint_as_float(kb.y & 0xffff0000u)};
+    q[a] = f4v{__uint_as_float(qb.x << 16), __uint_as_float(qb.x & 0xffff0000u), __uint_as_float(qb.y << 16),
+               __uint_as_float(qb.y & 0xffff0000u)};
+#pragma unroll
+    for (int r = 0; r < 4; ++r) kq = fmaf(k[a][r], q[a][r], kq);
+  }
+  kq = sum8(kq);
+  const float decay = __builtin_amdgcn_exp2f(gate<G>(p.g, bh) * kLog2e), beta = gate<G>(p.beta, bh);
+  float *to = p.h_last + (bh * p.vdim + row0) * KD + 4 * e;
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    float sk = 0.0f, sq = 0.0f;
+#pragma unroll
+    for (int a = 0; a < NP; ++a)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        sk = fmaf(s[r][a][i], k[a][i], sk);
+        sq = fmaf(s[r][a][i], q[a][i], sq);
+      }
+    sk = sum8(sk);
+    sq = sum8(sq);
+    const float v = ld(p.v, b * p.v_batch + h * p.vdim + row0 + 32 * r);
+    const float u = beta * fmaf(-decay, sk, v);
+#pragma unroll
+    for (int a = 0; a < NP; ++a) *reinterpret_cast<f4v *>(to + r * 32 * KD + 32 * a) = s[r][a] * decay + k[a] * u;
+    if (e == 0) st(p.y, bh * p.vdim + row0 + 32 * r, p.scale * fmaf(decay, sq, u * kq));
+  }
+}
+
+template <int KD, typename G>
+hipError_t fwd(const GdrParams &p, hipStream_t s) {
+  const int64_t heads = p.batch * p.nheads;
+  if (p.chunks > 0) hipLaunchKernelGGL((gdr_chunk_kernel<KD, G>), dim3(static_cast<uint32_t>(heads * p.chunks)), dim3(256), 0, s, p);
+  hipLaunchKernelGGL((gdr_fwd_kernel<KD, 1, 4>), dim3(static_cast<uint32_t>(heads * (p.vdim / 64))), dim3(256), 0, s, p);
+  return hipGetLastError();
+}
+
+template <int KD, typename G>
+hipError_t step(const GdrParams &p, hipStream_t s) {
+  const int64_t heads = p.batch * p.nheads;
+  if (heads * (p.vdim / 32) < 2048)
+    hipLaunchKernelGGL((gdr_step_kernel<KD, 1, G>), dim3(static_cast<uint32_t>(heads * (p.vdim / 32))), dim3(256), 0, s, p);
+  else
+    hipLaunchKernelGGL((gdr_step_kernel<KD, 2, G>), dim3(static_cast<uint32_t>(heads * (p.vdim / 64))), dim3(256), 0, s, p);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+size_t gdr_workspace(const GdrParams &p) {
+  return static_cast<size_t>(p.batch) * p.nheads * p.chunks * kGdrChunkBytes;
+}
+
+hipError_t launch_gdr_fwd(const GdrParams &p, hipStream_t s) {
+  if (p.kdim == 64) return p.gates_bf16 ? fwd<64, uint16_t>(p, s) : fwd<64, float>(p, s);
+  return p.gates_bf16 ? fwd<128, uint16_t>(p, s) : fwd<128, float>(p, s);
+}
+
+hipError_t launch_gdr_step(const GdrParams &p, hipStream_t s) {
+  if (p.kdim == 64) return p.gates_bf16 ? step<64, uint16_t>(p, s) : step<64, float>(p, s);
+  return p.gates_bf16 ? step<128, uint16_t>(p, s) : step<128, float>(p, s);
+}
+
+}  // namespace ssmb

@@ -1,0 +1,103 @@
+// Matrix-core operands of the gated delta rule's kernels.
+//
+// v_mfma_f32_16x16x32_bf16, lane l with m = l % 16, g = l / 16: A holds row m,
+// k = 8g .. 8g + 7; B column m, the same k; D column m, rows 4g + r in
+// register r.  Two D results, rows 0 .. 15 and 16 .. 31 of 32, become the next
+// product's B without crossing lanes when k is counted in their order: element
+// e of lane group g stands for row 16 (e / 4) + 4g + e % 4 of the 32, and A is
+// read, or was stored, in that order ("D's order").  So a column of a chunk's
+// products and of the state stays in its lanes from one chunk to the next:
+// the state is a D result whose rows are key elements (32 a + 8g + 4x + r in
+// register r of block 2a + x, which makes them B's plain order), the products
+// of a chunk have the tokens as rows.
+//
+// A float32 factor enters a product as two bfloat16 parts that hold it to
+// 2^-18 of its size; products of two such factors leave out the smallest term.
+// q, k, v and dy are bfloat16 already and enter as they are.
+#pragma once
+
+#include "gdr_internal.h"
+#include "block/swa_tile.h"
+
+namespace ssmb {
+
+typedef __attribute__((ext_vector_type(4))) float f4v;
+
+__device__ __forceinline__ f4v mfma16(bf8 a, bf8 b, f4v c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f4v mfma_f32(float a, float b, f4v c) {  // 16x16x4: k = lane / 16
+  return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0);
+}
+
+// Eight float32 values as an operand, and what that rounded off as another.
+struct Parts {
+  bf8 hi, lo;
+};
+__device__ __forceinline__ Parts parts(const f4v &a, const f4v &b) {
+  Parts p;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) p.hi[e] = static_cast<__bf16>(e < 4 ? a[e % 4] : b[e % 4]);
+  const u4 bits = __builtin_bit_cast(u4, p.hi);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float up = __uint_as_float(e % 2 != 0 ? bits[e / 2] & 0xffff0000u : bits[e / 2] << 16);
+    p.lo[e] = static_cast<__bf16>((e < 4 ? a[e % 4] : b[e % 4]) - up);
+  }
+  return p;
+}
+
+// c + a b for a factor in parts and an exact one, or two in parts.
+__device__ __forceinline__ f4v mul_exact(bf8 a, const Parts &b, f4v c) { return mfma16(a, b.lo, mfma16(a, b.hi, c)); }
+__device__ __forceinline__ f4v mul_parts(const Parts &a, const Parts &b, f4v c) {
+  return mfma16(a.hi, b.hi, mfma16(a.hi, b.lo, mfma16(a.lo, b.hi, c)));
+}
+
+// Where a lane reads in a tile of 64 rows of D elements laid out by slot<D>(),
+// in bytes: as row operand (rows m, elements 8g ..), and for transposing reads
+// of rows 4g .. 4g + 3 (elements 8 p .. of the tile's first 32, p = m % 4).
+struct Lanes16 {
+  unsigned row, col;
+};
+template <int D>
+__device__ __forceinline__ Lanes16 lanes16_of(int lane) {
+  const int m = lane & 15, g = lane >> 4;
+  return {static_cast<unsigned>(slot<D>(m, g)) * 16, static_cast<unsigned>(slot<D>(4 * g + (m >> 2), m & 3)) * 16};
+}
+
+// Operand of rows 16 i .., elements 32 a + 8g ..
+template <int D>
+__device__ __forceinline__ bf8 row16(unsigned tile, int i, int a, const Lanes16 &at) {
+  typedef __attribute__((address_space(3))) const u4 lds16;
+  return __builtin_bit_cast(bf8, *(lds16 *)(((tile + at.row) ^ (64 * a)) + i * 32 * D));
+}
+// Transposed operand: rows are the elements of the state's block j (32 (j / 2)
+// + 8 (m / 4) + 4 (j % 2) + m % 4), k the tile's rows 32 s .. in D's order.
+template <int D>
+__device__ __forceinline__ bf8 col16(unsigned tile, int j, int s, const Lanes16 &at) {
+  typedef __attribute__((address_space(3))) sh4 lds4;
+  const unsigned to = ((tile + at.col) ^ (64 * (j / 2))) + 8 * (j % 2) + s * 64 * D;
+  const sh4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)(to));
+  const sh4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)(to + 32 * D));
+  return __builtin_bit_cast(bf8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+// The operand that was stored as fragment f of 1024 bytes.
+__device__ __forceinline__ bf8 frag16(unsigned tile, int f, int lane) {
+  typedef __attribute__((address_space(3))) const u4 lds16;
+  return __builtin_bit_cast(bf8, *(lds16 *)(tile + f * 1024 + lane * 16));
+}
+__device__ __forceinline__ f4v lds_f4(unsigned at) {
+  typedef __attribute__((address_space(3))) const f4v lds16;
+  return *(lds16 *)(at);
+}
+
+// Fragment of a lower triangle: row block i (of 16), columns 32 s ..
+__host__ __device__ constexpr int tri(int i, int s) { return i < 2 ? i : 2 * (i - 1) + s; }
+
+__device__ __forceinline__ int gdr_length(const int32_t *lengths, int64_t b, int64_t seqlen) {
+  if (lengths == nullptr) return static_cast<int>(seqlen);
+  const int n = lengths[b], L = static_cast<int>(seqlen);
+  return n < 0 ? 0 : n > L ? L : n;
+}
+
+}  // namespace ssmb
