@@ -35,7 +35,7 @@ _BLOCK = (
 # The third library's binding (delta.py), likewise.
 _DELTA = (
     "GDR_STATE_STEP", "GdrDims", "delta_lib", "delta_library_path", "delta_last_error",
-    "gdr_fwd", "gdr_step", "gdr_workspace_size",
+    "gdr_fwd", "gdr_bwd", "gdr_step", "gdr_workspace_size", "gdr_bwd_workspace_size",
 )
 __all__ += _BLOCK + _DELTA
 

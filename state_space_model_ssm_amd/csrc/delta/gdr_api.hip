@@ -121,6 +121,63 @@ int ssm_gdr_fwd(const void *q, const void *k, const void *v, const void *g, cons
   return launched(launch_gdr_fwd(p, static_cast<hipStream_t>(stream)), "gdr_fwd");
 }
 
+int ssm_gdr_bwd_workspace_size(const ssm_gdr_dims_t *dims, size_t *bytes) {
+  if (!bytes) return fail(SSM_ERR_NULL, "bytes is NULL");
+  const int rc = check_gdr(dims, false);
+  if (rc != SSM_OK) return rc;
+  const GdrBwdSizes n = gdr_bwd_sizes(params(*dims));
+  *bytes = n.chunks + n.ds + n.e;
+  return ok();
+}
+
+int ssm_gdr_bwd(const void *q, const void *k, const void *v, const void *g, const void *beta, const int32_t *lengths,
+                const float *states, const void *dy, const float *dh_last, void *dq, void *dk, void *dv, void *dg,
+                void *dbeta, float *dh0, const ssm_gdr_dims_t *dims, void *stream) {
+  int rc = check_gdr(dims, false);
+  if (rc != SSM_OK) return rc;
+  const ssm_gdr_dims_t &d = *dims;
+  GdrParams p = params(d);
+  const size_t eg = dtype_size(d.gate_dtype), rows = static_cast<size_t>(d.batch) * d.seqlen;
+  const size_t state = static_cast<size_t>(d.batch) * d.nheads * d.vdim * d.kdim * 4;
+  const GdrBwdSizes n = gdr_bwd_sizes(p);
+  const Arg ins[] = {{"q", q, span(d, d.q_batch, d.q_token, d.nqk * d.kdim), 16, true},
+                     {"k", k, span(d, d.k_batch, d.k_token, d.nqk * d.kdim), 16, true},
+                     {"v", v, span(d, d.v_batch, d.v_token, d.nheads * d.vdim), 16, true},
+                     {"g", g, rows * d.nheads * eg, eg, true},
+                     {"beta", beta, rows * d.nheads * eg, eg, true},
+                     {"lengths", lengths, static_cast<size_t>(d.batch) * 4, 4, false},
+                     {"states", states, state * p.chunks, 16, true},
+                     {"dy", dy, rows * d.nheads * d.vdim * 2, 16, true},
+                     {"dh_last", dh_last, state, 16, false},
+                     {"workspace", d.workspace, d.workspace ? d.workspace_bytes : 0, 1, false}};
+  const Arg outs[] = {{"dq", dq, rows * d.nqk * d.kdim * 2, 16, true},   {"dk", dk, rows * d.nqk * d.kdim * 2, 16, true},
+                      {"dv", dv, rows * d.nheads * d.vdim * 2, 16, true}, {"dg", dg, rows * d.nheads * eg, eg, true},
+                      {"dbeta", dbeta, rows * d.nheads * eg, eg, true},  {"dh0", dh0, state, 16, false}};
+  const void *const same[6][2] = {};
+  rc = check_args(ins, outs, same);
+  if (rc == SSM_OK) rc = check_workspace(ins, n.chunks + n.ds + n.e);
+  if (rc != SSM_OK) return rc;
+  if (d.batch == 0 || (d.seqlen == 0 && dh0 == nullptr)) return ok();
+  p.q = static_cast<const uint16_t *>(q);
+  p.k = static_cast<const uint16_t *>(k);
+  p.v = static_cast<const uint16_t *>(v);
+  p.g = g;
+  p.beta = beta;
+  p.lengths = lengths;
+  p.states = const_cast<float *>(states);
+  p.dy = static_cast<const uint16_t *>(dy);
+  p.dh_last = dh_last;
+  p.dq = static_cast<uint16_t *>(dq);
+  p.dk = static_cast<uint16_t *>(dk);
+  p.dv = static_cast<uint16_t *>(dv);
+  p.dg = dg;
+  p.dbeta = dbeta;
+  p.dh0 = dh0;
+  p.ws_ds = reinterpret_cast<float *>(p.ws + n.chunks);
+  p.ws_e = reinterpret_cast<float *>(p.ws + n.chunks + n.ds);
+  return launched(launch_gdr_bwd(p, static_cast<hipStream_t>(stream)), "gdr_bwd");
+}
+
 int ssm_gdr_step(const void *q, const void *k, const void *v, const void *g, const void *beta, const float *h, void *y,
                  float *h_out, const ssm_gdr_dims_t *dims, void *stream) {
   int rc = check_gdr(dims, true);

@@ -1,0 +1,552 @@
+// Gated delta rule, backward, for gfx950.
+#include "gdr_tile.h"
+
+namespace ssmb {
+namespace {
+
+// ---------------------------------------------------------------------------
+// From chunk to chunk, the last one first: dS, and E = T^T dU, dv = beta E
+// ---------------------------------------------------------------------------
+
+template <int KD, int CT, int NW>
+__global__ void __launch_bounds__(64 * NW) gdr_bwd_kernel(const GdrParams p) {
+  constexpr int NT = 64 * NW, NC = 16 * CT * NW, NS = KD / 32, NB = KD / 16;
+  constexpr unsigned kRows = 64 * KD * 2, kValues = 64 * NC * 2, kTri = 2 * kGdrTriBytes, kOps = kTri + kGdrGateBytes;
+  constexpr unsigned kAtQ = kRows, kAtD = 2 * kRows, kAtW = kAtD + kValues, kBuffer = kAtW + kOps;
+  __shared__ __align__(16) u4 lds[2 * kBuffer / 16];
+  const int tid = threadIdx.x, lane = tid & 63, m = lane & 15, g = lane >> 4;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const unsigned vtiles = static_cast<unsigned>(p.vdim) / NC;
+  const int64_t vt = blockIdx.x % vtiles, bh = blockIdx.x / vtiles, b = bh / p.nheads, h = bh % p.nheads;
+  const int len = gdr_length(p.lengths, b, p.seqlen), n = (len + 63) / 64;
+  const int64_t hk = h / (p.nheads / p.nqk), yt = p.nheads * p.vdim;
+  const int col = static_cast<int>(vt) * NC + 16 * CT * w + m;
+  const uint16_t *kp = p.k + b * p.k_batch + hk * KD, *qp = p.q + b * p.q_batch + hk * KD;
+  const uint16_t *dp = p.dy + (b * p.seqlen * p.nheads + h) * p.vdim + vt * NC;
+  const char *ws = p.ws + bh * p.chunks * static_cast<int64_t>(kGdrBwdChunkBytes) + kGdrTriBytes;  // T^T, A^T, gates
+  const unsigned base = lds_at(lds);
+  const Lanes16 at = lanes16_of<KD>(lane);
+
+  auto fetch = [&](int c) {
+    u4 *to = lds + (c & 1) * (kBuffer / 16);
+    load_tile<KD, NT>(to, kp, p.k_token, 64 * c, len - 1, tid);
+    load_tile<KD, NT>(to + kAtQ / 16, qp, p.q_token, 64 * c, len - 1, tid);
+    const uint16_t *d0 = dp + 64 * c * yt;
+    const unsigned dl = __builtin_amdgcn_readfirstlane(base + (c & 1) * kBuffer + kAtD + (tid & ~63) * 16);
+    const int last = len - 1 - 64 * c;
+#pragma unroll
+    for (int k = 0; k < 64 * NC / 8 / NT; ++k) {
+      const int id = k * NT + tid, r = id / (NC / 8), e = vslot<NC>(r, id % (NC / 8)) - r * (NC / 8);
+      copy16(dl + k * NT * 16, d0, static_cast<unsigned>(r < last ? r : last) * static_cast<unsigned>(yt) * 2 + e * 16);
+    }
+    const char *wc = ws + c * static_cast<int64_t>(kGdrBwdChunkBytes);
+    for (int k = w; k < static_cast<int>(kOps / 1024); k += NW)
+      copy16(__builtin_amdgcn_readfirstlane(base + (c & 1) * kBuffer + kAtW + k * 1024), wc, k * 1024 + lane * 16);
+  };
+
+  if (n > 0) fetch(n - 1);
+  f4v s[CT][NB];  // dS, laid out as the state
+  const int64_t state = (bh * p.vdim + col) * KD + 8 * g;
+#pragma unroll
+  for (int t = 0; t < CT; ++t)
+#pragma unroll
+    for (int j = 0; j < NB; ++j)
+      s[t][j] = p.dh_last != nullptr
+                    ? *reinterpret_cast<const f4v *>(p.dh_last + state + t * 16 * KD + 32 * (j / 2) + 4 * (j % 2))
+                    : f4v{};
+  uint16_t *vp = p.dv + (b * p.seqlen * p.nheads + h) * p.vdim + col;
+
+  for (int c = n - 1; c >= 0; --c) {
+    float *to = p.ws_ds + ((bh * p.chunks + c) * p.vdim + col) * KD + 8 * g;
+#pragma unroll
+    for (int t = 0; t < CT; ++t)
+#pragma unroll
+      for (int j = 0; j < NB; ++j) *reinterpret_cast<f4v *>(to + t * 16 * KD + 32 * (j / 2) + 4 * (j % 2)) = s[t][j];
+    arrive<0>();
+    if (c > 0) fetch(c - 1);
+    const unsigned tile = base + (c & 1) * kBuffer, gates = tile + kAtW + kTri + 16 * g;
+    // K dS
+    f4v x[CT][4] = {};
+#pragma unroll
+    for (int a = 0; a < NS; ++a) {
+      Parts sp[CT];
+#pragma unroll
+      for (int t = 0; t < CT; ++t) sp[t] = parts(s[t][2 * a], s[t][2 * a + 1]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const bf8 ka = row16<KD>(tile, i, a, at);
+#pragma unroll
+        for (int t = 0; t < CT; ++t) x[t][i] = mul_exact(ka, sp[t], x[t][i]);
+      }
+    }
+    // dU = e^(GC - G) K dS + A^T dY
+    sh4 dy[CT][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const f4v out = lds_f4(gates + 512 + 64 * i);
+#pragma unroll
+      for (int t = 0; t < CT; ++t) {
+        x[t][i] *= out;
+        dy[t][i] = rows4<NC>(tile + kAtD, i, CT * w + t, lane);
+      }
+    }
+    const unsigned at_t = tile + kAtW, at_a = at_t + kGdrTriBytes;
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int j = 0; j <= 2 * k + 1; ++j) {
+        const Parts aa = {frag16(at_a, tri_t(j, k), lane), frag16(at_a, kGdrFrags + tri_t(j, k), lane)};
+#pragma unroll
+        for (int t = 0; t < CT; ++t) {
+          const bf8 d = __builtin_bit_cast(bf8, __builtin_shufflevector(dy[t][2 * k], dy[t][2 * k + 1], 0, 1, 2, 3, 4, 5, 6, 7));
+          x[t][j] = mfma16(aa.hi, d, mfma16(aa.lo, d, x[t][j]));
+        }
+      }
+    // E = T^T dU
+    f4v e[CT][4] = {};
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      Parts xp[CT];
+#pragma unroll
+      for (int t = 0; t < CT; ++t) xp[t] = parts(x[t][2 * k], x[t][2 * k + 1]);
+#pragma unroll
+      for (int j = 0; j <= 2 * k + 1; ++j) {
+        const Parts ta = {frag16(at_t, tri_t(j, k), lane), frag16(at_t, kGdrFrags + tri_t(j, k), lane)};
+#pragma unroll
+        for (int t = 0; t < CT; ++t) e[t][j] = mul_parts(ta, xp[t], e[t][j]);
+      }
+    }
+    // dS = e^GC dS + sum over tokens of q (scale e^G dy) - k (e^G beta E)
+    const float whole = lds_f4(tile + kAtW + kTri + 256 + 240)[3];
+#pragma unroll
+    for (int t = 0; t < CT; ++t)
+#pragma unroll
+      for (int j = 0; j < NB; ++j) s[t][j] *= whole;
+    float *eo = p.ws_e + (bh * p.chunks + c) * 64 * p.vdim + (vt * (NC / 16) + CT * w) * 1024 + lane * 4;
+#pragma unroll
+    for (int t = 0; t < CT; ++t)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) *reinterpret_cast<f4v *>(eo + t * 1024 + i * 256) = e[t][i];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      Parts ep[CT], yp[CT];
+      f4v beta[2], into[2], qs[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        qs[i] = lds_f4(gates + 64 * (2 * k + i));
+        into[i] = lds_f4(gates + 256 + 64 * (2 * k + i));
+        beta[i] = lds_f4(gates + 768 + 64 * (2 * k + i));
+      }
+#pragma unroll
+      for (int t = 0; t < CT; ++t) {
+        f4v y[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          e[t][2 * k + i] *= beta[i];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) y[i][r] = up(dy[t][2 * k + i][r]) * qs[i][r];
+        }
+        ep[t] = parts(e[t][2 * k] * -into[0], e[t][2 * k + 1] * -into[1]);
+        yp[t] = parts(y[0], y[1]);
+      }
+#pragma unroll
+      for (int j = 0; j < NB; ++j) {
+        const bf8 kt = col16<KD>(tile, j, k, at), qt = col16<KD>(tile + kAtQ, j, k, at);
+#pragma unroll
+        for (int t = 0; t < CT; ++t) s[t][j] = mul_exact(qt, yp[t], mul_exact(kt, ep[t], s[t][j]));
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int64_t row = 64 * static_cast<int64_t>(c) + 16 * i + 4 * g + r;
+        if (row < p.seqlen)
+#pragma unroll
+          for (int t = 0; t < CT; ++t) st(vp, row * yt + 16 * t, row < len ? e[t][i][r] : 0.0f);
+      }
+  }
+  for (int64_t row = 64 * static_cast<int64_t>(n) + g; row < p.seqlen; row += 4)
+#pragma unroll
+    for (int t = 0; t < CT; ++t) st(vp, row * yt + 16 * t, 0.0f);
+  if (p.dh0 != nullptr) {
+#pragma unroll
+    for (int t = 0; t < CT; ++t)
+#pragma unroll
+      for (int j = 0; j < NB; ++j)
+        *reinterpret_cast<f4v *>(p.dh0 + state + t * 16 * KD + 32 * (j / 2) + 4 * (j % 2)) = s[t][j];
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Within a chunk: dq, dk, dg, dbeta
+// ---------------------------------------------------------------------------
+
+// Transposed operands of a tile of 64-column rows [value][token], in two
+// parts: lane m stands for token 16 i + m, k for values 32 s + 8g ..
+struct Pair {
+  unsigned hi, lo;  // where the tiles are
+};
+__device__ __forceinline__ bf8 tokens16(unsigned tile, int i, int s, unsigned col) {
+  typedef __attribute__((address_space(3))) sh4 lds4;
+  const unsigned to = ((tile + col) ^ (32 * i)) + s * 32 * 128;
+  const sh4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)(to));
+  const sh4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)((to ^ 16) + 4 * 128));
+  return __builtin_bit_cast(bf8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+__device__ __forceinline__ Parts tokens16(const Pair &t, int i, int s, unsigned col) {
+  return {tokens16(t.hi, i, s, col), tokens16(t.lo, i, s, col)};
+}
+
+// Operand of the elements 16 ct + m of a row-major tile, k its rows 32 s .. in D's order.
+template <int D>
+__device__ __forceinline__ bf8 elems16(unsigned tile, int ct, int s, int lane) {
+  return __builtin_bit_cast(bf8, __builtin_shufflevector(rows4<D>(tile, 2 * s, ct, lane), rows4<D>(tile, 2 * s + 1, ct, lane), 0,
+                                                         1, 2, 3, 4, 5, 6, 7));
+}
+
+// The sum over the 16 lanes of a row.
+__device__ __forceinline__ float sum16(float v) {
+  v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0xB1, 0xf, 0xf, true));
+  v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x4E, 0xf, 0xf, true));
+  v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x141, 0xf, 0xf, true));
+  v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x140, 0xf, 0xf, true));
+  return v;
+}
+
+__device__ __forceinline__ void store_gate(void *p, int64_t i, float v, float) { st(static_cast<float *>(p), i, v); }
+__device__ __forceinline__ void store_gate(void *p, int64_t i, float v, uint16_t) { st(static_cast<uint16_t *>(p), i, v); }
+
+// A workgroup per chunk and query head, over the value heads that share it; a
+// wavefront per 16 key elements.
+template <int KD, int VD, typename G>
+__global__ void __launch_bounds__(4 * KD) gdr_grad_kernel(const GdrParams p) {
+  constexpr int NW = KD / 16, NT = 64 * NW, NS = KD / 32, NV = VD / 32;
+  constexpr unsigned kRows = 64 * KD * 2, kAtQ = kRows, kAtD = 2 * kRows, kAtU = kAtD + 64 * VD * 2, kPart = VD * 128;
+  constexpr unsigned kFour = 4 * (4 * kPart > 4 * kGdrTriBytes ? kPart : kGdrTriBytes);
+  __shared__ __align__(16) u4 lds[(kAtU + kFour) / 16];
+  __shared__ float red[2][NW][64], whole[NW];
+  const int tid = threadIdx.x, lane = tid & 63, m = lane & 15, g = lane >> 4;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int64_t c = blockIdx.x % p.chunks, bk = blockIdx.x / p.chunks, b = bk / p.nqk, hk = bk % p.nqk;
+  const int64_t share = p.nheads / p.nqk;
+  const int t0 = static_cast<int>(c) * 64, len = gdr_length(p.lengths, b, p.seqlen) - t0;
+  const int rows = p.seqlen - t0 < 64 ? static_cast<int>(p.seqlen - t0) : 64;
+  uint16_t *dqp = p.dq + ((b * p.seqlen + t0) * p.nqk + hk) * KD + 16 * w + m;
+  uint16_t *dkp = p.dk + ((b * p.seqlen + t0) * p.nqk + hk) * KD + 16 * w + m;
+  const int64_t row_step = p.nqk * KD;
+  f4v tq[4] = {}, tk[4] = {};
+  if (len > 0) {
+    const unsigned base = lds_at(lds);
+    const Lanes16 atk = lanes16_of<KD>(lane), atv = lanes16_of<VD>(lane);
+    // Where this lane's pieces of transposed reads lie: row 8g + m / 4, tokens 4 (m % 4) ..
+    const unsigned col = static_cast<unsigned>(slot<64>(8 * g + (m >> 2), (m & 3) >> 1)) * 16 + (m & 1) * 8;
+    const Pair U = {base + kAtU, base + kAtU + kPart}, D = {base + kAtU + 2 * kPart, base + kAtU + 3 * kPart};
+    load_tile<KD, NT>(lds, p.k + b * p.k_batch + hk * KD, p.k_token, t0, t0 + len - 1, tid);
+    load_tile<KD, NT>(lds + kAtQ / 16, p.q + b * p.q_batch + hk * KD, p.q_token, t0, t0 + len - 1, tid);
+    for (int64_t h = hk * share; h < (hk + 1) * share; ++h) {
+      const int64_t bh = b * p.nheads + h, id = bh * p.chunks + c, yt = p.nheads * VD;
+      const char *ws = p.ws + id * static_cast<int64_t>(kGdrBwdChunkBytes);
+      const float *gates = reinterpret_cast<const float *>(ws + 3 * kGdrTriBytes);
+      const double *sums = reinterpret_cast<const double *>(gates + 256);
+      arrive<0>();  // what the last head left in LDS has been read
+      load_tile<VD, NT>(lds + kAtD / 16, p.dy + (b * p.seqlen * p.nheads + h) * VD, yt, t0, t0 + len - 1, tid);
+      arrive<0>();
+      // U = T beta (V - e^G K S0), a wavefront per 16 values; U and D = beta E go to LDS in parts.
+      float db[4][4] = {};
+      for (int ct = w; ct < VD / 16; ct += NW) {
+        f4v x[4] = {};
+        const float *s0 = p.states + (id * VD + 16 * ct + m) * KD + 8 * g;
+#pragma unroll
+        for (int a = 0; a < NS; ++a) {
+          const Parts sp = parts(*reinterpret_cast<const f4v *>(s0 + 32 * a), *reinterpret_cast<const f4v *>(s0 + 32 * a + 4));
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x[i] = mul_exact(row16<KD>(base, i, a, atk), sp, x[i]);
+        }
+        const uint16_t *vp = p.v + b * p.v_batch + t0 * p.v_token + h * VD + 16 * ct + m;
+        f4v beta[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const f4v into = *reinterpret_cast<const f4v *>(gates + 64 + 16 * i + 4 * g);
+          beta[i] = *reinterpret_cast<const f4v *>(gates + 192 + 16 * i + 4 * g);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int row = 16 * i + 4 * g + r;
+            const float v = ld(vp, (row < len ? row : len - 1) * p.v_token);
+            x[i][r] = beta[i][r] * fmaf(-into[r], x[i][r], v);
+          }
+        }
+        f4v u[4] = {};
+        const u4 *tf = reinterpret_cast<const u4 *>(ws) + lane;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const Parts xp = parts(x[2 * k], x[2 * k + 1]);
+#pragma unroll
+          for (int i = 2 * k; i < 4; ++i) {
+            const Parts ta = {__builtin_bit_cast(bf8, tf[tri(i, k) * 64]), __builtin_bit_cast(bf8, tf[(kGdrFrags + tri(i, k)) * 64])};
+            u[i] = mul_parts(ta, xp, u[i]);
+          }
+        }
+        const float *ep = p.ws_e + id * 64 * VD + ct * 1024 + lane * 4;
+        f4v e[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          e[i] = *reinterpret_cast<const f4v *>(ep + i * 256);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) db[i][r] = fmaf(e[i][r], u[i][r] / beta[i][r], db[i][r]);
+          e[i] *= beta[i];
+        }
+        typedef __attribute__((address_space(3))) u2 lds8;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const Parts up = parts(u[2 * k], u[2 * k + 1]), dp = parts(e[2 * k], e[2 * k + 1]);
+#pragma unroll
+          for (int x2 = 0; x2 < 2; ++x2) {
+            const unsigned to = static_cast<unsigned>(slot<64>(16 * ct + m, 2 * (2 * k + x2) + (g >> 1))) * 16 + (g & 1) * 8;
+            *(lds8 *)(U.hi + to) = half_of(up.hi, x2);
+            *(lds8 *)(U.lo + to) = half_of(up.lo, x2);
+            *(lds8 *)(D.hi + to) = half_of(dp.hi, x2);
+            *(lds8 *)(D.lo + to) = half_of(dp.lo, x2);
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const float v = sum16(db[i][r]);
+          if (m == 0) red[0][w][16 * i + 4 * g + r] = v;
+        }
+      arrive<0>();
+      // Products over the values, a wavefront per 16 key elements.
+      f4v aq[4] = {}, ae[4] = {}, aw[4] = {};
+      float both = 0.0f;
+#pragma unroll
+      for (int s = 0; s < NV; ++s) {
+        const int64_t from = (id * VD + 32 * s + 8 * g) * KD + 16 * w + m;
+        f4v a[2], d[2];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          a[e / 4][e % 4] = p.states[from + e * KD];
+          d[e / 4][e % 4] = p.ws_ds[from + e * KD];
+          both = fmaf(a[e / 4][e % 4], d[e / 4][e % 4], both);
+        }
+        const Parts sp = parts(a[0], a[1]), dp = parts(d[0], d[1]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          aq[i] = mul_exact(row16<VD>(base + kAtD, i, s, atv), sp, aq[i]);
+          ae[i] = mul_parts(tokens16(D, i, s, col), sp, ae[i]);
+          aw[i] = mul_parts(tokens16(U, i, s, col), dp, aw[i]);
+        }
+      }
+      both *= gates[64 + 63];
+      sh4 kc[4], qc[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        kc[i] = rows4<KD>(base, i, w, lane);
+        qc[i] = rows4<KD>(base + kAtQ, i, w, lane);
+        const f4v qs = *reinterpret_cast<const f4v *>(gates + 16 * i + 4 * g);
+        const f4v into = *reinterpret_cast<const f4v *>(gates + 64 + 16 * i + 4 * g);
+        const f4v out = *reinterpret_cast<const f4v *>(gates + 128 + 16 * i + 4 * g);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          aq[i][r] *= qs[r];
+          ae[i][r] *= -into[r];
+          aw[i][r] *= out[r];
+          both = fmaf(up(kc[i][r]), aw[i][r], both);  // <S_C, dS> with what the chunk adds to S_C
+        }
+      }
+      // P = scale (dY U^T) M and H = -(D U^T) M within the chunk, and their transposes, as fragments.
+      u4 frag[2][2][4];  // [P or H of this wavefront][as it is or transposed][parts of 2 steps]
+      auto products = [&](auto wave, auto kind, u4 (&f)[2][4]) {
+        constexpr int W = wave;
+        constexpr bool HH = kind;
+        f4v lower[W + 1] = {}, upper[4 - W] = {};
+#pragma unroll
+        for (int s = 0; s < NV; ++s) {
+          const Parts uw = tokens16(U, W, s, col);
+          const Parts dw = HH ? tokens16(D, W, s, col) : Parts{row16<VD>(base + kAtD, W, s, atv), bf8{}};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            if (j <= W) {  // rows j, columns i = 16 W + m
+              const Parts uj = j == W ? uw : tokens16(U, j, s, col);
+              lower[j <= W ? j : 0] = HH ? mul_parts(uj, dw, lower[j <= W ? j : 0])
+                                         : mfma16(uj.hi, dw.hi, mfma16(uj.lo, dw.hi, lower[j <= W ? j : 0]));
+            }
+            if (j >= W) {  // rows i, columns j = 16 W + m
+              const Parts di = j == W ? dw : HH ? tokens16(D, j, s, col) : Parts{row16<VD>(base + kAtD, j, s, atv), bf8{}};
+              upper[j >= W ? j - W : 0] = HH ? mul_parts(di, uw, upper[j >= W ? j - W : 0])
+                                             : mul_exact(di.hi, uw, upper[j >= W ? j - W : 0]);
+            }
+          }
+        }
+        const int own = 16 * W + m;
+        const double so = sums[own];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int other = 16 * j + 4 * g + r;
+            const double st = sums[other];
+            if (j <= W) {  // i = own, j = other
+              const bool in = HH ? other < own : other <= own && own < len;
+              const float f = in ? (HH ? -1.0f : p.scale) * __builtin_amdgcn_exp2f(static_cast<float>(so - st)) : 0.0f;
+              lower[j <= W ? j : 0][r] = in ? lower[j <= W ? j : 0][r] * f : 0.0f;
+            }
+            if (j >= W) {
+              const bool in = HH ? own < other : own <= other && other < len;
+              const float f = in ? (HH ? -1.0f : p.scale) * __builtin_amdgcn_exp2f(static_cast<float>(st - so)) : 0.0f;
+              upper[j >= W ? j - W : 0][r] = in ? upper[j >= W ? j - W : 0][r] * f : 0.0f;
+            }
+          }
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          const f4v zero = {};
+          if (2 * s <= W) {
+            const Parts x = parts(lower[2 * s <= W ? 2 * s : 0], 2 * s + 1 <= W ? lower[2 * s + 1 <= W ? 2 * s + 1 : 0] : zero);
+            f[0][2 * s] = __builtin_bit_cast(u4, x.hi);
+            f[0][2 * s + 1] = __builtin_bit_cast(u4, x.lo);
+          }
+          if (2 * s + 1 >= W) {
+            const Parts x = parts(2 * s >= W ? upper[2 * s >= W ? 2 * s - W : 0] : zero, upper[2 * s + 1 >= W ? 2 * s + 1 - W : 0]);
+            f[1][2 * s] = __builtin_bit_cast(u4, x.hi);
+            f[1][2 * s + 1] = __builtin_bit_cast(u4, x.lo);
+          }
+        }
+      };
+      // Fragments of kind k in LDS: as they are at 2 k, transposed at 2 k + 1.
+      auto keep = [&](int W, int kind, const u4 (&f)[2][4]) {
+        u4 *to = lds + (kAtU + kind * 2 * kGdrTriBytes) / 16 + lane;
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          if (2 * s <= W) {
+            to[tri(W, s) * 64] = f[0][2 * s];
+            to[(kGdrFrags + tri(W, s)) * 64] = f[0][2 * s + 1];
+          }
+          if (2 * s + 1 >= W) {
+            to[kGdrTriBytes / 16 + tri_t(W, s) * 64] = f[1][2 * s];
+            to[kGdrTriBytes / 16 + (kGdrFrags + tri_t(W, s)) * 64] = f[1][2 * s + 1];
+          }
+        }
+      };
+      if constexpr (NW == 8) {
+        if (w < 4) by_wave(w, [&](auto wave) { products(wave, std::false_type{}, frag[0]); });
+        else by_wave(w - 4, [&](auto wave) { products(wave, std::true_type{}, frag[0]); });
+        arrive<0>();
+        keep(w & 3, w >> 2, frag[0]);
+      } else {
+        by_wave(w, [&](auto wave) {
+          products(wave, std::false_type{}, frag[0]);
+          products(wave, std::true_type{}, frag[1]);
+        });
+        arrive<0>();
+        keep(w, 0, frag[0]);
+        keep(w, 1, frag[1]);
+      }
+      arrive<0>();
+      const unsigned fp = base + kAtU, fh = fp + 2 * kGdrTriBytes;
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const bf8 kb = elems16<KD>(base, w, s, lane), qb = elems16<KD>(base + kAtQ, w, s, lane);
+        auto mul = [&](unsigned f, int k, bf8 x, f4v acc) {
+          return mfma16(frag16(f, k, lane), x, mfma16(frag16(f, kGdrFrags + k, lane), x, acc));
+        };
+#pragma unroll
+        for (int i = 2 * s; i < 4; ++i) {
+          aq[i] = mul(fp, tri(i, s), kb, aq[i]);
+          ae[i] = mul(fh, tri(i, s), kb, ae[i]);
+        }
+#pragma unroll
+        for (int j = 0; j <= 2 * s + 1; ++j) {
+          aw[j] = mul(fp + kGdrTriBytes, tri_t(j, s), qb, aw[j]);
+          aw[j] = mul(fh + kGdrTriBytes, tri_t(j, s), kb, aw[j]);
+        }
+      }
+      // d / dG, a term per token from each of q, the key that reads and the key that writes.
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const float v = sum16(fmaf(up(qc[i][r]), aq[i][r], up(kc[i][r]) * (ae[i][r] - aw[i][r])));
+          if (m == 0) red[1][w][16 * i + 4 * g + r] = v;
+        }
+        tq[i] += aq[i];
+        tk[i] += ae[i] + aw[i];
+      }
+      both = sum16(both);
+      both += __shfl_xor(both, 16);
+      both += __shfl_xor(both, 32);
+      if (lane == 0) whole[w] = both;
+      arrive<0>();
+      if (w == 0 && lane < rows) {
+        float dg = 0.0f, dbeta = 0.0f, total = 0.0f;
+#pragma unroll
+        for (int k = 0; k < NW; ++k) {
+          dbeta += red[0][k][lane];
+          dg += red[1][k][lane];
+          total += whole[k];
+        }
+        if (lane >= len) dg = dbeta = 0.0f;
+        if (lane == (len < 64 ? len - 1 : 63)) dg += total;
+        red[1][0][lane] = dg;
+        store_gate(p.dbeta, (b * p.seqlen + t0 + lane) * p.nheads + h, dbeta, G{});
+      }
+      if (w == 0) {  // dg_t is the sum of d / dG from t on
+        float v = lane < rows ? red[1][0][lane] : 0.0f;
+#pragma unroll
+        for (int d = 1; d < 64; d *= 2) {
+          const float next = __shfl_down(v, d);
+          if (lane + d < 64) v += next;
+        }
+        if (lane < rows) store_gate(p.dg, (b * p.seqlen + t0 + lane) * p.nheads + h, lane < len ? v : 0.0f, G{});
+      }
+    }
+  } else {
+    for (int64_t i = tid; i < rows * share; i += NT) {
+      const int64_t to = (b * p.seqlen + t0 + i / share) * p.nheads + hk * share + i % share;
+      store_gate(p.dg, to, 0.0f, G{});
+      store_gate(p.dbeta, to, 0.0f, G{});
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int row = 16 * i + 4 * g + r;
+      if (row < rows) {
+        st(dqp, row * row_step, row < len ? tq[i][r] : 0.0f);
+        st(dkp, row * row_step, row < len ? tk[i][r] : 0.0f);
+      }
+    }
+}
+
+template <int KD, int VD, typename G>
+void grad(const GdrParams &p, hipStream_t s) {
+  hipLaunchKernelGGL((gdr_grad_kernel<KD, VD, G>), dim3(static_cast<uint32_t>(p.batch * p.nqk * p.chunks)), dim3(4 * KD), 0, s, p);
+}
+
+template <int KD>
+hipError_t bwd(const GdrParams &p, hipStream_t s) {
+  const int64_t heads = p.batch * p.nheads;
+  hipLaunchKernelGGL((gdr_bwd_kernel<KD, 1, 4>), dim3(static_cast<uint32_t>(heads * (p.vdim / 64))), dim3(256), 0, s, p);
+  if (p.chunks > 0) {
+    if (p.vdim == 64) p.gates_bf16 ? grad<KD, 64, uint16_t>(p, s) : grad<KD, 64, float>(p, s);
+    else p.gates_bf16 ? grad<KD, 128, uint16_t>(p, s) : grad<KD, 128, float>(p, s);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace
+
+GdrBwdSizes gdr_bwd_sizes(const GdrParams &p) {
+  const size_t n = static_cast<size_t>(p.batch) * p.nheads * p.chunks;
+  return {n * kGdrBwdChunkBytes, n * p.vdim * p.kdim * 4, n * 64 * p.vdim * 4};
+}
+
+hipError_t launch_gdr_bwd(const GdrParams &p, hipStream_t s) {
+  const hipError_t e = launch_gdr_chunks(p, true, s);
+  if (e != hipSuccess) return e;
+  return p.kdim == 64 ? bwd<64>(p, s) : bwd<128>(p, s);
+}
+
+}  // namespace ssmb

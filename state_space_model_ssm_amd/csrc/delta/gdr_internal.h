@@ -8,13 +8,16 @@ namespace ssmb {
 
 constexpr int kGdrChunk = 64;
 
-// What the forward knows of a chunk of 64 tokens and a value head before it
-// has a state: T = (I + L)^-1 and the attention A within the chunk, as
-// operands in bfloat16 parts (see gdr_tile.h), and the gates' factors.
-constexpr int kGdrFrags = 6;                                   // operands of a lower triangle: 16 rows x 32 columns each
+// What is known of a chunk of 64 tokens and a value head before its state is:
+// T = (I + L)^-1 and the attention A within the chunk, as operands in bfloat16
+// parts (see gdr_tile.h), then the gates' factors.  The forward has T, A; the
+// backward T, T^T, A^T.
+constexpr int kGdrFrags = 6;                                   // operands of a triangle: 16 rows x 32 columns each
 constexpr size_t kGdrTriBytes = size_t{2} * kGdrFrags * 1024;  // both parts
-constexpr size_t kGdrGateBytes = 4 * kGdrChunk * 4;
+// Factors, 64 of each: scale e^G, e^G, e^(GC - G), beta (float32), and G log2(e) (float64).
+constexpr size_t kGdrGateBytes = 2048;
 constexpr size_t kGdrChunkBytes = 2 * kGdrTriBytes + kGdrGateBytes;
+constexpr size_t kGdrBwdChunkBytes = 3 * kGdrTriBytes + kGdrGateBytes;
 
 struct GdrParams {
   const uint16_t *q, *k, *v;   // bf16
@@ -23,13 +26,26 @@ struct GdrParams {
   const int32_t *lengths;      // nullable
   uint16_t *y;
   float *h_last, *states;      // nullable
-  char *ws;                    // kGdrChunkBytes per (row, value head, chunk)
+  char *ws;                    // kGdrChunkBytes (backward: kGdrBwdChunkBytes) per (row, value head, chunk)
+  const uint16_t *dy;          // backward
+  const float *dh_last;        // nullable
+  uint16_t *dq, *dk, *dv;
+  void *dg, *dbeta;            // gate dtype
+  float *dh0;                  // nullable
+  float *ws_ds, *ws_e;         // per (row, value head, chunk): dS behind it, and E = T^T dU in D's order
   int64_t batch, seqlen, nqk, nheads, chunks;
   int64_t q_batch, q_token, k_batch, k_token, v_batch, v_token;
   float scale;
   int32_t kdim, vdim, gates_bf16;
 };
 size_t gdr_workspace(const GdrParams &p);
+// Sizes of the backward's workspace: ws, ws_ds and ws_e in turn.
+struct GdrBwdSizes {
+  size_t chunks, ds, e;
+};
+GdrBwdSizes gdr_bwd_sizes(const GdrParams &p);
+hipError_t launch_gdr_chunks(const GdrParams &p, bool bwd, hipStream_t stream);
+hipError_t launch_gdr_bwd(const GdrParams &p, hipStream_t stream);
 hipError_t launch_gdr_fwd(const GdrParams &p, hipStream_t stream);
 hipError_t launch_gdr_step(const GdrParams &p, hipStream_t stream);  // h0 -> h_last
 

@@ -1,6 +1,4 @@
 // Gated delta rule, forward and single tokens, for gfx950.
-#include <type_traits>
-
 #include "gdr_tile.h"
 
 namespace ssmb {
@@ -10,24 +8,7 @@ namespace {
 // Within a chunk
 // ---------------------------------------------------------------------------
 
-template <typename G>
-__device__ __forceinline__ float gate(const void *p, int64_t i) { return ld(static_cast<const G *>(p), i); }
-
 constexpr int kPitch = 68, kDiagPitch = 20;  // floats between rows in LDS: 16-byte aligned, rows on other banks
-
-// Call f with the wavefront's number as a constant.  Each wavefront's products
-// are straight code then: the compiler leaves out the wait between a matrix
-// product and a read of its result where a branch by a wavefront's number lies
-// between them.
-template <typename F>
-__device__ __forceinline__ void by_wave(int w, F &&f) {
-  switch (w) {
-    case 0: f(std::integral_constant<int, 0>{}); break;
-    case 1: f(std::integral_constant<int, 1>{}); break;
-    case 2: f(std::integral_constant<int, 2>{}); break;
-    default: f(std::integral_constant<int, 3>{}); break;
-  }
-}
 
 // Store row block W of a lower triangle, transposed D results, as fragments in two parts.
 template <int W>
@@ -40,9 +21,30 @@ __device__ __forceinline__ void store_rows(const f4v (&t)[W + 1], u4 *to, int la
   }
 }
 
+// Row block J of a triangle's transpose, as fragments, from the triangle in LDS.
+__device__ __forceinline__ void store_cols(const float *t, int J, u4 *to, int lane) {
+  const int m = lane & 15, g = lane >> 4;
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    if (2 * s + 1 < J) continue;
+    f4v v[2];
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int i = 32 * s + 16 * x + 4 * g + r;
+        v[x][r] = i >= 16 * J + m ? t[i * kPitch + 16 * J + m] : 0.0f;
+      }
+    const Parts p = parts(v[0], v[1]);
+    to[tri_t(J, s) * 64 + lane] = __builtin_bit_cast(u4, p.hi);
+    to[(kGdrFrags + tri_t(J, s)) * 64 + lane] = __builtin_bit_cast(u4, p.lo);
+  }
+}
+
 // One workgroup per chunk and value head, one wavefront per 16 of its tokens.
-template <int KD, typename G>
+template <int KD, typename G, bool BWD>
 __global__ void __launch_bounds__(256) gdr_chunk_kernel(const GdrParams p) {
+  __shared__ __align__(16) float full[BWD ? 64 * kPitch : 4], inv[BWD ? 64 * kPitch : 4];  // A and T
   __shared__ double sums[64];                       // log2 of the decay up to each token
   __shared__ float betas[64];
   __shared__ __align__(16) float low[64 * kPitch];  // L^T
@@ -52,7 +54,7 @@ __global__ void __launch_bounds__(256) gdr_chunk_kernel(const GdrParams p) {
   const int64_t id = blockIdx.x, c = id % p.chunks, bh = id / p.chunks, b = bh / p.nheads, h = bh % p.nheads;
   const int t0 = static_cast<int>(c) * 64, len = gdr_length(p.lengths, b, p.seqlen) - t0;
   if (len <= 0) return;
-  char *ws = p.ws + id * static_cast<int64_t>(kGdrChunkBytes);
+  char *ws = p.ws + id * static_cast<int64_t>(BWD ? kGdrBwdChunkBytes : kGdrChunkBytes);
   constexpr int NS = KD / 32;
   const int64_t hk = h / (p.nheads / p.nqk);
   const uint16_t *kp = p.k + b * p.k_batch + t0 * p.k_token + hk * KD + 8 * g;
@@ -72,6 +74,8 @@ __global__ void __launch_bounds__(256) gdr_chunk_kernel(const GdrParams p) {
       gt = gt < -200.0f ? -200.0f : gt;  // exp(-200) is 0, and differences of the sums stay finite
       bt = gate<G>(p.beta, at);
     }
+    // The backward divides by beta: a gate that is shut counts as 2^-60 there.
+    if (BWD && fabsf(bt) < 0x1p-60f) bt = copysignf(0x1p-60f, bt);
     // In float64: after a strong decay the differences of later tokens' sums would lose what they have.
     double s = static_cast<double>(gt) * 1.4426950408889634;
 #pragma unroll
@@ -83,11 +87,12 @@ __global__ void __launch_bounds__(256) gdr_chunk_kernel(const GdrParams p) {
     betas[lane] = bt;
     const double last = __shfl(s, 63);
     const float into = __builtin_amdgcn_exp2f(static_cast<float>(s));
-    float *gates = reinterpret_cast<float *>(ws + 2 * kGdrTriBytes);
-    gates[lane] = p.scale * into;
+    float *gates = reinterpret_cast<float *>(ws + (BWD ? 3 : 2) * kGdrTriBytes);
+    gates[lane] = lane < len ? p.scale * into : 0.0f;
     gates[64 + lane] = into;
     gates[128 + lane] = __builtin_amdgcn_exp2f(static_cast<float>(last - s));
     gates[192 + lane] = bt;
+    if (BWD) reinterpret_cast<double *>(gates + 256)[lane] = s;
   }
   __syncthreads();
   u4 *out = reinterpret_cast<u4 *>(ws);
@@ -113,10 +118,11 @@ __global__ void __launch_bounds__(256) gdr_chunk_kernel(const GdrParams p) {
       for (int r = 0; r < 4; ++r) {
         const int j = 16 * jb + 4 * g + r;
         const float decay = j <= i ? __builtin_amdgcn_exp2f(static_cast<float>(si - sums[j])) : 0.0f;
-        att[jb][r] = j <= i ? att[jb][r] * decay * p.scale : 0.0f;
+        att[jb][r] = j <= i && i < len ? att[jb][r] * decay * p.scale : 0.0f;
+        if (BWD) full[i * kPitch + j] = att[jb][r];
         low[j * kPitch + i] = j < i ? kk[jb][r] * decay * bi : 0.0f;
       }
-    store_rows<W>(att, out + kGdrTriBytes / 16, lane);
+    if (!BWD) store_rows<W>(att, out + kGdrTriBytes / 16, lane);
   });
   __syncthreads();
   // Blocks on the diagonal, all in one wavefront: lane (block g, column m) by substitution.
@@ -160,25 +166,20 @@ __global__ void __launch_bounds__(256) gdr_chunk_kernel(const GdrParams p) {
       for (int r = 0; r < 4; ++r) t[j] = mfma_f32(-d[r], acc[r], t[j]);
     }
     store_rows<W>(t, out, lane);
+    if (BWD)
+#pragma unroll
+      for (int jb = 0; jb <= W; ++jb) *reinterpret_cast<f4v *>(inv + i * kPitch + 16 * jb + 4 * g) = t[jb];
   });
+  if (BWD) {
+    __syncthreads();
+    store_cols(inv, w, out + kGdrTriBytes / 16, lane);
+    store_cols(full, w, out + 2 * kGdrTriBytes / 16, lane);
+  }
 }
 
 // ---------------------------------------------------------------------------
 // From chunk to chunk
 // ---------------------------------------------------------------------------
-
-// All but the last N of this wavefront's copies and stores are done, then all wavefronts meet.
-template <int N>
-__device__ __forceinline__ void arrive() {
-  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
-}
-
-// LDS slot of a tile of 64 rows of NC values.
-template <int NC>
-__device__ __forceinline__ int vslot(int r, int c) {
-  if constexpr (NC == 32) return r * 4 + c;
-  else return slot<NC>(r, c);
-}
 
 // A workgroup takes 16 CT NW columns (value elements) of a head from chunk to
 // chunk, a wavefront 16 CT of them.
@@ -258,19 +259,15 @@ __global__ void __launch_bounds__(64 * NW) gdr_fwd_kernel(const GdrParams p) {
       }
     }
     // beta (v - e^G x), and e^G scale o
-    typedef __attribute__((address_space(3))) sh4 lds4;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const f4v qs = lds_f4(gates + 64 * i), into = lds_f4(gates + 256 + 64 * i), beta = lds_f4(gates + 768 + 64 * i);
 #pragma unroll
       for (int t = 0; t < CT; ++t) {
-        const int r0 = 16 * i + 4 * g + (m >> 2), piece = 4 * (CT * w + t) + (m & 3);
-        const sh4 v = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-            (lds4 *)(tile + kAtV + vslot<NC>(r0, piece >> 1) * 16 + (piece & 1) * 8));
+        const sh4 v = rows4<NC>(tile + kAtV, i, CT * w + t, lane);
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const float vf = __uint_as_float(static_cast<unsigned>(static_cast<uint16_t>(v[r])) << 16);
-          x[t][i][r] = beta[r] * fmaf(-into[r], x[t][i][r], vf);
+          x[t][i][r] = beta[r] * fmaf(-into[r], x[t][i][r], up(v[r]));
           o[t][i][r] *= qs[r];
         }
       }
@@ -407,9 +404,15 @@ __global__ void __launch_bounds__(256) gdr_step_kernel(const GdrParams p) {
 }
 
 template <int KD, typename G>
+void chunks(const GdrParams &p, bool bwd, hipStream_t s) {
+  const dim3 n(static_cast<uint32_t>(p.batch * p.nheads * p.chunks));
+  if (bwd) hipLaunchKernelGGL((gdr_chunk_kernel<KD, G, true>), n, dim3(256), 0, s, p);
+  else hipLaunchKernelGGL((gdr_chunk_kernel<KD, G, false>), n, dim3(256), 0, s, p);
+}
+
+template <int KD>
 hipError_t fwd(const GdrParams &p, hipStream_t s) {
   const int64_t heads = p.batch * p.nheads;
-  if (p.chunks > 0) hipLaunchKernelGGL((gdr_chunk_kernel<KD, G>), dim3(static_cast<uint32_t>(heads * p.chunks)), dim3(256), 0, s, p);
   hipLaunchKernelGGL((gdr_fwd_kernel<KD, 1, 4>), dim3(static_cast<uint32_t>(heads * (p.vdim / 64))), dim3(256), 0, s, p);
   return hipGetLastError();
 }
@@ -430,9 +433,17 @@ size_t gdr_workspace(const GdrParams &p) {
   return static_cast<size_t>(p.batch) * p.nheads * p.chunks * kGdrChunkBytes;
 }
 
+hipError_t launch_gdr_chunks(const GdrParams &p, bool bwd, hipStream_t s) {
+  if (p.chunks == 0) return hipSuccess;
+  if (p.kdim == 64) p.gates_bf16 ? chunks<64, uint16_t>(p, bwd, s) : chunks<64, float>(p, bwd, s);
+  else p.gates_bf16 ? chunks<128, uint16_t>(p, bwd, s) : chunks<128, float>(p, bwd, s);
+  return hipGetLastError();
+}
+
 hipError_t launch_gdr_fwd(const GdrParams &p, hipStream_t s) {
-  if (p.kdim == 64) return p.gates_bf16 ? fwd<64, uint16_t>(p, s) : fwd<64, float>(p, s);
-  return p.gates_bf16 ? fwd<128, uint16_t>(p, s) : fwd<128, float>(p, s);
+  const hipError_t e = launch_gdr_chunks(p, false, s);
+  if (e != hipSuccess) return e;
+  return p.kdim == 64 ? fwd<64>(p, s) : fwd<128>(p, s);
 }
 
 hipError_t launch_gdr_step(const GdrParams &p, hipStream_t s) {

@@ -16,12 +16,15 @@
 // q, k, v and dy are bfloat16 already and enter as they are.
 #pragma once
 
+#include <type_traits>
+
 #include "gdr_internal.h"
 #include "block/swa_tile.h"
 
 namespace ssmb {
 
 typedef __attribute__((ext_vector_type(4))) float f4v;
+typedef __attribute__((ext_vector_type(2))) unsigned int u2;
 
 __device__ __forceinline__ f4v mfma16(bf8 a, bf8 b, f4v c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
@@ -45,6 +48,12 @@ __device__ __forceinline__ Parts parts(const f4v &a, const f4v &b) {
     p.lo[e] = static_cast<__bf16>((e < 4 ? a[e % 4] : b[e % 4]) - up);
   }
   return p;
+}
+
+// The first or second four of an operand.
+__device__ __forceinline__ u2 half_of(bf8 v, int half) {
+  const u4 bits = __builtin_bit_cast(u4, v);
+  return half != 0 ? u2{bits[2], bits[3]} : u2{bits[0], bits[1]};
 }
 
 // c + a b for a factor in parts and an exact one, or two in parts.
@@ -91,8 +100,50 @@ __device__ __forceinline__ f4v lds_f4(unsigned at) {
   return *(lds16 *)(at);
 }
 
-// Fragment of a lower triangle: row block i (of 16), columns 32 s ..
+// Fragment of a lower triangle: row block i (of 16), columns 32 s .., and of
+// its transpose: row block j, columns 32 s .. (32 s + 31 >= 16 j).
 __host__ __device__ constexpr int tri(int i, int s) { return i < 2 ? i : 2 * (i - 1) + s; }
+__host__ __device__ constexpr int tri_t(int j, int s) { return j < 2 ? 2 * j + s : j + 2; }
+
+// Call f with the wavefront's number (of 4) as a constant.  Each wavefront's
+// products are straight code then: the compiler leaves out the wait between a
+// matrix product and a read of its result where a branch by a wavefront's
+// number lies between them.
+template <typename F>
+__device__ __forceinline__ void by_wave(int w, F &&f) {
+  switch (w) {
+    case 0: f(std::integral_constant<int, 0>{}); break;
+    case 1: f(std::integral_constant<int, 1>{}); break;
+    case 2: f(std::integral_constant<int, 2>{}); break;
+    default: f(std::integral_constant<int, 3>{}); break;
+  }
+}
+
+// All but the last N of this wavefront's copies and stores are done, then all wavefronts meet.
+template <int N>
+__device__ __forceinline__ void arrive() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+
+// LDS slot of a tile of 64 rows of NC values.
+template <int NC>
+__device__ __forceinline__ int vslot(int r, int c) {
+  if constexpr (NC == 32) return r * 4 + c;
+  else return slot<NC>(r, c);
+}
+// Rows 16 i + 4g .. + 3 of column 16 ct + m of such a tile.
+template <int NC>
+__device__ __forceinline__ sh4 rows4(unsigned tile, int i, int ct, int lane) {
+  typedef __attribute__((address_space(3))) sh4 lds4;
+  const int m = lane & 15, r = 16 * i + 4 * (lane >> 4) + (m >> 2), piece = 4 * ct + (m & 3);
+  return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)(tile + vslot<NC>(r, piece >> 1) * 16 + (piece & 1) * 8));
+}
+__device__ __forceinline__ float up(short v) {
+  return __uint_as_float(static_cast<unsigned>(static_cast<uint16_t>(v)) << 16);
+}
+
+template <typename G>
+__device__ __forceinline__ float gate(const void *p, int64_t i) { return ld(static_cast<const G *>(p), i); }
 
 __device__ __forceinline__ int gdr_length(const int32_t *lengths, int64_t b, int64_t seqlen) {
   if (lengths == nullptr) return static_cast<int>(seqlen);

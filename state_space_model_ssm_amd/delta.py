@@ -50,11 +50,11 @@ def delta_lib():
                 "(hipcc, gfx950). There is no fallback implementation.")
         L = ctypes.CDLL(_LIB_PATH)
         vp, size = ctypes.c_void_p, ctypes.POINTER(ctypes.c_size_t)
-        for name, pointers, dims in (("ssm_gdr_fwd", 10, GdrDims), ("ssm_gdr_step", 8, GdrDims)):
+        for name, pointers, dims in (("ssm_gdr_fwd", 10, GdrDims), ("ssm_gdr_bwd", 15, GdrDims), ("ssm_gdr_step", 8, GdrDims)):
             f = getattr(L, name)
             f.argtypes = [vp] * pointers + [ctypes.POINTER(dims), vp]
             f.restype = ctypes.c_int
-        for name, dims in (("ssm_gdr_workspace_size", GdrDims),):
+        for name, dims in (("ssm_gdr_workspace_size", GdrDims), ("ssm_gdr_bwd_workspace_size", GdrDims)):
             f = getattr(L, name)
             f.argtypes = [ctypes.POINTER(dims), size]
             f.restype = ctypes.c_int
@@ -81,6 +81,10 @@ def _size(call, dims) -> int:
 
 def gdr_workspace_size(dims: GdrDims) -> int:
     return _size(delta_lib().ssm_gdr_workspace_size, dims)
+
+
+def gdr_bwd_workspace_size(dims: GdrDims) -> int:
+    return _size(delta_lib().ssm_gdr_bwd_workspace_size, dims)
 
 
 def _scratch(dims, need: int, workspace, like, stream):
@@ -162,6 +166,33 @@ def gdr_fwd(q, k, v, g, beta, *, h0=None, lengths=None, scale=None, return_h_las
     _check(delta_lib().ssm_gdr_fwd(_at(q), _at(k), _at(v), _ptr(g), _ptr(beta), _ptr(h0), _ptr(lengths), _ptr(y),
                                    _ptr(h_last), _ptr(states), ctypes.byref(dims), _stream(stream)))
     return (y, h_last, states) if return_states else (y, h_last)
+
+
+def gdr_bwd(q, k, v, g, beta, states, dy, *, dh_last=None, lengths=None, scale=None, return_dh0: bool = True, out=None,
+            workspace=None, stream=None):
+    """Backward of ``gdr_fwd`` (``ssm_gdr_bwd``) from the states it saved and
+    the gradients of y (v's shape, bfloat16) and of h_last ((batch, nheads,
+    vdim, kdim) float32 or None).  Returns ``(dq, dk, dv, dg, dbeta, dh0)``:
+    dense, shaped and typed like q, k, v, g and beta; dh0 float32 (None without
+    return_dh0).  ``out``: a dict of preallocated outputs under those names.
+    """
+    _one_device(stream, q, k, v, g, beta, states, dy, dh_last, lengths, workspace)
+    dims = _gdr_dims(q, k, v, g, beta, scale, 2)
+    batch, L, H, vd = v.shape
+    state = (batch, H, vd, q.shape[-1])
+    _same("states", states, _F32, (batch, H, -(-L // GDR_STATE_STEP), vd, q.shape[-1]))
+    _same("dy", dy, _BF16, v.shape)
+    _same("dh_last", dh_last, _F32, state)
+    _same("lengths", lengths, torch.int32, (batch,))
+    o = out or {}
+    dq, dk, dv, dg, dbeta = (_out(o.get(n), t.shape, t.dtype, t, n, stream)
+                             for n, t in (("dq", q), ("dk", k), ("dv", v), ("dg", g), ("dbeta", beta)))
+    dh0 = _out(o.get("dh0"), state, _F32, q, "dh0", stream) if return_dh0 else None
+    workspace = _scratch(dims, gdr_bwd_workspace_size(dims), workspace, q, stream)
+    _check(delta_lib().ssm_gdr_bwd(_at(q), _at(k), _at(v), _ptr(g), _ptr(beta), _ptr(lengths), _ptr(states), _ptr(dy),
+                                   _ptr(dh_last), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dg), _ptr(dbeta), _ptr(dh0),
+                                   ctypes.byref(dims), _stream(stream)))
+    return dq, dk, dv, dg, dbeta, dh0
 
 
 def gdr_step(q, k, v, g, beta, h, *, scale=None, h_out=None, y=None, stream=None):

@@ -40,6 +40,59 @@ def gdr(q, k, v, g, beta, h0=None, lengths=None, scale=None):
     return torch.stack(ys), torch.stack(last), states, torch.stack(sizes)
 
 
+def gdr_bwd(q, k, v, g, beta, dy, h0=None, lengths=None, scale=None, dh_last=None):
+    """Gradients by the reverse recurrence, and sizes: what the terms of each
+    add up to at most, by norms (per token and head; of dg over the rest of
+    the token's block of 64, whose products the kernels sum)."""
+    B, L, H, V = v.shape
+    K, share = q.shape[3], H // q.shape[2]
+    scale = K ** -0.5 if scale is None else scale
+    zero = torch.zeros(B, H, V, K, dtype=torch.float64)
+    grads = {n: torch.zeros_like(t) for n, t in zip(("dq", "dk", "dv", "dg", "dbeta"), (q, k, v, g, beta))}
+    sizes = {n: torch.zeros(B, L, H, dtype=torch.float64) for n in grads}
+    grads["dh0"] = zero.clone()
+    for b in range(B):
+        n = L if lengths is None else min(max(int(lengths[b]), 0), L)
+        S, past = zero[b] if h0 is None else h0[b], []
+        for t in range(n):
+            kt, a = k[b, t].repeat_interleave(share, 0), torch.exp(g[b, t])[:, None]
+            seen = (S * kt[:, None]).sum(-1)
+            rest = v[b, t] - a * seen
+            u = beta[b, t][:, None] * rest
+            past.append((S, seen, rest, u))
+            S = a[:, :, None] * S + u[:, :, None] * kt[:, None]
+        dS = zero[b] if dh_last is None else dh_last[b]
+        after, run = S, torch.zeros(H, dtype=torch.float64)
+        for t in range(n - 1, -1, -1):
+            S, seen, rest, u = past[t]
+            kt, qt = (x[b, t].repeat_interleave(share, 0) for x in (k, q))
+            a, y = torch.exp(g[b, t])[:, None], dy[b, t]
+            if t % 64 == 63 or t == n - 1:
+                run = (after.flatten(1).norm(dim=1) * dS.flatten(1).norm(dim=1))
+            dS = dS + scale * y[:, :, None] * qt[:, None]
+            e = (dS * kt[:, None]).sum(-1)
+            dv = beta[b, t][:, None] * e
+            dq = scale * (after * y[:, :, None]).sum(1)
+            write, erase = (dS * u[:, :, None]).sum(1), a * (S * dv[:, :, None]).sum(1)
+            grads["dq"][b, t] += dq.unflatten(0, (-1, share)).sum(1)
+            grads["dk"][b, t] += (write - erase).unflatten(0, (-1, share)).sum(1)
+            grads["dv"][b, t], grads["dbeta"][b, t] = dv, (e * rest).sum(-1)
+            grads["dg"][b, t] = a[:, 0] * ((dS * S).sum((1, 2)) - (dv * seen).sum(-1))
+            nS, ndS = (x.flatten(1).norm(dim=1) for x in (after, dS))
+            nb = S.flatten(1).norm(dim=1)
+            nq, nk, ny, nu, nv = (x.norm(dim=-1) for x in (qt, kt, y, u, dv))
+            sizes["dq"][b, t] = abs(scale) * ny * nS
+            sizes["dk"][b, t] = nu * ndS + a[:, 0] * nv * nb
+            sizes["dv"][b, t] = beta[b, t].abs() * ndS * nk
+            sizes["dbeta"][b, t] = ndS * nk * (v[b, t].norm(dim=-1) + a[:, 0] * nb * nk)
+            run = run + nq * sizes["dq"][b, t] + nk * sizes["dk"][b, t]
+            sizes["dg"][b, t] = run
+            dS = a[:, :, None] * (dS - dv[:, :, None] * kt[:, None])
+            after = S
+        grads["dh0"][b] = dS
+    return grads, sizes
+
+
 def close(got, want, tol, what):
     """Elementwise |got - want| <= tol; NaN nowhere."""
     got, want = f64(got), f64(want)

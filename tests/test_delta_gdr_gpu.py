@@ -1,4 +1,4 @@
-"""The gated delta rule (forward, step) against float64."""
+"""The gated delta rule (forward, backward, step) against float64."""
 import pytest
 import torch
 
@@ -99,6 +99,92 @@ def test_forward(B, L, nqk, H, K, V, gates, with_h0, lengths):
     if with_h0:   # h_last in the place of h0
         ssm.gdr_fwd(cq, ck, cv, cg, cb, h0=ch, lengths=None if lens is None else lens.cuda(), h_last=ch, y=y)
         assert torch.equal(ch, hl) and torch.equal(y, again[0])
+
+
+def by_norm(t):
+    """How far an output may be off by norms: 2^-12 and its own rounding.  A rounding is off by at most half a step, U of
+    the value, so a few values by that together; over many the errors spread over the half step, and the root of
+    their mean square is 1 / sqrt(3) of it at most (the integral of x^2 over 0 .. 1)."""
+    return 2.0 ** -12 + (0.0 if t.dtype != BF16 else U if t.numel() < 1024 else U / 3 ** 0.5)
+
+
+BACKWARD = CASES + [(1, 300, 2, 8, 64, 128, BF16, True, None), (2, 140, 1, 4, 128, 64, F32, True, [140, 77])]
+
+
+@pytest.mark.parametrize("B,L,nqk,H,K,V,gates,with_h0,lengths", BACKWARD)
+def test_backward(B, L, nqk, H, K, V, gates, with_h0, lengths):
+    q, k, v, g, beta, h0, dy = make(B, L, nqk, H, K, V, L * 3 + H, gates)
+    h0 = h0 if with_h0 else None
+    dh = torch.randn(B, H, V, K, generator=torch.Generator().manual_seed(L)) if with_h0 else None
+    lens = None if lengths is None else torch.tensor(lengths, dtype=torch.int32)
+    want, size = ref.gdr_bwd(*(ref.f64(t) for t in (q, k, v, g, beta, dy, h0)), lens, dh_last=ref.f64(dh))
+    if lengths is not None:
+        for b, n in enumerate(lengths):
+            for t in (q, k, v, g, beta, dy):
+                t[b, max(n, 0):] = float("nan")
+    cl = None if lens is None else lens.cuda()
+    views = one_tensor(q, k, v)
+    cg, cb, ch, cdy, cdh = cuda(g, beta, h0, dy, dh)
+    states = nan((B, H, -(-L // 64), V, K))
+    ssm.gdr_fwd(*views, cg, cb, h0=ch, lengths=cl, states=states)
+    outs = {n: nan(t.shape, t.dtype) for n, t in (("dq", q), ("dk", k), ("dv", v), ("dg", g), ("dbeta", beta))}
+    outs["dh0"] = nan((B, H, V, K))
+    got = ssm.gdr_bwd(*views, cg, cb, states, cdy, dh_last=cdh, lengths=cl, out=outs)
+    names = ("dq", "dk", "dv", "dg", "dbeta", "dh0")
+    assert all(t is outs[n] for n, t in zip(names, got))
+    for n, t in zip(names, got):
+        w = want[n]
+        # Five products in turn at most: 5 * 3 * 2^-18 of the sizes, a share of them by norms; heads that share add up.
+        if n == "dh0":
+            small = 2.0 ** -14 * max(float(w.abs().max()), 4.0 * (1 if dh is None else float(dh.abs().max())))
+        else:
+            small = 2.0 ** -14 * size[n]
+            if n in ("dq", "dk"):
+                small = small.unflatten(2, (nqk, -1)).sum(3)
+            if n in ("dq", "dk", "dv"):
+                small = small[..., None]
+        ref.close(t, w, (U * w.abs() if t.dtype == BF16 else 0.0) + small, n)
+        far = float((ref.f64(t) - w).norm())
+        assert far <= by_norm(t) * float(w.norm()), (n, far / float(w.norm()))
+    again = ssm.gdr_bwd(*views, cg, cb, states, cdy, dh_last=cdh, lengths=cl)
+    assert all(torch.equal(a, b) for a, b in zip(again, got))
+
+
+def test_backward_against_differences():
+    q, k, v, g, beta, h0, dy = make(1, 70, 1, 2, 64, 64, 12)
+    dh = torch.randn(h0.shape, generator=torch.Generator().manual_seed(1))
+    states = ssm.gdr_fwd(*cuda(q, k, v, g, beta), h0=h0.cuda(), return_states=True)[2]
+    got = ssm.gdr_bwd(*cuda(q, k, v, g, beta), states, dy.cuda(), dh_last=dh.cuda())
+    at = [ref.f64(t) for t in (q, k, v, g, beta, h0)]
+
+    def loss(q, k, v, g, beta, h0):
+        y, last, _, _ = ref.gdr(q, k, v, g, beta, h0)
+        return float((y * dy.double()).sum() + (last * dh.double()).sum())
+
+    eps = 1e-5
+    for n, t in enumerate(got):
+        for j in torch.randint(t.numel(), (5,), generator=torch.Generator().manual_seed(n)).tolist():
+            up, down = [x.clone() for x in at], [x.clone() for x in at]
+            up[n].view(-1)[j] += eps
+            down[n].view(-1)[j] -= eps
+            # Central differences of a float64 loss of order 10^2: 1e-14 / eps, and eps^2 of third derivatives.
+            want = (loss(*up) - loss(*down)) / (2 * eps)
+            assert abs(float(t.view(-1)[j]) - want) <= U * abs(want) + 2.0 ** -11 * float(t.abs().max()), (n, j)
+
+
+def test_gradients_of_shut_gates_and_strong_decays():
+    """beta of exactly 0 has a gradient, and decays of exp(-200) and less leave the others as they are."""
+    q, k, v, g, beta, h0, dy = make(1, 130, 1, 2, 64, 64, 14)
+    beta[0, 3], beta[0, 40:44], beta[0, 129] = 0.0, 0.0, 0.0
+    g[0, 50], g[0, 100, 1] = -float("inf"), -1000.0
+    wide = [ref.f64(t) for t in (q, k, v, g.clamp(min=-1e4), beta, dy, h0)]
+    want, size = ref.gdr_bwd(*wide)
+    states = ssm.gdr_fwd(*cuda(q, k, v, g, beta), h0=h0.cuda(), return_states=True)[2]
+    got = ssm.gdr_bwd(*cuda(q, k, v, g, beta), states, dy.cuda())
+    for n, t in zip(("dq", "dk", "dv", "dg", "dbeta", "dh0"), got):
+        far = float((ref.f64(t) - want[n]).norm())
+        assert far <= by_norm(t) * float(want[n].norm()) + 1e-30, n
+    assert got[4][0, 40:44].abs().min() > 0
 
 
 @pytest.mark.parametrize("B,nqk,H,K,V,gates", [(1, 1, 1, 64, 64, F32), (3, 2, 4, 128, 64, BF16), (2, 1, 3, 64, 128, BF16),
