@@ -32,7 +32,7 @@
 #ifndef SSM_DELTA_H
 #define SSM_DELTA_H
 
-#include "ssm.h"
+#include "ssm_block.h"
 
 #ifdef __cplusplus
 extern "C" {
@@ -123,6 +123,104 @@ SSM_API int ssm_gdr_bwd(const void *q, const void *k, const void *v, const void 
  */
 SSM_API int ssm_gdr_step(const void *q, const void *k, const void *v, const void *g, const void *beta, const float *h,
                          void *y, float *h_out, const ssm_gdr_dims_t *dims, void *stream);
+
+/* ------------------------------------------------------------------------ */
+/* Norms of queries and keys with the rotation by position                   */
+/* ------------------------------------------------------------------------ */
+
+/*
+ * Sizes of one call.  dtype: q, k and what becomes of them (and gradients).
+ * headdim: a multiple of 16 up to 256; rot: how many of a head's elements are
+ * rotated, a multiple of 16 from 0 to headdim.  neighbours: 0 pairs element i
+ * with i + rot / 2, 1 pairs 2 i with 2 i + 1.
+ * q_batch, q_token, k_..: elements between batch rows and tokens of q and k;
+ * oq_.., ok_..: of q_out and k_out (dq and dk).  Heads of a token are
+ * adjacent.  Strides are multiples of 16 bytes, and q, k, wq, wk and the
+ * outputs aligned to 16 bytes.  nheads, nkv >= 1, at most 2^20.
+ */
+typedef struct {
+  int64_t batch, seqlen, nheads, nkv, headdim, rot;
+  int64_t q_batch, q_token, k_batch, k_token, oq_batch, oq_token, ok_batch, ok_token;
+  int32_t dtype, neighbours;
+  float eps;
+  int32_t reserved;
+  void *workspace;
+  size_t workspace_bytes;
+} ssm_qk_norm_dims_t;
+
+/*
+ * Per token and head of q, with w = wq, and of k, with w = wk:
+ *   n = x / sqrt(mean(x^2) + eps) w
+ *   (n_a, n_b) of pair i < rot / 2 becomes (n_a cos - n_b sin, n_b cos + n_a sin)
+ *   of the angle pos inv_freq_i, which is taken in float64; the others stay.
+ *   q, q_out: (batch, seqlen, nheads, headdim);  k, k_out: (batch, seqlen, nkv, headdim)
+ *   wq, wk  : (headdim) float32, nullable (ones): shared by all heads
+ *   inv_freq: (rot / 2) float32;  pos: (batch, seqlen) int32, nullable (0, 1, ..
+ *             in each batch row); neither is used with rot = 0
+ * q_out may be exactly q, and k_out exactly k (with the same strides); tensors
+ * that lie side by side in one (the same strides, as parts of one projection)
+ * do not count as overlapping.  w = headdim^-0.5 makes heads of unit length.
+ */
+SSM_API int ssm_qk_norm_fwd(const void *q, const void *k, const float *wq, const float *wk, const float *inv_freq,
+                            const int32_t *pos, void *q_out, void *k_out, const ssm_qk_norm_dims_t *dims, void *stream);
+
+/*
+ * Backward: with d the gradient of an output, rotated back, and m = x rstd,
+ *   dw = sum over tokens and heads of d m,   dx = rstd (d w - m mean(d w m))
+ *   q, k        : as in the forward, with its other arguments
+ *   dq_out, dk_out: the gradients of q_out and k_out, dense
+ *   dq, dk      : shaped like q and k, with the output strides
+ *   dwq, dwk    : (headdim) float32, both nullable; the workspace is used for
+ *                 them only
+ */
+SSM_API int ssm_qk_norm_bwd_workspace_size(const ssm_qk_norm_dims_t *dims, size_t *bytes);
+SSM_API int ssm_qk_norm_bwd(const void *q, const void *k, const float *wq, const float *wk, const float *inv_freq,
+                            const int32_t *pos, const void *dq_out, const void *dk_out, void *dq, void *dk, float *dwq,
+                            float *dwk, const ssm_qk_norm_dims_t *dims, void *stream);
+
+/* ------------------------------------------------------------------------ */
+/* Sliding-window attention over a cache in 8 bits                           */
+/* ------------------------------------------------------------------------ */
+
+/*
+ * One token per batch row, as ssm_swa_step (whose sizes, ssm_swa_dims_t, and
+ * rules these calls share), against a cache that holds most of the window in
+ * e4m3 floats (OCP: 4 exponent and 3 mantissa bits, largest 448).  window must
+ * be a multiple of 64.  The positions behind the sinks, sinks + 64 n .., form
+ * blocks of 64; per batch row and key head the cache has
+ *   near : (batch, nkv, sinks + 64, headdim) bfloat16: the sinks, then the
+ *          positions of the last block, as they came
+ *   ring : (batch, nkv, window, headdim) bytes: block n, once it is whole, at
+ *          64 (n mod (window / 64)), each value v as v / scale, rounded to the
+ *          nearest even
+ *   scale: (batch, nkv, window / 64) float32: max |v| / 448 over a block's 64
+ *          positions and headdim elements (0 for a block of zeros; a value
+ *          that is not finite makes its block NaN)
+ * each of them for keys and for values, 16-byte aligned (scales: 4).  The call
+ * stores k and v of position pos near, attends to what ssm_swa_step would
+ * (pos's block in bfloat16, the rest of the window as the ring holds it, and
+ * the sinks), and, if pos is its block's last, stores that in the ring.
+ * Places of positions not yet stored may hold anything.  A position is
+ * rounded once, when its block is whole; storing the same position again
+ * gives the same cache.
+ *   q, y: (batch, nheads, headdim);  k, v: (batch, nkv, headdim) bfloat16
+ *   pos : (batch) int32, negative for a row without a token: y = 0 and its
+ *         cache stays as it is
+ */
+SSM_API int ssm_swa_q8_step_workspace_size(const ssm_swa_dims_t *dims, size_t *bytes);
+SSM_API int ssm_swa_q8_step(const void *q, const void *k, const void *v, void *k_near, void *v_near, void *k_ring,
+                            void *v_ring, float *k_scale, float *v_scale, const int32_t *pos, void *y,
+                            const ssm_swa_dims_t *dims, void *stream);
+
+/*
+ * Store the keys and values of a prompt into such a cache: of every batch row
+ * the positions below its length that a next token would still see.
+ *   k, v: (batch, seqlen, nkv, headdim); lengths as ssm_swa_fwd
+ * Places that no such position owns keep what they hold.
+ */
+SSM_API int ssm_swa_q8_fill(const void *k, const void *v, const int32_t *lengths, void *k_near, void *v_near,
+                            void *k_ring, void *v_ring, float *k_scale, float *v_scale, const ssm_swa_dims_t *dims,
+                            void *stream);
 
 #ifdef __cplusplus
 }

@@ -1,0 +1,370 @@
+// One token of sliding-window attention against a ring cache in e4m3 floats
+// with a scale per block of 64 positions and head, and the ring's fill from a
+// prompt, for gfx950.
+//
+// A block's scale is known only when its last position has come, and a value
+// should be rounded once: so the block that is being filled stays in bfloat16,
+// beside the sinks ("near"), and is stored in 8 bits, all at once, by the step
+// that completes it.  The step is bound by memory like the one over a bfloat16
+// ring, at half its bytes: a wavefront streams tiles of 8 KiB (a block of the
+// ring, or 32 near positions; headdim 64: half) into LDS of its own, without
+// registers or barriers.  e4m3 values become bfloat16, exactly, as they are
+// read from LDS, keys along their elements and values transposed; the scales
+// multiply the scores and the weights, in float32.
+#include "block/swa_step.h"
+#include "delta_internal.h"
+
+namespace ssmb {
+namespace {
+
+typedef __attribute__((ext_vector_type(2))) int i2;
+typedef __attribute__((ext_vector_type(2))) __bf16 bf2;
+
+// Eight e4m3 bytes as an operand.
+__device__ __forceinline__ bf8 widen(i2 v) {
+  bf8 r;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const bf2 lo = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v[k], 1.0f, false);
+    const bf2 hi = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v[k], 1.0f, true);
+    r[4 * k] = lo[0];
+    r[4 * k + 1] = lo[1];
+    r[4 * k + 2] = hi[0];
+    r[4 * k + 3] = hi[1];
+  }
+  return r;
+}
+
+// Place of 16-byte chunk c of row r in a ring tile in LDS, exchanged so that
+// neighbouring rows' equal chunks lie on other banks.
+template <int D>
+__device__ __forceinline__ int chunk8(int r, int c) {
+  if constexpr (D == 128) return c ^ ((r >> 1) & 7);
+  else return c ^ ((r >> 2) & 3);
+}
+
+// Operand of keys 32 base .. + 31 (lane % 32), elements 16 s + 8 h ..
+template <int D>
+__device__ __forceinline__ bf8 row8(const u4 *tile, int base, int s, int lane) {
+  typedef __attribute__((address_space(3))) const i2 lds8;
+  const int r = 32 * base + (lane & 31);
+  return widen(*(lds8 *)(lds_at(tile) + r * D + chunk8<D>(r, s) * 16 + (lane >> 5) * 8));
+}
+// Operand of elements 32 db + lane % 32 over keys 16 ks .., in the order of a D result.
+template <int D>
+__device__ __forceinline__ bf8 col8(const u4 *tile, int ks, int db, int lane) {
+  typedef __attribute__((address_space(3))) i2 lds8;
+  const int i = lane & 15, g = (lane >> 4) & 1, h = lane >> 5;
+  const int r = 16 * ks + 8 * (i >> 3) + 4 * h + ((i >> 1) & 3);
+  return widen(__builtin_amdgcn_ds_read_tr8_b64_v2i32((lds8 *)(lds_at(tile) + r * D + chunk8<D>(r, 2 * db + g) * 16 + (i & 1) * 8)));
+}
+// Start the copy of a block of the ring.
+template <int D>
+__device__ __forceinline__ void load_block(u4 *tile, const uint8_t *block, int lane) {
+  const unsigned lds = __builtin_amdgcn_readfirstlane(lds_at(tile));
+#pragma unroll
+  for (int k = 0; k < D / 16; ++k) {
+    const int id = k * 64 + lane, r = id / (D / 16);
+    copy16(lds + k * 1024, block, static_cast<unsigned>(r * D + chunk8<D>(r, id % (D / 16)) * 16));
+  }
+}
+
+// A block's scale. `top`: the largest |value|'s bits, NaN above all.
+__device__ __forceinline__ float scale_of(unsigned top) { return __uint_as_float(top) / 448.0f; }
+__device__ __forceinline__ float hold(float v) { return v > 448.0f ? 448.0f : v < -448.0f ? -448.0f : v; }
+// Eight bfloat16 as bytes.  A true division: a product with the reciprocal
+// would put quotients that lie between two bytes on either side.
+__device__ __forceinline__ uint2 to_e4m3(const u4 &v, float scale) {
+  const float s = scale != 0.0f ? scale : 1.0f;
+  uint2 out;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    int b = 0;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const unsigned pair = v[2 * k + x];
+      const float lo = hold(__uint_as_float(pair << 16) / s), hi = hold(__uint_as_float(pair & 0xffff0000u) / s);
+      b = x != 0 ? __builtin_amdgcn_cvt_pk_fp8_f32(lo, hi, b, true) : __builtin_amdgcn_cvt_pk_fp8_f32(lo, hi, b, false);
+    }
+    (k != 0 ? out.y : out.x) = static_cast<unsigned>(b);
+  }
+  return out;
+}
+// The larger of the magnitudes' bits (NaN above infinity above all).
+__device__ __forceinline__ unsigned top_of(unsigned top, const u4 &v) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const unsigned lo = v[k] << 16 & 0x7fff0000u, hi = v[k] & 0x7fff0000u;
+    top = top > lo ? top : lo;
+    top = top > hi ? top : hi;
+  }
+  return top;
+}
+__device__ __forceinline__ unsigned wave_top(unsigned top) {
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) {
+    const unsigned other = __shfl_xor(top, d);
+    top = top > other ? top : other;
+  }
+  return top;
+}
+
+// One wavefront stores 64 near positions, the last of them from the
+// arguments, as a block of the ring.
+template <int D>
+__device__ __forceinline__ void store_block(const uint16_t *near, const uint16_t *own, uint8_t *block, float *scale, int lane) {
+  constexpr int CH = D / 8;
+  u4 v[CH];
+  unsigned top = 0;
+#pragma unroll
+  for (int k = 0; k < CH; ++k) {
+    const int id = k * 64 + lane, r = id / CH, c = id % CH;
+    v[k] = *reinterpret_cast<const u4 *>((r == 63 ? own : near + r * D) + c * 8);
+    top = top_of(top, v[k]);
+  }
+  const float s = scale_of(wave_top(top));
+#pragma unroll
+  for (int k = 0; k < CH; ++k) reinterpret_cast<uint2 *>(block)[k * 64 + lane] = to_e4m3(v[k], s);
+  if (lane == 0) *scale = s;
+}
+
+template <int D>
+__global__ void __launch_bounds__(256) swa_q8_step_kernel(const SwaStepParams p, const SwaQ8Cache cache, unsigned splits,
+                                                          unsigned qblocks) {
+  constexpr int CH = D / 8, NB = D / 32, NS = D / 16, kNear = 32;
+  constexpr int kCopies = D / 16;  // copies of 1 KiB per tile, of either kind
+  __shared__ __align__(16) u4 lds[4][2][kSwaBlock * D / 16];  // wavefront, K or V; in the end o, [32][D] float32
+  __shared__ float tops[4][32], sums[4][32];
+  const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const unsigned nkv = static_cast<unsigned>(p.nkv), group = static_cast<unsigned>(p.nheads) / nkv;
+  const unsigned split = blockIdx.x % splits, rest = blockIdx.x / splits, qb = rest % qblocks, bc = rest / qblocks;
+  const int64_t b = bc / nkv, c = bc % nkv;
+  const int g0 = qb * 32, heads = static_cast<int>(group) - g0 < 32 ? static_cast<int>(group) - g0 : 32;
+  const int sinks = static_cast<int>(p.sinks), blocks = static_cast<int>(p.window / kSwaBlock);
+  const int pos = p.pos[b];
+  // Of the positions behind the sinks, `spot` is the token's: blocks before
+  // `now` are whole, and in the ring; place `off` of the near block is its own.
+  const int spot = pos - sinks, now = spot >> 6, off = spot & 63;
+  const int count = pos < sinks ? pos + 1 : sinks + off + 1, own = count - 1;  // near positions, the token the last
+  const uint16_t *kn = p.k + b * p.k_batch + c * D, *vn = p.v + b * p.v_batch + c * D;
+  uint16_t *near_k = cache.k_near + static_cast<int64_t>(bc) * (sinks + kSwaBlock) * D;
+  uint16_t *near_v = cache.v_near + static_cast<int64_t>(bc) * (sinks + kSwaBlock) * D;
+  f16v o[NB] = {};
+  float top = -INFINITY, sum = 0.0f;
+  if (pos >= 0) {
+    const int64_t ring = static_cast<int64_t>(bc) * p.window * D, scales = static_cast<int64_t>(bc) * blocks;
+    const int near_tiles = (count + kNear - 1) / kNear;
+    // Blocks of the ring that are seen: all whole ones, and of the one that
+    // the near block will replace the places behind `off`.
+    const int held = spot < 0 ? 0 : now < blocks ? now : blocks;
+    const int old = now >= blocks ? now % blocks : -1;
+    const int skip = old >= 0 && off == 63 ? old : blocks;  // it has no such places
+    const int tiles = near_tiles + (skip < blocks ? held - 1 : held);
+    const unsigned parts = splits * 4, part = split * 4 + wave;
+    const unsigned each = tiles / parts, more = tiles % parts;
+    const int lo = static_cast<int>(each * part + (part < more ? part : more));
+    const int hi = lo + static_cast<int>(each + (part < more ? 1 : 0));
+    u4 *kt = lds[wave][0], *vt = lds[wave][1];
+    const Lanes at = lanes_of<D>(lane);
+    auto block_of = [&](int i) { return i - near_tiles + (i - near_tiles >= skip ? 1 : 0); };
+    auto load = [&](u4 *tile, const uint16_t *near, const uint8_t *bytes, int i) {
+      if (i < near_tiles) load_tile<D, 64, kNear>(tile, near, D, i * kNear, own, lane);
+      else load_block<D>(tile, bytes + ring + static_cast<int64_t>(block_of(i)) * kSwaBlock * D, lane);
+    };
+    if (lo < hi) {
+      bf8 q[NS];
+      const int row = (lane & 31) < heads ? lane & 31 : 0;  // lanes past the group repeat its first head
+      const u4 *src = reinterpret_cast<const u4 *>(p.q + b * p.q_batch + (c * group + g0 + row) * D);
+#pragma unroll
+      for (int s = 0; s < NS; ++s) {
+        u4 v = src[2 * s + half];
+        if (p.scale < 0.0f) v ^= 0x80008000u;  // a negative scale is taken as -q
+        q[s] = __builtin_bit_cast(bf8, v);
+      }
+      const float c2 = fabsf(p.scale) * kLog2e;
+      float k_scale = 0.0f, v_scale = 0.0f;  // lane l: those of tile i + l, for every 64th i
+      for (int i = lo; i < hi; ++i) {
+        if (((i - lo) & 63) == 0) {
+          const int mine = i + lane < hi ? i + lane : hi - 1;
+          k_scale = mine < near_tiles ? 1.0f : cache.k_scale[scales + block_of(mine)];
+          v_scale = mine < near_tiles ? 1.0f : cache.v_scale[scales + block_of(mine)];
+          if (i == lo) {
+            load(kt, near_k, cache.k_ring, i);
+            load(vt, near_v, cache.v_ring, i);
+          }
+        }
+        const float ks = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(k_scale), (i - lo) & 63));
+        const float vs = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v_scale), (i - lo) & 63));
+        const bool near = i < near_tiles;
+        const int k0 = i * kNear;
+        const bool has = near && own >= k0 && own < k0 + kNear;
+        wait_tiles<kCopies>();  // the keys: all but the copies of the values
+        f16v s[2] = {};
+        if (near) {
+          if (has) put_row<D>(kt, kn, own - k0, lane);
+#pragma unroll
+          for (int x = 0; x < NS; ++x) s[0] = mfma(row_operand<D>(kt, 0, x, at), q[x], s[0]);
+#pragma unroll
+          for (int r = 0; r < 16; ++r) {
+            if (k0 + d_row(r, half) >= count) s[0][r] = -INFINITY;
+            s[1][r] = -INFINITY;
+          }
+        } else {
+#pragma unroll
+          for (int blk = 0; blk < 2; ++blk)
+#pragma unroll
+            for (int x = 0; x < NS; ++x) s[blk] = mfma(row8<D>(kt, blk, x, lane), q[x], s[blk]);
+          const int from = block_of(i) == old ? off : -1;
+#pragma unroll
+          for (int blk = 0; blk < 2; ++blk)
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+              if (32 * blk + d_row(r, half) <= from) s[blk][r] = -INFINITY;
+        }
+        wait_reads();
+        if (i + 1 < hi) load(kt, near_k, cache.k_ring, i + 1);
+        to_weights(s, fmaxf(c2 * ks, 0x1p-100f), o, top, sum);
+        if (i + 1 < hi) wait_tiles<kCopies>();  // the values: all but the copies of the next keys
+        else wait_tiles<0>();
+        if (near) {
+          if (has) put_row<D>(vt, vn, own - k0, lane);
+          // Rows behind the token repeat its slot, which may hold anything.
+          for (int r = own + 1 - k0 + lane / CH; has && r < kNear; r += 64 / CH) vt[slot<D>(r, lane % CH)] = u4{};
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            bf8 cut, rest;
+            two_parts(s[0], x, cut, rest);
+#pragma unroll
+            for (int db = 0; db < NB; ++db) {
+              const bf8 v = col_operand<D>(vt, 16 * x, db, at);
+              o[db] = mfma(v, cut, o[db]);
+              o[db] = mfma(v, rest, o[db]);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            bf8 cut, rest;
+#pragma unroll
+            for (int r = 0; r < 8; ++r) s[x / 2][8 * (x % 2) + r] *= vs;
+            two_parts(s[x / 2], x % 2, cut, rest);
+#pragma unroll
+            for (int db = 0; db < NB; ++db) {
+              const bf8 v = col8<D>(vt, x, db, lane);
+              o[db] = mfma(v, cut, o[db]);
+              o[db] = mfma(v, rest, o[db]);
+            }
+          }
+        }
+        wait_reads();
+        if (i + 1 < hi) load(vt, near_v, cache.v_ring, i + 1);
+        if (has && lane < CH) {  // the token takes its place
+          reinterpret_cast<u4 *>(near_k + static_cast<int64_t>(own) * D)[lane] = reinterpret_cast<const u4 *>(kn)[lane];
+          reinterpret_cast<u4 *>(near_v + static_cast<int64_t>(own) * D)[lane] = reinterpret_cast<const u4 *>(vn)[lane];
+        }
+      }
+    }
+    sum += other_half(sum);
+    // The near block is whole: it takes its place in the ring, of which no
+    // workgroup reads the block there.
+    if (off == 63 && spot >= 0 && split == 0 && qb == 0 && wave < 2) {
+      const int64_t to = now % blocks;
+      if (wave == 0)
+        store_block<D>(near_k + static_cast<int64_t>(sinks) * D, kn, cache.k_ring + ring + to * kSwaBlock * D, cache.k_scale + scales + to, lane);
+      else
+        store_block<D>(near_v + static_cast<int64_t>(sinks) * D, vn, cache.v_ring + ring + to * kSwaBlock * D, cache.v_scale + scales + to, lane);
+    }
+  }
+  join_waves<D>(p, lds, o, top, sum, tops, sums, heads, b * p.nheads + c * group + g0, splits, split);
+}
+
+// A workgroup per (row, key head, block of the ring), and one for what is
+// near.  Block r of the ring holds, of the `whole` complete blocks of the
+// row's positions behind the sinks, the last whose number is r mod the ring's.
+template <int D>
+__global__ void __launch_bounds__(256) swa_q8_fill_kernel(const SwaParams p, const SwaQ8Cache cache) {
+  constexpr int CH = D / 8, kEach = kSwaBlock * CH / 256;
+  __shared__ unsigned tops[2][4];
+  const int tid = threadIdx.x, blocks = static_cast<int>(p.window / kSwaBlock);
+  const int64_t items = blocks + 1, all = p.batch * p.nkv * items;
+  for (int64_t id = blockIdx.x; id < all; id += gridDim.x) {
+    const int64_t r = id % items, bc = id / items, c = bc % p.nkv, b = bc / p.nkv;
+    const int64_t n = row_length(p, b), behind = n > p.sinks ? n - p.sinks : 0, whole = behind / kSwaBlock;
+    const uint16_t *src[2] = {p.k + b * p.k_batch + c * D, p.v + b * p.v_batch + c * D};
+    const int64_t token[2] = {p.k_token, p.v_token};
+    if (r == blocks) {
+      const int64_t slots = p.sinks + kSwaBlock;
+      uint16_t *near[2] = {cache.k_near + bc * slots * D, cache.v_near + bc * slots * D};
+      for (int64_t i = tid; i < slots * CH; i += 256) {
+        const int64_t s = i / CH, e = i % CH * 8, pos = s < p.sinks ? s : s + whole * kSwaBlock;
+        if (pos < n)
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+            *reinterpret_cast<u4 *>(near[t] + s * D + e) = *reinterpret_cast<const u4 *>(src[t] + pos * token[t] + e);
+      }
+      continue;
+    }
+    if (r >= whole) continue;
+    const int64_t pos = p.sinks + (r + (whole - 1 - r) / blocks * blocks) * kSwaBlock;
+    u4 v[2][kEach];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      unsigned top = 0;
+#pragma unroll
+      for (int k = 0; k < kEach; ++k) {
+        const int at = k * 256 + tid;
+        v[t][k] = *reinterpret_cast<const u4 *>(src[t] + (pos + at / CH) * token[t] + at % CH * 8);
+        top = top_of(top, v[t][k]);
+      }
+      top = wave_top(top);
+      if ((tid & 63) == 0) tops[t][tid >> 6] = top;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      unsigned top = tops[t][0];
+#pragma unroll
+      for (int w = 1; w < 4; ++w) top = top > tops[t][w] ? top : tops[t][w];
+      const float s = scale_of(top);
+      uint2 *to = reinterpret_cast<uint2 *>((t == 0 ? cache.k_ring : cache.v_ring) + (bc * blocks + r) * kSwaBlock * D);
+#pragma unroll
+      for (int k = 0; k < kEach; ++k) to[k * 256 + tid] = to_e4m3(v[t][k], s);
+      if (tid == 0) (t == 0 ? cache.k_scale : cache.v_scale)[bc * blocks + r] = s;
+    }
+    __syncthreads();
+  }
+}
+
+}  // namespace
+
+int swa_q8_splits(int64_t batch, int64_t nheads, int64_t nkv, int64_t window, int64_t sinks) {
+  // Eight workgroups per CU even out rows of unequal length; a wavefront has at least one tile.
+  const int64_t rows = batch * nkv * ((nheads / nkv + 31) / 32), tiles = window / kSwaBlock + (sinks + kSwaBlock + 31) / 32;
+  const int64_t want = (2048 + rows - 1) / (rows > 0 ? rows : 1), most = (tiles + 3) / 4;
+  return static_cast<int>(want < most ? want : most);
+}
+
+hipError_t launch_swa_q8_step(const SwaStepParams &p, const SwaQ8Cache &cache, int splits, hipStream_t s) {
+  const unsigned qblocks = static_cast<unsigned>((p.nheads / p.nkv + 31) / 32), sp = static_cast<unsigned>(splits);
+  const dim3 g(static_cast<uint32_t>(p.batch * p.nkv * qblocks * splits)), gj(static_cast<uint32_t>(p.batch * p.nheads));
+  if (p.headdim == 64) {
+    hipLaunchKernelGGL((swa_q8_step_kernel<64>), g, dim3(256), 0, s, p, cache, sp, qblocks);
+    if (splits > 1) hipLaunchKernelGGL((swa_join_kernel<64>), gj, dim3(64), 0, s, p, splits);
+  } else {
+    hipLaunchKernelGGL((swa_q8_step_kernel<128>), g, dim3(256), 0, s, p, cache, sp, qblocks);
+    if (splits > 1) hipLaunchKernelGGL((swa_join_kernel<128>), gj, dim3(128), 0, s, p, splits);
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_swa_q8_fill(const SwaParams &p, const SwaQ8Cache &cache, hipStream_t s) {
+  const int64_t n = p.batch * p.nkv * (p.window / kSwaBlock + 1);
+  if (n == 0) return hipSuccess;
+  const dim3 g(static_cast<uint32_t>(n < kMaxGroups ? n : kMaxGroups));
+  if (p.headdim == 64) hipLaunchKernelGGL((swa_q8_fill_kernel<64>), g, dim3(256), 0, s, p, cache);
+  else hipLaunchKernelGGL((swa_q8_fill_kernel<128>), g, dim3(256), 0, s, p, cache);
+  return hipGetLastError();
+}
+
+}  // namespace ssmb

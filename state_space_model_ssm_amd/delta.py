@@ -8,20 +8,24 @@ The names are also available from the package itself:
 
     import state_space_model_ssm_amd as ssm
     y, h_last = ssm.gdr_fwd(q, k, v, g, beta)
+    q, k = ssm.qk_norm_fwd(q, k, wq, wk, inv_freq=inv_freq, pos=pos)
+    cache = ssm.swa_q8_cache(batch, nkv, window, headdim, sinks=4, device="cuda")
 """
 from __future__ import annotations
 
 import ctypes
 import os
+from typing import NamedTuple
 
 import torch
 
 from . import _DELTA, SsmError
-from .block import _BF16, _F32, _code, _heads, _out, _ptr, _same, _stream
+from .block import SwaDims, _BF16, _F32, _code, _heads, _out, _ptr, _same, _stream, _swa_dims
 
 __all__ = list(_DELTA)
 
 GDR_STATE_STEP = 64   # steps between two saved states of the delta rule
+SWA_Q8_BLOCK = 64     # positions that share a scale in an 8-bit cache
 
 _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libssm_delta.so")
 _lib = None
@@ -34,6 +38,26 @@ class GdrDims(ctypes.Structure):
                 ("k_token", ctypes.c_int64), ("v_batch", ctypes.c_int64), ("v_token", ctypes.c_int64),
                 ("scale", ctypes.c_float), ("gate_dtype", ctypes.c_int32), ("workspace", ctypes.c_void_p),
                 ("workspace_bytes", ctypes.c_size_t)]
+
+
+class QkNormDims(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64), ("nheads", ctypes.c_int64),
+                ("nkv", ctypes.c_int64), ("headdim", ctypes.c_int64), ("rot", ctypes.c_int64),
+                ("q_batch", ctypes.c_int64), ("q_token", ctypes.c_int64), ("k_batch", ctypes.c_int64),
+                ("k_token", ctypes.c_int64), ("oq_batch", ctypes.c_int64), ("oq_token", ctypes.c_int64),
+                ("ok_batch", ctypes.c_int64), ("ok_token", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("neighbours", ctypes.c_int32), ("eps", ctypes.c_float), ("reserved", ctypes.c_int32),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
+
+
+class SwaQ8Cache(NamedTuple):
+    """An 8-bit ring cache of keys and values (see ``ssm_swa_q8_step``)."""
+    k_near: torch.Tensor    # (batch, nkv, sinks + 64, headdim) bfloat16: sinks, and the block that is being filled
+    v_near: torch.Tensor
+    k_ring: torch.Tensor    # (batch, nkv, window, headdim) float8_e4m3fn: whole blocks
+    v_ring: torch.Tensor
+    k_scale: torch.Tensor   # (batch, nkv, window / 64) float32
+    v_scale: torch.Tensor
 
 
 def delta_library_path() -> str:
@@ -50,11 +74,14 @@ def delta_lib():
                 "(hipcc, gfx950). There is no fallback implementation.")
         L = ctypes.CDLL(_LIB_PATH)
         vp, size = ctypes.c_void_p, ctypes.POINTER(ctypes.c_size_t)
-        for name, pointers, dims in (("ssm_gdr_fwd", 10, GdrDims), ("ssm_gdr_bwd", 15, GdrDims), ("ssm_gdr_step", 8, GdrDims)):
+        for name, pointers, dims in (("ssm_gdr_fwd", 10, GdrDims), ("ssm_gdr_bwd", 15, GdrDims), ("ssm_gdr_step", 8, GdrDims),
+                                     ("ssm_qk_norm_fwd", 8, QkNormDims), ("ssm_qk_norm_bwd", 12, QkNormDims),
+                                     ("ssm_swa_q8_step", 11, SwaDims), ("ssm_swa_q8_fill", 9, SwaDims)):
             f = getattr(L, name)
             f.argtypes = [vp] * pointers + [ctypes.POINTER(dims), vp]
             f.restype = ctypes.c_int
-        for name, dims in (("ssm_gdr_workspace_size", GdrDims), ("ssm_gdr_bwd_workspace_size", GdrDims)):
+        for name, dims in (("ssm_gdr_workspace_size", GdrDims), ("ssm_gdr_bwd_workspace_size", GdrDims),
+                           ("ssm_qk_norm_bwd_workspace_size", QkNormDims), ("ssm_swa_q8_step_workspace_size", SwaDims)):
             f = getattr(L, name)
             f.argtypes = [ctypes.POINTER(dims), size]
             f.restype = ctypes.c_int
@@ -85,6 +112,14 @@ def gdr_workspace_size(dims: GdrDims) -> int:
 
 def gdr_bwd_workspace_size(dims: GdrDims) -> int:
     return _size(delta_lib().ssm_gdr_bwd_workspace_size, dims)
+
+
+def qk_norm_bwd_workspace_size(dims: QkNormDims) -> int:
+    return _size(delta_lib().ssm_qk_norm_bwd_workspace_size, dims)
+
+
+def swa_q8_step_workspace_size(dims: SwaDims) -> int:
+    return _size(delta_lib().ssm_swa_q8_step_workspace_size, dims)
 
 
 def _scratch(dims, need: int, workspace, like, stream):
@@ -208,3 +243,136 @@ def gdr_step(q, k, v, g, beta, h, *, scale=None, h_out=None, y=None, stream=None
     _check(delta_lib().ssm_gdr_step(_at(q), _at(k), _at(v), _ptr(g), _ptr(beta), _ptr(h), _ptr(y), _ptr(h_out),
                                     ctypes.byref(dims), _stream(stream)))
     return y, h_out
+
+
+# ---------------------------------------------------------------------------
+# Norms of queries and keys with the rotation by position
+# ---------------------------------------------------------------------------
+
+def _qk_norm_dims(q, k, wq, wk, inv_freq, pos, eps, neighbours, out_q, out_k) -> QkNormDims:
+    lead = q.dim() - 2
+    if lead not in (1, 2) or k.dim() != q.dim() or k.shape[:lead] != q.shape[:lead] or k.shape[-1] != q.shape[-1]:
+        raise ValueError("q and k must be (batch, seqlen, heads, headdim), or (batch, heads, headdim) in a step, "
+                         "of one batch, seqlen and headdim")
+    if k.dtype != q.dtype:
+        raise TypeError(f"k must have dtype {q.dtype}")
+    d = q.shape[-1]
+    _same("wq", wq, _F32, (d,))
+    _same("wk", wk, _F32, (d,))
+    rot = 0
+    if inv_freq is not None:
+        if inv_freq.dim() != 1:
+            raise ValueError("inv_freq must be (pairs,)")
+        _same("inv_freq", inv_freq, _F32, inv_freq.shape)
+        rot = 2 * inv_freq.shape[0]
+        if pos is None and lead == 1:
+            raise ValueError("pos is required in a step")
+    _same("pos", pos, torch.int32, q.shape[:lead])
+    return QkNormDims(q.shape[0], q.shape[1] if lead == 2 else 1, q.shape[-2], k.shape[-2], d, rot,
+                      *_heads("q", q, lead, d), *_heads("k", k, lead, d), *_heads("q's output", out_q, lead, d),
+                      *_heads("k's output", out_k, lead, d), _code(q.dtype), int(neighbours), eps)
+
+
+def qk_norm_fwd(q, k, wq=None, wk=None, *, inv_freq=None, pos=None, eps: float = 1e-6, neighbours: bool = False,
+                q_out=None, k_out=None, stream=None):
+    """RMS norm of every head of q and of k with the rotation by position
+    (``ssm_qk_norm_fwd``): n = x / sqrt(mean(x^2) + eps) * w, whose pairs i are
+    then rotated by pos * inv_freq[i].  q: (batch, L, nheads, headdim); k:
+    (batch, L, nkv, headdim), or both without L in a step; float32 or bfloat16,
+    headdim a multiple of 16 up to 256, views with any batch and token strides
+    that are multiples of 16 bytes.  wq, wk: (headdim,) float32 (ones when
+    None; filled with headdim ** -0.5 they give heads of unit length).
+    inv_freq: (pairs,) float32, 2 * pairs <= headdim elements of a head being
+    rotated, in pairs (i, i + pairs) or, with ``neighbours``, (2 i, 2 i + 1);
+    None for no rotation.  pos: (batch, L) int32 (0, 1, .. when None), (batch,)
+    in a step.  Returns ``(q_out, k_out)``, dense, or where q_out and k_out (q
+    and k themselves, or other views) are given."""
+    _one_device(stream, q, k, wq, wk, inv_freq, pos)
+    q_out = _out(q_out, q.shape, q.dtype, q, "q_out", stream)
+    k_out = _out(k_out, k.shape, k.dtype, q, "k_out", stream)
+    dims = _qk_norm_dims(q, k, wq, wk, inv_freq, pos, eps, neighbours, q_out, k_out)
+    _check(delta_lib().ssm_qk_norm_fwd(_at(q), _at(k), _ptr(wq), _ptr(wk), _ptr(inv_freq), _ptr(pos), _at(q_out),
+                                       _at(k_out), ctypes.byref(dims), _stream(stream)))
+    return q_out, k_out
+
+
+def qk_norm_bwd(q, k, wq, wk, dq_out, dk_out, *, inv_freq=None, pos=None, eps: float = 1e-6, neighbours: bool = False,
+                return_dw: bool = True, out=None, workspace=None, stream=None):
+    """Backward of ``qk_norm_fwd`` (``ssm_qk_norm_bwd``) from its inputs and
+    the gradients of its outputs (dense).  Returns ``(dq, dk, dwq, dwk)``: dq
+    and dk shaped like q and k, dwq and dwk (headdim,) float32 (None without
+    return_dw).  ``out``: a dict of preallocated outputs under those names, dq
+    and dk with any strides that q and k may have."""
+    _one_device(stream, q, k, wq, wk, inv_freq, pos, dq_out, dk_out, workspace)
+    _same("dq_out", dq_out, q.dtype, q.shape)
+    _same("dk_out", dk_out, q.dtype, k.shape)
+    o = out or {}
+    dq, dk = _out(o.get("dq"), q.shape, q.dtype, q, "dq", stream), _out(o.get("dk"), k.shape, q.dtype, q, "dk", stream)
+    dims = _qk_norm_dims(q, k, wq, wk, inv_freq, pos, eps, neighbours, dq, dk)
+    dwq = dwk = None
+    if return_dw or "dwq" in o or "dwk" in o:
+        dwq, dwk = (_out(o.get(n), q.shape[-1:], _F32, q, n, stream) for n in ("dwq", "dwk"))
+        workspace = _scratch(dims, qk_norm_bwd_workspace_size(dims), workspace, q, stream)
+    _check(delta_lib().ssm_qk_norm_bwd(_at(q), _at(k), _ptr(wq), _ptr(wk), _ptr(inv_freq), _ptr(pos), _ptr(dq_out),
+                                       _ptr(dk_out), _at(dq), _at(dk), _ptr(dwq), _ptr(dwk), ctypes.byref(dims),
+                                       _stream(stream)))
+    return dq, dk, dwq, dwk
+
+
+# ---------------------------------------------------------------------------
+# Sliding-window attention over a cache in 8 bits
+# ---------------------------------------------------------------------------
+
+def swa_q8_cache(batch: int, nkv: int, window: int, headdim: int, *, sinks: int = 0, device="cuda") -> SwaQ8Cache:
+    """A new, empty cache for ``swa_q8_step`` and ``swa_q8_fill``; window must be a multiple of 64."""
+    if window < SWA_Q8_BLOCK or window % SWA_Q8_BLOCK:
+        raise ValueError(f"window must be a multiple of {SWA_Q8_BLOCK}, got {window}")
+    e8 = torch.float8_e4m3fn
+    shapes = ((sinks + SWA_Q8_BLOCK, headdim), _BF16), ((window, headdim), e8), ((window // SWA_Q8_BLOCK,), _F32)
+    return SwaQ8Cache(*(torch.empty(batch, nkv, *shape, dtype=dt, device=device) for shape, dt in shapes for _ in "kv"))
+
+
+def _q8_cache(cache, batch, nkv, headdim, sinks) -> int:
+    """The window of a cache, whose tensors are checked."""
+    window = cache.k_ring.shape[2] if cache.k_ring.dim() == 4 else 0
+    if window % SWA_Q8_BLOCK:
+        raise ValueError(f"the cache's window must be a multiple of {SWA_Q8_BLOCK}, got {window}")
+    lead = (batch, nkv)
+    for name, t in cache._asdict().items():
+        kind = name[2:]
+        if kind == "near":
+            _same(name, t, _BF16, (*lead, sinks + SWA_Q8_BLOCK, headdim))
+        elif kind == "ring":
+            _same(name, t, torch.float8_e4m3fn, (*lead, window, headdim))
+        else:
+            _same(name, t, _F32, (*lead, window // SWA_Q8_BLOCK))
+    return window
+
+
+def swa_q8_step(q, k, v, cache: SwaQ8Cache, pos, *, sinks: int = 0, scale=None, y=None, workspace=None, stream=None):
+    """One token per batch row, as ``swa_step``, against an 8-bit cache
+    (``ssm_swa_q8_step``), which takes the token's k and v in place.  q:
+    (batch, nheads, headdim); k, v: (batch, nkv, headdim), bfloat16; pos:
+    (batch,) int32, the token's position, negative for a row without a token.
+    Returns y."""
+    _one_device(stream, q, k, v, *cache, pos, workspace)
+    dims = _swa_dims(q, k, v, 1, sinks, scale, 1)
+    dims.window = _q8_cache(cache, k.shape[0], k.shape[1], k.shape[2], sinks)
+    _same("pos", pos, torch.int32, (q.shape[0],))
+    y = _out(y, q.shape, _BF16, q, "y", stream)
+    workspace = _scratch(dims, swa_q8_step_workspace_size(dims), workspace, q, stream)
+    _check(delta_lib().ssm_swa_q8_step(_at(q), _at(k), _at(v), *map(_ptr, cache), _ptr(pos), _ptr(y), ctypes.byref(dims),
+                                       _stream(stream)))
+    return y
+
+
+def swa_q8_fill(k, v, cache: SwaQ8Cache, *, sinks: int = 0, lengths=None, stream=None):
+    """Store a prompt's keys and values ((batch, L, nkv, headdim)) into the
+    cache that ``swa_q8_step`` goes on from (``ssm_swa_q8_fill``): what a next
+    token sees of the positions below each length."""
+    _one_device(stream, k, v, *cache, lengths)
+    dims = _swa_dims(k, k, v, 1, sinks, 1.0, 2)
+    dims.window = _q8_cache(cache, k.shape[0], k.shape[2], k.shape[3], sinks)
+    _same("lengths", lengths, torch.int32, (k.shape[0],))
+    _check(delta_lib().ssm_swa_q8_fill(_at(k), _at(v), _ptr(lengths), *map(_ptr, cache), ctypes.byref(dims),
+                                       _stream(stream)))

@@ -93,6 +93,54 @@ def gdr_bwd(q, k, v, g, beta, dy, h0=None, lengths=None, scale=None, dh_last=Non
     return grads, sizes
 
 
+def qk_norm(x, w, inv_freq, pos, eps, neighbours):
+    """One of q and k, (batch, L, heads, d) float64; differentiable."""
+    n = x / (x.pow(2).mean(-1, keepdim=True) + eps).sqrt() * (1.0 if w is None else w)
+    if inv_freq is None:
+        return n
+    half = inv_freq.shape[0]
+    angle = (pos.double()[..., None] * inv_freq.double())[:, :, None]
+    a = n[..., 0:2 * half:2] if neighbours else n[..., :half]
+    b = n[..., 1:2 * half:2] if neighbours else n[..., half:2 * half]
+    c, s = angle.cos(), angle.sin()
+    a, b = a * c - b * s, b * c + a * s
+    turned = torch.stack([a, b], -1).flatten(-2) if neighbours else torch.cat([a, b], -1)
+    return torch.cat([turned, n[..., 2 * half:]], -1)
+
+
+E4M3 = torch.tensor([[m / 8 * 2.0 ** -6 if e == 0 else (1 + m / 8) * 2.0 ** (e - 7) for m in range(8)] for e in range(16)],
+                    dtype=torch.float64).flatten()[:127]
+
+
+def to_e4m3(x):
+    """Values within +-448 rounded to the nearest of the format, ties to the even one, by its table."""
+    hi = torch.searchsorted(E4M3, x.abs().contiguous()).clamp(max=126)
+    lo = (hi - 1).clamp(min=0)
+    up, down = E4M3[hi] - x.abs(), x.abs() - E4M3[lo]
+    code = torch.where((up < down) | ((up == down) & (hi % 2 == 0)), hi, lo)
+    return torch.sign(x) * E4M3[code]
+
+
+class Q8Cache:
+    """An 8-bit cache by the definition: every position's key and value, and what a query would be given of them."""
+
+    def __init__(self, batch, nkv, window, d, sinks):
+        self.window, self.sinks = window, sinks
+        self.rows = [([], []) for _ in range(batch)]     # per row: keys and values, (nkv, d) per position
+
+    def held(self, b, t, pos):
+        """(positions, nkv, d) that position `pos` sees, t = 0 for keys: blocks that were whole before it in 8 bits."""
+        x = torch.stack(self.rows[b][t]).double()
+        block = (pos - self.sinks) // 64 if pos >= self.sinks else 0
+        for n in range(block):
+            at = slice(self.sinks + 64 * n, self.sinks + 64 * n + 64)
+            block32 = x[at].float()   # scales are float32, and so are the quotients
+            scale = block32.abs().amax((0, 2), keepdim=True) / 448
+            x[at] = to_e4m3((block32 / torch.where(scale > 0, scale, 1.0)).clamp(-448, 448).double()) * scale.double()
+        seen = [j for j in range(pos + 1) if j < self.sinks or pos - j < self.window]
+        return x[seen]
+
+
 def close(got, want, tol, what):
     """Elementwise |got - want| <= tol; NaN nowhere."""
     got, want = f64(got), f64(want)
