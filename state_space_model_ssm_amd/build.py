@@ -34,6 +34,9 @@ CFLAGS = [
     "-Wall", "-Wno-unused-command-line-argument",
     f"-I{INCLUDE}", f"-I{CSRC}",
 ]
+# libssm_delta's matrix products leave their results in ordinary registers: in
+# the accumulators, half of a recurrence's instructions were moves from and to them.
+DELTA_FLAGS = ["-mllvm", "-amdgpu-mfma-vgpr-form"]
 
 
 def _object(src: str) -> str:
@@ -51,7 +54,7 @@ def build(verbose: bool = False) -> str:
     procs = []
     for src in [src for srcs in objects.values() for src in srcs]:
         obj = _object(src)
-        cmd = [HIPCC, *CFLAGS, "-c", src, "-o", obj]
+        cmd = [HIPCC, *CFLAGS, *(DELTA_FLAGS if src in objects[DELTA_LIB] else []), "-c", src, "-o", obj]
         if verbose:
             print(" ".join(cmd), flush=True)
         procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))

@@ -62,7 +62,7 @@ __global__ void __launch_bounds__(64 * NW) gdr_bwd_kernel(const GdrParams p) {
     for (int t = 0; t < CT; ++t)
 #pragma unroll
       for (int j = 0; j < NB; ++j) *reinterpret_cast<f4v *>(to + t * 16 * KD + 32 * (j / 2) + 4 * (j % 2)) = s[t][j];
-    arrive<0>();
+    arrive();
     if (c > 0) fetch(c - 1);
     const unsigned tile = base + (c & 1) * kBuffer, gates = tile + kAtW + kTri + 16 * g;
     // K dS
@@ -249,9 +249,9 @@ __global__ void __launch_bounds__(4 * KD) gdr_grad_kernel(const GdrParams p) {
       const char *ws = p.ws + id * static_cast<int64_t>(kGdrBwdChunkBytes);
       const float *gates = reinterpret_cast<const float *>(ws + 3 * kGdrTriBytes);
       const double *sums = reinterpret_cast<const double *>(gates + 256);
-      arrive<0>();  // what the last head left in LDS has been read
+      arrive();  // what the last head left in LDS has been read
       load_tile<VD, NT>(lds + kAtD / 16, p.dy + (b * p.seqlen * p.nheads + h) * VD, yt, t0, t0 + len - 1, tid);
-      arrive<0>();
+      arrive();
       // U = T beta (V - e^G K S0), a wavefront per 16 values; U and D = beta E go to LDS in parts.
       float db[4][4] = {};
       for (int ct = w; ct < VD / 16; ct += NW) {
@@ -317,7 +317,7 @@ __global__ void __launch_bounds__(4 * KD) gdr_grad_kernel(const GdrParams p) {
           const float v = sum16(db[i][r]);
           if (m == 0) red[0][w][16 * i + 4 * g + r] = v;
         }
-      arrive<0>();
+      arrive();
       // Products over the values, a wavefront per 16 key elements.
       f4v aq[4] = {}, ae[4] = {}, aw[4] = {};
       float both = 0.0f;
@@ -432,18 +432,18 @@ __global__ void __launch_bounds__(4 * KD) gdr_grad_kernel(const GdrParams p) {
       if constexpr (NW == 8) {
         if (w < 4) by_wave(w, [&](auto wave) { products(wave, std::false_type{}, frag[0]); });
         else by_wave(w - 4, [&](auto wave) { products(wave, std::true_type{}, frag[0]); });
-        arrive<0>();
+        arrive();
         keep(w & 3, w >> 2, frag[0]);
       } else {
         by_wave(w, [&](auto wave) {
           products(wave, std::false_type{}, frag[0]);
           products(wave, std::true_type{}, frag[1]);
         });
-        arrive<0>();
+        arrive();
         keep(w, 0, frag[0]);
         keep(w, 1, frag[1]);
       }
-      arrive<0>();
+      arrive();
       const unsigned fp = base + kAtU, fh = fp + 2 * kGdrTriBytes;
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
@@ -477,7 +477,7 @@ __global__ void __launch_bounds__(4 * KD) gdr_grad_kernel(const GdrParams p) {
       both += __shfl_xor(both, 16);
       both += __shfl_xor(both, 32);
       if (lane == 0) whole[w] = both;
-      arrive<0>();
+      arrive();
       if (w == 0 && lane < rows) {
         float dg = 0.0f, dbeta = 0.0f, total = 0.0f;
 #pragma unroll

@@ -181,164 +181,199 @@ __global__ void __launch_bounds__(256) gdr_chunk_kernel(const GdrParams p) {
 // From chunk to chunk
 // ---------------------------------------------------------------------------
 
-// A workgroup takes 16 CT NW columns (value elements) of a head from chunk to
-// chunk, a wavefront 16 CT of them.
-template <int KD, int CT, int NW>
-__global__ void __launch_bounds__(64 * NW) gdr_fwd_kernel(const GdrParams p) {
-  constexpr int NT = 64 * NW, NC = 16 * CT * NW, NS = KD / 32, NB = KD / 16;
+// A workgroup takes 32 columns (value elements) of a head from chunk to chunk.
+// What a chunk has to wait for is the state, so two wavefronts do nothing but
+// carry that, 16 columns each, and two others make y from the operands that
+// those leave in LDS, and copy the next chunk there: each of the four has a
+// SIMD to itself.
+constexpr int kPairs = 2;
+
+template <int KD>
+__global__ void __launch_bounds__(256) gdr_fwd_kernel(const GdrParams p) {
+  constexpr int NT = 64 * kPairs, NC = 16 * kPairs, NS = KD / 32, NB = KD / 16;
   constexpr unsigned kRows = 64 * KD * 2, kValues = 64 * NC * 2;
   constexpr unsigned kAtQ = kRows, kAtV = 2 * kRows, kAtW = kAtV + kValues, kBuffer = kAtW + kGdrChunkBytes;
-  __shared__ __align__(16) u4 lds[2 * kBuffer / 16];
+  constexpr unsigned kState = NS * 2 * 1024, kUpdate = 2 * 2 * 1024;  // operands of the state and of u, of a wavefront
+  __shared__ __align__(16) u4 lds[(2 * kBuffer + kPairs * (kState + kUpdate)) / 16];
   const int tid = threadIdx.x, lane = tid & 63, m = lane & 15, g = lane >> 4;
-  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), w = wave % kPairs;
   const unsigned vtiles = static_cast<unsigned>(p.vdim) / NC;
   const int64_t vt = blockIdx.x % vtiles, bh = blockIdx.x / vtiles, b = bh / p.nheads, h = bh % p.nheads;
   const int len = gdr_length(p.lengths, b, p.seqlen), n = (len + 63) / 64;
-  const int64_t hk = h / (p.nheads / p.nqk);
-  const int col = static_cast<int>(vt) * NC + 16 * CT * w + m;
+  const int col0 = static_cast<int>(vt) * NC + 16 * w;
+  const unsigned base = lds_at(lds), parts_s = base + 2 * kBuffer + w * kState + lane * 16;
+  const unsigned parts_u = base + 2 * kBuffer + kPairs * kState + w * kUpdate + lane * 16;
+  const Lanes16 at = lanes16_of<KD>(lane);
+  typedef __attribute__((address_space(3))) u4 lds16;
+
+  if (wave < kPairs) {
+    // The state: column col0 + m, key elements 32 a + 8g + 4x + r.
+    f4v s[NB];
+    const int64_t state = (bh * p.vdim + col0 + m) * KD + 8 * g;
+#pragma unroll
+    for (int j = 0; j < NB; ++j)
+      s[j] = p.h0 != nullptr ? *reinterpret_cast<const f4v *>(p.h0 + state + 32 * (j / 2) + 4 * (j % 2)) : f4v{};
+    for (int c = 0; c < n; ++c) {
+      Parts sp[NS];
+#pragma unroll
+      for (int a = 0; a < NS; ++a) {
+        sp[a] = parts(s[2 * a], s[2 * a + 1]);
+        *(lds16 *)(parts_s + a * 2048) = __builtin_bit_cast(u4, sp[a].hi);
+        *(lds16 *)(parts_s + a * 2048 + 1024) = __builtin_bit_cast(u4, sp[a].lo);
+      }
+      if (p.states != nullptr) {
+        float *to = p.states + ((bh * p.chunks + c) * p.vdim + col0 + m) * KD + 8 * g;
+#pragma unroll
+        for (int j = 0; j < NB; ++j) *reinterpret_cast<f4v *>(to + 32 * (j / 2) + 4 * (j % 2)) = s[j];
+      }
+      meet();
+      const unsigned tile = base + (c & 1) * kBuffer, tri_t = tile + kAtW, gates = tri_t + 2 * kGdrTriBytes + 16 * g;
+      // Operands are read ahead of their use, in its order.
+      bf8 ka[NS][4], kt[2][NB];
+      Parts tf[kGdrFrags];
+      sh4 vf[4];
+      f4v into[4], beta[4];
+#pragma unroll
+      for (int a = 0; a < NS; ++a)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) ka[a][i] = row16<KD>(tile, i, a, at);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        vf[i] = rows4<NC>(tile + kAtV, i, w, lane);
+        into[i] = lds_f4(gates + 256 + 64 * i);
+        beta[i] = lds_f4(gates + 768 + 64 * i);
+      }
+#pragma unroll
+      for (int f = 0; f < kGdrFrags; ++f) tf[f] = {frag16(tri_t, f, lane), frag16(tri_t, kGdrFrags + f, lane)};
+      __builtin_amdgcn_sched_barrier(0);
+      f4v x[4] = {};
+#pragma unroll
+      for (int a = 0; a < NS; ++a)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = mul_exact(ka[a][i], sp[a], x[i]);
+      // beta (v - e^G x), and u = T of that
+      f4v u[4] = {};
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) x[i][r] = beta[i][r] * fmaf(-into[i][r], x[i][r], up(vf[i][r]));
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const Parts xp = parts(x[2 * k], x[2 * k + 1]);
+#pragma unroll
+        for (int i = 2 * k; i < 4; ++i) u[i] = mul_parts(tf[tri(i, k)], xp, u[i]);
+      }
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int j = 0; j < NB; ++j) kt[k][j] = col16<KD>(tile, j, k, at);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const Parts up = parts(u[2 * k], u[2 * k + 1]);
+        *(lds16 *)(parts_u + k * 2048) = __builtin_bit_cast(u4, up.hi);
+        *(lds16 *)(parts_u + k * 2048 + 1024) = __builtin_bit_cast(u4, up.lo);
+      }
+      meet();
+      // s = e^GC s + sum over tokens of k (e^(GC - G) u)
+      const float whole = lds_f4(tri_t + 2 * kGdrTriBytes + 256 + 240)[3];
+#pragma unroll
+      for (int j = 0; j < NB; ++j) s[j] *= whole;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const f4v o0 = lds_f4(gates + 512 + 128 * k), o1 = lds_f4(gates + 512 + 128 * k + 64);
+        const Parts up = parts(u[2 * k] * o0, u[2 * k + 1] * o1);
+#pragma unroll
+        for (int j = 0; j < NB; ++j) s[j] = mul_exact(kt[k][j], up, s[j]);
+      }
+    }
+    if (p.h_last != nullptr) {
+#pragma unroll
+      for (int j = 0; j < NB; ++j) *reinterpret_cast<f4v *>(p.h_last + state + 32 * (j / 2) + 4 * (j % 2)) = s[j];
+    }
+    return;
+  }
+
+  const int id = tid - NT;
+  const int64_t hk = h / (p.nheads / p.nqk), yt = p.nheads * p.vdim;
   const uint16_t *kp = p.k + b * p.k_batch + hk * KD, *qp = p.q + b * p.q_batch + hk * KD;
   const uint16_t *vp = p.v + b * p.v_batch + h * p.vdim + vt * NC;
   const char *ws = p.ws + bh * p.chunks * static_cast<int64_t>(kGdrChunkBytes);
-  const unsigned base = lds_at(lds);
-  const Lanes16 at = lanes16_of<KD>(lane);
-
-  auto fetch = [&](int c) {
+  uint16_t *yp = p.y + (b * p.seqlen * p.nheads + h) * p.vdim + col0;
+  TileCopy<KD, NT> k_copy, q_copy;
+  TileCopy<NC, NT> v_copy;
+  k_copy.init(p.k_token, id);
+  q_copy.init(p.q_token, id);
+  v_copy.init(p.v_token, id);
+  RowStore y_store;
+  y_store.init(yt, lane);
+  auto fetch_rows = [&](int c) {
     u4 *to = lds + (c & 1) * (kBuffer / 16);
-    load_tile<KD, NT>(to, kp, p.k_token, 64 * c, len - 1, tid);
-    load_tile<KD, NT>(to + kAtQ / 16, qp, p.q_token, 64 * c, len - 1, tid);
-    const uint16_t *v0 = vp + 64 * c * p.v_token;
-    const unsigned vl = __builtin_amdgcn_readfirstlane(base + (c & 1) * kBuffer + kAtV + (tid & ~63) * 16);
     const int last = len - 1 - 64 * c;
-#pragma unroll
-    for (int k = 0; k < 64 * NC / 8 / NT; ++k) {
-      const int id = k * NT + tid, r = id / (NC / 8), e = vslot<NC>(r, id % (NC / 8)) - r * (NC / 8);
-      copy16(vl + k * NT * 16, v0, static_cast<unsigned>(r < last ? r : last) * static_cast<unsigned>(p.v_token) * 2 + e * 16);
-    }
-    const char *wc = ws + c * static_cast<int64_t>(kGdrChunkBytes);
-    for (int k = w; k < static_cast<int>(kGdrChunkBytes / 1024); k += NW)
-      copy16(__builtin_amdgcn_readfirstlane(base + (c & 1) * kBuffer + kAtW + k * 1024), wc, k * 1024 + lane * 16);
+    k_copy.start(to, kp + 64 * c * p.k_token, last, id);
+    q_copy.start(to + kAtQ / 16, qp + 64 * c * p.q_token, last, id);
+    v_copy.start(to + kAtV / 16, vp + 64 * c * p.v_token, last, id);
   };
-
-  if (n > 0) fetch(0);
-  // The state: column `col` + 16 t, key elements 32 a + 8g + 4x + r.
-  f4v s[CT][NB];
-  const int64_t state = (bh * p.vdim + col) * KD + 8 * g;
-#pragma unroll
-  for (int t = 0; t < CT; ++t)
-#pragma unroll
-    for (int j = 0; j < NB; ++j)
-      s[t][j] = p.h0 != nullptr ? *reinterpret_cast<const f4v *>(p.h0 + state + t * 16 * KD + 32 * (j / 2) + 4 * (j % 2)) : f4v{};
-  uint16_t *yp = p.y + (b * p.seqlen * p.nheads + h) * p.vdim + col;
-  const int64_t yt = p.nheads * p.vdim;
-
+  auto fetch_ws = [&](int c) {
+    copy_share<kGdrChunkBytes / 1024, kPairs>(base + (c & 1) * kBuffer + kAtW, ws + c * static_cast<int64_t>(kGdrChunkBytes), w, lane * 16);
+  };
+  if (n > 0) {
+    fetch_rows(0);
+    fetch_ws(0);
+  }
+  f4v o[4];
+  auto store = [&](int c) {
+    const int64_t rest = p.seqlen - 64 * static_cast<int64_t>(c);
+    y_store.put(yp + 64 * c * yt, rest < 64 ? static_cast<int>(rest) : 64, o);
+  };
   for (int c = 0; c < n; ++c) {
-    if (p.states != nullptr) {
-      float *to = p.states + ((bh * p.chunks + c) * p.vdim + col) * KD + 8 * g;
-#pragma unroll
-      for (int t = 0; t < CT; ++t)
-#pragma unroll
-        for (int j = 0; j < NB; ++j) *reinterpret_cast<f4v *>(to + t * 16 * KD + 32 * (j / 2) + 4 * (j % 2)) = s[t][j];
-    }
-    arrive<0>();
-    if (c + 1 < n) fetch(c + 1);
-    const unsigned tile = base + (c & 1) * kBuffer, gates = tile + kAtW + 2 * kGdrTriBytes + 16 * g;
-    f4v x[CT][4] = {}, o[CT][4] = {};
+    // Stores may be done before or after older copies, so the wait is for both:
+    // y of a chunk is stored with the next one, long before that.
+    arrive();
+    if (c + 1 < n) fetch_rows(c + 1);
+    if (c > 0) store(c - 1);
+    const unsigned tile = base + (c & 1) * kBuffer, tri_a = tile + kAtW + kGdrTriBytes, gates = tri_a + kGdrTriBytes + 16 * g;
+    bf8 qa[NS][4];
+    Parts sp[NS], af[kGdrFrags];
+    f4v qs[4];
 #pragma unroll
     for (int a = 0; a < NS; ++a) {
-      Parts sp[CT];
+      sp[a] = {__builtin_bit_cast(bf8, *(const lds16 *)(parts_s + a * 2048)),
+               __builtin_bit_cast(bf8, *(const lds16 *)(parts_s + a * 2048 + 1024))};
 #pragma unroll
-      for (int t = 0; t < CT; ++t) sp[t] = parts(s[t][2 * a], s[t][2 * a + 1]);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const bf8 ka = row16<KD>(tile, i, a, at), qa = row16<KD>(tile + kAtQ, i, a, at);
-#pragma unroll
-        for (int t = 0; t < CT; ++t) {
-          x[t][i] = mul_exact(ka, sp[t], x[t][i]);
-          o[t][i] = mul_exact(qa, sp[t], o[t][i]);
-        }
-      }
+      for (int i = 0; i < 4; ++i) qa[a][i] = row16<KD>(tile + kAtQ, i, a, at);
     }
-    // beta (v - e^G x), and e^G scale o
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const f4v qs = lds_f4(gates + 64 * i), into = lds_f4(gates + 256 + 64 * i), beta = lds_f4(gates + 768 + 64 * i);
+    for (int i = 0; i < 4; ++i) qs[i] = lds_f4(gates + 64 * i);
 #pragma unroll
-      for (int t = 0; t < CT; ++t) {
-        const sh4 v = rows4<NC>(tile + kAtV, i, CT * w + t, lane);
+    for (int f = 0; f < kGdrFrags; ++f) af[f] = {frag16(tri_a, f, lane), frag16(tri_a, kGdrFrags + f, lane)};
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          x[t][i][r] = beta[r] * fmaf(-into[r], x[t][i][r], up(v[r]));
-          o[t][i][r] *= qs[r];
-        }
-      }
-    }
-    // u = T x
-    f4v u[CT][4] = {};
-    const unsigned tri_t = tile + kAtW, tri_a = tri_t + kGdrTriBytes;
+    for (int i = 0; i < 4; ++i) o[i] = f4v{};
+#pragma unroll
+    for (int a = 0; a < NS; ++a)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[i] = mul_exact(qa[a][i], sp[a], o[i]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] *= qs[i];
+    meet();
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      Parts xp[CT];
+      const Parts up = {__builtin_bit_cast(bf8, *(const lds16 *)(parts_u + k * 2048)),
+                        __builtin_bit_cast(bf8, *(const lds16 *)(parts_u + k * 2048 + 1024))};
 #pragma unroll
-      for (int t = 0; t < CT; ++t) xp[t] = parts(x[t][2 * k], x[t][2 * k + 1]);
-#pragma unroll
-      for (int i = 2 * k; i < 4; ++i) {
-        const Parts ta = {frag16(tri_t, tri(i, k), lane), frag16(tri_t, kGdrFrags + tri(i, k), lane)};
-#pragma unroll
-        for (int t = 0; t < CT; ++t) u[t][i] = mul_parts(ta, xp[t], u[t][i]);
-      }
+      for (int i = 2 * k; i < 4; ++i) o[i] = mul_parts(af[tri(i, k)], up, o[i]);
     }
-    // o += A u
+    if (c + 1 < n) fetch_ws(c + 1);
+    if (64 * c + 64 > len) {
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      Parts up[CT];
+      for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int t = 0; t < CT; ++t) up[t] = parts(u[t][2 * k], u[t][2 * k + 1]);
-#pragma unroll
-      for (int i = 2 * k; i < 4; ++i) {
-        const Parts aa = {frag16(tri_a, tri(i, k), lane), frag16(tri_a, kGdrFrags + tri(i, k), lane)};
-#pragma unroll
-        for (int t = 0; t < CT; ++t) o[t][i] = mul_parts(aa, up[t], o[t][i]);
-      }
+        for (int r = 0; r < 4; ++r)
+          if (64 * c + 16 * i + 4 * g + r >= len) o[i][r] = 0.0f;
     }
-    // s = e^GC s + sum over tokens of k (e^(GC - G) u)
-    const float whole = lds_f4(tile + kAtW + 2 * kGdrTriBytes + 256 + 240)[3];
-#pragma unroll
-    for (int t = 0; t < CT; ++t)
-#pragma unroll
-      for (int j = 0; j < NB; ++j) s[t][j] *= whole;
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      Parts up[CT];
-      const f4v o0 = lds_f4(gates + 512 + 128 * k), o1 = lds_f4(gates + 512 + 128 * k + 64);
-#pragma unroll
-      for (int t = 0; t < CT; ++t) up[t] = parts(u[t][2 * k] * o0, u[t][2 * k + 1] * o1);
-#pragma unroll
-      for (int j = 0; j < NB; ++j) {
-        const bf8 kt = col16<KD>(tile, j, k, at);
-#pragma unroll
-        for (int t = 0; t < CT; ++t) s[t][j] = mul_exact(kt, up[t], s[t][j]);
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int64_t row = 64 * static_cast<int64_t>(c) + 16 * i + 4 * g + r;
-        if (row < p.seqlen)
-#pragma unroll
-          for (int t = 0; t < CT; ++t) st(yp, row * yt + 16 * t, row < len ? o[t][i][r] : 0.0f);
-      }
   }
-  for (int64_t row = 64 * static_cast<int64_t>(n) + g; row < p.seqlen; row += 4)
-#pragma unroll
-    for (int t = 0; t < CT; ++t) st(yp, row * yt + 16 * t, 0.0f);
-  if (p.h_last != nullptr) {
-#pragma unroll
-    for (int t = 0; t < CT; ++t)
-#pragma unroll
-      for (int j = 0; j < NB; ++j)
-        *reinterpret_cast<f4v *>(p.h_last + state + t * 16 * KD + 32 * (j / 2) + 4 * (j % 2)) = s[t][j];
-  }
+  if (n > 0) store(n - 1);
+  for (int64_t row = 64 * static_cast<int64_t>(n) + g; row < p.seqlen; row += 4) st(yp, row * yt + m, 0.0f);
 }
 
 // ---------------------------------------------------------------------------
@@ -413,7 +448,7 @@ void chunks(const GdrParams &p, bool bwd, hipStream_t s) {
 template <int KD>
 hipError_t fwd(const GdrParams &p, hipStream_t s) {
   const int64_t heads = p.batch * p.nheads;
-  hipLaunchKernelGGL((gdr_fwd_kernel<KD, 1, 4>), dim3(static_cast<uint32_t>(heads * (p.vdim / 64))), dim3(256), 0, s, p);
+  hipLaunchKernelGGL((gdr_fwd_kernel<KD>), dim3(static_cast<uint32_t>(heads * (p.vdim / 32))), dim3(256), 0, s, p);
   return hipGetLastError();
 }
 

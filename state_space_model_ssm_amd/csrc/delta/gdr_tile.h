@@ -119,11 +119,11 @@ __device__ __forceinline__ void by_wave(int w, F &&f) {
   }
 }
 
-// All but the last N of this wavefront's copies and stores are done, then all wavefronts meet.
-template <int N>
-__device__ __forceinline__ void arrive() {
-  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
-}
+// This wavefront's copies and stores are done, then all wavefronts meet.
+__device__ __forceinline__ void arrive() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
+// All wavefronts meet, with what they have read and written in LDS.
+__device__ __forceinline__ void meet() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
 // LDS slot of a tile of 64 rows of NC values.
 template <int NC>
@@ -138,6 +138,134 @@ __device__ __forceinline__ sh4 rows4(unsigned tile, int i, int ct, int lane) {
   const int m = lane & 15, r = 16 * i + 4 * (lane >> 4) + (m >> 2), piece = 4 * ct + (m & 3);
   return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)(tile + vslot<NC>(r, piece >> 1) * 16 + (piece & 1) * 8));
 }
+typedef __attribute__((ext_vector_type(4))) int i4;
+// A value that all lanes share, in scalar registers.  A memory instruction may
+// read those five instructions after a vector instruction wrote them, which the
+// compiler keeps to for its own, not for those in asm.
+template <typename T>
+__device__ __forceinline__ T *uniform(T *p) {
+  const uint64_t at = reinterpret_cast<uint64_t>(p);
+  // (The builtin gives a signed int, which must not widen as one.)
+  const uint32_t hi = static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<int>(at >> 32)));
+  const uint32_t lo = static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<int>(at)));
+  uint64_t u = static_cast<uint64_t>(hi) << 32 | lo;
+  asm volatile("s_nop 4" : "+s"(u));
+  return reinterpret_cast<T *>(u);
+}
+// A buffer resource: `bytes` from p.
+__device__ __forceinline__ i4 resource(const void *p, unsigned bytes) {
+  const uint64_t at = reinterpret_cast<uint64_t>(p);
+  i4 r = {__builtin_amdgcn_readfirstlane(static_cast<int>(at)),
+          __builtin_amdgcn_readfirstlane(static_cast<int>(at >> 32)) & 0xffff,
+          __builtin_amdgcn_readfirstlane(static_cast<int>(bytes)), 0x00027000};
+  asm volatile("s_nop 4" : "+s"(r));
+  return r;
+}
+// Copies of 16 bytes per lane from memory to LDS (see copy16()), at a lane's
+// offset plus one that all lanes share: few instructions per copy, for a
+// wavefront that has its SIMD to itself is bound by how many it issues.
+__device__ __forceinline__ void copy16(unsigned lds, const i4 &from, unsigned lane_off, unsigned off) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+               :
+               : "s"(lds), "v"(lane_off), "s"(from), "s"(off)
+               : "memory", "m0");
+}
+// N KiB from `from` (this lane's 16 bytes at lane_off) to LDS, in order.
+template <int N>
+__device__ __forceinline__ void copy_kib(unsigned lds, const void *from, unsigned lane_off) {
+  static_assert(N >= 1 && N <= 4, "the immediate offset");
+  if constexpr (N == 1)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" : : "s"(lds), "v"(lane_off), "s"(from) : "memory", "m0");
+  else if constexpr (N == 2)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2\n\tglobal_load_lds_dwordx4 %1, %2 offset:1024"
+                 :
+                 : "s"(lds), "v"(lane_off), "s"(from)
+                 : "memory", "m0");
+  else if constexpr (N == 3)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2\n\tglobal_load_lds_dwordx4 %1, %2 offset:1024"
+                 "\n\tglobal_load_lds_dwordx4 %1, %2 offset:2048"
+                 :
+                 : "s"(lds), "v"(lane_off), "s"(from)
+                 : "memory", "m0");
+  else
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2\n\tglobal_load_lds_dwordx4 %1, %2 offset:1024"
+                 "\n\tglobal_load_lds_dwordx4 %1, %2 offset:2048\n\tglobal_load_lds_dwordx4 %1, %2 offset:3072"
+                 :
+                 : "s"(lds), "v"(lane_off), "s"(from)
+                 : "memory", "m0");
+}
+// A wavefront's share (of NW) of KIB KiB.
+template <int KIB, int NW>
+__device__ __forceinline__ void copy_share(unsigned lds, const char *from, int w, unsigned lane_off) {
+  constexpr int kEach = (KIB + NW - 1) / NW, kLast = KIB - kEach * (NW - 1);
+  static_assert(kLast > 0 && kLast <= kEach, "shares");
+  lds = __builtin_amdgcn_readfirstlane(lds + w * kEach * 1024);
+  from = uniform(from + w * kEach * 1024);
+#pragma unroll
+  for (int k = 0; k < kLast; k += 4) {
+    constexpr int kRest = kLast % 4;
+    if (k + 4 <= kLast) copy_kib<4>(lds + k * 1024, from + k * 1024, lane_off);
+    else copy_kib<kRest != 0 ? kRest : 4>(lds + k * 1024, from + k * 1024, lane_off);
+  }
+  if constexpr (kEach > kLast) {
+    if (w < NW - 1)
+#pragma unroll
+      for (int k = kLast; k < kEach; ++k) copy_kib<1>(lds + k * 1024, from + k * 1024, lane_off);
+  }
+}
+
+// Copies of a tile of 64 rows of NC values, laid out by vslot<NC>(), by NT
+// threads.  Rows a multiple of 16 apart have the same exchange of chunks, so a
+// lane has one offset, or two, for all its pieces.
+template <int NC, int NT>
+struct TileCopy {
+  static constexpr int kChunks = NC / 8, kRows = NT / kChunks, kOffsets = kRows >= 16 ? 1 : 16 / kRows;
+  unsigned off[kOffsets], stride;  // in bytes
+  __device__ __forceinline__ void init(int64_t token, int tid) {
+    stride = static_cast<unsigned>(token) * 2;
+#pragma unroll
+    for (int q = 0; q < kOffsets; ++q) {
+      const int r = q * kRows + tid / kChunks, c = tid % kChunks;
+      off[q] = r * stride + (vslot<NC>(r, c) - r * kChunks) * 16;
+    }
+  }
+  // p: the first of 64 rows, of which those past `last` are read as that one.
+  __device__ __forceinline__ void start(u4 *tile, const uint16_t *p, int last, int tid) const {
+    const unsigned lds = __builtin_amdgcn_readfirstlane(lds_at(tile) + (tid & ~63) * 16);
+    if (last >= 63) {
+      const i4 from = resource(p, 63 * stride + NC * 2);
+#pragma unroll
+      for (int k = 0; k < 64 / kRows; ++k)
+        copy16(lds + k * NT * 16, from, off[k % kOffsets], __builtin_amdgcn_readfirstlane(k / kOffsets * (kOffsets * kRows) * stride));
+    } else {
+      p = uniform(p);
+#pragma unroll
+      for (int k = 0; k < 64 / kRows; ++k) {
+        const int r = k * kRows + tid / kChunks, c = vslot<NC>(r, tid % kChunks) - r * kChunks;
+        copy16(lds + k * NT * 16, p, static_cast<unsigned>(r < last ? r : last) * stride + c * 16);
+      }
+    }
+  }
+};
+
+// Store D results (rows: tokens, this lane's column) of a chunk as bfloat16,
+// `stride` bytes between tokens.  Rows behind `rows` are dropped.
+struct RowStore {
+  unsigned lane_off, stride;
+  __device__ __forceinline__ void init(int64_t token, int lane) {
+    stride = static_cast<unsigned>(token) * 2;
+    lane_off = 4 * (lane >> 4) * stride + (lane & 15) * 2;
+  }
+  __device__ __forceinline__ void put(uint16_t *p, int rows, const f4v (&o)[4]) const {
+    const auto to = __builtin_amdgcn_make_buffer_rsrc(uniform(p), 0, rows > 0 ? (static_cast<unsigned>(rows) - 1) * stride + 32 : 0, 0x00027000);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(short, static_cast<__bf16>(o[i][r])), to, lane_off, (16 * i + r) * stride, 0);
+  }
+};
+
 __device__ __forceinline__ float up(short v) {
   return __uint_as_float(static_cast<unsigned>(static_cast<uint16_t>(v)) << 16);
 }
