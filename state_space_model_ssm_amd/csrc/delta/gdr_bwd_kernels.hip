@@ -198,6 +198,16 @@ __device__ __forceinline__ Parts tokens16(const Pair &t, int i, int s, unsigned 
   return {tokens16(t.hi, i, s, col), tokens16(t.lo, i, s, col)};
 }
 
+// Operand of a slice of 32 values [value][key element]: lane m stands for the
+// element at `at`, k for values 8g ..
+template <int D>
+__device__ __forceinline__ bf8 values16(unsigned at) {
+  typedef __attribute__((address_space(3))) sh4 lds4;
+  const sh4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)(at));
+  const sh4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)((at ^ 16) + 8 * D));
+  return __builtin_bit_cast(bf8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+
 // Operand of the elements 16 ct + m of a row-major tile, k its rows 32 s .. in D's order.
 template <int D>
 __device__ __forceinline__ bf8 elems16(unsigned tile, int ct, int s, int lane) {
@@ -223,75 +233,97 @@ template <int KD, int VD, typename G>
 __global__ void __launch_bounds__(4 * KD) gdr_grad_kernel(const GdrParams p) {
   constexpr int NW = KD / 16, NT = 64 * NW, NS = KD / 32, NV = VD / 32;
   constexpr unsigned kRows = 64 * KD * 2, kAtQ = kRows, kAtD = 2 * kRows, kAtU = kAtD + 64 * VD * 2, kPart = VD * 128;
-  constexpr unsigned kFour = 4 * (4 * kPart > 4 * kGdrTriBytes ? kPart : kGdrTriBytes);
-  __shared__ __align__(16) u4 lds[(kAtU + kFour) / 16];
+  constexpr unsigned kFour = 4 * (kPart > kGdrTriBytes ? kPart : kGdrTriBytes), kAtS = kAtU + kFour, kSlice = 32 * KD * 2;
+  __shared__ __align__(16) u4 lds[(kAtS + 4 * kSlice) / 16];
   __shared__ float red[2][NW][64], whole[NW];
-  const int tid = threadIdx.x, lane = tid & 63, m = lane & 15, g = lane >> 4;
-  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t c = blockIdx.x % p.chunks, bk = blockIdx.x / p.chunks, b = bk / p.nqk, hk = bk % p.nqk;
   const int64_t share = p.nheads / p.nqk;
   const int t0 = static_cast<int>(c) * 64, len = gdr_length(p.lengths, b, p.seqlen) - t0;
   const int rows = p.seqlen - t0 < 64 ? static_cast<int>(p.seqlen - t0) : 64;
-  uint16_t *dqp = p.dq + ((b * p.seqlen + t0) * p.nqk + hk) * KD + 16 * w + m;
-  uint16_t *dkp = p.dk + ((b * p.seqlen + t0) * p.nqk + hk) * KD + 16 * w + m;
-  const int64_t row_step = p.nqk * KD;
   f4v tq[4] = {}, tk[4] = {};
   if (len > 0) {
     const unsigned base = lds_at(lds);
-    const Lanes16 atk = lanes16_of<KD>(lane), atv = lanes16_of<VD>(lane);
-    // Where this lane's pieces of transposed reads lie: row 8g + m / 4, tokens 4 (m % 4) ..
-    const unsigned col = static_cast<unsigned>(slot<64>(8 * g + (m >> 2), (m & 3) >> 1)) * 16 + (m & 1) * 8;
-    const Pair U = {base + kAtU, base + kAtU + kPart}, D = {base + kAtU + 2 * kPart, base + kAtU + 3 * kPart};
-    load_tile<KD, NT>(lds, p.k + b * p.k_batch + hk * KD, p.k_token, t0, t0 + len - 1, tid);
-    load_tile<KD, NT>(lds + kAtQ / 16, p.q + b * p.q_batch + hk * KD, p.q_token, t0, t0 + len - 1, tid);
+    load_tile<KD, NT>(lds, p.k + b * p.k_batch + hk * KD, p.k_token, t0, t0 + len - 1, threadIdx.x);
+    load_tile<KD, NT>(lds + kAtQ / 16, p.q + b * p.q_batch + hk * KD, p.q_token, t0, t0 + len - 1, threadIdx.x);
+#pragma unroll 1
     for (int64_t h = hk * share; h < (hk + 1) * share; ++h) {
+    // (Made anew for each head: the compiler would keep all that follows from
+    // it, hundreds of addresses and masks, from one head to the next.)
+    int tid = threadIdx.x;
+    asm volatile("" : "+v"(tid));
+    const int lane = tid & 63, m = lane & 15, g = lane >> 4;
+    const Lanes16 atk = lanes16_of<KD>(lane), atv = lanes16_of<VD>(lane);
+    // Where this lane's pieces of transposed reads lie: row 8g + m / 4, elements 4 (m % 4) ..
+    const unsigned col = static_cast<unsigned>(slot<64>(8 * g + (m >> 2), (m & 3) >> 1)) * 16 + (m & 1) * 8;
+    const unsigned col_s = (static_cast<unsigned>(slot<KD>(8 * g + (m >> 2), (m & 3) >> 1)) * 16 + (m & 1) * 8) ^ (32 * w);
+    const Pair U = {base + kAtU, base + kAtU + kPart}, D = {base + kAtU + 2 * kPart, base + kAtU + 3 * kPart};
       const int64_t bh = b * p.nheads + h, id = bh * p.chunks + c, yt = p.nheads * VD;
       const char *ws = p.ws + id * static_cast<int64_t>(kGdrBwdChunkBytes);
       const float *gates = reinterpret_cast<const float *>(ws + 3 * kGdrTriBytes);
       const double *sums = reinterpret_cast<const double *>(gates + 256);
-      arrive();  // what the last head left in LDS has been read
+      const float *s0 = p.states + id * VD * KD, *ds0 = p.ws_ds + id * VD * KD;
       load_tile<VD, NT>(lds + kAtD / 16, p.dy + (b * p.seqlen * p.nheads + h) * VD, yt, t0, t0 + len - 1, tid);
-      arrive();
+      // Of 32 values at a time, this thread's 8 elements of the state and of dS.
+      f4v sv[2], dv[2];
+      auto fetch_slice = [&](int s) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          sv[k] = *reinterpret_cast<const f4v *>(s0 + s * 32 * KD + (k * NT + tid) * 4);
+          dv[k] = *reinterpret_cast<const f4v *>(ds0 + s * 32 * KD + (k * NT + tid) * 4);
+        }
+      };
       // U = T beta (V - e^G K S0), a wavefront per 16 values; U and D = beta E go to LDS in parts.
       float db[4][4] = {};
+#pragma unroll 1
       for (int ct = w; ct < VD / 16; ct += NW) {
-        f4v x[4] = {};
-        const float *s0 = p.states + (id * VD + 16 * ct + m) * KD + 8 * g;
+        f4v sf[NS][2], e[4], beta[4], into[4];
+        float vf[4][4];
+        Parts tf[kGdrFrags];
+        const float *from = s0 + (16 * ct + m) * KD + 8 * g;
 #pragma unroll
-        for (int a = 0; a < NS; ++a) {
-          const Parts sp = parts(*reinterpret_cast<const f4v *>(s0 + 32 * a), *reinterpret_cast<const f4v *>(s0 + 32 * a + 4));
+        for (int a = 0; a < NS; ++a)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) x[i] = mul_exact(row16<KD>(base, i, a, atk), sp, x[i]);
-        }
+          for (int k = 0; k < 2; ++k) sf[a][k] = *reinterpret_cast<const f4v *>(from + 32 * a + 4 * k);
         const uint16_t *vp = p.v + b * p.v_batch + t0 * p.v_token + h * VD + 16 * ct + m;
-        f4v beta[4];
+        const u4 *tp = reinterpret_cast<const u4 *>(ws) + lane;
+        const float *ep = p.ws_e + id * 64 * VD + ct * 1024 + lane * 4;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const f4v into = *reinterpret_cast<const f4v *>(gates + 64 + 16 * i + 4 * g);
+          into[i] = *reinterpret_cast<const f4v *>(gates + 64 + 16 * i + 4 * g);
           beta[i] = *reinterpret_cast<const f4v *>(gates + 192 + 16 * i + 4 * g);
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             const int row = 16 * i + 4 * g + r;
-            const float v = ld(vp, (row < len ? row : len - 1) * p.v_token);
-            x[i][r] = beta[i][r] * fmaf(-into[r], x[i][r], v);
+            vf[i][r] = ld(vp, (row < len ? row : len - 1) * p.v_token);
           }
         }
+#pragma unroll
+        for (int f = 0; f < kGdrFrags; ++f)
+          tf[f] = {__builtin_bit_cast(bf8, tp[f * 64]), __builtin_bit_cast(bf8, tp[(kGdrFrags + f) * 64])};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) e[i] = *reinterpret_cast<const f4v *>(ep + i * 256);
+        if (ct == w) arrive();  // keys, queries and dy are in LDS
+        f4v x[4] = {};
+#pragma unroll
+        for (int a = 0; a < NS; ++a) {
+          const Parts sp = parts(sf[a][0], sf[a][1]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x[i] = mul_exact(row16<KD>(base, i, a, atk), sp, x[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) x[i][r] = beta[i][r] * fmaf(-into[i][r], x[i][r], vf[i][r]);
         f4v u[4] = {};
-        const u4 *tf = reinterpret_cast<const u4 *>(ws) + lane;
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           const Parts xp = parts(x[2 * k], x[2 * k + 1]);
 #pragma unroll
-          for (int i = 2 * k; i < 4; ++i) {
-            const Parts ta = {__builtin_bit_cast(bf8, tf[tri(i, k) * 64]), __builtin_bit_cast(bf8, tf[(kGdrFrags + tri(i, k)) * 64])};
-            u[i] = mul_parts(ta, xp, u[i]);
-          }
+          for (int i = 2 * k; i < 4; ++i) u[i] = mul_parts(tf[tri(i, k)], xp, u[i]);
         }
-        const float *ep = p.ws_e + id * 64 * VD + ct * 1024 + lane * 4;
-        f4v e[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          e[i] = *reinterpret_cast<const f4v *>(ep + i * 256);
 #pragma unroll
           for (int r = 0; r < 4; ++r) db[i][r] = fmaf(e[i][r], u[i][r] / beta[i][r], db[i][r]);
           e[i] *= beta[i];
@@ -301,15 +333,17 @@ __global__ void __launch_bounds__(4 * KD) gdr_grad_kernel(const GdrParams p) {
         for (int k = 0; k < 2; ++k) {
           const Parts up = parts(u[2 * k], u[2 * k + 1]), dp = parts(e[2 * k], e[2 * k + 1]);
 #pragma unroll
-          for (int x2 = 0; x2 < 2; ++x2) {
-            const unsigned to = static_cast<unsigned>(slot<64>(16 * ct + m, 2 * (2 * k + x2) + (g >> 1))) * 16 + (g & 1) * 8;
-            *(lds8 *)(U.hi + to) = half_of(up.hi, x2);
-            *(lds8 *)(U.lo + to) = half_of(up.lo, x2);
-            *(lds8 *)(D.hi + to) = half_of(dp.hi, x2);
-            *(lds8 *)(D.lo + to) = half_of(dp.lo, x2);
+          for (int y = 0; y < 2; ++y) {
+            const unsigned to = static_cast<unsigned>(slot<64>(16 * ct + m, 2 * (2 * k + y) + (g >> 1))) * 16 + (g & 1) * 8;
+            *(lds8 *)(U.hi + to) = half_of(up.hi, y);
+            *(lds8 *)(U.lo + to) = half_of(up.lo, y);
+            *(lds8 *)(D.hi + to) = half_of(dp.hi, y);
+            *(lds8 *)(D.lo + to) = half_of(dp.lo, y);
           }
         }
       }
+      if (w >= VD / 16) arrive();
+      fetch_slice(0);
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -317,52 +351,14 @@ __global__ void __launch_bounds__(4 * KD) gdr_grad_kernel(const GdrParams p) {
           const float v = sum16(db[i][r]);
           if (m == 0) red[0][w][16 * i + 4 * g + r] = v;
         }
-      arrive();
-      // Products over the values, a wavefront per 16 key elements.
-      f4v aq[4] = {}, ae[4] = {}, aw[4] = {};
-      float both = 0.0f;
-#pragma unroll
-      for (int s = 0; s < NV; ++s) {
-        const int64_t from = (id * VD + 32 * s + 8 * g) * KD + 16 * w + m;
-        f4v a[2], d[2];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          a[e / 4][e % 4] = p.states[from + e * KD];
-          d[e / 4][e % 4] = p.ws_ds[from + e * KD];
-          both = fmaf(a[e / 4][e % 4], d[e / 4][e % 4], both);
-        }
-        const Parts sp = parts(a[0], a[1]), dp = parts(d[0], d[1]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          aq[i] = mul_exact(row16<VD>(base + kAtD, i, s, atv), sp, aq[i]);
-          ae[i] = mul_parts(tokens16(D, i, s, col), sp, ae[i]);
-          aw[i] = mul_parts(tokens16(U, i, s, col), dp, aw[i]);
-        }
-      }
-      both *= gates[64 + 63];
-      sh4 kc[4], qc[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        kc[i] = rows4<KD>(base, i, w, lane);
-        qc[i] = rows4<KD>(base + kAtQ, i, w, lane);
-        const f4v qs = *reinterpret_cast<const f4v *>(gates + 16 * i + 4 * g);
-        const f4v into = *reinterpret_cast<const f4v *>(gates + 64 + 16 * i + 4 * g);
-        const f4v out = *reinterpret_cast<const f4v *>(gates + 128 + 16 * i + 4 * g);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          aq[i][r] *= qs[r];
-          ae[i][r] *= -into[r];
-          aw[i][r] *= out[r];
-          both = fmaf(up(kc[i][r]), aw[i][r], both);  // <S_C, dS> with what the chunk adds to S_C
-        }
-      }
+      meet();
       // P = scale (dY U^T) M and H = -(D U^T) M within the chunk, and their transposes, as fragments.
-      u4 frag[2][2][4];  // [P or H of this wavefront][as it is or transposed][parts of 2 steps]
+      u4 frag[8 / NW][2][4];  // [P or H of this wavefront][as it is or transposed][parts of 2 steps]
       auto products = [&](auto wave, auto kind, u4 (&f)[2][4]) {
         constexpr int W = wave;
         constexpr bool HH = kind;
         f4v lower[W + 1] = {}, upper[4 - W] = {};
-#pragma unroll
+#pragma unroll 1
         for (int s = 0; s < NV; ++s) {
           const Parts uw = tokens16(U, W, s, col);
           const Parts dw = HH ? tokens16(D, W, s, col) : Parts{row16<VD>(base + kAtD, W, s, atv), bf8{}};
@@ -390,12 +386,12 @@ __global__ void __launch_bounds__(4 * KD) gdr_grad_kernel(const GdrParams p) {
             const double st = sums[other];
             if (j <= W) {  // i = own, j = other
               const bool in = HH ? other < own : other <= own && own < len;
-              const float f = in ? (HH ? -1.0f : p.scale) * __builtin_amdgcn_exp2f(static_cast<float>(so - st)) : 0.0f;
+              const float f = (HH ? -1.0f : p.scale) * __builtin_amdgcn_exp2f(static_cast<float>(so - st));
               lower[j <= W ? j : 0][r] = in ? lower[j <= W ? j : 0][r] * f : 0.0f;
             }
             if (j >= W) {
               const bool in = HH ? own < other : own <= other && other < len;
-              const float f = in ? (HH ? -1.0f : p.scale) * __builtin_amdgcn_exp2f(static_cast<float>(st - so)) : 0.0f;
+              const float f = (HH ? -1.0f : p.scale) * __builtin_amdgcn_exp2f(static_cast<float>(st - so));
               upper[j >= W ? j - W : 0][r] = in ? upper[j >= W ? j - W : 0][r] * f : 0.0f;
             }
           }
@@ -414,7 +410,48 @@ __global__ void __launch_bounds__(4 * KD) gdr_grad_kernel(const GdrParams p) {
           }
         }
       };
-      // Fragments of kind k in LDS: as they are at 2 k, transposed at 2 k + 1.
+      if constexpr (NW == 8) {
+        if (w < 4) by_wave(w, [&](auto wave) { products(wave, std::false_type{}, frag[0]); });
+        else by_wave(w - 4, [&](auto wave) { products(wave, std::true_type{}, frag[0]); });
+      } else {
+        by_wave(w, [&](auto wave) {
+          products(wave, std::false_type{}, frag[0]);
+          products(wave, std::true_type{}, frag[NW == 8 ? 0 : 1]);
+        });
+      }
+      // Products over the values, 32 at a time, a wavefront per 16 key elements.
+      f4v aq[4] = {}, ae[4] = {}, aw[4] = {};
+      float both = 0.0f;
+      const unsigned slice = base + kAtS;
+#pragma unroll 1
+      for (int s = 0; s < NV; ++s) {
+        typedef __attribute__((address_space(3))) u2 lds8;
+        const Parts sp = parts(sv[0], sv[1]), dp = parts(dv[0], dv[1]);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int id4 = k * NT + tid, r = id4 / (KD / 4), e4 = id4 % (KD / 4);
+          const unsigned to = slice + static_cast<unsigned>(slot<KD>(r, e4 >> 1)) * 16 + (e4 & 1) * 8;
+          *(lds8 *)(to) = half_of(sp.hi, k);
+          *(lds8 *)(to + kSlice) = half_of(sp.lo, k);
+          *(lds8 *)(to + 2 * kSlice) = half_of(dp.hi, k);
+          *(lds8 *)(to + 3 * kSlice) = half_of(dp.lo, k);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) both = fmaf(sv[k][e], dv[k][e], both);
+        }
+        if (s + 1 < NV) fetch_slice(s + 1);
+        meet();
+        Parts so, dso;
+        so = {values16<KD>(slice + col_s), values16<KD>(slice + kSlice + col_s)};
+        dso = {values16<KD>(slice + 2 * kSlice + col_s), values16<KD>(slice + 3 * kSlice + col_s)};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          aq[i] = mul_exact(row16<VD>(base + kAtD, i, s, atv), so, aq[i]);
+          ae[i] = mul_parts(tokens16(D, i, s, col), so, ae[i]);
+          aw[i] = mul_parts(tokens16(U, i, s, col), dso, aw[i]);
+        }
+        meet();
+      }
+      // Fragments of kind k take the place of U and D: as they are at 2 k, transposed at 2 k + 1.
       auto keep = [&](int W, int kind, const u4 (&f)[2][4]) {
         u4 *to = lds + (kAtU + kind * 2 * kGdrTriBytes) / 16 + lane;
 #pragma unroll
@@ -430,20 +467,29 @@ __global__ void __launch_bounds__(4 * KD) gdr_grad_kernel(const GdrParams p) {
         }
       };
       if constexpr (NW == 8) {
-        if (w < 4) by_wave(w, [&](auto wave) { products(wave, std::false_type{}, frag[0]); });
-        else by_wave(w - 4, [&](auto wave) { products(wave, std::true_type{}, frag[0]); });
-        arrive();
         keep(w & 3, w >> 2, frag[0]);
       } else {
-        by_wave(w, [&](auto wave) {
-          products(wave, std::false_type{}, frag[0]);
-          products(wave, std::true_type{}, frag[1]);
-        });
-        arrive();
         keep(w, 0, frag[0]);
-        keep(w, 1, frag[1]);
+        keep(w, 1, frag[NW == 8 ? 0 : 1]);
       }
-      arrive();
+      both *= gates[64 + 63];
+      sh4 kc[4], qc[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        kc[i] = rows4<KD>(base, i, w, lane);
+        qc[i] = rows4<KD>(base + kAtQ, i, w, lane);
+        const f4v qs = *reinterpret_cast<const f4v *>(gates + 16 * i + 4 * g);
+        const f4v into = *reinterpret_cast<const f4v *>(gates + 64 + 16 * i + 4 * g);
+        const f4v out = *reinterpret_cast<const f4v *>(gates + 128 + 16 * i + 4 * g);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          aq[i][r] *= qs[r];
+          ae[i][r] *= -into[r];
+          aw[i][r] *= out[r];
+          both = fmaf(up(kc[i][r]), aw[i][r], both);  // <S_C, dS> with what the chunk adds to S_C
+        }
+      }
+      meet();
       const unsigned fp = base + kAtU, fh = fp + 2 * kGdrTriBytes;
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
@@ -477,7 +523,7 @@ __global__ void __launch_bounds__(4 * KD) gdr_grad_kernel(const GdrParams p) {
       both += __shfl_xor(both, 16);
       both += __shfl_xor(both, 32);
       if (lane == 0) whole[w] = both;
-      arrive();
+      meet();
       if (w == 0 && lane < rows) {
         float dg = 0.0f, dbeta = 0.0f, total = 0.0f;
 #pragma unroll
@@ -502,12 +548,16 @@ __global__ void __launch_bounds__(4 * KD) gdr_grad_kernel(const GdrParams p) {
       }
     }
   } else {
-    for (int64_t i = tid; i < rows * share; i += NT) {
+    for (int64_t i = threadIdx.x; i < rows * share; i += NT) {
       const int64_t to = (b * p.seqlen + t0 + i / share) * p.nheads + hk * share + i % share;
       store_gate(p.dg, to, 0.0f, G{});
       store_gate(p.dbeta, to, 0.0f, G{});
     }
   }
+  const int m = threadIdx.x & 15, g = threadIdx.x >> 4 & 3;
+  uint16_t *dqp = p.dq + ((b * p.seqlen + t0) * p.nqk + hk) * KD + 16 * w + m;
+  uint16_t *dkp = p.dk + ((b * p.seqlen + t0) * p.nqk + hk) * KD + 16 * w + m;
+  const int64_t row_step = p.nqk * KD;
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
