@@ -8,174 +8,193 @@ namespace {
 // From chunk to chunk, the last one first: dS, and E = T^T dU, dv = beta E
 // ---------------------------------------------------------------------------
 
-template <int KD, int CT, int NW>
-__global__ void __launch_bounds__(64 * NW) gdr_bwd_kernel(const GdrParams p) {
-  constexpr int NT = 64 * NW, NC = 16 * CT * NW, NS = KD / 32, NB = KD / 16;
+// As in the forward two wavefronts carry dS, 16 columns each, and two others
+// make what does not depend on it, A^T dY and Q^T (scale e^G dY), copy the next
+// chunk, and store E and dv.
+template <int KD>
+__global__ void __launch_bounds__(256) gdr_bwd_kernel(const GdrParams p) {
+  constexpr int NT = 64 * kPairs, NC = 16 * kPairs, NS = KD / 32, NB = KD / 16;
   constexpr unsigned kRows = 64 * KD * 2, kValues = 64 * NC * 2, kTri = 2 * kGdrTriBytes, kOps = kTri + kGdrGateBytes;
   constexpr unsigned kAtQ = kRows, kAtD = 2 * kRows, kAtW = kAtD + kValues, kBuffer = kAtW + kOps;
-  __shared__ __align__(16) u4 lds[2 * kBuffer / 16];
+  constexpr unsigned kFour = 4 * 1024, kState = NB * 1024;  // float32 D results of the tokens, and of the state
+  __shared__ __align__(16) u4 lds[(2 * kBuffer + kPairs * (kFour + kState)) / 16];
   const int tid = threadIdx.x, lane = tid & 63, m = lane & 15, g = lane >> 4;
-  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const unsigned vtiles = static_cast<unsigned>(p.vdim) / NC;
-  const int64_t vt = blockIdx.x % vtiles, bh = blockIdx.x / vtiles, b = bh / p.nheads, h = bh % p.nheads;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), w = wave % kPairs;
+  const HeadTile which = head_tile(blockIdx.x, static_cast<unsigned>(p.batch * p.nheads), static_cast<unsigned>(p.vdim) / NC);
+  const int64_t vt = which.tile, bh = which.head, b = bh / p.nheads, h = bh % p.nheads;
   const int len = gdr_length(p.lengths, b, p.seqlen), n = (len + 63) / 64;
+  const int col0 = static_cast<int>(vt) * NC + 16 * w;
+  const unsigned base = lds_at(lds), four = base + 2 * kBuffer + w * kFour + lane * 16;
+  const unsigned grown = base + 2 * kBuffer + kPairs * kFour + w * kState + lane * 16;
+  const Lanes16 at = lanes16_of<KD>(lane);
+  typedef __attribute__((address_space(3))) f4v lds_f4v;
+
+  if (wave < kPairs) {
+    f4v s[NB];  // dS, laid out as the state
+    const int64_t state = (bh * p.vdim + col0 + m) * KD + 8 * g;
+#pragma unroll
+    for (int j = 0; j < NB; ++j)
+      s[j] = p.dh_last != nullptr ? *reinterpret_cast<const f4v *>(p.dh_last + state + 32 * (j / 2) + 4 * (j % 2)) : f4v{};
+    for (int c = n - 1; c >= 0; --c) {
+      float *to = p.ws_ds + ((bh * p.chunks + c) * p.vdim + col0 + m) * KD + 8 * g;
+#pragma unroll
+      for (int j = 0; j < NB; ++j) *reinterpret_cast<f4v *>(to + 32 * (j / 2) + 4 * (j % 2)) = s[j];
+      Parts sp[NS];
+#pragma unroll
+      for (int a = 0; a < NS; ++a) sp[a] = parts(s[2 * a], s[2 * a + 1]);
+      meet();
+      const unsigned tile = base + (c & 1) * kBuffer, at_t = tile + kAtW, gates = at_t + kTri + 16 * g;
+      bf8 ka[NS][4], kt[2][NB];
+      Parts tf[kGdrFrags];
+      f4v out[4], fac[4];
+#pragma unroll
+      for (int a = 0; a < NS; ++a)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) ka[a][i] = row16<KD>(tile, i, a, at);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        out[i] = lds_f4(gates + 512 + 64 * i);
+        fac[i] = lds_f4(gates + 256 + 64 * i) * -lds_f4(gates + 768 + 64 * i);
+      }
+#pragma unroll
+      for (int f = 0; f < kGdrFrags; ++f) tf[f] = {frag16(at_t, f, lane), frag16(at_t, kGdrFrags + f, lane)};
+      const float whole = lds_f4(at_t + kTri + 256 + 240)[3];
+      __builtin_amdgcn_sched_barrier(0);
+      // K dS, and dU = e^(GC - G) of that + A^T dY
+      f4v x[4] = {};
+#pragma unroll
+      for (int a = 0; a < NS; ++a)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = mul_exact(ka[a][i], sp[a], x[i]);
+      meet();
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] = x[i] * out[i] + *(const lds_f4v *)(four + i * 1024);
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int j = 0; j < NB; ++j) kt[k][j] = col16<KD>(tile, j, k, at);
+      // E = T^T dU
+      f4v e[4] = {};
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const Parts xp = parts(x[2 * k], x[2 * k + 1]);
+#pragma unroll
+        for (int j = 0; j <= 2 * k + 1; ++j) e[j] = mul_parts(tf[tri_t(j, k)], xp, e[j]);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) *(lds_f4v *)(four + i * 1024) = e[i];
+      const Parts ep[2] = {parts(e[0] * fac[0], e[1] * fac[1]), parts(e[2] * fac[2], e[3] * fac[3])};
+      meet();
+      // dS = e^GC dS + sum over tokens of q (scale e^G dy) - k (e^G beta E)
+#pragma unroll
+      for (int j = 0; j < NB; ++j) s[j] = s[j] * whole + *(const lds_f4v *)(grown + j * 1024);
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int j = 0; j < NB; ++j) s[j] = mul_exact(kt[k][j], ep[k], s[j]);
+    }
+    if (p.dh0 != nullptr) {
+#pragma unroll
+      for (int j = 0; j < NB; ++j) *reinterpret_cast<f4v *>(p.dh0 + state + 32 * (j / 2) + 4 * (j % 2)) = s[j];
+    }
+    return;
+  }
+
+  const int id = tid - NT;
   const int64_t hk = h / (p.nheads / p.nqk), yt = p.nheads * p.vdim;
-  const int col = static_cast<int>(vt) * NC + 16 * CT * w + m;
   const uint16_t *kp = p.k + b * p.k_batch + hk * KD, *qp = p.q + b * p.q_batch + hk * KD;
   const uint16_t *dp = p.dy + (b * p.seqlen * p.nheads + h) * p.vdim + vt * NC;
   const char *ws = p.ws + bh * p.chunks * static_cast<int64_t>(kGdrBwdChunkBytes) + kGdrTriBytes;  // T^T, A^T, gates
-  const unsigned base = lds_at(lds);
-  const Lanes16 at = lanes16_of<KD>(lane);
-
-  auto fetch = [&](int c) {
+  uint16_t *vp = p.dv + (b * p.seqlen * p.nheads + h) * p.vdim + col0;
+  TileCopy<KD, NT> k_copy, q_copy;
+  TileCopy<NC, NT> d_copy;
+  k_copy.init(p.k_token, id);
+  q_copy.init(p.q_token, id);
+  d_copy.init(yt, id);
+  RowStore v_store;
+  v_store.init(yt, lane);
+  auto fetch_rows = [&](int c) {
     u4 *to = lds + (c & 1) * (kBuffer / 16);
-    load_tile<KD, NT>(to, kp, p.k_token, 64 * c, len - 1, tid);
-    load_tile<KD, NT>(to + kAtQ / 16, qp, p.q_token, 64 * c, len - 1, tid);
-    const uint16_t *d0 = dp + 64 * c * yt;
-    const unsigned dl = __builtin_amdgcn_readfirstlane(base + (c & 1) * kBuffer + kAtD + (tid & ~63) * 16);
     const int last = len - 1 - 64 * c;
-#pragma unroll
-    for (int k = 0; k < 64 * NC / 8 / NT; ++k) {
-      const int id = k * NT + tid, r = id / (NC / 8), e = vslot<NC>(r, id % (NC / 8)) - r * (NC / 8);
-      copy16(dl + k * NT * 16, d0, static_cast<unsigned>(r < last ? r : last) * static_cast<unsigned>(yt) * 2 + e * 16);
-    }
-    const char *wc = ws + c * static_cast<int64_t>(kGdrBwdChunkBytes);
-    for (int k = w; k < static_cast<int>(kOps / 1024); k += NW)
-      copy16(__builtin_amdgcn_readfirstlane(base + (c & 1) * kBuffer + kAtW + k * 1024), wc, k * 1024 + lane * 16);
+    k_copy.start(to, kp + 64 * c * p.k_token, last, id);
+    q_copy.start(to + kAtQ / 16, qp + 64 * c * p.q_token, last, id);
+    d_copy.start(to + kAtD / 16, dp + 64 * c * yt, last, id);
   };
-
-  if (n > 0) fetch(n - 1);
-  f4v s[CT][NB];  // dS, laid out as the state
-  const int64_t state = (bh * p.vdim + col) * KD + 8 * g;
-#pragma unroll
-  for (int t = 0; t < CT; ++t)
-#pragma unroll
-    for (int j = 0; j < NB; ++j)
-      s[t][j] = p.dh_last != nullptr
-                    ? *reinterpret_cast<const f4v *>(p.dh_last + state + t * 16 * KD + 32 * (j / 2) + 4 * (j % 2))
-                    : f4v{};
-  uint16_t *vp = p.dv + (b * p.seqlen * p.nheads + h) * p.vdim + col;
-
-  for (int c = n - 1; c >= 0; --c) {
-    float *to = p.ws_ds + ((bh * p.chunks + c) * p.vdim + col) * KD + 8 * g;
-#pragma unroll
-    for (int t = 0; t < CT; ++t)
-#pragma unroll
-      for (int j = 0; j < NB; ++j) *reinterpret_cast<f4v *>(to + t * 16 * KD + 32 * (j / 2) + 4 * (j % 2)) = s[t][j];
-    arrive();
-    if (c > 0) fetch(c - 1);
-    const unsigned tile = base + (c & 1) * kBuffer, gates = tile + kAtW + kTri + 16 * g;
-    // K dS
-    f4v x[CT][4] = {};
-#pragma unroll
-    for (int a = 0; a < NS; ++a) {
-      Parts sp[CT];
-#pragma unroll
-      for (int t = 0; t < CT; ++t) sp[t] = parts(s[t][2 * a], s[t][2 * a + 1]);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const bf8 ka = row16<KD>(tile, i, a, at);
-#pragma unroll
-        for (int t = 0; t < CT; ++t) x[t][i] = mul_exact(ka, sp[t], x[t][i]);
-      }
-    }
-    // dU = e^(GC - G) K dS + A^T dY
-    sh4 dy[CT][4];
+  auto fetch_ws = [&](int c) {
+    copy_share<kOps / 1024, kPairs>(base + (c & 1) * kBuffer + kAtW, ws + c * static_cast<int64_t>(kGdrBwdChunkBytes), w, lane * 16);
+  };
+  f4v e[4];
+  auto store = [&](int c) {
+    float *to = p.ws_e + (bh * p.chunks + c) * 64 * p.vdim + (vt * kPairs + w) * 1024 + lane * 4;
+    const unsigned beta = base + (c & 1) * kBuffer + kAtW + kTri + 768 + 16 * g;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const f4v out = lds_f4(gates + 512 + 64 * i);
-#pragma unroll
-      for (int t = 0; t < CT; ++t) {
-        x[t][i] *= out;
-        dy[t][i] = rows4<NC>(tile + kAtD, i, CT * w + t, lane);
-      }
+      *reinterpret_cast<f4v *>(to + i * 256) = e[i];
+      e[i] *= lds_f4(beta + 64 * i);
     }
-    const unsigned at_t = tile + kAtW, at_a = at_t + kGdrTriBytes;
+    if (64 * c + 64 > len) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (64 * c + 16 * i + 4 * g + r >= len) e[i][r] = 0.0f;
+    }
+    const int64_t rest = p.seqlen - 64 * static_cast<int64_t>(c);
+    v_store.put(vp + 64 * c * yt, rest < 64 ? static_cast<int>(rest) : 64, e);
+  };
+  if (n > 0) {
+    fetch_rows(n - 1);
+    fetch_ws(n - 1);
+  }
+  for (int c = n - 1; c >= 0; --c) {
+    arrive();
+    const unsigned tile = base + (c & 1) * kBuffer, at_a = tile + kAtW + kGdrTriBytes, gates = at_a + kGdrTriBytes + 16 * g;
+    Parts af[kGdrFrags];
+    sh4 dy[4];
+    bf8 qt[2][NB];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) dy[i] = rows4<NC>(tile + kAtD, i, w, lane);
+#pragma unroll
+    for (int f = 0; f < kGdrFrags; ++f) af[f] = {frag16(at_a, f, lane), frag16(at_a, kGdrFrags + f, lane)};
 #pragma unroll
     for (int k = 0; k < 2; ++k)
 #pragma unroll
-      for (int j = 0; j <= 2 * k + 1; ++j) {
-        const Parts aa = {frag16(at_a, tri_t(j, k), lane), frag16(at_a, kGdrFrags + tri_t(j, k), lane)};
-#pragma unroll
-        for (int t = 0; t < CT; ++t) {
-          const bf8 d = __builtin_bit_cast(bf8, __builtin_shufflevector(dy[t][2 * k], dy[t][2 * k + 1], 0, 1, 2, 3, 4, 5, 6, 7));
-          x[t][j] = mfma16(aa.hi, d, mfma16(aa.lo, d, x[t][j]));
-        }
-      }
-    // E = T^T dU
-    f4v e[CT][4] = {};
+      for (int j = 0; j < NB; ++j) qt[k][j] = col16<KD>(tile + kAtQ, j, k, at);
+    __builtin_amdgcn_sched_barrier(0);
+    f4v x[4] = {};
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      Parts xp[CT];
+      const bf8 d = __builtin_bit_cast(bf8, __builtin_shufflevector(dy[2 * k], dy[2 * k + 1], 0, 1, 2, 3, 4, 5, 6, 7));
 #pragma unroll
-      for (int t = 0; t < CT; ++t) xp[t] = parts(x[t][2 * k], x[t][2 * k + 1]);
-#pragma unroll
-      for (int j = 0; j <= 2 * k + 1; ++j) {
-        const Parts ta = {frag16(at_t, tri_t(j, k), lane), frag16(at_t, kGdrFrags + tri_t(j, k), lane)};
-#pragma unroll
-        for (int t = 0; t < CT; ++t) e[t][j] = mul_parts(ta, xp[t], e[t][j]);
-      }
+      for (int j = 0; j <= 2 * k + 1; ++j) x[j] = mfma16(af[tri_t(j, k)].hi, d, mfma16(af[tri_t(j, k)].lo, d, x[j]));
     }
-    // dS = e^GC dS + sum over tokens of q (scale e^G dy) - k (e^G beta E)
-    const float whole = lds_f4(tile + kAtW + kTri + 256 + 240)[3];
 #pragma unroll
-    for (int t = 0; t < CT; ++t)
-#pragma unroll
-      for (int j = 0; j < NB; ++j) s[t][j] *= whole;
-    float *eo = p.ws_e + (bh * p.chunks + c) * 64 * p.vdim + (vt * (NC / 16) + CT * w) * 1024 + lane * 4;
-#pragma unroll
-    for (int t = 0; t < CT; ++t)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) *reinterpret_cast<f4v *>(eo + t * 1024 + i * 256) = e[t][i];
+    for (int i = 0; i < 4; ++i) *(lds_f4v *)(four + i * 1024) = x[i];
+    meet();
+    if (c > 0) fetch_rows(c - 1);
+    f4v z[NB] = {};
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      Parts ep[CT], yp[CT];
-      f4v beta[2], into[2], qs[2];
+      f4v y[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        qs[i] = lds_f4(gates + 64 * (2 * k + i));
-        into[i] = lds_f4(gates + 256 + 64 * (2 * k + i));
-        beta[i] = lds_f4(gates + 768 + 64 * (2 * k + i));
+        const f4v qs = lds_f4(gates + 64 * (2 * k + i));
+#pragma unroll
+        for (int r = 0; r < 4; ++r) y[i][r] = up(dy[2 * k + i][r]) * qs[r];
       }
+      const Parts yp = parts(y[0], y[1]);
 #pragma unroll
-      for (int t = 0; t < CT; ++t) {
-        f4v y[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          e[t][2 * k + i] *= beta[i];
-#pragma unroll
-          for (int r = 0; r < 4; ++r) y[i][r] = up(dy[t][2 * k + i][r]) * qs[i][r];
-        }
-        ep[t] = parts(e[t][2 * k] * -into[0], e[t][2 * k + 1] * -into[1]);
-        yp[t] = parts(y[0], y[1]);
-      }
-#pragma unroll
-      for (int j = 0; j < NB; ++j) {
-        const bf8 kt = col16<KD>(tile, j, k, at), qt = col16<KD>(tile + kAtQ, j, k, at);
-#pragma unroll
-        for (int t = 0; t < CT; ++t) s[t][j] = mul_exact(qt, yp[t], mul_exact(kt, ep[t], s[t][j]));
-      }
+      for (int j = 0; j < NB; ++j) z[j] = mul_exact(qt[k][j], yp, z[j]);
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int j = 0; j < NB; ++j) *(lds_f4v *)(grown + j * 1024) = z[j];
+    meet();
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int64_t row = 64 * static_cast<int64_t>(c) + 16 * i + 4 * g + r;
-        if (row < p.seqlen)
-#pragma unroll
-          for (int t = 0; t < CT; ++t) st(vp, row * yt + 16 * t, row < len ? e[t][i][r] : 0.0f);
-      }
+    for (int i = 0; i < 4; ++i) e[i] = *(const lds_f4v *)(four + i * 1024);
+    if (c > 0) fetch_ws(c - 1);
+    store(c);
   }
-  for (int64_t row = 64 * static_cast<int64_t>(n) + g; row < p.seqlen; row += 4)
-#pragma unroll
-    for (int t = 0; t < CT; ++t) st(vp, row * yt + 16 * t, 0.0f);
-  if (p.dh0 != nullptr) {
-#pragma unroll
-    for (int t = 0; t < CT; ++t)
-#pragma unroll
-      for (int j = 0; j < NB; ++j)
-        *reinterpret_cast<f4v *>(p.dh0 + state + t * 16 * KD + 32 * (j / 2) + 4 * (j % 2)) = s[t][j];
-  }
+  for (int64_t row = 64 * static_cast<int64_t>(n) + g; row < p.seqlen; row += 4) st(vp, row * yt + m, 0.0f);
 }
 
 // ---------------------------------------------------------------------------
@@ -578,7 +597,7 @@ void grad(const GdrParams &p, hipStream_t s) {
 template <int KD>
 hipError_t bwd(const GdrParams &p, hipStream_t s) {
   const int64_t heads = p.batch * p.nheads;
-  hipLaunchKernelGGL((gdr_bwd_kernel<KD, 1, 4>), dim3(static_cast<uint32_t>(heads * (p.vdim / 64))), dim3(256), 0, s, p);
+  hipLaunchKernelGGL((gdr_bwd_kernel<KD>), dim3(static_cast<uint32_t>(heads * (p.vdim / 32))), dim3(256), 0, s, p);
   if (p.chunks > 0) {
     if (p.vdim == 64) p.gates_bf16 ? grad<KD, 64, uint16_t>(p, s) : grad<KD, 64, float>(p, s);
     else p.gates_bf16 ? grad<KD, 128, uint16_t>(p, s) : grad<KD, 128, float>(p, s);

@@ -186,8 +186,6 @@ __global__ void __launch_bounds__(256) gdr_chunk_kernel(const GdrParams p) {
 // carry that, 16 columns each, and two others make y from the operands that
 // those leave in LDS, and copy the next chunk there: each of the four has a
 // SIMD to itself.
-constexpr int kPairs = 2;
-
 template <int KD>
 __global__ void __launch_bounds__(256) gdr_fwd_kernel(const GdrParams p) {
   constexpr int NT = 64 * kPairs, NC = 16 * kPairs, NS = KD / 32, NB = KD / 16;
@@ -197,8 +195,8 @@ __global__ void __launch_bounds__(256) gdr_fwd_kernel(const GdrParams p) {
   __shared__ __align__(16) u4 lds[(2 * kBuffer + kPairs * (kState + kUpdate)) / 16];
   const int tid = threadIdx.x, lane = tid & 63, m = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), w = wave % kPairs;
-  const unsigned vtiles = static_cast<unsigned>(p.vdim) / NC;
-  const int64_t vt = blockIdx.x % vtiles, bh = blockIdx.x / vtiles, b = bh / p.nheads, h = bh % p.nheads;
+  const HeadTile which = head_tile(blockIdx.x, static_cast<unsigned>(p.batch * p.nheads), static_cast<unsigned>(p.vdim) / NC);
+  const int64_t vt = which.tile, bh = which.head, b = bh / p.nheads, h = bh % p.nheads;
   const int len = gdr_length(p.lengths, b, p.seqlen), n = (len + 63) / 64;
   const int col0 = static_cast<int>(vt) * NC + 16 * w;
   const unsigned base = lds_at(lds), parts_s = base + 2 * kBuffer + w * kState + lane * 16;

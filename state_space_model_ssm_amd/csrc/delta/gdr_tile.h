@@ -100,6 +100,8 @@ __device__ __forceinline__ f4v lds_f4(unsigned at) {
   return *(lds16 *)(at);
 }
 
+constexpr int kPairs = 2;  // wavefronts that carry the state, and as many beside them
+
 // Fragment of a lower triangle: row block i (of 16), columns 32 s .., and of
 // its transpose: row block j, columns 32 s .. (32 s + 31 >= 16 j).
 __host__ __device__ constexpr int tri(int i, int s) { return i < 2 ? i : 2 * (i - 1) + s; }
@@ -272,6 +274,22 @@ __device__ __forceinline__ float up(short v) {
 
 template <typename G>
 __device__ __forceinline__ float gate(const void *p, int64_t i) { return ld(static_cast<const G *>(p), i); }
+
+// A workgroup's head and column tile: the tiles of a head, which read the same
+// keys and operands, 8 workgroups apart, so that they share an XCD's L2.
+struct HeadTile {
+  int64_t head;
+  unsigned tile;
+};
+__device__ __forceinline__ HeadTile head_tile(unsigned id, unsigned heads, unsigned tiles) {
+  const unsigned even = heads / 8 * 8;
+  if (id < even * tiles) {
+    const unsigned r = id % (8 * tiles);
+    return {id / (8 * tiles) * 8 + r % 8, r / 8};
+  }
+  const unsigned r = id - even * tiles;
+  return {even + r / tiles, r % tiles};
+}
 
 __device__ __forceinline__ int gdr_length(const int32_t *lengths, int64_t b, int64_t seqlen) {
   if (lengths == nullptr) return static_cast<int>(seqlen);
