@@ -55,7 +55,7 @@ SSM_API const char *ssm_delta_last_error(void);
  * token strides must be multiples of 8, token strides at most 2^24, and q, k,
  * v, y, dy, dq, dk, dv and the states 16-byte aligned; all but q, k and v are
  * dense.  scale multiplies y.  seqlen <= 2^30 and
- * batch * nheads * ceil(seqlen / 64) < 2^24.
+ * batch * nheads * max(4, ceil(seqlen / 64)) < 2^24.
  */
 typedef struct {
   int64_t batch, seqlen, nqk, nheads, kdim, vdim;

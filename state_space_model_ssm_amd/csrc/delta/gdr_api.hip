@@ -25,9 +25,9 @@ int check_gdr(const ssm_gdr_dims_t *d, bool step) {
   if (!isfinite(d->scale)) return fail(SSM_ERR_SHAPE, "scale must be finite");
   if (d->seqlen > (int64_t{1} << 30)) return fail(SSM_ERR_UNSUPPORTED, "seqlen must be at most 2^30");
   const int64_t chunks = ceil_div(d->seqlen, SSM_GDR_STATE_STEP), heads = mul(d->batch, d->nheads);
-  const int64_t all = mul(heads, chunks > 2 ? chunks : 2);
+  const int64_t all = mul(heads, chunks > 4 ? chunks : 4);  // a workgroup per chunk, and per 32 values
   if (heads < 0 || all < 0 || all > kMaxGroups)
-    return fail(SSM_ERR_UNSUPPORTED, "batch * nheads * ceil(seqlen / 64) must be below 2^24");
+    return fail(SSM_ERR_UNSUPPORTED, "batch * nheads * max(4, ceil(seqlen / 64)) must be below 2^24");
   const int64_t strides[] = {d->q_batch, d->q_token, d->k_batch, d->k_token, d->v_batch, d->v_token};
   for (const int64_t s : strides)
     if (s < 0 || s % 8 != 0 || s > (int64_t{1} << 40))
@@ -66,6 +66,7 @@ GdrParams params(const ssm_gdr_dims_t &d) {
   p.kdim = static_cast<int32_t>(d.kdim);
   p.vdim = static_cast<int32_t>(d.vdim);
   p.gates_bf16 = d.gate_dtype == SSM_BF16;
+  p.seg = gdr_segments(d.batch * d.nheads, d.vdim, p.chunks);
   return p;
 }
 
@@ -79,7 +80,8 @@ int ssm_gdr_workspace_size(const ssm_gdr_dims_t *dims, size_t *bytes) {
   if (!bytes) return fail(SSM_ERR_NULL, "bytes is NULL");
   const int rc = check_gdr(dims, false);
   if (rc != SSM_OK) return rc;
-  *bytes = gdr_workspace(params(*dims));
+  const GdrSizes n = gdr_sizes(params(*dims));
+  *bytes = n.chunks + n.state + n.carry;
   return ok();
 }
 
@@ -105,7 +107,8 @@ int ssm_gdr_fwd(const void *q, const void *k, const void *v, const void *g, cons
                       {"states", states, state * p.chunks, 16, false}};
   const void *const same[3][2] = {{nullptr, nullptr}, {h0, nullptr}, {nullptr, nullptr}};
   rc = check_args(ins, outs, same);
-  if (rc == SSM_OK) rc = check_workspace(ins, gdr_workspace(p));
+  const GdrSizes n = gdr_sizes(p);
+  if (rc == SSM_OK) rc = check_workspace(ins, n.chunks + n.state + n.carry);
   if (rc != SSM_OK) return rc;
   if (d.batch == 0 || (d.seqlen == 0 && h_last == nullptr)) return ok();
   p.q = static_cast<const uint16_t *>(q);
@@ -118,6 +121,8 @@ int ssm_gdr_fwd(const void *q, const void *k, const void *v, const void *g, cons
   p.y = static_cast<uint16_t *>(y);
   p.h_last = h_last;
   p.states = states;
+  p.ws_state = reinterpret_cast<float *>(p.ws + n.chunks);
+  p.ws_carry = reinterpret_cast<uint16_t *>(p.ws + n.chunks + n.state);
   return launched(launch_gdr_fwd(p, static_cast<hipStream_t>(stream)), "gdr_fwd");
 }
 

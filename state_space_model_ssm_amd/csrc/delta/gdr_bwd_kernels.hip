@@ -217,16 +217,6 @@ __device__ __forceinline__ Parts tokens16(const Pair &t, int i, int s, unsigned 
   return {tokens16(t.hi, i, s, col), tokens16(t.lo, i, s, col)};
 }
 
-// Operand of a slice of 32 values [value][key element]: lane m stands for the
-// element at `at`, k for values 8g ..
-template <int D>
-__device__ __forceinline__ bf8 values16(unsigned at) {
-  typedef __attribute__((address_space(3))) sh4 lds4;
-  const sh4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)(at));
-  const sh4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)((at ^ 16) + 8 * D));
-  return __builtin_bit_cast(bf8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
-}
-
 // Operand of the elements 16 ct + m of a row-major tile, k its rows 32 s .. in D's order.
 template <int D>
 __device__ __forceinline__ bf8 elems16(unsigned tile, int ct, int s, int lane) {

@@ -19,6 +19,14 @@ constexpr size_t kGdrGateBytes = 2048;
 constexpr size_t kGdrChunkBytes = 2 * kGdrTriBytes + kGdrGateBytes;
 constexpr size_t kGdrBwdChunkBytes = 3 * kGdrTriBytes + kGdrGateBytes;
 
+// Long sequences of few heads are cut into segments of `chunks` chunks, and the
+// state at the start of each is found before y is made: with S_0 = 0 and with
+// S_0 = I a segment gives E and P, and its end is P S_0 + E.
+struct GdrSegments {
+  int64_t count, chunks;
+};
+GdrSegments gdr_segments(int64_t heads, int64_t vdim, int64_t chunks);
+
 struct GdrParams {
   const uint16_t *q, *k, *v;   // bf16
   const void *g, *beta;        // gate dtype
@@ -33,12 +41,19 @@ struct GdrParams {
   void *dg, *dbeta;            // gate dtype
   float *dh0;                  // nullable
   float *ws_ds, *ws_e;         // per (row, value head, chunk): dS behind it, and E = T^T dU in D's order
+  GdrSegments seg;
+  float *ws_state;             // (row, value head, segment): E, and then the state before the segment
+  uint16_t *ws_carry;          // (row, value head, segment, part): P, (kdim in, kdim out)
   int64_t batch, seqlen, nqk, nheads, chunks;
   int64_t q_batch, q_token, k_batch, k_token, v_batch, v_token;
   float scale;
   int32_t kdim, vdim, gates_bf16;
 };
-size_t gdr_workspace(const GdrParams &p);
+// Sizes of the forward's workspace: ws, ws_state and ws_carry in turn.
+struct GdrSizes {
+  size_t chunks, state, carry;
+};
+GdrSizes gdr_sizes(const GdrParams &p);
 // Sizes of the backward's workspace: ws, ws_ds and ws_e in turn.
 struct GdrBwdSizes {
   size_t chunks, ds, e;

@@ -195,9 +195,13 @@ __global__ void __launch_bounds__(256) gdr_fwd_kernel(const GdrParams p) {
   __shared__ __align__(16) u4 lds[(2 * kBuffer + kPairs * (kState + kUpdate)) / 16];
   const int tid = threadIdx.x, lane = tid & 63, m = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), w = wave % kPairs;
-  const HeadTile which = head_tile(blockIdx.x, static_cast<unsigned>(p.batch * p.nheads), static_cast<unsigned>(p.vdim) / NC);
-  const int64_t vt = which.tile, bh = which.head, b = bh / p.nheads, h = bh % p.nheads;
-  const int len = gdr_length(p.lengths, b, p.seqlen), n = (len + 63) / 64;
+  const unsigned vtiles = static_cast<unsigned>(p.vdim) / NC;
+  const HeadTile which = head_tile(blockIdx.x, static_cast<unsigned>(p.batch * p.nheads), vtiles * static_cast<unsigned>(p.seg.count));
+  const int64_t vt = which.tile % vtiles, bh = which.head, b = bh / p.nheads, h = bh % p.nheads;
+  // Chunks first .. n - 1 of the row, of this segment.
+  const int segment = static_cast<int>(which.tile / vtiles), len = gdr_length(p.lengths, b, p.seqlen);
+  const int first = segment * static_cast<int>(p.seg.chunks), all = (len + 63) / 64;
+  const int n = all < first + p.seg.chunks ? all : first + static_cast<int>(p.seg.chunks);
   const int col0 = static_cast<int>(vt) * NC + 16 * w;
   const unsigned base = lds_at(lds), parts_s = base + 2 * kBuffer + w * kState + lane * 16;
   const unsigned parts_u = base + 2 * kBuffer + kPairs * kState + w * kUpdate + lane * 16;
@@ -208,10 +212,14 @@ __global__ void __launch_bounds__(256) gdr_fwd_kernel(const GdrParams p) {
     // The state: column col0 + m, key elements 32 a + 8g + 4x + r.
     f4v s[NB];
     const int64_t state = (bh * p.vdim + col0 + m) * KD + 8 * g;
+    // (Not from h0 where there are segments: the last one's workgroup may write h_last in its place.)
+    const float *from = p.seg.count > 1 ? p.ws_state + ((bh * p.seg.count + segment) * p.vdim + col0 + m) * KD + 8 * g
+                        : p.h0 != nullptr ? p.h0 + state
+                                          : nullptr;
+    const bool begins = from != nullptr && (first < n || segment == 0);
 #pragma unroll
-    for (int j = 0; j < NB; ++j)
-      s[j] = p.h0 != nullptr ? *reinterpret_cast<const f4v *>(p.h0 + state + 32 * (j / 2) + 4 * (j % 2)) : f4v{};
-    for (int c = 0; c < n; ++c) {
+    for (int j = 0; j < NB; ++j) s[j] = begins ? *reinterpret_cast<const f4v *>(from + 32 * (j / 2) + 4 * (j % 2)) : f4v{};
+    for (int c = first; c < n; ++c) {
       Parts sp[NS];
 #pragma unroll
       for (int a = 0; a < NS; ++a) {
@@ -284,7 +292,7 @@ __global__ void __launch_bounds__(256) gdr_fwd_kernel(const GdrParams p) {
         for (int j = 0; j < NB; ++j) s[j] = mul_exact(kt[k][j], up, s[j]);
       }
     }
-    if (p.h_last != nullptr) {
+    if (p.h_last != nullptr && ((n == all && first < n) || (all == 0 && segment == 0))) {
 #pragma unroll
       for (int j = 0; j < NB; ++j) *reinterpret_cast<f4v *>(p.h_last + state + 32 * (j / 2) + 4 * (j % 2)) = s[j];
     }
@@ -314,21 +322,21 @@ __global__ void __launch_bounds__(256) gdr_fwd_kernel(const GdrParams p) {
   auto fetch_ws = [&](int c) {
     copy_share<kGdrChunkBytes / 1024, kPairs>(base + (c & 1) * kBuffer + kAtW, ws + c * static_cast<int64_t>(kGdrChunkBytes), w, lane * 16);
   };
-  if (n > 0) {
-    fetch_rows(0);
-    fetch_ws(0);
+  if (first < n) {
+    fetch_rows(first);
+    fetch_ws(first);
   }
   f4v o[4];
   auto store = [&](int c) {
     const int64_t rest = p.seqlen - 64 * static_cast<int64_t>(c);
     y_store.put(yp + 64 * c * yt, rest < 64 ? static_cast<int>(rest) : 64, o);
   };
-  for (int c = 0; c < n; ++c) {
+  for (int c = first; c < n; ++c) {
     // Stores may be done before or after older copies, so the wait is for both:
     // y of a chunk is stored with the next one, long before that.
     arrive();
     if (c + 1 < n) fetch_rows(c + 1);
-    if (c > 0) store(c - 1);
+    if (c > first) store(c - 1);
     const unsigned tile = base + (c & 1) * kBuffer, tri_a = tile + kAtW + kGdrTriBytes, gates = tri_a + kGdrTriBytes + 16 * g;
     bf8 qa[NS][4];
     Parts sp[NS], af[kGdrFrags];
@@ -370,8 +378,156 @@ __global__ void __launch_bounds__(256) gdr_fwd_kernel(const GdrParams p) {
           if (64 * c + 16 * i + 4 * g + r >= len) o[i][r] = 0.0f;
     }
   }
-  if (n > 0) store(n - 1);
-  for (int64_t row = 64 * static_cast<int64_t>(n) + g; row < p.seqlen; row += 4) st(yp, row * yt + m, 0.0f);
+  if (first < n) store(n - 1);
+  const int64_t last = segment + 1 < p.seg.count ? 64 * (first + p.seg.chunks) : p.seqlen;  // the segment's rows behind the length
+  for (int64_t row = 64 * static_cast<int64_t>(n > first ? n : first) + g; row < last && row < p.seqlen; row += 4) st(yp, row * yt + m, 0.0f);
+}
+
+// E and P of a segment: 64 columns a workgroup, of E (the values' columns, from
+// a state of 0) or P (the columns of the unit matrix, without values).
+template <int KD>
+__global__ void __launch_bounds__(256, 2) gdr_segment_kernel(const GdrParams p) {
+  constexpr int NT = 256, NC = 64, NS = KD / 32, NB = KD / 16;
+  constexpr unsigned kRows = 64 * KD * 2, kAtV = kRows, kAtW = kAtV + 64 * NC * 2, kAtG = kAtW + kGdrTriBytes, kBuffer = kAtG + kGdrGateBytes;
+  __shared__ __align__(16) u4 lds[2 * kBuffer / 16];
+  const int tid = threadIdx.x, lane = tid & 63, m = lane & 15, g = lane >> 4;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const unsigned vtiles = static_cast<unsigned>(p.vdim) / NC, tiles = vtiles + KD / NC;
+  const HeadTile which = head_tile(blockIdx.x, static_cast<unsigned>(p.batch * p.nheads), tiles * static_cast<unsigned>(p.seg.count - 1));
+  const int64_t bh = which.head, b = bh / p.nheads, h = bh % p.nheads, hk = h / (p.nheads / p.nqk);
+  const int segment = static_cast<int>(which.tile / tiles), len = gdr_length(p.lengths, b, p.seqlen);
+  const int first = segment * static_cast<int>(p.seg.chunks), n = first + static_cast<int>(p.seg.chunks);
+  if (64 * static_cast<int64_t>(n) >= len) return;  // the row has no segment behind this one: all its chunks are whole, too
+  const unsigned tile = which.tile % tiles;
+  const bool values = tile < vtiles;
+  const int col = static_cast<int>(values ? tile : tile - vtiles) * NC + 16 * w + m;
+  const uint16_t *kp = p.k + b * p.k_batch + hk * KD, *vp = p.v + b * p.v_batch + h * p.vdim + tile * NC;
+  const char *ws = p.ws + bh * p.chunks * static_cast<int64_t>(kGdrChunkBytes);
+  const unsigned base = lds_at(lds);
+  const Lanes16 at = lanes16_of<KD>(lane);
+  TileCopy<KD, NT> k_copy;
+  TileCopy<NC, NT> v_copy;
+  k_copy.init(p.k_token, tid);
+  v_copy.init(p.v_token, tid);
+  auto fetch = [&](int c) {
+    u4 *to = lds + (c & 1) * (kBuffer / 16);
+    const char *wc = ws + c * static_cast<int64_t>(kGdrChunkBytes);
+    k_copy.start(to, kp + 64 * c * p.k_token, 63, tid);
+    if (values) v_copy.start(to + kAtV / 16, vp + 64 * c * p.v_token, 63, tid);
+    copy_share<kGdrTriBytes / 1024, 4>(base + (c & 1) * kBuffer + kAtW, wc, w, lane * 16);
+    if (w < static_cast<int>(kGdrGateBytes / 1024))
+      copy_kib<1>(__builtin_amdgcn_readfirstlane(base + (c & 1) * kBuffer + kAtG + w * 1024), uniform(wc + 2 * kGdrTriBytes + w * 1024), lane * 16);
+  };
+  fetch(first);
+  f4v s[NB];
+#pragma unroll
+  for (int j = 0; j < NB; ++j)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) s[j][r] = !values && 32 * (j / 2) + 8 * g + 4 * (j % 2) + r == col ? 1.0f : 0.0f;
+  for (int c = first; c < n; ++c) {
+    arrive();
+    if (c + 1 < n) fetch(c + 1);
+    const unsigned buffer = base + (c & 1) * kBuffer, tri_t = buffer + kAtW, gates = buffer + kAtG + 16 * g;
+    f4v x[4] = {};
+#pragma unroll
+    for (int a = 0; a < NS; ++a) {
+      const Parts sp = parts(s[2 * a], s[2 * a + 1]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] = mul_exact(row16<KD>(buffer, i, a, at), sp, x[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const f4v into = lds_f4(gates + 256 + 64 * i), beta = lds_f4(gates + 768 + 64 * i);
+      const sh4 v = rows4<NC>(buffer + kAtV, i, w, lane);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) x[i][r] = beta[r] * fmaf(-into[r], x[i][r], values ? up(v[r]) : 0.0f);
+    }
+    f4v u[4] = {};
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const Parts xp = parts(x[2 * k], x[2 * k + 1]);
+#pragma unroll
+      for (int i = 2 * k; i < 4; ++i)
+        u[i] = mul_parts(Parts{frag16(tri_t, tri(i, k), lane), frag16(tri_t, kGdrFrags + tri(i, k), lane)}, xp, u[i]);
+    }
+    const float whole = lds_f4(buffer + kAtG + 256 + 240)[3];
+#pragma unroll
+    for (int j = 0; j < NB; ++j) s[j] *= whole;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const Parts up = parts(u[2 * k] * lds_f4(gates + 512 + 128 * k), u[2 * k + 1] * lds_f4(gates + 512 + 128 * k + 64));
+#pragma unroll
+      for (int j = 0; j < NB; ++j) s[j] = mul_exact(col16<KD>(buffer, j, k, at), up, s[j]);
+    }
+  }
+  const int64_t seg = bh * p.seg.count + segment;
+  if (values) {
+    float *to = p.ws_state + ((seg + 1) * p.vdim + col) * KD + 8 * g;  // where the join reads it and puts the state itself
+#pragma unroll
+    for (int j = 0; j < NB; ++j) *reinterpret_cast<f4v *>(to + 32 * (j / 2) + 4 * (j % 2)) = s[j];
+  } else {
+    uint16_t *to = p.ws_carry + (seg * 2 * KD + col) * KD + 8 * g;
+#pragma unroll
+    for (int a = 0; a < NS; ++a) {
+      const Parts sp = parts(s[2 * a], s[2 * a + 1]);
+      *reinterpret_cast<bf8 *>(to + 32 * a) = sp.hi;
+      *reinterpret_cast<bf8 *>(to + KD * KD + 32 * a) = sp.lo;
+    }
+  }
+}
+
+// The state before each segment, 64 columns a workgroup.
+template <int KD>
+__global__ void __launch_bounds__(256) gdr_join_kernel(const GdrParams p) {
+  constexpr int NS = KD / 32, NB = KD / 16;
+  constexpr unsigned kPart = KD * KD * 2, kBuffer = 2 * kPart;
+  __shared__ __align__(16) u4 lds[2 * kBuffer / 16];
+  const int tid = threadIdx.x, lane = tid & 63, m = lane & 15, g = lane >> 4;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const unsigned vtiles = static_cast<unsigned>(p.vdim) / 64;
+  const int64_t bh = blockIdx.x / vtiles, b = bh / p.nheads;
+  const int col = static_cast<int>(blockIdx.x % vtiles) * 64 + 16 * w + m, len = gdr_length(p.lengths, b, p.seqlen);
+  const int span = static_cast<int>(p.seg.chunks) * 64, n = (len + span - 1) / span;  // segments of this row
+  f4v s[NB], next[NB];
+  const int64_t state = (bh * p.vdim + col) * KD + 8 * g;
+  float *begin = p.ws_state + (bh * p.seg.count * p.vdim + col) * KD + 8 * g;
+#pragma unroll
+  for (int j = 0; j < NB; ++j) {
+    s[j] = p.h0 != nullptr ? *reinterpret_cast<const f4v *>(p.h0 + state + 32 * (j / 2) + 4 * (j % 2)) : f4v{};
+    *reinterpret_cast<f4v *>(begin + 32 * (j / 2) + 4 * (j % 2)) = s[j];
+  }
+  if (n < 2) return;
+  const unsigned base = lds_at(lds);
+  const unsigned from = static_cast<unsigned>(slot<KD>(8 * g + (m >> 2), m & 3)) * 16;
+  auto fetch = [&](int i) {  // both parts of P, rows of KD elements laid out by slot<KD>()
+    const uint16_t *src = p.ws_carry + (bh * p.seg.count + i) * 2 * KD * KD;
+    load_tile<KD, 256, KD>(lds + (i & 1) * (kBuffer / 16), src, KD, 0, KD - 1, tid);
+    load_tile<KD, 256, KD>(lds + ((i & 1) * kBuffer + kPart) / 16, src + KD * KD, KD, 0, KD - 1, tid);
+  };
+  fetch(0);
+  for (int i = 0; i + 1 < n; ++i) {
+    float *to = p.ws_state + ((bh * p.seg.count + i + 1) * p.vdim + col) * KD + 8 * g;
+#pragma unroll
+    for (int j = 0; j < NB; ++j) next[j] = *reinterpret_cast<const f4v *>(to + 32 * (j / 2) + 4 * (j % 2));
+    arrive();
+    if (i + 2 < n) fetch(i + 1);
+    const unsigned tile = base + (i & 1) * kBuffer + from;
+#pragma unroll
+    for (int a = 0; a < NS; ++a) {
+      const Parts sp = parts(s[2 * a], s[2 * a + 1]);
+#pragma unroll
+      for (int j = 0; j < NB; ++j) {
+        const unsigned at = (tile ^ (64 * (j / 2))) + 8 * (j % 2) + a * 64 * KD;
+        next[j] = mul_parts(Parts{values16<KD>(at), values16<KD>(at + kPart)}, sp, next[j]);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < NB; ++j) {
+      s[j] = next[j];
+      *reinterpret_cast<f4v *>(to + 32 * (j / 2) + 4 * (j % 2)) = s[j];
+    }
+    meet();
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -446,7 +602,12 @@ void chunks(const GdrParams &p, bool bwd, hipStream_t s) {
 template <int KD>
 hipError_t fwd(const GdrParams &p, hipStream_t s) {
   const int64_t heads = p.batch * p.nheads;
-  hipLaunchKernelGGL((gdr_fwd_kernel<KD>), dim3(static_cast<uint32_t>(heads * (p.vdim / 32))), dim3(256), 0, s, p);
+  if (p.seg.count > 1) {
+    const int64_t parts = heads * (p.seg.count - 1) * ((p.vdim + KD) / 64);
+    hipLaunchKernelGGL((gdr_segment_kernel<KD>), dim3(static_cast<uint32_t>(parts)), dim3(256), 0, s, p);
+    hipLaunchKernelGGL((gdr_join_kernel<KD>), dim3(static_cast<uint32_t>(heads * (p.vdim / 64))), dim3(256), 0, s, p);
+  }
+  hipLaunchKernelGGL((gdr_fwd_kernel<KD>), dim3(static_cast<uint32_t>(heads * (p.vdim / 32) * p.seg.count)), dim3(256), 0, s, p);
   return hipGetLastError();
 }
 
@@ -462,8 +623,28 @@ hipError_t step(const GdrParams &p, hipStream_t s) {
 
 }  // namespace
 
-size_t gdr_workspace(const GdrParams &p) {
-  return static_cast<size_t>(p.batch) * p.nheads * p.chunks * kGdrChunkBytes;
+GdrSegments gdr_segments(int64_t heads, int64_t vdim, int64_t chunks) {
+  // In turn a chunk takes 2 us.  With G segments each is gone through twice, 3.6
+  // us a chunk in all while there are compute units for them (a workgroup of
+  // the second pass has one to itself), and joining costs 1.5 us a segment and
+  // 10 us of two more launches.
+  const int64_t groups = heads * (vdim / 32);
+  int64_t best = 1, most = groups > 0 ? 256 / groups : 1;
+  double least = 2.0 * static_cast<double>(chunks);
+  for (int64_t g = 2; g <= most && g <= 64 && g <= chunks; ++g) {
+    const double us = 3.6 * static_cast<double>((chunks + g - 1) / g) + 1.5 * static_cast<double>(g) + 10.0;
+    if (us < least) {
+      least = us;
+      best = g;
+    }
+  }
+  const int64_t each = (chunks + best - 1) / best;
+  return {each > 0 ? (chunks + each - 1) / each : 1, each > 0 ? each : 1};
+}
+
+GdrSizes gdr_sizes(const GdrParams &p) {
+  const size_t heads = static_cast<size_t>(p.batch) * p.nheads, n = p.seg.count > 1 ? heads * p.seg.count : 0;
+  return {heads * p.chunks * kGdrChunkBytes, n * p.vdim * p.kdim * 4, n * 2 * p.kdim * p.kdim * 2};
 }
 
 hipError_t launch_gdr_chunks(const GdrParams &p, bool bwd, hipStream_t s) {

@@ -68,6 +68,9 @@ CASES = [  # batch, L, qk heads, value heads, K, V, gates, h0, lengths
     (3, 129, 2, 2, 128, 128, BF16, True, [129, 0, 64]), (4, 200, 1, 2, 64, 64, F32, True, [1, 63, 65, 300]),
     (2, 257, 3, 3, 64, 128, F32, False, [-5, 193]), (1, 513, 1, 1, 128, 128, F32, True, None),
     (5, 70, 16, 16, 64, 64, BF16, True, [70, 69, 2, 64, 33]),
+    # Long rows of few heads: cut into segments along time, some of which a row does not reach.
+    (1, 1500, 1, 2, 64, 64, F32, True, None), (4, 2113, 1, 1, 128, 128, F32, True, [2113, 700, 0, 1537]),
+    (1, 2048, 1, 1, 64, 128, BF16, False, None), (2, 3001, 1, 2, 128, 64, F32, False, [64, 2990]),
 ]
 
 
