@@ -66,7 +66,7 @@ typedef struct {
   size_t workspace_bytes;
 } ssm_gdr_dims_t;
 
-/* Steps between two saved states (see `states` below). */
+/* Tokens that are taken at a time. */
 enum { SSM_GDR_STATE_STEP = 64 };
 
 /*
@@ -83,17 +83,19 @@ enum { SSM_GDR_STATE_STEP = 64 };
  *            taken as the nearer end.  Rows at or past the length are not used.
  *   h_last : as h0, nullable: the state after the row's last token (h0 where
  *            there is none); may be exactly h0
- *   states : (batch, nheads, ceil(seqlen / 64), vdim, kdim) float32, nullable:
- *            the state before token 64 c, which ssm_gdr_bwd starts from;
- *            those at or past the row's length are not written
+ *   states : ssm_gdr_states_size() bytes, 16-byte aligned, nullable: what
+ *            ssm_gdr_bwd starts from, the state before every 64th token and the
+ *            u_t, in an order of their own; those at or past the row's length
+ *            are not written
  * The rule is stable for beta |k|^2 below 2: keys are meant to have unit length.
  * Tokens are taken 64 at a time: a value that is not finite reaches y from the
  * start of its block of 64 tokens (of its channel, if it is one of v; of the
  * value heads that share it, if it is one of q or k) and what comes after.
  */
 SSM_API int ssm_gdr_workspace_size(const ssm_gdr_dims_t *dims, size_t *bytes);
+SSM_API int ssm_gdr_states_size(const ssm_gdr_dims_t *dims, size_t *bytes);
 SSM_API int ssm_gdr_fwd(const void *q, const void *k, const void *v, const void *g, const void *beta, const float *h0,
-                        const int32_t *lengths, void *y, float *h_last, float *states, const ssm_gdr_dims_t *dims,
+                        const int32_t *lengths, void *y, float *h_last, void *states, const ssm_gdr_dims_t *dims,
                         void *stream);
 
 /*
@@ -111,7 +113,7 @@ SSM_API int ssm_gdr_fwd(const void *q, const void *k, const void *v, const void 
  */
 SSM_API int ssm_gdr_bwd_workspace_size(const ssm_gdr_dims_t *dims, size_t *bytes);
 SSM_API int ssm_gdr_bwd(const void *q, const void *k, const void *v, const void *g, const void *beta,
-                        const int32_t *lengths, const float *states, const void *dy, const float *dh_last, void *dq,
+                        const int32_t *lengths, const void *states, const void *dy, const float *dh_last, void *dq,
                         void *dk, void *dv, void *dg, void *dbeta, float *dh0, const ssm_gdr_dims_t *dims,
                         void *stream);
 

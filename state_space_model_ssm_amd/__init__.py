@@ -35,7 +35,7 @@ _BLOCK = (
 # The third library's binding (delta.py), likewise.
 _DELTA = (
     "GDR_STATE_STEP", "SWA_Q8_BLOCK", "GdrDims", "QkNormDims", "SwaQ8Cache", "delta_lib", "delta_library_path", "delta_last_error",
-    "gdr_fwd", "gdr_bwd", "gdr_step", "gdr_workspace_size", "gdr_bwd_workspace_size",
+    "gdr_fwd", "gdr_bwd", "gdr_step", "gdr_workspace_size", "gdr_states_size", "gdr_bwd_workspace_size",
     "qk_norm_fwd", "qk_norm_bwd", "qk_norm_bwd_workspace_size",
     "swa_q8_cache", "swa_q8_step", "swa_q8_step_workspace_size", "swa_q8_fill",
 )

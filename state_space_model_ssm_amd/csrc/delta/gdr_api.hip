@@ -48,6 +48,10 @@ size_t span(const ssm_gdr_dims_t &d, int64_t batch_stride, int64_t token_stride,
   return static_cast<size_t>((d.batch - 1) * batch_stride + (d.seqlen - 1) * token_stride + token) * 2;
 }
 
+size_t saved_bytes(const ssm_gdr_dims_t &d) {
+  return static_cast<size_t>(d.batch) * d.nheads * ceil_div(d.seqlen, SSM_GDR_STATE_STEP) * gdr_saved_bytes(d.kdim, d.vdim);
+}
+
 GdrParams params(const ssm_gdr_dims_t &d) {
   GdrParams p{};
   p.ws = static_cast<char *>(d.workspace);
@@ -85,8 +89,16 @@ int ssm_gdr_workspace_size(const ssm_gdr_dims_t *dims, size_t *bytes) {
   return ok();
 }
 
+int ssm_gdr_states_size(const ssm_gdr_dims_t *dims, size_t *bytes) {
+  if (!bytes) return fail(SSM_ERR_NULL, "bytes is NULL");
+  const int rc = check_gdr(dims, false);
+  if (rc != SSM_OK) return rc;
+  *bytes = saved_bytes(*dims);
+  return ok();
+}
+
 int ssm_gdr_fwd(const void *q, const void *k, const void *v, const void *g, const void *beta, const float *h0,
-                const int32_t *lengths, void *y, float *h_last, float *states, const ssm_gdr_dims_t *dims,
+                const int32_t *lengths, void *y, float *h_last, void *states, const ssm_gdr_dims_t *dims,
                 void *stream) {
   int rc = check_gdr(dims, false);
   if (rc != SSM_OK) return rc;
@@ -104,7 +116,7 @@ int ssm_gdr_fwd(const void *q, const void *k, const void *v, const void *g, cons
                      {"workspace", d.workspace, d.workspace ? d.workspace_bytes : 0, 1, false}};
   const Arg outs[] = {{"y", y, rows * d.nheads * d.vdim * 2, 16, true},
                       {"h_last", h_last, state, 16, false},
-                      {"states", states, state * p.chunks, 16, false}};
+                      {"states", states, saved_bytes(d), 16, false}};
   const void *const same[3][2] = {{nullptr, nullptr}, {h0, nullptr}, {nullptr, nullptr}};
   rc = check_args(ins, outs, same);
   const GdrSizes n = gdr_sizes(p);
@@ -120,7 +132,7 @@ int ssm_gdr_fwd(const void *q, const void *k, const void *v, const void *g, cons
   p.lengths = lengths;
   p.y = static_cast<uint16_t *>(y);
   p.h_last = h_last;
-  p.states = states;
+  p.saved = static_cast<char *>(states);
   p.ws_state = reinterpret_cast<float *>(p.ws + n.chunks);
   p.ws_carry = reinterpret_cast<uint16_t *>(p.ws + n.chunks + n.state);
   return launched(launch_gdr_fwd(p, static_cast<hipStream_t>(stream)), "gdr_fwd");
@@ -131,12 +143,12 @@ int ssm_gdr_bwd_workspace_size(const ssm_gdr_dims_t *dims, size_t *bytes) {
   const int rc = check_gdr(dims, false);
   if (rc != SSM_OK) return rc;
   const GdrBwdSizes n = gdr_bwd_sizes(params(*dims));
-  *bytes = n.chunks + n.ds + n.e;
+  *bytes = n.chunks + n.saved;
   return ok();
 }
 
 int ssm_gdr_bwd(const void *q, const void *k, const void *v, const void *g, const void *beta, const int32_t *lengths,
-                const float *states, const void *dy, const float *dh_last, void *dq, void *dk, void *dv, void *dg,
+                const void *states, const void *dy, const float *dh_last, void *dq, void *dk, void *dv, void *dg,
                 void *dbeta, float *dh0, const ssm_gdr_dims_t *dims, void *stream) {
   int rc = check_gdr(dims, false);
   if (rc != SSM_OK) return rc;
@@ -151,7 +163,7 @@ int ssm_gdr_bwd(const void *q, const void *k, const void *v, const void *g, cons
                      {"g", g, rows * d.nheads * eg, eg, true},
                      {"beta", beta, rows * d.nheads * eg, eg, true},
                      {"lengths", lengths, static_cast<size_t>(d.batch) * 4, 4, false},
-                     {"states", states, state * p.chunks, 16, true},
+                     {"states", states, saved_bytes(d), 16, true},
                      {"dy", dy, rows * d.nheads * d.vdim * 2, 16, true},
                      {"dh_last", dh_last, state, 16, false},
                      {"workspace", d.workspace, d.workspace ? d.workspace_bytes : 0, 1, false}};
@@ -160,7 +172,7 @@ int ssm_gdr_bwd(const void *q, const void *k, const void *v, const void *g, cons
                       {"dbeta", dbeta, rows * d.nheads * eg, eg, true},  {"dh0", dh0, state, 16, false}};
   const void *const same[6][2] = {};
   rc = check_args(ins, outs, same);
-  if (rc == SSM_OK) rc = check_workspace(ins, n.chunks + n.ds + n.e);
+  if (rc == SSM_OK) rc = check_workspace(ins, n.chunks + n.saved);
   if (rc != SSM_OK) return rc;
   if (d.batch == 0 || (d.seqlen == 0 && dh0 == nullptr)) return ok();
   p.q = static_cast<const uint16_t *>(q);
@@ -169,7 +181,7 @@ int ssm_gdr_bwd(const void *q, const void *k, const void *v, const void *g, cons
   p.g = g;
   p.beta = beta;
   p.lengths = lengths;
-  p.states = const_cast<float *>(states);
+  p.saved = static_cast<char *>(const_cast<void *>(states));
   p.dy = static_cast<const uint16_t *>(dy);
   p.dh_last = dh_last;
   p.dq = static_cast<uint16_t *>(dq);
@@ -178,8 +190,7 @@ int ssm_gdr_bwd(const void *q, const void *k, const void *v, const void *g, cons
   p.dg = dg;
   p.dbeta = dbeta;
   p.dh0 = dh0;
-  p.ws_ds = reinterpret_cast<float *>(p.ws + n.chunks);
-  p.ws_e = reinterpret_cast<float *>(p.ws + n.chunks + n.ds);
+  p.ws_saved = p.ws + n.chunks;
   return launched(launch_gdr_bwd(p, static_cast<hipStream_t>(stream)), "gdr_bwd");
 }
 

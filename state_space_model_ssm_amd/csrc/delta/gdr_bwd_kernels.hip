@@ -16,7 +16,7 @@ __global__ void __launch_bounds__(256) gdr_bwd_kernel(const GdrParams p) {
   constexpr int NT = 64 * kPairs, NC = 16 * kPairs, NS = KD / 32, NB = KD / 16;
   constexpr unsigned kRows = 64 * KD * 2, kValues = 64 * NC * 2, kTri = 2 * kGdrTriBytes, kOps = kTri + kGdrGateBytes;
   constexpr unsigned kAtQ = kRows, kAtD = 2 * kRows, kAtW = kAtD + kValues, kBuffer = kAtW + kOps;
-  constexpr unsigned kFour = 4 * 1024, kState = NB * 1024;  // float32 D results of the tokens, and of the state
+  constexpr unsigned kFour = 4 * 1024, kState = NB * 1024;  // D results of the tokens and of the state: float32, or two parts
   __shared__ __align__(16) u4 lds[(2 * kBuffer + kPairs * (kFour + kState)) / 16];
   const int tid = threadIdx.x, lane = tid & 63, m = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), w = wave % kPairs;
@@ -28,6 +28,7 @@ __global__ void __launch_bounds__(256) gdr_bwd_kernel(const GdrParams p) {
   const unsigned grown = base + 2 * kBuffer + kPairs * kFour + w * kState + lane * 16;
   const Lanes16 at = lanes16_of<KD>(lane);
   typedef __attribute__((address_space(3))) f4v lds_f4v;
+  typedef __attribute__((address_space(3))) u4 lds16;
 
   if (wave < kPairs) {
     f4v s[NB];  // dS, laid out as the state
@@ -36,12 +37,13 @@ __global__ void __launch_bounds__(256) gdr_bwd_kernel(const GdrParams p) {
     for (int j = 0; j < NB; ++j)
       s[j] = p.dh_last != nullptr ? *reinterpret_cast<const f4v *>(p.dh_last + state + 32 * (j / 2) + 4 * (j % 2)) : f4v{};
     for (int c = n - 1; c >= 0; --c) {
-      float *to = p.ws_ds + ((bh * p.chunks + c) * p.vdim + col0 + m) * KD + 8 * g;
-#pragma unroll
-      for (int j = 0; j < NB; ++j) *reinterpret_cast<f4v *>(to + 32 * (j / 2) + 4 * (j % 2)) = s[j];
       Parts sp[NS];
 #pragma unroll
-      for (int a = 0; a < NS; ++a) sp[a] = parts(s[2 * a], s[2 * a + 1]);
+      for (int a = 0; a < NS; ++a) {
+        sp[a] = parts(s[2 * a], s[2 * a + 1]);
+        *(lds16 *)(grown + a * 2048) = __builtin_bit_cast(u4, sp[a].hi);
+        *(lds16 *)(grown + a * 2048 + 1024) = __builtin_bit_cast(u4, sp[a].lo);
+      }
       meet();
       const unsigned tile = base + (c & 1) * kBuffer, at_t = tile + kAtW, gates = at_t + kTri + 16 * g;
       bf8 ka[NS][4], kt[2][NB];
@@ -104,7 +106,7 @@ __global__ void __launch_bounds__(256) gdr_bwd_kernel(const GdrParams p) {
   const int64_t hk = h / (p.nheads / p.nqk), yt = p.nheads * p.vdim;
   const uint16_t *kp = p.k + b * p.k_batch + hk * KD, *qp = p.q + b * p.q_batch + hk * KD;
   const uint16_t *dp = p.dy + (b * p.seqlen * p.nheads + h) * p.vdim + vt * NC;
-  const char *ws = p.ws + bh * p.chunks * static_cast<int64_t>(kGdrBwdChunkBytes) + kGdrTriBytes;  // T^T, A^T, gates
+  const char *ws = p.ws + bh * p.chunks * static_cast<int64_t>(kGdrChunkBytes);  // T^T, A^T, gates
   uint16_t *vp = p.dv + (b * p.seqlen * p.nheads + h) * p.vdim + col0;
   TileCopy<KD, NT> k_copy, q_copy;
   TileCopy<NC, NT> d_copy;
@@ -121,17 +123,28 @@ __global__ void __launch_bounds__(256) gdr_bwd_kernel(const GdrParams p) {
     d_copy.start(to + kAtD / 16, dp + 64 * c * yt, last, id);
   };
   auto fetch_ws = [&](int c) {
-    copy_share<kOps / 1024, kPairs>(base + (c & 1) * kBuffer + kAtW, ws + c * static_cast<int64_t>(kGdrBwdChunkBytes), w, lane * 16);
+    copy_share<kOps / 1024, kPairs>(base + (c & 1) * kBuffer + kAtW, ws + c * static_cast<int64_t>(kGdrChunkBytes), w, lane * 16);
   };
   f4v e[4];
+  const int vcol = col0 / 16, nv = static_cast<int>(p.vdim) / 32;
+  auto saved = [&](int c) {
+    return p.ws_saved + (bh * p.chunks + c) * static_cast<int64_t>(gdr_saved_bytes(KD, p.vdim)) + lane * 16 + vcol % 2 * 8;
+  };
+  // D = beta E, as operands over the values and as dv.
   auto store = [&](int c) {
-    float *to = p.ws_e + (bh * p.chunks + c) * 64 * p.vdim + (vt * kPairs + w) * 1024 + lane * 4;
     const unsigned beta = base + (c & 1) * kBuffer + kAtW + kTri + 768 + 16 * g;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      *reinterpret_cast<f4v *>(to + i * 256) = e[i];
-      e[i] *= lds_f4(beta + 64 * i);
+    for (int i = 0; i < 4; ++i) e[i] *= lds_f4(beta + 64 * i);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const Parts d = parts(e[2 * k], e[2 * k + 1]);
+      *(lds16 *)(four + k * 2048) = __builtin_bit_cast(u4, d.hi);
+      *(lds16 *)(four + k * 2048 + 1024) = __builtin_bit_cast(u4, d.lo);
     }
+    wait_reads();
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      turn_round<false>(four - lane * 16, i, saved(c) + gdr_state_bytes(KD, p.vdim) + (vcol / 2 * 4 + i) * 2048, lane);
     if (64 * c + 64 > len) {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
@@ -170,6 +183,8 @@ __global__ void __launch_bounds__(256) gdr_bwd_kernel(const GdrParams p) {
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) *(lds_f4v *)(four + i * 1024) = x[i];
+#pragma unroll
+    for (int j = 0; j < NB; ++j) turn_round<true>(grown - lane * 16, j, saved(c) + (j * nv + vcol / 2) * 2048, lane);
     meet();
     if (c > 0) fetch_rows(c - 1);
     f4v z[NB] = {};
@@ -201,22 +216,6 @@ __global__ void __launch_bounds__(256) gdr_bwd_kernel(const GdrParams p) {
 // Within a chunk: dq, dk, dg, dbeta
 // ---------------------------------------------------------------------------
 
-// Transposed operands of a tile of 64-column rows [value][token], in two
-// parts: lane m stands for token 16 i + m, k for values 32 s + 8g ..
-struct Pair {
-  unsigned hi, lo;  // where the tiles are
-};
-__device__ __forceinline__ bf8 tokens16(unsigned tile, int i, int s, unsigned col) {
-  typedef __attribute__((address_space(3))) sh4 lds4;
-  const unsigned to = ((tile + col) ^ (32 * i)) + s * 32 * 128;
-  const sh4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)(to));
-  const sh4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)((to ^ 16) + 4 * 128));
-  return __builtin_bit_cast(bf8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
-}
-__device__ __forceinline__ Parts tokens16(const Pair &t, int i, int s, unsigned col) {
-  return {tokens16(t.hi, i, s, col), tokens16(t.lo, i, s, col)};
-}
-
 // Operand of the elements 16 ct + m of a row-major tile, k its rows 32 s .. in D's order.
 template <int D>
 __device__ __forceinline__ bf8 elems16(unsigned tile, int ct, int s, int lane) {
@@ -236,285 +235,199 @@ __device__ __forceinline__ float sum16(float v) {
 __device__ __forceinline__ void store_gate(void *p, int64_t i, float v, float) { st(static_cast<float *>(p), i, v); }
 __device__ __forceinline__ void store_gate(void *p, int64_t i, float v, uint16_t) { st(static_cast<uint16_t *>(p), i, v); }
 
+// A fragment of 1024 bytes in memory.
+__device__ __forceinline__ bf8 frag_at(const char *p, int lane) { return *reinterpret_cast<const bf8 *>(p + lane * 16); }
+
+// Operand of rows 16 i .. of a tile of 64 values a row, k its values 32 s .. in D's order.
+__device__ __forceinline__ bf8 row16_d(unsigned tile, int i, int s, unsigned row) {
+  typedef __attribute__((address_space(3))) const u2 lds8;
+  const unsigned at = ((tile + row) ^ (64 * s)) + i * 2048;
+  const u2 lo = *(lds8 *)(at), hi = *(lds8 *)(at ^ 32);
+  return __builtin_bit_cast(bf8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3));
+}
+
+__device__ __forceinline__ float dot2(bf8 a, bf8 b, float c) {
+  typedef __attribute__((ext_vector_type(2))) __bf16 bf2;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) c = __builtin_amdgcn_fdot2_f32_bf16(bf2{a[2 * k], a[2 * k + 1]}, bf2{b[2 * k], b[2 * k + 1]}, c, false);
+  return c;
+}
+
 // A workgroup per chunk and query head, over the value heads that share it; a
-// wavefront per 16 key elements.
-template <int KD, int VD, typename G>
-__global__ void __launch_bounds__(4 * KD) gdr_grad_kernel(const GdrParams p) {
-  constexpr int NW = KD / 16, NT = 64 * NW, NS = KD / 32, NV = VD / 32;
-  constexpr unsigned kRows = 64 * KD * 2, kAtQ = kRows, kAtD = 2 * kRows, kAtU = kAtD + 64 * VD * 2, kPart = VD * 128;
-  constexpr unsigned kFour = 4 * (kPart > kGdrTriBytes ? kPart : kGdrTriBytes), kAtS = kAtU + kFour, kSlice = 32 * KD * 2;
-  __shared__ __align__(16) u4 lds[(kAtS + 4 * kSlice) / 16];
-  __shared__ float red[2][NW][64], whole[NW];
+// wavefront per quarter of the key elements, and per 16 tokens of what the
+// tokens are to each other.
+template <int KD, int VD, bool SHARED, typename G>
+__global__ void __launch_bounds__(256, 2) gdr_grad_kernel(const GdrParams p) {
+  constexpr int NT = 256, NW = 4, NE = KD / 64, NV = VD / 32;  // NE: blocks of 16 key elements of a wavefront
+  constexpr unsigned kRows = 64 * KD * 2, kAtQ = kRows, kAtD = 2 * kRows, kAtU = kAtD + 64 * 64 * 2, kParts = 2 * 8 * 1024;
+  // dY, U and D of 64 values; then fragments of a triangle and its transpose, and the triangle in float32.
+  constexpr unsigned kTriangle = 2 * kGdrTriBytes, kValues = 64 * 64 * 2 + 2 * kParts, kAll = kTriangle + 64 * kPitch * 4;
+  constexpr unsigned kArea = kValues > kAll ? kValues : kAll;
+  __shared__ __align__(16) u4 lds[(kAtD + kArea) / 16];
+  __shared__ float red[NW][64], diag[64], whole[NW];
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t c = blockIdx.x % p.chunks, bk = blockIdx.x / p.chunks, b = bk / p.nqk, hk = bk % p.nqk;
-  const int64_t share = p.nheads / p.nqk;
+  const unsigned chunks = static_cast<unsigned>(p.chunks), nqk = static_cast<unsigned>(p.nqk);
+  const int64_t c = blockIdx.x % chunks, bk = blockIdx.x / chunks, b = static_cast<unsigned>(bk) / nqk, hk = static_cast<unsigned>(bk) % nqk;
+  const int64_t share = static_cast<unsigned>(p.nheads) / nqk;
   const int t0 = static_cast<int>(c) * 64, len = gdr_length(p.lengths, b, p.seqlen) - t0;
   const int rows = p.seqlen - t0 < 64 ? static_cast<int>(p.seqlen - t0) : 64;
-  f4v tq[4] = {}, tk[4] = {};
+  f4v aq[NE][4] = {}, ak[NE][4] = {};  // dq and dk
   if (len > 0) {
     const unsigned base = lds_at(lds);
     load_tile<KD, NT>(lds, p.k + b * p.k_batch + hk * KD, p.k_token, t0, t0 + len - 1, threadIdx.x);
     load_tile<KD, NT>(lds + kAtQ / 16, p.q + b * p.q_batch + hk * KD, p.q_token, t0, t0 + len - 1, threadIdx.x);
 #pragma unroll 1
     for (int64_t h = hk * share; h < (hk + 1) * share; ++h) {
-    // (Made anew for each head: the compiler would keep all that follows from
-    // it, hundreds of addresses and masks, from one head to the next.)
-    int tid = threadIdx.x;
-    asm volatile("" : "+v"(tid));
-    const int lane = tid & 63, m = lane & 15, g = lane >> 4;
-    const Lanes16 atk = lanes16_of<KD>(lane), atv = lanes16_of<VD>(lane);
-    // Where this lane's pieces of transposed reads lie: row 8g + m / 4, elements 4 (m % 4) ..
-    const unsigned col = static_cast<unsigned>(slot<64>(8 * g + (m >> 2), (m & 3) >> 1)) * 16 + (m & 1) * 8;
-    const unsigned col_s = (static_cast<unsigned>(slot<KD>(8 * g + (m >> 2), (m & 3) >> 1)) * 16 + (m & 1) * 8) ^ (32 * w);
-    const Pair U = {base + kAtU, base + kAtU + kPart}, D = {base + kAtU + 2 * kPart, base + kAtU + 3 * kPart};
+      // (Made anew for each head: the compiler would keep all that follows from
+      // it, hundreds of addresses and masks, from one head to the next.)
+      int tid = threadIdx.x;
+      asm volatile("" : "+v"(tid));
+      const int lane = tid & 63, m = lane & 15, g = lane >> 4;
+      const unsigned row = static_cast<unsigned>(slot<64>(m, g >> 1)) * 16 + (g & 1) * 8;
       const int64_t bh = b * p.nheads + h, id = bh * p.chunks + c, yt = p.nheads * VD;
-      const char *ws = p.ws + id * static_cast<int64_t>(kGdrBwdChunkBytes);
-      const float *gates = reinterpret_cast<const float *>(ws + 3 * kGdrTriBytes);
+      const float *gates = reinterpret_cast<const float *>(p.ws + id * static_cast<int64_t>(kGdrChunkBytes) + 2 * kGdrTriBytes);
       const double *sums = reinterpret_cast<const double *>(gates + 256);
-      const float *s0 = p.states + id * VD * KD, *ds0 = p.ws_ds + id * VD * KD;
-      load_tile<VD, NT>(lds + kAtD / 16, p.dy + (b * p.seqlen * p.nheads + h) * VD, yt, t0, t0 + len - 1, tid);
-      // Of 32 values at a time, this thread's 8 elements of the state and of dS.
-      f4v sv[2], dv[2];
-      auto fetch_slice = [&](int s) {
+      const char *fs = p.saved + id * static_cast<int64_t>(gdr_saved_bytes(KD, VD)), *fu = fs + gdr_state_bytes(KD, VD);
+      const char *fds = p.ws_saved + id * static_cast<int64_t>(gdr_saved_bytes(KD, VD)), *fd = fds + gdr_state_bytes(KD, VD);
+      const uint16_t *dyp = p.dy + (b * p.seqlen * p.nheads + h) * VD;
+      f4v tq[NE][4], tk[NE][4];  // of the heads before
+      if (SHARED)
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          sv[k] = *reinterpret_cast<const f4v *>(s0 + s * 32 * KD + (k * NT + tid) * 4);
-          dv[k] = *reinterpret_cast<const f4v *>(ds0 + s * 32 * KD + (k * NT + tid) * 4);
-        }
-      };
-      // U = T beta (V - e^G K S0), a wavefront per 16 values; U and D = beta E go to LDS in parts.
-      float db[4][4] = {};
+        for (int x = 0; x < NE; ++x)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            tq[x][i] = aq[x][i];
+            tk[x][i] = ak[x][i];
+            aq[x][i] = f4v{};
+          }
+      f4v ae[NE][4] = {}, aw[NE][4] = {};  // what keys get as they read, and as they write
+      f4v py[4] = {}, pd[4] = {};          // dY U^T and D U^T: rows j, columns i = 16 w + m
+      float both = 0.0f;
 #pragma unroll 1
-      for (int ct = w; ct < VD / 16; ct += NW) {
-        f4v sf[NS][2], e[4], beta[4], into[4];
-        float vf[4][4];
-        Parts tf[kGdrFrags];
-        const float *from = s0 + (16 * ct + m) * KD + 8 * g;
+      for (int hv = 0; hv < VD / 64; ++hv) {
+        arrive();  // what was in LDS has been read
+        load_tile<64, NT>(lds + kAtD / 16, dyp + 64 * hv, yt, t0, t0 + len - 1, tid);
+        copy_share<16, NW>(base + kAtU, fu + hv * 16384, w, lane * 16);
+        copy_share<16, NW>(base + kAtU + kParts, fd + hv * 16384, w, lane * 16);
+        Parts sp[NE], dp[NE];
+        auto load = [&](int s) {
 #pragma unroll
-        for (int a = 0; a < NS; ++a)
-#pragma unroll
-          for (int k = 0; k < 2; ++k) sf[a][k] = *reinterpret_cast<const f4v *>(from + 32 * a + 4 * k);
-        const uint16_t *vp = p.v + b * p.v_batch + t0 * p.v_token + h * VD + 16 * ct + m;
-        const u4 *tp = reinterpret_cast<const u4 *>(ws) + lane;
-        const float *ep = p.ws_e + id * 64 * VD + ct * 1024 + lane * 4;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          into[i] = *reinterpret_cast<const f4v *>(gates + 64 + 16 * i + 4 * g);
-          beta[i] = *reinterpret_cast<const f4v *>(gates + 192 + 16 * i + 4 * g);
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const int row = 16 * i + 4 * g + r;
-            vf[i][r] = ld(vp, (row < len ? row : len - 1) * p.v_token);
+          for (int x = 0; x < NE; ++x) {
+            const int64_t at = ((NE * w + x) * NV + 2 * hv + s) * 2048;
+            sp[x] = {frag_at(fs + at, lane), frag_at(fs + at + 1024, lane)};
+            dp[x] = {frag_at(fds + at, lane), frag_at(fds + at + 1024, lane)};
           }
-        }
+        };
+        load(0);
+        arrive();
+        const unsigned dy = base + kAtD, u = base + kAtU, d = u + kParts;
+        auto part = [&](unsigned from, int i, int s) {  // U or D, token block i
+          return Parts{frag16(from, (4 * s + i) * 2, lane), frag16(from, (4 * s + i) * 2 + 1, lane)};
+        };
+#pragma unroll 1
+        for (int s = 0; s < 2; ++s) {
+          const Parts dw = part(d, w, s);
+          const bf8 yw = row16_d(dy, w, s, row);
 #pragma unroll
-        for (int f = 0; f < kGdrFrags; ++f)
-          tf[f] = {__builtin_bit_cast(bf8, tp[f * 64]), __builtin_bit_cast(bf8, tp[(kGdrFrags + f) * 64])};
+          for (int i = 0; i < 4; ++i) {
+            const Parts ui = part(u, i, s), di = part(d, i, s);
+            const bf8 yi = row16_d(dy, i, s, row);
+            py[i] = mfma16(ui.hi, yw, mfma16(ui.lo, yw, py[i]));
+            pd[i] = mul_parts(ui, dw, pd[i]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) e[i] = *reinterpret_cast<const f4v *>(ep + i * 256);
-        if (ct == w) arrive();  // keys, queries and dy are in LDS
-        f4v x[4] = {};
-#pragma unroll
-        for (int a = 0; a < NS; ++a) {
-          const Parts sp = parts(sf[a][0], sf[a][1]);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) x[i] = mul_exact(row16<KD>(base, i, a, atk), sp, x[i]);
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) x[i][r] = beta[i][r] * fmaf(-into[i][r], x[i][r], vf[i][r]);
-        f4v u[4] = {};
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const Parts xp = parts(x[2 * k], x[2 * k + 1]);
-#pragma unroll
-          for (int i = 2 * k; i < 4; ++i) u[i] = mul_parts(tf[tri(i, k)], xp, u[i]);
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-#pragma unroll
-          for (int r = 0; r < 4; ++r) db[i][r] = fmaf(e[i][r], u[i][r] / beta[i][r], db[i][r]);
-          e[i] *= beta[i];
-        }
-        typedef __attribute__((address_space(3))) u2 lds8;
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const Parts up = parts(u[2 * k], u[2 * k + 1]), dp = parts(e[2 * k], e[2 * k + 1]);
-#pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            const unsigned to = static_cast<unsigned>(slot<64>(16 * ct + m, 2 * (2 * k + y) + (g >> 1))) * 16 + (g & 1) * 8;
-            *(lds8 *)(U.hi + to) = half_of(up.hi, y);
-            *(lds8 *)(U.lo + to) = half_of(up.lo, y);
-            *(lds8 *)(D.hi + to) = half_of(dp.hi, y);
-            *(lds8 *)(D.lo + to) = half_of(dp.lo, y);
+            for (int x = 0; x < NE; ++x) {
+              aq[x][i] = mul_exact(yi, sp[x], aq[x][i]);
+              ae[x][i] = mul_parts(di, sp[x], ae[x][i]);
+              aw[x][i] = mul_parts(ui, dp[x], aw[x][i]);
+            }
           }
+#pragma unroll
+          for (int x = 0; x < NE; ++x) both = dot2(sp[x].hi, dp[x].hi, dot2(sp[x].hi, dp[x].lo, dot2(sp[x].lo, dp[x].hi, both)));
+          if (s == 0) load(1);
         }
       }
-      if (w >= VD / 16) arrive();
-      fetch_slice(0);
+      // P = scale (dY U^T) M and H = -(D U^T) M, and the diagonal of D U^T = beta E (beta Z).
+      const int own = 16 * w + m;
+      const double so = sums[own];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int j = 0; j < 4; ++j)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const float v = sum16(db[i][r]);
-          if (m == 0) red[0][w][16 * i + 4 * g + r] = v;
+          const int other = 16 * j + 4 * g + r;
+          const float gap = static_cast<float>(so - sums[other]);
+          if (other == own) diag[own] = pd[j][r];
+          const float decay = __builtin_amdgcn_exp2f(gap);
+          py[j][r] = other <= own && own < len ? py[j][r] * p.scale * decay : 0.0f;
+          pd[j][r] = other < own ? -pd[j][r] * decay : 0.0f;
         }
-      meet();
-      // P = scale (dY U^T) M and H = -(D U^T) M within the chunk, and their transposes, as fragments.
-      u4 frag[8 / NW][2][4];  // [P or H of this wavefront][as it is or transposed][parts of 2 steps]
-      auto products = [&](auto wave, auto kind, u4 (&f)[2][4]) {
-        constexpr int W = wave;
-        constexpr bool HH = kind;
-        f4v lower[W + 1] = {}, upper[4 - W] = {};
-#pragma unroll 1
-        for (int s = 0; s < NV; ++s) {
-          const Parts uw = tokens16(U, W, s, col);
-          const Parts dw = HH ? tokens16(D, W, s, col) : Parts{row16<VD>(base + kAtD, W, s, atv), bf8{}};
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            if (j <= W) {  // rows j, columns i = 16 W + m
-              const Parts uj = j == W ? uw : tokens16(U, j, s, col);
-              lower[j <= W ? j : 0] = HH ? mul_parts(uj, dw, lower[j <= W ? j : 0])
-                                         : mfma16(uj.hi, dw.hi, mfma16(uj.lo, dw.hi, lower[j <= W ? j : 0]));
-            }
-            if (j >= W) {  // rows i, columns j = 16 W + m
-              const Parts di = j == W ? dw : HH ? tokens16(D, j, s, col) : Parts{row16<VD>(base + kAtD, j, s, atv), bf8{}};
-              upper[j >= W ? j - W : 0] = HH ? mul_parts(di, uw, upper[j >= W ? j - W : 0])
-                                             : mul_exact(di.hi, uw, upper[j >= W ? j - W : 0]);
-            }
-          }
-        }
-        const int own = 16 * W + m;
-        const double so = sums[own];
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const int other = 16 * j + 4 * g + r;
-            const double st = sums[other];
-            if (j <= W) {  // i = own, j = other
-              const bool in = HH ? other < own : other <= own && own < len;
-              const float f = (HH ? -1.0f : p.scale) * __builtin_amdgcn_exp2f(static_cast<float>(so - st));
-              lower[j <= W ? j : 0][r] = in ? lower[j <= W ? j : 0][r] * f : 0.0f;
-            }
-            if (j >= W) {
-              const bool in = HH ? own < other : own <= other && other < len;
-              const float f = (HH ? -1.0f : p.scale) * __builtin_amdgcn_exp2f(static_cast<float>(st - so));
-              upper[j >= W ? j - W : 0][r] = in ? upper[j >= W ? j - W : 0][r] * f : 0.0f;
-            }
-          }
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          const f4v zero = {};
-          if (2 * s <= W) {
-            const Parts x = parts(lower[2 * s <= W ? 2 * s : 0], 2 * s + 1 <= W ? lower[2 * s + 1 <= W ? 2 * s + 1 : 0] : zero);
-            f[0][2 * s] = __builtin_bit_cast(u4, x.hi);
-            f[0][2 * s + 1] = __builtin_bit_cast(u4, x.lo);
-          }
-          if (2 * s + 1 >= W) {
-            const Parts x = parts(2 * s >= W ? upper[2 * s >= W ? 2 * s - W : 0] : zero, upper[2 * s + 1 >= W ? 2 * s + 1 - W : 0]);
-            f[1][2 * s] = __builtin_bit_cast(u4, x.hi);
-            f[1][2 * s + 1] = __builtin_bit_cast(u4, x.lo);
-          }
-        }
-      };
-      if constexpr (NW == 8) {
-        if (w < 4) by_wave(w, [&](auto wave) { products(wave, std::false_type{}, frag[0]); });
-        else by_wave(w - 4, [&](auto wave) { products(wave, std::true_type{}, frag[0]); });
-      } else {
-        by_wave(w, [&](auto wave) {
-          products(wave, std::false_type{}, frag[0]);
-          products(wave, std::true_type{}, frag[NW == 8 ? 0 : 1]);
-        });
-      }
-      // Products over the values, 32 at a time, a wavefront per 16 key elements.
-      f4v aq[4] = {}, ae[4] = {}, aw[4] = {};
-      float both = 0.0f;
-      const unsigned slice = base + kAtS;
-#pragma unroll 1
-      for (int s = 0; s < NV; ++s) {
-        typedef __attribute__((address_space(3))) u2 lds8;
-        const Parts sp = parts(sv[0], sv[1]), dp = parts(dv[0], dv[1]);
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int id4 = k * NT + tid, r = id4 / (KD / 4), e4 = id4 % (KD / 4);
-          const unsigned to = slice + static_cast<unsigned>(slot<KD>(r, e4 >> 1)) * 16 + (e4 & 1) * 8;
-          *(lds8 *)(to) = half_of(sp.hi, k);
-          *(lds8 *)(to + kSlice) = half_of(sp.lo, k);
-          *(lds8 *)(to + 2 * kSlice) = half_of(dp.hi, k);
-          *(lds8 *)(to + 3 * kSlice) = half_of(dp.lo, k);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) both = fmaf(sv[k][e], dv[k][e], both);
-        }
-        if (s + 1 < NV) fetch_slice(s + 1);
-        meet();
-        Parts so, dso;
-        so = {values16<KD>(slice + col_s), values16<KD>(slice + kSlice + col_s)};
-        dso = {values16<KD>(slice + 2 * kSlice + col_s), values16<KD>(slice + 3 * kSlice + col_s)};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          aq[i] = mul_exact(row16<VD>(base + kAtD, i, s, atv), so, aq[i]);
-          ae[i] = mul_parts(tokens16(D, i, s, col), so, ae[i]);
-          aw[i] = mul_parts(tokens16(U, i, s, col), dso, aw[i]);
-        }
-        meet();
-      }
-      // Fragments of kind k take the place of U and D: as they are at 2 k, transposed at 2 k + 1.
-      auto keep = [&](int W, int kind, const u4 (&f)[2][4]) {
-        u4 *to = lds + (kAtU + kind * 2 * kGdrTriBytes) / 16 + lane;
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          if (2 * s <= W) {
-            to[tri(W, s) * 64] = f[0][2 * s];
-            to[(kGdrFrags + tri(W, s)) * 64] = f[0][2 * s + 1];
-          }
-          if (2 * s + 1 >= W) {
-            to[kGdrTriBytes / 16 + tri_t(W, s) * 64] = f[1][2 * s];
-            to[kGdrTriBytes / 16 + (kGdrFrags + tri_t(W, s)) * 64] = f[1][2 * s + 1];
-          }
-        }
-      };
-      if constexpr (NW == 8) {
-        keep(w & 3, w >> 2, frag[0]);
-      } else {
-        keep(w, 0, frag[0]);
-        keep(w, 1, frag[NW == 8 ? 0 : 1]);
-      }
+      sh4 kc[NE][4], qc[NE][4];
       both *= gates[64 + 63];
-      sh4 kc[4], qc[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        kc[i] = rows4<KD>(base, i, w, lane);
-        qc[i] = rows4<KD>(base + kAtQ, i, w, lane);
         const f4v qs = *reinterpret_cast<const f4v *>(gates + 16 * i + 4 * g);
         const f4v into = *reinterpret_cast<const f4v *>(gates + 64 + 16 * i + 4 * g);
         const f4v out = *reinterpret_cast<const f4v *>(gates + 128 + 16 * i + 4 * g);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          aq[i][r] *= qs[r];
-          ae[i][r] *= -into[r];
-          aw[i][r] *= out[r];
-          both = fmaf(up(kc[i][r]), aw[i][r], both);  // <S_C, dS> with what the chunk adds to S_C
+        for (int x = 0; x < NE; ++x) {
+          kc[x][i] = rows4<KD>(base, i, NE * w + x, lane);
+          qc[x][i] = rows4<KD>(base + kAtQ, i, NE * w + x, lane);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            aq[x][i][r] *= qs[r];
+            ae[x][i][r] *= -into[r];
+            aw[x][i][r] *= out[r];
+            both = fmaf(up(kc[x][i][r]), aw[x][i][r], both);  // <S_C, dS> with what the chunk adds to S_C
+          }
         }
       }
-      meet();
-      const unsigned fp = base + kAtU, fh = fp + 2 * kGdrTriBytes;
+      // P and P^T, then H and H^T, as fragments in LDS, where all wavefronts take them.
+      const unsigned area = base + kAtD;
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        const bf8 kb = elems16<KD>(base, w, s, lane), qb = elems16<KD>(base + kAtQ, w, s, lane);
-        auto mul = [&](unsigned f, int k, bf8 x, f4v acc) {
-          return mfma16(frag16(f, k, lane), x, mfma16(frag16(f, kGdrFrags + k, lane), x, acc));
-        };
+      for (int kind = 0; kind < 2; ++kind) {
+        meet();
+        const f4v (&lower)[4] = kind == 0 ? py : pd;
+        u4 *to = lds + kAtD / 16;
+        float *full = reinterpret_cast<float *>(to + kTriangle / 16);
 #pragma unroll
-        for (int i = 2 * s; i < 4; ++i) {
-          aq[i] = mul(fp, tri(i, s), kb, aq[i]);
-          ae[i] = mul(fh, tri(i, s), kb, ae[i]);
+        for (int j = 0; j < 4; ++j) *reinterpret_cast<f4v *>(full + own * kPitch + 16 * j + 4 * g) = lower[j];
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          const Parts x = parts(lower[2 * s], lower[2 * s + 1]);
+          if (2 * s <= w) {
+            const int f = w < 2 ? w : 2 * (w - 1) + s;
+            to[f * 64 + lane] = __builtin_bit_cast(u4, x.hi);
+            to[(kGdrFrags + f) * 64 + lane] = __builtin_bit_cast(u4, x.lo);
+          }
         }
+        meet();
+        store_cols(full, w, to + kGdrTriBytes / 16, lane);
+        meet();
 #pragma unroll
-        for (int j = 0; j <= 2 * s + 1; ++j) {
-          aw[j] = mul(fp + kGdrTriBytes, tri_t(j, s), qb, aw[j]);
-          aw[j] = mul(fh + kGdrTriBytes, tri_t(j, s), kb, aw[j]);
+        for (int s = 0; s < 2; ++s) {
+          bf8 kb[NE], qb[NE];
+#pragma unroll
+          for (int x = 0; x < NE; ++x) {
+            kb[x] = elems16<KD>(base, NE * w + x, s, lane);
+            if (kind == 0) qb[x] = elems16<KD>(base + kAtQ, NE * w + x, s, lane);
+          }
+#pragma unroll
+          for (int i = 2 * s; i < 4; ++i) {
+            const Parts f = {frag16(area, tri(i, s), lane), frag16(area, kGdrFrags + tri(i, s), lane)};
+#pragma unroll
+            for (int x = 0; x < NE; ++x) {
+              f4v &acc = kind == 0 ? aq[x][i] : ae[x][i];
+              acc = mfma16(f.hi, kb[x], mfma16(f.lo, kb[x], acc));
+            }
+          }
+#pragma unroll
+          for (int j = 0; j <= 2 * s + 1; ++j) {
+            const Parts f = {frag16(area + kGdrTriBytes, tri_t(j, s), lane), frag16(area + kGdrTriBytes, kGdrFrags + tri_t(j, s), lane)};
+#pragma unroll
+            for (int x = 0; x < NE; ++x) {
+              const bf8 right = kind == 0 ? qb[x] : kb[x];
+              aw[x][j] = mfma16(f.hi, right, mfma16(f.lo, right, aw[x][j]));
+            }
+          }
         }
       }
       // d / dG, a term per token from each of q, the key that reads and the key that writes.
@@ -522,38 +435,47 @@ __global__ void __launch_bounds__(4 * KD) gdr_grad_kernel(const GdrParams p) {
       for (int i = 0; i < 4; ++i) {
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const float v = sum16(fmaf(up(qc[i][r]), aq[i][r], up(kc[i][r]) * (ae[i][r] - aw[i][r])));
-          if (m == 0) red[1][w][16 * i + 4 * g + r] = v;
+          float v = 0.0f;
+#pragma unroll
+          for (int x = 0; x < NE; ++x)
+            v = fmaf(up(qc[x][i][r]), aq[x][i][r], fmaf(up(kc[x][i][r]), ae[x][i][r] - aw[x][i][r], v));
+          v = sum16(v);
+          if (m == 0) red[w][16 * i + 4 * g + r] = v;
         }
-        tq[i] += aq[i];
-        tk[i] += ae[i] + aw[i];
+#pragma unroll
+        for (int x = 0; x < NE; ++x) {
+          ak[x][i] = ae[x][i] + aw[x][i];
+          if (SHARED) {
+            aq[x][i] += tq[x][i];
+            ak[x][i] += tk[x][i];
+          }
+        }
       }
       both = sum16(both);
       both += __shfl_xor(both, 16);
       both += __shfl_xor(both, 32);
       if (lane == 0) whole[w] = both;
       meet();
-      if (w == 0 && lane < rows) {
-        float dg = 0.0f, dbeta = 0.0f, total = 0.0f;
+      if (w == 0) {  // dg_t is the sum of d / dG from t on; dbeta = E.Z
+        float dg = 0.0f, total = 0.0f;
 #pragma unroll
         for (int k = 0; k < NW; ++k) {
-          dbeta += red[0][k][lane];
-          dg += red[1][k][lane];
+          dg += red[k][lane];
           total += whole[k];
         }
-        if (lane >= len) dg = dbeta = 0.0f;
+        if (lane >= len) dg = 0.0f;
         if (lane == (len < 64 ? len - 1 : 63)) dg += total;
-        red[1][0][lane] = dg;
-        store_gate(p.dbeta, (b * p.seqlen + t0 + lane) * p.nheads + h, dbeta, G{});
-      }
-      if (w == 0) {  // dg_t is the sum of d / dG from t on
-        float v = lane < rows ? red[1][0][lane] : 0.0f;
 #pragma unroll
         for (int d = 1; d < 64; d *= 2) {
-          const float next = __shfl_down(v, d);
-          if (lane + d < 64) v += next;
+          const float next = __shfl_down(dg, d);
+          if (lane + d < 64) dg += next;
         }
-        if (lane < rows) store_gate(p.dg, (b * p.seqlen + t0 + lane) * p.nheads + h, lane < len ? v : 0.0f, G{});
+        const float beta = gates[192 + lane];
+        if (lane < rows) {
+          const int64_t to = (b * p.seqlen + t0 + lane) * p.nheads + h;
+          store_gate(p.dg, to, lane < len ? dg : 0.0f, G{});
+          store_gate(p.dbeta, to, lane < len ? diag[lane] / beta / beta : 0.0f, G{});
+        }
       }
     }
   } else {
@@ -563,25 +485,27 @@ __global__ void __launch_bounds__(4 * KD) gdr_grad_kernel(const GdrParams p) {
       store_gate(p.dbeta, to, 0.0f, G{});
     }
   }
-  const int m = threadIdx.x & 15, g = threadIdx.x >> 4 & 3;
-  uint16_t *dqp = p.dq + ((b * p.seqlen + t0) * p.nqk + hk) * KD + 16 * w + m;
-  uint16_t *dkp = p.dk + ((b * p.seqlen + t0) * p.nqk + hk) * KD + 16 * w + m;
-  const int64_t row_step = p.nqk * KD;
+  const int lane = threadIdx.x & 63, g = lane >> 4;
+  RowStore out;
+  out.init(p.nqk * KD, lane);
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int x = 0; x < NE; ++x) {
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int row = 16 * i + 4 * g + r;
-      if (row < rows) {
-        st(dqp, row * row_step, row < len ? tq[i][r] : 0.0f);
-        st(dkp, row * row_step, row < len ? tk[i][r] : 0.0f);
-      }
-    }
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (16 * i + 4 * g + r >= len) aq[x][i][r] = ak[x][i][r] = 0.0f;
+    const int64_t to = ((b * p.seqlen + t0) * p.nqk + hk) * KD + 16 * (NE * w + x);
+    out.put(p.dq + to, rows, aq[x]);
+    out.put(p.dk + to, rows, ak[x]);
+  }
 }
 
 template <int KD, int VD, typename G>
 void grad(const GdrParams &p, hipStream_t s) {
-  hipLaunchKernelGGL((gdr_grad_kernel<KD, VD, G>), dim3(static_cast<uint32_t>(p.batch * p.nqk * p.chunks)), dim3(4 * KD), 0, s, p);
+  const dim3 n(static_cast<uint32_t>(p.batch * p.nqk * p.chunks));
+  if (p.nheads == p.nqk) hipLaunchKernelGGL((gdr_grad_kernel<KD, VD, false, G>), n, dim3(256), 0, s, p);
+  else hipLaunchKernelGGL((gdr_grad_kernel<KD, VD, true, G>), n, dim3(256), 0, s, p);
 }
 
 template <int KD>
@@ -599,7 +523,7 @@ hipError_t bwd(const GdrParams &p, hipStream_t s) {
 
 GdrBwdSizes gdr_bwd_sizes(const GdrParams &p) {
   const size_t n = static_cast<size_t>(p.batch) * p.nheads * p.chunks;
-  return {n * kGdrBwdChunkBytes, n * p.vdim * p.kdim * 4, n * 64 * p.vdim * 4};
+  return {n * kGdrChunkBytes, n * gdr_saved_bytes(p.kdim, p.vdim)};
 }
 
 hipError_t launch_gdr_bwd(const GdrParams &p, hipStream_t s) {

@@ -10,14 +10,17 @@ constexpr int kGdrChunk = 64;
 
 // What is known of a chunk of 64 tokens and a value head before its state is:
 // T = (I + L)^-1 and the attention A within the chunk, as operands in bfloat16
-// parts (see gdr_tile.h), then the gates' factors.  The forward has T, A; the
-// backward T, T^T, A^T.
+// parts (see gdr_tile.h), then the gates' factors.  The backward has T^T, A^T.
 constexpr int kGdrFrags = 6;                                   // operands of a triangle: 16 rows x 32 columns each
 constexpr size_t kGdrTriBytes = size_t{2} * kGdrFrags * 1024;  // both parts
 // Factors, 64 of each: scale e^G, e^G, e^(GC - G), beta (float32), and G log2(e) (float64).
 constexpr size_t kGdrGateBytes = 2048;
 constexpr size_t kGdrChunkBytes = 2 * kGdrTriBytes + kGdrGateBytes;
-constexpr size_t kGdrBwdChunkBytes = 3 * kGdrTriBytes + kGdrGateBytes;
+// Of a chunk and value head, in two bfloat16 parts as operands over 32 values
+// (see gdr_tile.h): the state before it or dS behind it, [16 key elements][32
+// values][part], then U or D = beta E, [32 values][16 tokens][part], 1 KiB each.
+constexpr size_t gdr_state_bytes(int64_t kdim, int64_t vdim) { return static_cast<size_t>(kdim * vdim) * 4; }
+constexpr size_t gdr_saved_bytes(int64_t kdim, int64_t vdim) { return gdr_state_bytes(kdim, vdim) + static_cast<size_t>(64 * vdim) * 4; }
 
 // Long sequences of few heads are cut into segments of `chunks` chunks, and the
 // state at the start of each is found before y is made: with S_0 = 0 and with
@@ -33,14 +36,15 @@ struct GdrParams {
   const float *h0;             // nullable
   const int32_t *lengths;      // nullable
   uint16_t *y;
-  float *h_last, *states;      // nullable
-  char *ws;                    // kGdrChunkBytes (backward: kGdrBwdChunkBytes) per (row, value head, chunk)
+  float *h_last;               // nullable
+  char *saved;                 // gdr_saved_bytes() of S and U per (row, value head, chunk), nullable in the forward
+  char *ws;                    // kGdrChunkBytes per (row, value head, chunk)
   const uint16_t *dy;          // backward
   const float *dh_last;        // nullable
   uint16_t *dq, *dk, *dv;
   void *dg, *dbeta;            // gate dtype
   float *dh0;                  // nullable
-  float *ws_ds, *ws_e;         // per (row, value head, chunk): dS behind it, and E = T^T dU in D's order
+  char *ws_saved;              // the backward's dS and D, as `saved`
   GdrSegments seg;
   float *ws_state;             // (row, value head, segment): E, and then the state before the segment
   uint16_t *ws_carry;          // (row, value head, segment, part): P, (kdim in, kdim out)
@@ -54,9 +58,9 @@ struct GdrSizes {
   size_t chunks, state, carry;
 };
 GdrSizes gdr_sizes(const GdrParams &p);
-// Sizes of the backward's workspace: ws, ws_ds and ws_e in turn.
+// Sizes of the backward's workspace: ws and ws_saved in turn.
 struct GdrBwdSizes {
-  size_t chunks, ds, e;
+  size_t chunks, saved;
 };
 GdrBwdSizes gdr_bwd_sizes(const GdrParams &p);
 hipError_t launch_gdr_chunks(const GdrParams &p, bool bwd, hipStream_t stream);

@@ -8,7 +8,7 @@ namespace {
 // Within a chunk
 // ---------------------------------------------------------------------------
 
-constexpr int kPitch = 68, kDiagPitch = 20;  // floats between rows in LDS: 16-byte aligned, rows on other banks
+constexpr int kDiagPitch = 20;  // floats between rows in LDS
 
 // Store row block W of a lower triangle, transposed D results, as fragments in two parts.
 template <int W>
@@ -18,26 +18,6 @@ __device__ __forceinline__ void store_rows(const f4v (&t)[W + 1], u4 *to, int la
     const Parts x = parts(t[2 * s], 2 * s + 1 <= W ? t[2 * s + 1 <= W ? 2 * s + 1 : 0] : f4v{});
     to[tri(W, s) * 64 + lane] = __builtin_bit_cast(u4, x.hi);
     to[(kGdrFrags + tri(W, s)) * 64 + lane] = __builtin_bit_cast(u4, x.lo);
-  }
-}
-
-// Row block J of a triangle's transpose, as fragments, from the triangle in LDS.
-__device__ __forceinline__ void store_cols(const float *t, int J, u4 *to, int lane) {
-  const int m = lane & 15, g = lane >> 4;
-#pragma unroll
-  for (int s = 0; s < 2; ++s) {
-    if (2 * s + 1 < J) continue;
-    f4v v[2];
-#pragma unroll
-    for (int x = 0; x < 2; ++x)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int i = 32 * s + 16 * x + 4 * g + r;
-        v[x][r] = i >= 16 * J + m ? t[i * kPitch + 16 * J + m] : 0.0f;
-      }
-    const Parts p = parts(v[0], v[1]);
-    to[tri_t(J, s) * 64 + lane] = __builtin_bit_cast(u4, p.hi);
-    to[(kGdrFrags + tri_t(J, s)) * 64 + lane] = __builtin_bit_cast(u4, p.lo);
   }
 }
 
@@ -54,7 +34,7 @@ __global__ void __launch_bounds__(256) gdr_chunk_kernel(const GdrParams p) {
   const int64_t id = blockIdx.x, c = id % p.chunks, bh = id / p.chunks, b = bh / p.nheads, h = bh % p.nheads;
   const int t0 = static_cast<int>(c) * 64, len = gdr_length(p.lengths, b, p.seqlen) - t0;
   if (len <= 0) return;
-  char *ws = p.ws + id * static_cast<int64_t>(BWD ? kGdrBwdChunkBytes : kGdrChunkBytes);
+  char *ws = p.ws + id * static_cast<int64_t>(kGdrChunkBytes);
   constexpr int NS = KD / 32;
   const int64_t hk = h / (p.nheads / p.nqk);
   const uint16_t *kp = p.k + b * p.k_batch + t0 * p.k_token + hk * KD + 8 * g;
@@ -74,8 +54,10 @@ __global__ void __launch_bounds__(256) gdr_chunk_kernel(const GdrParams p) {
       gt = gt < -200.0f ? -200.0f : gt;  // exp(-200) is 0, and differences of the sums stay finite
       bt = gate<G>(p.beta, at);
     }
-    // The backward divides by beta: a gate that is shut counts as 2^-60 there.
-    if (BWD && fabsf(bt) < 0x1p-60f) bt = copysignf(0x1p-60f, bt);
+    // The gradient of beta is a quotient by it: a gate that is shut counts as
+    // 2^-30, which adds less than the last bit of what the token's value is to
+    // the state.  (Behind the length nothing is added.)
+    if (lane < len && fabsf(bt) < 0x1p-30f) bt = copysignf(0x1p-30f, bt);
     // In float64: after a strong decay the differences of later tokens' sums would lose what they have.
     double s = static_cast<double>(gt) * 1.4426950408889634;
 #pragma unroll
@@ -87,7 +69,7 @@ __global__ void __launch_bounds__(256) gdr_chunk_kernel(const GdrParams p) {
     betas[lane] = bt;
     const double last = __shfl(s, 63);
     const float into = __builtin_amdgcn_exp2f(static_cast<float>(s));
-    float *gates = reinterpret_cast<float *>(ws + (BWD ? 3 : 2) * kGdrTriBytes);
+    float *gates = reinterpret_cast<float *>(ws + 2 * kGdrTriBytes);
     gates[lane] = lane < len ? p.scale * into : 0.0f;
     gates[64 + lane] = into;
     gates[128 + lane] = __builtin_amdgcn_exp2f(static_cast<float>(last - s));
@@ -165,15 +147,15 @@ __global__ void __launch_bounds__(256) gdr_chunk_kernel(const GdrParams p) {
 #pragma unroll
       for (int r = 0; r < 4; ++r) t[j] = mfma_f32(-d[r], acc[r], t[j]);
     }
-    store_rows<W>(t, out, lane);
+    if (!BWD) store_rows<W>(t, out, lane);
     if (BWD)
 #pragma unroll
       for (int jb = 0; jb <= W; ++jb) *reinterpret_cast<f4v *>(inv + i * kPitch + 16 * jb + 4 * g) = t[jb];
   });
   if (BWD) {
     __syncthreads();
-    store_cols(inv, w, out + kGdrTriBytes / 16, lane);
-    store_cols(full, w, out + 2 * kGdrTriBytes / 16, lane);
+    store_cols(inv, w, out, lane);
+    store_cols(full, w, out + kGdrTriBytes / 16, lane);
   }
 }
 
@@ -226,11 +208,6 @@ __global__ void __launch_bounds__(256) gdr_fwd_kernel(const GdrParams p) {
         sp[a] = parts(s[2 * a], s[2 * a + 1]);
         *(lds16 *)(parts_s + a * 2048) = __builtin_bit_cast(u4, sp[a].hi);
         *(lds16 *)(parts_s + a * 2048 + 1024) = __builtin_bit_cast(u4, sp[a].lo);
-      }
-      if (p.states != nullptr) {
-        float *to = p.states + ((bh * p.chunks + c) * p.vdim + col0 + m) * KD + 8 * g;
-#pragma unroll
-        for (int j = 0; j < NB; ++j) *reinterpret_cast<f4v *>(to + 32 * (j / 2) + 4 * (j % 2)) = s[j];
       }
       meet();
       const unsigned tile = base + (c & 1) * kBuffer, tri_t = tile + kAtW, gates = tri_t + 2 * kGdrTriBytes + 16 * g;
@@ -361,6 +338,13 @@ __global__ void __launch_bounds__(256) gdr_fwd_kernel(const GdrParams p) {
       for (int i = 0; i < 4; ++i) o[i] = mul_exact(qa[a][i], sp[a], o[i]);
 #pragma unroll
     for (int i = 0; i < 4; ++i) o[i] *= qs[i];
+    // What the backward starts from: its operands have the values as k.
+    const int vcol = col0 / 16, nv = static_cast<int>(p.vdim) / 32;
+    char *saved = p.saved + (bh * p.chunks + c) * static_cast<int64_t>(gdr_saved_bytes(KD, p.vdim)) + lane * 16 + vcol % 2 * 8;
+    if (p.saved != nullptr) {
+#pragma unroll
+      for (int j = 0; j < NB; ++j) turn_round<true>(parts_s - lane * 16, j, saved + (j * nv + vcol / 2) * 2048, lane);
+    }
     meet();
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
@@ -370,6 +354,11 @@ __global__ void __launch_bounds__(256) gdr_fwd_kernel(const GdrParams p) {
       for (int i = 2 * k; i < 4; ++i) o[i] = mul_parts(af[tri(i, k)], up, o[i]);
     }
     if (c + 1 < n) fetch_ws(c + 1);
+    if (p.saved != nullptr) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        turn_round<false>(parts_u - lane * 16, i, saved + gdr_state_bytes(KD, p.vdim) + (vcol / 2 * 4 + i) * 2048, lane);
+    }
     if (64 * c + 64 > len) {
 #pragma unroll
       for (int i = 0; i < 4; ++i)

@@ -105,6 +105,22 @@ __device__ __forceinline__ bf8 frag16(unsigned tile, int f, int lane) {
   typedef __attribute__((address_space(3))) const u4 lds16;
   return __builtin_bit_cast(bf8, *(lds16 *)(tile + f * 1024 + lane * 16));
 }
+// A D result in two parts, as operands left them in LDS (fragments of 32 rows,
+// high and low part in turn; rows: tokens in D's order, or, PLAIN, key elements
+// in plain order), turned round: lane m stands for row 16 i + m, and its four
+// values for columns 4g .. 4g + 3, half of an operand over 32 columns.  To
+// `to`, this lane's place in a fragment, high and low part.
+template <bool PLAIN>
+__device__ __forceinline__ void turn_round(unsigned from, int i, char *to, int lane) {
+  typedef __attribute__((address_space(3))) sh4 lds4;
+  const int m = lane & 15, col = 4 * (lane >> 4) + (m >> 2), p = m & 3;
+  const unsigned at = from + (i / 2) * 2048 +
+                      (PLAIN ? (16 * (2 * (i % 2) + (p >> 1)) + col) * 16 + (p & 1) * 8 : (16 * p + col) * 16 + (i % 2) * 8);
+#pragma unroll
+  for (int part = 0; part < 2; ++part)
+    *reinterpret_cast<sh4 *>(to + part * 1024) = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)(at + part * 1024));
+}
+
 __device__ __forceinline__ f4v lds_f4(unsigned at) {
   typedef __attribute__((address_space(3))) const f4v lds16;
   return *(lds16 *)(at);
@@ -284,6 +300,28 @@ __device__ __forceinline__ float up(short v) {
 
 template <typename G>
 __device__ __forceinline__ float gate(const void *p, int64_t i) { return ld(static_cast<const G *>(p), i); }
+
+constexpr int kPitch = 68;  // floats between rows of 64 in LDS: 16-byte aligned, rows on other banks
+
+// Row block J of a triangle's transpose, as fragments, from the triangle in LDS.
+__device__ __forceinline__ void store_cols(const float *t, int J, u4 *to, int lane) {
+  const int m = lane & 15, g = lane >> 4;
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    if (2 * s + 1 < J) continue;
+    f4v v[2];
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int i = 32 * s + 16 * x + 4 * g + r;
+        v[x][r] = i >= 16 * J + m ? t[i * kPitch + 16 * J + m] : 0.0f;
+      }
+    const Parts p = parts(v[0], v[1]);
+    to[tri_t(J, s) * 64 + lane] = __builtin_bit_cast(u4, p.hi);
+    to[(kGdrFrags + tri_t(J, s)) * 64 + lane] = __builtin_bit_cast(u4, p.lo);
+  }
+}
 
 // A workgroup's head and column tile: the tiles of a head, which read the same
 // keys and operands, 8 workgroups apart, so that they share an XCD's L2.

@@ -24,7 +24,7 @@ from .block import SwaDims, _BF16, _F32, _code, _heads, _out, _ptr, _same, _stre
 
 __all__ = list(_DELTA)
 
-GDR_STATE_STEP = 64   # steps between two saved states of the delta rule
+GDR_STATE_STEP = 64   # tokens that the delta rule takes at a time
 SWA_Q8_BLOCK = 64     # positions that share a scale in an 8-bit cache
 
 _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libssm_delta.so")
@@ -80,7 +80,8 @@ def delta_lib():
             f = getattr(L, name)
             f.argtypes = [vp] * pointers + [ctypes.POINTER(dims), vp]
             f.restype = ctypes.c_int
-        for name, dims in (("ssm_gdr_workspace_size", GdrDims), ("ssm_gdr_bwd_workspace_size", GdrDims),
+        for name, dims in (("ssm_gdr_workspace_size", GdrDims), ("ssm_gdr_states_size", GdrDims),
+                           ("ssm_gdr_bwd_workspace_size", GdrDims),
                            ("ssm_qk_norm_bwd_workspace_size", QkNormDims), ("ssm_swa_q8_step_workspace_size", SwaDims)):
             f = getattr(L, name)
             f.argtypes = [ctypes.POINTER(dims), size]
@@ -108,6 +109,10 @@ def _size(call, dims) -> int:
 
 def gdr_workspace_size(dims: GdrDims) -> int:
     return _size(delta_lib().ssm_gdr_workspace_size, dims)
+
+
+def gdr_states_size(dims: GdrDims) -> int:
+    return _size(delta_lib().ssm_gdr_states_size, dims)
 
 
 def gdr_bwd_workspace_size(dims: GdrDims) -> int:
@@ -182,8 +187,9 @@ def gdr_fwd(q, k, v, g, beta, *, h0=None, lengths=None, scale=None, return_h_las
     (batch, nheads, vdim, kdim) float32 (zero when None); lengths: (batch,)
     int32 or None; rows past a length may hold anything and give zeros.  scale
     defaults to kdim ** -0.5.  Returns ``(y, h_last)``, and with
-    ``return_states`` also the states before every 64th token, (batch, nheads,
-    ceil(L / 64), vdim, kdim) float32, that ``gdr_bwd`` starts from.  h_last
+    ``return_states`` also what ``gdr_bwd`` starts from, a uint8 tensor of
+    ``gdr_states_size`` bytes (the states before every 64th token and the u_t:
+    per value head and 64 tokens, 4 vdim (kdim + 64) bytes).  h_last
     (float32, after each row's last token) may be h0 itself.
     """
     _one_device(stream, q, k, v, g, beta, h0, lengths, workspace)
@@ -196,7 +202,7 @@ def gdr_fwd(q, k, v, g, beta, *, h0=None, lengths=None, scale=None, return_h_las
     if h_last is not None or return_h_last:
         h_last = _out(h_last, state, _F32, q, "h_last", stream)
     if states is not None or return_states:
-        states = _out(states, (batch, H, -(-L // GDR_STATE_STEP), vd, q.shape[-1]), _F32, q, "states", stream)
+        states = _out(states, (gdr_states_size(dims),), torch.uint8, q, "states", stream)
     workspace = _scratch(dims, gdr_workspace_size(dims), workspace, q, stream)
     _check(delta_lib().ssm_gdr_fwd(_at(q), _at(k), _at(v), _ptr(g), _ptr(beta), _ptr(h0), _ptr(lengths), _ptr(y),
                                    _ptr(h_last), _ptr(states), ctypes.byref(dims), _stream(stream)))
@@ -205,7 +211,7 @@ def gdr_fwd(q, k, v, g, beta, *, h0=None, lengths=None, scale=None, return_h_las
 
 def gdr_bwd(q, k, v, g, beta, states, dy, *, dh_last=None, lengths=None, scale=None, return_dh0: bool = True, out=None,
             workspace=None, stream=None):
-    """Backward of ``gdr_fwd`` (``ssm_gdr_bwd``) from the states it saved and
+    """Backward of ``gdr_fwd`` (``ssm_gdr_bwd``) from what it saved and
     the gradients of y (v's shape, bfloat16) and of h_last ((batch, nheads,
     vdim, kdim) float32 or None).  Returns ``(dq, dk, dv, dg, dbeta, dh0)``:
     dense, shaped and typed like q, k, v, g and beta; dh0 float32 (None without
@@ -215,7 +221,7 @@ def gdr_bwd(q, k, v, g, beta, states, dy, *, dh_last=None, lengths=None, scale=N
     dims = _gdr_dims(q, k, v, g, beta, scale, 2)
     batch, L, H, vd = v.shape
     state = (batch, H, vd, q.shape[-1])
-    _same("states", states, _F32, (batch, H, -(-L // GDR_STATE_STEP), vd, q.shape[-1]))
+    _same("states", states, torch.uint8, (gdr_states_size(dims),))
     _same("dy", dy, _BF16, v.shape)
     _same("dh_last", dh_last, _F32, state)
     _same("lengths", lengths, torch.int32, (batch,))

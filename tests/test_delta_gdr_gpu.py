@@ -59,6 +59,14 @@ def state_tol(states, last):
     return SMALL * max([float(s.abs().max()) for row in states for s in row] + [float(last.abs().max()), 4.0])
 
 
+def unpack(saved, B, H, chunks, K, V):
+    """The states (B, H, chunks, V, K) that a forward saved: two bfloat16 parts, [16 key elements][32 values][part], a lane
+    per (element, group g) with the values 4 g .. and 16 + 4 g .."""
+    per = saved.view(B, H, chunks, -1)[..., :4 * K * V].contiguous()
+    x = per.view(BF16).double().view(B, H, chunks, K // 16, V // 32, 2, 4, 16, 2, 4).sum(5)   # part; g, element, half, value
+    return x.permute(0, 1, 2, 4, 7, 5, 8, 3, 6).reshape(B, H, chunks, V, K)
+
+
 CASES = [  # batch, L, qk heads, value heads, K, V, gates, h0, lengths
     (1, 1, 1, 1, 64, 64, F32, True, None), (2, 2, 1, 2, 128, 64, BF16, False, None),
     (1, 15, 2, 2, 64, 128, F32, True, None), (1, 16, 1, 1, 128, 128, BF16, True, None),
@@ -86,16 +94,19 @@ def test_forward(B, L, nqk, H, K, V, gates, with_h0, lengths):
                 t[b, max(n, 0):] = float("nan")
     cq, ck, cv = one_tensor(q, k, v)
     cg, cb, ch = cuda(g, beta, h0)
-    y, hl, st = nan((B, L, H, V), BF16), nan((B, H, V, K)), nan((B, H, -(-L // 64), V, K))
+    chunks = -(-L // 64)
+    y, hl = nan((B, L, H, V), BF16), nan((B, H, V, K))
+    st = torch.full((B * H * chunks * 4 * V * (K + 64),), 0xff, dtype=torch.uint8, device="cuda")   # NaN
     got = ssm.gdr_fwd(cq, ck, cv, cg, cb, h0=ch, lengths=None if lens is None else lens.cuda(), return_states=True, y=y,
                       h_last=hl, states=st)
     assert got[0] is y and got[1] is hl and got[2] is st
     tol = state_tol(states, last)
     ref.close(hl, last, tol, "h_last")
+    saved = unpack(st, B, H, chunks, K, V)
     for b, row in enumerate(states):
         for c, s in enumerate(row):
-            ref.close(st[b, :, c], s, tol, f"state {c} of row {b}")
-        assert st[b, :, len(row):].isnan().all()   # not written
+            ref.close(saved[b, :, c], s, tol, f"state {c} of row {b}")
+        assert saved[b, :, len(row):].isnan().all()   # not written
     ref.close(y, want, U * want.abs() + SMALL * (size + K ** -0.5), "y")
     again = ssm.gdr_fwd(cq, ck, cv, cg, cb, h0=ch, lengths=None if lens is None else lens.cuda())
     assert torch.equal(again[0], y) and torch.equal(again[1], hl)
@@ -128,7 +139,7 @@ def test_backward(B, L, nqk, H, K, V, gates, with_h0, lengths):
     cl = None if lens is None else lens.cuda()
     views = one_tensor(q, k, v)
     cg, cb, ch, cdy, cdh = cuda(g, beta, h0, dy, dh)
-    states = nan((B, H, -(-L // 64), V, K))
+    states = torch.full((B * H * -(-L // 64) * 4 * V * (K + 64),), 0xff, dtype=torch.uint8, device="cuda")   # NaN
     ssm.gdr_fwd(*views, cg, cb, h0=ch, lengths=cl, states=states)
     outs = {n: nan(t.shape, t.dtype) for n, t in (("dq", q), ("dk", k), ("dv", v), ("dg", g), ("dbeta", beta))}
     outs["dh0"] = nan((B, H, V, K))
