@@ -126,9 +126,9 @@ __global__ void __launch_bounds__(256) gdr_bwd_kernel(const GdrParams p) {
     copy_share<kOps / 1024, kPairs>(base + (c & 1) * kBuffer + kAtW, ws + c * static_cast<int64_t>(kGdrChunkBytes), w, lane * 16);
   };
   f4v e[4];
-  const int vcol = col0 / 16, nv = static_cast<int>(p.vdim) / 32;
+  const int64_t nv = p.vdim / 32;
   auto saved = [&](int c) {
-    return p.ws_saved + (bh * p.chunks + c) * static_cast<int64_t>(gdr_saved_bytes(KD, p.vdim)) + lane * 16 + vcol % 2 * 8;
+    return p.ws_saved + (bh * p.chunks + c) * static_cast<int64_t>(gdr_saved_bytes(KD, p.vdim)) + lane * 16;
   };
   // D = beta E, as operands over the values and as dv.
   auto store = [&](int c) {
@@ -144,7 +144,7 @@ __global__ void __launch_bounds__(256) gdr_bwd_kernel(const GdrParams p) {
     wait_reads();
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      turn_round<false>(four - lane * 16, i, saved(c) + gdr_state_bytes(KD, p.vdim) + (vcol / 2 * 4 + i) * 2048, lane);
+      turn_half<false>(four - lane * 16, i, saved(c) + gdr_state_bytes(KD, p.vdim) + (vt * 4 + i) * 2048 + w * 8, lane);
     if (64 * c + 64 > len) {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
@@ -183,8 +183,11 @@ __global__ void __launch_bounds__(256) gdr_bwd_kernel(const GdrParams p) {
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) *(lds_f4v *)(four + i * 1024) = x[i];
+    // dS behind the chunk, half of both columns' tiles by each of the two wavefronts.
+    const unsigned all = base + 2 * kBuffer + kPairs * kFour;
 #pragma unroll
-    for (int j = 0; j < NB; ++j) turn_round<true>(grown - lane * 16, j, saved(c) + (j * nv + vcol / 2) * 2048, lane);
+    for (int j = 0; j < NB / 2; ++j)
+      turn_both<true>(all, all + kState, 2 * j + w, saved(c) + ((2 * j + w) * nv + vt) * 2048, lane);
     meet();
     if (c > 0) fetch_rows(c - 1);
     f4v z[NB] = {};

@@ -338,12 +338,15 @@ __global__ void __launch_bounds__(256) gdr_fwd_kernel(const GdrParams p) {
       for (int i = 0; i < 4; ++i) o[i] = mul_exact(qa[a][i], sp[a], o[i]);
 #pragma unroll
     for (int i = 0; i < 4; ++i) o[i] *= qs[i];
-    // What the backward starts from: its operands have the values as k.
-    const int vcol = col0 / 16, nv = static_cast<int>(p.vdim) / 32;
-    char *saved = p.saved + (bh * p.chunks + c) * static_cast<int64_t>(gdr_saved_bytes(KD, p.vdim)) + lane * 16 + vcol % 2 * 8;
+    // What the backward starts from, whose operands have the values as k: each
+    // of the two wavefronts turns half of both columns' tiles round.
+    const unsigned all_s = base + 2 * kBuffer, all_u = all_s + kPairs * kState;
+    const int64_t nv = p.vdim / 32;
+    char *saved = p.saved + (bh * p.chunks + c) * static_cast<int64_t>(gdr_saved_bytes(KD, p.vdim)) + lane * 16;
     if (p.saved != nullptr) {
 #pragma unroll
-      for (int j = 0; j < NB; ++j) turn_round<true>(parts_s - lane * 16, j, saved + (j * nv + vcol / 2) * 2048, lane);
+      for (int j = 0; j < NB / 2; ++j)
+        turn_both<true>(all_s, all_s + kState, 2 * j + w, saved + ((2 * j + w) * nv + vt) * 2048, lane);
     }
     meet();
 #pragma unroll
@@ -356,8 +359,8 @@ __global__ void __launch_bounds__(256) gdr_fwd_kernel(const GdrParams p) {
     if (c + 1 < n) fetch_ws(c + 1);
     if (p.saved != nullptr) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        turn_round<false>(parts_u - lane * 16, i, saved + gdr_state_bytes(KD, p.vdim) + (vcol / 2 * 4 + i) * 2048, lane);
+      for (int i = 0; i < 2; ++i)
+        turn_both<false>(all_u, all_u + kUpdate, 2 * i + w, saved + gdr_state_bytes(KD, p.vdim) + (vt * 4 + 2 * i + w) * 2048, lane);
     }
     if (64 * c + 64 > len) {
 #pragma unroll

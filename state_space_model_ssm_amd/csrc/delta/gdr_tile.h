@@ -107,18 +107,29 @@ __device__ __forceinline__ bf8 frag16(unsigned tile, int f, int lane) {
 }
 // A D result in two parts, as operands left them in LDS (fragments of 32 rows,
 // high and low part in turn; rows: tokens in D's order, or, PLAIN, key elements
-// in plain order), turned round: lane m stands for row 16 i + m, and its four
-// values for columns 4g .. 4g + 3, half of an operand over 32 columns.  To
-// `to`, this lane's place in a fragment, high and low part.
+// in plain order), turned round: lane m stands for row 16 i + m, its four
+// values for columns 4g .. 4g + 3, half of an operand over 32 columns.
 template <bool PLAIN>
-__device__ __forceinline__ void turn_round(unsigned from, int i, char *to, int lane) {
+__device__ __forceinline__ sh4 turned(unsigned from, int i, int part, int lane) {
   typedef __attribute__((address_space(3))) sh4 lds4;
   const int m = lane & 15, col = 4 * (lane >> 4) + (m >> 2), p = m & 3;
-  const unsigned at = from + (i / 2) * 2048 +
+  const unsigned at = from + (i / 2) * 2048 + part * 1024 +
                       (PLAIN ? (16 * (2 * (i % 2) + (p >> 1)) + col) * 16 + (p & 1) * 8 : (16 * p + col) * 16 + (i % 2) * 8);
+  return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)(at));
+}
+// One half to `to`, this lane's place in a fragment (high and low part in turn).
+template <bool PLAIN>
+__device__ __forceinline__ void turn_half(unsigned from, int i, char *to, int lane) {
+#pragma unroll
+  for (int part = 0; part < 2; ++part) *reinterpret_cast<sh4 *>(to + part * 1024) = turned<PLAIN>(from, i, part, lane);
+}
+// Both halves, of two column tiles.
+template <bool PLAIN>
+__device__ __forceinline__ void turn_both(unsigned first, unsigned second, int i, char *to, int lane) {
 #pragma unroll
   for (int part = 0; part < 2; ++part)
-    *reinterpret_cast<sh4 *>(to + part * 1024) = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)(at + part * 1024));
+    *reinterpret_cast<bf8 *>(to + part * 1024) = __builtin_bit_cast(
+        bf8, __builtin_shufflevector(turned<PLAIN>(first, i, part, lane), turned<PLAIN>(second, i, part, lane), 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
 __device__ __forceinline__ f4v lds_f4(unsigned at) {
