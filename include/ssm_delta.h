@@ -84,10 +84,12 @@ enum { SSM_GDR_STATE_STEP = 64 };
  *   h_last : as h0, nullable: the state after the row's last token (h0 where
  *            there is none); may be exactly h0
  *   states : ssm_gdr_states_size() bytes, 16-byte aligned, nullable: what
- *            ssm_gdr_bwd starts from, the state before every 64th token and the
- *            u_t, in an order of their own; those at or past the row's length
- *            are not written
+ *            ssm_gdr_bwd starts from (the state before every 64th token, the
+ *            u_t, and what of v, g and beta it needs), in an order of its own;
+ *            what is of tokens past a row's last block of 64 is not written
  * The rule is stable for beta |k|^2 below 2: keys are meant to have unit length.
+ * A beta of less than 2^-30 in size counts as that (below the last bit of what
+ * the token adds to a state with its value's size).
  * Tokens are taken 64 at a time: a value that is not finite reaches y from the
  * start of its block of 64 tokens (of its channel, if it is one of v; of the
  * value heads that share it, if it is one of q or k) and what comes after.
@@ -106,16 +108,15 @@ SSM_API int ssm_gdr_fwd(const void *q, const void *k, const void *v, const void 
  *   dg_t = a_t (<dS_t, S_{t-1}> - dv_t.S_{t-1} k_t)
  * dq and dk are summed over the value heads that share a head.  Rows at or
  * past the length get zero gradients.
- *   states : what ssm_gdr_fwd saved for these inputs
+ *   q, k, lengths: as in the forward;  states: what it saved for them
  *   dh_last, dh0: (batch, nheads, vdim, kdim) float32, both nullable
  *   dq, dk : (batch, seqlen, nqk, kdim);  dv, dy: (batch, seqlen, nheads, vdim)
  *   dg, dbeta: (batch, seqlen, nheads) gate_dtype
  */
 SSM_API int ssm_gdr_bwd_workspace_size(const ssm_gdr_dims_t *dims, size_t *bytes);
-SSM_API int ssm_gdr_bwd(const void *q, const void *k, const void *v, const void *g, const void *beta,
-                        const int32_t *lengths, const void *states, const void *dy, const float *dh_last, void *dq,
-                        void *dk, void *dv, void *dg, void *dbeta, float *dh0, const ssm_gdr_dims_t *dims,
-                        void *stream);
+SSM_API int ssm_gdr_bwd(const void *q, const void *k, const int32_t *lengths, const void *states, const void *dy,
+                        const float *dh_last, void *dq, void *dk, void *dv, void *dg, void *dbeta, float *dh0,
+                        const ssm_gdr_dims_t *dims, void *stream);
 
 /*
  * One token per batch row (dims.seqlen must be 1; no workspace): q, k are

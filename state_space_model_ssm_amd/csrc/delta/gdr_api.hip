@@ -142,13 +142,11 @@ int ssm_gdr_bwd_workspace_size(const ssm_gdr_dims_t *dims, size_t *bytes) {
   if (!bytes) return fail(SSM_ERR_NULL, "bytes is NULL");
   const int rc = check_gdr(dims, false);
   if (rc != SSM_OK) return rc;
-  const GdrBwdSizes n = gdr_bwd_sizes(params(*dims));
-  *bytes = n.chunks + n.saved;
+  *bytes = gdr_bwd_workspace(params(*dims));
   return ok();
 }
 
-int ssm_gdr_bwd(const void *q, const void *k, const void *v, const void *g, const void *beta, const int32_t *lengths,
-                const void *states, const void *dy, const float *dh_last, void *dq, void *dk, void *dv, void *dg,
+int ssm_gdr_bwd(const void *q, const void *k, const int32_t *lengths, const void *states, const void *dy, const float *dh_last, void *dq, void *dk, void *dv, void *dg,
                 void *dbeta, float *dh0, const ssm_gdr_dims_t *dims, void *stream) {
   int rc = check_gdr(dims, false);
   if (rc != SSM_OK) return rc;
@@ -156,12 +154,8 @@ int ssm_gdr_bwd(const void *q, const void *k, const void *v, const void *g, cons
   GdrParams p = params(d);
   const size_t eg = dtype_size(d.gate_dtype), rows = static_cast<size_t>(d.batch) * d.seqlen;
   const size_t state = static_cast<size_t>(d.batch) * d.nheads * d.vdim * d.kdim * 4;
-  const GdrBwdSizes n = gdr_bwd_sizes(p);
   const Arg ins[] = {{"q", q, span(d, d.q_batch, d.q_token, d.nqk * d.kdim), 16, true},
                      {"k", k, span(d, d.k_batch, d.k_token, d.nqk * d.kdim), 16, true},
-                     {"v", v, span(d, d.v_batch, d.v_token, d.nheads * d.vdim), 16, true},
-                     {"g", g, rows * d.nheads * eg, eg, true},
-                     {"beta", beta, rows * d.nheads * eg, eg, true},
                      {"lengths", lengths, static_cast<size_t>(d.batch) * 4, 4, false},
                      {"states", states, saved_bytes(d), 16, true},
                      {"dy", dy, rows * d.nheads * d.vdim * 2, 16, true},
@@ -172,14 +166,11 @@ int ssm_gdr_bwd(const void *q, const void *k, const void *v, const void *g, cons
                       {"dbeta", dbeta, rows * d.nheads * eg, eg, true},  {"dh0", dh0, state, 16, false}};
   const void *const same[6][2] = {};
   rc = check_args(ins, outs, same);
-  if (rc == SSM_OK) rc = check_workspace(ins, n.chunks + n.saved);
+  if (rc == SSM_OK) rc = check_workspace(ins, gdr_bwd_workspace(p));
   if (rc != SSM_OK) return rc;
   if (d.batch == 0 || (d.seqlen == 0 && dh0 == nullptr)) return ok();
   p.q = static_cast<const uint16_t *>(q);
   p.k = static_cast<const uint16_t *>(k);
-  p.v = static_cast<const uint16_t *>(v);
-  p.g = g;
-  p.beta = beta;
   p.lengths = lengths;
   p.saved = static_cast<char *>(const_cast<void *>(states));
   p.dy = static_cast<const uint16_t *>(dy);
@@ -190,7 +181,7 @@ int ssm_gdr_bwd(const void *q, const void *k, const void *v, const void *g, cons
   p.dg = dg;
   p.dbeta = dbeta;
   p.dh0 = dh0;
-  p.ws_saved = p.ws + n.chunks;
+  p.ws_both = p.ws;
   return launched(launch_gdr_bwd(p, static_cast<hipStream_t>(stream)), "gdr_bwd");
 }
 

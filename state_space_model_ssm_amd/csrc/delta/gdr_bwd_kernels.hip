@@ -106,7 +106,8 @@ __global__ void __launch_bounds__(256) gdr_bwd_kernel(const GdrParams p) {
   const int64_t hk = h / (p.nheads / p.nqk), yt = p.nheads * p.vdim;
   const uint16_t *kp = p.k + b * p.k_batch + hk * KD, *qp = p.q + b * p.q_batch + hk * KD;
   const uint16_t *dp = p.dy + (b * p.seqlen * p.nheads + h) * p.vdim + vt * NC;
-  const char *ws = p.ws + bh * p.chunks * static_cast<int64_t>(kGdrChunkBytes);  // T^T, A^T, gates
+  const int64_t step = static_cast<int64_t>(gdr_saved_bytes(KD, p.vdim));
+  const char *ws = p.saved + bh * p.chunks * step + gdr_both_bytes(KD, p.vdim);  // T^T, A^T, gates
   uint16_t *vp = p.dv + (b * p.seqlen * p.nheads + h) * p.vdim + col0;
   TileCopy<KD, NT> k_copy, q_copy;
   TileCopy<NC, NT> d_copy;
@@ -123,12 +124,12 @@ __global__ void __launch_bounds__(256) gdr_bwd_kernel(const GdrParams p) {
     d_copy.start(to + kAtD / 16, dp + 64 * c * yt, last, id);
   };
   auto fetch_ws = [&](int c) {
-    copy_share<kOps / 1024, kPairs>(base + (c & 1) * kBuffer + kAtW, ws + c * static_cast<int64_t>(kGdrChunkBytes), w, lane * 16);
+    copy_share<kOps / 1024, kPairs>(base + (c & 1) * kBuffer + kAtW, ws + c * step, w, lane * 16);
   };
   f4v e[4];
   const int64_t nv = p.vdim / 32;
   auto saved = [&](int c) {
-    return p.ws_saved + (bh * p.chunks + c) * static_cast<int64_t>(gdr_saved_bytes(KD, p.vdim)) + lane * 16;
+    return p.ws_both + (bh * p.chunks + c) * static_cast<int64_t>(gdr_both_bytes(KD, p.vdim)) + lane * 16;
   };
   // D = beta E, as operands over the values and as dv.
   auto store = [&](int c) {
@@ -288,10 +289,10 @@ __global__ void __launch_bounds__(256, 2) gdr_grad_kernel(const GdrParams p) {
       const int lane = tid & 63, m = lane & 15, g = lane >> 4;
       const unsigned row = static_cast<unsigned>(slot<64>(m, g >> 1)) * 16 + (g & 1) * 8;
       const int64_t bh = b * p.nheads + h, id = bh * p.chunks + c, yt = p.nheads * VD;
-      const float *gates = reinterpret_cast<const float *>(p.ws + id * static_cast<int64_t>(kGdrChunkBytes) + 2 * kGdrTriBytes);
-      const double *sums = reinterpret_cast<const double *>(gates + 256);
       const char *fs = p.saved + id * static_cast<int64_t>(gdr_saved_bytes(KD, VD)), *fu = fs + gdr_state_bytes(KD, VD);
-      const char *fds = p.ws_saved + id * static_cast<int64_t>(gdr_saved_bytes(KD, VD)), *fd = fds + gdr_state_bytes(KD, VD);
+      const char *fds = p.ws_both + id * static_cast<int64_t>(gdr_both_bytes(KD, VD)), *fd = fds + gdr_state_bytes(KD, VD);
+      const float *gates = reinterpret_cast<const float *>(fs + gdr_both_bytes(KD, VD) + 2 * kGdrTriBytes);
+      const double *sums = reinterpret_cast<const double *>(gates + 256);
       const uint16_t *dyp = p.dy + (b * p.seqlen * p.nheads + h) * VD;
       f4v tq[NE][4], tk[NE][4];  // of the heads before
       if (SHARED)
@@ -524,15 +525,10 @@ hipError_t bwd(const GdrParams &p, hipStream_t s) {
 
 }  // namespace
 
-GdrBwdSizes gdr_bwd_sizes(const GdrParams &p) {
-  const size_t n = static_cast<size_t>(p.batch) * p.nheads * p.chunks;
-  return {n * kGdrChunkBytes, n * gdr_saved_bytes(p.kdim, p.vdim)};
+size_t gdr_bwd_workspace(const GdrParams &p) {
+  return static_cast<size_t>(p.batch) * p.nheads * p.chunks * gdr_both_bytes(p.kdim, p.vdim);
 }
 
-hipError_t launch_gdr_bwd(const GdrParams &p, hipStream_t s) {
-  const hipError_t e = launch_gdr_chunks(p, true, s);
-  if (e != hipSuccess) return e;
-  return p.kdim == 64 ? bwd<64>(p, s) : bwd<128>(p, s);
-}
+hipError_t launch_gdr_bwd(const GdrParams &p, hipStream_t s) { return p.kdim == 64 ? bwd<64>(p, s) : bwd<128>(p, s); }
 
 }  // namespace ssmb

@@ -10,7 +10,7 @@ constexpr int kGdrChunk = 64;
 
 // What is known of a chunk of 64 tokens and a value head before its state is:
 // T = (I + L)^-1 and the attention A within the chunk, as operands in bfloat16
-// parts (see gdr_tile.h), then the gates' factors.  The backward has T^T, A^T.
+// parts (see gdr_tile.h), then the gates' factors.
 constexpr int kGdrFrags = 6;                                   // operands of a triangle: 16 rows x 32 columns each
 constexpr size_t kGdrTriBytes = size_t{2} * kGdrFrags * 1024;  // both parts
 // Factors, 64 of each: scale e^G, e^G, e^(GC - G), beta (float32), and G log2(e) (float64).
@@ -20,7 +20,9 @@ constexpr size_t kGdrChunkBytes = 2 * kGdrTriBytes + kGdrGateBytes;
 // (see gdr_tile.h): the state before it or dS behind it, [16 key elements][32
 // values][part], then U or D = beta E, [32 values][16 tokens][part], 1 KiB each.
 constexpr size_t gdr_state_bytes(int64_t kdim, int64_t vdim) { return static_cast<size_t>(kdim * vdim) * 4; }
-constexpr size_t gdr_saved_bytes(int64_t kdim, int64_t vdim) { return gdr_state_bytes(kdim, vdim) + static_cast<size_t>(64 * vdim) * 4; }
+constexpr size_t gdr_both_bytes(int64_t kdim, int64_t vdim) { return gdr_state_bytes(kdim, vdim) + static_cast<size_t>(64 * vdim) * 4; }
+// What the forward saves: those, T^T, A^T and the factors.
+constexpr size_t gdr_saved_bytes(int64_t kdim, int64_t vdim) { return gdr_both_bytes(kdim, vdim) + kGdrChunkBytes; }
 
 // Long sequences of few heads are cut into segments of `chunks` chunks, and the
 // state at the start of each is found before y is made: with S_0 = 0 and with
@@ -37,14 +39,14 @@ struct GdrParams {
   const int32_t *lengths;      // nullable
   uint16_t *y;
   float *h_last;               // nullable
-  char *saved;                 // gdr_saved_bytes() of S and U per (row, value head, chunk), nullable in the forward
+  char *saved;                 // gdr_saved_bytes() per (row, value head, chunk), nullable in the forward
   char *ws;                    // kGdrChunkBytes per (row, value head, chunk)
   const uint16_t *dy;          // backward
   const float *dh_last;        // nullable
   uint16_t *dq, *dk, *dv;
   void *dg, *dbeta;            // gate dtype
   float *dh0;                  // nullable
-  char *ws_saved;              // the backward's dS and D, as `saved`
+  char *ws_both;               // the backward's dS and D: gdr_both_bytes() each
   GdrSegments seg;
   float *ws_state;             // (row, value head, segment): E, and then the state before the segment
   uint16_t *ws_carry;          // (row, value head, segment, part): P, (kdim in, kdim out)
@@ -58,12 +60,7 @@ struct GdrSizes {
   size_t chunks, state, carry;
 };
 GdrSizes gdr_sizes(const GdrParams &p);
-// Sizes of the backward's workspace: ws and ws_saved in turn.
-struct GdrBwdSizes {
-  size_t chunks, saved;
-};
-GdrBwdSizes gdr_bwd_sizes(const GdrParams &p);
-hipError_t launch_gdr_chunks(const GdrParams &p, bool bwd, hipStream_t stream);
+size_t gdr_bwd_workspace(const GdrParams &p);
 hipError_t launch_gdr_bwd(const GdrParams &p, hipStream_t stream);
 hipError_t launch_gdr_fwd(const GdrParams &p, hipStream_t stream);
 hipError_t launch_gdr_step(const GdrParams &p, hipStream_t stream);  // h0 -> h_last

@@ -22,9 +22,10 @@ __device__ __forceinline__ void store_rows(const f4v (&t)[W + 1], u4 *to, int la
 }
 
 // One workgroup per chunk and value head, one wavefront per 16 of its tokens.
-template <int KD, typename G, bool BWD>
+// SAVE: also T^T and A^T, which the backward needs.
+template <int KD, typename G, bool SAVE>
 __global__ void __launch_bounds__(256) gdr_chunk_kernel(const GdrParams p) {
-  __shared__ __align__(16) float full[BWD ? 64 * kPitch : 4], inv[BWD ? 64 * kPitch : 4];  // A and T
+  __shared__ __align__(16) float full[SAVE ? 64 * kPitch : 4], inv[SAVE ? 64 * kPitch : 4];  // A and T
   __shared__ double sums[64];                       // log2 of the decay up to each token
   __shared__ float betas[64];
   __shared__ __align__(16) float low[64 * kPitch];  // L^T
@@ -35,6 +36,7 @@ __global__ void __launch_bounds__(256) gdr_chunk_kernel(const GdrParams p) {
   const int t0 = static_cast<int>(c) * 64, len = gdr_length(p.lengths, b, p.seqlen) - t0;
   if (len <= 0) return;
   char *ws = p.ws + id * static_cast<int64_t>(kGdrChunkBytes);
+  const int64_t kept_bytes = static_cast<int64_t>(gdr_saved_bytes(KD, p.vdim));
   constexpr int NS = KD / 32;
   const int64_t hk = h / (p.nheads / p.nqk);
   const uint16_t *kp = p.k + b * p.k_batch + t0 * p.k_token + hk * KD + 8 * g;
@@ -74,7 +76,12 @@ __global__ void __launch_bounds__(256) gdr_chunk_kernel(const GdrParams p) {
     gates[64 + lane] = into;
     gates[128 + lane] = __builtin_amdgcn_exp2f(static_cast<float>(last - s));
     gates[192 + lane] = bt;
-    if (BWD) reinterpret_cast<double *>(gates + 256)[lane] = s;
+    if (SAVE) {
+      float *kept = reinterpret_cast<float *>(p.saved + id * kept_bytes + gdr_both_bytes(KD, p.vdim) + 2 * kGdrTriBytes);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) kept[64 * k + lane] = gates[64 * k + lane];
+      reinterpret_cast<double *>(kept + 256)[lane] = s;
+    }
   }
   __syncthreads();
   u4 *out = reinterpret_cast<u4 *>(ws);
@@ -101,10 +108,10 @@ __global__ void __launch_bounds__(256) gdr_chunk_kernel(const GdrParams p) {
         const int j = 16 * jb + 4 * g + r;
         const float decay = j <= i ? __builtin_amdgcn_exp2f(static_cast<float>(si - sums[j])) : 0.0f;
         att[jb][r] = j <= i && i < len ? att[jb][r] * decay * p.scale : 0.0f;
-        if (BWD) full[i * kPitch + j] = att[jb][r];
+        if (SAVE) full[i * kPitch + j] = att[jb][r];
         low[j * kPitch + i] = j < i ? kk[jb][r] * decay * bi : 0.0f;
       }
-    if (!BWD) store_rows<W>(att, out + kGdrTriBytes / 16, lane);
+    store_rows<W>(att, out + kGdrTriBytes / 16, lane);
   });
   __syncthreads();
   // Blocks on the diagonal, all in one wavefront: lane (block g, column m) by substitution.
@@ -147,15 +154,16 @@ __global__ void __launch_bounds__(256) gdr_chunk_kernel(const GdrParams p) {
 #pragma unroll
       for (int r = 0; r < 4; ++r) t[j] = mfma_f32(-d[r], acc[r], t[j]);
     }
-    if (!BWD) store_rows<W>(t, out, lane);
-    if (BWD)
+    store_rows<W>(t, out, lane);
+    if (SAVE)
 #pragma unroll
       for (int jb = 0; jb <= W; ++jb) *reinterpret_cast<f4v *>(inv + i * kPitch + 16 * jb + 4 * g) = t[jb];
   });
-  if (BWD) {
+  if (SAVE) {
+    u4 *kept = reinterpret_cast<u4 *>(p.saved + id * kept_bytes + gdr_both_bytes(KD, p.vdim));
     __syncthreads();
-    store_cols(inv, w, out, lane);
-    store_cols(full, w, out + kGdrTriBytes / 16, lane);
+    store_cols(inv, w, kept, lane);
+    store_cols(full, w, kept + kGdrTriBytes / 16, lane);
   }
 }
 
@@ -585,15 +593,16 @@ __global__ void __launch_bounds__(256) gdr_step_kernel(const GdrParams p) {
 }
 
 template <int KD, typename G>
-void chunks(const GdrParams &p, bool bwd, hipStream_t s) {
+void chunks(const GdrParams &p, hipStream_t s) {
   const dim3 n(static_cast<uint32_t>(p.batch * p.nheads * p.chunks));
-  if (bwd) hipLaunchKernelGGL((gdr_chunk_kernel<KD, G, true>), n, dim3(256), 0, s, p);
+  if (p.saved != nullptr) hipLaunchKernelGGL((gdr_chunk_kernel<KD, G, true>), n, dim3(256), 0, s, p);
   else hipLaunchKernelGGL((gdr_chunk_kernel<KD, G, false>), n, dim3(256), 0, s, p);
 }
 
 template <int KD>
 hipError_t fwd(const GdrParams &p, hipStream_t s) {
   const int64_t heads = p.batch * p.nheads;
+  if (p.chunks > 0) p.gates_bf16 ? chunks<KD, uint16_t>(p, s) : chunks<KD, float>(p, s);
   if (p.seg.count > 1) {
     const int64_t parts = heads * (p.seg.count - 1) * ((p.vdim + KD) / 64);
     hipLaunchKernelGGL((gdr_segment_kernel<KD>), dim3(static_cast<uint32_t>(parts)), dim3(256), 0, s, p);
@@ -639,18 +648,7 @@ GdrSizes gdr_sizes(const GdrParams &p) {
   return {heads * p.chunks * kGdrChunkBytes, n * p.vdim * p.kdim * 4, n * 2 * p.kdim * p.kdim * 2};
 }
 
-hipError_t launch_gdr_chunks(const GdrParams &p, bool bwd, hipStream_t s) {
-  if (p.chunks == 0) return hipSuccess;
-  if (p.kdim == 64) p.gates_bf16 ? chunks<64, uint16_t>(p, bwd, s) : chunks<64, float>(p, bwd, s);
-  else p.gates_bf16 ? chunks<128, uint16_t>(p, bwd, s) : chunks<128, float>(p, bwd, s);
-  return hipGetLastError();
-}
-
-hipError_t launch_gdr_fwd(const GdrParams &p, hipStream_t s) {
-  const hipError_t e = launch_gdr_chunks(p, false, s);
-  if (e != hipSuccess) return e;
-  return p.kdim == 64 ? fwd<64>(p, s) : fwd<128>(p, s);
-}
+hipError_t launch_gdr_fwd(const GdrParams &p, hipStream_t s) { return p.kdim == 64 ? fwd<64>(p, s) : fwd<128>(p, s); }
 
 hipError_t launch_gdr_step(const GdrParams &p, hipStream_t s) {
   if (p.kdim == 64) return p.gates_bf16 ? step<64, uint16_t>(p, s) : step<64, float>(p, s);

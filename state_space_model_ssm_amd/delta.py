@@ -74,7 +74,7 @@ def delta_lib():
                 "(hipcc, gfx950). There is no fallback implementation.")
         L = ctypes.CDLL(_LIB_PATH)
         vp, size = ctypes.c_void_p, ctypes.POINTER(ctypes.c_size_t)
-        for name, pointers, dims in (("ssm_gdr_fwd", 10, GdrDims), ("ssm_gdr_bwd", 15, GdrDims), ("ssm_gdr_step", 8, GdrDims),
+        for name, pointers, dims in (("ssm_gdr_fwd", 10, GdrDims), ("ssm_gdr_bwd", 12, GdrDims), ("ssm_gdr_step", 8, GdrDims),
                                      ("ssm_qk_norm_fwd", 8, QkNormDims), ("ssm_qk_norm_bwd", 12, QkNormDims),
                                      ("ssm_swa_q8_step", 11, SwaDims), ("ssm_swa_q8_fill", 9, SwaDims)):
             f = getattr(L, name)
@@ -188,8 +188,8 @@ def gdr_fwd(q, k, v, g, beta, *, h0=None, lengths=None, scale=None, return_h_las
     int32 or None; rows past a length may hold anything and give zeros.  scale
     defaults to kdim ** -0.5.  Returns ``(y, h_last)``, and with
     ``return_states`` also what ``gdr_bwd`` starts from, a uint8 tensor of
-    ``gdr_states_size`` bytes (the states before every 64th token and the u_t:
-    per value head and 64 tokens, 4 vdim (kdim + 64) bytes).  h_last
+    ``gdr_states_size`` bytes (per value head and 64 tokens 4 vdim (kdim + 64)
+    + 26624: the state before them and what is needed of v, g and beta).  h_last
     (float32, after each row's last token) may be h0 itself.
     """
     _one_device(stream, q, k, v, g, beta, h0, lengths, workspace)
@@ -213,7 +213,8 @@ def gdr_bwd(q, k, v, g, beta, states, dy, *, dh_last=None, lengths=None, scale=N
             workspace=None, stream=None):
     """Backward of ``gdr_fwd`` (``ssm_gdr_bwd``) from what it saved and
     the gradients of y (v's shape, bfloat16) and of h_last ((batch, nheads,
-    vdim, kdim) float32 or None).  Returns ``(dq, dk, dv, dg, dbeta, dh0)``:
+    vdim, kdim) float32 or None); of v, g and beta it takes the shapes and
+    types, their values being in what was saved.  Returns ``(dq, dk, dv, dg, dbeta, dh0)``:
     dense, shaped and typed like q, k, v, g and beta; dh0 float32 (None without
     return_dh0).  ``out``: a dict of preallocated outputs under those names.
     """
@@ -230,8 +231,7 @@ def gdr_bwd(q, k, v, g, beta, states, dy, *, dh_last=None, lengths=None, scale=N
                              for n, t in (("dq", q), ("dk", k), ("dv", v), ("dg", g), ("dbeta", beta)))
     dh0 = _out(o.get("dh0"), state, _F32, q, "dh0", stream) if return_dh0 else None
     workspace = _scratch(dims, gdr_bwd_workspace_size(dims), workspace, q, stream)
-    _check(delta_lib().ssm_gdr_bwd(_at(q), _at(k), _at(v), _ptr(g), _ptr(beta), _ptr(lengths), _ptr(states), _ptr(dy),
-                                   _ptr(dh_last), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dg), _ptr(dbeta), _ptr(dh0),
+    _check(delta_lib().ssm_gdr_bwd(_at(q), _at(k), _ptr(lengths), _ptr(states), _ptr(dy), _ptr(dh_last), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dg), _ptr(dbeta), _ptr(dh0),
                                    ctypes.byref(dims), _stream(stream)))
     return dq, dk, dv, dg, dbeta, dh0
 

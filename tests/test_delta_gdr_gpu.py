@@ -96,7 +96,7 @@ def test_forward(B, L, nqk, H, K, V, gates, with_h0, lengths):
     cg, cb, ch = cuda(g, beta, h0)
     chunks = -(-L // 64)
     y, hl = nan((B, L, H, V), BF16), nan((B, H, V, K))
-    st = torch.full((B * H * chunks * 4 * V * (K + 64),), 0xff, dtype=torch.uint8, device="cuda")   # NaN
+    st = torch.full((B * H * chunks * (4 * V * (K + 64) + 26624),), 0xff, dtype=torch.uint8, device="cuda")   # NaN
     got = ssm.gdr_fwd(cq, ck, cv, cg, cb, h0=ch, lengths=None if lens is None else lens.cuda(), return_states=True, y=y,
                       h_last=hl, states=st)
     assert got[0] is y and got[1] is hl and got[2] is st
@@ -139,7 +139,7 @@ def test_backward(B, L, nqk, H, K, V, gates, with_h0, lengths):
     cl = None if lens is None else lens.cuda()
     views = one_tensor(q, k, v)
     cg, cb, ch, cdy, cdh = cuda(g, beta, h0, dy, dh)
-    states = torch.full((B * H * -(-L // 64) * 4 * V * (K + 64),), 0xff, dtype=torch.uint8, device="cuda")   # NaN
+    states = torch.full((B * H * -(-L // 64) * (4 * V * (K + 64) + 26624),), 0xff, dtype=torch.uint8, device="cuda")   # NaN
     ssm.gdr_fwd(*views, cg, cb, h0=ch, lengths=cl, states=states)
     outs = {n: nan(t.shape, t.dtype) for n, t in (("dq", q), ("dk", k), ("dv", v), ("dg", g), ("dbeta", beta))}
     outs["dh0"] = nan((B, H, V, K))
