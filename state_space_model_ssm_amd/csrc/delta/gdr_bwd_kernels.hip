@@ -128,14 +128,15 @@ __global__ void __launch_bounds__(256) gdr_bwd_kernel(const GdrParams p) {
   };
   f4v e[4];
   const int64_t nv = p.vdim / 32;
-  auto saved = [&](int c) {
+  auto both = [&](int c) {
     return p.ws_both + (bh * p.chunks + c) * static_cast<int64_t>(gdr_both_bytes(KD, p.vdim)) + lane * 16;
   };
-  // D = beta E, as operands over the values and as dv.
-  auto store = [&](int c) {
+  // D = beta E: dv, and operands over the values, of which this column tile has halves.
+  sh4 dt[4][2];
+  auto turn = [&](int c) {
     const unsigned beta = base + (c & 1) * kBuffer + kAtW + kTri + 768 + 16 * g;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) e[i] *= lds_f4(beta + 64 * i);
+    for (int i = 0; i < 4; ++i) e[i] = *(const lds_f4v *)(four + i * 1024) * lds_f4(beta + 64 * i);
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       const Parts d = parts(e[2 * k], e[2 * k + 1]);
@@ -145,7 +146,8 @@ __global__ void __launch_bounds__(256) gdr_bwd_kernel(const GdrParams p) {
     wait_reads();
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      turn_half<false>(four - lane * 16, i, saved(c) + gdr_state_bytes(KD, p.vdim) + (vt * 4 + i) * 2048 + w * 8, lane);
+#pragma unroll
+      for (int part = 0; part < 2; ++part) dt[i][part] = turned<false>(four - lane * 16, i, part, lane);
     if (64 * c + 64 > len) {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
@@ -153,6 +155,13 @@ __global__ void __launch_bounds__(256) gdr_bwd_kernel(const GdrParams p) {
         for (int r = 0; r < 4; ++r)
           if (64 * c + 16 * i + 4 * g + r >= len) e[i][r] = 0.0f;
     }
+  };
+  auto store = [&](int c) {
+    char *to = both(c) + gdr_state_bytes(KD, p.vdim) + vt * 8192 + w * 8;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int part = 0; part < 2; ++part) __builtin_nontemporal_store(dt[i][part], reinterpret_cast<sh4 *>(to + i * 2048 + part * 1024));
     const int64_t rest = p.seqlen - 64 * static_cast<int64_t>(c);
     v_store.put(vp + 64 * c * yt, rest < 64 ? static_cast<int>(rest) : 64, e);
   };
@@ -162,6 +171,15 @@ __global__ void __launch_bounds__(256) gdr_bwd_kernel(const GdrParams p) {
   }
   for (int c = n - 1; c >= 0; --c) {
     arrive();
+    if (c + 1 < n) store(c + 1);
+    // dS behind the chunk, half of both columns' tiles by each of the two wavefronts.
+    const unsigned all = base + 2 * kBuffer + kPairs * kFour;
+    char *to = both(c) + vt * 2048;
+#pragma unroll
+    for (int j = 0; j < NB / 2; ++j)
+#pragma unroll
+      for (int part = 0; part < 2; ++part)
+        *reinterpret_cast<bf8 *>(to + (2 * j + w) * nv * 2048 + part * 1024) = turned<true>(all, all + kState, 2 * j + w, part, lane);
     const unsigned tile = base + (c & 1) * kBuffer, at_a = tile + kAtW + kGdrTriBytes, gates = at_a + kGdrTriBytes + 16 * g;
     Parts af[kGdrFrags];
     sh4 dy[4];
@@ -184,11 +202,6 @@ __global__ void __launch_bounds__(256) gdr_bwd_kernel(const GdrParams p) {
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) *(lds_f4v *)(four + i * 1024) = x[i];
-    // dS behind the chunk, half of both columns' tiles by each of the two wavefronts.
-    const unsigned all = base + 2 * kBuffer + kPairs * kFour;
-#pragma unroll
-    for (int j = 0; j < NB / 2; ++j)
-      turn_both<true>(all, all + kState, 2 * j + w, saved(c) + ((2 * j + w) * nv + vt) * 2048, lane);
     meet();
     if (c > 0) fetch_rows(c - 1);
     f4v z[NB] = {};
@@ -208,11 +221,10 @@ __global__ void __launch_bounds__(256) gdr_bwd_kernel(const GdrParams p) {
 #pragma unroll
     for (int j = 0; j < NB; ++j) *(lds_f4v *)(grown + j * 1024) = z[j];
     meet();
-#pragma unroll
-    for (int i = 0; i < 4; ++i) e[i] = *(const lds_f4v *)(four + i * 1024);
     if (c > 0) fetch_ws(c - 1);
-    store(c);
+    turn(c);
   }
+  if (n > 0) store(0);
   for (int64_t row = 64 * static_cast<int64_t>(n) + g; row < p.seqlen; row += 4) st(vp, row * yt + m, 0.0f);
 }
 

@@ -117,19 +117,11 @@ __device__ __forceinline__ sh4 turned(unsigned from, int i, int part, int lane) 
                       (PLAIN ? (16 * (2 * (i % 2) + (p >> 1)) + col) * 16 + (p & 1) * 8 : (16 * p + col) * 16 + (i % 2) * 8);
   return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)(at));
 }
-// One half to `to`, this lane's place in a fragment (high and low part in turn).
-template <bool PLAIN>
-__device__ __forceinline__ void turn_half(unsigned from, int i, char *to, int lane) {
-#pragma unroll
-  for (int part = 0; part < 2; ++part) *reinterpret_cast<sh4 *>(to + part * 1024) = turned<PLAIN>(from, i, part, lane);
-}
 // Both halves, of two column tiles.
 template <bool PLAIN>
-__device__ __forceinline__ void turn_both(unsigned first, unsigned second, int i, char *to, int lane) {
-#pragma unroll
-  for (int part = 0; part < 2; ++part)
-    *reinterpret_cast<bf8 *>(to + part * 1024) = __builtin_bit_cast(
-        bf8, __builtin_shufflevector(turned<PLAIN>(first, i, part, lane), turned<PLAIN>(second, i, part, lane), 0, 1, 2, 3, 4, 5, 6, 7));
+__device__ __forceinline__ bf8 turned(unsigned first, unsigned second, int i, int part, int lane) {
+  return __builtin_bit_cast(bf8, __builtin_shufflevector(turned<PLAIN>(first, i, part, lane), turned<PLAIN>(second, i, part, lane),
+                                                         0, 1, 2, 3, 4, 5, 6, 7));
 }
 
 __device__ __forceinline__ f4v lds_f4(unsigned at) {
