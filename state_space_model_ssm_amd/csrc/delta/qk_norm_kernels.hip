@@ -249,19 +249,22 @@ __global__ void __launch_bounds__(256) qk_norm_bwd_kernel(const QkNormParams p) 
     }
 }
 
-// dw = the sum over the workgroups' terms: 16 columns by 16 threads of a share each.
-__global__ void __launch_bounds__(256) qk_norm_sum_kernel(const QkNormParams p, int parts) {
-  __shared__ float sums[16][17];
+// dw = the sum over the workgroups' terms: 16 columns by 64 threads of a share each.
+__global__ void __launch_bounds__(1024) qk_norm_sum_kernel(const QkNormParams p, int parts) {
+  __shared__ float sums[64][17];
   const int c = threadIdx.x % 16, k = threadIdx.x / 16, col = blockIdx.x * 16 + c;
   const int64_t step = 2 * p.headdim;
   float sum = 0.0f;
-  for (int i = k; i < parts; i += 16) sum += p.ws[i * step + col];
+  for (int i = k; i < parts; i += 64) sum += p.ws[i * step + col];
   sums[k][c] = sum;
   __syncthreads();
-  if (k != 0) return;
+  if (k >= 4) return;
   sum = 0.0f;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) sum += sums[i][c];
+  for (int i = 0; i < 16; ++i) sum += sums[16 * k + i][c];
+  sum += __shfl_down(sum, 32);
+  sum += __shfl_down(sum, 16);
+  if (k != 0) return;
   float *to = col < p.headdim ? p.dwq : p.dwk;
   if (to != nullptr) to[col % p.headdim] = sum;
 }
@@ -313,7 +316,7 @@ hipError_t launch_qk_norm_bwd(const QkNormParams &p0, int bf16, hipStream_t s) {
   const int parts = static_cast<int>(qk_norm_parts(p.tokens));
   if (parts > 0) bf16 ? run<uint16_t>(p, true, static_cast<unsigned>(parts), s) : run<float>(p, true, static_cast<unsigned>(parts), s);
   if (p.ws != nullptr)
-    hipLaunchKernelGGL(qk_norm_sum_kernel, dim3(static_cast<uint32_t>(2 * p.headdim / 16)), dim3(256), 0, s, p, parts);
+    hipLaunchKernelGGL(qk_norm_sum_kernel, dim3(static_cast<uint32_t>(2 * p.headdim / 16)), dim3(1024), 0, s, p, parts);
   return hipGetLastError();
 }
 

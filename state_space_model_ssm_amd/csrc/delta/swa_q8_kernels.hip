@@ -129,7 +129,7 @@ __device__ __forceinline__ void store_block(const uint16_t *near, const uint16_t
 }
 
 template <int D>
-__global__ void __launch_bounds__(256) swa_q8_step_kernel(const SwaStepParams p, const SwaQ8Cache cache, unsigned splits,
+__global__ void __launch_bounds__(256, 2) swa_q8_step_kernel(const SwaStepParams p, const SwaQ8Cache cache, unsigned splits,
                                                           unsigned qblocks) {
   constexpr int CH = D / 8, NB = D / 32, NS = D / 16, kNear = 32;
   constexpr int kCopies = D / 16;  // copies of 1 KiB per tile, of either kind
@@ -138,7 +138,10 @@ __global__ void __launch_bounds__(256) swa_q8_step_kernel(const SwaStepParams p,
   const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const unsigned nkv = static_cast<unsigned>(p.nkv), group = static_cast<unsigned>(p.nheads) / nkv;
-  const unsigned split = blockIdx.x % splits, rest = blockIdx.x / splits, qb = rest % qblocks, bc = rest / qblocks;
+  // Workgroups of a (row, key head): `splits` for each block of 32 heads, and
+  // one that stores the near block in the ring if it has become whole.
+  const unsigned each_row = splits * qblocks + 1, bc = blockIdx.x / each_row, rest = blockIdx.x % each_row;
+  const unsigned split = rest % splits, qb = rest / splits;
   const int64_t b = bc / nkv, c = bc % nkv;
   const int g0 = qb * 32, heads = static_cast<int>(group) - g0 < 32 ? static_cast<int>(group) - g0 : 32;
   const int sinks = static_cast<int>(p.sinks), blocks = static_cast<int>(p.window / kSwaBlock);
@@ -150,6 +153,16 @@ __global__ void __launch_bounds__(256) swa_q8_step_kernel(const SwaStepParams p,
   const uint16_t *kn = p.k + b * p.k_batch + c * D, *vn = p.v + b * p.v_batch + c * D;
   uint16_t *near_k = cache.k_near + static_cast<int64_t>(bc) * (sinks + kSwaBlock) * D;
   uint16_t *near_v = cache.v_near + static_cast<int64_t>(bc) * (sinks + kSwaBlock) * D;
+  if (qb == qblocks) {
+    if (pos < sinks || off != 63) return;
+    // (No other workgroup reads the block of the ring that it replaces, nor writes what is near but the token's own place.)
+    const int64_t to = static_cast<int64_t>(bc) * blocks + now % blocks;
+    if (wave == 0)
+      store_block<D>(near_k + static_cast<int64_t>(sinks) * D, kn, cache.k_ring + to * kSwaBlock * D, cache.k_scale + to, lane);
+    else if (wave == 1)
+      store_block<D>(near_v + static_cast<int64_t>(sinks) * D, vn, cache.v_ring + to * kSwaBlock * D, cache.v_scale + to, lane);
+    return;
+  }
   f16v o[NB] = {};
   float top = -INFINITY, sum = 0.0f;
   if (pos >= 0) {
@@ -186,13 +199,13 @@ __global__ void __launch_bounds__(256) swa_q8_step_kernel(const SwaStepParams p,
       float k_scale = 0.0f, v_scale = 0.0f;  // lane l: those of tile i + l, for every 64th i
       for (int i = lo; i < hi; ++i) {
         if (((i - lo) & 63) == 0) {
-          const int mine = i + lane < hi ? i + lane : hi - 1;
-          k_scale = mine < near_tiles ? 1.0f : cache.k_scale[scales + block_of(mine)];
-          v_scale = mine < near_tiles ? 1.0f : cache.v_scale[scales + block_of(mine)];
           if (i == lo) {
             load(kt, near_k, cache.k_ring, i);
             load(vt, near_v, cache.v_ring, i);
           }
+          const int mine = i + lane < hi ? i + lane : hi - 1;
+          k_scale = mine < near_tiles ? 1.0f : cache.k_scale[scales + block_of(mine)];
+          v_scale = mine < near_tiles ? 1.0f : cache.v_scale[scales + block_of(mine)];
         }
         const float ks = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(k_scale), (i - lo) & 63));
         const float vs = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v_scale), (i - lo) & 63));
@@ -266,15 +279,6 @@ __global__ void __launch_bounds__(256) swa_q8_step_kernel(const SwaStepParams p,
       }
     }
     sum += other_half(sum);
-    // The near block is whole: it takes its place in the ring, of which no
-    // workgroup reads the block there.
-    if (off == 63 && spot >= 0 && split == 0 && qb == 0 && wave < 2) {
-      const int64_t to = now % blocks;
-      if (wave == 0)
-        store_block<D>(near_k + static_cast<int64_t>(sinks) * D, kn, cache.k_ring + ring + to * kSwaBlock * D, cache.k_scale + scales + to, lane);
-      else
-        store_block<D>(near_v + static_cast<int64_t>(sinks) * D, vn, cache.v_ring + ring + to * kSwaBlock * D, cache.v_scale + scales + to, lane);
-    }
   }
   join_waves<D>(p, lds, o, top, sum, tops, sums, heads, b * p.nheads + c * group + g0, splits, split);
 }
@@ -347,7 +351,7 @@ int swa_q8_splits(int64_t batch, int64_t nheads, int64_t nkv, int64_t window, in
 
 hipError_t launch_swa_q8_step(const SwaStepParams &p, const SwaQ8Cache &cache, int splits, hipStream_t s) {
   const unsigned qblocks = static_cast<unsigned>((p.nheads / p.nkv + 31) / 32), sp = static_cast<unsigned>(splits);
-  const dim3 g(static_cast<uint32_t>(p.batch * p.nkv * qblocks * splits)), gj(static_cast<uint32_t>(p.batch * p.nheads));
+  const dim3 g(static_cast<uint32_t>(p.batch * p.nkv * (qblocks * splits + 1))), gj(static_cast<uint32_t>(p.batch * p.nheads));
   if (p.headdim == 64) {
     hipLaunchKernelGGL((swa_q8_step_kernel<64>), g, dim3(256), 0, s, p, cache, sp, qblocks);
     if (splits > 1) hipLaunchKernelGGL((swa_join_kernel<64>), gj, dim3(64), 0, s, p, splits);
