@@ -232,13 +232,6 @@ __global__ void __launch_bounds__(256) gdr_bwd_kernel(const GdrParams p) {
 // Within a chunk: dq, dk, dg, dbeta
 // ---------------------------------------------------------------------------
 
-// Operand of the elements 16 ct + m of a row-major tile, k its rows 32 s .. in D's order.
-template <int D>
-__device__ __forceinline__ bf8 elems16(unsigned tile, int ct, int s, int lane) {
-  return __builtin_bit_cast(bf8, __builtin_shufflevector(rows4<D>(tile, 2 * s, ct, lane), rows4<D>(tile, 2 * s + 1, ct, lane), 0,
-                                                         1, 2, 3, 4, 5, 6, 7));
-}
-
 // The sum over the 16 lanes of a row.
 __device__ __forceinline__ float sum16(float v) {
   v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0xB1, 0xf, 0xf, true));

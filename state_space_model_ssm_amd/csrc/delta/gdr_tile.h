@@ -297,6 +297,13 @@ struct RowStore {
   }
 };
 
+// Operand of the elements 16 ct + m of a row-major tile, k its rows 32 s .. in D's order.
+template <int D>
+__device__ __forceinline__ bf8 elems16(unsigned tile, int ct, int s, int lane) {
+  return __builtin_bit_cast(bf8, __builtin_shufflevector(rows4<D>(tile, 2 * s, ct, lane), rows4<D>(tile, 2 * s + 1, ct, lane), 0,
+                                                         1, 2, 3, 4, 5, 6, 7));
+}
+
 __device__ __forceinline__ float up(short v) {
   return __uint_as_float(static_cast<unsigned>(static_cast<uint16_t>(v)) << 16);
 }

@@ -13,6 +13,7 @@
 // multiply the scores and the weights, in float32.
 #include "block/swa_step.h"
 #include "delta_internal.h"
+#include "gdr_tile.h"
 
 namespace ssmb {
 namespace {
@@ -43,20 +44,20 @@ __device__ __forceinline__ int chunk8(int r, int c) {
   else return c ^ ((r >> 2) & 3);
 }
 
-// Operand of keys 32 base .. + 31 (lane % 32), elements 16 s + 8 h ..
+// Operand of keys 16 i .. (lane m), elements 32 a + 8g ..
 template <int D>
-__device__ __forceinline__ bf8 row8(const u4 *tile, int base, int s, int lane) {
+__device__ __forceinline__ bf8 keys16(const u4 *tile, int i, int a, int lane) {
   typedef __attribute__((address_space(3))) const i2 lds8;
-  const int r = 32 * base + (lane & 31);
-  return widen(*(lds8 *)(lds_at(tile) + r * D + chunk8<D>(r, s) * 16 + (lane >> 5) * 8));
+  const int r = 16 * i + (lane & 15), g = lane >> 4;
+  return widen(*(lds8 *)(lds_at(tile) + r * D + chunk8<D>(r, 2 * a + (g >> 1)) * 16 + (g & 1) * 8));
 }
-// Operand of elements 32 db + lane % 32 over keys 16 ks .., in the order of a D result.
+// Operand of elements 16 e + m over keys 32 s .. in the order of a D result.
 template <int D>
-__device__ __forceinline__ bf8 col8(const u4 *tile, int ks, int db, int lane) {
+__device__ __forceinline__ bf8 values16(const u4 *tile, int s, int e, int lane) {
   typedef __attribute__((address_space(3))) i2 lds8;
-  const int i = lane & 15, g = (lane >> 4) & 1, h = lane >> 5;
-  const int r = 16 * ks + 8 * (i >> 3) + 4 * h + ((i >> 1) & 3);
-  return widen(__builtin_amdgcn_ds_read_tr8_b64_v2i32((lds8 *)(lds_at(tile) + r * D + chunk8<D>(r, 2 * db + g) * 16 + (i & 1) * 8)));
+  const int i = lane & 15, g = lane >> 4, k = i >> 1;  // lanes 2 k and 2 k + 1 read key k of the group's eight
+  const int r = 32 * s + 16 * (k >> 2) + 4 * g + (k & 3);
+  return widen(__builtin_amdgcn_ds_read_tr8_b64_v2i32((lds8 *)(lds_at(tile) + r * D + chunk8<D>(r, e) * 16 + (i & 1) * 8)));
 }
 // Start the copy of a block of the ring.
 template <int D>
@@ -128,22 +129,72 @@ __device__ __forceinline__ void store_block(const uint16_t *near, const uint16_t
   if (lane == 0) *scale = s;
 }
 
+// The value of the lane 16 away within its 32.
+__device__ __forceinline__ float other_row(float v) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float((threadIdx.x & 16) ? r[0] : r[1]);
+}
+
+// Weights as two operands whose sum they are to 2^-16: cut off after 8 bits, and
+// what that leaves, held above 0, so that both times an infinity have its sign.
+__device__ __forceinline__ void two_parts(const f4v &lo, const f4v &hi, bf8 &cut, bf8 &rest) {
+  u4 c;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float a = k < 2 ? lo[2 * (k % 2)] : hi[2 * (k % 2)], b = k < 2 ? lo[2 * (k % 2) + 1] : hi[2 * (k % 2) + 1];
+    const unsigned ca = __float_as_uint(a) & 0xffff0000u, cb = __float_as_uint(b) & 0xffff0000u;
+    c[k] = ca >> 16 | cb;
+    rest[2 * k] = static_cast<__bf16>(fmaxf(a - __uint_as_float(ca), 0x1p-100f));
+    rest[2 * k + 1] = static_cast<__bf16>(fmaxf(b - __uint_as_float(cb), 0x1p-100f));
+  }
+  cut = __builtin_bit_cast(bf8, c);
+}
+
+// Scores of 64 keys for the lane's head -> weights 2^(c2 s - top), with the
+// running maximum and sum of this lane's quarter of the keys, and o, as
+// to_weights() in swa_tile.h.
+template <int NB>
+__device__ __forceinline__ void weigh(f4v (&s)[4], float c2, f4v (&o)[NB], float &top, float &sum) {
+  float m = s[0][0];
+#pragma unroll
+  for (int r = 1; r < 16; ++r) m = fmaxf(m, s[r / 4][r % 4]);
+  m = fmaxf(m, other_row(m));
+  m = fmaxf(m, other_half(m)) * c2;
+  if (__any(m > top + kSlack)) {
+    const float now = m > top + kSlack ? m : top;
+    const float keep = now == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(top - now);
+    sum *= keep;
+#pragma unroll
+    for (int e = 0; e < NB; ++e) o[e] *= keep;
+    top = now;
+  }
+  const float off = top == -INFINITY ? 0.0f : top;
+  float part[2] = {};
+#pragma unroll
+  for (int r = 0; r < 16; ++r) {
+    s[r / 4][r % 4] = __builtin_amdgcn_exp2f(fmaf(s[r / 4][r % 4], c2, -off));
+    part[r & 1] += s[r / 4][r % 4];
+  }
+  sum += part[0] + part[1];
+}
+
+// Heads that share a key head, 16 at a time, as columns.
 template <int D>
 __global__ void __launch_bounds__(256, 2) swa_q8_step_kernel(const SwaStepParams p, const SwaQ8Cache cache, unsigned splits,
-                                                          unsigned qblocks) {
-  constexpr int CH = D / 8, NB = D / 32, NS = D / 16, kNear = 32;
+                                                             unsigned qblocks) {
+  constexpr int CH = D / 8, NB = D / 16, NS = D / 32, kNear = 32;
   constexpr int kCopies = D / 16;  // copies of 1 KiB per tile, of either kind
-  __shared__ __align__(16) u4 lds[4][2][kSwaBlock * D / 16];  // wavefront, K or V; in the end o, [32][D] float32
-  __shared__ float tops[4][32], sums[4][32];
-  const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
+  __shared__ __align__(16) u4 lds[4][2][kSwaBlock * D / 16];  // wavefront, K or V; in the end o, [16][D] float32
+  __shared__ float tops[4][16], sums[4][16];
+  const int tid = threadIdx.x, lane = tid & 63, m = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const unsigned nkv = static_cast<unsigned>(p.nkv), group = static_cast<unsigned>(p.nheads) / nkv;
-  // Workgroups of a (row, key head): `splits` for each block of 32 heads, and
+  // Workgroups of a (row, key head): `splits` for each block of 16 heads, and
   // one that stores the near block in the ring if it has become whole.
   const unsigned each_row = splits * qblocks + 1, bc = blockIdx.x / each_row, rest = blockIdx.x % each_row;
   const unsigned split = rest % splits, qb = rest / splits;
   const int64_t b = bc / nkv, c = bc % nkv;
-  const int g0 = qb * 32, heads = static_cast<int>(group) - g0 < 32 ? static_cast<int>(group) - g0 : 32;
+  const int g0 = qb * 16, heads = static_cast<int>(group) - g0 < 16 ? static_cast<int>(group) - g0 : 16;
   const int sinks = static_cast<int>(p.sinks), blocks = static_cast<int>(p.window / kSwaBlock);
   const int pos = p.pos[b];
   // Of the positions behind the sinks, `spot` is the token's: blocks before
@@ -163,7 +214,7 @@ __global__ void __launch_bounds__(256, 2) swa_q8_step_kernel(const SwaStepParams
       store_block<D>(near_v + static_cast<int64_t>(sinks) * D, vn, cache.v_ring + to * kSwaBlock * D, cache.v_scale + to, lane);
     return;
   }
-  f16v o[NB] = {};
+  f4v o[NB] = {};
   float top = -INFINITY, sum = 0.0f;
   if (pos >= 0) {
     const int64_t ring = static_cast<int64_t>(bc) * p.window * D, scales = static_cast<int64_t>(bc) * blocks;
@@ -179,7 +230,7 @@ __global__ void __launch_bounds__(256, 2) swa_q8_step_kernel(const SwaStepParams
     const int lo = static_cast<int>(each * part + (part < more ? part : more));
     const int hi = lo + static_cast<int>(each + (part < more ? 1 : 0));
     u4 *kt = lds[wave][0], *vt = lds[wave][1];
-    const Lanes at = lanes_of<D>(lane);
+    const Lanes16 at = lanes16_of<D>(lane);
     auto block_of = [&](int i) { return i - near_tiles + (i - near_tiles >= skip ? 1 : 0); };
     auto load = [&](u4 *tile, const uint16_t *near, const uint8_t *bytes, int i) {
       if (i < near_tiles) load_tile<D, 64, kNear>(tile, near, D, i * kNear, own, lane);
@@ -187,16 +238,17 @@ __global__ void __launch_bounds__(256, 2) swa_q8_step_kernel(const SwaStepParams
     };
     if (lo < hi) {
       bf8 q[NS];
-      const int row = (lane & 31) < heads ? lane & 31 : 0;  // lanes past the group repeat its first head
+      const int row = m < heads ? m : 0;  // lanes past the group repeat its first head
       const u4 *src = reinterpret_cast<const u4 *>(p.q + b * p.q_batch + (c * group + g0 + row) * D);
 #pragma unroll
-      for (int s = 0; s < NS; ++s) {
-        u4 v = src[2 * s + half];
+      for (int a = 0; a < NS; ++a) {
+        u4 v = src[4 * a + g];
         if (p.scale < 0.0f) v ^= 0x80008000u;  // a negative scale is taken as -q
-        q[s] = __builtin_bit_cast(bf8, v);
+        q[a] = __builtin_bit_cast(bf8, v);
       }
       const float c2 = fabsf(p.scale) * kLog2e;
       float k_scale = 0.0f, v_scale = 0.0f;  // lane l: those of tile i + l, for every 64th i
+#pragma unroll 1
       for (int i = lo; i < hi; ++i) {
         if (((i - lo) & 63) == 0) {
           if (i == lo) {
@@ -213,60 +265,57 @@ __global__ void __launch_bounds__(256, 2) swa_q8_step_kernel(const SwaStepParams
         const int k0 = i * kNear;
         const bool has = near && own >= k0 && own < k0 + kNear;
         wait_tiles<kCopies>();  // the keys: all but the copies of the values
-        f16v s[2] = {};
+        f4v s[4] = {};
         if (near) {
           if (has) put_row<D>(kt, kn, own - k0, lane);
 #pragma unroll
-          for (int x = 0; x < NS; ++x) s[0] = mfma(row_operand<D>(kt, 0, x, at), q[x], s[0]);
+          for (int a = 0; a < NS; ++a)
 #pragma unroll
-          for (int r = 0; r < 16; ++r) {
-            if (k0 + d_row(r, half) >= count) s[0][r] = -INFINITY;
-            s[1][r] = -INFINITY;
+            for (int x = 0; x < 2; ++x) s[x] = mfma16(row16<D>(lds_at(kt), x, a, at), q[a], s[x]);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+              if (k0 + 16 * x + 4 * g + r >= count) s[x][r] = -INFINITY;
+            s[2][r] = s[3][r] = -INFINITY;
           }
         } else {
 #pragma unroll
-          for (int blk = 0; blk < 2; ++blk)
+          for (int a = 0; a < NS; ++a)
 #pragma unroll
-            for (int x = 0; x < NS; ++x) s[blk] = mfma(row8<D>(kt, blk, x, lane), q[x], s[blk]);
+            for (int x = 0; x < 4; ++x) s[x] = mfma16(keys16<D>(kt, x, a, lane), q[a], s[x]);
           const int from = block_of(i) == old ? off : -1;
 #pragma unroll
-          for (int blk = 0; blk < 2; ++blk)
+          for (int x = 0; x < 4; ++x)
 #pragma unroll
-            for (int r = 0; r < 16; ++r)
-              if (32 * blk + d_row(r, half) <= from) s[blk][r] = -INFINITY;
+            for (int r = 0; r < 4; ++r)
+              if (16 * x + 4 * g + r <= from) s[x][r] = -INFINITY;
         }
         wait_reads();
         if (i + 1 < hi) load(kt, near_k, cache.k_ring, i + 1);
-        to_weights(s, fmaxf(c2 * ks, 0x1p-100f), o, top, sum);
+        weigh(s, fmaxf(c2 * ks, 0x1p-100f), o, top, sum);
         if (i + 1 < hi) wait_tiles<kCopies>();  // the values: all but the copies of the next keys
         else wait_tiles<0>();
         if (near) {
           if (has) put_row<D>(vt, vn, own - k0, lane);
           // Rows behind the token repeat its slot, which may hold anything.
           for (int r = own + 1 - k0 + lane / CH; has && r < kNear; r += 64 / CH) vt[slot<D>(r, lane % CH)] = u4{};
+          bf8 cut, left;
+          two_parts(s[0], s[1], cut, left);
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            bf8 cut, rest;
-            two_parts(s[0], x, cut, rest);
-#pragma unroll
-            for (int db = 0; db < NB; ++db) {
-              const bf8 v = col_operand<D>(vt, 16 * x, db, at);
-              o[db] = mfma(v, cut, o[db]);
-              o[db] = mfma(v, rest, o[db]);
-            }
+          for (int e = 0; e < NB; ++e) {
+            const bf8 v = elems16<D>(lds_at(vt), e, 0, lane);
+            o[e] = mfma16(v, left, mfma16(v, cut, o[e]));
           }
         } else {
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            bf8 cut, rest;
+          for (int x = 0; x < 2; ++x) {
+            bf8 cut, left;
+            two_parts(s[2 * x] * vs, s[2 * x + 1] * vs, cut, left);
 #pragma unroll
-            for (int r = 0; r < 8; ++r) s[x / 2][8 * (x % 2) + r] *= vs;
-            two_parts(s[x / 2], x % 2, cut, rest);
-#pragma unroll
-            for (int db = 0; db < NB; ++db) {
-              const bf8 v = col8<D>(vt, x, db, lane);
-              o[db] = mfma(v, cut, o[db]);
-              o[db] = mfma(v, rest, o[db]);
+            for (int e = 0; e < NB; ++e) {
+              const bf8 v = values16<D>(vt, x, e, lane);
+              o[e] = mfma16(v, left, mfma16(v, cut, o[e]));
             }
           }
         }
@@ -278,9 +327,42 @@ __global__ void __launch_bounds__(256, 2) swa_q8_step_kernel(const SwaStepParams
         }
       }
     }
+    sum += other_row(sum);
     sum += other_half(sum);
   }
-  join_waves<D>(p, lds, o, top, sum, tops, sums, heads, b * p.nheads + c * group + g0, splits, split);
+  // Join the four wavefronts.
+  float *mine = reinterpret_cast<float *>(lds[wave]);
+#pragma unroll
+  for (int e = 0; e < NB; ++e) *reinterpret_cast<f4v *>(mine + m * D + 16 * e + 4 * g) = o[e];
+  if (g == 0) {
+    tops[wave][m] = top;
+    sums[wave][m] = sum;
+  }
+  __syncthreads();
+  for (int i = tid; i < heads * D; i += 256) {
+    const int row = i / D, e = i % D;
+    float best = tops[0][row];
+#pragma unroll
+    for (int w = 1; w < 4; ++w) best = fmaxf(best, tops[w][row]);
+    // (A share without a maximum holds zeros, or the NaN that all its scores were.)
+    float acc = 0.0f, all = 0.0f;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const float f = tops[w][row] == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(tops[w][row] - best);
+      acc = fmaf(f, reinterpret_cast<const float *>(lds[w])[row * D + e], acc);
+      all = fmaf(f, sums[w][row], all);
+    }
+    const int64_t head = b * p.nheads + c * group + g0 + row;
+    if (splits == 1) {
+      st(p.y, head * D + e, all == 0.0f ? 0.0f : acc / all);
+    } else {
+      p.ws_o[(head * splits + split) * D + e] = acc;
+      if (e == 0) {
+        p.ws_stat[(head * splits + split) * 2] = best;
+        p.ws_stat[(head * splits + split) * 2 + 1] = all;
+      }
+    }
+  }
 }
 
 // A workgroup per (row, key head, block of the ring), and one for what is
@@ -343,14 +425,14 @@ __global__ void __launch_bounds__(256) swa_q8_fill_kernel(const SwaParams p, con
 }  // namespace
 
 int swa_q8_splits(int64_t batch, int64_t nheads, int64_t nkv, int64_t window, int64_t sinks) {
-  // Eight workgroups per CU even out rows of unequal length; a wavefront has at least one tile.
-  const int64_t rows = batch * nkv * ((nheads / nkv + 31) / 32), tiles = window / kSwaBlock + (sinks + kSwaBlock + 31) / 32;
-  const int64_t want = (2048 + rows - 1) / (rows > 0 ? rows : 1), most = (tiles + 3) / 4;
+  // Four workgroups per CU even out rows of unequal length; a wavefront has at least one tile.
+  const int64_t rows = batch * nkv * ((nheads / nkv + 15) / 16), tiles = window / kSwaBlock + (sinks + kSwaBlock + 31) / 32;
+  const int64_t want = (1024 + rows - 1) / (rows > 0 ? rows : 1), most = (tiles + 3) / 4;
   return static_cast<int>(want < most ? want : most);
 }
 
 hipError_t launch_swa_q8_step(const SwaStepParams &p, const SwaQ8Cache &cache, int splits, hipStream_t s) {
-  const unsigned qblocks = static_cast<unsigned>((p.nheads / p.nkv + 31) / 32), sp = static_cast<unsigned>(splits);
+  const unsigned qblocks = static_cast<unsigned>((p.nheads / p.nkv + 15) / 16), sp = static_cast<unsigned>(splits);
   const dim3 g(static_cast<uint32_t>(p.batch * p.nkv * (qblocks * splits + 1))), gj(static_cast<uint32_t>(p.batch * p.nheads));
   if (p.headdim == 64) {
     hipLaunchKernelGGL((swa_q8_step_kernel<64>), g, dim3(256), 0, s, p, cache, sp, qblocks);
