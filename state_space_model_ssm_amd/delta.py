@@ -26,6 +26,7 @@ __all__ = list(_DELTA)
 
 GDR_STATE_STEP = 64   # tokens that the delta rule takes at a time
 SWA_Q8_BLOCK = 64     # positions that share a scale in an 8-bit cache
+_E4M3 = torch.float8_e4m3fn
 
 _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libssm_delta.so")
 _lib = None
@@ -140,15 +141,25 @@ def _scratch(dims, need: int, workspace, like, stream):
 
 def _one_device(stream, first, *others):
     """All tensors on the device whose stream the call goes to."""
-    at = first.device
+    at = first.get_device()   # -1 on the CPU
     for t in others:
-        if t is not None and t.device != at:
-            raise ValueError(f"tensors must be on one device, got {t.device} and {at}")
-    if at.type != "cuda":
+        if t is not None and t.get_device() != at:
+            raise ValueError(f"tensors must be on one device, got {t.device} and {first.device}")
+    if at < 0:
         raise ValueError("tensors must be on the GPU")
     here = torch._C._cuda_getDevice() if stream is None else stream.device_index
-    if at.index != here:
-        raise ValueError(f"tensors are on {at}, the stream on cuda:{here}")
+    if at != here:
+        raise ValueError(f"tensors are on cuda:{at}, the stream on cuda:{here}")
+
+
+_DENSE = torch.contiguous_format
+
+
+def _like(t, like, name, stream):
+    """A caller-given output, or a new dense one, of ``like``'s shape and type."""
+    if t is None and stream is None:
+        return torch.empty_like(like, memory_format=_DENSE)
+    return _out(t, like.shape, like.dtype, like, name, stream)
 
 
 def _at(t):
@@ -198,7 +209,7 @@ def gdr_fwd(q, k, v, g, beta, *, h0=None, lengths=None, scale=None, return_h_las
     state = (batch, H, vd, q.shape[-1])
     _same("h0", h0, _F32, state)
     _same("lengths", lengths, torch.int32, (batch,))
-    y = _out(y, v.shape, _BF16, q, "y", stream)
+    y = _like(y, v, "y", stream)
     if h_last is not None or return_h_last:
         h_last = _out(h_last, state, _F32, q, "h_last", stream)
     if states is not None or return_states:
@@ -227,7 +238,7 @@ def gdr_bwd(q, k, v, g, beta, states, dy, *, dh_last=None, lengths=None, scale=N
     _same("dh_last", dh_last, _F32, state)
     _same("lengths", lengths, torch.int32, (batch,))
     o = out or {}
-    dq, dk, dv, dg, dbeta = (_out(o.get(n), t.shape, t.dtype, t, n, stream)
+    dq, dk, dv, dg, dbeta = (_like(o.get(n), t, n, stream)
                              for n, t in (("dq", q), ("dk", k), ("dv", v), ("dg", g), ("dbeta", beta)))
     dh0 = _out(o.get("dh0"), state, _F32, q, "dh0", stream) if return_dh0 else None
     workspace = _scratch(dims, gdr_bwd_workspace_size(dims), workspace, q, stream)
@@ -244,7 +255,7 @@ def gdr_step(q, k, v, g, beta, h, *, scale=None, h_out=None, y=None, stream=None
     _one_device(stream, q, k, v, g, beta, h)
     dims = _gdr_dims(q, k, v, g, beta, scale, 1)
     _same("h", h, _F32, (*v.shape, q.shape[-1]))
-    y = _out(y, v.shape, _BF16, q, "y", stream)
+    y = _like(y, v, "y", stream)
     h_out = h if h_out is None else _out(h_out, h.shape, _F32, q, "h_out", stream)
     _check(delta_lib().ssm_gdr_step(_at(q), _at(k), _at(v), _ptr(g), _ptr(beta), _ptr(h), _ptr(y), _ptr(h_out),
                                     ctypes.byref(dims), _stream(stream)))
@@ -255,7 +266,15 @@ def gdr_step(q, k, v, g, beta, h, *, scale=None, h_out=None, y=None, stream=None
 # Norms of queries and keys with the rotation by position
 # ---------------------------------------------------------------------------
 
-def _qk_norm_dims(q, k, wq, wk, inv_freq, pos, eps, neighbours, out_q, out_k) -> QkNormDims:
+def _rows(name, t, given, lead, d) -> tuple:
+    """Batch and token stride of an output, which is dense if it is new."""
+    if given:
+        return _heads(name, t, lead, d)
+    token = t.shape[-2] * d
+    return (token, 0) if lead == 1 else (t.shape[1] * token, token)
+
+
+def _qk_norm_dims(q, k, wq, wk, inv_freq, pos, eps, neighbours, out_q, out_k, given_q, given_k) -> QkNormDims:
     lead = q.dim() - 2
     if lead not in (1, 2) or k.dim() != q.dim() or k.shape[:lead] != q.shape[:lead] or k.shape[-1] != q.shape[-1]:
         raise ValueError("q and k must be (batch, seqlen, heads, headdim), or (batch, heads, headdim) in a step, "
@@ -275,8 +294,8 @@ def _qk_norm_dims(q, k, wq, wk, inv_freq, pos, eps, neighbours, out_q, out_k) ->
             raise ValueError("pos is required in a step")
     _same("pos", pos, torch.int32, q.shape[:lead])
     return QkNormDims(q.shape[0], q.shape[1] if lead == 2 else 1, q.shape[-2], k.shape[-2], d, rot,
-                      *_heads("q", q, lead, d), *_heads("k", k, lead, d), *_heads("q's output", out_q, lead, d),
-                      *_heads("k's output", out_k, lead, d), _code(q.dtype), int(neighbours), eps)
+                      *_heads("q", q, lead, d), *_heads("k", k, lead, d), *_rows("q's output", out_q, given_q, lead, d),
+                      *_rows("k's output", out_k, given_k, lead, d), _code(q.dtype), int(neighbours), eps)
 
 
 def qk_norm_fwd(q, k, wq=None, wk=None, *, inv_freq=None, pos=None, eps: float = 1e-6, neighbours: bool = False,
@@ -294,9 +313,9 @@ def qk_norm_fwd(q, k, wq=None, wk=None, *, inv_freq=None, pos=None, eps: float =
     in a step.  Returns ``(q_out, k_out)``, dense, or where q_out and k_out (q
     and k themselves, or other views) are given."""
     _one_device(stream, q, k, wq, wk, inv_freq, pos)
-    q_out = _out(q_out, q.shape, q.dtype, q, "q_out", stream)
-    k_out = _out(k_out, k.shape, k.dtype, q, "k_out", stream)
-    dims = _qk_norm_dims(q, k, wq, wk, inv_freq, pos, eps, neighbours, q_out, k_out)
+    given_q, given_k = q_out is not None, k_out is not None
+    q_out, k_out = _like(q_out, q, "q_out", stream), _like(k_out, k, "k_out", stream)
+    dims = _qk_norm_dims(q, k, wq, wk, inv_freq, pos, eps, neighbours, q_out, k_out, given_q, given_k)
     _check(delta_lib().ssm_qk_norm_fwd(_at(q), _at(k), _ptr(wq), _ptr(wk), _ptr(inv_freq), _ptr(pos), _at(q_out),
                                        _at(k_out), ctypes.byref(dims), _stream(stream)))
     return q_out, k_out
@@ -313,8 +332,8 @@ def qk_norm_bwd(q, k, wq, wk, dq_out, dk_out, *, inv_freq=None, pos=None, eps: f
     _same("dq_out", dq_out, q.dtype, q.shape)
     _same("dk_out", dk_out, q.dtype, k.shape)
     o = out or {}
-    dq, dk = _out(o.get("dq"), q.shape, q.dtype, q, "dq", stream), _out(o.get("dk"), k.shape, q.dtype, q, "dk", stream)
-    dims = _qk_norm_dims(q, k, wq, wk, inv_freq, pos, eps, neighbours, dq, dk)
+    dq, dk = _like(o.get("dq"), q, "dq", stream), _like(o.get("dk"), k, "dk", stream)
+    dims = _qk_norm_dims(q, k, wq, wk, inv_freq, pos, eps, neighbours, dq, dk, "dq" in o, "dk" in o)
     dwq = dwk = None
     if return_dw or "dwq" in o or "dwk" in o:
         dwq, dwk = (_out(o.get(n), q.shape[-1:], _F32, q, n, stream) for n in ("dwq", "dwk"))
@@ -333,25 +352,24 @@ def swa_q8_cache(batch: int, nkv: int, window: int, headdim: int, *, sinks: int 
     """A new, empty cache for ``swa_q8_step`` and ``swa_q8_fill``; window must be a multiple of 64."""
     if window < SWA_Q8_BLOCK or window % SWA_Q8_BLOCK:
         raise ValueError(f"window must be a multiple of {SWA_Q8_BLOCK}, got {window}")
-    e8 = torch.float8_e4m3fn
-    shapes = ((sinks + SWA_Q8_BLOCK, headdim), _BF16), ((window, headdim), e8), ((window // SWA_Q8_BLOCK,), _F32)
+    shapes = ((sinks + SWA_Q8_BLOCK, headdim), _BF16), ((window, headdim), _E4M3), ((window // SWA_Q8_BLOCK,), _F32)
     return SwaQ8Cache(*(torch.empty(batch, nkv, *shape, dtype=dt, device=device) for shape, dt in shapes for _ in "kv"))
 
 
 def _q8_cache(cache, batch, nkv, headdim, sinks) -> int:
     """The window of a cache, whose tensors are checked."""
-    window = cache.k_ring.shape[2] if cache.k_ring.dim() == 4 else 0
+    near_k, near_v, ring_k, ring_v, scale_k, scale_v = cache
+    window = ring_k.shape[2] if ring_k.dim() == 4 else 0
     if window % SWA_Q8_BLOCK:
         raise ValueError(f"the cache's window must be a multiple of {SWA_Q8_BLOCK}, got {window}")
-    lead = (batch, nkv)
-    for name, t in cache._asdict().items():
-        kind = name[2:]
-        if kind == "near":
-            _same(name, t, _BF16, (*lead, sinks + SWA_Q8_BLOCK, headdim))
-        elif kind == "ring":
-            _same(name, t, torch.float8_e4m3fn, (*lead, window, headdim))
-        else:
-            _same(name, t, _F32, (*lead, window // SWA_Q8_BLOCK))
+    near, ring = (batch, nkv, sinks + SWA_Q8_BLOCK, headdim), (batch, nkv, window, headdim)
+    scale = (batch, nkv, window // SWA_Q8_BLOCK)
+    _same("k_near", near_k, _BF16, near)
+    _same("v_near", near_v, _BF16, near)
+    _same("k_ring", ring_k, _E4M3, ring)
+    _same("v_ring", ring_v, _E4M3, ring)
+    _same("k_scale", scale_k, _F32, scale)
+    _same("v_scale", scale_v, _F32, scale)
     return window
 
 
@@ -365,7 +383,7 @@ def swa_q8_step(q, k, v, cache: SwaQ8Cache, pos, *, sinks: int = 0, scale=None, 
     dims = _swa_dims(q, k, v, 1, sinks, scale, 1)
     dims.window = _q8_cache(cache, k.shape[0], k.shape[1], k.shape[2], sinks)
     _same("pos", pos, torch.int32, (q.shape[0],))
-    y = _out(y, q.shape, _BF16, q, "y", stream)
+    y = _like(y, q, "y", stream)
     workspace = _scratch(dims, swa_q8_step_workspace_size(dims), workspace, q, stream)
     _check(delta_lib().ssm_swa_q8_step(_at(q), _at(k), _at(v), *map(_ptr, cache), _ptr(pos), _ptr(y), ctypes.byref(dims),
                                        _stream(stream)))
