@@ -45,6 +45,12 @@ int check_qk(const ssm_qk_norm_dims_t *d) {
       return fail(SSM_ERR_SHAPE, "strides must be multiples of %lld elements, not negative (got %lld)", (long long)each, (long long)s);
     if ((k % 2 == 0 ? d->batch : d->seqlen) > 1 && s < token) return fail(SSM_ERR_SHAPE, "a stride is smaller than a token");
   }
+  // Bytes from the first token to the last: below 2^62.
+  for (int k = 0; k < 8; k += 2) {
+    const int64_t rows = mul(d->batch > 1 ? d->batch - 1 : 0, strides[k]);
+    const int64_t far = mul(d->seqlen > 1 ? d->seqlen - 1 : 0, strides[k + 1]);
+    if (rows < 0 || far < 0 || mul(rows + far, 8) < 0) return fail(SSM_ERR_UNSUPPORTED, "the tensors are too large");
+  }
   // Rows of one output must not meet: a batch row's tokens end before the next one's, or between them.
   for (int k = 4; k < 8; k += 2) {
     const int64_t token = (k == 4 ? d->nheads : d->nkv) * d->headdim, sb = strides[k], st = strides[k + 1];

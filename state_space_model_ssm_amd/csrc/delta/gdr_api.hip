@@ -26,7 +26,7 @@ int check_gdr(const ssm_gdr_dims_t *d, bool step) {
   if (d->seqlen > (int64_t{1} << 30)) return fail(SSM_ERR_UNSUPPORTED, "seqlen must be at most 2^30");
   const int64_t chunks = ceil_div(d->seqlen, SSM_GDR_STATE_STEP), heads = mul(d->batch, d->nheads);
   const int64_t all = mul(heads, chunks > 4 ? chunks : 4);  // a workgroup per chunk, and per 32 values
-  if (heads < 0 || all < 0 || all > kMaxGroups)
+  if (d->nheads > kMaxGroups || heads < 0 || all < 0 || all > kMaxGroups)
     return fail(SSM_ERR_UNSUPPORTED, "batch * nheads * max(4, ceil(seqlen / 64)) must be below 2^24");
   const int64_t strides[] = {d->q_batch, d->q_token, d->k_batch, d->k_token, d->v_batch, d->v_token};
   for (const int64_t s : strides)

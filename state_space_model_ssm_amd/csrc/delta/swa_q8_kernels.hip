@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(256, 2) swa_q8_step_kernel(const SwaStepParams
   const int64_t b = bc / nkv, c = bc % nkv;
   const int g0 = qb * 16, heads = static_cast<int>(group) - g0 < 16 ? static_cast<int>(group) - g0 : 16;
   const int sinks = static_cast<int>(p.sinks), blocks = static_cast<int>(p.window / kSwaBlock);
-  const int pos = p.pos[b];
+  const int pos = p.pos[b] < 0 ? -1 : p.pos[b];
   // Of the positions behind the sinks, `spot` is the token's: blocks before
   // `now` are whole, and in the ring; place `off` of the near block is its own.
   const int spot = pos - sinks, now = spot >> 6, off = spot & 63;
