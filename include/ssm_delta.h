@@ -54,8 +54,8 @@ SSM_API const char *ssm_delta_last_error(void);
  * k and v (heads of a token are adjacent: head stride kdim or vdim); batch and
  * token strides must be multiples of 8, token strides at most 2^24, and q, k,
  * v, y, dy, dq, dk, dv and the states 16-byte aligned; all but q, k and v are
- * dense.  scale multiplies y.  seqlen <= 2^30 and
- * batch * nheads * max(4, ceil(seqlen / 64)) < 2^24.
+ * dense.  scale multiplies y.  seqlen <= 2^30, nqk * kdim and nheads * vdim
+ * <= 2^24, and batch * nheads * max(4, ceil(seqlen / 64)) < 2^24.
  */
 typedef struct {
   int64_t batch, seqlen, nqk, nheads, kdim, vdim;
@@ -77,7 +77,8 @@ enum { SSM_GDR_STATE_STEP = 64 };
  *   q, k   : (batch, seqlen, nqk, kdim);  v, y: (batch, seqlen, nheads, vdim)
  *   g, beta: (batch, seqlen, nheads) gate_dtype; g is the logarithm of the
  *            decay (at or below 0 for a state that fades; -inf forgets, and
- *            so does anything below -200)
+ *            so does anything below -200; above 0 the sum over a block of 64
+ *            tokens must stay below 88, where exp leaves float32)
  *   h0     : (batch, nheads, vdim, kdim) float32, nullable (zero)
  *   lengths: (batch) int32, nullable (seqlen); values outside 0 .. seqlen are
  *            taken as the nearer end.  Rows at or past the length are not used.

@@ -34,7 +34,10 @@ int check_gdr(const ssm_gdr_dims_t *d, bool step) {
       return fail(SSM_ERR_SHAPE, "strides must be multiples of 8 elements, not negative (got %lld)", (long long)s);
   if (d->q_token > kMaxToken || d->k_token > kMaxToken || d->v_token > kMaxToken)
     return fail(SSM_ERR_UNSUPPORTED, "token strides must be at most 2^24 elements");
+  // (Outputs are dense, and a block's 64 tokens are addressed in 32 bits.)
   const int64_t nk = d->nqk * d->kdim, nv = d->nheads * d->vdim;
+  if (nk > kMaxToken || nv > kMaxToken)
+    return fail(SSM_ERR_UNSUPPORTED, "nqk * kdim and nheads * vdim must be at most 2^24");
   if (d->seqlen > 1 && (d->q_token < nk || d->k_token < nk || d->v_token < nv))
     return fail(SSM_ERR_SHAPE, "a token stride is smaller than the token");
   if (d->batch > 1 && (d->q_batch < nk || d->k_batch < nk || d->v_batch < nv))

@@ -315,7 +315,7 @@ hipError_t launch_qk_norm_bwd(const QkNormParams &p0, int bf16, hipStream_t s) {
   p.tile = tile_of(p.tokens);
   const int parts = static_cast<int>(qk_norm_parts(p.tokens));
   if (parts > 0) bf16 ? run<uint16_t>(p, true, static_cast<unsigned>(parts), s) : run<float>(p, true, static_cast<unsigned>(parts), s);
-  if (p.ws != nullptr)
+  if (p.dwq != nullptr || p.dwk != nullptr)  // (without tokens, too: zeros)
     hipLaunchKernelGGL(qk_norm_sum_kernel, dim3(static_cast<uint32_t>(2 * p.headdim / 16)), dim3(1024), 0, s, p, parts);
   return hipGetLastError();
 }

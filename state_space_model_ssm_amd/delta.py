@@ -271,7 +271,7 @@ def _rows(name, t, given, lead, d) -> tuple:
     if given:
         return _heads(name, t, lead, d)
     token = t.shape[-2] * d
-    return (token, 0) if lead == 1 else (t.shape[1] * token, token)
+    return (token, 0) if lead == 1 else (max(t.shape[1], 1) * token, token)
 
 
 def _qk_norm_dims(q, k, wq, wk, inv_freq, pos, eps, neighbours, out_q, out_k, given_q, given_k) -> QkNormDims:

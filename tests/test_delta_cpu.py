@@ -172,6 +172,8 @@ def test_gdr_sizes():
             assert call(name, **{axis: 64}) == SHAPE and "smaller" in ssm.delta_last_error()
         assert call(name, batch=1 << 22) == UNSUPPORTED and call(name, batch=1 << 62) == UNSUPPORTED
         assert call(name, batch=0, nheads=1 << 62, nqk=1 << 62) == UNSUPPORTED
+        wide = dict(batch=1, seqlen=1, nheads=1 << 18, nqk=1, v_batch=0, v_token=0)   # 2^25 elements a token
+        assert call(name, **wide) == UNSUPPORTED and "2^24" in ssm.delta_last_error()
     for name in ("ssm_gdr_fwd", "ssm_gdr_bwd"):
         assert call(name, seqlen=-1) == SHAPE and call(name, seqlen=(1 << 30) + 1) == UNSUPPORTED
         assert call(name, batch=1, nheads=1, nqk=1, seqlen=1 << 30) == UNSUPPORTED   # 2^24 blocks of 64 tokens
