@@ -136,6 +136,8 @@ int ssm_gdr_fwd(const void *q, const void *k, const void *v, const void *g, cons
   p.y = static_cast<uint16_t *>(y);
   p.h_last = h_last;
   p.saved = static_cast<char *>(states);
+  p.ops = states ? p.saved + gdr_both_bytes(d.kdim, d.vdim) : p.ws;
+  p.ops_step = static_cast<int64_t>(states ? gdr_saved_bytes(d.kdim, d.vdim) : kGdrChunkBytes);
   p.ws_state = reinterpret_cast<float *>(p.ws + n.chunks);
   p.ws_carry = reinterpret_cast<uint16_t *>(p.ws + n.chunks + n.state);
   return launched(launch_gdr_fwd(p, static_cast<hipStream_t>(stream)), "gdr_fwd");

@@ -59,7 +59,9 @@ __global__ void __launch_bounds__(256) gdr_bwd_kernel(const GdrParams p) {
         fac[i] = lds_f4(gates + 256 + 64 * i) * -lds_f4(gates + 768 + 64 * i);
       }
 #pragma unroll
-      for (int f = 0; f < kGdrFrags; ++f) tf[f] = {frag16(at_t, f, lane), frag16(at_t, kGdrFrags + f, lane)};
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int j = 0; j <= 2 * k + 1; ++j) tf[tri_t(j, k)] = {tri_cols(at_t, j, k, 0, lane), tri_cols(at_t, j, k, 1, lane)};
       const float whole = lds_f4(at_t + kTri + 256 + 240)[3];
       __builtin_amdgcn_sched_barrier(0);
       // K dS, and dU = e^(GC - G) of that + A^T dY
@@ -107,7 +109,7 @@ __global__ void __launch_bounds__(256) gdr_bwd_kernel(const GdrParams p) {
   const uint16_t *kp = p.k + b * p.k_batch + hk * KD, *qp = p.q + b * p.q_batch + hk * KD;
   const uint16_t *dp = p.dy + (b * p.seqlen * p.nheads + h) * p.vdim + vt * NC;
   const int64_t step = static_cast<int64_t>(gdr_saved_bytes(KD, p.vdim));
-  const char *ws = p.saved + bh * p.chunks * step + gdr_both_bytes(KD, p.vdim);  // T^T, A^T, gates
+  const char *ws = p.saved + bh * p.chunks * step + gdr_both_bytes(KD, p.vdim);  // T, A, gates
   uint16_t *vp = p.dv + (b * p.seqlen * p.nheads + h) * p.vdim + col0;
   TileCopy<KD, NT> k_copy, q_copy;
   TileCopy<NC, NT> d_copy;
@@ -187,7 +189,9 @@ __global__ void __launch_bounds__(256) gdr_bwd_kernel(const GdrParams p) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) dy[i] = rows4<NC>(tile + kAtD, i, w, lane);
 #pragma unroll
-    for (int f = 0; f < kGdrFrags; ++f) af[f] = {frag16(at_a, f, lane), frag16(at_a, kGdrFrags + f, lane)};
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int j = 0; j <= 2 * k + 1; ++j) af[tri_t(j, k)] = {tri_cols(at_a, j, k, 0, lane), tri_cols(at_a, j, k, 1, lane)};
 #pragma unroll
     for (int k = 0; k < 2; ++k)
 #pragma unroll

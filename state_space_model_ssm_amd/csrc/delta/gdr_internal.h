@@ -21,7 +21,7 @@ constexpr size_t kGdrChunkBytes = 2 * kGdrTriBytes + kGdrGateBytes;
 // values][part], then U or D = beta E, [32 values][16 tokens][part], 1 KiB each.
 constexpr size_t gdr_state_bytes(int64_t kdim, int64_t vdim) { return static_cast<size_t>(kdim * vdim) * 4; }
 constexpr size_t gdr_both_bytes(int64_t kdim, int64_t vdim) { return gdr_state_bytes(kdim, vdim) + static_cast<size_t>(64 * vdim) * 4; }
-// What the forward saves: those, T^T, A^T and the factors.
+// What the forward saves: those, and what is known of the chunk.
 constexpr size_t gdr_saved_bytes(int64_t kdim, int64_t vdim) { return gdr_both_bytes(kdim, vdim) + kGdrChunkBytes; }
 
 // Long sequences of few heads are cut into segments of `chunks` chunks, and the
@@ -40,7 +40,9 @@ struct GdrParams {
   uint16_t *y;
   float *h_last;               // nullable
   char *saved;                 // gdr_saved_bytes() per (row, value head, chunk), nullable in the forward
-  char *ws;                    // kGdrChunkBytes per (row, value head, chunk)
+  char *ws;
+  char *ops;                   // kGdrChunkBytes per (row, value head, chunk), ops_step bytes apart: in `saved` or the workspace
+  int64_t ops_step;
   const uint16_t *dy;          // backward
   const float *dh_last;        // nullable
   uint16_t *dq, *dk, *dv;

@@ -22,10 +22,8 @@ __device__ __forceinline__ void store_rows(const f4v (&t)[W + 1], u4 *to, int la
 }
 
 // One workgroup per chunk and value head, one wavefront per 16 of its tokens.
-// SAVE: also T^T and A^T, which the backward needs.
-template <int KD, typename G, bool SAVE>
+template <int KD, typename G>
 __global__ void __launch_bounds__(256) gdr_chunk_kernel(const GdrParams p) {
-  __shared__ __align__(16) float full[SAVE ? 64 * kPitch : 4], inv[SAVE ? 64 * kPitch : 4];  // A and T
   __shared__ double sums[64];                       // log2 of the decay up to each token
   __shared__ float betas[64];
   __shared__ __align__(16) float low[64 * kPitch];  // L^T
@@ -35,8 +33,7 @@ __global__ void __launch_bounds__(256) gdr_chunk_kernel(const GdrParams p) {
   const int64_t id = blockIdx.x, c = id % p.chunks, bh = id / p.chunks, b = bh / p.nheads, h = bh % p.nheads;
   const int t0 = static_cast<int>(c) * 64, len = gdr_length(p.lengths, b, p.seqlen) - t0;
   if (len <= 0) return;
-  char *ws = p.ws + id * static_cast<int64_t>(kGdrChunkBytes);
-  const int64_t kept_bytes = static_cast<int64_t>(gdr_saved_bytes(KD, p.vdim));
+  char *ws = p.ops + id * p.ops_step;
   constexpr int NS = KD / 32;
   const int64_t hk = h / (p.nheads / p.nqk);
   const uint16_t *kp = p.k + b * p.k_batch + t0 * p.k_token + hk * KD + 8 * g;
@@ -76,12 +73,7 @@ __global__ void __launch_bounds__(256) gdr_chunk_kernel(const GdrParams p) {
     gates[64 + lane] = into;
     gates[128 + lane] = __builtin_amdgcn_exp2f(static_cast<float>(last - s));
     gates[192 + lane] = bt;
-    if (SAVE) {
-      float *kept = reinterpret_cast<float *>(p.saved + id * kept_bytes + gdr_both_bytes(KD, p.vdim) + 2 * kGdrTriBytes);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) kept[64 * k + lane] = gates[64 * k + lane];
-      reinterpret_cast<double *>(kept + 256)[lane] = s;
-    }
+    reinterpret_cast<double *>(gates + 256)[lane] = s;
   }
   __syncthreads();
   u4 *out = reinterpret_cast<u4 *>(ws);
@@ -108,7 +100,6 @@ __global__ void __launch_bounds__(256) gdr_chunk_kernel(const GdrParams p) {
         const int j = 16 * jb + 4 * g + r;
         const float decay = j <= i ? __builtin_amdgcn_exp2f(static_cast<float>(si - sums[j])) : 0.0f;
         att[jb][r] = j <= i && i < len ? att[jb][r] * decay * p.scale : 0.0f;
-        if (SAVE) full[i * kPitch + j] = att[jb][r];
         low[j * kPitch + i] = j < i ? kk[jb][r] * decay * bi : 0.0f;
       }
     store_rows<W>(att, out + kGdrTriBytes / 16, lane);
@@ -155,16 +146,7 @@ __global__ void __launch_bounds__(256) gdr_chunk_kernel(const GdrParams p) {
       for (int r = 0; r < 4; ++r) t[j] = mfma_f32(-d[r], acc[r], t[j]);
     }
     store_rows<W>(t, out, lane);
-    if (SAVE)
-#pragma unroll
-      for (int jb = 0; jb <= W; ++jb) *reinterpret_cast<f4v *>(inv + i * kPitch + 16 * jb + 4 * g) = t[jb];
   });
-  if (SAVE) {
-    u4 *kept = reinterpret_cast<u4 *>(p.saved + id * kept_bytes + gdr_both_bytes(KD, p.vdim));
-    __syncthreads();
-    store_cols(inv, w, kept, lane);
-    store_cols(full, w, kept + kGdrTriBytes / 16, lane);
-  }
 }
 
 // ---------------------------------------------------------------------------
@@ -288,7 +270,7 @@ __global__ void __launch_bounds__(256) gdr_fwd_kernel(const GdrParams p) {
   const int64_t hk = h / (p.nheads / p.nqk), yt = p.nheads * p.vdim;
   const uint16_t *kp = p.k + b * p.k_batch + hk * KD, *qp = p.q + b * p.q_batch + hk * KD;
   const uint16_t *vp = p.v + b * p.v_batch + h * p.vdim + vt * NC;
-  const char *ws = p.ws + bh * p.chunks * static_cast<int64_t>(kGdrChunkBytes);
+  const char *ws = p.ops + bh * p.chunks * p.ops_step;
   uint16_t *yp = p.y + (b * p.seqlen * p.nheads + h) * p.vdim + col0;
   TileCopy<KD, NT> k_copy, q_copy;
   TileCopy<NC, NT> v_copy;
@@ -305,7 +287,7 @@ __global__ void __launch_bounds__(256) gdr_fwd_kernel(const GdrParams p) {
     v_copy.start(to + kAtV / 16, vp + 64 * c * p.v_token, last, id);
   };
   auto fetch_ws = [&](int c) {
-    copy_share<kGdrChunkBytes / 1024, kPairs>(base + (c & 1) * kBuffer + kAtW, ws + c * static_cast<int64_t>(kGdrChunkBytes), w, lane * 16);
+    copy_share<kGdrChunkBytes / 1024, kPairs>(base + (c & 1) * kBuffer + kAtW, ws + c * p.ops_step, w, lane * 16);
   };
   if (first < n) {
     fetch_rows(first);
@@ -417,7 +399,7 @@ __global__ void __launch_bounds__(256, 2) gdr_segment_kernel(const GdrParams p) 
   const bool values = tile < vtiles;
   const int col = static_cast<int>(values ? tile : tile - vtiles) * NC + 16 * w + m;
   const uint16_t *kp = p.k + b * p.k_batch + hk * KD, *vp = p.v + b * p.v_batch + h * p.vdim + tile * NC;
-  const char *ws = p.ws + bh * p.chunks * static_cast<int64_t>(kGdrChunkBytes);
+  const char *ws = p.ops + bh * p.chunks * p.ops_step;
   const unsigned base = lds_at(lds);
   const Lanes16 at = lanes16_of<KD>(lane);
   TileCopy<KD, NT> k_copy;
@@ -426,7 +408,7 @@ __global__ void __launch_bounds__(256, 2) gdr_segment_kernel(const GdrParams p) 
   v_copy.init(p.v_token, tid);
   auto fetch = [&](int c) {
     u4 *to = lds + (c & 1) * (kBuffer / 16);
-    const char *wc = ws + c * static_cast<int64_t>(kGdrChunkBytes);
+    const char *wc = ws + c * p.ops_step;
     k_copy.start(to, kp + 64 * c * p.k_token, 63, tid);
     if (values) v_copy.start(to + kAtV / 16, vp + 64 * c * p.v_token, 63, tid);
     copy_share<kGdrTriBytes / 1024, 4>(base + (c & 1) * kBuffer + kAtW, wc, w, lane * 16);
@@ -610,8 +592,7 @@ __global__ void __launch_bounds__(256) gdr_step_kernel(const GdrParams p) {
 template <int KD, typename G>
 void chunks(const GdrParams &p, hipStream_t s) {
   const dim3 n(static_cast<uint32_t>(p.batch * p.nheads * p.chunks));
-  if (p.saved != nullptr) hipLaunchKernelGGL((gdr_chunk_kernel<KD, G, true>), n, dim3(256), 0, s, p);
-  else hipLaunchKernelGGL((gdr_chunk_kernel<KD, G, false>), n, dim3(256), 0, s, p);
+  hipLaunchKernelGGL((gdr_chunk_kernel<KD, G>), n, dim3(256), 0, s, p);
 }
 
 template <int KD>

@@ -124,17 +124,26 @@ __device__ __forceinline__ bf8 turned(unsigned first, unsigned second, int i, in
                                                          0, 1, 2, 3, 4, 5, 6, 7));
 }
 
+// Fragment of a lower triangle: row block i (of 16), columns 32 s .., and of
+// its transpose: row block j, columns 32 s .. (32 s + 31 >= 16 j).
+__host__ __device__ constexpr int tri(int i, int s) { return i < 2 ? i : 2 * (i - 1) + s; }
+__host__ __device__ constexpr int tri_t(int j, int s) { return j < 2 ? 2 * j + s : j + 2; }
+// Operand of the transpose's row block j, columns 32 s .., of a triangle that lies as its own operands.
+__device__ __forceinline__ bf8 tri_cols(unsigned from, int j, int s, int part, int lane) {
+  typedef __attribute__((address_space(3))) sh4 lds4;
+  const int m = lane & 15;
+  const unsigned at = from + (16 * (m & 3) + 4 * (lane >> 4) + (m >> 2)) * 16 + (j % 2) * 8;
+  const sh4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)(at + (part * kGdrFrags + tri(2 * s, j / 2)) * 1024));
+  const sh4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)(at + (part * kGdrFrags + tri(2 * s + 1, j / 2)) * 1024));
+  return __builtin_bit_cast(bf8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+
 __device__ __forceinline__ f4v lds_f4(unsigned at) {
   typedef __attribute__((address_space(3))) const f4v lds16;
   return *(lds16 *)(at);
 }
 
 constexpr int kPairs = 2;  // wavefronts that carry the state, and as many beside them
-
-// Fragment of a lower triangle: row block i (of 16), columns 32 s .., and of
-// its transpose: row block j, columns 32 s .. (32 s + 31 >= 16 j).
-__host__ __device__ constexpr int tri(int i, int s) { return i < 2 ? i : 2 * (i - 1) + s; }
-__host__ __device__ constexpr int tri_t(int j, int s) { return j < 2 ? 2 * j + s : j + 2; }
 
 // Call f with the wavefront's number (of 4) as a constant.  Each wavefront's
 // products are straight code then: the compiler leaves out the wait between a
