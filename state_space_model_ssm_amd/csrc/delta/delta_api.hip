@@ -60,6 +60,11 @@ int check_qk(const ssm_qk_norm_dims_t *d) {
   return SSM_OK;
 }
 
+size_t dw_workspace(const ssm_qk_norm_dims_t &d) {
+  const QkNormGroups n = qk_norm_groups(d.batch * d.seqlen, d.nheads, d.nkv, d.headdim, true);
+  return up256(static_cast<size_t>(n.q + n.k) * d.headdim * 4);
+}
+
 // A strided (batch, seqlen, heads, headdim) tensor of a call.
 struct Rows {
   const char *name;
@@ -105,7 +110,7 @@ int qk_run(const void *q, const void *k, const float *wq, const float *wk, const
   const Arg rows[] = {{"q", q, rq.bytes, 16, true}, {"k", k, rk.bytes, 16, true}};
   for (const Arg &a : rows)
     if ((rc = check_in(a)) != SSM_OK) return rc;
-  const size_t need = bwd && (dwq != nullptr || dwk != nullptr) ? up256(static_cast<size_t>(qk_norm_parts(tokens)) * 2 * w) : 0;
+  const size_t need = bwd && (dwq != nullptr || dwk != nullptr) ? dw_workspace(d) : 0;
   const Arg ins[] = {{"wq", wq, w, 16, false},
                      {"wk", wk, w, 16, false},
                      {"inv_freq", inv_freq, static_cast<size_t>(d.rot) / 2 * 4, 4, n > 0},
@@ -219,7 +224,7 @@ int ssm_qk_norm_bwd_workspace_size(const ssm_qk_norm_dims_t *dims, size_t *bytes
   if (!bytes) return fail(SSM_ERR_NULL, "bytes is NULL");
   const int rc = check_qk(dims);
   if (rc != SSM_OK) return rc;
-  *bytes = up256(static_cast<size_t>(qk_norm_parts(dims->batch * dims->seqlen)) * 2 * dims->headdim * 4);
+  *bytes = dw_workspace(*dims);
   return ok();
 }
 

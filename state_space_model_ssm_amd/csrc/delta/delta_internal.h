@@ -14,13 +14,19 @@ struct QkNormParams {
   const int32_t *pos;             // nullable (0, 1, ..)
   const void *dyq, *dyk;          // backward: gradients of the outputs, dense
   void *out_q, *out_k;            // outputs, or dq and dk
-  float *dwq, *dwk, *ws;          // nullable; (parts, 2, headdim) terms of both
+  float *dwq, *dwk, *ws;          // nullable; (workgroups, headdim) terms, of those of q and then of k
   int64_t tokens, seqlen, nheads, nkv;
   int64_t q_batch, q_token, k_batch, k_token, oq_batch, oq_token, ok_batch, ok_token;
   float eps;
-  int32_t headdim, rot, neighbours, tile;  // tile: tokens that a workgroup takes at a time
+  int32_t headdim, rot, neighbours;
+  int32_t tile_q, tile_k;         // tokens that a workgroup of either takes at a time
+  int64_t nq;                     // workgroups of q
 };
-int64_t qk_norm_parts(int64_t tokens);
+struct QkNormGroups {
+  int64_t q, k;
+  int tile_q, tile_k;
+};
+QkNormGroups qk_norm_groups(int64_t tokens, int64_t nheads, int64_t nkv, int64_t headdim, bool bwd);
 hipError_t launch_qk_norm(const QkNormParams &p, int bf16, hipStream_t stream);
 hipError_t launch_qk_norm_bwd(const QkNormParams &p, int bf16, hipStream_t stream);
 

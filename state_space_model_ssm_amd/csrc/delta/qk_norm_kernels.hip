@@ -3,10 +3,18 @@
 //
 // Bound by memory: an element is read once and written once.  A head is 16
 // elements per lane, in two pieces of 8 that hold the two elements of each
-// pair that is rotated together; a workgroup takes all heads of a few tokens,
-// whose sines and cosines it makes once, in LDS.  The angle pos * inv_freq is
+// pair that is rotated together; a workgroup takes all of q's heads of a few
+// tokens, or all of k's, whose sines and cosines it makes once, in LDS.  (One
+// that took both kept two sets of weights and of their gradients in registers:
+// 170 in the backward, now 131.)  The angle pos * inv_freq is
 // taken in float64 and reduced to a fraction of a turn there: in float32 a
 // position of 10^6 would have lost a sixteenth of a radian.
+//
+// Measured: 32749 tokens of 16 and 4 heads of 128 in 68 us, 4.9 TB/s of what is
+// read and written (a large copy: 4.8); training's 8192 tokens of 32 and 8 heads
+// of 64 forward in 17.9 us (4.7 TB/s), backward in 27.0 (4.7) and the sum of the
+// weights' gradients in 4.0, which is the latency of two reads; one token of 32
+// sequences in 4.2 us.
 #include "delta_internal.h"
 
 namespace ssmb {
@@ -14,24 +22,40 @@ namespace {
 
 typedef __attribute__((ext_vector_type(4))) unsigned int u4;
 typedef __attribute__((ext_vector_type(4))) float f4;
-constexpr int kMaxTile = 8;    // tokens
+constexpr int kMaxTile = 16;   // tokens
 constexpr int kMaxPairs = 128;
 
-__device__ __forceinline__ void load8(float (&x)[8], const uint16_t *p) {
-  const u4 v = *reinterpret_cast<const u4 *>(p);
+// Eight elements as they lie in memory, and as numbers.
+template <typename T>
+struct Eight;
+template <>
+struct Eight<uint16_t> {
+  u4 v;
+  __device__ __forceinline__ void load(const uint16_t *p) { v = *reinterpret_cast<const u4 *>(p); }
+  __device__ __forceinline__ void get(float (&x)[8]) const {
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    x[2 * k] = __uint_as_float(v[k] << 16);
-    x[2 * k + 1] = __uint_as_float(v[k] & 0xffff0000u);
+    for (int k = 0; k < 4; ++k) {
+      x[2 * k] = __uint_as_float(v[k] << 16);
+      x[2 * k + 1] = __uint_as_float(v[k] & 0xffff0000u);
+    }
   }
-}
+};
+template <>
+struct Eight<float> {
+  f4 v[2];
+  __device__ __forceinline__ void load(const float *p) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) v[k] = reinterpret_cast<const f4 *>(p)[k];
+  }
+  __device__ __forceinline__ void get(float (&x)[8]) const {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = v[e / 4][e % 4];
+  }
+};
 __device__ __forceinline__ void load8(float (&x)[8], const float *p) {
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const f4 v = reinterpret_cast<const f4 *>(p)[k];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) x[4 * k + e] = v[e];
-  }
+  Eight<float> v;
+  v.load(p);
+  v.get(x);
 }
 __device__ __forceinline__ void store8(const float (&x)[8], uint16_t *p) {
   typedef __attribute__((ext_vector_type(8))) __bf16 bf8;
@@ -91,20 +115,32 @@ __device__ __forceinline__ void rotate(float (&lo)[8], float (&hi)[8], const flo
   }
 }
 
+// What a workgroup works on: the first `nq` take q's heads, the others k's.
+struct Side {
+  bool key;
+  int heads, tile;
+  int64_t group, groups;  // its number among the workgroups of its side
+  int64_t x_batch, x_token, y_batch, y_token;
+};
+__device__ __forceinline__ Side side_of(const QkNormParams &p) {
+  const bool key = blockIdx.x >= p.nq;
+  const unsigned nq = static_cast<unsigned>(p.nq);
+  if (key) return {true, static_cast<int>(p.nkv), p.tile_k, blockIdx.x - nq, gridDim.x - nq, p.k_batch, p.k_token, p.ok_batch, p.ok_token};
+  return {false, static_cast<int>(p.nheads), p.tile_q, blockIdx.x, nq, p.q_batch, p.q_token, p.oq_batch, p.oq_token};
+}
+
 struct Shared {
-  float2 turn[kMaxTile][kMaxPairs];  // cosine and sine
-  int64_t q[kMaxTile], k[kMaxTile], oq[kMaxTile], ok[kMaxTile];  // offsets of the tokens
+  float2 turn[kMaxTile][kMaxPairs];    // cosine and sine
+  int64_t x[kMaxTile], y[kMaxTile];    // offsets of the tokens, of what is read and written
 };
 
 // Angles and offsets of tokens first .. first + count - 1.
-__device__ __forceinline__ void begin(const QkNormParams &p, Shared &sh, int64_t first, int count) {
+__device__ __forceinline__ void begin(const QkNormParams &p, const Side &side, Shared &sh, int64_t first, int count) {
   const int tid = threadIdx.x, half = p.rot / 2;
   if (tid < count) {
     const int64_t b = (first + tid) / p.seqlen, t = (first + tid) % p.seqlen;
-    sh.q[tid] = b * p.q_batch + t * p.q_token;
-    sh.k[tid] = b * p.k_batch + t * p.k_token;
-    sh.oq[tid] = b * p.oq_batch + t * p.oq_token;
-    sh.ok[tid] = b * p.ok_batch + t * p.ok_token;
+    sh.x[tid] = b * side.x_batch + t * side.x_token;
+    sh.y[tid] = b * side.y_batch + t * side.y_token;
   }
   for (int i = tid; i < count * half; i += 256) {
     const int t = i / half, f = i % half;
@@ -120,43 +156,51 @@ __device__ __forceinline__ void begin(const QkNormParams &p, Shared &sh, int64_t
 template <typename T, int G, bool NEIGHBOURS>
 __global__ void __launch_bounds__(256) qk_norm_kernel(const QkNormParams p) {
   __shared__ Shared sh;
-  const int tid = threadIdx.x, j = tid % G, heads = static_cast<int>(p.nheads + p.nkv);
+  const int tid = threadIdx.x, j = tid % G;
+  const Side side = side_of(p);
   const Place at = place_of(p, j);
-  float wq[2][8], wk[2][8];
+  const T *x = static_cast<const T *>(side.key ? p.k : p.q);
+  T *y = static_cast<T *>(side.key ? p.out_k : p.out_q);
+  const float *weights = side.key ? p.wk : p.wq;
+  float w[2][8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) wq[0][e] = wq[1][e] = wk[0][e] = wk[1][e] = 1.0f;
-  if (p.wq != nullptr) load8(wq[0], p.wq + at.lo), load8(wq[1], p.wq + at.hi);
-  if (p.wk != nullptr) load8(wk[0], p.wk + at.lo), load8(wk[1], p.wk + at.hi);
+  for (int e = 0; e < 8; ++e) w[0][e] = w[1][e] = 1.0f;
+  if (weights != nullptr) load8(w[0], weights + at.lo), load8(w[1], weights + at.hi);
   const float mean = 1.0f / static_cast<float>(p.headdim);
-  for (int64_t first = static_cast<int64_t>(blockIdx.x) * p.tile; first < p.tokens; first += static_cast<int64_t>(gridDim.x) * p.tile) {
-    const int count = p.tokens - first < p.tile ? static_cast<int>(p.tokens - first) : p.tile;
-    begin(p, sh, first, count);
+  for (int64_t first = side.group * side.tile; first < p.tokens; first += side.groups * side.tile) {
+    const int count = p.tokens - first < side.tile ? static_cast<int>(p.tokens - first) : side.tile;
+    begin(p, side, sh, first, count);
     __syncthreads();
-    const int rows = count * heads;
-    for (int row0 = 0; row0 < rows; row0 += 256 / G) {
-      const int row = row0 + tid / G;
-      if (row >= rows) continue;
-      const int t = row / heads, h = row % heads;
-      const bool key = h >= p.nheads;
-      const int64_t head = static_cast<int64_t>(key ? h - p.nheads : h) * p.headdim;
-      const T *x = key ? static_cast<const T *>(p.k) + sh.k[t] + head : static_cast<const T *>(p.q) + sh.q[t] + head;
+    const int rows = count * side.heads;
+    // A row's elements are on their way while the one before is worked on.
+    Eight<T> next[2];
+    auto fetch = [&](int row) {
+      row = row < rows ? row : rows - 1;
+      const T *from = x + sh.x[row / side.heads] + static_cast<int64_t>(row % side.heads) * p.headdim;
+      next[0].load(from + at.lo);
+      next[1].load(from + at.hi);
+    };
+    fetch(tid / G);
+    for (int row = tid / G; row < rows; row += 256 / G) {
+      const int t = row / side.heads;
       float lo[8], hi[8], sum = 0.0f;
-      load8(lo, x + at.lo);
-      load8(hi, x + at.hi);
+      next[0].get(lo);
+      next[1].get(hi);
+      fetch(row + 256 / G);
 #pragma unroll
       for (int e = 0; e < 8; ++e) sum = fmaf(lo[e], lo[e], fmaf(hi[e], hi[e], sum));
       sum = sum_lanes<G>(at.live ? sum : 0.0f);
       const float rstd = 1.0f / sqrtf(fmaf(sum, mean, p.eps));
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        lo[e] *= rstd * (key ? wk[0][e] : wq[0][e]);
-        hi[e] *= rstd * (key ? wk[1][e] : wq[1][e]);
+        lo[e] *= rstd * w[0][e];
+        hi[e] *= rstd * w[1][e];
       }
       if (at.turns) rotate<NEIGHBOURS, 1>(lo, hi, sh.turn[t] + at.pair);
       if (at.live) {
-        T *y = key ? static_cast<T *>(p.out_k) + sh.ok[t] + head : static_cast<T *>(p.out_q) + sh.oq[t] + head;
-        store8(lo, y + at.lo);
-        store8(hi, y + at.hi);
+        T *to = y + sh.y[t] + static_cast<int64_t>(row % side.heads) * p.headdim;
+        store8(lo, to + at.lo);
+        store8(hi, to + at.hi);
       }
     }
     __syncthreads();
@@ -168,34 +212,42 @@ __global__ void __launch_bounds__(256) qk_norm_kernel(const QkNormParams p) {
 template <typename T, int G, bool NEIGHBOURS>
 __global__ void __launch_bounds__(256) qk_norm_bwd_kernel(const QkNormParams p) {
   __shared__ Shared sh;
-  __shared__ float part[256 / G * 16 * G / 2];  // (wavefronts' halves in turn) [group][16 G]
-  const int tid = threadIdx.x, j = tid % G, heads = static_cast<int>(p.nheads + p.nkv);
+  __shared__ float part[256 * 8];  // a piece of every thread
+  const int tid = threadIdx.x, j = tid % G;
+  const Side side = side_of(p);
   const Place at = place_of(p, j);
-  float w[2][2][8], dw[2][2][8] = {};  // [q or k][piece]
+  const T *x = static_cast<const T *>(side.key ? p.k : p.q), *dy = static_cast<const T *>(side.key ? p.dyk : p.dyq);
+  T *dx = static_cast<T *>(side.key ? p.out_k : p.out_q);
+  const float *weights = side.key ? p.wk : p.wq;
+  float w[2][8], dw[2][8] = {};
 #pragma unroll
-  for (int e = 0; e < 8; ++e) w[0][0][e] = w[0][1][e] = w[1][0][e] = w[1][1][e] = 1.0f;
-  if (p.wq != nullptr) load8(w[0][0], p.wq + at.lo), load8(w[0][1], p.wq + at.hi);
-  if (p.wk != nullptr) load8(w[1][0], p.wk + at.lo), load8(w[1][1], p.wk + at.hi);
+  for (int e = 0; e < 8; ++e) w[0][e] = w[1][e] = 1.0f;
+  if (weights != nullptr) load8(w[0], weights + at.lo), load8(w[1], weights + at.hi);
   const float mean = 1.0f / static_cast<float>(p.headdim);
-  for (int64_t first = static_cast<int64_t>(blockIdx.x) * p.tile; first < p.tokens; first += static_cast<int64_t>(gridDim.x) * p.tile) {
-    const int count = p.tokens - first < p.tile ? static_cast<int>(p.tokens - first) : p.tile;
-    begin(p, sh, first, count);
+  for (int64_t first = side.group * side.tile; first < p.tokens; first += side.groups * side.tile) {
+    const int count = p.tokens - first < side.tile ? static_cast<int>(p.tokens - first) : side.tile;
+    begin(p, side, sh, first, count);
     __syncthreads();
-    const int rows = count * heads;
-    for (int row0 = 0; row0 < rows; row0 += 256 / G) {
-      const int row = row0 + tid / G;
-      if (row >= rows) continue;
-      const int t = row / heads, h = row % heads;
-      const bool key = h >= p.nheads;
-      const int64_t n = key ? h - p.nheads : h, head = n * p.headdim;
-      const T *x = key ? static_cast<const T *>(p.k) + sh.k[t] + head : static_cast<const T *>(p.q) + sh.q[t] + head;
-      const T *dy = key ? static_cast<const T *>(p.dyk) + ((first + t) * p.nkv + n) * p.headdim
-                        : static_cast<const T *>(p.dyq) + ((first + t) * p.nheads + n) * p.headdim;
+    const int rows = count * side.heads;
+    Eight<T> next[4];  // x and its output's gradient, as in the forward
+    auto fetch = [&](int row) {
+      row = row < rows ? row : rows - 1;
+      const T *from = x + sh.x[row / side.heads] + static_cast<int64_t>(row % side.heads) * p.headdim;
+      const T *grad = dy + (first * side.heads + row) * p.headdim;
+      next[0].load(from + at.lo);
+      next[1].load(from + at.hi);
+      next[2].load(grad + at.lo);
+      next[3].load(grad + at.hi);
+    };
+    fetch(tid / G);
+    for (int row = tid / G; row < rows; row += 256 / G) {
+      const int t = row / side.heads;
       float lo[8], hi[8], dlo[8], dhi[8], sum = 0.0f;
-      load8(lo, x + at.lo);
-      load8(hi, x + at.hi);
-      load8(dlo, dy + at.lo);
-      load8(dhi, dy + at.hi);
+      next[0].get(lo);
+      next[1].get(hi);
+      next[2].get(dlo);
+      next[3].get(dhi);
+      fetch(row + 256 / G);
 #pragma unroll
       for (int e = 0; e < 8; ++e) sum = fmaf(lo[e], lo[e], fmaf(hi[e], hi[e], sum));
       sum = sum_lanes<G>(at.live ? sum : 0.0f);
@@ -206,13 +258,10 @@ __global__ void __launch_bounds__(256) qk_norm_bwd_kernel(const QkNormParams p) 
       for (int e = 0; e < 8; ++e) {
         lo[e] *= rstd;
         hi[e] *= rstd;
-        const float a = dlo[e] * lo[e], b = dhi[e] * hi[e];
-        dw[0][0][e] += key ? 0.0f : a;
-        dw[0][1][e] += key ? 0.0f : b;
-        dw[1][0][e] += key ? a : 0.0f;
-        dw[1][1][e] += key ? b : 0.0f;
-        dlo[e] *= key ? w[1][0][e] : w[0][0][e];
-        dhi[e] *= key ? w[1][1][e] : w[0][1][e];
+        dw[0][e] = fmaf(dlo[e], lo[e], dw[0][e]);
+        dw[1][e] = fmaf(dhi[e], hi[e], dw[1][e]);
+        dlo[e] *= w[0][e];
+        dhi[e] *= w[1][e];
         dot = fmaf(dlo[e], lo[e], fmaf(dhi[e], hi[e], dot));
       }
       dot = sum_lanes<G>(at.live ? dot : 0.0f) * mean;
@@ -222,9 +271,9 @@ __global__ void __launch_bounds__(256) qk_norm_bwd_kernel(const QkNormParams p) 
         hi[e] = rstd * fmaf(-hi[e], dot, dhi[e]);
       }
       if (at.live) {
-        T *dx = key ? static_cast<T *>(p.out_k) + sh.ok[t] + head : static_cast<T *>(p.out_q) + sh.oq[t] + head;
-        store8(lo, dx + at.lo);
-        store8(hi, dx + at.hi);
+        T *to = dx + sh.y[t] + static_cast<int64_t>(row % side.heads) * p.headdim;
+        store8(lo, to + at.lo);
+        store8(hi, to + at.hi);
       }
     }
     __syncthreads();
@@ -233,29 +282,32 @@ __global__ void __launch_bounds__(256) qk_norm_bwd_kernel(const QkNormParams p) 
   // The groups' terms, one piece at a time, in a fixed order.
   constexpr int N = 256 / G;
 #pragma unroll
-  for (int x = 0; x < 2; ++x)
+  for (int piece = 0; piece < 2; ++piece) {
 #pragma unroll
-    for (int piece = 0; piece < 2; ++piece) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) part[tid * 8 + e] = dw[x][piece][e];
-      __syncthreads();
-      if (tid < 8 * G && 16 * (tid / 8) < p.headdim) {
-        float sum = 0.0f;
-        for (int k = 0; k < N; ++k) sum += part[k * 8 * G + tid];
-        const Place to = place_of(p, tid / 8);
-        p.ws[(static_cast<int64_t>(blockIdx.x) * 2 + x) * p.headdim + (piece != 0 ? to.hi : to.lo) + tid % 8] = sum;
-      }
-      __syncthreads();
+    for (int e = 0; e < 8; ++e) part[tid * 8 + e] = dw[piece][e];
+    __syncthreads();
+    if (tid < 8 * G && 16 * (tid / 8) < p.headdim) {
+      float sum = 0.0f;
+      for (int k = 0; k < N; ++k) sum += part[k * 8 * G + tid];
+      const Place to = place_of(p, tid / 8);
+      p.ws[static_cast<int64_t>(blockIdx.x) * p.headdim + (piece != 0 ? to.hi : to.lo) + tid % 8] = sum;
     }
+    __syncthreads();
+  }
 }
 
 // dw = the sum over the workgroups' terms: 16 columns by 64 threads of a share each.
-__global__ void __launch_bounds__(1024) qk_norm_sum_kernel(const QkNormParams p, int parts) {
+__global__ void __launch_bounds__(1024) qk_norm_sum_kernel(const QkNormParams p, int nk) {
   __shared__ float sums[64][17];
-  const int c = threadIdx.x % 16, k = threadIdx.x / 16, col = blockIdx.x * 16 + c;
-  const int64_t step = 2 * p.headdim;
+  const int tiles = p.headdim / 16;
+  const bool key = static_cast<int>(blockIdx.x) >= tiles;
+  const int c = threadIdx.x % 16, k = threadIdx.x / 16, col = (blockIdx.x - (key ? tiles : 0)) * 16 + c;
+  float *to = key ? p.dwk : p.dwq;
+  if (to == nullptr) return;
+  const int64_t parts = key ? nk : p.nq;
+  const float *from = p.ws + (key ? p.nq * p.headdim : 0) + col;
   float sum = 0.0f;
-  for (int i = k; i < parts; i += 64) sum += p.ws[i * step + col];
+  for (int64_t i = k; i < parts; i += 64) sum += from[i * p.headdim];
   sums[k][c] = sum;
   __syncthreads();
   if (k >= 4) return;
@@ -264,9 +316,7 @@ __global__ void __launch_bounds__(1024) qk_norm_sum_kernel(const QkNormParams p,
   for (int i = 0; i < 16; ++i) sum += sums[16 * k + i][c];
   sum += __shfl_down(sum, 32);
   sum += __shfl_down(sum, 16);
-  if (k != 0) return;
-  float *to = col < p.headdim ? p.dwq : p.dwk;
-  if (to != nullptr) to[col % p.headdim] = sum;
+  if (k == 0) to[col] = sum;
 }
 
 template <typename T, int G>
@@ -281,43 +331,65 @@ void run(const QkNormParams &p, bool bwd, unsigned groups, hipStream_t s) {
   }
 }
 
+// Lanes of 16 elements that share a head.
+int lanes_of(int64_t headdim) { return headdim > 128 ? 16 : headdim > 64 ? 8 : headdim > 32 ? 4 : 2; }
+
 template <typename T>
 void run(const QkNormParams &p, bool bwd, unsigned groups, hipStream_t s) {
-  if (p.headdim > 128) run<T, 16>(p, bwd, groups, s);
-  else if (p.headdim > 64) run<T, 8>(p, bwd, groups, s);
-  else if (p.headdim > 32) run<T, 4>(p, bwd, groups, s);
-  else run<T, 2>(p, bwd, groups, s);
+  switch (lanes_of(p.headdim)) {
+    case 16: run<T, 16>(p, bwd, groups, s); break;
+    case 8: run<T, 8>(p, bwd, groups, s); break;
+    case 4: run<T, 4>(p, bwd, groups, s); break;
+    default: run<T, 2>(p, bwd, groups, s);
+  }
 }
 
-// Tokens that a workgroup takes at a time: one where there are few, so that
-// all of the chip has some; more share the work of a workgroup's beginning.
-int tile_of(int64_t tokens) { return tokens >= 16384 ? kMaxTile : tokens >= 4096 ? 2 : 1; }
+// Tokens that a workgroup takes at a time: as many as its lanes have heads for,
+// and up to four times those while 512 workgroups are left, which share the
+// work of a workgroup's beginning.  Forward of 16 and 4 heads of 128: 512 tokens
+// take 6.1 us, with 8 at a time 10.5; 8192 take 26.8, with 1 at a time 30.6.
+int tile_of(int64_t tokens, int64_t heads, int64_t headdim) {
+  const int64_t rows = 256 / lanes_of(headdim), most = tokens / 512;
+  int tile = 1;
+  while (tile < kMaxTile && (2 * tile * heads <= rows || (2 * tile * heads <= 4 * rows && 2 * tile <= most))) tile *= 2;
+  return tile;
+}
 
 }  // namespace
 
-// Workgroups of the backward, and so the terms of dwq and dwk.
-int64_t qk_norm_parts(int64_t tokens) {
-  const int64_t n = (tokens + tile_of(tokens) - 1) / tile_of(tokens);
-  return n < 1024 ? n : 1024;
+QkNormGroups qk_norm_groups(int64_t tokens, int64_t nheads, int64_t nkv, int64_t headdim, bool bwd) {
+  QkNormGroups n;
+  n.tile_q = tile_of(tokens, nheads, headdim);
+  n.tile_k = tile_of(tokens, nkv, headdim);
+  const int64_t tq = (tokens + n.tile_q - 1) / n.tile_q, tk = (tokens + n.tile_k - 1) / n.tile_k;
+  // The backward's workgroups each leave a term of dw.  768 are there at once
+  // (2048 tokens of 16 and 4 heads of 128: 13.6 us, with at most 512 17.6); what
+  // takes more goes round in 512 (4096 tokens of 64 and 8: 78 us, in 768 80; the
+  // sum of their terms 4.7, of 1024 6.8).
+  const int64_t most = bwd ? (tq + tk <= 768 ? 768 : 512) : int64_t{1} << 21;
+  // Shares by the heads: a workgroup of either side has about the same rows.
+  const int64_t share = most * nheads / (nheads + nkv), mq = share < 1 ? 1 : share < most ? share : most - 1;
+  n.q = tq + tk <= most || tq < mq ? tq : mq;
+  n.k = tq + tk <= most || tk < most - mq ? tk : most - mq;
+  return n;
 }
 
-hipError_t launch_qk_norm(const QkNormParams &p0, int bf16, hipStream_t s) {
+namespace {
+hipError_t launch(const QkNormParams &p0, int bf16, bool bwd, hipStream_t s) {
   QkNormParams p = p0;
-  p.tile = tile_of(p.tokens);
-  const int64_t n = (p.tokens + p.tile - 1) / p.tile;
-  const unsigned groups = static_cast<unsigned>(n < (1 << 20) ? n : 1 << 20);
-  bf16 ? run<uint16_t>(p, false, groups, s) : run<float>(p, false, groups, s);
-  return hipGetLastError();
-}
-
-hipError_t launch_qk_norm_bwd(const QkNormParams &p0, int bf16, hipStream_t s) {
-  QkNormParams p = p0;
-  p.tile = tile_of(p.tokens);
-  const int parts = static_cast<int>(qk_norm_parts(p.tokens));
-  if (parts > 0) bf16 ? run<uint16_t>(p, true, static_cast<unsigned>(parts), s) : run<float>(p, true, static_cast<unsigned>(parts), s);
+  const QkNormGroups n = qk_norm_groups(p.tokens, p.nheads, p.nkv, p.headdim, bwd);
+  p.nq = n.q;
+  p.tile_q = n.tile_q;
+  p.tile_k = n.tile_k;
+  const unsigned groups = static_cast<unsigned>(n.q + n.k);
+  if (groups > 0) bf16 ? run<uint16_t>(p, bwd, groups, s) : run<float>(p, bwd, groups, s);
   if (p.dwq != nullptr || p.dwk != nullptr)  // (without tokens, too: zeros)
-    hipLaunchKernelGGL(qk_norm_sum_kernel, dim3(static_cast<uint32_t>(2 * p.headdim / 16)), dim3(1024), 0, s, p, parts);
+    hipLaunchKernelGGL(qk_norm_sum_kernel, dim3(static_cast<uint32_t>(2 * p.headdim / 16)), dim3(1024), 0, s, p, static_cast<int>(n.k));
   return hipGetLastError();
 }
+}  // namespace
+
+hipError_t launch_qk_norm(const QkNormParams &p, int bf16, hipStream_t s) { return launch(p, bf16, false, s); }
+hipError_t launch_qk_norm_bwd(const QkNormParams &p, int bf16, hipStream_t s) { return launch(p, bf16, true, s); }
 
 }  // namespace ssmb
