@@ -213,7 +213,7 @@ __device__ __forceinline__ void copy16(unsigned lds, const i4 &from, unsigned la
 // N KiB from `from` (this lane's 16 bytes at lane_off) to LDS, in order.
 template <int N>
 __device__ __forceinline__ void copy_kib(unsigned lds, const void *from, unsigned lane_off) {
-  static_assert(N >= 1 && N <= 4, "the immediate offset");
+  static_assert(N >= 1 && N <= 3, "the immediate offset");
   if constexpr (N == 1)
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" : : "s"(lds), "v"(lane_off), "s"(from) : "memory", "m0");
   else if constexpr (N == 2)
@@ -221,15 +221,9 @@ __device__ __forceinline__ void copy_kib(unsigned lds, const void *from, unsigne
                  :
                  : "s"(lds), "v"(lane_off), "s"(from)
                  : "memory", "m0");
-  else if constexpr (N == 3)
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2\n\tglobal_load_lds_dwordx4 %1, %2 offset:1024"
-                 "\n\tglobal_load_lds_dwordx4 %1, %2 offset:2048"
-                 :
-                 : "s"(lds), "v"(lane_off), "s"(from)
-                 : "memory", "m0");
   else
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2\n\tglobal_load_lds_dwordx4 %1, %2 offset:1024"
-                 "\n\tglobal_load_lds_dwordx4 %1, %2 offset:2048\n\tglobal_load_lds_dwordx4 %1, %2 offset:3072"
+                 "\n\tglobal_load_lds_dwordx4 %1, %2 offset:2048"
                  :
                  : "s"(lds), "v"(lane_off), "s"(from)
                  : "memory", "m0");
@@ -242,10 +236,10 @@ __device__ __forceinline__ void copy_share(unsigned lds, const char *from, int w
   lds = __builtin_amdgcn_readfirstlane(lds + w * kEach * 1024);
   from = uniform(from + w * kEach * 1024);
 #pragma unroll
-  for (int k = 0; k < kLast; k += 4) {
-    constexpr int kRest = kLast % 4;
-    if (k + 4 <= kLast) copy_kib<4>(lds + k * 1024, from + k * 1024, lane_off);
-    else copy_kib<kRest != 0 ? kRest : 4>(lds + k * 1024, from + k * 1024, lane_off);
+  for (int k = 0; k < kLast; k += 3) {
+    constexpr int kRest = kLast % 3;
+    if (k + 3 <= kLast) copy_kib<3>(lds + k * 1024, from + k * 1024, lane_off);
+    else copy_kib<kRest != 0 ? kRest : 3>(lds + k * 1024, from + k * 1024, lane_off);
   }
   if constexpr (kEach > kLast) {
     if (w < NW - 1)
