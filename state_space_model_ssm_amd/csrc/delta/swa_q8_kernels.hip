@@ -18,6 +18,7 @@
 namespace ssmb {
 namespace {
 
+constexpr int kMaxSplits = 1024;
 typedef __attribute__((ext_vector_type(2))) int i2;
 typedef __attribute__((ext_vector_type(2))) __bf16 bf2;
 
@@ -189,9 +190,14 @@ __global__ void __launch_bounds__(256, 2) swa_q8_step_kernel(const SwaStepParams
   const int tid = threadIdx.x, lane = tid & 63, m = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const unsigned nkv = static_cast<unsigned>(p.nkv), group = static_cast<unsigned>(p.nheads) / nkv;
-  // Workgroups of a (row, key head): `splits` for each block of 16 heads, and
-  // one that stores the near block in the ring if it has become whole.
-  const unsigned each_row = splits * qblocks + 1, bc = blockIdx.x / each_row, rest = blockIdx.x % each_row;
+  // First a workgroup per (row, key head) that stores the near block in the
+  // ring if it has become whole; then `splits` for each block of 16 heads.
+  // (Beside those of their row, the ones that mostly have nothing to do would
+  // all fall to the same XCDs: 100 sequences, 8 key heads of 128, window 1024,
+  // 3 splits 66 us, now 46.)
+  const unsigned rows = static_cast<unsigned>(p.batch) * nkv, each_row = splits * qblocks;
+  const bool stores = blockIdx.x < rows;
+  const unsigned id = stores ? blockIdx.x * each_row : blockIdx.x - rows, bc = id / each_row, rest = id % each_row;
   const unsigned split = rest % splits, qb = rest / splits;
   const int64_t b = bc / nkv, c = bc % nkv;
   const int g0 = qb * 16, heads = static_cast<int>(group) - g0 < 16 ? static_cast<int>(group) - g0 : 16;
@@ -204,7 +210,7 @@ __global__ void __launch_bounds__(256, 2) swa_q8_step_kernel(const SwaStepParams
   const uint16_t *kn = p.k + b * p.k_batch + c * D, *vn = p.v + b * p.v_batch + c * D;
   uint16_t *near_k = cache.k_near + static_cast<int64_t>(bc) * (sinks + kSwaBlock) * D;
   uint16_t *near_v = cache.v_near + static_cast<int64_t>(bc) * (sinks + kSwaBlock) * D;
-  if (qb == qblocks) {
+  if (stores) {
     if (pos < sinks || off != 63) return;
     // (No other workgroup reads the block of the ring that it replaces, nor writes what is near but the token's own place.)
     const int64_t to = static_cast<int64_t>(bc) * blocks + now % blocks;
@@ -365,6 +371,44 @@ __global__ void __launch_bounds__(256, 2) swa_q8_step_kernel(const SwaStepParams
   }
 }
 
+// Join the splits of a head.  The splits' factors, which all its elements take,
+// are made first, by all threads; then 256 / D threads share an element.
+template <int D>
+__global__ void __launch_bounds__(256) swa_q8_join_kernel(const SwaStepParams p, int splits) {
+  constexpr int NG = 256 / D;
+  __shared__ float factor[kMaxSplits], best_of[4], all_of[4], sums[NG][D];
+  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+  const int64_t head = blockIdx.x;
+  const float *stat = p.ws_stat + head * splits * 2, *part = p.ws_o + head * splits * D;
+  float best = -INFINITY, all = 0.0f;
+  for (int k = tid; k < splits; k += 256) best = fmaxf(best, stat[2 * k]);
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) best = fmaxf(best, __shfl_xor(best, d));
+  if (lane == 0) best_of[w] = best;
+  __syncthreads();
+  best = fmaxf(fmaxf(best_of[0], best_of[1]), fmaxf(best_of[2], best_of[3]));
+  for (int k = tid; k < splits; k += 256) {
+    const float f = stat[2 * k] == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(stat[2 * k] - best);
+    factor[k] = f;
+    all = fmaf(f, stat[2 * k + 1], all);
+  }
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) all += __shfl_xor(all, d);
+  if (lane == 0) all_of[w] = all;
+  __syncthreads();
+  const int e = tid % D, group = tid / D;
+  float acc = 0.0f;
+#pragma unroll 8
+  for (int k = group; k < splits; k += NG) acc = fmaf(factor[k], part[static_cast<int64_t>(k) * D + e], acc);
+  sums[group][e] = acc;
+  __syncthreads();
+  if (group != 0) return;
+#pragma unroll
+  for (int k = 1; k < NG; ++k) acc += sums[k][e];
+  all = (all_of[0] + all_of[1]) + (all_of[2] + all_of[3]);
+  st(p.y, head * D + e, all == 0.0f ? 0.0f : acc / all);
+}
+
 // A workgroup per (row, key head, block of the ring), and one for what is
 // near.  Block r of the ring holds, of the `whole` complete blocks of the
 // row's positions behind the sinks, the last whose number is r mod the ring's.
@@ -425,10 +469,14 @@ __global__ void __launch_bounds__(256) swa_q8_fill_kernel(const SwaParams p, con
 }  // namespace
 
 int swa_q8_splits(int64_t batch, int64_t nheads, int64_t nkv, int64_t window, int64_t sinks) {
-  // Four workgroups per CU even out rows of unequal length; a wavefront has at least one tile.
+  // As many workgroups as there is LDS for at once, two per CU; a wavefront has
+  // at least one tile.  32 heads on 8 of 128: 64 sequences, window 4096, 1 split
+  // 104 us, 2 and their join 110; 64, window 1024, 29 and 37; 4, window 4096, 16
+  // splits 15, 18 (of a tile each) 18.
   const int64_t rows = batch * nkv * ((nheads / nkv + 15) / 16), tiles = window / kSwaBlock + (sinks + kSwaBlock + 31) / 32;
-  const int64_t want = (1024 + rows - 1) / (rows > 0 ? rows : 1), most = (tiles + 3) / 4;
-  return static_cast<int>(want < most ? want : most);
+  const int64_t want = (512 + rows - 1) / (rows > 0 ? rows : 1), most = (tiles + 3) / 4;
+  const int64_t n = want < most ? want : most;
+  return static_cast<int>(n < kMaxSplits ? n : kMaxSplits);
 }
 
 hipError_t launch_swa_q8_step(const SwaStepParams &p, const SwaQ8Cache &cache, int splits, hipStream_t s) {
@@ -436,10 +484,10 @@ hipError_t launch_swa_q8_step(const SwaStepParams &p, const SwaQ8Cache &cache, i
   const dim3 g(static_cast<uint32_t>(p.batch * p.nkv * (qblocks * splits + 1))), gj(static_cast<uint32_t>(p.batch * p.nheads));
   if (p.headdim == 64) {
     hipLaunchKernelGGL((swa_q8_step_kernel<64>), g, dim3(256), 0, s, p, cache, sp, qblocks);
-    if (splits > 1) hipLaunchKernelGGL((swa_join_kernel<64>), gj, dim3(64), 0, s, p, splits);
+    if (splits > 1) hipLaunchKernelGGL((swa_q8_join_kernel<64>), gj, dim3(256), 0, s, p, splits);
   } else {
     hipLaunchKernelGGL((swa_q8_step_kernel<128>), g, dim3(256), 0, s, p, cache, sp, qblocks);
-    if (splits > 1) hipLaunchKernelGGL((swa_join_kernel<128>), gj, dim3(128), 0, s, p, splits);
+    if (splits > 1) hipLaunchKernelGGL((swa_q8_join_kernel<128>), gj, dim3(256), 0, s, p, splits);
   }
   return hipGetLastError();
 }
