@@ -73,7 +73,7 @@ GdrParams params(const ssm_gdr_dims_t &d) {
   p.kdim = static_cast<int32_t>(d.kdim);
   p.vdim = static_cast<int32_t>(d.vdim);
   p.gates_bf16 = d.gate_dtype == SSM_BF16;
-  p.seg = gdr_segments(d.batch * d.nheads, d.vdim, p.chunks);
+  p.seg = gdr_segments(d.batch * d.nheads, d.kdim, d.vdim, p.chunks);
   return p;
 }
 

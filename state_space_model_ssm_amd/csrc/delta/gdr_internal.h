@@ -30,7 +30,7 @@ constexpr size_t gdr_saved_bytes(int64_t kdim, int64_t vdim) { return gdr_both_b
 struct GdrSegments {
   int64_t count, chunks;
 };
-GdrSegments gdr_segments(int64_t heads, int64_t vdim, int64_t chunks);
+GdrSegments gdr_segments(int64_t heads, int64_t kdim, int64_t vdim, int64_t chunks);
 
 struct GdrParams {
   const uint16_t *q, *k, *v;   // bf16
@@ -51,7 +51,7 @@ struct GdrParams {
   char *ws_both;               // the backward's dS and D: gdr_both_bytes() each
   GdrSegments seg;
   float *ws_state;             // (row, value head, segment): E, and then the state before the segment
-  uint16_t *ws_carry;          // (row, value head, segment, part): P, (kdim in, kdim out)
+  uint16_t *ws_carry;          // (row, value head, segment): P, as operands in two parts
   int64_t batch, seqlen, nqk, nheads, chunks;
   int64_t q_batch, q_token, k_batch, k_token, v_batch, v_token;
   float scale;

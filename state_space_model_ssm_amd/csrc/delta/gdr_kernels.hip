@@ -463,67 +463,88 @@ __global__ void __launch_bounds__(256, 2) gdr_segment_kernel(const GdrParams p) 
 #pragma unroll
     for (int j = 0; j < NB; ++j) *reinterpret_cast<f4v *>(to + 32 * (j / 2) + 4 * (j % 2)) = s[j];
   } else {
-    uint16_t *to = p.ws_carry + (seg * 2 * KD + col) * KD + 8 * g;
+    // P as the join's operands, [16 key elements out][32 in][part], 1 KiB each: turned round in LDS.
+    typedef __attribute__((address_space(3))) u4 lds16;
+    meet();
 #pragma unroll
     for (int a = 0; a < NS; ++a) {
       const Parts sp = parts(s[2 * a], s[2 * a + 1]);
-      *reinterpret_cast<bf8 *>(to + 32 * a) = sp.hi;
-      *reinterpret_cast<bf8 *>(to + KD * KD + 32 * a) = sp.lo;
+      *(lds16 *)(base + (w * NS + a) * 2048 + lane * 16) = __builtin_bit_cast(u4, sp.hi);
+      *(lds16 *)(base + (w * NS + a) * 2048 + 1024 + lane * 16) = __builtin_bit_cast(u4, sp.lo);
     }
+    meet();
+    const unsigned left = base + (w & ~1) * NS * 2048;
+    char *to = reinterpret_cast<char *>(p.ws_carry + seg * 2 * KD * KD) + (2 * (tile - vtiles) + w / 2) * 2048 + lane * 16;
+#pragma unroll
+    for (int i = 0; i < NB / 2; ++i)
+#pragma unroll
+      for (int part = 0; part < 2; ++part)
+        *reinterpret_cast<bf8 *>(to + (2 * i + w % 2) * NS * 2048 + part * 1024) = turned<true>(left, left + NS * 2048, 2 * i + w % 2, part, lane);
   }
 }
 
-// The state before each segment, 64 columns a workgroup.
+// The state before each segment, P S + E of the one before: 16 columns a
+// workgroup, a quarter of the key elements a wavefront.  Each takes its part of
+// P from memory, one segment ahead, and the columns' state from LDS, where all
+// four leave theirs.  1.2 us a segment (keys of 64: 0.4); with 64 columns a
+// workgroup and P in LDS 4.3.
 template <int KD>
 __global__ void __launch_bounds__(256) gdr_join_kernel(const GdrParams p) {
-  constexpr int NS = KD / 32, NB = KD / 16;
-  constexpr unsigned kPart = KD * KD * 2, kBuffer = 2 * kPart;
-  __shared__ __align__(16) u4 lds[2 * kBuffer / 16];
+  constexpr int NS = KD / 32, NB = KD / 16, NJ = NB / 4;
+  __shared__ __align__(16) u4 lds[2][NS * 2 * 64];
   const int tid = threadIdx.x, lane = tid & 63, m = lane & 15, g = lane >> 4;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const unsigned vtiles = static_cast<unsigned>(p.vdim) / 64;
-  const int64_t bh = blockIdx.x / vtiles, b = bh / p.nheads;
-  const int col = static_cast<int>(blockIdx.x % vtiles) * 64 + 16 * w + m, len = gdr_length(p.lengths, b, p.seqlen);
+  const HeadTile which = head_tile(blockIdx.x, static_cast<unsigned>(p.batch * p.nheads), static_cast<unsigned>(p.vdim) / 16);
+  const int64_t bh = which.head, b = bh / p.nheads;
+  const int col = static_cast<int>(which.tile) * 16 + m, len = gdr_length(p.lengths, b, p.seqlen);
   const int span = static_cast<int>(p.seg.chunks) * 64, n = (len + span - 1) / span;  // segments of this row
-  f4v s[NB], next[NB];
-  const int64_t state = (bh * p.vdim + col) * KD + 8 * g;
-  float *begin = p.ws_state + (bh * p.seg.count * p.vdim + col) * KD + 8 * g;
+  // This wavefront's blocks of 16 key elements, as they come out of a product: 16 j + 4g + r.
+  const int at = 16 * NJ * w + 4 * g;
+  float *begin = p.ws_state + (bh * p.seg.count * p.vdim + col) * KD + at;
+  const char *carry = reinterpret_cast<const char *>(p.ws_carry + bh * p.seg.count * 2 * KD * KD) + NJ * w * NS * 2048 + lane * 16;
+  f4v s[NJ], next[NJ];
+  Parts pp[NJ][NS];
+  auto fetch = [&](int i) {
 #pragma unroll
-  for (int j = 0; j < NB; ++j) {
-    s[j] = p.h0 != nullptr ? *reinterpret_cast<const f4v *>(p.h0 + state + 32 * (j / 2) + 4 * (j % 2)) : f4v{};
-    *reinterpret_cast<f4v *>(begin + 32 * (j / 2) + 4 * (j % 2)) = s[j];
-  }
-  if (n < 2) return;
-  const unsigned base = lds_at(lds);
-  const unsigned from = static_cast<unsigned>(slot<KD>(8 * g + (m >> 2), m & 3)) * 16;
-  auto fetch = [&](int i) {  // both parts of P, rows of KD elements laid out by slot<KD>()
-    const uint16_t *src = p.ws_carry + (bh * p.seg.count + i) * 2 * KD * KD;
-    load_tile<KD, 256, KD>(lds + (i & 1) * (kBuffer / 16), src, KD, 0, KD - 1, tid);
-    load_tile<KD, 256, KD>(lds + ((i & 1) * kBuffer + kPart) / 16, src + KD * KD, KD, 0, KD - 1, tid);
-  };
-  fetch(0);
-  for (int i = 0; i + 1 < n; ++i) {
-    float *to = p.ws_state + ((bh * p.seg.count + i + 1) * p.vdim + col) * KD + 8 * g;
+    for (int j = 0; j < NJ; ++j) {
+      next[j] = *reinterpret_cast<const f4v *>(begin + static_cast<int64_t>(i + 1) * p.vdim * KD + 16 * j);
 #pragma unroll
-    for (int j = 0; j < NB; ++j) next[j] = *reinterpret_cast<const f4v *>(to + 32 * (j / 2) + 4 * (j % 2));
-    arrive();
-    if (i + 2 < n) fetch(i + 1);
-    const unsigned tile = base + (i & 1) * kBuffer + from;
-#pragma unroll
-    for (int a = 0; a < NS; ++a) {
-      const Parts sp = parts(s[2 * a], s[2 * a + 1]);
-#pragma unroll
-      for (int j = 0; j < NB; ++j) {
-        const unsigned at = (tile ^ (64 * (j / 2))) + 8 * (j % 2) + a * 64 * KD;
-        next[j] = mul_parts(Parts{values16<KD>(at), values16<KD>(at + kPart)}, sp, next[j]);
+      for (int a = 0; a < NS; ++a) {
+        const char *from = carry + static_cast<int64_t>(i) * 4 * KD * KD + (j * NS + a) * 2048;
+        pp[j][a] = {*reinterpret_cast<const bf8 *>(from), *reinterpret_cast<const bf8 *>(from + 1024)};
       }
     }
+  };
+  if (n > 1) fetch(0);
 #pragma unroll
-    for (int j = 0; j < NB; ++j) {
-      s[j] = next[j];
-      *reinterpret_cast<f4v *>(to + 32 * (j / 2) + 4 * (j % 2)) = s[j];
+  for (int j = 0; j < NJ; ++j) {
+    s[j] = p.h0 != nullptr ? *reinterpret_cast<const f4v *>(p.h0 + (bh * p.vdim + col) * KD + at + 16 * j) : f4v{};
+    *reinterpret_cast<f4v *>(begin + 16 * j) = s[j];
+  }
+  for (int i = 0; i + 1 < n; ++i) {
+    char *mine = reinterpret_cast<char *>(lds[i & 1]);
+    if constexpr (NJ == 2) {
+      const Parts sp = parts(s[0], s[1]);
+      *reinterpret_cast<bf8 *>(mine + w * 2048 + lane * 16) = sp.hi;
+      *reinterpret_cast<bf8 *>(mine + w * 2048 + 1024 + lane * 16) = sp.lo;
+    } else {
+      const Parts sp = parts(s[0], s[0]);
+      *reinterpret_cast<u2 *>(mine + w / 2 * 2048 + lane * 16 + w % 2 * 8) = half_of(sp.hi, 0);
+      *reinterpret_cast<u2 *>(mine + w / 2 * 2048 + 1024 + lane * 16 + w % 2 * 8) = half_of(sp.lo, 0);
     }
-    meet();
+    __syncthreads();  // (What is read here is written again after the next one.)
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) s[j] = next[j];
+#pragma unroll
+    for (int a = 0; a < NS; ++a) {
+      const Parts sp = {*reinterpret_cast<const bf8 *>(mine + a * 2048 + lane * 16),
+                        *reinterpret_cast<const bf8 *>(mine + a * 2048 + 1024 + lane * 16)};
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) s[j] = mul_parts(pp[j][a], sp, s[j]);
+    }
+    if (i + 2 < n) fetch(i + 1);
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) *reinterpret_cast<f4v *>(begin + static_cast<int64_t>(i + 1) * p.vdim * KD + 16 * j) = s[j];
   }
 }
 
@@ -539,21 +560,19 @@ __device__ __forceinline__ float sum8(float v) {
   return v;
 }
 
-// 8 lanes share a row of the state (a value element), 32 R rows a workgroup.
-template <int KD, int R, typename G>
+// 8 lanes share a row of the state (a value element), 32 rows a workgroup.
+template <int KD, typename G>
 __global__ void __launch_bounds__(256) gdr_step_kernel(const GdrParams p) {
   constexpr int NP = KD / 32;  // pieces of 4 floats per lane
   const int tid = threadIdx.x, e = tid & 7;
-  const unsigned vtiles = static_cast<unsigned>(p.vdim) / (32 * R);
+  const unsigned vtiles = static_cast<unsigned>(p.vdim) / 32;
   const int64_t vt = blockIdx.x % vtiles, bh = blockIdx.x / vtiles, b = bh / p.nheads, h = bh % p.nheads;
   const int64_t hk = h / (p.nheads / p.nqk);
-  const int row0 = static_cast<int>(vt) * 32 * R + (tid >> 3);
-  f4v s[R][NP], k[NP], q[NP];
-  const float *from = p.h0 + (bh * p.vdim + row0) * KD + 4 * e;
+  const int row = static_cast<int>(vt) * 32 + (tid >> 3);
+  f4v s[NP], k[NP], q[NP];
+  const float *from = p.h0 + (bh * p.vdim + row) * KD + 4 * e;
 #pragma unroll
-  for (int r = 0; r < R; ++r)
-#pragma unroll
-    for (int a = 0; a < NP; ++a) s[r][a] = *reinterpret_cast<const f4v *>(from + r * 32 * KD + 32 * a);
+  for (int a = 0; a < NP; ++a) s[a] = *reinterpret_cast<const f4v *>(from + 32 * a);
   float kq = 0.0f;
 #pragma unroll
   for (int a = 0; a < NP; ++a) {
@@ -568,25 +587,21 @@ __global__ void __launch_bounds__(256) gdr_step_kernel(const GdrParams p) {
   }
   kq = sum8(kq);
   const float decay = __builtin_amdgcn_exp2f(gate<G>(p.g, bh) * kLog2e), beta = gate<G>(p.beta, bh);
-  float *to = p.h_last + (bh * p.vdim + row0) * KD + 4 * e;
+  float *to = p.h_last + (bh * p.vdim + row) * KD + 4 * e;
+  float sk = 0.0f, sq = 0.0f;
 #pragma unroll
-  for (int r = 0; r < R; ++r) {
-    float sk = 0.0f, sq = 0.0f;
+  for (int a = 0; a < NP; ++a)
 #pragma unroll
-    for (int a = 0; a < NP; ++a)
+    for (int i = 0; i < 4; ++i) {
+      sk = fmaf(s[a][i], k[a][i], sk);
+      sq = fmaf(s[a][i], q[a][i], sq);
+    }
+  sk = sum8(sk);
+  sq = sum8(sq);
+  const float u = beta * fmaf(-decay, sk, ld(p.v, b * p.v_batch + h * p.vdim + row));
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        sk = fmaf(s[r][a][i], k[a][i], sk);
-        sq = fmaf(s[r][a][i], q[a][i], sq);
-      }
-    sk = sum8(sk);
-    sq = sum8(sq);
-    const float v = ld(p.v, b * p.v_batch + h * p.vdim + row0 + 32 * r);
-    const float u = beta * fmaf(-decay, sk, v);
-#pragma unroll
-    for (int a = 0; a < NP; ++a) *reinterpret_cast<f4v *>(to + r * 32 * KD + 32 * a) = s[r][a] * decay + k[a] * u;
-    if (e == 0) st(p.y, bh * p.vdim + row0 + 32 * r, p.scale * fmaf(decay, sq, u * kq));
-  }
+  for (int a = 0; a < NP; ++a) *reinterpret_cast<f4v *>(to + 32 * a) = s[a] * decay + k[a] * u;
+  if (e == 0) st(p.y, bh * p.vdim + row, p.scale * fmaf(decay, sq, u * kq));
 }
 
 template <int KD, typename G>
@@ -602,7 +617,7 @@ hipError_t fwd(const GdrParams &p, hipStream_t s) {
   if (p.seg.count > 1) {
     const int64_t parts = heads * (p.seg.count - 1) * ((p.vdim + KD) / 64);
     hipLaunchKernelGGL((gdr_segment_kernel<KD>), dim3(static_cast<uint32_t>(parts)), dim3(256), 0, s, p);
-    hipLaunchKernelGGL((gdr_join_kernel<KD>), dim3(static_cast<uint32_t>(heads * (p.vdim / 64))), dim3(256), 0, s, p);
+    hipLaunchKernelGGL((gdr_join_kernel<KD>), dim3(static_cast<uint32_t>(heads * (p.vdim / 16))), dim3(256), 0, s, p);
   }
   hipLaunchKernelGGL((gdr_fwd_kernel<KD>), dim3(static_cast<uint32_t>(heads * (p.vdim / 32) * p.seg.count)), dim3(256), 0, s, p);
   return hipGetLastError();
@@ -611,25 +626,30 @@ hipError_t fwd(const GdrParams &p, hipStream_t s) {
 template <int KD, typename G>
 hipError_t step(const GdrParams &p, hipStream_t s) {
   const int64_t heads = p.batch * p.nheads;
-  if (heads * (p.vdim / 32) < 2048)
-    hipLaunchKernelGGL((gdr_step_kernel<KD, 1, G>), dim3(static_cast<uint32_t>(heads * (p.vdim / 32))), dim3(256), 0, s, p);
-  else
-    hipLaunchKernelGGL((gdr_step_kernel<KD, 2, G>), dim3(static_cast<uint32_t>(heads * (p.vdim / 64))), dim3(256), 0, s, p);
+  hipLaunchKernelGGL((gdr_step_kernel<KD, G>), dim3(static_cast<uint32_t>(heads * (p.vdim / 32))), dim3(256), 0, s, p);
   return hipGetLastError();
 }
 
 }  // namespace
 
-GdrSegments gdr_segments(int64_t heads, int64_t vdim, int64_t chunks) {
-  // In turn a chunk takes 2 us.  With G segments each is gone through twice, 3.6
-  // us a chunk in all while there are compute units for them (a workgroup of
-  // the second pass has one to itself), and joining costs 1.5 us a segment and
-  // 10 us of two more launches.
-  const int64_t groups = heads * (vdim / 32);
-  int64_t best = 1, most = groups > 0 ? 256 / groups : 1;
-  double least = 2.0 * static_cast<double>(chunks);
-  for (int64_t g = 2; g <= most && g <= 64 && g <= chunks; ++g) {
-    const double us = 3.6 * static_cast<double>((chunks + g - 1) / g) + 1.5 * static_cast<double>(g) + 10.0;
+GdrSegments gdr_segments(int64_t heads, int64_t kdim, int64_t vdim, int64_t chunks) {
+  // Times in us, measured.  In turn a chunk takes 1.8 (keys of 64: 1.45).  With G
+  // segments each is gone through twice, once for E and P (a compute unit has
+  // two workgroups of these, and they are faster together) and once for y (it
+  // has one), and the join takes a step per segment.  16 heads of 128, 8192
+  // tokens: 1 segment 264, 4 176, 8 169, 16 190; 2 heads of 64, 16384 tokens: 1
+  // 388, 32 57, 64 61; 32 heads of 128, 4096 tokens: 1 151, 2 166, 4 160.
+  const bool wide = kdim == 128;
+  const int64_t columns = heads * (vdim / 32), pairs = heads * ((vdim + kdim) / 64);
+  const double a = wide ? 2.0 : 1.45;
+  auto rounds = [](int64_t n, int64_t room) { return static_cast<double>((n + room - 1) / room); };
+  int64_t best = 1;
+  double least = (wide ? 1.8 : 1.45) * static_cast<double>(chunks) + 4.0;
+  for (int64_t g = 2; g <= 64 && g <= chunks && columns * g <= 512; ++g) {
+    const double each = static_cast<double>((chunks + g - 1) / g);
+    const int64_t n = pairs * (g - 1);
+    const double first = n <= 256 ? a * each + 4.0 : (1.55 * a * each + 4.0) * rounds(n, 512);
+    const double us = first + (a * each + 4.0) * rounds(columns * g, 256) + 4.0 + (wide ? 1.2 : 0.4) * static_cast<double>(g);
     if (us < least) {
       least = us;
       best = g;

@@ -189,8 +189,8 @@ def test_gdr_sizes():
 
 @needs_no_gpu
 def test_segments_stay_within_what_is_launched():
-    """A long sequence of few heads is cut into segments, each with a state of its own: no size of a call makes more
-    than 256 workgroups' worth, and the workspace grows by that and no more."""
+    """A long sequence of few heads is cut into segments, each with a state of its own: at most 64 of them and 512
+    workgroups' worth, and the workspace grows by that and no more."""
     for batch in (1, 2, 5, 33, 64, 300):
         for nheads, nqk in ((1, 1), (3, 1), (16, 4), (64, 64)):
             for seqlen in (0, 1, 63, 64, 65, 640, 4096, 4097, 65536, 1 << 20):
@@ -201,7 +201,7 @@ def test_segments_stay_within_what_is_launched():
                     if heads * max(4, chunks) >= 1 << 24:
                         assert size("ssm_gdr_workspace_size", d) == UNSUPPORTED
                         continue
-                    segments = max(1, min(64, chunks, 256 // (heads * vdim // 32)))
+                    segments = max(1, min(64, chunks, 512 // (heads * vdim // 32)))
                     each = 4 * vdim * kdim + 4 * kdim * kdim
                     need = size("ssm_gdr_workspace_size", d)
                     if segments == 1:   # the blocks' parts alone
