@@ -437,16 +437,22 @@ __global__ void __launch_bounds__(256) swa_q8_fill_kernel(const SwaParams p, con
     }
     if (r >= whole) continue;
     const int64_t pos = p.sinks + (r + (whole - 1 - r) / blocks * blocks) * kSwaBlock;
+    // (All reads first: in turns with the maxima they took 58 us, not 45, for 8
+    // prompts, a window of 4096 and 8 heads of 128; 4.5 TB/s.)
     u4 v[2][kEach];
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      unsigned top = 0;
+    for (int t = 0; t < 2; ++t)
 #pragma unroll
       for (int k = 0; k < kEach; ++k) {
         const int at = k * 256 + tid;
         v[t][k] = *reinterpret_cast<const u4 *>(src[t] + (pos + at / CH) * token[t] + at % CH * 8);
-        top = top_of(top, v[t][k]);
       }
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      unsigned top = 0;
+#pragma unroll
+      for (int k = 0; k < kEach; ++k) top = top_of(top, v[t][k]);
       top = wave_top(top);
       if ((tid & 63) == 0) tops[t][tid >> 6] = top;
     }
