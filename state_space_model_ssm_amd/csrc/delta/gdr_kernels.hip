@@ -24,8 +24,8 @@ __device__ __forceinline__ void store_rows(const f4v (&t)[W + 1], u4 *to, int la
 // One workgroup per chunk and value head, one wavefront per 16 of its tokens.
 template <int KD, typename G>
 __global__ void __launch_bounds__(256) gdr_chunk_kernel(const GdrParams p) {
-  __shared__ double sums[64];                       // log2 of the decay up to each token
-  __shared__ float betas[64];
+  __shared__ double all_sums[4][64];                // log2 of the decay up to each token, of each wavefront
+  __shared__ float all_betas[4][64];
   __shared__ __align__(16) float low[64 * kPitch];  // L^T
   __shared__ __align__(16) float diag[64 * kDiagPitch];  // (the blocks of T on the diagonal)^T
   const int tid = threadIdx.x, lane = tid & 63, m = lane & 15, g = lane >> 4;
@@ -45,18 +45,18 @@ __global__ void __launch_bounds__(256) gdr_chunk_kernel(const GdrParams p) {
     ki[a] = *reinterpret_cast<const bf8 *>(kp + ri * p.k_token + 32 * a);
     qi[a] = *reinterpret_cast<const bf8 *>(qp + ri * p.q_token + 32 * a);
   }
-  if (w == 0) {
-    const int64_t at = (b * p.seqlen + t0 + lane) * p.nheads + h;
-    float gt = 0.0f, bt = 0.0f;
-    if (lane < len) {
-      gt = gate<G>(p.g, at);
-      gt = gt < -200.0f ? -200.0f : gt;  // exp(-200) is 0, and differences of the sums stay finite
-      bt = gate<G>(p.beta, at);
-    }
+  // Every wavefront makes the gates' sums for itself, while the keys and queries are on their way.
+  double *sums = all_sums[w];
+  float *betas = all_betas[w];
+  {
+    const int64_t at = (b * p.seqlen + t0 + (lane < len ? lane : len - 1)) * p.nheads + h;
+    float gt = gate<G>(p.g, at), bt = gate<G>(p.beta, at);
+    gt = gt < -200.0f ? -200.0f : gt;  // exp(-200) is 0, and differences of the sums stay finite
     // The gradient of beta is a quotient by it: a gate that is shut counts as
     // 2^-30, which adds less than the last bit of what the token's value is to
     // the state.  (Behind the length nothing is added.)
-    if (lane < len && fabsf(bt) < 0x1p-30f) bt = copysignf(0x1p-30f, bt);
+    if (fabsf(bt) < 0x1p-30f) bt = copysignf(0x1p-30f, bt);
+    if (lane >= len) gt = bt = 0.0f;
     // In float64: after a strong decay the differences of later tokens' sums would lose what they have.
     double s = static_cast<double>(gt) * 1.4426950408889634;
 #pragma unroll
@@ -67,15 +67,17 @@ __global__ void __launch_bounds__(256) gdr_chunk_kernel(const GdrParams p) {
     sums[lane] = s;
     betas[lane] = bt;
     const double last = __shfl(s, 63);
-    const float into = __builtin_amdgcn_exp2f(static_cast<float>(s));
-    float *gates = reinterpret_cast<float *>(ws + 2 * kGdrTriBytes);
-    gates[lane] = lane < len ? p.scale * into : 0.0f;
-    gates[64 + lane] = into;
-    gates[128 + lane] = __builtin_amdgcn_exp2f(static_cast<float>(last - s));
-    gates[192 + lane] = bt;
-    reinterpret_cast<double *>(gates + 256)[lane] = s;
+    if (w == 0) {
+      const float into = __builtin_amdgcn_exp2f(static_cast<float>(s));
+      float *gates = reinterpret_cast<float *>(ws + 2 * kGdrTriBytes);
+      gates[lane] = lane < len ? p.scale * into : 0.0f;
+      gates[64 + lane] = into;
+      gates[128 + lane] = __builtin_amdgcn_exp2f(static_cast<float>(last - s));
+      gates[192 + lane] = bt;
+      reinterpret_cast<double *>(gates + 256)[lane] = s;
+    }
   }
-  __syncthreads();
+  wait_reads();
   u4 *out = reinterpret_cast<u4 *>(ws);
   // Products of keys with this wavefront's keys and queries, transposed: rows j, columns i = 16 w + m.
   by_wave(w, [&](auto wave) {
