@@ -1,4 +1,29 @@
 // Gated delta rule, forward and single tokens, for gfx950.
+//
+// 64 tokens at a time.  With G_t the sum of g from the chunk's start to t, K, Q,
+// V its tokens as rows and S the state before it (value elements x key
+// elements), the u_t that the tokens add solve a triangular system:
+//   L_ij = beta_i e^(G_i - G_j) k_i.k_j (j < i),  T = (I + L)^-1
+//   U = T beta (V - e^G K S^T)
+//   A_ij = scale e^(G_i - G_j) q_i.k_j (j <= i),  Y = scale e^G Q S^T + A U
+//   S' = e^(G_64) S + U^T e^(G_64 - G) K
+// Exponents are differences that are at most 0 where g is: nothing overflows,
+// and a strong decay is a 0.  T and A need no state: a first kernel makes them
+// for all chunks at once.  What is left is a chain from chunk to chunk of three
+// products, whose latency bounds the forward, not its arithmetic (7% of the
+// matrix cores' time) nor its bytes: each value column's chain is its own, so
+// the columns are spread over all compute units, and where they do not fill
+// them, time is cut into segments (see gdr_segments()).
+//
+// Rounding: keys, queries and values are exact; T, A, S, U and what T takes
+// enter products as two bfloat16 parts, to 2^-18 of their size (in one part the
+// state would lose what bfloat16 cannot hold at every chunk; three would make
+// the chain's products half as many again for a state that is 4e-6 off at the
+// end, by norms, beside inputs of 2^-9).  Sums are float32, sums of g float64.
+//
+// Measured, 16 heads of 128: one prompt of 8192 tokens in 160 us a call (chunks
+// 35 us, segments 54, join 11, y 74); training's 4 x 2048 in 36 and 104, of
+// which saving for the backward, 200 MB, is a third.
 #include "gdr_tile.h"
 
 namespace ssmb {
@@ -22,6 +47,10 @@ __device__ __forceinline__ void store_rows(const f4v (&t)[W + 1], u4 *to, int la
 }
 
 // One workgroup per chunk and value head, one wavefront per 16 of its tokens.
+// T by blocks of 16: those on the diagonal by substitution, the others from
+// them by products in float32, since errors of T's entries would grow along its
+// rows.  Bound by latency at four workgroups per CU: 2048 chunks of 128 in 35
+// us, where their 121 MB would take 25.
 template <int KD, typename G>
 __global__ void __launch_bounds__(256) gdr_chunk_kernel(const GdrParams p) {
   __shared__ double all_sums[4][64];                // log2 of the decay up to each token, of each wavefront
@@ -159,7 +188,9 @@ __global__ void __launch_bounds__(256) gdr_chunk_kernel(const GdrParams p) {
 // What a chunk has to wait for is the state, so two wavefronts do nothing but
 // carry that, 16 columns each, and two others make y from the operands that
 // those leave in LDS, and copy the next chunk there: each of the four has a
-// SIMD to itself.
+// SIMD to itself.  A chunk takes 2.2 us (keys of 64: 1.5), 1300 cycles of which
+// are the state's own matrix instructions; the rest is its operands' way
+// through LDS and the splitting into parts.  With what the backward needs 3.2.
 template <int KD>
 __global__ void __launch_bounds__(256) gdr_fwd_kernel(const GdrParams p) {
   constexpr int NT = 64 * kPairs, NC = 16 * kPairs, NS = KD / 32, NB = KD / 16;
@@ -562,7 +593,12 @@ __device__ __forceinline__ float sum8(float v) {
   return v;
 }
 
-// 8 lanes share a row of the state (a value element), 32 rows a workgroup.
+// Bound by memory: the state is read and written once, in float32 throughout,
+// and y = scale (a S q + u (k.q)) needs no second pass over it.  8 lanes share a
+// row of the state (a value element), 32 rows a workgroup.  (Two rows per lane
+// were no faster: 42.1 and 42.1 us at 64 sequences and 32 heads of 128, 195 and
+// 182 at 256.)  64 sequences, 32 heads of 128: 48 us a call, 5.6 TB/s; 4
+// sequences, 16 heads: 4.0 us, of a call's 10.
 template <int KD, typename G>
 __global__ void __launch_bounds__(256) gdr_step_kernel(const GdrParams p) {
   constexpr int NP = KD / 32;  // pieces of 4 floats per lane
