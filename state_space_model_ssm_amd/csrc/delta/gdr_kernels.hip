@@ -10,8 +10,8 @@
 // Exponents are differences that are at most 0 where g is: nothing overflows,
 // and a strong decay is a 0.  T and A need no state: a first kernel makes them
 // for all chunks at once.  What is left is a chain from chunk to chunk of three
-// products, whose latency bounds the forward, not its arithmetic (7% of the
-// matrix cores' time) nor its bytes: each value column's chain is its own, so
+// products, whose latency bounds the forward, not its arithmetic (14 to 20% of
+// the matrix cores' time) nor its bytes: each value column's chain is its own, so
 // the columns are spread over all compute units, and where they do not fill
 // them, time is cut into segments (see gdr_segments()).
 //
