@@ -140,16 +140,17 @@ def _scratch(dims, need: int, workspace, like, stream):
 
 
 def _one_device(stream, first, *others):
-    """All tensors on the device whose stream the call goes to."""
+    """All tensors on the current device, where the call launches, and the stream if one is given."""
     at = first.get_device()   # -1 on the CPU
     for t in others:
         if t is not None and t.get_device() != at:
             raise ValueError(f"tensors must be on one device, got {t.device} and {first.device}")
     if at < 0:
         raise ValueError("tensors must be on the GPU")
-    here = torch._C._cuda_getDevice() if stream is None else stream.device_index
-    if at != here:
-        raise ValueError(f"tensors are on cuda:{at}, the stream on cuda:{here}")
+    here = torch._C._cuda_getDevice()
+    if at != here or (stream is not None and stream.device_index != here):
+        raise ValueError(f"tensors are on cuda:{at}, the current device is cuda:{here}"
+                         + ("" if stream is None else f", the stream's cuda:{stream.device_index}"))
 
 
 _DENSE = torch.contiguous_format
@@ -173,15 +174,16 @@ def _at(t):
 def _gdr_dims(q, k, v, g, beta, scale, lead) -> GdrDims:
     if q.dtype != _BF16 or k.dtype != _BF16 or v.dtype != _BF16:
         raise TypeError("q, k and v must be bfloat16")
-    if q.dim() != lead + 2 or q.shape != k.shape or v.dim() != lead + 2 or v.shape[:lead] != q.shape[:lead]:
+    qs, vs = q.shape, v.shape
+    if len(qs) != lead + 2 or qs != k.shape or len(vs) != lead + 2 or vs[:lead] != qs[:lead]:
         raise ValueError("q and k must be (batch, seqlen, nqk, kdim) and v (batch, seqlen, nheads, vdim), "
                          "without seqlen in a step")
-    _same("g", g, g.dtype, v.shape[:-1])
-    _same("beta", beta, g.dtype, v.shape[:-1])
-    kd = q.shape[-1]
-    return GdrDims(q.shape[0], q.shape[1] if lead == 2 else 1, q.shape[-2], v.shape[-2], kd, v.shape[-1],
-                   *_heads("q", q, lead, kd), *_heads("k", k, lead, kd), *_heads("v", v, lead, v.shape[-1]),
-                   kd ** -0.5 if scale is None else scale, _code(g.dtype))
+    gates, gs = g.dtype, vs[:-1]
+    _same("g", g, gates, gs)
+    _same("beta", beta, gates, gs)
+    kd, vd = qs[-1], vs[-1]
+    return GdrDims(qs[0], qs[1] if lead == 2 else 1, qs[-2], vs[-2], kd, vd, *_heads("q", q, lead, kd),
+                   *_heads("k", k, lead, kd), *_heads("v", v, lead, vd), kd ** -0.5 if scale is None else scale, _code(gates))
 
 
 def gdr_fwd(q, k, v, g, beta, *, h0=None, lengths=None, scale=None, return_h_last: bool = True,
@@ -275,13 +277,14 @@ def _rows(name, t, given, lead, d) -> tuple:
 
 
 def _qk_norm_dims(q, k, wq, wk, inv_freq, pos, eps, neighbours, out_q, out_k, given_q, given_k) -> QkNormDims:
-    lead = q.dim() - 2
-    if lead not in (1, 2) or k.dim() != q.dim() or k.shape[:lead] != q.shape[:lead] or k.shape[-1] != q.shape[-1]:
+    qs, ks = q.shape, k.shape
+    lead = len(qs) - 2
+    if lead not in (1, 2) or len(ks) != lead + 2 or ks[:lead] != qs[:lead] or ks[-1] != qs[-1]:
         raise ValueError("q and k must be (batch, seqlen, heads, headdim), or (batch, heads, headdim) in a step, "
                          "of one batch, seqlen and headdim")
-    if k.dtype != q.dtype:
-        raise TypeError(f"k must have dtype {q.dtype}")
-    d = q.shape[-1]
+    dtype, d = q.dtype, qs[-1]
+    if k.dtype != dtype:
+        raise TypeError(f"k must have dtype {dtype}")
     _same("wq", wq, _F32, (d,))
     _same("wk", wk, _F32, (d,))
     rot = 0
@@ -292,10 +295,10 @@ def _qk_norm_dims(q, k, wq, wk, inv_freq, pos, eps, neighbours, out_q, out_k, gi
         rot = 2 * inv_freq.shape[0]
         if pos is None and lead == 1:
             raise ValueError("pos is required in a step")
-    _same("pos", pos, torch.int32, q.shape[:lead])
-    return QkNormDims(q.shape[0], q.shape[1] if lead == 2 else 1, q.shape[-2], k.shape[-2], d, rot,
-                      *_heads("q", q, lead, d), *_heads("k", k, lead, d), *_rows("q's output", out_q, given_q, lead, d),
-                      *_rows("k's output", out_k, given_k, lead, d), _code(q.dtype), int(neighbours), eps)
+    _same("pos", pos, torch.int32, qs[:lead])
+    return QkNormDims(qs[0], qs[1] if lead == 2 else 1, qs[-2], ks[-2], d, rot, *_heads("q", q, lead, d),
+                      *_heads("k", k, lead, d), *_rows("q's output", out_q, given_q, lead, d),
+                      *_rows("k's output", out_k, given_k, lead, d), _code(dtype), int(neighbours), eps)
 
 
 def qk_norm_fwd(q, k, wq=None, wk=None, *, inv_freq=None, pos=None, eps: float = 1e-6, neighbours: bool = False,
