@@ -197,13 +197,14 @@ CacheBytes cache_bytes(const ssm_swa_dims_t &d) {
   return {rows * (d.sinks + kSwaBlock) * d.headdim * 2, rows * d.window * d.headdim, rows * (d.window / kSwaBlock) * 4};
 }
 
-int q8_splits(const ssm_swa_dims_t &d) { return swa_q8_splits(d.batch, d.nheads, d.nkv, d.window, d.sinks); }
+SwaQ8Plan q8_plan(const ssm_swa_dims_t &d) { return swa_q8_plan(d.batch, d.nheads, d.nkv, d.window, d.sinks); }
 size_t q8_sums(const ssm_swa_dims_t &d) {
-  return up256(static_cast<size_t>(d.batch) * d.nheads * q8_splits(d) * d.headdim * 4);
+  return up256(static_cast<size_t>(d.batch) * d.nheads * q8_plan(d).splits * d.headdim * 4);
 }
 size_t q8_workspace(const ssm_swa_dims_t &d) {
-  const size_t rows = static_cast<size_t>(d.batch) * d.nheads * q8_splits(d);
-  return q8_splits(d) > 1 ? q8_sums(d) + up256(rows * 8) : 0;
+  const int splits = q8_plan(d).splits;
+  const size_t rows = static_cast<size_t>(d.batch) * d.nheads * splits;
+  return splits > 1 ? q8_sums(d) + up256(rows * 8) : 0;
 }
 
 SwaQ8Cache cache_of(void *k_near, void *v_near, void *k_ring, void *v_ring, float *k_scale, float *v_scale) {
@@ -281,7 +282,7 @@ int ssm_swa_q8_step(const void *q, const void *k, const void *v, void *k_near, v
   p.headdim = static_cast<int32_t>(d.headdim);
   p.ws_o = static_cast<float *>(d.workspace);
   if (d.workspace) p.ws_stat = reinterpret_cast<float *>(static_cast<char *>(d.workspace) + q8_sums(d));
-  return launched(launch_swa_q8_step(p, cache_of(k_near, v_near, k_ring, v_ring, k_scale, v_scale), q8_splits(d),
+  return launched(launch_swa_q8_step(p, cache_of(k_near, v_near, k_ring, v_ring, k_scale, v_scale), q8_plan(d),
                                      static_cast<hipStream_t>(stream)),
                   "swa_q8_step");
 }

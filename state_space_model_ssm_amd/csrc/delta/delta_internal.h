@@ -37,8 +37,11 @@ struct SwaQ8Cache {
   uint8_t *k_ring, *v_ring;       // (batch, nkv, window, headdim) e4m3
   float *k_scale, *v_scale;       // (batch, nkv, window / 64)
 };
-int swa_q8_splits(int64_t batch, int64_t nheads, int64_t nkv, int64_t window, int64_t sinks);
-hipError_t launch_swa_q8_step(const SwaStepParams &p, const SwaQ8Cache &cache, int splits, hipStream_t stream);
+struct SwaQ8Plan {
+  int splits, waves;  // workgroups that share a row's tiles, and wavefronts of each
+};
+SwaQ8Plan swa_q8_plan(int64_t batch, int64_t nheads, int64_t nkv, int64_t window, int64_t sinks);
+hipError_t launch_swa_q8_step(const SwaStepParams &p, const SwaQ8Cache &cache, const SwaQ8Plan &plan, hipStream_t stream);
 hipError_t launch_swa_q8_fill(const SwaParams &p, const SwaQ8Cache &cache, hipStream_t stream);
 
 }  // namespace ssmb

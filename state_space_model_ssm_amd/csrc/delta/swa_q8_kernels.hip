@@ -18,8 +18,7 @@
 //
 // Measured: 64 sequences, 32 heads of 128 on 8, windows of up to 4096 in 83 us
 // a call, 4.85 TB/s of the cache's bytes, where a large copy reaches 4.8; 4
-// sequences, 16 heads on 4, window 1024: 7.2 us and 3.6 to join 5 splits, all
-// latency.
+// sequences, 16 heads on 4, window 1024: 11 us, of a call's 12, all latency.
 #include "block/swa_step.h"
 #include "delta_internal.h"
 #include "gdr_tile.h"
@@ -188,14 +187,14 @@ __device__ __forceinline__ void weigh(f4v (&s)[4], float c2, f4v (&o)[NB], float
   sum += part[0] + part[1];
 }
 
-// Heads that share a key head, 16 at a time, as columns.
-template <int D>
-__global__ void __launch_bounds__(256, 2) swa_q8_step_kernel(const SwaStepParams p, const SwaQ8Cache cache, unsigned splits,
+// Heads that share a key head, 16 at a time, as columns; NW wavefronts share the tiles.
+template <int D, int NW>
+__global__ void __launch_bounds__(64 * NW, 2) swa_q8_step_kernel(const SwaStepParams p, const SwaQ8Cache cache, unsigned splits,
                                                              unsigned qblocks) {
   constexpr int CH = D / 8, NB = D / 16, NS = D / 32, kNear = 32;
   constexpr int kCopies = D / 16;  // copies of 1 KiB per tile, of either kind
-  __shared__ __align__(16) u4 lds[4][2][kSwaBlock * D / 16];  // wavefront, K or V; in the end o, [16][D] float32
-  __shared__ float tops[4][16], sums[4][16];
+  __shared__ __align__(16) u4 lds[NW][2][kSwaBlock * D / 16];  // wavefront, K or V; in the end o, [16][D] float32
+  __shared__ float tops[NW][16], sums[NW][16];
   const int tid = threadIdx.x, lane = tid & 63, m = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const unsigned nkv = static_cast<unsigned>(p.nkv), group = static_cast<unsigned>(p.nheads) / nkv;
@@ -240,7 +239,7 @@ __global__ void __launch_bounds__(256, 2) swa_q8_step_kernel(const SwaStepParams
     const int old = now >= blocks ? now % blocks : -1;
     const int skip = old >= 0 && off == 63 ? old : blocks;  // it has no such places
     const int tiles = near_tiles + (skip < blocks ? held - 1 : held);
-    const unsigned parts = splits * 4, part = split * 4 + wave;
+    const unsigned parts = splits * NW, part = split * NW + wave;
     const unsigned each = tiles / parts, more = tiles % parts;
     const int lo = static_cast<int>(each * part + (part < more ? part : more));
     const int hi = lo + static_cast<int>(each + (part < more ? 1 : 0));
@@ -345,7 +344,7 @@ __global__ void __launch_bounds__(256, 2) swa_q8_step_kernel(const SwaStepParams
     sum += other_row(sum);
     sum += other_half(sum);
   }
-  // Join the four wavefronts.
+  // Join the wavefronts.
   float *mine = reinterpret_cast<float *>(lds[wave]);
 #pragma unroll
   for (int e = 0; e < NB; ++e) *reinterpret_cast<f4v *>(mine + m * D + 16 * e + 4 * g) = o[e];
@@ -354,15 +353,15 @@ __global__ void __launch_bounds__(256, 2) swa_q8_step_kernel(const SwaStepParams
     sums[wave][m] = sum;
   }
   __syncthreads();
-  for (int i = tid; i < heads * D; i += 256) {
+  for (int i = tid; i < heads * D; i += 64 * NW) {
     const int row = i / D, e = i % D;
     float best = tops[0][row];
 #pragma unroll
-    for (int w = 1; w < 4; ++w) best = fmaxf(best, tops[w][row]);
+    for (int w = 1; w < NW; ++w) best = fmaxf(best, tops[w][row]);
     // (A share without a maximum holds zeros, or the NaN that all its scores were.)
     float acc = 0.0f, all = 0.0f;
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
+    for (int w = 0; w < NW; ++w) {
       const float f = tops[w][row] == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(tops[w][row] - best);
       acc = fmaf(f, reinterpret_cast<const float *>(lds[w])[row * D + e], acc);
       all = fmaf(f, sums[w][row], all);
@@ -483,28 +482,37 @@ __global__ void __launch_bounds__(256) swa_q8_fill_kernel(const SwaParams p, con
 
 }  // namespace
 
-int swa_q8_splits(int64_t batch, int64_t nheads, int64_t nkv, int64_t window, int64_t sinks) {
+SwaQ8Plan swa_q8_plan(int64_t batch, int64_t nheads, int64_t nkv, int64_t window, int64_t sinks) {
   // As many workgroups as there is LDS for at once, two per CU, while a wavefront
   // has a tile; up to three tiles each it is as fast not to split, without the
   // join's launch.  32 heads on 8 of 128: 64 sequences, window 4096, 1 split 104
   // us, 2 and their join 110; 64, window 1024, 29 and 37; 4, window 4096, 16
   // splits 15, 18 (of a tile each) 18; 32, window 256, 1 split 9, 2 13.
+  // Eight wavefronts, where a CU has one workgroup anyway, do so up to 24 tiles:
+  // 8 sequences, window 1024, 12 us, 4 wavefronts and splits 14; 30, 18 and 27; 1
+  // of 8 heads on 1, window 512, 8.7, 4 wavefronts alone 10.2.
   const int64_t rows = batch * nkv * ((nheads / nkv + 15) / 16), tiles = window / kSwaBlock + (sinks + kSwaBlock + 31) / 32;
-  const int64_t want = (512 + rows - 1) / (rows > 0 ? rows : 1), most = tiles <= 12 ? 1 : (tiles + 3) / 4;
+  if (tiles <= 24 && rows <= 256) return {1, 8};
+  if (tiles <= 12) return {1, 4};
+  const int64_t want = (512 + rows - 1) / (rows > 0 ? rows : 1), most = (tiles + 3) / 4;
   const int64_t n = want < most ? want : most;
-  return static_cast<int>(n < kMaxSplits ? n : kMaxSplits);
+  return {static_cast<int>(n < kMaxSplits ? n : kMaxSplits), 4};
 }
 
-hipError_t launch_swa_q8_step(const SwaStepParams &p, const SwaQ8Cache &cache, int splits, hipStream_t s) {
-  const unsigned qblocks = static_cast<unsigned>((p.nheads / p.nkv + 15) / 16), sp = static_cast<unsigned>(splits);
-  const dim3 g(static_cast<uint32_t>(p.batch * p.nkv * (qblocks * splits + 1))), gj(static_cast<uint32_t>(p.batch * p.nheads));
-  if (p.headdim == 64) {
-    hipLaunchKernelGGL((swa_q8_step_kernel<64>), g, dim3(256), 0, s, p, cache, sp, qblocks);
-    if (splits > 1) hipLaunchKernelGGL((swa_q8_join_kernel<64>), gj, dim3(256), 0, s, p, splits);
-  } else {
-    hipLaunchKernelGGL((swa_q8_step_kernel<128>), g, dim3(256), 0, s, p, cache, sp, qblocks);
-    if (splits > 1) hipLaunchKernelGGL((swa_q8_join_kernel<128>), gj, dim3(256), 0, s, p, splits);
-  }
+namespace {
+template <int D>
+void step(const SwaStepParams &p, const SwaQ8Cache &cache, const SwaQ8Plan &plan, hipStream_t s) {
+  const unsigned qblocks = static_cast<unsigned>((p.nheads / p.nkv + 15) / 16), splits = static_cast<unsigned>(plan.splits);
+  const dim3 g(static_cast<uint32_t>(p.batch * p.nkv * (qblocks * splits + 1)));
+  if (plan.waves == 4) hipLaunchKernelGGL((swa_q8_step_kernel<D, 4>), g, dim3(256), 0, s, p, cache, splits, qblocks);
+  else hipLaunchKernelGGL((swa_q8_step_kernel<D, 8>), g, dim3(512), 0, s, p, cache, splits, qblocks);
+  if (splits > 1)
+    hipLaunchKernelGGL((swa_q8_join_kernel<D>), dim3(static_cast<uint32_t>(p.batch * p.nheads)), dim3(256), 0, s, p, plan.splits);
+}
+}  // namespace
+
+hipError_t launch_swa_q8_step(const SwaStepParams &p, const SwaQ8Cache &cache, const SwaQ8Plan &plan, hipStream_t s) {
+  p.headdim == 64 ? step<64>(p, cache, plan, s) : step<128>(p, cache, plan, s);
   return hipGetLastError();
 }
 

@@ -367,12 +367,12 @@ def _q8_cache(cache, batch, nkv, headdim, sinks) -> int:
         raise ValueError(f"the cache's window must be a multiple of {SWA_Q8_BLOCK}, got {window}")
     near, ring = (batch, nkv, sinks + SWA_Q8_BLOCK, headdim), (batch, nkv, window, headdim)
     scale = (batch, nkv, window // SWA_Q8_BLOCK)
-    _same("k_near", near_k, _BF16, near)
-    _same("v_near", near_v, _BF16, near)
-    _same("k_ring", ring_k, _E4M3, ring)
-    _same("v_ring", ring_v, _E4M3, ring)
-    _same("k_scale", scale_k, _F32, scale)
-    _same("v_scale", scale_v, _F32, scale)
+    if not (near_k.shape == near == near_v.shape and ring_k.shape == ring == ring_v.shape
+            and scale_k.shape == scale == scale_v.shape and near_k.dtype is _BF16 is near_v.dtype
+            and ring_k.dtype is _E4M3 is ring_v.dtype and scale_k.dtype is _F32 is scale_v.dtype):
+        for name, t, dtype, shape in zip(SwaQ8Cache._fields, cache, (_BF16, _BF16, _E4M3, _E4M3, _F32, _F32),
+                                         (near, near, ring, ring, scale, scale)):
+            _same(name, t, dtype, shape)
     return window
 
 

@@ -112,6 +112,26 @@ def test_fill_then_step(B, H, KV, d, window, sinks, L, lengths):
             check(y[b], q[b, pos[b]], model, b, int(pos[b]), f"row {b} step {step}", d ** -0.5)
 
 
+@pytest.mark.parametrize("B,H,KV,d,window,sinks,L", [(70, 4, 4, 128, 128, 4, 150), (70, 8, 4, 64, 128, 0, 140),
+                                                     (66, 4, 4, 64, 1024, 3, 1100)])
+def test_many_rows(B, H, KV, d, window, sinks, L):
+    """More rows than compute units, which take fewer wavefronts each; prompts of any length, then a token, checked in every fifth row."""
+    q, k, v = make(B, L + 1, H, KV, d, L + d)
+    g = torch.Generator().manual_seed(B)
+    lens = torch.randint(0, L + 1, (B,), generator=g, dtype=torch.int32)
+    lens[5] = L
+    cache, model = empty(B, KV, window, d, sinks), ref.Q8Cache(B, KV, window, d, sinks)
+    ssm.swa_q8_fill(k[:, :L].cuda(), v[:, :L].cuda(), cache, sinks=sinks, lengths=lens.cuda())
+    rows = torch.arange(B)
+    y = ssm.swa_q8_step(*(x[rows, lens.long()].cuda() for x in (q, k, v)), cache, lens.cuda(), sinks=sinks)
+    assert not y.isnan().any()
+    for b in range(0, B, 5):
+        n = int(lens[b])
+        model.rows[b][0].extend(k[b, :n + 1])
+        model.rows[b][1].extend(v[b, :n + 1])
+        check(y[b], q[b, n], model, b, n, f"row {b}", d ** -0.5)
+
+
 def test_blocks_hold_their_values():
     """Bytes and scales of a whole block: the nearest e4m3 value, ties to even; zeros; a tiny, a huge and a NaN block."""
     B, KV, d, window = 1, 6, 64, 64
