@@ -21,8 +21,8 @@
 // the chain's products half as many again for a state that is 4e-6 off at the
 // end, by norms, beside inputs of 2^-9).  Sums are float32, sums of g float64.
 //
-// Measured, 16 heads of 128: one prompt of 8192 tokens in 160 us a call (chunks
-// 35 us, segments 54, join 11, y 74); training's 4 x 2048 in 36 and 104, of
+// Measured, 16 heads of 128: one prompt of 8192 tokens in 152 us a call (chunks
+// 29 us, segments 54, join 11, y 74); training's 4 x 2048 in 29 and 105, of
 // which saving for the backward, 200 MB, is a third.
 #include "gdr_tile.h"
 
@@ -49,14 +49,16 @@ __device__ __forceinline__ void store_rows(const f4v (&t)[W + 1], u4 *to, int la
 // One workgroup per chunk and value head, one wavefront per 16 of its tokens.
 // T by blocks of 16: those on the diagonal by substitution, the others from
 // them by products in float32, since errors of T's entries would grow along its
-// rows.  Bound by latency at four workgroups per CU: 2048 chunks of 128 in 35
-// us, where their 121 MB would take 25.
+// rows.  2048 chunks of 128 in 29 us, where their 121 MB would take 25.  (Keys
+// through LDS, not from memory by each wavefront: 37.)
 template <int KD, typename G>
 __global__ void __launch_bounds__(256) gdr_chunk_kernel(const GdrParams p) {
-  __shared__ double all_sums[4][64];                // log2 of the decay up to each token, of each wavefront
+  // Keys, and after their products L^T and (the blocks of T on the diagonal)^T.
+  constexpr int kTiles = 64 * KD * 2, kAfter = (64 * kPitch + 64 * kDiagPitch) * 4;
+  __shared__ __align__(16) u4 lds[(kTiles > kAfter ? kTiles : kAfter) / 16];
+  __shared__ double all_sums[4][64];  // log2 of the decay up to each token, of each wavefront
   __shared__ float all_betas[4][64];
-  __shared__ __align__(16) float low[64 * kPitch];  // L^T
-  __shared__ __align__(16) float diag[64 * kDiagPitch];  // (the blocks of T on the diagonal)^T
+  float *low = reinterpret_cast<float *>(lds), *diag = low + 64 * kPitch;
   const int tid = threadIdx.x, lane = tid & 63, m = lane & 15, g = lane >> 4;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int64_t id = blockIdx.x, c = id % p.chunks, bh = id / p.chunks, b = bh / p.nheads, h = bh % p.nheads;
@@ -65,21 +67,19 @@ __global__ void __launch_bounds__(256) gdr_chunk_kernel(const GdrParams p) {
   char *ws = p.ops + id * p.ops_step;
   constexpr int NS = KD / 32;
   const int64_t hk = h / (p.nheads / p.nqk);
-  const uint16_t *kp = p.k + b * p.k_batch + t0 * p.k_token + hk * KD + 8 * g;
-  const uint16_t *qp = p.q + b * p.q_batch + t0 * p.q_token + hk * KD + 8 * g;
-  const int i = 16 * w + m, ri = i < len ? i : len - 1;  // rows past the length repeat the last one
-  bf8 ki[NS], qi[NS];
+  const int i = 16 * w + m, last_row = t0 + (len < 64 ? len : 64) - 1;  // rows past the length repeat the last one
+  load_tile<KD, 256>(lds, uniform(p.k + b * p.k_batch + t0 * p.k_token + hk * KD), p.k_token, 0, last_row - t0, tid);
+  // Queries, of which a wavefront takes its own only, straight to registers.
+  bf8 qi[NS];
 #pragma unroll
-  for (int a = 0; a < NS; ++a) {
-    ki[a] = *reinterpret_cast<const bf8 *>(kp + ri * p.k_token + 32 * a);
-    qi[a] = *reinterpret_cast<const bf8 *>(qp + ri * p.q_token + 32 * a);
-  }
+  for (int a = 0; a < NS; ++a)
+    qi[a] = *reinterpret_cast<const bf8 *>(p.q + b * p.q_batch + (t0 + i < last_row ? t0 + i : last_row) * p.q_token + hk * KD + 32 * a + 8 * g);
   // Every wavefront makes the gates' sums for itself, while the keys and queries are on their way.
   double *sums = all_sums[w];
   float *betas = all_betas[w];
   {
-    const int64_t at = (b * p.seqlen + t0 + (lane < len ? lane : len - 1)) * p.nheads + h;
-    float gt = gate<G>(p.g, at), bt = gate<G>(p.beta, at);
+    const int64_t from = (b * p.seqlen + t0 + (lane < len ? lane : len - 1)) * p.nheads + h;
+    float gt = gate<G>(p.g, from), bt = gate<G>(p.beta, from);
     gt = gt < -200.0f ? -200.0f : gt;  // exp(-200) is 0, and differences of the sums stay finite
     // The gradient of beta is a quotient by it: a gate that is shut counts as
     // 2^-30, which adds less than the last bit of what the token's value is to
@@ -106,22 +106,25 @@ __global__ void __launch_bounds__(256) gdr_chunk_kernel(const GdrParams p) {
       reinterpret_cast<double *>(gates + 256)[lane] = s;
     }
   }
-  wait_reads();
+  arrive();
+  const unsigned keys = lds_at(lds);
+  const Lanes16 at = lanes16_of<KD>(lane);
   u4 *out = reinterpret_cast<u4 *>(ws);
   // Products of keys with this wavefront's keys and queries, transposed: rows j, columns i = 16 w + m.
   by_wave(w, [&](auto wave) {
     constexpr int W = wave;
     f4v kk[W + 1] = {}, att[W + 1] = {};
 #pragma unroll
-    for (int jb = 0; jb <= W; ++jb) {
-      const int j = 16 * jb + m, rj = j < len ? j : len - 1;
+    for (int a = 0; a < NS; ++a) {
+      const bf8 ki = row16<KD>(keys, W, a, at);
 #pragma unroll
-      for (int a = 0; a < NS; ++a) {
-        const bf8 kj = *reinterpret_cast<const bf8 *>(kp + rj * p.k_token + 32 * a);
-        kk[jb] = mfma16(kj, ki[a], kk[jb]);
+      for (int jb = 0; jb <= W; ++jb) {
+        const bf8 kj = row16<KD>(keys, jb, a, at);
+        kk[jb] = mfma16(kj, ki, kk[jb]);
         att[jb] = mfma16(kj, qi[a], att[jb]);
       }
     }
+    meet();
     const double si = sums[i];
     const float bi = betas[i];
 #pragma unroll
