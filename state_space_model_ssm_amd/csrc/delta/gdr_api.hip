@@ -55,7 +55,7 @@ size_t saved_bytes(const ssm_gdr_dims_t &d) {
   return static_cast<size_t>(d.batch) * d.nheads * ceil_div(d.seqlen, SSM_GDR_STATE_STEP) * gdr_saved_bytes(d.kdim, d.vdim);
 }
 
-GdrParams params(const ssm_gdr_dims_t &d) {
+GdrParams params(const ssm_gdr_dims_t &d, bool bwd = false) {
   GdrParams p{};
   p.ws = static_cast<char *>(d.workspace);
   p.batch = d.batch;
@@ -73,7 +73,8 @@ GdrParams params(const ssm_gdr_dims_t &d) {
   p.kdim = static_cast<int32_t>(d.kdim);
   p.vdim = static_cast<int32_t>(d.vdim);
   p.gates_bf16 = d.gate_dtype == SSM_BF16;
-  p.seg = gdr_segments(d.batch * d.nheads, d.kdim, d.vdim, p.chunks);
+  p.seg = bwd ? gdr_bwd_segments(d.batch * d.nheads, d.kdim, d.vdim, p.chunks)
+              : gdr_segments(d.batch * d.nheads, d.kdim, d.vdim, p.chunks);
   return p;
 }
 
@@ -147,16 +148,18 @@ int ssm_gdr_bwd_workspace_size(const ssm_gdr_dims_t *dims, size_t *bytes) {
   if (!bytes) return fail(SSM_ERR_NULL, "bytes is NULL");
   const int rc = check_gdr(dims, false);
   if (rc != SSM_OK) return rc;
-  *bytes = gdr_bwd_workspace(params(*dims));
+  const GdrSizes n = gdr_bwd_sizes(params(*dims, true));
+  *bytes = n.chunks + n.state + n.carry;
   return ok();
 }
 
-int ssm_gdr_bwd(const void *q, const void *k, const int32_t *lengths, const void *states, const void *dy, const float *dh_last, void *dq, void *dk, void *dv, void *dg,
-                void *dbeta, float *dh0, const ssm_gdr_dims_t *dims, void *stream) {
+int ssm_gdr_bwd(const void *q, const void *k, const int32_t *lengths, const void *states, const void *dy,
+                const float *dh_last, void *dq, void *dk, void *dv, void *dg, void *dbeta, float *dh0,
+                const ssm_gdr_dims_t *dims, void *stream) {
   int rc = check_gdr(dims, false);
   if (rc != SSM_OK) return rc;
   const ssm_gdr_dims_t &d = *dims;
-  GdrParams p = params(d);
+  GdrParams p = params(d, true);
   const size_t eg = dtype_size(d.gate_dtype), rows = static_cast<size_t>(d.batch) * d.seqlen;
   const size_t state = static_cast<size_t>(d.batch) * d.nheads * d.vdim * d.kdim * 4;
   const Arg ins[] = {{"q", q, span(d, d.q_batch, d.q_token, d.nqk * d.kdim), 16, true},
@@ -171,7 +174,8 @@ int ssm_gdr_bwd(const void *q, const void *k, const int32_t *lengths, const void
                       {"dbeta", dbeta, rows * d.nheads * eg, eg, true},  {"dh0", dh0, state, 16, false}};
   const void *const same[6][2] = {};
   rc = check_args(ins, outs, same);
-  if (rc == SSM_OK) rc = check_workspace(ins, gdr_bwd_workspace(p));
+  const GdrSizes n = gdr_bwd_sizes(p);
+  if (rc == SSM_OK) rc = check_workspace(ins, n.chunks + n.state + n.carry);
   if (rc != SSM_OK) return rc;
   if (d.batch == 0 || (d.seqlen == 0 && dh0 == nullptr)) return ok();
   p.q = static_cast<const uint16_t *>(q);
@@ -187,6 +191,10 @@ int ssm_gdr_bwd(const void *q, const void *k, const int32_t *lengths, const void
   p.dbeta = dbeta;
   p.dh0 = dh0;
   p.ws_both = p.ws;
+  p.ops = p.saved + gdr_both_bytes(d.kdim, d.vdim);
+  p.ops_step = static_cast<int64_t>(gdr_saved_bytes(d.kdim, d.vdim));
+  p.ws_state = reinterpret_cast<float *>(p.ws + n.chunks);
+  p.ws_carry = reinterpret_cast<uint16_t *>(p.ws + n.chunks + n.state);
   return launched(launch_gdr_bwd(p, static_cast<hipStream_t>(stream)), "gdr_bwd");
 }
 

@@ -33,8 +33,9 @@ namespace {
 
 // As in the forward two wavefronts carry dS, 16 columns each, and two others
 // make what does not depend on it, A^T dY and Q^T (scale e^G dY), copy the next
-// chunk, and store E and dv.
-template <int KD>
+// chunk, and store D and dv.  FIND: of all segments but the first, only the dS
+// before it, from 0 or, of a row's last, from dh_last.
+template <int KD, bool FIND>
 __global__ void __launch_bounds__(256) gdr_bwd_kernel(const GdrParams p) {
   constexpr int NT = 64 * kPairs, NC = 16 * kPairs, NS = KD / 32, NB = KD / 16;
   constexpr unsigned kRows = 64 * KD * 2, kValues = 64 * NC * 2, kTri = 2 * kGdrTriBytes, kOps = kTri + kGdrGateBytes;
@@ -43,9 +44,14 @@ __global__ void __launch_bounds__(256) gdr_bwd_kernel(const GdrParams p) {
   __shared__ __align__(16) u4 lds[(2 * kBuffer + kPairs * (kFour + kState)) / 16];
   const int tid = threadIdx.x, lane = tid & 63, m = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), w = wave % kPairs;
-  const HeadTile which = head_tile(blockIdx.x, static_cast<unsigned>(p.batch * p.nheads), static_cast<unsigned>(p.vdim) / NC);
-  const int64_t vt = which.tile, bh = which.head, b = bh / p.nheads, h = bh % p.nheads;
-  const int len = gdr_length(p.lengths, b, p.seqlen), n = (len + 63) / 64;
+  const unsigned vtiles = static_cast<unsigned>(p.vdim) / NC;
+  const HeadTile which = head_tile(blockIdx.x, static_cast<unsigned>(p.batch * p.nheads), vtiles * static_cast<unsigned>(p.seg.count - (FIND ? 1 : 0)));
+  const int64_t vt = which.tile % vtiles, bh = which.head, b = bh / p.nheads, h = bh % p.nheads;
+  // Chunks n - 1 .. first of the row, of this segment.
+  const int segment = static_cast<int>(which.tile / vtiles) + (FIND ? 1 : 0), len = gdr_length(p.lengths, b, p.seqlen);
+  const int first = segment * static_cast<int>(p.seg.chunks), all = (len + 63) / 64;
+  const int n = all < first + p.seg.chunks ? all : first + static_cast<int>(p.seg.chunks);
+  if (FIND && n <= first) return;
   const int col0 = static_cast<int>(vt) * NC + 16 * w;
   const unsigned base = lds_at(lds), four = base + 2 * kBuffer + w * kFour + lane * 16;
   const unsigned grown = base + 2 * kBuffer + kPairs * kFour + w * kState + lane * 16;
@@ -56,10 +62,12 @@ __global__ void __launch_bounds__(256) gdr_bwd_kernel(const GdrParams p) {
   if (wave < kPairs) {
     f4v s[NB];  // dS, laid out as the state
     const int64_t state = (bh * p.vdim + col0 + m) * KD + 8 * g;
+    float *behind = p.ws_state + ((bh * p.seg.count + segment) * p.vdim + col0 + m) * KD + 8 * g;
+    const float *from = first + p.seg.chunks >= all ? (p.dh_last != nullptr ? p.dh_last + state : nullptr) : FIND ? nullptr : behind;
 #pragma unroll
     for (int j = 0; j < NB; ++j)
-      s[j] = p.dh_last != nullptr ? *reinterpret_cast<const f4v *>(p.dh_last + state + 32 * (j / 2) + 4 * (j % 2)) : f4v{};
-    for (int c = n - 1; c >= 0; --c) {
+      s[j] = from != nullptr ? *reinterpret_cast<const f4v *>(from + 32 * (j / 2) + 4 * (j % 2)) : f4v{};
+    for (int c = n - 1; c >= first; --c) {
       Parts sp[NS];
 #pragma unroll
       for (int a = 0; a < NS; ++a) {
@@ -120,9 +128,10 @@ __global__ void __launch_bounds__(256) gdr_bwd_kernel(const GdrParams p) {
 #pragma unroll
         for (int j = 0; j < NB; ++j) s[j] = mul_exact(kt[k][j], ep[k], s[j]);
     }
-    if (p.dh0 != nullptr) {
+    float *to = FIND ? behind - p.vdim * KD : segment == 0 && p.dh0 != nullptr ? p.dh0 + state : nullptr;
+    if (to != nullptr) {
 #pragma unroll
-      for (int j = 0; j < NB; ++j) *reinterpret_cast<f4v *>(p.dh0 + state + 32 * (j / 2) + 4 * (j % 2)) = s[j];
+      for (int j = 0; j < NB; ++j) *reinterpret_cast<f4v *>(to + 32 * (j / 2) + 4 * (j % 2)) = s[j];
     }
     return;
   }
@@ -190,21 +199,21 @@ __global__ void __launch_bounds__(256) gdr_bwd_kernel(const GdrParams p) {
     const int64_t rest = p.seqlen - 64 * static_cast<int64_t>(c);
     v_store.put(vp + 64 * c * yt, rest < 64 ? static_cast<int>(rest) : 64, e);
   };
-  if (n > 0) {
+  if (n > first) {
     fetch_rows(n - 1);
     fetch_ws(n - 1);
   }
-  for (int c = n - 1; c >= 0; --c) {
+  for (int c = n - 1; c >= first; --c) {
     arrive();
-    if (c + 1 < n) store(c + 1);
+    if (!FIND && c + 1 < n) store(c + 1);
     // dS behind the chunk, half of both columns' tiles by each of the two wavefronts.
-    const unsigned all = base + 2 * kBuffer + kPairs * kFour;
+    const unsigned all_s = base + 2 * kBuffer + kPairs * kFour;
     char *to = both(c) + vt * 2048;
 #pragma unroll
-    for (int j = 0; j < NB / 2; ++j)
+    for (int j = 0; j < (FIND ? 0 : NB / 2); ++j)
 #pragma unroll
       for (int part = 0; part < 2; ++part)
-        __builtin_nontemporal_store(turned<true>(all, all + kState, 2 * j + w, part, lane),
+        __builtin_nontemporal_store(turned<true>(all_s, all_s + kState, 2 * j + w, part, lane),
                                     reinterpret_cast<bf8 *>(to + (2 * j + w) * nv * 2048 + part * 1024));
     const unsigned tile = base + (c & 1) * kBuffer, at_a = tile + kAtW + kGdrTriBytes, gates = at_a + kGdrTriBytes + 16 * g;
     Parts af[kGdrFrags];
@@ -231,7 +240,7 @@ __global__ void __launch_bounds__(256) gdr_bwd_kernel(const GdrParams p) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) *(lds_f4v *)(four + i * 1024) = x[i];
     meet();
-    if (c > 0) fetch_rows(c - 1);
+    if (c > first) fetch_rows(c - 1);
     f4v z[NB] = {};
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
@@ -249,11 +258,13 @@ __global__ void __launch_bounds__(256) gdr_bwd_kernel(const GdrParams p) {
 #pragma unroll
     for (int j = 0; j < NB; ++j) *(lds_f4v *)(grown + j * 1024) = z[j];
     meet();
-    if (c > 0) fetch_ws(c - 1);
-    turn(c);
+    if (c > first) fetch_ws(c - 1);
+    if (!FIND) turn(c);
   }
-  if (n > 0) store(0);
-  for (int64_t row = 64 * static_cast<int64_t>(n) + g; row < p.seqlen; row += 4) st(vp, row * yt + m, 0.0f);
+  if (FIND) return;
+  if (n > first) store(first);
+  const int64_t last = segment + 1 < p.seg.count ? 64 * (first + p.seg.chunks) : p.seqlen;  // the segment's rows behind the length
+  for (int64_t row = 64 * static_cast<int64_t>(n > first ? n : first) + g; row < last && row < p.seqlen; row += 4) st(vp, row * yt + m, 0.0f);
 }
 
 // ---------------------------------------------------------------------------
@@ -551,7 +562,15 @@ void grad(const GdrParams &p, hipStream_t s) {
 template <int KD>
 hipError_t bwd(const GdrParams &p, hipStream_t s) {
   const int64_t heads = p.batch * p.nheads;
-  hipLaunchKernelGGL((gdr_bwd_kernel<KD>), dim3(static_cast<uint32_t>(heads * (p.vdim / 32))), dim3(256), 0, s, p);
+  const int64_t columns = heads * (p.vdim / 32);
+  if (p.seg.count > 1) {
+    hipLaunchKernelGGL((gdr_bwd_kernel<KD, true>), dim3(static_cast<uint32_t>(columns * (p.seg.count - 1))), dim3(256), 0, s, p);
+    if (p.seg.count > 2) {
+      launch_gdr_bwd_carry(p, s);
+      launch_gdr_bwd_join(p, s);
+    }
+  }
+  hipLaunchKernelGGL((gdr_bwd_kernel<KD, false>), dim3(static_cast<uint32_t>(columns * p.seg.count)), dim3(256), 0, s, p);
   if (p.chunks > 0) {
     if (p.vdim == 64) p.gates_bf16 ? grad<KD, 64, uint16_t>(p, s) : grad<KD, 64, float>(p, s);
     else p.gates_bf16 ? grad<KD, 128, uint16_t>(p, s) : grad<KD, 128, float>(p, s);
@@ -561,8 +580,29 @@ hipError_t bwd(const GdrParams &p, hipStream_t s) {
 
 }  // namespace
 
-size_t gdr_bwd_workspace(const GdrParams &p) {
-  return static_cast<size_t>(p.batch) * p.nheads * p.chunks * gdr_both_bytes(p.kdim, p.vdim);
+GdrSegments gdr_bwd_segments(int64_t heads, int64_t kdim, int64_t vdim, int64_t chunks) {
+  // As gdr_segments(): in turn a chunk takes 2.7 us (keys of 64: 1.9), without
+  // what is stored 2.3 (1.7).
+  const bool wide = kdim == 128;
+  const int64_t columns = heads * (vdim / 32), pairs = heads * (kdim / 64);
+  int64_t best = 1;
+  double least = (wide ? 2.7 : 1.9) * static_cast<double>(chunks) + 4.0;
+  for (int64_t g = 2; g <= 64 && g <= chunks && columns * g <= 256; ++g) {
+    const double each = static_cast<double>((chunks + g - 1) / g);
+    double us = ((wide ? 2.3 : 1.7) + (wide ? 2.7 : 1.9)) * each + 8.0;
+    if (g > 2) us += (wide ? 2.0 : 1.45) * each * static_cast<double>((pairs * (g - 2) + 255) / 256) + 8.0 + (wide ? 1.2 : 0.4) * static_cast<double>(g);
+    if (us < least) {
+      least = us;
+      best = g;
+    }
+  }
+  const int64_t each = (chunks + best - 1) / best;
+  return {each > 0 ? (chunks + each - 1) / each : 1, each > 0 ? each : 1};
+}
+
+GdrSizes gdr_bwd_sizes(const GdrParams &p) {
+  const size_t heads = static_cast<size_t>(p.batch) * p.nheads, n = p.seg.count > 1 ? heads * p.seg.count : 0;
+  return {heads * p.chunks * gdr_both_bytes(p.kdim, p.vdim), n * p.vdim * p.kdim * 4, n * 2 * p.kdim * p.kdim * 2};
 }
 
 hipError_t launch_gdr_bwd(const GdrParams &p, hipStream_t s) { return p.kdim == 64 ? bwd<64>(p, s) : bwd<128>(p, s); }

@@ -27,6 +27,8 @@ constexpr size_t gdr_saved_bytes(int64_t kdim, int64_t vdim) { return gdr_both_b
 // Long sequences of few heads are cut into segments of `chunks` chunks, and the
 // state at the start of each is found before y is made: with S_0 = 0 and with
 // S_0 = I a segment gives E and P, and its end is P S_0 + E.
+// Backwards alike: from dS = 0 a segment gives an E of its own, and dS before
+// it is P^T dS + E.
 struct GdrSegments {
   int64_t count, chunks;
 };
@@ -50,8 +52,8 @@ struct GdrParams {
   float *dh0;                  // nullable
   char *ws_both;               // the backward's dS and D: gdr_both_bytes() each
   GdrSegments seg;
-  float *ws_state;             // (row, value head, segment): E, and then the state before the segment
-  uint16_t *ws_carry;          // (row, value head, segment): P, as operands in two parts
+  float *ws_state;             // (row, value head, segment): E, and then the state before the segment, or dS behind it
+  uint16_t *ws_carry;          // (row, value head, segment): P (backward: P^T), as operands in two parts
   int64_t batch, seqlen, nqk, nheads, chunks;
   int64_t q_batch, q_token, k_batch, k_token, v_batch, v_token;
   float scale;
@@ -62,7 +64,10 @@ struct GdrSizes {
   size_t chunks, state, carry;
 };
 GdrSizes gdr_sizes(const GdrParams &p);
-size_t gdr_bwd_workspace(const GdrParams &p);
+GdrSegments gdr_bwd_segments(int64_t heads, int64_t kdim, int64_t vdim, int64_t chunks);
+GdrSizes gdr_bwd_sizes(const GdrParams &p);  // of the backward's: ws_both, ws_state and ws_carry
+void launch_gdr_bwd_carry(const GdrParams &p, hipStream_t stream);
+void launch_gdr_bwd_join(const GdrParams &p, hipStream_t stream);
 hipError_t launch_gdr_bwd(const GdrParams &p, hipStream_t stream);
 hipError_t launch_gdr_fwd(const GdrParams &p, hipStream_t stream);
 hipError_t launch_gdr_step(const GdrParams &p, hipStream_t stream);  // h0 -> h_last

@@ -417,22 +417,23 @@ __global__ void __launch_bounds__(256) gdr_fwd_kernel(const GdrParams p) {
 }
 
 // E and P of a segment: 64 columns a workgroup, of E (the values' columns, from
-// a state of 0) or P (the columns of the unit matrix, without values).
-template <int KD>
+// a state of 0) or P (the columns of the unit matrix, without values).  The
+// backward takes P alone, transposed, of all segments but the first and last.
+template <int KD, bool BWD>
 __global__ void __launch_bounds__(256, 2) gdr_segment_kernel(const GdrParams p) {
   constexpr int NT = 256, NC = 64, NS = KD / 32, NB = KD / 16;
   constexpr unsigned kRows = 64 * KD * 2, kAtV = kRows, kAtW = kAtV + 64 * NC * 2, kAtG = kAtW + kGdrTriBytes, kBuffer = kAtG + kGdrGateBytes;
   __shared__ __align__(16) u4 lds[2 * kBuffer / 16];
   const int tid = threadIdx.x, lane = tid & 63, m = lane & 15, g = lane >> 4;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const unsigned vtiles = static_cast<unsigned>(p.vdim) / NC, tiles = vtiles + KD / NC;
-  const HeadTile which = head_tile(blockIdx.x, static_cast<unsigned>(p.batch * p.nheads), tiles * static_cast<unsigned>(p.seg.count - 1));
+  const unsigned vtiles = BWD ? 0 : static_cast<unsigned>(p.vdim) / NC, tiles = vtiles + KD / NC;
+  const HeadTile which = head_tile(blockIdx.x, static_cast<unsigned>(p.batch * p.nheads), tiles * static_cast<unsigned>(p.seg.count - (BWD ? 2 : 1)));
   const int64_t bh = which.head, b = bh / p.nheads, h = bh % p.nheads, hk = h / (p.nheads / p.nqk);
-  const int segment = static_cast<int>(which.tile / tiles), len = gdr_length(p.lengths, b, p.seqlen);
+  const int segment = static_cast<int>(which.tile / tiles) + (BWD ? 1 : 0), len = gdr_length(p.lengths, b, p.seqlen);
   const int first = segment * static_cast<int>(p.seg.chunks), n = first + static_cast<int>(p.seg.chunks);
   if (64 * static_cast<int64_t>(n) >= len) return;  // the row has no segment behind this one: all its chunks are whole, too
   const unsigned tile = which.tile % tiles;
-  const bool values = tile < vtiles;
+  const bool values = !BWD && tile < vtiles;
   const int col = static_cast<int>(values ? tile : tile - vtiles) * NC + 16 * w + m;
   const uint16_t *kp = p.k + b * p.k_batch + hk * KD, *vp = p.v + b * p.v_batch + h * p.vdim + tile * NC;
   const char *ws = p.ops + bh * p.chunks * p.ops_step;
@@ -498,6 +499,15 @@ __global__ void __launch_bounds__(256, 2) gdr_segment_kernel(const GdrParams p) 
     float *to = p.ws_state + ((seg + 1) * p.vdim + col) * KD + 8 * g;  // where the join reads it and puts the state itself
 #pragma unroll
     for (int j = 0; j < NB; ++j) *reinterpret_cast<f4v *>(to + 32 * (j / 2) + 4 * (j % 2)) = s[j];
+  } else if (BWD) {
+    // P^T as the join's operands, [16 key elements in][32 out][part], 1 KiB each: as it lies.
+    char *to = reinterpret_cast<char *>(p.ws_carry + seg * 2 * KD * KD) + (4 * tile + w) * NS * 2048 + lane * 16;
+#pragma unroll
+    for (int a = 0; a < NS; ++a) {
+      const Parts sp = parts(s[2 * a], s[2 * a + 1]);
+      *reinterpret_cast<bf8 *>(to + a * 2048) = sp.hi;
+      *reinterpret_cast<bf8 *>(to + a * 2048 + 1024) = sp.lo;
+    }
   } else {
     // P as the join's operands, [16 key elements out][32 in][part], 1 KiB each: turned round in LDS.
     typedef __attribute__((address_space(3))) u4 lds16;
@@ -523,8 +533,9 @@ __global__ void __launch_bounds__(256, 2) gdr_segment_kernel(const GdrParams p) 
 // workgroup, a quarter of the key elements a wavefront.  Each takes its part of
 // P from memory, one segment ahead, and the columns' state from LDS, where all
 // four leave theirs.  1.2 us a segment (keys of 64: 0.4); with 64 columns a
-// workgroup and P in LDS 4.3.
-template <int KD>
+// workgroup and P in LDS 4.3.  Backwards the dS behind each segment, P^T dS + E
+// of the one behind, from the last but one's, which is there.
+template <int KD, bool BWD>
 __global__ void __launch_bounds__(256) gdr_join_kernel(const GdrParams p) {
   constexpr int NS = KD / 32, NB = KD / 16, NJ = NB / 4;
   __shared__ __align__(16) u4 lds[2][NS * 2 * 64];
@@ -534,31 +545,43 @@ __global__ void __launch_bounds__(256) gdr_join_kernel(const GdrParams p) {
   const int64_t bh = which.head, b = bh / p.nheads;
   const int col = static_cast<int>(which.tile) * 16 + m, len = gdr_length(p.lengths, b, p.seqlen);
   const int span = static_cast<int>(p.seg.chunks) * 64, n = (len + span - 1) / span;  // segments of this row
-  // This wavefront's blocks of 16 key elements, as they come out of a product: 16 j + 4g + r.
-  const int at = 16 * NJ * w + 4 * g;
-  float *begin = p.ws_state + (bh * p.seg.count * p.vdim + col) * KD + at;
-  const char *carry = reinterpret_cast<const char *>(p.ws_carry + bh * p.seg.count * 2 * KD * KD) + NJ * w * NS * 2048 + lane * 16;
+  const int steps = n - (BWD ? 2 : 1);
+  if (BWD && steps < 1) return;
+  // This wavefront's blocks of 16 key elements in a column: P's rows lie as its
+  // products leave them (16 j + 4g + r), P^T's are put in the order of the state
+  // in the chains (32 (j / 2) + 8g + 4 (j % 2) + r), which its columns have.
+  auto place = [&](int j) { return BWD ? 32 * ((NJ * w + j) / 2) + 8 * g + 4 * ((NJ * w + j) % 2) : 16 * (NJ * w + j) + 4 * g; };
+  auto row = [&](int j) { return BWD ? 32 * ((NJ * w + j) / 2) + 8 * (m >> 2) + 4 * ((NJ * w + j) % 2) + (m & 3) : 16 * (NJ * w + j) + m; };
+  auto slot_of = [&](int i) { return p.ws_state + ((bh * p.seg.count + i) * p.vdim + col) * KD; };
+  const char *carry = reinterpret_cast<const char *>(p.ws_carry + bh * p.seg.count * 2 * KD * KD) + g * 256;
   f4v s[NJ], next[NJ];
   Parts pp[NJ][NS];
-  auto fetch = [&](int i) {
+  auto segment = [&](int t) { return BWD ? n - 2 - t : t; };
+  auto fetch = [&](int t) {
+    const int i = segment(t);
+    const float *to = slot_of(BWD ? i - 1 : i + 1);
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
-      next[j] = *reinterpret_cast<const f4v *>(begin + static_cast<int64_t>(i + 1) * p.vdim * KD + 16 * j);
+      next[j] = *reinterpret_cast<const f4v *>(to + place(j));
 #pragma unroll
       for (int a = 0; a < NS; ++a) {
-        const char *from = carry + static_cast<int64_t>(i) * 4 * KD * KD + (j * NS + a) * 2048;
+        const char *from = carry + static_cast<int64_t>(i) * 4 * KD * KD + ((row(j) >> 4) * NS + a) * 2048 + (row(j) & 15) * 16;
         pp[j][a] = {*reinterpret_cast<const bf8 *>(from), *reinterpret_cast<const bf8 *>(from + 1024)};
       }
     }
   };
-  if (n > 1) fetch(0);
+  if (steps > 0) fetch(0);
 #pragma unroll
   for (int j = 0; j < NJ; ++j) {
-    s[j] = p.h0 != nullptr ? *reinterpret_cast<const f4v *>(p.h0 + (bh * p.vdim + col) * KD + at + 16 * j) : f4v{};
-    *reinterpret_cast<f4v *>(begin + 16 * j) = s[j];
+    if constexpr (BWD) {
+      s[j] = *reinterpret_cast<const f4v *>(slot_of(n - 2) + place(j));
+    } else {
+      s[j] = p.h0 != nullptr ? *reinterpret_cast<const f4v *>(p.h0 + (bh * p.vdim + col) * KD + place(j)) : f4v{};
+      *reinterpret_cast<f4v *>(slot_of(0) + place(j)) = s[j];
+    }
   }
-  for (int i = 0; i + 1 < n; ++i) {
-    char *mine = reinterpret_cast<char *>(lds[i & 1]);
+  for (int t = 0; t < steps; ++t) {
+    char *mine = reinterpret_cast<char *>(lds[t & 1]);
     if constexpr (NJ == 2) {
       const Parts sp = parts(s[0], s[1]);
       *reinterpret_cast<bf8 *>(mine + w * 2048 + lane * 16) = sp.hi;
@@ -578,9 +601,10 @@ __global__ void __launch_bounds__(256) gdr_join_kernel(const GdrParams p) {
 #pragma unroll
       for (int j = 0; j < NJ; ++j) s[j] = mul_parts(pp[j][a], sp, s[j]);
     }
-    if (i + 2 < n) fetch(i + 1);
+    if (t + 1 < steps) fetch(t + 1);
+    float *to = slot_of(BWD ? segment(t) - 1 : segment(t) + 1);
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) *reinterpret_cast<f4v *>(begin + static_cast<int64_t>(i + 1) * p.vdim * KD + 16 * j) = s[j];
+    for (int j = 0; j < NJ; ++j) *reinterpret_cast<f4v *>(to + place(j)) = s[j];
   }
 }
 
@@ -657,11 +681,23 @@ hipError_t fwd(const GdrParams &p, hipStream_t s) {
   if (p.chunks > 0) p.gates_bf16 ? chunks<KD, uint16_t>(p, s) : chunks<KD, float>(p, s);
   if (p.seg.count > 1) {
     const int64_t parts = heads * (p.seg.count - 1) * ((p.vdim + KD) / 64);
-    hipLaunchKernelGGL((gdr_segment_kernel<KD>), dim3(static_cast<uint32_t>(parts)), dim3(256), 0, s, p);
-    hipLaunchKernelGGL((gdr_join_kernel<KD>), dim3(static_cast<uint32_t>(heads * (p.vdim / 16))), dim3(256), 0, s, p);
+    hipLaunchKernelGGL((gdr_segment_kernel<KD, false>), dim3(static_cast<uint32_t>(parts)), dim3(256), 0, s, p);
+    hipLaunchKernelGGL((gdr_join_kernel<KD, false>), dim3(static_cast<uint32_t>(heads * (p.vdim / 16))), dim3(256), 0, s, p);
   }
   hipLaunchKernelGGL((gdr_fwd_kernel<KD>), dim3(static_cast<uint32_t>(heads * (p.vdim / 32) * p.seg.count)), dim3(256), 0, s, p);
   return hipGetLastError();
+}
+
+template <int KD>
+void bwd_carry(const GdrParams &p, hipStream_t s) {
+  const int64_t parts = p.batch * p.nheads * (p.seg.count - 2) * (KD / 64);
+  hipLaunchKernelGGL((gdr_segment_kernel<KD, true>), dim3(static_cast<uint32_t>(parts)), dim3(256), 0, s, p);
+}
+
+template <int KD>
+void bwd_join(const GdrParams &p, hipStream_t s) {
+  const int64_t groups = p.batch * p.nheads * (p.vdim / 16);
+  hipLaunchKernelGGL((gdr_join_kernel<KD, true>), dim3(static_cast<uint32_t>(groups)), dim3(256), 0, s, p);
 }
 
 template <int KD, typename G>
@@ -699,6 +735,9 @@ GdrSegments gdr_segments(int64_t heads, int64_t kdim, int64_t vdim, int64_t chun
   const int64_t each = (chunks + best - 1) / best;
   return {each > 0 ? (chunks + each - 1) / each : 1, each > 0 ? each : 1};
 }
+
+void launch_gdr_bwd_carry(const GdrParams &p, hipStream_t s) { p.kdim == 64 ? bwd_carry<64>(p, s) : bwd_carry<128>(p, s); }
+void launch_gdr_bwd_join(const GdrParams &p, hipStream_t s) { p.kdim == 64 ? bwd_join<64>(p, s) : bwd_join<128>(p, s); }
 
 GdrSizes gdr_sizes(const GdrParams &p) {
   const size_t heads = static_cast<size_t>(p.batch) * p.nheads, n = p.seg.count > 1 ? heads * p.seg.count : 0;

@@ -207,7 +207,7 @@ def test_segments_stay_within_what_is_launched():
                     if segments == 1:   # the blocks' parts alone
                         assert need % max(1, heads * chunks) == 0
                     assert 0 <= need <= heads * chunks * (1 << 17) + heads * segments * each
-                    assert size("ssm_gdr_bwd_workspace_size", d) <= heads * chunks * (1 << 18) + heads * each
+                    assert size("ssm_gdr_bwd_workspace_size", d) <= heads * chunks * (1 << 18) + heads * segments * each
 
 
 @needs_no_gpu

@@ -122,7 +122,10 @@ def by_norm(t):
     return 2.0 ** -12 + (0.0 if t.dtype != BF16 else U if t.numel() < 1024 else U / 3 ** 0.5)
 
 
-BACKWARD = CASES + [(1, 300, 2, 8, 64, 128, BF16, True, None), (2, 140, 1, 4, 128, 64, F32, True, [140, 77])]
+BACKWARD = CASES + [(1, 300, 2, 8, 64, 128, BF16, True, None), (2, 140, 1, 4, 128, 64, F32, True, [140, 77]),
+                    # Few heads: time in segments, of rows that end in any of them.
+                    (1, 1300, 1, 2, 128, 64, F32, True, None), (2, 1500, 1, 1, 64, 128, BF16, True, [1500, 200]),
+                    (3, 1400, 1, 1, 128, 128, F32, False, [1, 0, 1400]), (4, 1024, 2, 2, 64, 64, F32, True, [1024, 129, 128, 900])]
 
 
 @pytest.mark.parametrize("B,L,nqk,H,K,V,gates,with_h0,lengths", BACKWARD)
