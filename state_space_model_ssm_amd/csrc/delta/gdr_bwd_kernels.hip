@@ -15,12 +15,12 @@
 //
 // A first kernel goes from chunk to chunk backwards with dS (as the forward,
 // bound by its chain; 3.4 us a chunk with the 96 KiB of dS and D that it leaves
-// behind); a second has all chunks at once and is bound by reading those and
-// what the forward saved.  Roundings as in the forward, outputs when they are
-// stored.
+// behind), and is cut into segments where heads are few; a second has all
+// chunks at once and is bound by reading those and what the forward saved.
+// Roundings as in the forward, outputs when they are stored.
 //
-// Measured, 4 x 2048 tokens, 16 heads of 128: 108 us, and 162 for 557 MB (3.4
-// TB/s, where a large read reaches 4.0); a training pass 394 us with the
+// Measured, 4 x 2048 tokens, 16 heads of 128: 110 us, and 162 for 557 MB (3.4
+// TB/s, where a large read reaches 4.0); a training pass 386 us with the
 // forward.
 #include "gdr_tile.h"
 
@@ -582,7 +582,10 @@ hipError_t bwd(const GdrParams &p, hipStream_t s) {
 
 GdrSegments gdr_bwd_segments(int64_t heads, int64_t kdim, int64_t vdim, int64_t chunks) {
   // As gdr_segments(): in turn a chunk takes 2.7 us (keys of 64: 1.9), without
-  // what is stored 2.3 (1.7).
+  // what is stored 2.3 (1.7).  Kernels of forward and backward together, us: 2
+  // heads of 64, 8192 tokens: 1 segment of the backward 329, 8 155, 32 115; 8 of
+  // 128 on 2, 2048 tokens: 1 206, 8 171, 16 184; 16 of 128, 4 x 2048: 1 406, 2
+  // 453.
   const bool wide = kdim == 128;
   const int64_t columns = heads * (vdim / 32), pairs = heads * (kdim / 64);
   int64_t best = 1;
