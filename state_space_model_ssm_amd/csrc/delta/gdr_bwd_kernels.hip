@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(256) gdr_bwd_kernel(const GdrParams p) {
 #pragma unroll
         for (int j = 0; j < NB; ++j) kt[k][j] = col16<KD>(tile, j, k, at);
       // E = T^T dU
-      f4v e[4] = {};
+      f4v e[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const Parts xp = parts(x[2 * k], x[2 * k + 1]);

@@ -179,6 +179,9 @@ __global__ void __launch_bounds__(256) gdr_chunk_kernel(const GdrParams p) {
 #pragma unroll
       for (int r = 0; r < 4; ++r) t[j] = mfma_f32(-d[r], acc[r], t[j]);
     }
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      if (4 * g + r == m) t[W][r] = 0.0f;  // the ones stay out of what is rounded
     store_rows<W>(t, out, lane);
   });
 }
@@ -194,7 +197,7 @@ __global__ void __launch_bounds__(256) gdr_chunk_kernel(const GdrParams p) {
 // SIMD to itself.  A chunk takes 2.2 us (keys of 64: 1.5), 1300 cycles of which
 // are the state's own matrix instructions; the rest is its operands' way
 // through LDS and the splitting into parts.  With what the backward needs 3.2.
-template <int KD>
+template <int KD, bool LAST>
 __global__ void __launch_bounds__(256) gdr_fwd_kernel(const GdrParams p) {
   constexpr int NT = 64 * kPairs, NC = 16 * kPairs, NS = KD / 32, NB = KD / 16;
   constexpr unsigned kRows = 64 * KD * 2, kValues = 64 * NC * 2;
@@ -228,10 +231,10 @@ __global__ void __launch_bounds__(256) gdr_fwd_kernel(const GdrParams p) {
 #pragma unroll
     for (int j = 0; j < NB; ++j) s[j] = begins ? *reinterpret_cast<const f4v *>(from + 32 * (j / 2) + 4 * (j % 2)) : f4v{};
     for (int c = first; c < n; ++c) {
-      Parts sp[NS];
+      decltype(split<LAST>(s[0], s[0])) sp[NS];
 #pragma unroll
       for (int a = 0; a < NS; ++a) {
-        sp[a] = parts(s[2 * a], s[2 * a + 1]);
+        sp[a] = split<LAST>(s[2 * a], s[2 * a + 1]);
         *(lds16 *)(parts_s + a * 2048) = __builtin_bit_cast(u4, sp[a].hi);
         *(lds16 *)(parts_s + a * 2048 + 1024) = __builtin_bit_cast(u4, sp[a].lo);
       }
@@ -261,14 +264,16 @@ __global__ void __launch_bounds__(256) gdr_fwd_kernel(const GdrParams p) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) x[i] = mul_exact(ka[a][i], sp[a], x[i]);
       // beta (v - e^G x), and u = T of that
-      f4v u[4] = {};
+      f4v u[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < 4; ++i) {
 #pragma unroll
         for (int r = 0; r < 4; ++r) x[i][r] = beta[i][r] * fmaf(-into[i][r], x[i][r], up(vf[i][r]));
+        u[i] = x[i];
+      }
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        const Parts xp = parts(x[2 * k], x[2 * k + 1]);
+        const auto xp = split<LAST>(x[2 * k], x[2 * k + 1]);
 #pragma unroll
         for (int i = 2 * k; i < 4; ++i) u[i] = mul_parts(tf[tri(i, k)], xp, u[i]);
       }
@@ -290,7 +295,7 @@ __global__ void __launch_bounds__(256) gdr_fwd_kernel(const GdrParams p) {
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const f4v o0 = lds_f4(gates + 512 + 128 * k), o1 = lds_f4(gates + 512 + 128 * k + 64);
-        const Parts up = parts(u[2 * k] * o0, u[2 * k + 1] * o1);
+        const auto up = split<LAST>(u[2 * k] * o0, u[2 * k + 1] * o1);
 #pragma unroll
         for (int j = 0; j < NB; ++j) s[j] = mul_exact(kt[k][j], up, s[j]);
       }
@@ -465,7 +470,7 @@ __global__ void __launch_bounds__(256, 2) gdr_segment_kernel(const GdrParams p) 
     f4v x[4] = {};
 #pragma unroll
     for (int a = 0; a < NS; ++a) {
-      const Parts sp = parts(s[2 * a], s[2 * a + 1]);
+      const auto sp = split<!BWD>(s[2 * a], s[2 * a + 1]);
 #pragma unroll
       for (int i = 0; i < 4; ++i) x[i] = mul_exact(row16<KD>(buffer, i, a, at), sp, x[i]);
     }
@@ -476,10 +481,10 @@ __global__ void __launch_bounds__(256, 2) gdr_segment_kernel(const GdrParams p) 
 #pragma unroll
       for (int r = 0; r < 4; ++r) x[i][r] = beta[r] * fmaf(-into[r], x[i][r], values ? up(v[r]) : 0.0f);
     }
-    f4v u[4] = {};
+    f4v u[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      const Parts xp = parts(x[2 * k], x[2 * k + 1]);
+      const auto xp = split<!BWD>(x[2 * k], x[2 * k + 1]);
 #pragma unroll
       for (int i = 2 * k; i < 4; ++i)
         u[i] = mul_parts(Parts{frag16(tri_t, tri(i, k), lane), frag16(tri_t, kGdrFrags + tri(i, k), lane)}, xp, u[i]);
@@ -489,7 +494,7 @@ __global__ void __launch_bounds__(256, 2) gdr_segment_kernel(const GdrParams p) 
     for (int j = 0; j < NB; ++j) s[j] *= whole;
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      const Parts up = parts(u[2 * k] * lds_f4(gates + 512 + 128 * k), u[2 * k + 1] * lds_f4(gates + 512 + 128 * k + 64));
+      const auto up = split<!BWD>(u[2 * k] * lds_f4(gates + 512 + 128 * k), u[2 * k + 1] * lds_f4(gates + 512 + 128 * k + 64));
 #pragma unroll
       for (int j = 0; j < NB; ++j) s[j] = mul_exact(col16<KD>(buffer, j, k, at), up, s[j]);
     }
@@ -509,23 +514,28 @@ __global__ void __launch_bounds__(256, 2) gdr_segment_kernel(const GdrParams p) 
       *reinterpret_cast<bf8 *>(to + a * 2048 + 1024) = sp.lo;
     }
   } else {
-    // P as the join's operands, [16 key elements out][32 in][part], 1 KiB each: turned round in LDS.
+    // P as the join's operands, [16 key elements out][32 in][part], 1 KiB each,
+    // turned round in LDS: the first two parts, then the third.
     typedef __attribute__((address_space(3))) u4 lds16;
-    meet();
-#pragma unroll
-    for (int a = 0; a < NS; ++a) {
-      const Parts sp = parts(s[2 * a], s[2 * a + 1]);
-      *(lds16 *)(base + (w * NS + a) * 2048 + lane * 16) = __builtin_bit_cast(u4, sp.hi);
-      *(lds16 *)(base + (w * NS + a) * 2048 + 1024 + lane * 16) = __builtin_bit_cast(u4, sp.lo);
-    }
-    meet();
     const unsigned left = base + (w & ~1) * NS * 2048;
-    char *to = reinterpret_cast<char *>(p.ws_carry + seg * 2 * KD * KD) + (2 * (tile - vtiles) + w / 2) * 2048 + lane * 16;
+    char *to = reinterpret_cast<char *>(p.ws_carry + seg * 3 * KD * KD) + (2 * (tile - vtiles) + w / 2) * (3 * 1024) + lane * 16;
 #pragma unroll
-    for (int i = 0; i < NB / 2; ++i)
+    for (int pass = 0; pass < 2; ++pass) {
+      meet();
 #pragma unroll
-      for (int part = 0; part < 2; ++part)
-        *reinterpret_cast<bf8 *>(to + (2 * i + w % 2) * NS * 2048 + part * 1024) = turned<true>(left, left + NS * 2048, 2 * i + w % 2, part, lane);
+      for (int a = 0; a < NS; ++a) {
+        const Parts3 sp = parts3(s[2 * a], s[2 * a + 1]);
+        *(lds16 *)(base + (w * NS + a) * 2048 + lane * 16) = __builtin_bit_cast(u4, pass == 0 ? sp.hi : sp.rest);
+        if (pass == 0) *(lds16 *)(base + (w * NS + a) * 2048 + 1024 + lane * 16) = __builtin_bit_cast(u4, sp.lo);
+      }
+      meet();
+#pragma unroll
+      for (int i = 0; i < NB / 2; ++i)
+#pragma unroll
+        for (int part = 0; part < 2 - pass; ++part)
+          *reinterpret_cast<bf8 *>(to + (2 * i + w % 2) * NS * (3 * 1024) + (2 * pass + part) * 1024) =
+              turned<true>(left, left + NS * 2048, 2 * i + w % 2, part, lane);
+    }
   }
 }
 
@@ -537,8 +547,9 @@ __global__ void __launch_bounds__(256, 2) gdr_segment_kernel(const GdrParams p) 
 // of the one behind, from the last but one's, which is there.
 template <int KD, bool BWD>
 __global__ void __launch_bounds__(256) gdr_join_kernel(const GdrParams p) {
-  constexpr int NS = KD / 32, NB = KD / 16, NJ = NB / 4;
-  __shared__ __align__(16) u4 lds[2][NS * 2 * 64];
+  constexpr int NS = KD / 32, NB = KD / 16, NJ = NB / 4, NP = BWD ? 2 : 3, kFrag = NP * 1024;
+  typedef std::conditional_t<BWD, Parts, Parts3> Split;
+  __shared__ __align__(16) u4 lds[2][NS * NP * 64];
   const int tid = threadIdx.x, lane = tid & 63, m = lane & 15, g = lane >> 4;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const HeadTile which = head_tile(blockIdx.x, static_cast<unsigned>(p.batch * p.nheads), static_cast<unsigned>(p.vdim) / 16);
@@ -553,9 +564,9 @@ __global__ void __launch_bounds__(256) gdr_join_kernel(const GdrParams p) {
   auto place = [&](int j) { return BWD ? 32 * ((NJ * w + j) / 2) + 8 * g + 4 * ((NJ * w + j) % 2) : 16 * (NJ * w + j) + 4 * g; };
   auto row = [&](int j) { return BWD ? 32 * ((NJ * w + j) / 2) + 8 * (m >> 2) + 4 * ((NJ * w + j) % 2) + (m & 3) : 16 * (NJ * w + j) + m; };
   auto slot_of = [&](int i) { return p.ws_state + ((bh * p.seg.count + i) * p.vdim + col) * KD; };
-  const char *carry = reinterpret_cast<const char *>(p.ws_carry + bh * p.seg.count * 2 * KD * KD) + g * 256;
+  const char *carry = reinterpret_cast<const char *>(p.ws_carry + bh * p.seg.count * NP * KD * KD) + g * 256;
   f4v s[NJ], next[NJ];
-  Parts pp[NJ][NS];
+  Split pp[NJ][NS];
   auto segment = [&](int t) { return BWD ? n - 2 - t : t; };
   auto fetch = [&](int t) {
     const int i = segment(t);
@@ -565,8 +576,10 @@ __global__ void __launch_bounds__(256) gdr_join_kernel(const GdrParams p) {
       next[j] = *reinterpret_cast<const f4v *>(to + place(j));
 #pragma unroll
       for (int a = 0; a < NS; ++a) {
-        const char *from = carry + static_cast<int64_t>(i) * 4 * KD * KD + ((row(j) >> 4) * NS + a) * 2048 + (row(j) & 15) * 16;
-        pp[j][a] = {*reinterpret_cast<const bf8 *>(from), *reinterpret_cast<const bf8 *>(from + 1024)};
+        const char *from = carry + static_cast<int64_t>(i) * NP * 2 * KD * KD + ((row(j) >> 4) * NS + a) * kFrag + (row(j) & 15) * 16;
+        pp[j][a].hi = *reinterpret_cast<const bf8 *>(from);
+        pp[j][a].lo = *reinterpret_cast<const bf8 *>(from + 1024);
+        if constexpr (!BWD) pp[j][a].rest = *reinterpret_cast<const bf8 *>(from + 2048);
       }
     }
   };
@@ -582,22 +595,23 @@ __global__ void __launch_bounds__(256) gdr_join_kernel(const GdrParams p) {
   }
   for (int t = 0; t < steps; ++t) {
     char *mine = reinterpret_cast<char *>(lds[t & 1]);
-    if constexpr (NJ == 2) {
-      const Parts sp = parts(s[0], s[1]);
-      *reinterpret_cast<bf8 *>(mine + w * 2048 + lane * 16) = sp.hi;
-      *reinterpret_cast<bf8 *>(mine + w * 2048 + 1024 + lane * 16) = sp.lo;
-    } else {
-      const Parts sp = parts(s[0], s[0]);
-      *reinterpret_cast<u2 *>(mine + w / 2 * 2048 + lane * 16 + w % 2 * 8) = half_of(sp.hi, 0);
-      *reinterpret_cast<u2 *>(mine + w / 2 * 2048 + 1024 + lane * 16 + w % 2 * 8) = half_of(sp.lo, 0);
-    }
+    const Split own = split<!BWD>(s[0], s[NJ - 1]);
+    auto put = [&](int part, bf8 v) {
+      if constexpr (NJ == 2) *reinterpret_cast<bf8 *>(mine + w * kFrag + part * 1024 + lane * 16) = v;
+      else *reinterpret_cast<u2 *>(mine + w / 2 * kFrag + part * 1024 + lane * 16 + w % 2 * 8) = half_of(v, 0);
+    };
+    put(0, own.hi);
+    put(1, own.lo);
+    if constexpr (!BWD) put(2, own.rest);
     __syncthreads();  // (What is read here is written again after the next one.)
 #pragma unroll
     for (int j = 0; j < NJ; ++j) s[j] = next[j];
 #pragma unroll
     for (int a = 0; a < NS; ++a) {
-      const Parts sp = {*reinterpret_cast<const bf8 *>(mine + a * 2048 + lane * 16),
-                        *reinterpret_cast<const bf8 *>(mine + a * 2048 + 1024 + lane * 16)};
+      Split sp;
+      sp.hi = *reinterpret_cast<const bf8 *>(mine + a * kFrag + lane * 16);
+      sp.lo = *reinterpret_cast<const bf8 *>(mine + a * kFrag + 1024 + lane * 16);
+      if constexpr (!BWD) sp.rest = *reinterpret_cast<const bf8 *>(mine + a * kFrag + 2048 + lane * 16);
 #pragma unroll
       for (int j = 0; j < NJ; ++j) s[j] = mul_parts(pp[j][a], sp, s[j]);
     }
@@ -684,7 +698,9 @@ hipError_t fwd(const GdrParams &p, hipStream_t s) {
     hipLaunchKernelGGL((gdr_segment_kernel<KD, false>), dim3(static_cast<uint32_t>(parts)), dim3(256), 0, s, p);
     hipLaunchKernelGGL((gdr_join_kernel<KD, false>), dim3(static_cast<uint32_t>(heads * (p.vdim / 16))), dim3(256), 0, s, p);
   }
-  hipLaunchKernelGGL((gdr_fwd_kernel<KD>), dim3(static_cast<uint32_t>(heads * (p.vdim / 32) * p.seg.count)), dim3(256), 0, s, p);
+  const dim3 n(static_cast<uint32_t>(heads * (p.vdim / 32) * p.seg.count));
+  if (p.h_last != nullptr) hipLaunchKernelGGL((gdr_fwd_kernel<KD, true>), n, dim3(256), 0, s, p);
+  else hipLaunchKernelGGL((gdr_fwd_kernel<KD, false>), n, dim3(256), 0, s, p);
   return hipGetLastError();
 }
 
@@ -741,7 +757,7 @@ void launch_gdr_bwd_join(const GdrParams &p, hipStream_t s) { p.kdim == 64 ? bwd
 
 GdrSizes gdr_sizes(const GdrParams &p) {
   const size_t heads = static_cast<size_t>(p.batch) * p.nheads, n = p.seg.count > 1 ? heads * p.seg.count : 0;
-  return {heads * p.chunks * kGdrChunkBytes, n * p.vdim * p.kdim * 4, n * 2 * p.kdim * p.kdim * 2};
+  return {heads * p.chunks * kGdrChunkBytes, n * p.vdim * p.kdim * 4, n * 3 * p.kdim * p.kdim * 2};
 }
 
 hipError_t launch_gdr_fwd(const GdrParams &p, hipStream_t s) { return p.kdim == 64 ? fwd<64>(p, s) : fwd<128>(p, s); }

@@ -50,6 +50,23 @@ __device__ __forceinline__ Parts parts(const f4v &a, const f4v &b) {
   return p;
 }
 
+// And what that left off: 2^-27 of their size.
+struct Parts3 : Parts {
+  bf8 rest;
+};
+__device__ __forceinline__ Parts3 parts3(const f4v &a, const f4v &b) {
+  Parts3 p;
+  static_cast<Parts &>(p) = parts(a, b);
+  const u4 hi = __builtin_bit_cast(u4, p.hi), lo = __builtin_bit_cast(u4, p.lo);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float x = __uint_as_float(e % 2 != 0 ? hi[e / 2] & 0xffff0000u : hi[e / 2] << 16);
+    const float y = __uint_as_float(e % 2 != 0 ? lo[e / 2] & 0xffff0000u : lo[e / 2] << 16);
+    p.rest[e] = static_cast<__bf16>((e < 4 ? a[e % 4] : b[e % 4]) - x - y);
+  }
+  return p;
+}
+
 // The first or second four of an operand.
 __device__ __forceinline__ u2 half_of(bf8 v, int half) {
   const u4 bits = __builtin_bit_cast(u4, v);
@@ -60,6 +77,22 @@ __device__ __forceinline__ u2 half_of(bf8 v, int half) {
 __device__ __forceinline__ f4v mul_exact(bf8 a, const Parts &b, f4v c) { return mfma16(a, b.lo, mfma16(a, b.hi, c)); }
 __device__ __forceinline__ f4v mul_parts(const Parts &a, const Parts &b, f4v c) {
   return mfma16(a.hi, b.hi, mfma16(a.hi, b.lo, mfma16(a.lo, b.hi, c)));
+}
+// With the third part: to 2^-26.
+__device__ __forceinline__ f4v mul_exact(bf8 a, const Parts3 &b, f4v c) {
+  return mfma16(a, b.hi, mfma16(a, b.lo, mfma16(a, b.rest, c)));
+}
+__device__ __forceinline__ f4v mul_parts(const Parts &a, const Parts3 &b, f4v c) {
+  return mfma16(a.hi, b.hi, mfma16(a.hi, b.lo, mfma16(a.lo, b.hi, mfma16(a.hi, b.rest, mfma16(a.lo, b.lo, c)))));
+}
+__device__ __forceinline__ f4v mul_parts(const Parts3 &a, const Parts3 &b, f4v c) {
+  return mul_parts(static_cast<const Parts &>(a), b, mfma16(a.rest, b.hi, c));
+}
+// As many parts as asked for.
+template <bool THREE>
+__device__ __forceinline__ auto split(const f4v &a, const f4v &b) {
+  if constexpr (THREE) return parts3(a, b);
+  else return parts(a, b);
 }
 
 // Where a lane reads in a tile of 64 rows of D elements laid out by slot<D>(),
