@@ -9,8 +9,8 @@ namespace ssmb {
 constexpr int kGdrChunk = 64;
 
 // What is known of a chunk of 64 tokens and a value head before its state is:
-// T = (I + L)^-1 and the attention A within the chunk, as operands in bfloat16
-// parts (see gdr_tile.h), then the gates' factors.
+// T = (I + L)^-1 less I and the attention A within the chunk, as operands in
+// bfloat16 parts (see gdr_tile.h), then the gates' factors.
 constexpr int kGdrFrags = 6;                                   // operands of a triangle: 16 rows x 32 columns each
 constexpr size_t kGdrTriBytes = size_t{2} * kGdrFrags * 1024;  // both parts
 // Factors, 64 of each: scale e^G, e^G, e^(GC - G), beta (float32), and G log2(e) (float64).
@@ -53,7 +53,7 @@ struct GdrParams {
   char *ws_both;               // the backward's dS and D: gdr_both_bytes() each
   GdrSegments seg;
   float *ws_state;             // (row, value head, segment): E, and then the state before the segment, or dS behind it
-  uint16_t *ws_carry;          // (row, value head, segment): P (backward: P^T), as operands in two parts
+  uint16_t *ws_carry;          // (row, value head, segment): P in three parts (backward: P^T in two), as operands
   int64_t batch, seqlen, nqk, nheads, chunks;
   int64_t q_batch, q_token, k_batch, k_token, v_batch, v_token;
   float scale;

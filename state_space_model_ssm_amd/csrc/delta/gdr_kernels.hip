@@ -15,15 +15,19 @@
 // the columns are spread over all compute units, and where they do not fill
 // them, time is cut into segments (see gdr_segments()).
 //
-// Rounding: keys, queries and values are exact; T, A, S, U and what T takes
-// enter products as two bfloat16 parts, to 2^-18 of their size (in one part the
-// state would lose what bfloat16 cannot hold at every chunk; three would make
-// the chain's products half as many again for a state that is 4e-6 off at the
-// end, by norms, beside inputs of 2^-9).  Sums are float32, sums of g float64.
+// Rounding: keys, queries and values are exact; T - I, A and what of S and U
+// makes y and is saved enter products as two bfloat16 parts, to 2^-18 of their
+// size.  Two would leave the state itself 4e-6 off at the end, by norms, where
+// float32 token by token is 2e-7: where it is returned, S, U and what T takes
+// are in three parts as they make the next S (2^-26; below 1e-6 with the rest),
+// and so are a segment's E and P.  That costs a quarter of the chain's time (16
+// heads of 128, 8192 tokens: 151 us without).  T's ones are kept out of what is
+// rounded.  Sums are float32, sums of g float64.
 //
-// Measured, 16 heads of 128: one prompt of 8192 tokens in 152 us a call (chunks
-// 29 us, segments 54, join 11, y 74); training's 4 x 2048 in 29 and 105, of
-// which saving for the backward, 200 MB, is a third.
+// Measured, 16 heads of 128: one prompt of 8192 tokens in 184 us a call (chunks
+// 29 us, segments 73, join 15, y 91); training's 4 x 2048, where the last state
+// is not asked for, in 29 and 105, of which saving for the backward, 200 MB, is
+// a third.
 #include "gdr_tile.h"
 
 namespace ssmb {
@@ -194,9 +198,11 @@ __global__ void __launch_bounds__(256) gdr_chunk_kernel(const GdrParams p) {
 // What a chunk has to wait for is the state, so two wavefronts do nothing but
 // carry that, 16 columns each, and two others make y from the operands that
 // those leave in LDS, and copy the next chunk there: each of the four has a
-// SIMD to itself.  A chunk takes 2.2 us (keys of 64: 1.5), 1300 cycles of which
-// are the state's own matrix instructions; the rest is its operands' way
-// through LDS and the splitting into parts.  With what the backward needs 3.2.
+// SIMD to itself.  LAST: the last state is returned, and held to float32.  A
+// chunk takes 2.7 us then (keys of 64: 1.7), 2000 cycles of which are the
+// state's own matrix instructions, else 2.2 (1.5) with 1300; the rest is its
+// operands' way through LDS and the splitting into parts.  With what the
+// backward needs 3.2.
 template <int KD, bool LAST>
 __global__ void __launch_bounds__(256) gdr_fwd_kernel(const GdrParams p) {
   constexpr int NT = 64 * kPairs, NC = 16 * kPairs, NS = KD / 32, NB = KD / 16;
@@ -542,8 +548,8 @@ __global__ void __launch_bounds__(256, 2) gdr_segment_kernel(const GdrParams p) 
 // The state before each segment, P S + E of the one before: 16 columns a
 // workgroup, a quarter of the key elements a wavefront.  Each takes its part of
 // P from memory, one segment ahead, and the columns' state from LDS, where all
-// four leave theirs.  1.2 us a segment (keys of 64: 0.4); with 64 columns a
-// workgroup and P in LDS 4.3.  Backwards the dS behind each segment, P^T dS + E
+// four leave theirs.  1.7 us a segment (keys of 64: 0.5), 1.2 with two parts;
+// with 64 columns a workgroup and P in LDS 4.3.  Backwards the dS behind each segment, P^T dS + E
 // of the one behind, from the last but one's, which is there.
 template <int KD, bool BWD>
 __global__ void __launch_bounds__(256) gdr_join_kernel(const GdrParams p) {
@@ -726,23 +732,23 @@ hipError_t step(const GdrParams &p, hipStream_t s) {
 }  // namespace
 
 GdrSegments gdr_segments(int64_t heads, int64_t kdim, int64_t vdim, int64_t chunks) {
-  // Times in us, measured.  In turn a chunk takes 1.8 (keys of 64: 1.45).  With G
+  // Times in us, measured.  In turn a chunk takes 2.3 (keys of 64: 1.6).  With G
   // segments each is gone through twice, once for E and P (a compute unit has
   // two workgroups of these, and they are faster together) and once for y (it
   // has one), and the join takes a step per segment.  16 heads of 128, 8192
-  // tokens: 1 segment 264, 4 176, 8 169, 16 190; 2 heads of 64, 16384 tokens: 1
-  // 388, 32 57, 64 61; 32 heads of 128, 4096 tokens: 1 151, 2 166, 4 160.
+  // tokens: 1 segment 320, 4 210, 8 203, 16 223; 2 heads of 64, 16384 tokens: 1
+  // 427, 32 64, 64 63; 32 heads of 128, 4096 tokens: 1 172, 2 192, 4 186.
   const bool wide = kdim == 128;
   const int64_t columns = heads * (vdim / 32), pairs = heads * ((vdim + kdim) / 64);
-  const double a = wide ? 2.0 : 1.45;
+  const double a = wide ? 2.6 : 1.65;
   auto rounds = [](int64_t n, int64_t room) { return static_cast<double>((n + room - 1) / room); };
   int64_t best = 1;
-  double least = (wide ? 1.8 : 1.45) * static_cast<double>(chunks) + 4.0;
+  double least = (wide ? 2.3 : 1.6) * static_cast<double>(chunks) + 4.0;
   for (int64_t g = 2; g <= 64 && g <= chunks && columns * g <= 512; ++g) {
     const double each = static_cast<double>((chunks + g - 1) / g);
     const int64_t n = pairs * (g - 1);
     const double first = n <= 256 ? a * each + 4.0 : (1.55 * a * each + 4.0) * rounds(n, 512);
-    const double us = first + (a * each + 4.0) * rounds(columns * g, 256) + 4.0 + (wide ? 1.2 : 0.4) * static_cast<double>(g);
+    const double us = first + (a * each + 4.0) * rounds(columns * g, 256) + 4.0 + (wide ? 1.65 : 0.55) * static_cast<double>(g);
     if (us < least) {
       least = us;
       best = g;

@@ -12,8 +12,8 @@
 // of a chunk have the tokens as rows.
 //
 // A float32 factor enters a product as two bfloat16 parts that hold it to
-// 2^-18 of its size; products of two such factors leave out the smallest term.
-// q, k, v and dy are bfloat16 already and enter as they are.
+// 2^-18 of its size, or three (2^-26); products of two such factors leave out
+// the smallest term.  q, k, v and dy are bfloat16 already and enter as they are.
 #pragma once
 
 #include <type_traits>

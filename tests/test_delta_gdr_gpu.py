@@ -115,6 +115,17 @@ def test_forward(B, L, nqk, H, K, V, gates, with_h0, lengths):
         assert torch.equal(ch, hl) and torch.equal(y, again[0])
 
 
+@pytest.mark.parametrize("L,H,K,V", [(700, 2, 128, 128), (640, 1, 64, 64), (2500, 1, 64, 128), (2000, 1, 128, 64)])
+def test_the_last_state_is_held_to_float32(L, H, K, V):
+    """By norms, in one chain and over segments.  What is left of the roundings to bfloat16 is that of T - I's entries in
+    two parts, 2^-18 of each at most and 1 / sqrt(3) of that over many, on the half or less of U that they make (keys of
+    unit length, random: entries of K K^T of K^-1/2): 2^-19.8.  Sums of 64 to 128 float32 terms: 2^-22."""
+    q, k, v, g, beta, h0, _ = make(1, L, 1, H, K, V, L + K, rate=(0.001, 0.02))
+    want = ref.gdr(*(ref.f64(t) for t in (q, k, v, g, beta, h0)))[1]
+    got = ref.f64(ssm.gdr_fwd(*cuda(q, k, v, g, beta), h0=h0.cuda())[1])
+    assert float((got - want).norm()) <= 2.0 ** -19 * float(want.norm())
+
+
 def by_norm(t):
     """How far an output may be off by norms: 2^-12 and its own rounding.  A rounding is off by at most half a step, U of
     the value, so a few values by that together; over many the errors spread over the half step, and the root of
