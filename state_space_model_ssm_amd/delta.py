@@ -203,7 +203,8 @@ def gdr_fwd(q, k, v, g, beta, *, h0=None, lengths=None, scale=None, return_h_las
     ``return_states`` also what ``gdr_bwd`` starts from, a uint8 tensor of
     ``gdr_states_size`` bytes (per value head and 64 tokens 4 vdim (kdim + 64)
     + 26624: the state before them and what is needed of v, g and beta).  h_last
-    (float32, after each row's last token) may be h0 itself.
+    (float32, after each row's last token) may be h0 itself; without it
+    (return_h_last False) the call takes less time, and y's last bits may differ.
     """
     _one_device(stream, q, k, v, g, beta, h0, lengths, workspace)
     dims = _gdr_dims(q, k, v, g, beta, scale, 2)
