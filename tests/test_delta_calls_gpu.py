@@ -34,8 +34,8 @@ def qk_inputs(B, L, H, KV, d, seed=0):
                                r(B, L, H, d).to(BF16), r(B, L, KV, d).to(BF16))]
 
 
-def gdr_train(seed):
-    q, k, v, g, beta, h0, dy = gdr_inputs(2, 150, 2, 4, 128, 64, seed, BF16)
+def gdr_train(seed, *sizes):
+    q, k, v, g, beta, h0, dy = gdr_inputs(*(sizes or (2, 150, 2, 4, 128, 64)), seed, BF16)
 
     def run():
         y, last, states = ssm.gdr_fwd(q, k, v, g, beta, h0=h0, return_states=True)
@@ -47,6 +47,10 @@ def gdr_long(seed):
     """Of few heads: cut into segments."""
     args = gdr_inputs(1, 5000, 1, 2, 64, 128, seed)[:6]
     return args, lambda: ssm.gdr_fwd(*args[:5], h0=args[5])
+
+
+def gdr_train_long(seed):
+    return gdr_train(seed, 1, 1500, 1, 2, 128, 64)
 
 
 def gdr_step(seed):
@@ -96,7 +100,7 @@ def same(a, b):
         assert torch.equal(x, y), n
 
 
-OPS = [gdr_train, gdr_long, gdr_step, qk_train, swa_step, swa_fill]
+OPS = [gdr_train, gdr_train_long, gdr_long, gdr_step, qk_train, swa_step, swa_fill]
 
 
 @pytest.mark.parametrize("make", OPS)
