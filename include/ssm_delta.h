@@ -84,8 +84,9 @@ enum { SSM_GDR_STATE_STEP = 64 };
  *            taken as the nearer end.  Rows at or past the length are not used.
  *   h_last : as h0, nullable: the state after the row's last token (h0 where
  *            there is none); may be exactly h0.  Where it is asked for, the
- *            state is held to float32 on its way, else to 2^-18: y's last bits
- *            may differ with and without it
+ *            state is held to float32 on its way (it ends less than 1e-6 of its
+ *            norm off, as float32 token by token would), else to 2^-18: y's last
+ *            bits may differ with and without it
  *   states : ssm_gdr_states_size() bytes, 16-byte aligned, nullable: what
  *            ssm_gdr_bwd starts from (the state before every 64th token, the
  *            u_t, and what of v, g and beta it needs), in an order of its own;

@@ -89,7 +89,7 @@ int ssm_gdr_workspace_size(const ssm_gdr_dims_t *dims, size_t *bytes) {
   const int rc = check_gdr(dims, false);
   if (rc != SSM_OK) return rc;
   const GdrSizes n = gdr_sizes(params(*dims));
-  *bytes = n.chunks + n.state + n.carry;
+  *bytes = n.all();
   return ok();
 }
 
@@ -124,7 +124,7 @@ int ssm_gdr_fwd(const void *q, const void *k, const void *v, const void *g, cons
   const void *const same[3][2] = {{nullptr, nullptr}, {h0, nullptr}, {nullptr, nullptr}};
   rc = check_args(ins, outs, same);
   const GdrSizes n = gdr_sizes(p);
-  if (rc == SSM_OK) rc = check_workspace(ins, n.chunks + n.state + n.carry);
+  if (rc == SSM_OK) rc = check_workspace(ins, n.all());
   if (rc != SSM_OK) return rc;
   if (d.batch == 0 || (d.seqlen == 0 && h_last == nullptr)) return ok();
   p.q = static_cast<const uint16_t *>(q);
@@ -139,8 +139,9 @@ int ssm_gdr_fwd(const void *q, const void *k, const void *v, const void *g, cons
   p.saved = static_cast<char *>(states);
   p.ops = states ? p.saved + gdr_both_bytes(d.kdim, d.vdim) : p.ws;
   p.ops_step = static_cast<int64_t>(states ? gdr_saved_bytes(d.kdim, d.vdim) : kGdrChunkBytes);
-  p.ws_state = reinterpret_cast<float *>(p.ws + n.chunks);
-  p.ws_carry = reinterpret_cast<uint16_t *>(p.ws + n.chunks + n.state);
+  p.rest = h_last != nullptr || p.seg.count > 1 ? p.ws + n.chunks : nullptr;
+  p.ws_state = reinterpret_cast<float *>(p.ws + n.chunks + n.rest);
+  p.ws_carry = reinterpret_cast<uint16_t *>(p.ws + n.chunks + n.rest + n.state);
   return launched(launch_gdr_fwd(p, static_cast<hipStream_t>(stream)), "gdr_fwd");
 }
 
@@ -149,7 +150,7 @@ int ssm_gdr_bwd_workspace_size(const ssm_gdr_dims_t *dims, size_t *bytes) {
   const int rc = check_gdr(dims, false);
   if (rc != SSM_OK) return rc;
   const GdrSizes n = gdr_bwd_sizes(params(*dims, true));
-  *bytes = n.chunks + n.state + n.carry;
+  *bytes = n.all();
   return ok();
 }
 
@@ -175,7 +176,7 @@ int ssm_gdr_bwd(const void *q, const void *k, const int32_t *lengths, const void
   const void *const same[6][2] = {};
   rc = check_args(ins, outs, same);
   const GdrSizes n = gdr_bwd_sizes(p);
-  if (rc == SSM_OK) rc = check_workspace(ins, n.chunks + n.state + n.carry);
+  if (rc == SSM_OK) rc = check_workspace(ins, n.all());
   if (rc != SSM_OK) return rc;
   if (d.batch == 0 || (d.seqlen == 0 && dh0 == nullptr)) return ok();
   p.q = static_cast<const uint16_t *>(q);
@@ -193,8 +194,8 @@ int ssm_gdr_bwd(const void *q, const void *k, const int32_t *lengths, const void
   p.ws_both = p.ws;
   p.ops = p.saved + gdr_both_bytes(d.kdim, d.vdim);
   p.ops_step = static_cast<int64_t>(gdr_saved_bytes(d.kdim, d.vdim));
-  p.ws_state = reinterpret_cast<float *>(p.ws + n.chunks);
-  p.ws_carry = reinterpret_cast<uint16_t *>(p.ws + n.chunks + n.state);
+  p.ws_state = reinterpret_cast<float *>(p.ws + n.chunks + n.rest);
+  p.ws_carry = reinterpret_cast<uint16_t *>(p.ws + n.chunks + n.rest + n.state);
   return launched(launch_gdr_bwd(p, static_cast<hipStream_t>(stream)), "gdr_bwd");
 }
 

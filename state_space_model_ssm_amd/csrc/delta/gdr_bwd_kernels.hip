@@ -605,7 +605,7 @@ GdrSegments gdr_bwd_segments(int64_t heads, int64_t kdim, int64_t vdim, int64_t 
 
 GdrSizes gdr_bwd_sizes(const GdrParams &p) {
   const size_t heads = static_cast<size_t>(p.batch) * p.nheads, n = p.seg.count > 1 ? heads * p.seg.count : 0;
-  return {heads * p.chunks * gdr_both_bytes(p.kdim, p.vdim), n * p.vdim * p.kdim * 4, n * 2 * p.kdim * p.kdim * 2};
+  return {heads * p.chunks * gdr_both_bytes(p.kdim, p.vdim), 0, n * p.vdim * p.kdim * 4, n * 2 * p.kdim * p.kdim * 2};
 }
 
 hipError_t launch_gdr_bwd(const GdrParams &p, hipStream_t s) { return p.kdim == 64 ? bwd<64>(p, s) : bwd<128>(p, s); }

@@ -16,6 +16,7 @@ constexpr size_t kGdrTriBytes = size_t{2} * kGdrFrags * 1024;  // both parts
 // Factors, 64 of each: scale e^G, e^G, e^(GC - G), beta (float32), and G log2(e) (float64).
 constexpr size_t kGdrGateBytes = 2048;
 constexpr size_t kGdrChunkBytes = 2 * kGdrTriBytes + kGdrGateBytes;
+constexpr size_t kGdrRestBytes = kGdrTriBytes / 2;  // T's third part, where the state is held to float32
 // Of a chunk and value head, in two bfloat16 parts as operands over 32 values
 // (see gdr_tile.h): the state before it or dS behind it, [16 key elements][32
 // values][part], then U or D = beta E, [32 values][16 tokens][part], 1 KiB each.
@@ -45,6 +46,7 @@ struct GdrParams {
   char *ws;
   char *ops;                   // kGdrChunkBytes per (row, value head, chunk), ops_step bytes apart: in `saved` or the workspace
   int64_t ops_step;
+  char *rest;                  // kGdrRestBytes per (row, value head, chunk), in the workspace; null where T is taken in two parts
   const uint16_t *dy;          // backward
   const float *dh_last;        // nullable
   uint16_t *dq, *dk, *dv;
@@ -59,9 +61,10 @@ struct GdrParams {
   float scale;
   int32_t kdim, vdim, gates_bf16;
 };
-// Sizes of the forward's workspace: ws, ws_state and ws_carry in turn.
+// Sizes of the forward's workspace: ws, rest, ws_state and ws_carry in turn.
 struct GdrSizes {
-  size_t chunks, state, carry;
+  size_t chunks, rest, state, carry;
+  size_t all() const { return chunks + rest + state + carry; }
 };
 GdrSizes gdr_sizes(const GdrParams &p);
 GdrSegments gdr_bwd_segments(int64_t heads, int64_t kdim, int64_t vdim, int64_t chunks);

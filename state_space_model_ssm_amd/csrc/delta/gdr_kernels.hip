@@ -18,14 +18,15 @@
 // Rounding: keys, queries and values are exact; T - I, A and what of S and U
 // makes y and is saved enter products as two bfloat16 parts, to 2^-18 of their
 // size.  Two would leave the state itself 4e-6 off at the end, by norms, where
-// float32 token by token is 2e-7: where it is returned, S, U and what T takes
-// are in three parts as they make the next S (2^-26; below 1e-6 with the rest),
-// and so are a segment's E and P.  That costs a quarter of the chain's time (16
-// heads of 128, 8192 tokens: 151 us without).  T's ones are kept out of what is
-// rounded.  Sums are float32, sums of g float64.
+// float32 token by token is 2e-7 to 1e-6: where it is returned, S, U, T - I and
+// what T takes are in three parts as they make the next S (2^-26; 2.5e-7 to
+// 8e-7 off with the rest), and so are a segment's E and P.  (T - I in two: 7e-7
+// with random keys, 2e-6 to 6e-6 with keys that are alike.)  That costs a
+// quarter of the chain's time (16 heads of 128, 8192 tokens: 199 us, 151
+// without).  T's ones are kept out of what is rounded.  Sums are float32, sums of
+// g float64.
 //
-// Measured, 16 heads of 128: one prompt of 8192 tokens in 184 us a call (chunks
-// 29 us, segments 73, join 15, y 91); training's 4 x 2048, where the last state
+// Measured, 16 heads of 128: one prompt of 8192 tokens in 199 us a call; training's 4 x 2048, where the last state
 // is not asked for, in 29 and 105, of which saving for the backward, 200 MB, is
 // a third.
 #include "gdr_tile.h"
@@ -39,15 +40,22 @@ namespace {
 
 constexpr int kDiagPitch = 20;  // floats between rows in LDS
 
-// Store row block W of a lower triangle, transposed D results, as fragments in two parts.
+// Store row block W of a lower triangle, transposed D results, as fragments in
+// two parts, and the third where there is a place for it.
 template <int W>
-__device__ __forceinline__ void store_rows(const f4v (&t)[W + 1], u4 *to, int lane) {
+__device__ __forceinline__ void store_rows(const f4v (&t)[W + 1], u4 *to, u4 *rest, int lane) {
 #pragma unroll
   for (int s = 0; 2 * s <= W; ++s) {
-    const Parts x = parts(t[2 * s], 2 * s + 1 <= W ? t[2 * s + 1 <= W ? 2 * s + 1 : 0] : f4v{});
+    const Parts3 x = parts3(t[2 * s], 2 * s + 1 <= W ? t[2 * s + 1 <= W ? 2 * s + 1 : 0] : f4v{});
     to[tri(W, s) * 64 + lane] = __builtin_bit_cast(u4, x.hi);
     to[(kGdrFrags + tri(W, s)) * 64 + lane] = __builtin_bit_cast(u4, x.lo);
+    if (rest != nullptr) rest[tri(W, s) * 64 + lane] = __builtin_bit_cast(u4, x.rest);
   }
+}
+// The third parts, from memory: in the order of fragments.
+__device__ __forceinline__ void load_rest(bf8 (&t)[kGdrFrags], const char *from, int lane) {
+#pragma unroll
+  for (int f = 0; f < kGdrFrags; ++f) t[f] = *reinterpret_cast<const bf8 *>(from + f * 1024 + lane * 16);
 }
 
 // One workgroup per chunk and value head, one wavefront per 16 of its tokens.
@@ -140,7 +148,7 @@ __global__ void __launch_bounds__(256) gdr_chunk_kernel(const GdrParams p) {
         att[jb][r] = j <= i && i < len ? att[jb][r] * decay * p.scale : 0.0f;
         low[j * kPitch + i] = j < i ? kk[jb][r] * decay * bi : 0.0f;
       }
-    store_rows<W>(att, out + kGdrTriBytes / 16, lane);
+    store_rows<W>(att, out + kGdrTriBytes / 16, nullptr, lane);
   });
   __syncthreads();
   // Blocks on the diagonal, all in one wavefront: lane (block g, column m) by substitution.
@@ -186,7 +194,7 @@ __global__ void __launch_bounds__(256) gdr_chunk_kernel(const GdrParams p) {
 #pragma unroll
     for (int r = 0; r < 4; ++r)
       if (4 * g + r == m) t[W][r] = 0.0f;  // the ones stay out of what is rounded
-    store_rows<W>(t, out, lane);
+    store_rows<W>(t, out, p.rest != nullptr ? reinterpret_cast<u4 *>(p.rest + id * kGdrRestBytes) : nullptr, lane);
   });
 }
 
@@ -236,6 +244,9 @@ __global__ void __launch_bounds__(256) gdr_fwd_kernel(const GdrParams p) {
     const bool begins = from != nullptr && (first < n || segment == 0);
 #pragma unroll
     for (int j = 0; j < NB; ++j) s[j] = begins ? *reinterpret_cast<const f4v *>(from + 32 * (j / 2) + 4 * (j % 2)) : f4v{};
+    // T's third part comes from memory to registers, a chunk ahead: there is no room for it in LDS.
+    bf8 t3[kGdrFrags];
+    if (LAST && first < n) load_rest(t3, p.rest + (bh * p.chunks + first) * kGdrRestBytes, lane);
     for (int c = first; c < n; ++c) {
       decltype(split<LAST>(s[0], s[0])) sp[NS];
 #pragma unroll
@@ -248,7 +259,7 @@ __global__ void __launch_bounds__(256) gdr_fwd_kernel(const GdrParams p) {
       const unsigned tile = base + (c & 1) * kBuffer, tri_t = tile + kAtW, gates = tri_t + 2 * kGdrTriBytes + 16 * g;
       // Operands are read ahead of their use, in its order.
       bf8 ka[NS][4], kt[2][NB];
-      Parts tf[kGdrFrags];
+      decltype(split<LAST>(s[0], s[0])) tf[kGdrFrags];
       sh4 vf[4];
       f4v into[4], beta[4];
 #pragma unroll
@@ -262,7 +273,12 @@ __global__ void __launch_bounds__(256) gdr_fwd_kernel(const GdrParams p) {
         beta[i] = lds_f4(gates + 768 + 64 * i);
       }
 #pragma unroll
-      for (int f = 0; f < kGdrFrags; ++f) tf[f] = {frag16(tri_t, f, lane), frag16(tri_t, kGdrFrags + f, lane)};
+      for (int f = 0; f < kGdrFrags; ++f) {
+        tf[f].hi = frag16(tri_t, f, lane);
+        tf[f].lo = frag16(tri_t, kGdrFrags + f, lane);
+        if constexpr (LAST) tf[f].rest = t3[f];
+      }
+      if (LAST && c + 1 < n) load_rest(t3, p.rest + (bh * p.chunks + c + 1) * kGdrRestBytes, lane);
       __builtin_amdgcn_sched_barrier(0);
       f4v x[4] = {};
 #pragma unroll
@@ -464,6 +480,8 @@ __global__ void __launch_bounds__(256, 2) gdr_segment_kernel(const GdrParams p) 
       copy_kib<1>(__builtin_amdgcn_readfirstlane(base + (c & 1) * kBuffer + kAtG + w * 1024), uniform(wc + 2 * kGdrTriBytes + w * 1024), lane * 16);
   };
   fetch(first);
+  bf8 t3[kGdrFrags], next[kGdrFrags];  // T's third part, a chunk ahead
+  if (!BWD) load_rest(next, p.rest + (bh * p.chunks + first) * kGdrRestBytes, lane);
   f4v s[NB];
 #pragma unroll
   for (int j = 0; j < NB; ++j)
@@ -472,6 +490,11 @@ __global__ void __launch_bounds__(256, 2) gdr_segment_kernel(const GdrParams p) 
   for (int c = first; c < n; ++c) {
     arrive();
     if (c + 1 < n) fetch(c + 1);
+    if (!BWD) {
+#pragma unroll
+      for (int f = 0; f < kGdrFrags; ++f) t3[f] = next[f];
+      if (c + 1 < n) load_rest(next, p.rest + (bh * p.chunks + c + 1) * kGdrRestBytes, lane);
+    }
     const unsigned buffer = base + (c & 1) * kBuffer, tri_t = buffer + kAtW, gates = buffer + kAtG + 16 * g;
     f4v x[4] = {};
 #pragma unroll
@@ -492,8 +515,13 @@ __global__ void __launch_bounds__(256, 2) gdr_segment_kernel(const GdrParams p) 
     for (int k = 0; k < 2; ++k) {
       const auto xp = split<!BWD>(x[2 * k], x[2 * k + 1]);
 #pragma unroll
-      for (int i = 2 * k; i < 4; ++i)
-        u[i] = mul_parts(Parts{frag16(tri_t, tri(i, k), lane), frag16(tri_t, kGdrFrags + tri(i, k), lane)}, xp, u[i]);
+      for (int i = 2 * k; i < 4; ++i) {
+        decltype(split<!BWD>(s[0], s[0])) tf;
+        tf.hi = frag16(tri_t, tri(i, k), lane);
+        tf.lo = frag16(tri_t, kGdrFrags + tri(i, k), lane);
+        if constexpr (!BWD) tf.rest = t3[tri(i, k)];
+        u[i] = mul_parts(tf, xp, u[i]);
+      }
     }
     const float whole = lds_f4(buffer + kAtG + 256 + 240)[3];
 #pragma unroll
@@ -763,7 +791,7 @@ void launch_gdr_bwd_join(const GdrParams &p, hipStream_t s) { p.kdim == 64 ? bwd
 
 GdrSizes gdr_sizes(const GdrParams &p) {
   const size_t heads = static_cast<size_t>(p.batch) * p.nheads, n = p.seg.count > 1 ? heads * p.seg.count : 0;
-  return {heads * p.chunks * kGdrChunkBytes, n * p.vdim * p.kdim * 4, n * 3 * p.kdim * p.kdim * 2};
+  return {heads * p.chunks * kGdrChunkBytes, heads * p.chunks * kGdrRestBytes, n * p.vdim * p.kdim * 4, n * 3 * p.kdim * p.kdim * 2};
 }
 
 hipError_t launch_gdr_fwd(const GdrParams &p, hipStream_t s) { return p.kdim == 64 ? fwd<64>(p, s) : fwd<128>(p, s); }
