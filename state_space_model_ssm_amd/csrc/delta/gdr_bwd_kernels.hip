@@ -8,10 +8,14 @@
 //   dQ = scale e^G dY S + P K
 //   dK = (H K - e^G D S) + (e^(G_64 - G) U dS + P^T Q + H^T K), as read and as written
 //   dbeta = E.(U / beta), whose sum is the diagonal of D U^T by beta^2
-// and of G_i the gradient is q_i.dq_i + k_i.(dk_i as read - dk_i as written),
-// with <S', dS> added at the last: every exponent of the chunk is a difference
-// of two G that stand beside a query, a key that reads or one that writes.  So
-// dg, their sum from t on, needs no products of its own.
+// and dg_t is the sum of the terms whose decay passes token t, those of
+//   W_ij = P_ij q_i.k_j + H_ij k_i.k_j   from j < t to i >= t
+//   q_i.(scale e^G dY S)_i - k_i.(e^G D S)_i   for i >= t, from the state before
+//   k_j.(e^(G_64 - G) U dS)_j   for j < t, to the state behind, and e^(G_64) <S, dS>
+// each of which has a_t as a factor, as dg_t itself does.  (The sum over i >= t
+// of what G_i's gradient is, q_i.dq_i + k_i.(dk_i as read - dk_i as written),
+// is the same without W; but all that lies behind t has to cancel in it then,
+// and where a_t is small only the roundings of that are left.)
 //
 // A first kernel goes from chunk to chunk backwards with dS (as the forward,
 // bound by its chain; 3.4 us a chunk with the 96 KiB of dS and D that it leaves
@@ -280,6 +284,18 @@ __device__ __forceinline__ float sum16(float v) {
   return v;
 }
 
+// The sum over the lanes before.
+__device__ __forceinline__ float sum_before(float v) {
+  v = __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x138, 0xf, 0xf, false));   // from the lane before
+  v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x111, 0xf, 0xf, false));  // 1, 2, 4, 8 before, of 16
+  v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x112, 0xf, 0xf, false));
+  v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x114, 0xf, 0xf, false));
+  v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x118, 0xf, 0xf, false));
+  v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x142, 0xa, 0xf, false));  // the last of the 16 before
+  v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x143, 0xc, 0xf, false));  // and of the 32
+  return v;
+}
+
 __device__ __forceinline__ void store_gate(void *p, int64_t i, float v, float) { st(static_cast<float *>(p), i, v); }
 __device__ __forceinline__ void store_gate(void *p, int64_t i, float v, uint16_t) { st(static_cast<uint16_t *>(p), i, v); }
 
@@ -315,7 +331,7 @@ __global__ void __launch_bounds__(256, 2) gdr_grad_kernel(const GdrParams p) {
   constexpr unsigned kTriangle = 2 * kGdrTriBytes, kValues = 64 * 64 * 2 + 2 * kParts, kAll = kTriangle + 64 * kPitch * 4;
   constexpr unsigned kArea = kValues > kAll ? kValues : kAll;
   __shared__ __align__(16) u4 lds[(kAtD + kArea) / 16];
-  __shared__ float red[NW][64], diag[64], whole[NW];
+  __shared__ float red[3][NW][64], diag[64], whole[NW];  // red: sums of W, and the tokens' terms with S and with dS
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const unsigned chunks = static_cast<unsigned>(p.chunks), nqk = static_cast<unsigned>(p.nqk);
   const int64_t c = blockIdx.x % chunks, bk = blockIdx.x / chunks, b = static_cast<unsigned>(bk) / nqk, hk = static_cast<unsigned>(bk) % nqk;
@@ -397,11 +413,22 @@ __global__ void __launch_bounds__(256, 2) gdr_grad_kernel(const GdrParams p) {
           if (s == 0) load(1);
         }
       }
+      meet();  // what was in LDS has been read
       // P = scale (dY U^T) M and H = -(D U^T) M, and the diagonal of D U^T = beta E (beta Z).
       const int own = 16 * w + m;
       const double so = sums[own];
+      const Lanes16 at = lanes16_of<KD>(lane);
+      float *full = reinterpret_cast<float *>(lds + kAtD / 16 + kTriangle / 16);
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
+      for (int j = 0; j < 4; ++j) {
+        f4v qk = {}, kk = {};  // q_i.k_j and k_i.k_j, laid out as P and H
+#pragma unroll
+        for (int a = 0; a < KD / 32; ++a) {
+          const bf8 kj = row16<KD>(base, j, a, at);
+          qk = mfma16(kj, row16<KD>(base + kAtQ, w, a, at), qk);
+          kk = mfma16(kj, row16<KD>(base, w, a, at), kk);
+        }
+        f4v sum;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const int other = 16 * j + 4 * g + r;
@@ -410,24 +437,45 @@ __global__ void __launch_bounds__(256, 2) gdr_grad_kernel(const GdrParams p) {
           const float decay = __builtin_amdgcn_exp2f(gap);
           py[j][r] = other <= own && own < len ? py[j][r] * p.scale * decay : 0.0f;
           pd[j][r] = other < own ? -pd[j][r] * decay : 0.0f;
+          sum[r] = other < own ? fmaf(py[j][r], qk[r], pd[j][r] * kk[r]) : 0.0f;
         }
-      sh4 kc[NE][4], qc[NE][4];
+        *reinterpret_cast<f4v *>(full + own * kPitch + 16 * j + 4 * g) = sum;
+      }
+      wait_reads();
+      {  // Lane t: W from j < t to this wavefront's i >= t.
+        float cut = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float before = sum_before(full[(16 * w + i) * kPitch + lane]);
+          cut += 16 * w + i >= lane ? before : 0.0f;
+        }
+        red[0][w][lane] = cut;
+      }
       both *= gates[64 + 63];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const f4v qs = *reinterpret_cast<const f4v *>(gates + 16 * i + 4 * g);
         const f4v into = *reinterpret_cast<const f4v *>(gates + 64 + 16 * i + 4 * g);
         const f4v out = *reinterpret_cast<const f4v *>(gates + 128 + 16 * i + 4 * g);
+        f4v before = {}, behind = {};
 #pragma unroll
         for (int x = 0; x < NE; ++x) {
-          kc[x][i] = rows4<KD>(base, i, NE * w + x, lane);
-          qc[x][i] = rows4<KD>(base + kAtQ, i, NE * w + x, lane);
+          const sh4 kc = rows4<KD>(base, i, NE * w + x, lane), qc = rows4<KD>(base + kAtQ, i, NE * w + x, lane);
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             aq[x][i][r] *= qs[r];
             ae[x][i][r] *= -into[r];
             aw[x][i][r] *= out[r];
-            both = fmaf(up(kc[x][i][r]), aw[x][i][r], both);  // <S_C, dS> with what the chunk adds to S_C
+            before[r] = fmaf(up(qc[r]), aq[x][i][r], fmaf(up(kc[r]), ae[x][i][r], before[r]));
+            behind[r] = fmaf(up(kc[r]), aw[x][i][r], behind[r]);
+          }
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const float b0 = sum16(before[r]), b1 = sum16(behind[r]);
+          if (m == 0) {
+            red[1][w][16 * i + 4 * g + r] = b0;
+            red[2][w][16 * i + 4 * g + r] = b1;
           }
         }
       }
@@ -438,7 +486,6 @@ __global__ void __launch_bounds__(256, 2) gdr_grad_kernel(const GdrParams p) {
         meet();
         const f4v (&lower)[4] = kind == 0 ? py : pd;
         u4 *to = lds + kAtD / 16;
-        float *full = reinterpret_cast<float *>(to + kTriangle / 16);
 #pragma unroll
         for (int j = 0; j < 4; ++j) *reinterpret_cast<f4v *>(full + own * kPitch + 16 * j + 4 * g) = lower[j];
 #pragma unroll
@@ -481,46 +528,35 @@ __global__ void __launch_bounds__(256, 2) gdr_grad_kernel(const GdrParams p) {
           }
         }
       }
-      // d / dG, a term per token from each of q, the key that reads and the key that writes.
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int x = 0; x < NE; ++x)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          float v = 0.0f;
-#pragma unroll
-          for (int x = 0; x < NE; ++x)
-            v = fmaf(up(qc[x][i][r]), aq[x][i][r], fmaf(up(kc[x][i][r]), ae[x][i][r] - aw[x][i][r], v));
-          v = sum16(v);
-          if (m == 0) red[w][16 * i + 4 * g + r] = v;
-        }
-#pragma unroll
-        for (int x = 0; x < NE; ++x) {
+        for (int i = 0; i < 4; ++i) {
           ak[x][i] = ae[x][i] + aw[x][i];
           if (SHARED) {
             aq[x][i] += tq[x][i];
             ak[x][i] += tk[x][i];
           }
         }
-      }
       both = sum16(both);
       both += __shfl_xor(both, 16);
       both += __shfl_xor(both, 32);
       if (lane == 0) whole[w] = both;
       meet();
-      if (w == 0) {  // dg_t is the sum of d / dG from t on; dbeta = E.Z
-        float dg = 0.0f, total = 0.0f;
+      if (w == 0) {  // dg; dbeta = E.Z
+        float dg = 0.0f, before = 0.0f, behind = 0.0f;
 #pragma unroll
         for (int k = 0; k < NW; ++k) {
-          dg += red[k][lane];
-          total += whole[k];
+          dg += red[0][k][lane] + whole[k];
+          before += red[1][k][lane];
+          behind += red[2][k][lane];
         }
-        if (lane >= len) dg = 0.0f;
-        if (lane == (len < 64 ? len - 1 : 63)) dg += total;
 #pragma unroll
         for (int d = 1; d < 64; d *= 2) {
-          const float next = __shfl_down(dg, d);
-          if (lane + d < 64) dg += next;
+          const float next = __shfl_down(before, d);
+          if (lane + d < 64) before += next;
         }
+        dg += before + sum_before(behind);
         const float beta = gates[192 + lane];
         if (lane < rows) {
           const int64_t to = (b * p.seqlen + t0 + lane) * p.nheads + h;

@@ -48,3 +48,31 @@ def test_the_last_state_is_held_to_float32_whatever_the_keys(L, H, K, V, cosine,
     # Asked for beside what the backward starts from, too.
     both = ssm.gdr_fwd(*cuda(q, k, v, g, beta), h0=h0.cuda(), return_states=True)[1]
     assert torch.equal(both.cpu().double(), got)
+
+
+@pytest.mark.parametrize("gates", [F32, BF16])
+@pytest.mark.parametrize("L,nqk,K,V", [(200, 4, 64, 64), (333, 2, 128, 128), (130, 1, 128, 64), (1100, 1, 64, 128)])
+def test_gradients_of_gates_head_by_head(L, nqk, K, V, gates):
+    """Decays of about 1, 3e-1, 7e-3 and 3e-7 a token beside each other: dg has its own decay as a factor, and is held
+    to that.  By norms of one head: at most five products in turn of factors in two parts, 3 * 2^-18 each, and its own
+    rounding: each value is off by U of itself at most, so their norm by U of theirs.  (1 / sqrt(3) of that holds for
+    many values of a size, not for these, a few of which make the norm.)  Where the gate is shut (below -200), dg is 0."""
+    q, k, v, g, beta, h0 = make(L, 4, K, V, L + V, 0.0, 0.0)
+    gen = torch.Generator().manual_seed(K)
+    q, k = (torch.nn.functional.normalize(torch.randn(1, L, nqk, K, generator=gen), dim=-1).to(BF16) for _ in range(2))
+    g = (-torch.tensor([0.01, 1.0, 5.0, 15.0]) * (0.8 + 0.4 * torch.rand(1, L, 4, generator=gen))).to(gates)
+    g[0, 37, 0], g[0, 70, 1], g[0, 127, 2], g[0, 64, 3] = -float("inf"), -1e30, -300.0, -1000.0
+    beta = beta.to(gates)
+    dy, dh = torch.randn(1, L, 4, V, generator=gen).to(BF16), torch.randn(1, 4, V, K, generator=gen)
+    want = ref.gdr_bwd(*(ref.f64(t) for t in (q, k, v, g.clamp(min=-1e4), beta, dy, h0)), dh_last=ref.f64(dh))[0]
+    cs = cuda(q, k, v, g, beta)
+    states = ssm.gdr_fwd(*cs, h0=h0.cuda(), return_states=True)[2]
+    got = ssm.gdr_bwd(*cs, states, dy.cuda(), dh_last=dh.cuda())
+    shut = g[0].float() <= -200
+    assert int(shut.sum()) == 4 and not got[3][0].cpu()[shut].any()
+    for name, t in (("dg", got[3]), ("dbeta", got[4])):
+        for h in range(4):
+            w = want[name][0, :, h]
+            far = float((ref.f64(t[0, :, h]) - w).norm() / w.norm())
+            print(name, h, f"{far:.1e}")
+            assert far <= 2.0 ** -14 + (U if gates == BF16 else 0.0), (name, h, far)
