@@ -89,11 +89,9 @@ enum { SSM_GDR_STATE_STEP = 64 };
  *            bits may differ with and without it
  *   states : ssm_gdr_states_size() bytes, 16-byte aligned, nullable: what
  *            ssm_gdr_bwd starts from (the state before every 64th token, the
- *            u_t, and what of v, g and beta it needs), in an order of its own;
+ *            u_t / beta_t, and what of v, g and beta it needs), in an order of its own;
  *            what is of tokens past a row's last block of 64 is not written
  * The rule is stable for beta |k|^2 below 2: keys are meant to have unit length.
- * A beta of less than 2^-30 in size counts as that (below the last bit of what
- * the token adds to a state with its value's size).
  * Tokens are taken 64 at a time: a value that is not finite reaches y from the
  * start of its block of 64 tokens (of its channel, if it is one of v; of the
  * value heads that share it, if it is one of q or k) and what comes after.

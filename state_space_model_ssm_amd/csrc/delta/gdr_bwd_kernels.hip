@@ -1,17 +1,19 @@
 // Gated delta rule, backward, for gfx950.
 //
-// With the forward's T, A, U and states, dS the gradient of the state behind a
+// With the forward's T, A, Z and states, dS the gradient of the state behind a
 // chunk, and M_ij = e^(G_i - G_j):
-//   dU = A^T dY + e^(G_64 - G) K dS^T,  E = T^T dU,  D = beta E = dV
+//   D = T^T (A^T dY + beta e^(G_64 - G) K dS^T) = dV
 //   dS' = e^(G_64) dS + (scale e^G dY)^T Q - (e^G D)^T K
-//   P = scale (dY U^T) M (j <= i),  H = -(D U^T) M (j < i)
-//   dQ = scale e^G dY S + P K
-//   dK = (H K - e^G D S) + (e^(G_64 - G) U dS + P^T Q + H^T K), as read and as written
-//   dbeta = E.(U / beta), whose sum is the diagonal of D U^T by beta^2
+//   P = scale (dY Z^T) M (j <= i),  H = -(D Z^T) M (j < i)
+//   dQ = scale e^G dY S + (P beta) K
+//   dK = (H beta) K - e^G D S + beta (e^(G_64 - G) Z dS + P^T Q + H^T K), as read and as written
+// (beta by rows of the last sum and by columns of P and H in the others).  With
+//   W_ij = P_ij q_i.k_j + H_ij k_i.k_j,  c_j = k_j.(e^(G_64 - G) Z dS)_j
+// dbeta_j is c_j and the sum of W over i >= j, without a quotient by beta,
 // and dg_t is the sum of the terms whose decay passes token t, those of
-//   W_ij = P_ij q_i.k_j + H_ij k_i.k_j   from j < t to i >= t
+//   W_ij beta_j   from j < t to i >= t
 //   q_i.(scale e^G dY S)_i - k_i.(e^G D S)_i   for i >= t, from the state before
-//   k_j.(e^(G_64 - G) U dS)_j   for j < t, to the state behind, and e^(G_64) <S, dS>
+//   c_j beta_j   for j < t, to the state behind, and e^(G_64) <S, dS>
 // each of which has a_t as a factor, as dg_t itself does.  (The sum over i >= t
 // of what G_i's gradient is, q_i.dq_i + k_i.(dk_i as read - dk_i as written),
 // is the same without W; but all that lies behind t has to cancel in it then,
@@ -32,7 +34,7 @@ namespace ssmb {
 namespace {
 
 // ---------------------------------------------------------------------------
-// From chunk to chunk, the last one first: dS, and E = T^T dU, dv = beta E
+// From chunk to chunk, the last one first: dS, and D = dv
 // ---------------------------------------------------------------------------
 
 // As in the forward two wavefronts carry dS, 16 columns each, and two others
@@ -91,7 +93,7 @@ __global__ void __launch_bounds__(256) gdr_bwd_kernel(const GdrParams p) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         out[i] = lds_f4(gates + 512 + 64 * i);
-        fac[i] = lds_f4(gates + 256 + 64 * i) * -lds_f4(gates + 768 + 64 * i);
+        fac[i] = -lds_f4(gates + 256 + 64 * i);
       }
 #pragma unroll
       for (int k = 0; k < 2; ++k)
@@ -99,7 +101,7 @@ __global__ void __launch_bounds__(256) gdr_bwd_kernel(const GdrParams p) {
         for (int j = 0; j <= 2 * k + 1; ++j) tf[tri_t(j, k)] = {tri_cols(at_t, j, k, 0, lane), tri_cols(at_t, j, k, 1, lane)};
       const float whole = lds_f4(at_t + kTri + 256 + 240)[3];
       __builtin_amdgcn_sched_barrier(0);
-      // K dS, and dU = e^(GC - G) of that + A^T dY
+      // K dS, and beta e^(GC - G) of that + A^T dY
       f4v x[4] = {};
 #pragma unroll
       for (int a = 0; a < NS; ++a)
@@ -112,7 +114,7 @@ __global__ void __launch_bounds__(256) gdr_bwd_kernel(const GdrParams p) {
       for (int k = 0; k < 2; ++k)
 #pragma unroll
         for (int j = 0; j < NB; ++j) kt[k][j] = col16<KD>(tile, j, k, at);
-      // E = T^T dU
+      // D = T^T of that
       f4v e[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
@@ -124,7 +126,7 @@ __global__ void __launch_bounds__(256) gdr_bwd_kernel(const GdrParams p) {
       for (int i = 0; i < 4; ++i) *(lds_f4v *)(four + i * 1024) = e[i];
       const Parts ep[2] = {parts(e[0] * fac[0], e[1] * fac[1]), parts(e[2] * fac[2], e[3] * fac[3])};
       meet();
-      // dS = e^GC dS + sum over tokens of q (scale e^G dy) - k (e^G beta E)
+      // dS = e^GC dS + sum over tokens of q (scale e^G dy) - k (e^G D)
 #pragma unroll
       for (int j = 0; j < NB; ++j) s[j] = s[j] * whole + *(const lds_f4v *)(grown + j * 1024);
 #pragma unroll
@@ -169,12 +171,11 @@ __global__ void __launch_bounds__(256) gdr_bwd_kernel(const GdrParams p) {
   auto both = [&](int c) {
     return p.ws_both + (bh * p.chunks + c) * static_cast<int64_t>(gdr_both_bytes(KD, p.vdim)) + lane * 16;
   };
-  // D = beta E: dv, and operands over the values, of which this column tile has halves.
+  // D: dv, and operands over the values, of which this column tile has halves.
   sh4 dt[4][2];
   auto turn = [&](int c) {
-    const unsigned beta = base + (c & 1) * kBuffer + kAtW + kTri + 768 + 16 * g;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) e[i] = *(const lds_f4v *)(four + i * 1024) * lds_f4(beta + 64 * i);
+    for (int i = 0; i < 4; ++i) e[i] = *(const lds_f4v *)(four + i * 1024);
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       const Parts d = parts(e[2 * k], e[2 * k + 1]);
@@ -327,11 +328,11 @@ template <int KD, int VD, bool SHARED, typename G>
 __global__ void __launch_bounds__(256, 2) gdr_grad_kernel(const GdrParams p) {
   constexpr int NT = 256, NW = 4, NE = KD / 64, NV = VD / 32;  // NE: blocks of 16 key elements of a wavefront
   constexpr unsigned kRows = 64 * KD * 2, kAtQ = kRows, kAtD = 2 * kRows, kAtU = kAtD + 64 * 64 * 2, kParts = 2 * 8 * 1024;
-  // dY, U and D of 64 values; then fragments of a triangle and its transpose, and the triangle in float32.
+  // dY, Z and D of 64 values; then fragments of a triangle and its transpose, and the triangle in float32.
   constexpr unsigned kTriangle = 2 * kGdrTriBytes, kValues = 64 * 64 * 2 + 2 * kParts, kAll = kTriangle + 64 * kPitch * 4;
   constexpr unsigned kArea = kValues > kAll ? kValues : kAll;
   __shared__ __align__(16) u4 lds[(kAtD + kArea) / 16];
-  __shared__ float red[3][NW][64], diag[64], whole[NW];  // red: sums of W, and the tokens' terms with S and with dS
+  __shared__ float red[4][NW][64], whole[NW];  // red: sums of W for dg and for dbeta, and the tokens' terms with S and with dS
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const unsigned chunks = static_cast<unsigned>(p.chunks), nqk = static_cast<unsigned>(p.nqk);
   const int64_t c = blockIdx.x % chunks, bk = blockIdx.x / chunks, b = static_cast<unsigned>(bk) / nqk, hk = static_cast<unsigned>(bk) % nqk;
@@ -368,7 +369,7 @@ __global__ void __launch_bounds__(256, 2) gdr_grad_kernel(const GdrParams p) {
             aq[x][i] = f4v{};
           }
       f4v ae[NE][4] = {}, aw[NE][4] = {};  // what keys get as they read, and as they write
-      f4v py[4] = {}, pd[4] = {};          // dY U^T and D U^T: rows j, columns i = 16 w + m
+      f4v py[4] = {}, pd[4] = {};          // dY Z^T and D Z^T: rows j, columns i = 16 w + m
       float both = 0.0f;
 #pragma unroll 1
       for (int hv = 0; hv < VD / 64; ++hv) {
@@ -388,7 +389,7 @@ __global__ void __launch_bounds__(256, 2) gdr_grad_kernel(const GdrParams p) {
         load(0);
         arrive();
         const unsigned dy = base + kAtD, u = base + kAtU, d = u + kParts;
-        auto part = [&](unsigned from, int i, int s) {  // U or D, token block i
+        auto part = [&](unsigned from, int i, int s) {  // Z or D, token block i
           return Parts{frag16(from, (4 * s + i) * 2, lane), frag16(from, (4 * s + i) * 2 + 1, lane)};
         };
 #pragma unroll 1
@@ -414,7 +415,7 @@ __global__ void __launch_bounds__(256, 2) gdr_grad_kernel(const GdrParams p) {
         }
       }
       meet();  // what was in LDS has been read
-      // P = scale (dY U^T) M and H = -(D U^T) M, and the diagonal of D U^T = beta E (beta Z).
+      // P = scale (dY Z^T) M, H = -(D Z^T) M and W.
       const int own = 16 * w + m;
       const double so = sums[own];
       const Lanes16 at = lanes16_of<KD>(lane);
@@ -433,30 +434,32 @@ __global__ void __launch_bounds__(256, 2) gdr_grad_kernel(const GdrParams p) {
         for (int r = 0; r < 4; ++r) {
           const int other = 16 * j + 4 * g + r;
           const float gap = static_cast<float>(so - sums[other]);
-          if (other == own) diag[own] = pd[j][r];
           const float decay = __builtin_amdgcn_exp2f(gap);
           py[j][r] = other <= own && own < len ? py[j][r] * p.scale * decay : 0.0f;
           pd[j][r] = other < own ? -pd[j][r] * decay : 0.0f;
-          sum[r] = other < own ? fmaf(py[j][r], qk[r], pd[j][r] * kk[r]) : 0.0f;
+          sum[r] = fmaf(py[j][r], qk[r], pd[j][r] * kk[r]);
         }
         *reinterpret_cast<f4v *>(full + own * kPitch + 16 * j + 4 * g) = sum;
       }
       wait_reads();
-      {  // Lane t: W from j < t to this wavefront's i >= t.
-        float cut = 0.0f;
+      {  // Lane t: W beta from j < t to this wavefront's i >= t, and W from j = t.
+        const float beta = gates[192 + lane];
+        float cut = 0.0f, column = 0.0f;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          const float before = sum_before(full[(16 * w + i) * kPitch + lane]);
+          const float here = full[(16 * w + i) * kPitch + lane], before = sum_before(here * beta);
           cut += 16 * w + i >= lane ? before : 0.0f;
+          column += here;
         }
         red[0][w][lane] = cut;
+        red[3][w][lane] = column;
       }
       both *= gates[64 + 63];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const f4v qs = *reinterpret_cast<const f4v *>(gates + 16 * i + 4 * g);
         const f4v into = *reinterpret_cast<const f4v *>(gates + 64 + 16 * i + 4 * g);
-        const f4v out = *reinterpret_cast<const f4v *>(gates + 128 + 16 * i + 4 * g);
+        const f4v out = *reinterpret_cast<const f4v *>(gates + 384 + 16 * i + 4 * g);
         f4v before = {}, behind = {};
 #pragma unroll
         for (int x = 0; x < NE; ++x) {
@@ -490,7 +493,8 @@ __global__ void __launch_bounds__(256, 2) gdr_grad_kernel(const GdrParams p) {
         for (int j = 0; j < 4; ++j) *reinterpret_cast<f4v *>(full + own * kPitch + 16 * j + 4 * g) = lower[j];
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-          const Parts x = parts(lower[2 * s], lower[2 * s + 1]);
+          const f4v *beta = reinterpret_cast<const f4v *>(gates + 192 + 32 * s + 4 * g);
+          const Parts x = parts(lower[2 * s] * beta[0], lower[2 * s + 1] * beta[4]);
           if (2 * s <= w) {
             const int f = w < 2 ? w : 2 * (w - 1) + s;
             to[f * 64 + lane] = __builtin_bit_cast(u4, x.hi);
@@ -529,39 +533,42 @@ __global__ void __launch_bounds__(256, 2) gdr_grad_kernel(const GdrParams p) {
         }
       }
 #pragma unroll
-      for (int x = 0; x < NE; ++x)
+      for (int i = 0; i < 4; ++i) {
+        const f4v beta = *reinterpret_cast<const f4v *>(gates + 192 + 16 * i + 4 * g);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          ak[x][i] = ae[x][i] + aw[x][i];
+        for (int x = 0; x < NE; ++x) {
+          ak[x][i] = ae[x][i] + beta * aw[x][i];
           if (SHARED) {
             aq[x][i] += tq[x][i];
             ak[x][i] += tk[x][i];
           }
         }
+      }
       both = sum16(both);
       both += __shfl_xor(both, 16);
       both += __shfl_xor(both, 32);
       if (lane == 0) whole[w] = both;
       meet();
-      if (w == 0) {  // dg; dbeta = E.Z
-        float dg = 0.0f, before = 0.0f, behind = 0.0f;
+      if (w == 0) {
+        float dg = 0.0f, before = 0.0f, behind = 0.0f, dbeta = 0.0f;
 #pragma unroll
         for (int k = 0; k < NW; ++k) {
           dg += red[0][k][lane] + whole[k];
           before += red[1][k][lane];
           behind += red[2][k][lane];
+          dbeta += red[3][k][lane];
         }
 #pragma unroll
         for (int d = 1; d < 64; d *= 2) {
           const float next = __shfl_down(before, d);
           if (lane + d < 64) before += next;
         }
-        dg += before + sum_before(behind);
-        const float beta = gates[192 + lane];
+        dg += before + sum_before(gates[192 + lane] * behind);
+        dbeta += behind;
         if (lane < rows) {
           const int64_t to = (b * p.seqlen + t0 + lane) * p.nheads + h;
           store_gate(p.dg, to, lane < len ? dg : 0.0f, G{});
-          store_gate(p.dbeta, to, lane < len ? diag[lane] / beta / beta : 0.0f, G{});
+          store_gate(p.dbeta, to, lane < len ? dbeta : 0.0f, G{});
         }
       }
     }

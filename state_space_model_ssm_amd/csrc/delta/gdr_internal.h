@@ -13,13 +13,13 @@ constexpr int kGdrChunk = 64;
 // bfloat16 parts (see gdr_tile.h), then the gates' factors.
 constexpr int kGdrFrags = 6;                                   // operands of a triangle: 16 rows x 32 columns each
 constexpr size_t kGdrTriBytes = size_t{2} * kGdrFrags * 1024;  // both parts
-// Factors, 64 of each: scale e^G, e^G, e^(GC - G), beta (float32), and G log2(e) (float64).
+// Factors, 64 of each: scale e^G, e^G, beta e^(GC - G), beta (float32), G log2(e) (float64), e^(GC - G).
 constexpr size_t kGdrGateBytes = 2048;
 constexpr size_t kGdrChunkBytes = 2 * kGdrTriBytes + kGdrGateBytes;
 constexpr size_t kGdrRestBytes = kGdrTriBytes / 2;  // T's third part, where the state is held to float32
 // Of a chunk and value head, in two bfloat16 parts as operands over 32 values
 // (see gdr_tile.h): the state before it or dS behind it, [16 key elements][32
-// values][part], then U or D = beta E, [32 values][16 tokens][part], 1 KiB each.
+// values][part], then Z or D, [32 values][16 tokens][part], 1 KiB each.
 constexpr size_t gdr_state_bytes(int64_t kdim, int64_t vdim) { return static_cast<size_t>(kdim * vdim) * 4; }
 constexpr size_t gdr_both_bytes(int64_t kdim, int64_t vdim) { return gdr_state_bytes(kdim, vdim) + static_cast<size_t>(64 * vdim) * 4; }
 // What the forward saves: those, and what is known of the chunk.

@@ -2,11 +2,13 @@
 //
 // 64 tokens at a time.  With G_t the sum of g from the chunk's start to t, K, Q,
 // V its tokens as rows and S the state before it (value elements x key
-// elements), the u_t that the tokens add solve a triangular system:
-//   L_ij = beta_i e^(G_i - G_j) k_i.k_j (j < i),  T = (I + L)^-1
-//   U = T beta (V - e^G K S^T)
-//   A_ij = scale e^(G_i - G_j) q_i.k_j (j <= i),  Y = scale e^G Q S^T + A U
-//   S' = e^(G_64) S + U^T e^(G_64 - G) K
+// elements), the z_t = u_t / beta_t of the tokens solve a triangular system:
+//   L_ij = e^(G_i - G_j) k_i.k_j beta_j (j < i),  T = (I + L)^-1
+//   Z = T (V - e^G K S^T)
+//   A_ij = scale e^(G_i - G_j) q_i.k_j beta_j (j <= i),  Y = scale e^G Q S^T + A Z
+//   S' = e^(G_64) S + (beta e^(G_64 - G) Z)^T K
+// beta stands with what a token writes, so that a token whose beta is 0 leaves
+// all others as they are, and its own z is there for beta's gradient.
 // Exponents are differences that are at most 0 where g is: nothing overflows,
 // and a strong decay is a 0.  T and A need no state: a first kernel makes them
 // for all chunks at once.  What is left is a chain from chunk to chunk of three
@@ -15,10 +17,10 @@
 // the columns are spread over all compute units, and where they do not fill
 // them, time is cut into segments (see gdr_segments()).
 //
-// Rounding: keys, queries and values are exact; T - I, A and what of S and U
+// Rounding: keys, queries and values are exact; T - I, A and what of S and Z
 // makes y and is saved enter products as two bfloat16 parts, to 2^-18 of their
 // size.  Two would leave the state itself 4e-6 off at the end, by norms, where
-// float32 token by token is 2e-7 to 1e-6: where it is returned, S, U, T - I and
+// float32 token by token is 2e-7 to 1e-6: where it is returned, S, Z, T - I and
 // what T takes are in three parts as they make the next S (2^-26; 2.5e-7 to
 // 8e-7 off with the rest), and so are a segment's E and P.  (T - I in two: 7e-7
 // with random keys, 2e-6 to 6e-6 with keys that are alike.)  That costs a
@@ -93,11 +95,7 @@ __global__ void __launch_bounds__(256) gdr_chunk_kernel(const GdrParams p) {
     const int64_t from = (b * p.seqlen + t0 + (lane < len ? lane : len - 1)) * p.nheads + h;
     float gt = gate<G>(p.g, from), bt = gate<G>(p.beta, from);
     gt = gt < -200.0f ? -200.0f : gt;  // exp(-200) is 0, and differences of the sums stay finite
-    // The gradient of beta is a quotient by it: a gate that is shut counts as
-    // 2^-30, which adds less than the last bit of what the token's value is to
-    // the state.  (Behind the length nothing is added.)
-    if (fabsf(bt) < 0x1p-30f) bt = copysignf(0x1p-30f, bt);
-    if (lane >= len) gt = bt = 0.0f;
+    if (lane >= len) gt = bt = 0.0f;  // nothing is added
     // In float64: after a strong decay the differences of later tokens' sums would lose what they have.
     double s = static_cast<double>(gt) * 1.4426950408889634;
 #pragma unroll
@@ -113,8 +111,10 @@ __global__ void __launch_bounds__(256) gdr_chunk_kernel(const GdrParams p) {
       float *gates = reinterpret_cast<float *>(ws + 2 * kGdrTriBytes);
       gates[lane] = lane < len ? p.scale * into : 0.0f;
       gates[64 + lane] = into;
-      gates[128 + lane] = __builtin_amdgcn_exp2f(static_cast<float>(last - s));
+      const float out = __builtin_amdgcn_exp2f(static_cast<float>(last - s));
+      gates[128 + lane] = bt * out;
       gates[192 + lane] = bt;
+      gates[384 + lane] = out;
       reinterpret_cast<double *>(gates + 256)[lane] = s;
     }
   }
@@ -138,15 +138,14 @@ __global__ void __launch_bounds__(256) gdr_chunk_kernel(const GdrParams p) {
     }
     meet();
     const double si = sums[i];
-    const float bi = betas[i];
 #pragma unroll
     for (int jb = 0; jb <= W; ++jb)
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const int j = 16 * jb + 4 * g + r;
-        const float decay = j <= i ? __builtin_amdgcn_exp2f(static_cast<float>(si - sums[j])) : 0.0f;
+        const float decay = (j <= i ? __builtin_amdgcn_exp2f(static_cast<float>(si - sums[j])) : 0.0f) * betas[j];
         att[jb][r] = j <= i && i < len ? att[jb][r] * decay * p.scale : 0.0f;
-        low[j * kPitch + i] = j < i ? kk[jb][r] * decay * bi : 0.0f;
+        low[j * kPitch + i] = j < i ? kk[jb][r] * decay : 0.0f;
       }
     store_rows<W>(att, out + kGdrTriBytes / 16, nullptr, lane);
   });
@@ -216,7 +215,7 @@ __global__ void __launch_bounds__(256) gdr_fwd_kernel(const GdrParams p) {
   constexpr int NT = 64 * kPairs, NC = 16 * kPairs, NS = KD / 32, NB = KD / 16;
   constexpr unsigned kRows = 64 * KD * 2, kValues = 64 * NC * 2;
   constexpr unsigned kAtQ = kRows, kAtV = 2 * kRows, kAtW = kAtV + kValues, kBuffer = kAtW + kGdrChunkBytes;
-  constexpr unsigned kState = NS * 2 * 1024, kUpdate = 2 * 2 * 1024;  // operands of the state and of u, of a wavefront
+  constexpr unsigned kState = NS * 2 * 1024, kUpdate = 2 * 2 * 1024;  // operands of the state and of z, of a wavefront
   __shared__ __align__(16) u4 lds[(2 * kBuffer + kPairs * (kState + kUpdate)) / 16];
   const int tid = threadIdx.x, lane = tid & 63, m = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), w = wave % kPairs;
@@ -229,7 +228,7 @@ __global__ void __launch_bounds__(256) gdr_fwd_kernel(const GdrParams p) {
   const int n = all < first + p.seg.chunks ? all : first + static_cast<int>(p.seg.chunks);
   const int col0 = static_cast<int>(vt) * NC + 16 * w;
   const unsigned base = lds_at(lds), parts_s = base + 2 * kBuffer + w * kState + lane * 16;
-  const unsigned parts_u = base + 2 * kBuffer + kPairs * kState + w * kUpdate + lane * 16;
+  const unsigned parts_z = base + 2 * kBuffer + kPairs * kState + w * kUpdate + lane * 16;
   const Lanes16 at = lanes16_of<KD>(lane);
   typedef __attribute__((address_space(3))) u4 lds16;
 
@@ -261,7 +260,7 @@ __global__ void __launch_bounds__(256) gdr_fwd_kernel(const GdrParams p) {
       bf8 ka[NS][4], kt[2][NB];
       decltype(split<LAST>(s[0], s[0])) tf[kGdrFrags];
       sh4 vf[4];
-      f4v into[4], beta[4];
+      f4v into[4];
 #pragma unroll
       for (int a = 0; a < NS; ++a)
 #pragma unroll
@@ -270,7 +269,6 @@ __global__ void __launch_bounds__(256) gdr_fwd_kernel(const GdrParams p) {
       for (int i = 0; i < 4; ++i) {
         vf[i] = rows4<NC>(tile + kAtV, i, w, lane);
         into[i] = lds_f4(gates + 256 + 64 * i);
-        beta[i] = lds_f4(gates + 768 + 64 * i);
       }
 #pragma unroll
       for (int f = 0; f < kGdrFrags; ++f) {
@@ -285,19 +283,19 @@ __global__ void __launch_bounds__(256) gdr_fwd_kernel(const GdrParams p) {
       for (int a = 0; a < NS; ++a)
 #pragma unroll
         for (int i = 0; i < 4; ++i) x[i] = mul_exact(ka[a][i], sp[a], x[i]);
-      // beta (v - e^G x), and u = T of that
-      f4v u[4];
+      // v - e^G x, and z = T of that
+      f4v z[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
 #pragma unroll
-        for (int r = 0; r < 4; ++r) x[i][r] = beta[i][r] * fmaf(-into[i][r], x[i][r], up(vf[i][r]));
-        u[i] = x[i];
+        for (int r = 0; r < 4; ++r) x[i][r] = fmaf(-into[i][r], x[i][r], up(vf[i][r]));
+        z[i] = x[i];
       }
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const auto xp = split<LAST>(x[2 * k], x[2 * k + 1]);
 #pragma unroll
-        for (int i = 2 * k; i < 4; ++i) u[i] = mul_parts(tf[tri(i, k)], xp, u[i]);
+        for (int i = 2 * k; i < 4; ++i) z[i] = mul_parts(tf[tri(i, k)], xp, z[i]);
       }
 #pragma unroll
       for (int k = 0; k < 2; ++k)
@@ -305,21 +303,21 @@ __global__ void __launch_bounds__(256) gdr_fwd_kernel(const GdrParams p) {
         for (int j = 0; j < NB; ++j) kt[k][j] = col16<KD>(tile, j, k, at);
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        const Parts up = parts(u[2 * k], u[2 * k + 1]);
-        *(lds16 *)(parts_u + k * 2048) = __builtin_bit_cast(u4, up.hi);
-        *(lds16 *)(parts_u + k * 2048 + 1024) = __builtin_bit_cast(u4, up.lo);
+        const Parts zp = parts(z[2 * k], z[2 * k + 1]);
+        *(lds16 *)(parts_z + k * 2048) = __builtin_bit_cast(u4, zp.hi);
+        *(lds16 *)(parts_z + k * 2048 + 1024) = __builtin_bit_cast(u4, zp.lo);
       }
       meet();
-      // s = e^GC s + sum over tokens of k (e^(GC - G) u)
+      // s = e^GC s + sum over tokens of k (beta e^(GC - G) z)
       const float whole = lds_f4(tri_t + 2 * kGdrTriBytes + 256 + 240)[3];
 #pragma unroll
       for (int j = 0; j < NB; ++j) s[j] *= whole;
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const f4v o0 = lds_f4(gates + 512 + 128 * k), o1 = lds_f4(gates + 512 + 128 * k + 64);
-        const auto up = split<LAST>(u[2 * k] * o0, u[2 * k + 1] * o1);
+        const auto zp = split<LAST>(z[2 * k] * o0, z[2 * k + 1] * o1);
 #pragma unroll
-        for (int j = 0; j < NB; ++j) s[j] = mul_exact(kt[k][j], up, s[j]);
+        for (int j = 0; j < NB; ++j) s[j] = mul_exact(kt[k][j], zp, s[j]);
       }
     }
     if (p.h_last != nullptr && ((n == all && first < n) || (all == 0 && segment == 0))) {
@@ -359,8 +357,8 @@ __global__ void __launch_bounds__(256) gdr_fwd_kernel(const GdrParams p) {
   f4v o[4];
   // What the backward starts from, whose operands have the values as k: each of
   // the two wavefronts turns half of both columns' tiles round.
-  bf8 ut[2][2];
-  const unsigned all_s = base + 2 * kBuffer, all_u = all_s + kPairs * kState;
+  bf8 zt[2][2];
+  const unsigned all_s = base + 2 * kBuffer, all_z = all_s + kPairs * kState;
   const int64_t nv = p.vdim / 32;
   auto saved = [&](int c) { return p.saved + (bh * p.chunks + c) * static_cast<int64_t>(gdr_saved_bytes(KD, p.vdim)) + lane * 16; };
   auto store = [&](int c) {
@@ -372,7 +370,7 @@ __global__ void __launch_bounds__(256) gdr_fwd_kernel(const GdrParams p) {
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int part = 0; part < 2; ++part) __builtin_nontemporal_store(ut[i][part], reinterpret_cast<bf8 *>(to + (2 * i + w) * 2048 + part * 1024));
+        for (int part = 0; part < 2; ++part) __builtin_nontemporal_store(zt[i][part], reinterpret_cast<bf8 *>(to + (2 * i + w) * 2048 + part * 1024));
     }
   };
   for (int c = first; c < n; ++c) {
@@ -419,17 +417,17 @@ __global__ void __launch_bounds__(256) gdr_fwd_kernel(const GdrParams p) {
     }
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      const Parts up = {__builtin_bit_cast(bf8, *(const lds16 *)(parts_u + k * 2048)),
-                        __builtin_bit_cast(bf8, *(const lds16 *)(parts_u + k * 2048 + 1024))};
+      const Parts zp = {__builtin_bit_cast(bf8, *(const lds16 *)(parts_z + k * 2048)),
+                        __builtin_bit_cast(bf8, *(const lds16 *)(parts_z + k * 2048 + 1024))};
 #pragma unroll
-      for (int i = 2 * k; i < 4; ++i) o[i] = mul_parts(af[tri(i, k)], up, o[i]);
+      for (int i = 2 * k; i < 4; ++i) o[i] = mul_parts(af[tri(i, k)], zp, o[i]);
     }
     if (c + 1 < n) fetch_ws(c + 1);
     if (p.saved != nullptr)
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int part = 0; part < 2; ++part) ut[i][part] = turned<false>(all_u, all_u + kUpdate, 2 * i + w, part, lane);
+        for (int part = 0; part < 2; ++part) zt[i][part] = turned<false>(all_z, all_z + kUpdate, 2 * i + w, part, lane);
     if (64 * c + 64 > len) {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
@@ -505,12 +503,12 @@ __global__ void __launch_bounds__(256, 2) gdr_segment_kernel(const GdrParams p) 
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const f4v into = lds_f4(gates + 256 + 64 * i), beta = lds_f4(gates + 768 + 64 * i);
+      const f4v into = lds_f4(gates + 256 + 64 * i);
       const sh4 v = rows4<NC>(buffer + kAtV, i, w, lane);
 #pragma unroll
-      for (int r = 0; r < 4; ++r) x[i][r] = beta[r] * fmaf(-into[r], x[i][r], values ? up(v[r]) : 0.0f);
+      for (int r = 0; r < 4; ++r) x[i][r] = fmaf(-into[r], x[i][r], values ? up(v[r]) : 0.0f);
     }
-    f4v u[4] = {x[0], x[1], x[2], x[3]};
+    f4v z[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       const auto xp = split<!BWD>(x[2 * k], x[2 * k + 1]);
@@ -520,7 +518,7 @@ __global__ void __launch_bounds__(256, 2) gdr_segment_kernel(const GdrParams p) 
         tf.hi = frag16(tri_t, tri(i, k), lane);
         tf.lo = frag16(tri_t, kGdrFrags + tri(i, k), lane);
         if constexpr (!BWD) tf.rest = t3[tri(i, k)];
-        u[i] = mul_parts(tf, xp, u[i]);
+        z[i] = mul_parts(tf, xp, z[i]);
       }
     }
     const float whole = lds_f4(buffer + kAtG + 256 + 240)[3];
@@ -528,9 +526,9 @@ __global__ void __launch_bounds__(256, 2) gdr_segment_kernel(const GdrParams p) 
     for (int j = 0; j < NB; ++j) s[j] *= whole;
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      const auto up = split<!BWD>(u[2 * k] * lds_f4(gates + 512 + 128 * k), u[2 * k + 1] * lds_f4(gates + 512 + 128 * k + 64));
+      const auto zp = split<!BWD>(z[2 * k] * lds_f4(gates + 512 + 128 * k), z[2 * k + 1] * lds_f4(gates + 512 + 128 * k + 64));
 #pragma unroll
-      for (int j = 0; j < NB; ++j) s[j] = mul_exact(col16<KD>(buffer, j, k, at), up, s[j]);
+      for (int j = 0; j < NB; ++j) s[j] = mul_exact(col16<KD>(buffer, j, k, at), zp, s[j]);
     }
   }
   const int64_t seg = bh * p.seg.count + segment;

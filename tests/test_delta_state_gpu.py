@@ -76,3 +76,40 @@ def test_gradients_of_gates_head_by_head(L, nqk, K, V, gates):
             far = float((ref.f64(t[0, :, h]) - w).norm() / w.norm())
             print(name, h, f"{far:.1e}")
             assert far <= 2.0 ** -14 + (U if gates == BF16 else 0.0), (name, h, far)
+
+
+@pytest.mark.parametrize("L,K,V", [(1, 64, 64), (150, 128, 128), (200, 64, 128), (3000, 128, 64)])
+def test_a_token_whose_beta_is_zero_writes_nothing(L, K, V):
+    """Whatever its key and value are: every output and gradient of the others has the same bits."""
+    q, k, v, g, beta, h0 = make(L, 2, K, V, L, 0.5, 1.0)
+    gen = torch.Generator().manual_seed(V)
+    shut = torch.rand(L, generator=gen) < 0.4
+    shut[-1] = True
+    beta[0, shut] = 0.0
+    dy, dh = torch.randn(1, L, 2, V, generator=gen).to(BF16), torch.randn(1, 2, V, K, generator=gen)
+    other = [q, k.clone(), v.clone(), g, beta]
+    other[1][0, shut] = torch.randn(int(shut.sum()), 1, K, generator=gen).to(BF16)
+    other[2][0, shut] = 1e3 * torch.randn(int(shut.sum()), 2, V, generator=gen).to(BF16)
+    outs = []
+    for args in ((q, k, v, g, beta), other):
+        cs = cuda(*args)
+        y, last, states = ssm.gdr_fwd(*cs, h0=h0.cuda(), return_states=True)
+        dq, dk, dv, dg, dbeta, dh0 = ssm.gdr_bwd(*cs, states, dy.cuda(), dh_last=dh.cuda())
+        assert not dv[0, shut.cuda()].any()
+        on = ~shut.cuda()
+        outs.append((y, last, dq, dk[0, on], dv, dg, dbeta[0, on], dh0))
+        if not shut[0] or L == 1:
+            want = ref.gdr_bwd(*(ref.f64(t) for t in (*args, dy, h0)), dh_last=ref.f64(dh))[0]["dbeta"]
+            # Products of factors in two parts, five in turn at most: 5 * 3 * 2^-18, by norms.
+            assert float((ref.f64(dbeta) - want).norm()) <= 2.0 ** -14 * float(want.norm())
+    for a, b in zip(*outs):
+        assert torch.equal(a, b)
+
+
+def test_shut_gates_keep_a_state():
+    """No beta and no decay: the state, bit for bit, over many tokens, and nothing from nothing."""
+    q, k, v, g, beta, h0 = make(2000, 40, 64, 64, 5, 0.0, 0.0)
+    g, beta = torch.zeros_like(g), torch.zeros_like(beta)
+    assert torch.equal(ssm.gdr_fwd(*cuda(q, k, v, g, beta), h0=h0.cuda())[1].cpu(), h0)
+    y, last = ssm.gdr_fwd(*cuda(q, k, v, g, beta))
+    assert not y.any() and not last.any()
