@@ -109,7 +109,9 @@ SSM_API int ssm_gdr_fwd(const void *q, const void *k, const void *v, const void 
  *   dq_t = scale S_t^T dy_t,  dk_t = dS_t^T u_t - a_t S_{t-1}^T dv_t
  *   dg_t = a_t (<dS_t, S_{t-1}> - dv_t.S_{t-1} k_t)
  * dq and dk are summed over the value heads that share a head.  Rows at or
- * past the length get zero gradients.
+ * past the length get zero gradients.  dg, dbeta and dh0 are right to 1e-5 of
+ * their norms, also where they are float32 (2^-15 at most with keys of unit
+ * length), the others to their own rounding.
  *   q, k, lengths: as in the forward;  states: what it saved for them
  *   dh_last, dh0: (batch, nheads, vdim, kdim) float32, both nullable
  *   dq, dk : (batch, seqlen, nqk, kdim);  dv, dy: (batch, seqlen, nheads, vdim)

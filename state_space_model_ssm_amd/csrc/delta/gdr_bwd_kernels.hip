@@ -9,7 +9,9 @@
 //   dK = (H beta) K - e^G D S + beta (e^(G_64 - G) Z dS + P^T Q + H^T K), as read and as written
 // (beta by rows of the last sum and by columns of P and H in the others).  With
 //   W_ij = P_ij q_i.k_j + H_ij k_i.k_j,  c_j = k_j.(e^(G_64 - G) Z dS)_j
-// dbeta_j is c_j and the sum of W over i >= j, without a quotient by beta,
+// dbeta_j is D_j.Z_j / beta_j, or, where beta is 0, c_j and the sum of W over
+// i >= j (the same; but keys that are alike make that sum's terms cancel: 4e-5
+// off by norms, not 1e-5),
 // and dg_t is the sum of the terms whose decay passes token t, those of
 //   W_ij beta_j   from j < t to i >= t
 //   q_i.(scale e^G dY S)_i - k_i.(e^G D S)_i   for i >= t, from the state before
@@ -23,7 +25,14 @@
 // bound by its chain; 3.4 us a chunk with the 96 KiB of dS and D that it leaves
 // behind), and is cut into segments where heads are few; a second has all
 // chunks at once and is bound by reading those and what the forward saved.
-// Roundings as in the forward, outputs when they are stored.
+// Roundings: q, k and dy are exact; S, Z, dS, D, T, A, P and H enter products as
+// two bfloat16 parts, 2^-18 of their size, and products of two such leave out the
+// smallest term; sums are float32.  So dg, dbeta and dh0, which are stored in
+// float32 where the gates are (dh0 always), are 2e-6 to 1.2e-5 off by norms,
+// where float32 token by token is 2e-7 to 2e-6.  They are linear in dy and
+// dh_last: dy's own rounding to bfloat16 has left 2^-9 a value in them, 150 times
+// more.  Three parts, as the forward's last state has, would take half as many
+// bytes again of what it saves and what these kernels hand on, which bound them.
 //
 // Measured, 4 x 2048 tokens, 16 heads of 128: 110 us, and 162 for 557 MB (3.4
 // TB/s, where a large read reaches 4.0); a training pass 386 us with the
@@ -332,7 +341,7 @@ __global__ void __launch_bounds__(256, 2) gdr_grad_kernel(const GdrParams p) {
   constexpr unsigned kTriangle = 2 * kGdrTriBytes, kValues = 64 * 64 * 2 + 2 * kParts, kAll = kTriangle + 64 * kPitch * 4;
   constexpr unsigned kArea = kValues > kAll ? kValues : kAll;
   __shared__ __align__(16) u4 lds[(kAtD + kArea) / 16];
-  __shared__ float red[4][NW][64], whole[NW];  // red: sums of W for dg and for dbeta, and the tokens' terms with S and with dS
+  __shared__ float red[4][NW][64], diag[64], whole[NW];  // red: sums of W for dg and for dbeta, and the tokens' terms with S and with dS
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const unsigned chunks = static_cast<unsigned>(p.chunks), nqk = static_cast<unsigned>(p.nqk);
   const int64_t c = blockIdx.x % chunks, bk = blockIdx.x / chunks, b = static_cast<unsigned>(bk) / nqk, hk = static_cast<unsigned>(bk) % nqk;
@@ -415,7 +424,7 @@ __global__ void __launch_bounds__(256, 2) gdr_grad_kernel(const GdrParams p) {
         }
       }
       meet();  // what was in LDS has been read
-      // P = scale (dY Z^T) M, H = -(D Z^T) M and W.
+      // P = scale (dY Z^T) M, H = -(D Z^T) M and W, and the diagonal of D Z^T.
       const int own = 16 * w + m;
       const double so = sums[own];
       const Lanes16 at = lanes16_of<KD>(lane);
@@ -434,6 +443,7 @@ __global__ void __launch_bounds__(256, 2) gdr_grad_kernel(const GdrParams p) {
         for (int r = 0; r < 4; ++r) {
           const int other = 16 * j + 4 * g + r;
           const float gap = static_cast<float>(so - sums[other]);
+          if (other == own) diag[own] = pd[j][r];
           const float decay = __builtin_amdgcn_exp2f(gap);
           py[j][r] = other <= own && own < len ? py[j][r] * p.scale * decay : 0.0f;
           pd[j][r] = other < own ? -pd[j][r] * decay : 0.0f;
@@ -550,6 +560,7 @@ __global__ void __launch_bounds__(256, 2) gdr_grad_kernel(const GdrParams p) {
       if (lane == 0) whole[w] = both;
       meet();
       if (w == 0) {
+        const float beta = gates[192 + lane];
         float dg = 0.0f, before = 0.0f, behind = 0.0f, dbeta = 0.0f;
 #pragma unroll
         for (int k = 0; k < NW; ++k) {
@@ -563,8 +574,8 @@ __global__ void __launch_bounds__(256, 2) gdr_grad_kernel(const GdrParams p) {
           const float next = __shfl_down(before, d);
           if (lane + d < 64) before += next;
         }
-        dg += before + sum_before(gates[192 + lane] * behind);
-        dbeta += behind;
+        dg += before + sum_before(beta * behind);
+        dbeta = fabsf(beta) >= 0x1p-100f ? diag[lane] / beta : dbeta + behind;
         if (lane < rows) {
           const int64_t to = (b * p.seqlen + t0 + lane) * p.nheads + h;
           store_gate(p.dg, to, lane < len ? dg : 0.0f, G{});

@@ -113,3 +113,23 @@ def test_shut_gates_keep_a_state():
     assert torch.equal(ssm.gdr_fwd(*cuda(q, k, v, g, beta), h0=h0.cuda())[1].cpu(), h0)
     y, last = ssm.gdr_fwd(*cuda(q, k, v, g, beta))
     assert not y.any() and not last.any()
+
+
+@pytest.mark.parametrize("cosine,strength", [(0.0, 0.0), (0.5, 3.0), (0.9, 3.0)])
+@pytest.mark.parametrize("L,H,K,V,rate", [(640, 2, 128, 128, 0.01), (640, 2, 64, 64, 0.3), (2500, 1, 64, 128, 0.002), (300, 4, 128, 64, 5.0)])
+def test_float32_gradients_by_norms(L, H, K, V, rate, cosine, strength):
+    """dg, dbeta and dh0.  A product of two factors in two parts loses 3 * 2^-18 of its terms at most, 2^-18 of them by
+    norms, where roundings are spread over their half steps; five in turn, each of which passes the others' on, 2^-15.7
+    with T's row sums of 2 at most on two of them: 2^-15 is a third of 1e-4, which a mistaken term would be."""
+    q, k, v, g, beta, h0 = make(L, H, K, V, L + K, cosine, strength, rate)
+    gen = torch.Generator().manual_seed(L)
+    dy, dh = torch.randn(1, L, H, V, generator=gen).to(BF16), torch.randn(1, H, V, K, generator=gen)
+    want = ref.gdr_bwd(*(ref.f64(t) for t in (q, k, v, g, beta, dy, h0)), dh_last=ref.f64(dh))[0]
+    cs = cuda(q, k, v, g, beta)
+    for last in (True, False):
+        states = ssm.gdr_fwd(*cs, h0=h0.cuda(), return_h_last=last, return_states=True)[2]
+        got = ssm.gdr_bwd(*cs, states, dy.cuda(), dh_last=dh.cuda())
+        for name, t in zip(("dg", "dbeta", "dh0"), got[3:]):
+            far = float((ref.f64(t) - want[name]).norm() / want[name].norm())
+            print(name, f"{far:.1e}")
+            assert far <= 2.0 ** -15, (name, far)
