@@ -145,7 +145,11 @@ __device__ __forceinline__ float other_row(float v) {
 }
 
 // Weights as two operands whose sum they are to 2^-16: cut off after 8 bits, and
-// what that leaves, held above 0, so that both times an infinity have its sign.
+// what that leaves.  INF, where values may be infinities: held above 0, so that
+// both times an infinity have its sign.  (Not with a block's bytes, which are
+// not infinite: its scale is in the weights already, and the least that is held
+// would be added to what may be smaller.)
+template <bool INF>
 __device__ __forceinline__ void two_parts(const f4v &lo, const f4v &hi, bf8 &cut, bf8 &rest) {
   u4 c;
 #pragma unroll
@@ -153,8 +157,9 @@ __device__ __forceinline__ void two_parts(const f4v &lo, const f4v &hi, bf8 &cut
     const float a = k < 2 ? lo[2 * (k % 2)] : hi[2 * (k % 2)], b = k < 2 ? lo[2 * (k % 2) + 1] : hi[2 * (k % 2) + 1];
     const unsigned ca = __float_as_uint(a) & 0xffff0000u, cb = __float_as_uint(b) & 0xffff0000u;
     c[k] = ca >> 16 | cb;
-    rest[2 * k] = static_cast<__bf16>(fmaxf(a - __uint_as_float(ca), 0x1p-100f));
-    rest[2 * k + 1] = static_cast<__bf16>(fmaxf(b - __uint_as_float(cb), 0x1p-100f));
+    const float ra = a - __uint_as_float(ca), rb = b - __uint_as_float(cb);
+    rest[2 * k] = static_cast<__bf16>(INF ? fmaxf(ra, 0x1p-100f) : ra);
+    rest[2 * k + 1] = static_cast<__bf16>(INF ? fmaxf(rb, 0x1p-100f) : rb);
   }
   cut = __builtin_bit_cast(bf8, c);
 }
@@ -315,7 +320,7 @@ __global__ void __launch_bounds__(64 * NW, 2) swa_q8_step_kernel(const SwaStepPa
           // Rows behind the token repeat its slot, which may hold anything.
           for (int r = own + 1 - k0 + lane / CH; has && r < kNear; r += 64 / CH) vt[slot<D>(r, lane % CH)] = u4{};
           bf8 cut, left;
-          two_parts(s[0], s[1], cut, left);
+          two_parts<true>(s[0], s[1], cut, left);
 #pragma unroll
           for (int e = 0; e < NB; ++e) {
             const bf8 v = elems16<D>(lds_at(vt), e, 0, lane);
@@ -325,7 +330,7 @@ __global__ void __launch_bounds__(64 * NW, 2) swa_q8_step_kernel(const SwaStepPa
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             bf8 cut, left;
-            two_parts(s[2 * x] * vs, s[2 * x + 1] * vs, cut, left);
+            two_parts<false>(s[2 * x] * vs, s[2 * x + 1] * vs, cut, left);
 #pragma unroll
             for (int e = 0; e < NB; ++e) {
               const bf8 v = values16<D>(vt, x, e, lane);
