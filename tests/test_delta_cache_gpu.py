@@ -74,3 +74,27 @@ def test_tiny_values(H, KV, d, window, size):
     v = (v.float() * size).to(BF16)
     cache, model = filled(k, v, window, 0, lengths)
     check_step(q, k, v, cache, model, window, 0, lengths)
+
+
+@pytest.mark.parametrize("scale", [-0.3, 0.0, 2.0])
+@pytest.mark.parametrize("H,KV,d,window,sinks", [(4, 2, 64, 128, 4), (6, 2, 128, 1024, 0)])
+def test_any_scale(H, KV, d, window, sinks, scale):
+    """Negative ones turn the queries round; 0 weighs all that is seen alike."""
+    lengths = [sinks + window + 64 + 63, sinks + 2 * window + 10, 70, 3]
+    q, k, v = make(4, max(lengths) + 1, H, KV, d, window)
+    cache, model = filled(k, v, window, sinks, lengths)
+    check_step(q, k, v, cache, model, window, sinks, lengths, scale)
+
+
+@pytest.mark.parametrize("H,KV,d", [(40, 1, 128), (17, 1, 64), (64, 2, 64)])
+def test_many_heads_of_a_key_head_over_split_windows(H, KV, d):
+    """Blocks of 16 heads of which each stores the token, and shares of the window that a second kernel joins; at a
+    block's last place, its first, and within it, before and after the ring is full."""
+    window, sinks = 4096, 3
+    lengths = [sinks + 4096 + 64 * 3 - 1, sinks + 1000, sinks + 5000, 1, sinks + 63]
+    dims = ssm.SwaDims(batch=5, seqlen=1, nheads=H, nkv=KV, headdim=d, window=window, sinks=sinks, q_batch=H * d, q_token=H * d,
+                       k_batch=KV * d, k_token=KV * d, v_batch=KV * d, v_token=KV * d, scale=1.0)
+    assert ssm.swa_q8_step_workspace_size(dims) > 0   # it is split
+    q, k, v = make(5, max(lengths) + 1, H, KV, d, H)
+    cache, model = filled(k, v, window, sinks, lengths)
+    check_step(q, k, v, cache, model, window, sinks, lengths)
