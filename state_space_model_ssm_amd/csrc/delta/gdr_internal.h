@@ -6,8 +6,6 @@
 
 namespace ssmb {
 
-constexpr int kGdrChunk = 64;
-
 // What is known of a chunk of 64 tokens and a value head before its state is:
 // T = (I + L)^-1 less I and the attention A within the chunk, as operands in
 // bfloat16 parts (see gdr_tile.h), then the gates' factors.

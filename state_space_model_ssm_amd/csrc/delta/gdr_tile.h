@@ -123,16 +123,6 @@ __device__ __forceinline__ bf8 col16(unsigned tile, int j, int s, const Lanes16 
   const sh4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)(to + 32 * D));
   return __builtin_bit_cast(bf8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
 }
-// Transposed operand in plain order: k stands for rows 8g .. of a tile, the
-// lane's pieces of which lie at `at` (row 8g + m / 4) and 4 rows on.
-template <int D>
-__device__ __forceinline__ bf8 values16(unsigned at) {
-  typedef __attribute__((address_space(3))) sh4 lds4;
-  const sh4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)(at));
-  const sh4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)((at ^ 16) + 8 * D));
-  return __builtin_bit_cast(bf8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
-}
-
 // The operand that was stored as fragment f of 1024 bytes.
 __device__ __forceinline__ bf8 frag16(unsigned tile, int f, int lane) {
   typedef __attribute__((address_space(3))) const u4 lds16;
