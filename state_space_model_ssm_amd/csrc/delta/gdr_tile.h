@@ -169,9 +169,12 @@ __device__ __forceinline__ f4v lds_f4(unsigned at) {
 constexpr int kPairs = 2;  // wavefronts that carry the state, and as many beside them
 
 // Call f with the wavefront's number (of 4) as a constant.  Each wavefront's
-// products are straight code then: the compiler leaves out the wait between a
+// products are straight code then: the compiler has left out the wait between a
 // matrix product and a read of its result where a branch by a wavefront's
-// number lies between them.
+// number lay between them.  (tests/test_matrix_waits.py looks for that in every
+// built library, over all paths.  Other branches by a wavefront's number, as in
+// the backward's stores of triangles, have vector instructions that read the
+// products before them, in the same straight code.)
 template <typename F>
 __device__ __forceinline__ void by_wave(int w, F &&f) {
   switch (w) {
