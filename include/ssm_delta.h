@@ -91,11 +91,14 @@ enum { SSM_GDR_STATE_STEP = 64 };
  *            ssm_gdr_bwd starts from (the state before every 64th token, the
  *            u_t / beta_t, and what of v, g and beta it needs), in an order of its own;
  *            what is of tokens past a row's last block of 64 is not written
- * The rule is stable for beta |k|^2 below 2: keys are meant to have unit length.
+ * The rule is stable for beta |k|^2 from 0 to 2: keys are meant to have unit
+ * length.
  * Tokens are taken 64 at a time: a value that is not finite reaches y from the
  * start of its block of 64 tokens (of its channel, if it is one of v; of the
- * value heads that share it, if it is one of q or k) and what comes after.
+ * value heads that share it, if it is one of q or k; of its own, if it is one of
+ * beta, or of g and not -inf) and what comes after.
  */
+/* (Of a call without states: one with them takes as many bytes, and uses fewer.) */
 SSM_API int ssm_gdr_workspace_size(const ssm_gdr_dims_t *dims, size_t *bytes);
 SSM_API int ssm_gdr_states_size(const ssm_gdr_dims_t *dims, size_t *bytes);
 SSM_API int ssm_gdr_fwd(const void *q, const void *k, const void *v, const void *g, const void *beta, const float *h0,
@@ -109,9 +112,9 @@ SSM_API int ssm_gdr_fwd(const void *q, const void *k, const void *v, const void 
  *   dq_t = scale S_t^T dy_t,  dk_t = dS_t^T u_t - a_t S_{t-1}^T dv_t
  *   dg_t = a_t (<dS_t, S_{t-1}> - dv_t.S_{t-1} k_t)
  * dq and dk are summed over the value heads that share a head.  Rows at or
- * past the length get zero gradients.  dg, dbeta and dh0 are right to 1e-5 of
- * their norms, also where they are float32 (2^-15 at most with keys of unit
- * length), the others to their own rounding.
+ * past the length get zero gradients.  dg, dbeta and dh0 are right to about
+ * 1e-5 of their norms, also where they are float32, the others to their own
+ * rounding.
  *   q, k, lengths: as in the forward;  states: what it saved for them
  *   dh_last, dh0: (batch, nheads, vdim, kdim) float32, both nullable
  *   dq, dk : (batch, seqlen, nqk, kdim);  dv, dy: (batch, seqlen, nheads, vdim)

@@ -34,9 +34,11 @@
 // more.  Three parts, as the forward's last state has, would take half as many
 // bytes again of what it saves and what these kernels hand on, which bound them.
 //
-// Measured, 4 x 2048 tokens, 16 heads of 128: 110 us, and 162 for 557 MB (3.4
-// TB/s, where a large read reaches 4.0); a training pass 386 us with the
-// forward.
+// Measured, 4 x 2048 tokens, 16 heads of 128: 109 us, and 157 for 557 MB (3.5
+// TB/s, where a large read reaches 4.0); a training pass 375 us with the
+// forward.  With keys of 128 the second kernel has more than its 256 registers:
+// 13 are spilled, 125 to 130 where value heads share keys, whose sums it carries
+// along (8 query heads: 378 us all the same).
 #include "gdr_tile.h"
 
 namespace ssmb {
@@ -636,10 +638,9 @@ hipError_t bwd(const GdrParams &p, hipStream_t s) {
 
 GdrSegments gdr_bwd_segments(int64_t heads, int64_t kdim, int64_t vdim, int64_t chunks) {
   // As gdr_segments(): in turn a chunk takes 2.7 us (keys of 64: 1.9), without
-  // what is stored 2.3 (1.7).  Kernels of forward and backward together, us: 2
-  // heads of 64, 8192 tokens: 1 segment of the backward 329, 8 155, 32 115; 8 of
-  // 128 on 2, 2048 tokens: 1 206, 8 171, 16 184; 16 of 128, 4 x 2048: 1 406, 2
-  // 453.
+  // what is stored 2.3 (1.7).  Forward and backward together, us a call: 2 heads
+  // of 64, 8192 tokens: 1 segment of the backward 330, 8 169, 32 128; 8 of 128 on
+  // 2, 2048 tokens: 1 222, 8 189, 16 203; 16 of 128, 4 x 2048: 1 368, 2 420.
   const bool wide = kdim == 128;
   const int64_t columns = heads * (vdim / 32), pairs = heads * (kdim / 64);
   int64_t best = 1;

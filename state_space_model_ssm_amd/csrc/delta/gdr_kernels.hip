@@ -28,8 +28,9 @@
 // without).  T's ones are kept out of what is rounded.  Sums are float32, sums of
 // g float64.
 //
-// Measured, 16 heads of 128: one prompt of 8192 tokens in 199 us a call; training's 4 x 2048, where the last state
-// is not asked for, in 29 and 105, of which saving for the backward, 200 MB, is
+// Measured, 16 heads of 128: one prompt of 8192 tokens in 199 us a call (chunks
+// 31 us, segments 82, join 15, y 96); training's 4 x 2048, where the last state
+// is not asked for, in 31 and 103, of which saving for the backward, 200 MB, is
 // a third.
 #include "gdr_tile.h"
 
@@ -63,7 +64,7 @@ __device__ __forceinline__ void load_rest(bf8 (&t)[kGdrFrags], const char *from,
 // One workgroup per chunk and value head, one wavefront per 16 of its tokens.
 // T by blocks of 16: those on the diagonal by substitution, the others from
 // them by products in float32, since errors of T's entries would grow along its
-// rows.  2048 chunks of 128 in 29 us, where their 121 MB would take 25.  (Keys
+// rows.  2048 chunks of 128 in 31 us, where their 121 MB would take 25.  (Keys
 // through LDS, not from memory by each wavefront: 37.)
 template <int KD, typename G>
 __global__ void __launch_bounds__(256) gdr_chunk_kernel(const GdrParams p) {
@@ -206,10 +207,10 @@ __global__ void __launch_bounds__(256) gdr_chunk_kernel(const GdrParams p) {
 // carry that, 16 columns each, and two others make y from the operands that
 // those leave in LDS, and copy the next chunk there: each of the four has a
 // SIMD to itself.  LAST: the last state is returned, and held to float32.  A
-// chunk takes 2.7 us then (keys of 64: 1.7), 2000 cycles of which are the
-// state's own matrix instructions, else 2.2 (1.5) with 1300; the rest is its
-// operands' way through LDS and the splitting into parts.  With what the
-// backward needs 3.2.
+// chunk takes 2.4 us then (keys of 64: 1.8), 3.0 with a workgroup on every
+// compute unit, 2100 cycles of which are the state's own matrix instructions,
+// else 1.7 (1.5) with 1300; the rest is its operands' way through LDS and the
+// splitting into parts.  With what the backward needs 3.2.
 template <int KD, bool LAST>
 __global__ void __launch_bounds__(256) gdr_fwd_kernel(const GdrParams p) {
   constexpr int NT = 64 * kPairs, NC = 16 * kPairs, NS = KD / 32, NB = KD / 16;
@@ -758,12 +759,14 @@ hipError_t step(const GdrParams &p, hipStream_t s) {
 }  // namespace
 
 GdrSegments gdr_segments(int64_t heads, int64_t kdim, int64_t vdim, int64_t chunks) {
-  // Times in us, measured.  In turn a chunk takes 2.3 (keys of 64: 1.6).  With G
-  // segments each is gone through twice, once for E and P (a compute unit has
-  // two workgroups of these, and they are faster together) and once for y (it
-  // has one), and the join takes a step per segment.  16 heads of 128, 8192
-  // tokens: 1 segment 320, 4 210, 8 203, 16 223; 2 heads of 64, 16384 tokens: 1
-  // 427, 32 64, 64 63; 32 heads of 128, 4096 tokens: 1 172, 2 192, 4 186.
+  // Times in us, between those with the last state and those without.  In turn a
+  // chunk takes 2.4 or 1.7 (keys of 64: 1.8, 1.5).  With G segments each is gone
+  // through twice, once for E and P (a compute unit has two workgroups of these,
+  // and they are faster together) and once for y (it has one), and the join
+  // takes a step per segment.  Calls with the last state, measured: 16 heads of
+  // 128, 8192 tokens: 1 segment 336, 4 208, 8 195, 16 212; 2 heads of 64, 16384
+  // tokens: 1 480, 32 73, 64 77; 32 heads of 128, 4096 tokens: 1 185, 2 205, 4
+  // 186; without it 247, 186, 177, 193; 389, 69, 75; 141, 181, 165.
   const bool wide = kdim == 128;
   const int64_t columns = heads * (vdim / 32), pairs = heads * ((vdim + kdim) / 64);
   const double a = wide ? 2.6 : 1.65;

@@ -14,10 +14,10 @@
 // product in two parts (2^-16), as those over a bfloat16 ring do: the rest of
 // the error is the cache's own rounding.  Heads that share a key head are the
 // matrix instruction's 16 columns, 16 at a time (32 at a time, with half of
-// them empty in groups of four, took 170 us where this takes 92).
+// them empty in groups of four, took 170 us where 16 took 95).
 //
-// Measured: 64 sequences, 32 heads of 128 on 8, windows of up to 4096 in 83 us
-// a call, 4.85 TB/s of the cache's bytes, where a large copy reaches 4.8; 4
+// Measured: 64 sequences, 32 heads of 128 on 8, windows of up to 4096 in 84 to
+// 88 us a call, 4.6 to 4.8 TB/s of the cache's bytes, where a large copy reaches 4.8; 4
 // sequences, 16 heads on 4, window 1024: 11 us, of a call's 12, all latency.
 #include "block/swa_step.h"
 #include "delta_internal.h"

@@ -133,3 +133,17 @@ def test_float32_gradients_by_norms(L, H, K, V, rate, cosine, strength):
             far = float((ref.f64(t) - want[name]).norm() / want[name].norm())
             print(name, f"{far:.1e}")
             assert far <= 2.0 ** -15, (name, far)
+
+
+@pytest.mark.parametrize("gate", [3, 4])
+def test_a_gate_that_is_not_finite_reaches_its_own_head(gate):
+    """From the start of its 64 tokens on."""
+    args = list(make(200, 3, 64, 64, 3, 0.0, 0.0))[:5]
+    clean = ssm.gdr_fwd(*cuda(*args))
+    args[gate] = args[gate].clone()
+    args[gate][0, 100, 1] = float("nan")
+    y, last = ssm.gdr_fwd(*cuda(*args))
+    others = [0, 2]
+    assert torch.equal(y[0, :64], clean[0][0, :64]) and torch.equal(y[0, :, others], clean[0][0, :, others])
+    assert torch.equal(last[0, others], clean[1][0, others])
+    assert y[0, 100:, 1].isnan().all() and last[0, 1].isnan().all()
